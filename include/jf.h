@@ -501,6 +501,164 @@ jf_status jf_compact_accepted_kv(void* k_cache, void* v_cache, const int32_t* bl
                                  int32_t num_pages, int32_t* new_prefix_len, int32_t* dev_err,
                                  jf_stream_t stream);
 
+/* ---------------------------------------------------------------- a bounded cache
+ * Between two steps a serving loop may have to shrink a sequence's cache.  The three calls
+ * below evict by accumulated attention weight (keys that later queries hardly attended to
+ * go first): jf_attention_weight adds what a step's rows attended to, jf_select_kept picks
+ * the positions that stay, jf_evict_kv moves their K/V (and weights) to the front.  The
+ * pages have no counterpart; the selection rule is that of heavy-hitter caches (kept: the
+ * first `sink` keys, the last `recent` keys, and the keys of greatest weight).  Each
+ * kv-head keeps its own set of positions; all heads of a sequence keep the same number, so
+ * one block table and one length still describe the sequence.  Keys carry their rotary
+ * position from when they were cached, so position ids go on from the number of tokens seen,
+ * not from the cache's length (give jf_build_tree_mask that number as its prefix_len to
+ * get the ids, and the other calls the cache's length).
+ *
+ * jf_attention_weight -- the attention probabilities every cached key received from this
+ * step's rows, added to what it had.  Call it after jf_compact_accepted_kv (rows: the
+ * accepted path) or, for a chain of tokens without verification (a decoded token, a window
+ * of prompt tokens), after jf_tree_attention.  With n_k = path[b][k], or k without a path,
+ * and R_b = accept_len[b] + 1 rows, or all N without accept_len:
+ *   weight_out[b][g][t] = (t < P_b ? weight[b][g][t] : 0) +
+ *       sum_{k < R_b, t <= P_b + k} sum_{h in kv-head g's group}
+ *           exp(scale * q[b][n_k][h] . k_t - lse[b][h][n_k])          for t < P_b + R_b.
+ *   q            bf16 [B][N][Hq][D], the attention call's.
+ *   k_cache, block_table, prefix_len (P_b: the length before this step): as in
+ *                jf_tree_attention; the rows' own keys sit at P_b .. P_b + R_b - 1.
+ *   path         int32 [B][N] or NULL; accept_len int32 [B] (-1: no rows) or NULL; a path
+ *                needs accept_len.
+ *   lse          float [B][Hq][N], written by the attention call for the same keys.  A row
+ *                whose lse is -inf attended to nothing and adds nothing.
+ *   weight       float [B][Hkv][max_pages * page_size], or NULL for zero.
+ *   weight_out   the same shape; may be weight itself.  Positions t >= P_b + R_b are left
+ *                as they were.
+ *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + R_b past the block table),
+ *                _BAD_PATH (accept_len or a path entry out of range), _BAD_PAGE, _TIMEOUT,
+ *                and _BAD_TREE_LEN for the packed call.  May be NULL.
+ * Sums are fp32 in a fixed order: the same call gives the same bits.
+ * Limits: as jf_tree_attention, but G = Hq / Hkv may be any number up to 128, and
+ * weight, weight_out and lse need only their own 4-byte alignment.
+ * jf_attention_weight_packed takes the packed layout: q [T][Hq][D], lse [Hq][T],
+ * sequence b's nodes at rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1; path stays
+ * [B][N_max].  A sequence with a bad span has no rows.
+ */
+jf_status jf_attention_weight(const void* q, const void* k_cache, const int32_t* block_table,
+                              const int32_t* prefix_len, const int32_t* path,
+                              const int32_t* accept_len, const float* lse, const float* weight,
+                              int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                              int32_t page_size, int32_t max_pages, int32_t num_pages, float scale,
+                              float* weight_out, int32_t* dev_err, jf_stream_t stream);
+jf_status jf_attention_weight_packed(const void* q, const void* k_cache, const int32_t* block_table,
+                                     const int32_t* prefix_len, const int32_t* cu_seqlens,
+                                     const int32_t* path, const int32_t* accept_len,
+                                     const float* lse, const float* weight, int32_t B,
+                                     int32_t N_max, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t page_size, int32_t max_pages, int32_t num_pages,
+                                     float scale, float* weight_out, int32_t* dev_err,
+                                     jf_stream_t stream);
+
+/*
+ * jf_select_kept -- the positions that stay when every sequence may keep `budget` keys.
+ *   weight    float [B][Hkv][capacity]; only positions below seq_len[b] are read.
+ *   seq_len   int32 [B], cached keys L_b (clamped to [0, capacity], JF_DEVERR_BAD_PREFIX).
+ *   L_b <= budget: every position stays.  Otherwise, for every kv-head, the first `sink`
+ *   and the last `recent` positions and, of the others, the budget - sink - recent with the
+ *   greatest weights: values compared as real numbers, NaN below all others, ties to the
+ *   lowest position.
+ *   keep      int32 [B][Hkv][budget]: the kept positions in rising order, then -1.
+ *   kept_len  int32 [B]: min(L_b, budget).
+ * Limits: sink, recent >= 0, 1 <= budget, sink + recent <= budget; capacity and budget
+ * up to 2^30.
+ */
+jf_status jf_select_kept(const float* weight, const int32_t* seq_len, int32_t B, int32_t Hkv,
+                         int32_t capacity, int32_t sink, int32_t recent, int32_t budget,
+                         int32_t* keep, int32_t* kept_len, int32_t* dev_err, jf_stream_t stream);
+
+/*
+ * jf_evict_kv -- moves the kept keys' K/V rows to positions 0 .. kept_len[b] - 1:
+ *   for every kv-head g and j < kept_len[b], rows keep[b][g][j] of K and V go to position j,
+ *   and weight[b][g][keep[b][g][j]] to weight_out[b][g][j].
+ *   k_cache, v_cache bf16 [num_pages][page_size][Hkv][D], modified.
+ *   block_table      int32 [B][max_pages]; seq_len int32 [B], the length before the call.
+ *   keep, kept_len   as written by jf_select_kept (keep[b][g] rises strictly).  kept_len is
+ *                    the sequence's new length.
+ *   new_block_table  NULL: the rows move inside block_table's pages (the table's pages from
+ *                    ceil(kept_len / page_size) on are free afterwards; positions past
+ *                    kept_len hold old rows).  Otherwise int32 [B][max_pages]: the rows go
+ *                    into that table's pages, which must appear nowhere in block_table;
+ *                    the old pages keep their contents.  Pages that several sequences share
+ *                    (forked beams) need this form.
+ *   weight, weight_out  float [B][Hkv][max_pages * page_size], or both NULL; may be the
+ *                    same array, and must not otherwise overlap.
+ *   dev_err          JF_DEVERR_BAD_PREFIX (seq_len), _BAD_PATH (kept_len or keep malformed),
+ *                    _BAD_PAGE.  May be NULL.
+ * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned, kept_len != seq_len (the
+ * arrays).
+ */
+jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
+                      const int32_t* seq_len, const int32_t* keep, const int32_t* kept_len,
+                      const int32_t* new_block_table, const float* weight, float* weight_out,
+                      int32_t B, int32_t Hkv, int32_t D, int32_t budget, int32_t page_size,
+                      int32_t max_pages, int32_t num_pages, int32_t* dev_err, jf_stream_t stream);
+
+/* ---------------------------------------------------------------- beams
+ * Beam decoding on the paged cache: beam w of prompt b is sequence b * W + w of the other
+ * calls (jf_tree_attention with N = 1), with its own block-table row.  jf_beam_select picks
+ * the next step's beams from the logits, jf_beam_fork_kv gives each its block table.  The
+ * same selection grows a draft tree level by level when the drafter runs once per level
+ * (jf_build_draft_tree takes all levels' logits at once).
+ *
+ * jf_beam_select -- the K best continuations of every prompt:
+ *   s(w, v) = score[b][w] + logits[b][w][v] - logsumexp(logits[b][w]);
+ *   a beam with finished[b][w] != 0 goes on with eos_token alone, at score[b][w]: its other
+ *   tokens have s = -inf.  So has every token of a beam whose score is -inf (an unused
+ *   beam; its logits are not read) and every token whose logit is -inf.
+ *   The K greatest s(w, v), in falling order, ties to the lowest w * V + v:
+ *   parent int32 [B][K] (w), token int32 [B][K] (v), new_score float [B][K] (s, rounded to
+ *   fp32), new_finished int32 [B][K] (1 where the parent had finished or v == eos_token;
+ *   may be NULL).
+ *   logits     [B][W][V] bf16 or fp32 (dtype); -inf marks a token that may not be chosen,
+ *              NaN and +inf leave the outputs of that prompt unspecified.
+ *   score      float [B][W]; must not be new_score.
+ *   finished   int32 [B][W] or NULL; must not be new_finished.  eos_token: -1 for none, in
+ *              [0, V) where finished is given.
+ *   workspace  at least jf_beam_select_workspace_size(...) bytes, 8-byte aligned, no
+ *              initialisation.
+ * s is ranked in 64 bits, with logsumexp from per-slice fp32 sums of exponentials (relative
+ * error about 1e-7): pairs of different beams closer than that may come in either order.
+ * Limits: 1 <= K <= 64, 1 <= W <= 64, K <= W * V, W * V < 2^31, B * W < 2^20.
+ */
+size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K, int32_t dtype);
+jf_status jf_beam_select(const void* logits, int32_t dtype, const float* score,
+                         const int32_t* finished, int32_t eos_token, int32_t B, int32_t W,
+                         int32_t V, int32_t K, int32_t* parent, int32_t* token, float* new_score,
+                         int32_t* new_finished, void* workspace, size_t workspace_bytes,
+                         jf_stream_t stream);
+
+/*
+ * jf_beam_fork_kv -- block tables of the new beams.  New beam j of prompt b continues beam
+ * w = parent[b][j] with its P = prefix_len[b * W + w] cached tokens: it shares the parent's
+ * floor(P / page_size) full pages (their ids are copied) and gets a page of its own,
+ * fresh_page[b][j], as the next entry, into which the slots of the parent's partial page
+ * are copied (none when P is a multiple of page_size).  Later entries are -1.
+ *   k_cache, v_cache  bf16 [num_pages][page_size][Hkv][D]; only fresh pages are written.
+ *   block_table       int32 [B * W][max_pages]; prefix_len int32 [B * W].
+ *   parent            int32 [B][K] as written by jf_beam_select.
+ *   fresh_page        int32 [B][K]: distinct pages that no sequence uses.  Where P fills the
+ *                     whole block table none is used.
+ *   new_block_table   int32 [B * K][max_pages]; new_prefix_len int32 [B * K].  Must not be
+ *                     block_table and prefix_len.
+ *   dev_err           JF_DEVERR_BAD_PATH (parent; the beam then gets length 0 and no pages),
+ *                     _BAD_PREFIX (the same), _BAD_PAGE.  May be NULL.
+ * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned.
+ */
+jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_table,
+                          const int32_t* prefix_len, const int32_t* parent,
+                          const int32_t* fresh_page, int32_t B, int32_t W, int32_t K, int32_t Hkv,
+                          int32_t D, int32_t page_size, int32_t max_pages, int32_t num_pages,
+                          int32_t* new_block_table, int32_t* new_prefix_len, int32_t* dev_err,
+                          jf_stream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

@@ -1,0 +1,197 @@
+"""GPU parity of beam selection and the beams' cache fork with plain 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+from test_gpu_cache import Pool, dev, new_err
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def jf():
+    from tree_speculative_decoding_jf_gb300 import build
+    build.build()
+    from tree_speculative_decoding_jf_gb300 import jf as mod
+    return mod
+
+
+def check_beams(logits, score, finished, eos, got, K):
+    """Every prompt's output against the definition.  Within a beam the order is exact (by
+    logit, then token).  Across beams a pair may stand where the exact ranking has one whose
+    s differs by less than the stated precision: with u = 2^-24, a sum of V exponentials is
+    off by at most (40 + 2 span) u relative (under 40 roundings on any path of the sum; the
+    exponent's product and the exponential by 2 span u), span the logits' finite range."""
+    parent, token, new_score, new_fin = (x.cpu().numpy() for x in got)
+    B, W, V = logits.shape
+    for b in range(B):
+        s = ref.beam_scores(logits[b], score[b], None if finished is None else finished[b], eos)
+        flat = s.reshape(-1)
+        order = np.lexsort((np.arange(flat.size), -flat))[:K]
+        pick = parent[b].astype(np.int64) * V + token[b]
+        assert ((parent[b] >= 0) & (parent[b] < W) & (token[b] >= 0) & (token[b] < V)).all()
+        assert len(set(pick.tolist())) == K
+        fin = logits[b][np.isfinite(logits[b])].astype(np.float64)
+        span = fin.max() - fin.min() if fin.size else 0.0
+        tol = (40 + 2 * span) * 2.0 ** -24
+        a, e = flat[pick], flat[order]
+        assert (np.isneginf(a) == np.isneginf(e)).all(), b
+        live = ~np.isneginf(e)
+        assert (np.abs(a[live] - e[live]) <= 2 * tol).all(), (b, a, e)
+        if not live.all():                     # pairs at -inf: the lowest ones, in order
+            assert (pick[~live] == order[~live]).all(), (b, pick, order)
+        assert (np.isneginf(new_score[b]) == ~live).all()
+        assert (np.abs(new_score[b][live] - a[live]) <= tol + 2.0 ** -24 * np.abs(a[live])).all()
+        for w in range(W):
+            mine = pick[(parent[b] == w) & live]
+            row = np.lexsort((np.arange(V), -s[w]))[:len(mine)] + w * V
+            assert (mine == row).all(), (b, w)
+        for j in range(K):
+            f = (finished is not None and finished[b, parent[b, j]] != 0) or token[b, j] == eos
+            assert new_fin[b, j] == int(f)
+
+
+def run_beams(jf, logits, score, K, finished=None, eos=-1, dtype=torch.bfloat16):
+    t = torch.from_numpy(np.ascontiguousarray(logits, np.float32)).to(dtype)
+    got = jf.beam_select(t.cuda(), dev(score.astype(np.float32)), K,
+                         finished=None if finished is None else dev(finished.astype(np.int32)), eos_token=eos)
+    torch.cuda.synchronize()
+    check_beams(t.float().numpy(), score.astype(np.float32), finished, eos, got, K)
+    return got
+
+
+@pytest.mark.parametrize("B,W,V,K", [
+    (1, 4, 151936, 8), (2, 1, 1000, 1), (3, 5, 50257, 5), (1, 3, 32003, 6), (4, 8, 4097, 16), (2, 2, 17, 8),
+    (1, 1, 1, 1), (1, 64, 700, 64), (2, 6, 8, 40), (1, 2, 131072, 64), (5, 7, 2049, 33), (40, 3, 16387, 4),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_beams_match_reference(jf, B, W, V, K, dtype):
+    rng = np.random.default_rng(B * 100 + W * 10 + K)
+    logits = 2.5 * rng.standard_normal((B, W, V))
+    score = -8 * rng.random((B, W)) - 2
+    run_beams(jf, logits, score, K, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_finished_and_unused_beams(jf, dtype):
+    rng = np.random.default_rng(5)
+    B, W, V, K = 6, 5, 5003, 10
+    logits = 3 * rng.standard_normal((B, W, V))
+    score = -3 * rng.random((B, W)) - 1
+    finished = np.zeros((B, W), np.int32)
+    finished[0, 2] = 1                         # one finished beam
+    finished[1] = 1                            # all of them: W pairs, then -inf ones
+    score[2, 1:] = -np.inf                     # the first step: one beam in use
+    score[3] = -np.inf                         # none in use
+    finished[4, :4] = 1
+    score[4, 4] = -np.inf
+    score[5, 0] = -np.inf
+    finished[5, 0] = 1                         # finished at -inf
+    for eos in (0, 4, V - 1):
+        run_beams(jf, logits, score, K, finished, eos, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_masked_tokens_and_ties(jf, dtype):
+    rng = np.random.default_rng(6)
+    V = 20011
+    logits = rng.standard_normal((5, 3, V)) * 2
+    allowed = rng.permutation(V)[:7]
+    masked = np.full_like(logits[0], -np.inf)
+    masked[:, allowed] = logits[0][:, allowed]
+    logits[0] = masked                         # seven tokens allowed in each beam
+    logits[1, 1] = -np.inf                     # a beam without any
+    logits[2] = -np.inf                        # a prompt without any
+    logits[3] = np.round(logits[3])            # many ties
+    logits[4] = 1.5                            # one value everywhere
+    score = np.tile(np.array([[-1.0, -2.5, -2.5]]), (5, 1))
+    for K in (4, 16, 40):
+        run_beams(jf, logits, score, K, dtype=dtype)
+
+
+def test_unaligned_logits(jf):
+    """A logits tensor that starts two bytes past a 16-byte boundary."""
+    rng = np.random.default_rng(7)
+    B, W, V, K = 2, 3, 4096, 6
+    logits = torch.from_numpy((2 * rng.standard_normal(B * W * V + 1)).astype(np.float32)).to(torch.bfloat16).cuda()
+    view = logits[1:].view(B, W, V)
+    score = (-rng.random((B, W))).astype(np.float32)
+    got = jf.beam_select(view, dev(score), K)
+    torch.cuda.synchronize()
+    check_beams(view.float().cpu().numpy(), score, None, -1, got, K)
+
+
+def test_beams_in_a_graph(jf):
+    rng = np.random.default_rng(8)
+    B, W, V, K = 3, 4, 30000, 8
+    logits = dev((2 * rng.standard_normal((B, W, V))).astype(np.float32)).to(torch.bfloat16)
+    score = dev((-rng.random((B, W))).astype(np.float32))
+    want = jf.beam_select(logits, score, K)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = jf.beam_select(logits, score, K)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def fork_case(seed, B, W, K, Hkv, D, lens, cap_pages):
+    rng = np.random.default_rng(seed)
+    pool = Pool(rng, lens, cap_pages, Hkv, D, spare=B * K)
+    parent = rng.integers(0, W, (B, K)).astype(np.int32)
+    return pool, parent, pool.spare.reshape(B, K)
+
+
+@pytest.mark.parametrize("B,W,K,Hkv,D,cap", [(1, 4, 4, 8, 128, 20), (3, 2, 5, 2, 64, 9), (2, 3, 1, 1, 128, 4),
+                                             (8, 4, 8, 4, 128, 300)])
+def test_fork_matches_reference(jf, B, W, K, Hkv, D, cap):
+    rng = np.random.default_rng(cap)
+    lens = rng.integers(0, cap * 16 + 1, B * W)
+    lens[0], lens[-1] = 0, cap * 16            # an empty beam, and one that fills its table
+    if B * W > 4:
+        lens[1], lens[2] = 16, 17
+    pool, parent, fresh = fork_case(cap, B, W, K, Hkv, D, lens, cap)
+    parent.reshape(-1)[0] = 0
+    parent[-1, -1] = W - 1
+    k, v, err = pool.k.cuda(), pool.v.cuda(), new_err()
+    table, new_len = jf.beam_fork_kv(k, v, dev(pool.table), dev(lens.astype(np.int32)), dev(parent), dev(fresh),
+                                     dev_err=err)
+    torch.cuda.synchronize()
+    want_table, want_len, copies = ref.beam_fork(pool.table, lens, parent, fresh)
+    assert err.item() == 0
+    assert (table.cpu().numpy() == want_table).all() and (new_len.cpu().numpy() == want_len).all()
+    for cache, got in ((pool.k, k), (pool.v, v)):
+        bits = cache.view(torch.int16).clone()
+        for to, frm, slots in copies:
+            bits[to, :slots] = cache.view(torch.int16)[frm, :slots]
+        assert torch.equal(got.view(torch.int16).cpu(), bits)
+
+
+def test_fork_reports_bad_input_and_stays_in_bounds(jf):
+    lens = np.array([20, 33, 5, 40], np.int32)
+    pool, parent, fresh = fork_case(2, 2, 2, 2, 2, 64, lens, 4)
+    parent[:] = [[0, 1], [0, 1]]
+    for what, bit in (("parent", jf.DEVERR_BAD_PATH), ("len", jf.DEVERR_BAD_PREFIX), ("fresh", jf.DEVERR_BAD_PAGE),
+                      ("page", jf.DEVERR_BAD_PAGE)):
+        pr, ln, fr, tb = parent.copy(), lens.copy(), fresh.copy(), pool.table.copy()
+        if what == "parent":
+            pr[1, 0] = 2
+        elif what == "len":
+            ln[2] = 65
+        elif what == "fresh":
+            fr[1, 0] = pool.k.shape[0]
+        else:
+            tb[2, 0] = -1
+        k, v, err = pool.k.cuda(), pool.v.cuda(), new_err()
+        table, new_len = jf.beam_fork_kv(k, v, dev(tb), dev(ln), dev(pr), dev(fr), dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() & bit, what
+        want_table, want_len, _ = ref.beam_fork(pool.table, lens, parent, fresh)
+        for j in (0, 1, 3):                    # the other beams are as without it
+            assert (table[j].cpu().numpy() == want_table[j]).all() and new_len[j].item() == want_len[j]
+        if what in ("parent", "len"):
+            assert new_len[2].item() == 0 and (table[2] == -1).all()

@@ -1,0 +1,429 @@
+"""GPU parity of the bounded-cache calls (accumulated attention weight, kept positions,
+eviction) with plain 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+
+pytestmark = pytest.mark.gpu
+PAGE = 16
+
+
+@pytest.fixture(scope="module")
+def jf():
+    from tree_speculative_decoding_jf_gb300 import build
+    build.build()
+    from tree_speculative_decoding_jf_gb300 import jf as mod
+    return mod
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def new_err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+class Pool:
+    """A paged K (and V) pool: every sequence's pages in random order, NaN in every slot that
+    no sequence's first `live` positions use, -1 in the table past a sequence's pages."""
+
+    def __init__(self, rng, live, cap_pages, Hkv, D, spare=0):
+        B = len(live)
+        need = [-(-n // PAGE) for n in live]
+        pages = sum(need) + spare + 3
+        order = rng.permutation(pages).astype(np.int32)
+        self.table = np.full((B, cap_pages), -1, np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.spare = order[at:at + spare]
+        full = torch.full((pages, PAGE, Hkv, D), float("nan"), dtype=torch.bfloat16)
+        self.k, self.v = full.clone(), full.clone()
+        for b, n in enumerate(live):
+            t = np.arange(n)
+            for c in (self.k, self.v):
+                c[self.table[b, t // PAGE], t % PAGE] = torch.from_numpy(
+                    rng.standard_normal((n, Hkv, D)).astype(np.float32)).to(torch.bfloat16)
+
+
+def weight_case(seed, prefix, rows, N, Hq, Hkv, D, path, cap_pages=None, dead_rows=()):
+    """Inputs of one accumulate call and the expected output; rows[b] < 0 clears nothing but
+    gives no rows.  The lse is the exact one of the rows' own keys, rounded to fp32."""
+    rng = np.random.default_rng(seed)
+    B, G, scale = len(prefix), Hq // Hkv, D ** -0.5
+    cap_pages = cap_pages or max(1, max(-(-(p + max(r, 1)) // PAGE) for p, r in zip(prefix, rows)))
+    pool = Pool(rng, [p + r for p, r in zip(prefix, rows)], cap_pages, Hkv, D)
+    q = torch.from_numpy(rng.standard_normal((B, N, Hq, D)).astype(np.float32)).to(torch.bfloat16)
+    qn, kn = q.double().numpy(), pool.k.double().numpy()
+    cap = cap_pages * PAGE
+    weight = rng.random((B, Hkv, cap)).astype(np.float32) * np.float32(0.01)
+    before = np.full((B, Hkv, cap), -7.0, np.float32)
+    lse = np.full((B, Hq, N), np.nan, np.float32)
+    nodes, paths = [], np.full((B, N), -1, np.int32)
+    for b in range(B):
+        R = rows[b]
+        ids = np.concatenate([[0], np.sort(rng.permutation(N - 1)[:R - 1]) + 1])[:R].astype(np.int64) \
+            if path else np.arange(R)
+        paths[b, :R] = ids
+        nodes.append(ids)
+        L = prefix[b] + R
+        kk = ref.rows_of(kn, pool.table[b], np.arange(L)) if L else np.zeros((0, Hkv, D))
+        for k, node in enumerate(ids):
+            for h in range(Hq):
+                s = scale * kk[:prefix[b] + k + 1, h // G] @ qn[b, node, h]
+                m = s.max()
+                lse[b, h, node] = m + np.log(np.exp(s - m).sum())
+            if (b, k) in dead_rows:
+                lse[b, :, node] = -np.inf
+    want = np.empty((B, Hkv, cap))
+    tol = np.empty((B, Hkv, cap))
+    for b in range(B):
+        want[b], tol[b] = ref.attention_weight(qn[b], kn, pool.table[b], prefix[b], nodes[b], lse[b], weight[b],
+                                               before[b], scale)
+    acc = np.array([r - 1 for r in rows], np.int32)
+    return dict(pool=pool, q=q.cuda(), lse=dev(lse), weight=dev(weight), out=dev(before), want=want, tol=tol,
+                path=dev(paths) if path else None, accept_len=dev(acc), prefix=dev(np.array(prefix, np.int32)),
+                table=dev(pool.table), k=pool.k.cuda(), scale=scale, rows=rows, paths=paths)
+
+
+def close(got, want, tol):
+    g = got.cpu().numpy().astype(np.float64)
+    bad = ~(np.abs(g - want) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:5].tolist(), g[bad][:5], want[bad][:5], tol[bad][:5])
+
+
+CASES = [
+    # prefix lengths, rows, N, Hq, Hkv, D, path
+    ([2048], [5], 16, 32, 8, 128, True),
+    ([0], [1], 1, 4, 1, 64, False),                        # a first token
+    ([1], [1], 1, 4, 4, 128, False),                       # G = 1
+    ([130, 0, 15, 16, 700], [3, 1, 0, 9, 17], 20, 8, 2, 64, True),
+    ([127, 128, 129, 1000], [1, 2, 1, 40], 40, 12, 4, 128, True),     # G = 3
+    ([300, 5], [64, 64], 64, 14, 2, 128, False),           # G = 7, 448 rows a kv-head
+    ([37, 513], [200, 200], 200, 8, 1, 64, False),         # 1600 rows a kv-head, window from the start
+    ([900], [33], 256, 40, 8, 128, True),                  # G = 5
+    ([4000, 77], [129, 1], 256, 16, 1, 128, True),         # G = 16, 2064 rows
+    ([31], [300], 300, 2, 2, 128, False),                  # G = 1, long window over a short prefix
+    ([260] * 9, [4] * 9, 8, 4, 2, 64, True),
+    ([20, 0, 3], [0, 0, 0], 4, 4, 2, 128, True),           # nothing accepted anywhere
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_weight_matches_reference(jf, case):
+    prefix, rows, N, Hq, Hkv, D, path = CASES[case]
+    c = weight_case(case, prefix, rows, N, Hq, Hkv, D, path)
+    err = new_err()
+    full = not path and all(r == N for r in rows)
+    got = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=None if full else c["accept_len"], weight=c["weight"],
+                                         scale=c["scale"], out=c["out"], dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(got, c["want"], c["tol"])
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 8), (128, 3)])
+def test_weight_long_cache(jf, D, G):
+    """More key tiles than CTAs of one wave, ragged, with a capacity past the live keys."""
+    prefix, rows = [20011, 1, 9000], [6, 2, 11]
+    c = weight_case(50 + D + G, prefix, rows, 12, G * 2, 2, D, True, cap_pages=1300)
+    err = new_err()
+    jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                   accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"], out=c["out"],
+                                   dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(c["out"], c["want"], c["tol"])
+
+
+def test_weight_rows_that_attended_to_nothing(jf):
+    c = weight_case(3, [100, 40], [5, 3], 8, 8, 2, 64, True, dead_rows={(0, 1), (1, 0), (1, 1), (1, 2)})
+    got = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"])
+    close(got, c["want"], c["tol"])
+
+
+def test_weight_from_zero_in_place_and_repeatable(jf):
+    c = weight_case(4, [333, 64], [7, 2], 9, 8, 2, 128, True)
+    args = (c["q"], c["k"], c["table"], c["prefix"], c["lse"])
+    kw = dict(path=c["path"], accept_len=c["accept_len"], scale=c["scale"])
+    zero = jf.accumulate_attention_weight(*args, **kw)
+    a = jf.accumulate_attention_weight(*args, weight=c["weight"], **kw)
+    b = jf.accumulate_attention_weight(*args, weight=c["weight"], **kw)
+    assert torch.equal(a, b)
+    w = c["weight"].clone()
+    jf.accumulate_attention_weight(*args, weight=w, out=w, **kw)
+    for s, (P, R) in enumerate(zip([333, 64], [7, 2])):
+        assert torch.equal(w[s, :, :P + R], a[s, :, :P + R])
+        assert torch.equal(w[s, :, P + R:], c["weight"][s, :, P + R:])
+        assert (zero[s, :, P + R:] == 0).all()
+        close(zero[s, :, :P + R], c["want"][s, :, :P + R] - np.where(
+            np.arange(P + R) < P, c["weight"][s, :, :P + R].cpu().numpy().astype(np.float64), 0.0),
+            c["tol"][s, :, :P + R] + 2.0 ** -23)
+
+
+@pytest.mark.parametrize("seed,D,G", [(0, 64, 4), (1, 128, 8), (2, 128, 6)])
+def test_weight_packed_equals_padded(jf, seed, D, G):
+    """Packed rows give the padded call's bits."""
+    sizes, prefix, rows, N = [5, 40, 1, 17], [100, 3, 700, 0], [2, 30, 1, 0], 40
+    c = weight_case(seed + 20, prefix, rows, N, G * 2, 2, D, True)
+    for b, n in enumerate(sizes):                          # paths inside each tree's own nodes
+        ids = np.arange(rows[b])
+        c["paths"][b] = -1
+        c["paths"][b, :rows[b]] = ids
+    path = dev(c["paths"])
+    lse = torch.nan_to_num(c["lse"], nan=3.0)
+    kw = dict(path=path, accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    pad = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], lse, **kw)
+    at = torch.cat([torch.arange(n) + b * N for b, n in enumerate(sizes)]).cuda()
+    qp = c["q"].flatten(0, 1)[at].contiguous()
+    lp = lse.transpose(0, 1).flatten(1)[:, at].contiguous()
+    cu = dev(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32))
+    err = new_err()
+    got = jf.accumulate_attention_weight(qp, c["k"], c["table"], c["prefix"], lp, cu_seqlens=cu, dev_err=err, **kw)
+    assert torch.equal(got, pad) and err.item() == 0
+    # every node a row: spans are the row counts
+    cu2 = dev(np.array([0, 5, 5, 6, 23], np.int32))        # the second span is empty: bad
+    err = new_err()
+    pool = c["pool"]
+    got = jf.accumulate_attention_weight(qp, c["k"], c["table"], dev(np.zeros(4, np.int32)), lp, cu_seqlens=cu2,
+                                         scale=c["scale"], path=None, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() & jf.DEVERR_BAD_TREE_LEN
+    assert (got[1] == 0).all() and pool is c["pool"]
+
+
+def test_weight_reports_bad_input_and_stays_in_bounds(jf):
+    c = weight_case(8, [100, 50, 60, 30], [3, 3, 3, 3], 6, 4, 2, 64, True, cap_pages=7)
+    for what, bit in (("prefix", jf.DEVERR_BAD_PREFIX), ("neg", jf.DEVERR_BAD_PREFIX), ("acc", jf.DEVERR_BAD_PATH),
+                      ("path", jf.DEVERR_BAD_PATH), ("page", jf.DEVERR_BAD_PAGE), ("page2", jf.DEVERR_BAD_PAGE)):
+        prefix, acc, path, table = (c[k].clone() for k in ("prefix", "accept_len", "path", "table"))
+        if what == "prefix":
+            prefix[1] = 7 * 16 - 1
+        elif what == "neg":
+            prefix[1] = -5
+        elif what == "acc":
+            acc[1] = 6
+        elif what == "path":
+            path[1, 1] = 6
+        else:
+            table[1, 1] = -1 if what == "page" else c["k"].shape[0]
+        err, out = new_err(), c["out"].clone()
+        jf.accumulate_attention_weight(c["q"], c["k"], table, prefix, c["lse"], path=path, accept_len=acc,
+                                       weight=c["weight"], scale=c["scale"], out=out, dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() & bit, what
+        for b in (0, 2, 3):                                # the other sequences are as without it
+            close(out[b], c["want"][b], c["tol"][b])
+
+
+def test_weight_on_another_stream_and_in_a_graph(jf):
+    c = weight_case(9, [1000, 1500], [4, 2], 8, 8, 2, 128, True)
+    args = (c["q"], c["k"], c["table"], c["prefix"], c["lse"])
+    kw = dict(path=c["path"], accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    want = jf.accumulate_attention_weight(*args, out=c["out"].clone(), **kw)
+    s = torch.cuda.Stream()
+    out = c["out"].clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        jf.accumulate_attention_weight(*args, out=out, **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, want)
+    out.fill_(-7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        jf.accumulate_attention_weight(*args, out=out, **kw)
+    for _ in range(2):
+        out.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------------- kept positions
+
+def run_select(jf, w, L, budget, sink, recent):
+    err = new_err()
+    keep, kept = jf.select_kept_keys(dev(w), dev(np.array(L, np.int32)), budget, sink=sink, recent=recent, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    want, want_len = ref.select_kept(w, np.array(L, np.int32), sink, recent, budget)
+    assert (kept.cpu().numpy() == want_len).all()
+    assert (keep.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("L,budget,sink,recent", [
+    ([2304], 2048, 4, 64), ([1, 0, 16, 500], 16, 0, 0), ([33, 100], 1, 0, 0), ([33, 100], 1, 1, 0),
+    ([33, 100], 1, 0, 1), ([700, 701], 20, 10, 10), ([700, 300], 699, 3, 5), ([4097, 513, 512, 511], 500, 4, 32),
+    ([9000, 8193, 20000], 3000, 2, 100),
+])
+@pytest.mark.parametrize("kind", ["weights", "ties"])
+def test_select_matches_reference(jf, L, budget, sink, recent, kind):
+    rng = np.random.default_rng(len(L) * 1000 + budget)
+    w = np.exp(1.5 * rng.standard_normal((len(L), 3, -(-max(L) // PAGE) * PAGE + PAGE))).astype(np.float32)
+    if kind == "ties":
+        w = np.floor(w).astype(np.float32)
+    run_select(jf, w, L, budget, sink, recent)
+
+
+def test_select_special_values(jf):
+    """NaN below -inf, -0 equal to +0, infinities, one value everywhere, ordered rows."""
+    rng = np.random.default_rng(1)
+    n = 1000
+    rows = [np.zeros(n), np.where(rng.random(n) < 0.5, -0.0, 0.0), np.full(n, np.nan),
+            rng.choice([np.nan, -np.inf, np.inf, 0.0, -1.0, 1.0, 1e-45, -1e-45], n), np.arange(n) * 1.0,
+            -np.arange(n) * 1.0, np.full(n, -np.inf), rng.standard_normal(n) * 1e38]
+    w = np.array(rows, np.float32)[None].repeat(2, 0)
+    w = np.pad(w, ((0, 0), (0, 0), (0, 8)))
+    for budget, sink, recent in ((400, 5, 7), (1, 0, 0), (999, 0, 0), (12, 5, 7)):
+        run_select(jf, w, [n, n - 3], budget, sink, recent)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_select_long_rows(jf, rows):
+    """Rows longer than a cluster holds at once, and clusters of every size."""
+    rng = np.random.default_rng(rows)
+    w = rng.random((rows, 1, 80000 if rows == 1 else 17008)).astype(np.float32)
+    L = [79999] if rows == 1 else [17008 - 400 * i for i in range(rows)]
+    run_select(jf, w, L, 30000 if rows == 1 else 5000, 4, 100)
+    w[:] = np.floor(w * 3)
+    run_select(jf, w, L, 30000 if rows == 1 else 5000, 4, 100)
+
+
+def test_select_clamps_lengths(jf):
+    w = np.random.default_rng(0).random((2, 2, 64)).astype(np.float32)
+    err = new_err()
+    keep, kept = jf.select_kept_keys(dev(w), dev(np.array([-3, 70], np.int32)), 8, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() & jf.DEVERR_BAD_PREFIX
+    assert kept.tolist() == [0, 8] and (keep[0] == -1).all() and keep[1].max().item() < 64
+
+
+# ------------------------------------------------------------------------------------ eviction
+
+def evict_case(seed, lens, budget, Hkv, D, out_of_place, kind="random", weights=True):
+    rng = np.random.default_rng(seed)
+    B, cap_pages = len(lens), max(1, -(-max(max(lens), budget) // PAGE))
+    per = -(-min(budget, max(lens)) // PAGE)
+    pool = Pool(rng, lens, cap_pages, Hkv, D, spare=per * B if out_of_place else 0)
+    new_table = pool.table
+    if out_of_place:
+        new_table = np.full((B, cap_pages), -1, np.int32)
+        new_table[:, :per] = pool.spare.reshape(B, per)
+    keep = np.full((B, Hkv, budget), -1, np.int32)
+    kept = np.minimum(lens, budget).astype(np.int32)
+    for b, L in enumerate(lens):
+        for g in range(Hkv):
+            n = int(kept[b])
+            keep[b, g, :n] = {"random": np.sort(rng.permutation(L)[:n]), "last": np.arange(L - n, L),
+                              "first": np.arange(n)}[kind]
+    weight = rng.random((B, Hkv, cap_pages * PAGE)).astype(np.float32) if weights else None
+    return pool, new_table, keep, kept, weight
+
+
+@pytest.mark.parametrize("lens,budget,Hkv,D,kind", [
+    ([2304], 2048, 8, 128, "random"), ([2304], 2048, 8, 128, "last"), ([100, 7, 0, 16], 20, 2, 64, "random"),
+    ([500, 333], 120, 3, 128, "random"), ([3000, 2999], 2990, 1, 64, "last"), ([64, 65], 64, 2, 128, "first"),
+    ([33], 1, 1, 64, "last"), ([5000, 1, 4096], 1000, 4, 128, "random"), ([40], 64, 2, 64, "random"),
+])
+@pytest.mark.parametrize("out_of_place", [False, True])
+def test_evict_matches_reference(jf, lens, budget, Hkv, D, kind, out_of_place):
+    pool, new_table, keep, kept, weight = evict_case(budget, lens, budget, Hkv, D, out_of_place, kind)
+    bits = lambda t: t.view(torch.int16).numpy()   # noqa: E731
+    rk, rv, rw = ref.evict_kv(bits(pool.k), bits(pool.v), pool.table, new_table, keep, kept, weight)
+    k, v, w, err = pool.k.cuda(), pool.v.cuda(), dev(weight), new_err()
+    got = jf.evict_kv(k, v, dev(pool.table), dev(np.array(lens, np.int32)), dev(keep), dev(kept),
+                      new_block_table=dev(new_table) if out_of_place else None, weight=w, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and (got.cpu().numpy() == kept).all()
+    assert (bits(k.cpu()) == rk).all() and (bits(v.cpu()) == rv).all()
+    assert (w.cpu().numpy() == rw).all()
+
+
+def test_evict_weights_to_another_array_or_none(jf):
+    pool, table, keep, kept, weight = evict_case(2, [300, 200], 100, 2, 64, False)
+    bits = lambda t: t.view(torch.int16).numpy()   # noqa: E731
+    rk, _, rw = ref.evict_kv(bits(pool.k), bits(pool.v), table, table, keep, kept, weight)
+    for with_weight in (True, False):
+        k, v, out = pool.k.cuda(), pool.v.cuda(), torch.full(weight.shape, -3.0, device="cuda")
+        jf.evict_kv(k, v, dev(table), dev(np.array([300, 200], np.int32)), dev(keep), dev(kept),
+                    weight=dev(weight) if with_weight else None, weight_out=out if with_weight else None)
+        torch.cuda.synchronize()
+        assert (bits(k.cpu()) == rk).all()
+        if with_weight:
+            assert (out[..., :100].cpu().numpy() == rw[..., :100]).all() and (out[..., 100:] == -3.0).all()
+
+
+def test_evict_reports_bad_input_and_stays_in_bounds(jf):
+    pool, table, keep, kept, weight = evict_case(5, [300, 200], 100, 2, 64, False)
+    L = np.array([300, 200], np.int32)
+    bits = lambda t: t.view(torch.int16).numpy()   # noqa: E731
+    rk, rv, rw = ref.evict_kv(bits(pool.k), bits(pool.v), table, table, keep, kept, weight)
+    for what, bit in (("order", jf.DEVERR_BAD_PATH), ("past", jf.DEVERR_BAD_PATH), ("low", jf.DEVERR_BAD_PATH),
+                      ("kept", jf.DEVERR_BAD_PATH), ("len", jf.DEVERR_BAD_PREFIX), ("page", jf.DEVERR_BAD_PAGE)):
+        kp, kl, sl, tb = keep.copy(), kept.copy(), L.copy(), table.copy()
+        if what == "order":
+            kp[1, 0, 50] = kp[1, 0, 49]
+        elif what == "past":
+            kp[1, 0, 99] = 200
+        elif what == "low":
+            kp[1, 1, 0] = -1
+        elif what == "kept":
+            kl[1] = 101
+        elif what == "len":
+            sl[1] = -1
+        else:
+            tb[1, 12] = pool.k.shape[0] + 5
+            kp[1, :, 99] = 199
+        k, v, w, err = pool.k.cuda(), pool.v.cuda(), dev(weight), new_err()
+        jf.evict_kv(k, v, dev(tb), dev(sl), dev(kp), dev(kl), weight=w, dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() & bit, what
+        own = table[0][table[0] >= 0]
+        assert (bits(k.cpu())[own] == rk[own]).all() and (w[0].cpu().numpy() == rw[0]).all()
+        other = np.setdiff1d(np.arange(pool.k.shape[0]), table[table >= 0])
+        assert (bits(v.cpu())[other] == bits(pool.v)[other]).all()
+
+
+def test_pages_past_four_gigabytes(jf):
+    """Page ids whose byte offsets pass 32 bits, in every call that reads or moves pages."""
+    Hkv, D, pages = 8, 128, 140000                          # 16 KB pages of one head set: 4.6 GB a pool
+    k = torch.zeros((pages, PAGE, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    rng = np.random.default_rng(0)
+    table = np.array([[139999, 3, 139990, 131072]], np.int32)
+    P, R, N = 50, 2, 2
+    t = np.arange(P + R)
+    new = torch.from_numpy(rng.standard_normal((2, P + R, Hkv, D)).astype(np.float32)).to(torch.bfloat16)
+    idx = dev(table[0][t // PAGE].astype(np.int64)), dev(t % PAGE)
+    k[idx], v[idx] = new[0].cuda(), new[1].cuda()
+    q = torch.from_numpy(rng.standard_normal((1, N, 16, D)).astype(np.float32)).to(torch.bfloat16)
+    lse = rng.random((1, 16, N)).astype(np.float32) + 4
+    small = np.zeros((4, PAGE, Hkv, D))
+    small.reshape(-1, Hkv, D)[:P + R] = new[0].double().numpy()
+    want, tol = ref.attention_weight(q[0].double().numpy(), small, np.arange(4), P, np.arange(R), lse[0], None,
+                                     np.zeros((Hkv, 64)), D ** -0.5)
+    err = new_err()
+    got = jf.accumulate_attention_weight(q.cuda(), k, dev(table), dev(np.array([P], np.int32)), dev(lse), dev_err=err)
+    close(got[0], want, tol)
+    keep, kept = jf.select_kept_keys(got, dev(np.array([P + R], np.int32)), 20)
+    jf.evict_kv(k, v, dev(table), dev(np.array([P + R], np.int32)), keep, kept, weight=got, dev_err=err)
+    torch.cuda.synchronize()
+    kp = keep[0].cpu().numpy()
+    for g in range(Hkv):
+        for j in range(20):
+            assert torch.equal(k[table[0, j // PAGE], j % PAGE, g].cpu(), new[0][kp[g, j], g])
+            assert torch.equal(v[table[0, j // PAGE], j % PAGE, g].cpu(), new[1][kp[g, j], g])
+    fresh = torch.tensor([[139000, 138000]], dtype=torch.int32, device="cuda")
+    nt, nl = jf.beam_fork_kv(k, v, dev(table), dev(np.array([20], np.int32)), torch.zeros((1, 2), dtype=torch.int32,
+                             device="cuda"), fresh, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and nl.tolist() == [20, 20]
+    assert nt.tolist() == [[139999, 139000, -1, -1], [139999, 138000, -1, -1]]
+    assert torch.equal(k[139000, :4], k[3, :4]) and torch.equal(v[138000, :4], v[3, :4])

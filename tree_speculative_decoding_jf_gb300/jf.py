@@ -101,6 +101,20 @@ def _load():
     lib.jf_tree_verify_sampled_packed.argtypes = [P, i32, P, P, P, P, P, f32, i32, i32, i32, i32,
                                                   P, P, P, P, sz, P, P]
     lib.jf_tree_verify_sampled_packed.restype = ctypes.c_int
+    lib.jf_attention_weight.argtypes = [P, P, P, P, P, P, P, P] + [i32] * 8 + [f32, P, P, P]
+    lib.jf_attention_weight.restype = ctypes.c_int
+    lib.jf_attention_weight_packed.argtypes = [P, P, P, P, P, P, P, P, P] + [i32] * 9 + [f32, P, P, P]
+    lib.jf_attention_weight_packed.restype = ctypes.c_int
+    lib.jf_select_kept.argtypes = [P, P] + [i32] * 6 + [P, P, P, P]
+    lib.jf_select_kept.restype = ctypes.c_int
+    lib.jf_evict_kv.argtypes = [P, P, P, P, P, P, P, P, P] + [i32] * 7 + [P, P]
+    lib.jf_evict_kv.restype = ctypes.c_int
+    lib.jf_beam_select_workspace_size.argtypes = [i32] * 5
+    lib.jf_beam_select_workspace_size.restype = sz
+    lib.jf_beam_select.argtypes = [P, i32, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, sz, P]
+    lib.jf_beam_select.restype = ctypes.c_int
+    lib.jf_beam_fork_kv.argtypes = [P, P, P, P, P, P] + [i32] * 8 + [P, P, P, P]
+    lib.jf_beam_fork_kv.restype = ctypes.c_int
     return lib
 
 
@@ -618,6 +632,151 @@ def jf_build_draft_tree_ragged(draft_logits, K, N, budget, cand_token, cand_logp
         _ptr(dev_err), _stream(stream)))
 
 
+def _need_all(dtype_shapes, dev_err=None):
+    """Checks of the cache and beam calls: _need for each (name, tensor, dtype, shape) whose
+    tensor is given, and one device, the current one, for all of them."""
+    cur = torch.cuda.current_device()
+    for name, t, dtype, shape in dtype_shapes:
+        if t is None:
+            continue
+        _need(t, name, dtype, shape)
+        if t.device.index != cur:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{cur}")
+    if dev_err is not None:
+        _need(dev_err, "dev_err", torch.int32, (1,))
+        if dev_err.device.index != cur:
+            raise ValueError(f"dev_err is on cuda:{dev_err.device.index}, the current device is cuda:{cur}")
+
+
+def jf_attention_weight(q, k_cache, block_table, prefix_len, lse, weight_out, scale, path=None,
+                        accept_len=None, weight=None, dev_err=None, stream=None) -> None:
+    """Adds the attention probabilities that every cached key received (see include/jf.h)."""
+    B, N, Hq, D = q.shape
+    num_pages, page, Hkv, D2 = k_cache.shape
+    max_pages = block_table.shape[1]
+    if D2 != D:
+        raise ValueError("q and k_cache head dims differ")
+    wshape = (B, Hkv, max_pages * page)
+    _need_all((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+               ("block_table", block_table, torch.int32, (B, max_pages)),
+               ("prefix_len", prefix_len, torch.int32, (B,)),
+               ("lse", lse, torch.float32, (B, Hq, N)), ("path", path, torch.int32, (B, N)),
+               ("accept_len", accept_len, torch.int32, (B,)),
+               ("weight", weight, torch.float32, wshape),
+               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    _check("jf_attention_weight", _lib.jf_attention_weight(
+        _ptr(q), _ptr(k_cache), _ptr(block_table), _ptr(prefix_len), _ptr(path), _ptr(accept_len),
+        _ptr(lse), _ptr(weight), B, N, Hq, Hkv, D, page, max_pages, num_pages, float(scale),
+        _ptr(weight_out), _ptr(dev_err), _stream(stream)))
+
+
+def jf_attention_weight_packed(q, k_cache, block_table, prefix_len, cu_seqlens, lse, weight_out,
+                               scale, N_max, path=None, accept_len=None, weight=None,
+                               dev_err=None, stream=None) -> None:
+    """jf_attention_weight on packed rows: q [T][Hq][D], lse [Hq][T], path [B][N_max]."""
+    T, Hq, D = q.shape
+    B, max_pages = block_table.shape
+    num_pages, page, Hkv, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("q and k_cache head dims differ")
+    wshape = (B, Hkv, max_pages * page)
+    _need_all((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+               ("block_table", block_table, torch.int32, None),
+               ("prefix_len", prefix_len, torch.int32, (B,)),
+               ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)),
+               ("lse", lse, torch.float32, (Hq, T)), ("path", path, torch.int32, (B, N_max)),
+               ("accept_len", accept_len, torch.int32, (B,)),
+               ("weight", weight, torch.float32, wshape),
+               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    _check("jf_attention_weight_packed", _lib.jf_attention_weight_packed(
+        _ptr(q), _ptr(k_cache), _ptr(block_table), _ptr(prefix_len), _ptr(cu_seqlens), _ptr(path),
+        _ptr(accept_len), _ptr(lse), _ptr(weight), B, N_max, T, Hq, Hkv, D, page, max_pages,
+        num_pages, float(scale), _ptr(weight_out), _ptr(dev_err), _stream(stream)))
+
+
+def jf_select_kept(weight, seq_len, keep, kept_len, sink=0, recent=0, dev_err=None,
+                   stream=None) -> None:
+    """The positions a cache of keep.shape[-1] keys keeps (see include/jf.h)."""
+    B, Hkv, capacity = weight.shape
+    budget = keep.shape[-1]
+    _need_all((("weight", weight, torch.float32, None), ("seq_len", seq_len, torch.int32, (B,)),
+               ("keep", keep, torch.int32, (B, Hkv, budget)),
+               ("kept_len", kept_len, torch.int32, (B,))), dev_err)
+    _check("jf_select_kept", _lib.jf_select_kept(
+        _ptr(weight), _ptr(seq_len), B, Hkv, capacity, int(sink), int(recent), budget, _ptr(keep),
+        _ptr(kept_len), _ptr(dev_err), _stream(stream)))
+
+
+def jf_evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_block_table=None,
+                weight=None, weight_out=None, dev_err=None, stream=None) -> None:
+    """Moves the kept rows to the front of the cache (see include/jf.h)."""
+    num_pages, page, Hkv, D = k_cache.shape
+    B, max_pages = block_table.shape
+    budget = keep.shape[-1]
+    wshape = (B, Hkv, max_pages * page)
+    _need_all((("k_cache", k_cache, torch.bfloat16, None),
+               ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+               ("block_table", block_table, torch.int32, None),
+               ("seq_len", seq_len, torch.int32, (B,)),
+               ("keep", keep, torch.int32, (B, Hkv, budget)),
+               ("kept_len", kept_len, torch.int32, (B,)),
+               ("new_block_table", new_block_table, torch.int32, (B, max_pages)),
+               ("weight", weight, torch.float32, wshape),
+               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    _check("jf_evict_kv", _lib.jf_evict_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_len), _ptr(keep), _ptr(kept_len),
+        _ptr(new_block_table), _ptr(weight), _ptr(weight_out), B, Hkv, D, budget, page, max_pages,
+        num_pages, _ptr(dev_err), _stream(stream)))
+
+
+def jf_beam_select_workspace_size(B, W, V, K, dtype) -> int:
+    n = _lib.jf_beam_select_workspace_size(B, W, V, K, dtype)
+    if n == SIZE_MAX:
+        raise JFError("jf_beam_select_workspace_size", 3)
+    return int(n)
+
+
+def jf_beam_select(logits, score, parent, token, new_score, workspace, finished=None,
+                   eos_token=-1, new_finished=None, stream=None) -> None:
+    """The best (beam, token) pairs of every prompt (see include/jf.h)."""
+    B, W, V = logits.shape
+    K = parent.shape[-1]
+    dt = _logit_dtype(logits)
+    _need_all((("logits", logits, logits.dtype, None), ("score", score, torch.float32, (B, W)),
+               ("finished", finished, torch.int32, (B, W)),
+               ("parent", parent, torch.int32, (B, K)), ("token", token, torch.int32, (B, K)),
+               ("new_score", new_score, torch.float32, (B, K)),
+               ("new_finished", new_finished, torch.int32, (B, K)),
+               ("workspace", workspace, torch.uint8, None)))
+    _check("jf_beam_select", _lib.jf_beam_select(
+        _ptr(logits), dt, _ptr(score), _ptr(finished), int(eos_token), B, W, V, K, _ptr(parent),
+        _ptr(token), _ptr(new_score), _ptr(new_finished), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+
+
+def jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page,
+                    new_block_table, new_prefix_len, dev_err=None, stream=None) -> None:
+    """Block tables of the new beams, with their partial pages copied (see include/jf.h)."""
+    num_pages, page, Hkv, D = k_cache.shape
+    rows, max_pages = block_table.shape
+    B, K = parent.shape
+    if B < 1 or rows % B != 0:
+        raise ValueError(f"block_table has {rows} rows, not a multiple of {B} prompts")
+    W = rows // B
+    _need_all((("k_cache", k_cache, torch.bfloat16, None),
+               ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+               ("block_table", block_table, torch.int32, None),
+               ("prefix_len", prefix_len, torch.int32, (B * W,)),
+               ("parent", parent, torch.int32, (B, K)),
+               ("fresh_page", fresh_page, torch.int32, (B, K)),
+               ("new_block_table", new_block_table, torch.int32, (B * K, max_pages)),
+               ("new_prefix_len", new_prefix_len, torch.int32, (B * K,))), dev_err)
+    _check("jf_beam_fork_kv", _lib.jf_beam_fork_kv(
+        _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(prefix_len), _ptr(parent),
+        _ptr(fresh_page), B, W, K, Hkv, D, page, max_pages, num_pages, _ptr(new_block_table),
+        _ptr(new_prefix_len), _ptr(dev_err), _stream(stream)))
+
+
 # ----------------------------------------------------------------------------- conveniences
 
 def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
@@ -739,3 +898,72 @@ def build_draft_tree(draft_logits, K, N, root_token=None, stream=None):
                         root_token, score, stream)
     return parent, draft, depth, score, cand_token, cand_logp
 
+
+def accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path=None,
+                                accept_len=None, weight=None, scale=None, cu_seqlens=None,
+                                out=None, dev_err=None, stream=None):
+    """Accumulated attention weight [B][Hkv][max_pages * page] after this step: weight (zeros
+    if None) plus what the step's rows gave every key.  Written to out if given (out may be
+    weight), else to a new tensor.  With cu_seqlens, q and lse are packed; N_max is then the
+    path's width, or without a path the number of packed rows."""
+    D = q.shape[-1]
+    Hkv, page = k_cache.shape[2], k_cache.shape[1]
+    B, max_pages = block_table.shape
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.zeros((B, Hkv, max_pages * page), dtype=torch.float32, device=q.device)
+    if cu_seqlens is None:
+        jf_attention_weight(q, k_cache, block_table, prefix_len, lse, out, scale, path, accept_len,
+                            weight, dev_err, stream)
+    else:
+        N_max = path.shape[1] if path is not None else min(q.shape[0], MAX_NODES)
+        jf_attention_weight_packed(q, k_cache, block_table, prefix_len, cu_seqlens, lse, out, scale,
+                                   N_max, path, accept_len, weight, dev_err, stream)
+    return out
+
+
+def select_kept_keys(weight, seq_len, budget, sink=0, recent=0, dev_err=None, stream=None):
+    """(keep [B][Hkv][budget], kept_len [B]): the positions that stay, by weight."""
+    B, Hkv, _ = weight.shape
+    keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weight.device)
+    kept_len = torch.empty((B,), dtype=torch.int32, device=weight.device)
+    jf_select_kept(weight, seq_len, keep, kept_len, sink, recent, dev_err, stream)
+    return keep, kept_len
+
+
+def evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_block_table=None,
+             weight=None, weight_out=None, dev_err=None, stream=None):
+    """Moves the kept rows to the front, in place or into new_block_table's pages; the weights
+    likewise (in place if weight_out is None).  Returns kept_len, the new lengths."""
+    if weight is not None and weight_out is None:
+        weight_out = weight
+    jf_evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_block_table, weight,
+                weight_out, dev_err, stream)
+    return kept_len
+
+
+def beam_select(logits, score, K, finished=None, eos_token=-1, stream=None):
+    """(parent, token, score, finished), each [B][K]: the K best continuations of every prompt."""
+    B, W, V = logits.shape
+    dev = logits.device
+    parent = torch.empty((B, K), dtype=torch.int32, device=dev)
+    token = torch.empty((B, K), dtype=torch.int32, device=dev)
+    new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
+    new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
+    ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
+    jf_beam_select(logits, score, parent, token, new_score, ws, finished, eos_token, new_finished,
+                   stream)
+    return parent, token, new_score, new_finished
+
+
+def beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, dev_err=None,
+                 stream=None):
+    """(block_table [B * K][max_pages], prefix_len [B * K]) of the new beams."""
+    B, K = parent.shape
+    new_table = torch.empty((B * K, block_table.shape[1]), dtype=torch.int32,
+                            device=block_table.device)
+    new_len = torch.empty((B * K,), dtype=torch.int32, device=block_table.device)
+    jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, new_table,
+                    new_len, dev_err, stream)
+    return new_table, new_len
