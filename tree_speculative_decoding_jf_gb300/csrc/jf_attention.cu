@@ -59,6 +59,7 @@
 
 #include "jf_common.cuh"
 #include "jf_sm100.cuh"
+#include "jf_tensormap.cuh"
 
 namespace jf {
 namespace {
@@ -149,23 +150,11 @@ __device__ __forceinline__ int tree_nodes(const int32_t* tree_len, int b, int N)
   return tree_len == nullptr ? N : max(1, min(tree_len[b], N));
 }
 
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          uint64_t wlim) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, wlim) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  return ok != 0;
-}
-
 __device__ __forceinline__ void set_abort(volatile int* abort, int32_t* dev_err) {
   if (*abort == 0) {
     *abort = 1;
     report(dev_err, JF_DEVERR_TIMEOUT);
   }
-}
-
-__device__ __forceinline__ void named_bar(int id, int count) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // Named barrier that also ANDs a predicate over the participating threads.
@@ -182,25 +171,7 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool pred) {
   return r != 0;
 }
 
-// Paired fp32 arithmetic (one instruction for two lanes of data) and a 3-input max.
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+// A 3-input max.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -1995,31 +1966,6 @@ bool plan_attention(int B, int N, int Hq, int Hkv, int D, int max_pages, int sms
                        sizeof(float) + static_cast<size_t>(pl->nvirt) * 8 * sizeof(int) + 256;
   }
   return true;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box,
-            CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  return fn(m, dt, rank, const_cast<void*>(base), dims, strides, box,
-            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NT, int D, bool LPT>
