@@ -150,27 +150,6 @@ __device__ __forceinline__ int tree_nodes(const int32_t* tree_len, int b, int N)
   return tree_len == nullptr ? N : max(1, min(tree_len[b], N));
 }
 
-__device__ __forceinline__ void set_abort(volatile int* abort, int32_t* dev_err) {
-  if (*abort == 0) {
-    *abort = 1;
-    report(dev_err, JF_DEVERR_TIMEOUT);
-  }
-}
-
-// Named barrier that also ANDs a predicate over the participating threads.
-__device__ __forceinline__ bool named_bar_and(int id, int count, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
 // A 3-input max.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

@@ -506,9 +506,8 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   const size_t room = std::max(static_cast<size_t>(lists) * first, static_cast<size_t>(K) * K);
   const size_t smem = sizeof(double) * (W + (W + 1) / 2) + room * (sizeof(uint64_t) + sizeof(uint32_t));
   if (smem > 200 * 1024) return JF_ERR_UNSUPPORTED;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (attr != cudaSuccess) return JF_ERR_CUDA;
+  static SmemAttr attr;
+  if (!attr.ensure(beam_merge_kernel, 200 * 1024)) return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(rows * pl.chunks);
   cudaError_t e = dtype == JF_DTYPE_BF16 ? launch_scan<uint16_t>(p, pl.nv, grid, s)

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "jf.h"
 
 namespace jf {
@@ -69,6 +71,29 @@ __device__ __forceinline__ void grid_dependency_wait() {
 __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+
+// Raises a kernel's dynamic shared-memory limit once per device (a static of the launching
+// function).
+class SmemAttr {
+ public:
+  template <typename Kernel>
+  bool ensure(Kernel* kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    std::lock_guard<std::mutex> lock(mu_);
+    if (dev < 64 && done_[dev]) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    if (dev < 64) done_[dev] = true;
+    return true;
+  }
+
+ private:
+  std::mutex mu_;
+  bool done_[64] = {false};
+};
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,

@@ -5,21 +5,66 @@
 //     sum_{k < R_b} sum_{h in group g} [t <= P_b + k] exp(scale q_kh . K_t - lse_kh),
 // where lse is what the attention call left, so no softmax statistics are formed here and
 // every key is independent: no reduction crosses keys.
+//
+// The scores are taken transposed, S^T = K Q^T: a 128-key tile is the A operand, a block of
+// up to 128 query rows (row = k * G + head in group) the B operand, and a TMEM lane is a
+// key.  So the thread that owns a lane owns its key: it adds its probabilities in registers
+// over all row blocks and writes the key's weight once.  K is read once, nothing is merged
+// between CTAs, and the order of every sum is fixed.
+//
+// Work: the tiles of all (sequence, kv-head) pairs lie end to end, a tile weighted by its
+// row blocks, and each CTA (one per SM) takes an equal range.  Up to four consecutive tiles
+// of a pair form a group that shares every row block loaded; with one row block (a verified
+// path) it stays in shared memory for the whole run of the pair.
+//
+// Roles (768 threads):
+//   warp 0       K tiles by TMA into a ring, page ids one tile ahead; pages past the end
+//                and malformed ids load as zeros.
+//   warp 1       allocates TMEM, issues the MMAs.
+//   warps 4..7   gather the query rows (path, heads, packed layouts) with 16-byte
+//                asynchronous copies into the swizzled B layout, and the rows' lse.
+//   warps 8..23  four warpgroups, one per TMEM slot (128 columns): tile c of the CTA goes
+//                to slot c % 4.
+// Slots past a block's rows and rows whose lse is -inf get zero queries and lse = +inf, so
+// they add exp(-inf) = 0.  Keys past the sequence's end are lanes whose sum is dropped:
+// whatever their page slots hold stays in their lane.
+// All waits are bounded; on a timeout the CTA records JF_DEVERR_TIMEOUT, drains its copies
+// and MMAs, frees TMEM and returns.
 #include <algorithm>
 #include <cmath>
 
 #include "jf_common.cuh"
+#include "jf_sm100.cuh"
+#include "jf_tensormap.cuh"
 
 namespace jf {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kKeys = 128;             // keys (threads) per CTA
+constexpr int kKeyTile = 128;
+constexpr int kPagesPerTile = kKeyTile / kPage;
+constexpr int kRowBlock = 128;
+constexpr int kSlots = 4;                 // TMEM slots = epilogue warpgroups
+constexpr int kGroup = kSlots;            // key tiles that share a loaded row block
+constexpr int kThreads = 768;
+constexpr int kQWarp = 4, kEpiWarp = 8;   // first warps of the two roles
 constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kKeyTile * D * 2;
+  static constexpr int kHalfBytes = kKeyTile * 128;
+  // 160 KB of K in flight, far above the ~45 KB an SM needs to cover the latency of HBM at
+  // its share of the bandwidth, and a group's four tiles plus the next one for D = 128.
+  static constexpr int kKStages = D == 128 ? 5 : 10;
+  static constexpr int kQStages = 2;
+  static constexpr int kQOff = kKStages * kTileBytes;
+  static constexpr int kSmemBytes = kQOff + kQStages * kTileBytes + 1024;
+};
 
 struct WeightParams {
   const uint16_t* q;
-  const uint16_t* k_cache;
   const int32_t* block_table;
   const int32_t* prefix_len;
   const int32_t* path;        // or null: row k is node k
@@ -30,80 +75,471 @@ struct WeightParams {
   float* weight_out;
   int32_t* dev_err;
   long long T;
-  int B, N, Hq, Hkv, max_pages, num_pages;
+  int B, N, Hq, Hkv, G, max_pages, num_pages;
   float scale_log2;
 };
 
-__device__ __forceinline__ float bf16_f32(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
+struct SeqInfo {
+  long long row0;             // first row of the sequence in q
+  int n, P, R, L;             // nodes, prefix, query rows, keys
+  int tiles, blocks, unit;    // key tiles and row blocks of a kv-head, cost of a tile
+  int bits;
+};
 
-template <int D>
-__global__ void __launch_bounds__(kKeys) weight_kernel(const WeightParams p) {
-  __shared__ float s_q[D];
-  grid_dependency_wait();
-  const int b = blockIdx.z, g = blockIdx.y, t0 = blockIdx.x * kKeys, t = t0 + threadIdx.x;
-  const int G = p.Hq / p.Hkv, cap = p.max_pages * kPage;
+__device__ __forceinline__ SeqInfo seq_info(const WeightParams& p, int b) {
+  SeqInfo s;
+  const int cap = p.max_pages * kPage;
   const SeqSpan sp = seq_span(p.cu, nullptr, b, p.N, p.T);
-  int bits = sp.ok ? 0 : JF_DEVERR_BAD_TREE_LEN;
-  int R = p.accept_len == nullptr ? sp.n : p.accept_len[b] + 1;
-  if (R < 0 || R > sp.n) {
-    if (sp.ok) bits |= JF_DEVERR_BAD_PATH;
-    R = max(0, min(R, sp.n));
+  s.bits = sp.ok ? 0 : JF_DEVERR_BAD_TREE_LEN;
+  s.row0 = sp.row0;
+  s.n = sp.n;
+  int R = sp.n;
+  if (p.accept_len != nullptr) {
+    const int a = p.accept_len[b];
+    R = a < -1 ? 0 : (a >= sp.n ? sp.n : a + 1);
+    if (sp.ok && (a < -1 || a >= sp.n)) s.bits |= JF_DEVERR_BAD_PATH;
   }
   int P = p.prefix_len[b];
   if (P < 0 || P > cap - R) {
-    bits |= JF_DEVERR_BAD_PREFIX;
+    s.bits |= JF_DEVERR_BAD_PREFIX;
     P = max(0, min(P, cap));
     R = min(R, cap - P);
   }
-  const int L = P + R;
-  if (t0 >= L) {
-    if (t0 == 0 && threadIdx.x == 0 && bits) report(p.dev_err, bits);
+  s.P = P;
+  s.R = R;
+  s.L = P + R;
+  s.tiles = (s.L + kKeyTile - 1) / kKeyTile;
+  s.blocks = (R * p.G + kRowBlock - 1) / kRowBlock;
+  // A tile with one or two row blocks costs its 32 KB from HBM, one with more its blocks.
+  s.unit = s.blocks == 0 ? 1 : max(2, s.blocks);
+  return s;
+}
+
+// This CTA's range [x0, x1) of the total cost, and the sequence where it starts.
+struct Range {
+  long long x0, x1, base;
+  int b;
+};
+
+// Calls f(b, g, first tile, tiles, info) for every run of tiles of one (sequence, kv-head)
+// in the range, in order, until f returns false.
+template <typename F>
+__device__ __forceinline__ void for_each_run(const WeightParams& p, const Range& r, F f) {
+  long long base = r.base;
+  for (int b = r.b; b < p.B && base < r.x1; ++b) {
+    const SeqInfo s = seq_info(p, b);
+    const int every = s.tiles * p.Hkv;
+    const long long lo = r.x0 - base, hi = r.x1 - base;
+    int i = lo <= 0 ? 0 : static_cast<int>((lo + s.unit - 1) / s.unit);
+    const long long last = (hi + s.unit - 1) / s.unit;
+    const int end = last < every ? static_cast<int>(last) : every;
+    while (i < end) {
+      const int g = i / s.tiles, t0 = i - g * s.tiles, n = min(s.tiles - t0, end - i);
+      if (!f(b, g, t0, n, s)) return;
+      i += n;
+    }
+    base += static_cast<long long>(every) * s.unit;
+  }
+}
+
+// Rows of earlier positions than the group's first key do not see it: the first row block
+// that does.
+__device__ __forceinline__ int first_block(const SeqInfo& s, int tile, int G) {
+  return max(0, tile * kKeyTile - s.P) * G / kRowBlock;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weight_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap_run,
+                  const WeightParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* k_s = sm;
+  uint8_t* q_s = sm + C::kQOff;
+  __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages];
+  __shared__ uint64_t q_full[C::kQStages], q_empty[C::kQStages];
+  __shared__ uint64_t s_full[kSlots], s_empty[kSlots], fin;
+  __shared__ __align__(16) float s_nlse[C::kQStages][kRowBlock];   // -lse in log2 units
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ Range s_range;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kQStages; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&q_empty[i], 1 + 4 * kSlots);   // the MMAs and every epilogue warp
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(&fin, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&kmap_run);
+  }
+  grid_dependency_wait();
+
+  // ---- this CTA's range: the block scans the sequences' costs, kThreads at a time.
+  auto cost_of = [&](int b) -> long long {
+    if (b >= p.B) return 0;
+    const SeqInfo s = seq_info(p, b);
+    if (s.bits && blockIdx.x == 0) report(p.dev_err, s.bits);
+    return static_cast<long long>(s.tiles) * p.Hkv * s.unit;
+  };
+  auto scan = [&](long long mine, long long* excl) -> long long {   // returns the block's sum
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    *excl = before + incl - mine;
+    return all;
+  };
+  long long total = 0, excl = 0, mine = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    mine = cost_of(b0 + tid);
+    total += scan(mine, &excl);
+  }
+  const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (x0 == x1) {
+    grid_dependents_launch();
     return;
   }
-  float kf[D];
-  bool live = t < L;
-  if (live) {
-    const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + t / kPage];
-    if (page < 0 || page >= p.num_pages) {
-      bits |= JF_DEVERR_BAD_PAGE;
-      live = false;
-    } else {
-      const uint4* row = reinterpret_cast<const uint4*>(
-          p.k_cache + ((static_cast<size_t>(page) * kPage + t % kPage) * p.Hkv + g) * D);
+  long long run = 0;
+  for (int b0 = 0; b0 < p.B && run <= x0; b0 += kThreads) {
+    if (p.B > kThreads) mine = cost_of(b0 + tid);
+    const long long all = p.B > kThreads ? scan(mine, &excl) : total;
+    if (run + excl <= x0 && x0 < run + excl + mine) s_range = Range{x0, x1, run + excl, b0 + tid};
+    run += all;
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Range range = s_range;
+  const uint32_t tmem = tmem_slot;
+  const uint64_t wlim = kWaitLimitNs;
+  const int G = p.G;
+
+  if (warp == 0) {
+    // ================================================================ K producer
+    int issued = 0, bits = 0;
+    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
+      if (s.blocks == 0) return true;
+      const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
+      auto page_of = [&](int tile) -> int {   // num_pages: loads as zeros
+        const int pl = tile * kPagesPerTile + lane;
+        if (lane >= kPagesPerTile || tile >= t0 + n || pl * kPage >= s.L) return p.num_pages;
+        const int page = __ldg(bt + pl);
+        if (page >= 0 && page < p.num_pages) return page;
+        bits |= JF_DEVERR_BAD_PAGE;
+        return p.num_pages;
+      };
+      int next = page_of(t0);
+      for (int tile = t0; tile < t0 + n; ++tile) {
+        const int mine_page = next;
+        next = page_of(tile + 1);
+        const int st = issued % C::kKStages;
+        if (!wait_warp(&k_empty[st], (static_cast<uint32_t>(issued / C::kKStages) & 1u) ^ 1u, abort, wlim)) {
+          if (lane == 0) set_abort(abort, p.dev_err);
+          return false;
+        }
+        const int page = __shfl_sync(0xffffffffu, mine_page, lane % kPagesPerTile);
+        const int page0 = __shfl_sync(0xffffffffu, mine_page, 0);
+        const bool together = __all_sync(0xffffffffu, page == page0 + lane % kPagesPerTile) &&
+                              page0 + kPagesPerTile <= p.num_pages;
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
+        __syncwarp();
+        uint8_t* dst = k_s + st * C::kTileBytes;
+        if (together) {                       // eight consecutive pages: one box per half
+          if (lane < C::kHalves)
+            tma_load_3d(dst + lane * C::kHalfBytes, &kmap_run, &k_full[st], lane * 64, g, page0 * kPage);
+        } else if (lane < kPagesPerTile * C::kHalves) {
+          const int pq = lane % kPagesPerTile, hh = lane / kPagesPerTile;
+          tma_load_3d(dst + hh * C::kHalfBytes + pq * (kPage * 128), &kmap, &k_full[st], hh * 64, g,
+                      page * kPage);
+        }
+        ++issued;
+      }
+      return true;
+    });
+    if (bits) report(p.dev_err, bits);
+    __syncwarp();
+    if (lane == 0) {                          // no copy is still landing when the CTA exits
+      int zero = 0;
+      for (int i = max(0, issued - C::kKStages); i < issued; ++i)
+        mbar_wait(&k_full[i % C::kKStages], static_cast<uint32_t>(i / C::kKStages) & 1u, &zero);
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    const uint64_t dk = desc_sw128(smem_u32(k_s), 16, 1024);
+    const uint64_t dq = desc_sw128(smem_u32(q_s), 16, 1024);
+    int tile_no = 0, k_no = 0, q_no = 0;      // tiles, K stages and row blocks so far
+    uint32_t free_phase = (1u << kSlots) - 1u;  // parity to wait for on s_empty, per slot
+    auto fail = [&]() -> bool {
+      if (lane == 0) set_abort(abort, p.dev_err);
+      return false;
+    };
+    // S^T of K stage k_at and row block q_at into a slot.
+    auto issue = [&](int k_at, int q_at, int slot, int cols) -> bool {
+      if (!wait_warp(&s_empty[slot], (free_phase >> slot) & 1u, abort, wlim)) return false;
+      free_phase ^= 1u << slot;
+      tc_fence_after();
+      mma_ss_tile<D / 16>(tmem + slot * kRowBlock,
+                          dk + static_cast<uint64_t>((k_at * C::kTileBytes) >> 4),
+                          dq + static_cast<uint64_t>((q_at * C::kTileBytes) >> 4),
+                          idesc_bf16(kKeyTile, cols, false, false));
+      mma_commit(&s_full[slot]);
+      return true;
+    };
+    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
+      const int rows = s.R * G;
+      if (s.blocks == 1) {
+        const int cols = (rows + 31) & ~31;
+        const int qs = q_no % C::kQStages;
+        if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+        for (int i = 0; i < n; ++i, ++tile_no, ++k_no) {
+          const int st = k_no % C::kKStages;
+          if (!wait_warp(&k_full[st], static_cast<uint32_t>(k_no / C::kKStages) & 1u, abort, wlim) ||
+              !issue(st, qs, tile_no % kSlots, cols))
+            return fail();
+          mma_commit(&k_empty[st]);
+        }
+        mma_commit(&q_empty[qs]);
+        ++q_no;
+        return true;
+      }
+      for (int i0 = 0; i0 < n; i0 += kGroup) {
+        const int m = min(kGroup, n - i0);
+        const int qb0 = first_block(s, t0 + i0, G);
+        for (int qb = qb0; qb < s.blocks; ++qb, ++q_no) {
+          const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
+          const int qs = q_no % C::kQStages;
+          if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+          for (int i = 0; i < m; ++i) {
+            const int st = (k_no + i) % C::kKStages;
+            if (qb == qb0 &&
+                !wait_warp(&k_full[st], static_cast<uint32_t>((k_no + i) / C::kKStages) & 1u, abort, wlim))
+              return fail();
+            if (!issue(st, qs, (tile_no + i) % kSlots, cols)) return fail();
+            if (qb == s.blocks - 1) mma_commit(&k_empty[st]);
+          }
+          mma_commit(&q_empty[qs]);
+        }
+        tile_no += m;
+        if (s.blocks > 0) k_no += m;
+      }
+      return true;
+    });
+    mma_commit(&fin);                         // all MMAs are done before TMEM is released
+    if (lane == 0) {
+      int zero = 0;
+      mbar_wait(&fin, 0, &zero);
+    }
+    __syncwarp();
+  } else if (warp >= kQWarp && warp < kEpiWarp) {
+    // ================================================================ query rows
+    constexpr int kVecs = D / 8;              // 16-byte vectors of a row
+    constexpr int kRowsPerPass = 128 / kVecs;
+    const int qt = tid - kQWarp * 32;
+    int q_no = 0, bits = 0;
+    // Loads the rows of block qb of (b, g) into the next stage.
+    auto load = [&](int b, int g, const SeqInfo& s, int qb) -> bool {
+      const int qs = q_no % C::kQStages;
+      const bool ok = wait_warp(&q_empty[qs], (static_cast<uint32_t>(q_no / C::kQStages) & 1u) ^ 1u, abort, wlim);
+      ++q_no;
+      if (!ok && lane == 0) set_abort(abort, p.dev_err);
+      const int rows = s.R * G;
+      const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
+      auto node_of = [&](int j) -> int {      // -1: no such row
+        const int k = j / G;
+        if (j >= rows) return -1;
+        const int node = p.path == nullptr ? k : __ldg(p.path + static_cast<size_t>(b) * p.N + k);
+        if (node >= 0 && node < s.n) return node;
+        bits |= JF_DEVERR_BAD_PATH;
+        return -1;
+      };
+      uint8_t* dst = q_s + qs * C::kTileBytes;
+      if (ok) {
+        for (int r0 = 0; r0 < cols; r0 += kRowsPerPass) {
+          const int r = r0 + qt / kVecs, c = qt % kVecs;
+          const int j = qb * kRowBlock + r, node = node_of(j);
+          const uint16_t* src = p.q + (static_cast<size_t>(s.row0 + max(node, 0)) * p.Hq + g * G + j % G) * D + c * 8;
+          const uint32_t to = smem_u32(dst + (c / 8) * C::kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src),
+                       "r"(node >= 0 ? 16 : 0) : "memory");
+        }
+        const int j = qb * kRowBlock + qt, node = qt < cols ? node_of(j) : -1;
+        float nl = -INFINITY;
+        if (node >= 0) {
+          const int h = g * G + j % G;
+          const float lse = p.cu != nullptr ? __ldg(p.lse + static_cast<size_t>(h) * p.T + s.row0 + node)
+                                            : __ldg(p.lse + (static_cast<size_t>(b) * p.Hq + h) * p.N + node);
+          if (lse != -INFINITY) nl = -lse * kLog2e;
+        }
+        s_nlse[qs][qt] = nl;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!named_bar_and(1, 128, ok)) return false;   // all four warps go on, or none
+      // A row with no lse adds nothing whatever its query holds.
+      for (int r0 = 0; r0 < cols; r0 += kRowsPerPass) {
+        const int r = r0 + qt / kVecs, c = qt % kVecs;
+        if (s_nlse[qs][r] == -INFINITY)
+          *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4)) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full[qs]);
+      return true;
+    };
+    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
+      if (s.blocks == 1) return load(b, g, s, 0);
+      for (int i0 = 0; i0 < n; i0 += kGroup)
+        for (int qb = first_block(s, t0 + i0, G); qb < s.blocks; ++qb)
+          if (!load(b, g, s, qb)) return false;
+      return true;
+    });
+    if (bits) report(p.dev_err, bits);
+  } else if (warp >= kEpiWarp) {
+    // ================================================================ probabilities
+    const int slot = (warp - kEpiWarp) / 4;
+    const int key = (warp & 3) * 32 + lane;   // TMEM lane = key of the tile
+    const uint32_t s_addr = tmem + slot * kRowBlock + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
+    int tile_no = 0, q_no = 0;
+    uint32_t phase = 0;
+    auto fail = [&]() -> bool {
+      if (lane == 0) set_abort(abort, p.dev_err);
+      return false;
+    };
+    // Adds the block's probabilities to acc; row j of the block counts if j >= j_min.
+    auto add_block = [&](int qs, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
+      if (!wait_warp(&s_full[slot], phase, abort, wlim)) return false;
+      phase ^= 1u;
+      __syncwarp();                           // lane 0 waited for the rows' lse, too
+      tc_fence_after();
+      const bool all = __all_sync(0xffffffffu, j_min <= 0);
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        uint32_t sv[32];
+        tmem_ld32(s_addr + c0, sv);
+        tmem_ld_wait(sv);
+        const float4* nl = reinterpret_cast<const float4*>(&s_nlse[qs][c0]);
 #pragma unroll
-      for (int v = 0; v < D / 8; ++v) {
-        const uint4 x = row[v];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kf[v * 8 + e * 2] = bf16_f32(w[e] & 0xffffu);
-          kf[v * 8 + e * 2 + 1] = bf16_f32(w[e] >> 16);
+        for (int v = 0; v < 8; ++v) {
+          const float4 l = nl[v];
+          float x0, x1, x2, x3;
+          f2_split(ffma2(f2(__uint_as_float(sv[4 * v]), __uint_as_float(sv[4 * v + 1])), c2, f2(l.x, l.y)), x0, x1);
+          f2_split(ffma2(f2(__uint_as_float(sv[4 * v + 2]), __uint_as_float(sv[4 * v + 3])), c2, f2(l.z, l.w)), x2, x3);
+          if (!all) {
+            const int j = c0 + 4 * v;
+            if (j + 0 < j_min) x0 = -INFINITY;
+            if (j + 1 < j_min) x1 = -INFINITY;
+            if (j + 2 < j_min) x2 = -INFINITY;
+            if (j + 3 < j_min) x3 = -INFINITY;
+          }
+          acc[0] = fadd2(acc[0], f2(fast_exp2(x0), fast_exp2(x1)));
+          acc[1] = fadd2(acc[1], f2(fast_exp2(x2), fast_exp2(x3)));
         }
       }
-    }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[slot]);
+      return true;
+    };
+    auto old_weight = [&](int b, int g, int t, const SeqInfo& s) -> float {
+      const size_t at = (static_cast<size_t>(b) * p.Hkv + g) * (static_cast<size_t>(p.max_pages) * kPage) + t;
+      return t < s.P && p.weight != nullptr ? p.weight[at] : 0.f;
+    };
+    auto write = [&](int b, int g, int t, const SeqInfo& s, float old, const uint64_t (&acc)[2]) {
+      float a, c, d, e;
+      f2_split(acc[0], a, c);
+      f2_split(acc[1], d, e);
+      const size_t at = (static_cast<size_t>(b) * p.Hkv + g) * (static_cast<size_t>(p.max_pages) * kPage) + t;
+      if (t < s.L) p.weight_out[at] = old + ((a + c) + (d + e));
+    };
+    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
+      const int rows = s.R * G;
+      if (s.blocks <= 1) {
+        const int cols = (rows + 31) & ~31;
+        const int qs = q_no % C::kQStages;
+        if (s.blocks == 1 &&
+            !wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim))
+          return fail();
+        for (int i = 0; i < n; ++i, ++tile_no) {
+          if (tile_no % kSlots != slot) continue;
+          const int t = (t0 + i) * kKeyTile + key;
+          const float old = old_weight(b, g, t, s);
+          uint64_t acc[2] = {0ull, 0ull};
+          if (s.blocks == 1 && !add_block(qs, cols, max(t - s.P, 0) * G, acc)) return fail();
+          write(b, g, t, s, old, acc);
+        }
+        if (s.blocks == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_empty[qs]);
+          ++q_no;
+        }
+        return true;
+      }
+      for (int i0 = 0; i0 < n; i0 += kGroup) {
+        const int m = min(kGroup, n - i0);
+        const int my = (slot - tile_no % kSlots + kSlots) % kSlots;   // this slot's tile of the group
+        const int t = (t0 + i0 + my) * kKeyTile + key;
+        float old = 0.f;
+        if (my < m) old = old_weight(b, g, t, s);
+        uint64_t acc[2] = {0ull, 0ull};
+        for (int qb = first_block(s, t0 + i0, G); qb < s.blocks; ++qb, ++q_no) {
+          const int qs = q_no % C::kQStages;
+          if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+          if (my < m) {
+            const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
+            if (!add_block(qs, cols, max(t - s.P, 0) * G - qb * kRowBlock, acc)) return fail();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_empty[qs]);
+        }
+        if (my < m) write(b, g, t, s, old, acc);
+        tile_no += m;
+      }
+      return true;
+    });
   }
-  const size_t wi = (static_cast<size_t>(b) * p.Hkv + g) * cap + t;
-  float sum = 0.f;
-  for (int r = 0; r < R * G; ++r) {
-    const int k = r / G, h = g * G + r % G;
-    const int node = p.path == nullptr ? k : p.path[static_cast<size_t>(b) * p.N + k];
-    const bool ok = node >= 0 && node < sp.n;
-    if (!ok) bits |= JF_DEVERR_BAD_PATH;
-    __syncthreads();
-    if (ok)
-      for (int d = threadIdx.x; d < D; d += kKeys)
-        s_q[d] = bf16_f32(p.q[(static_cast<size_t>(sp.row0 + node) * p.Hq + h) * D + d]);
-    __syncthreads();
-    if (!ok || !live || t > P + k) continue;
-    const float lse = p.cu != nullptr ? p.lse[static_cast<size_t>(h) * p.T + sp.row0 + node]
-                                      : p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.N + node];
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < D; ++d) s = fmaf(s_q[d], kf[d], s);
-    if (lse != -INFINITY) sum += exp2f(fmaf(s, p.scale_log2, -lse * kLog2e));
-  }
-  if (live) p.weight_out[wi] = (t < P && p.weight != nullptr ? p.weight[wi] : 0.f) + sum;
-  if (bits) report(p.dev_err, bits);
+  tc_fence_before();
+  __syncthreads();
+  grid_dependents_launch();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+jf_status launch_weight(const CUtensorMap& km, const CUtensorMap& kr, const WeightParams& p, int sms,
+                        cudaStream_t s) {
+  static SmemAttr attr;
+  if (!attr.ensure(weight_kernel<D>, Cfg<D>::kSmemBytes)) return JF_ERR_CUDA;
+  const cudaError_t e = launch_pdl(weight_kernel<D>, dim3(static_cast<unsigned>(sms)), dim3(kThreads),
+                                   Cfg<D>::kSmemBytes, s, km, kr, p);
+  return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
 jf_status attention_weight_call(const void* q, const void* k_cache, const int32_t* block_table,
@@ -128,13 +564,13 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
       static_cast<long long>(num_pages) * kPage >= (1ll << 31) ||
       static_cast<long long>(N) * (Hq / Hkv) >= (1ll << 30))
     return JF_ERR_UNSUPPORTED;
-  if (cu == nullptr && static_cast<long long>(max_pages) * kPage < 1) return JF_ERR_UNSUPPORTED;
   if (cu != nullptr && T < 1) return JF_ERR_INVALID_ARGUMENT;
   if (cu != nullptr && static_cast<long long>(T) + N >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16)) return JF_ERR_MISALIGNED;
+  const int sms = current_sm_count();
+  if (sms <= 0) return JF_ERR_CUDA;
   WeightParams p;
   p.q = static_cast<const uint16_t*>(q);
-  p.k_cache = static_cast<const uint16_t*>(k_cache);
   p.block_table = block_table;
   p.prefix_len = prefix_len;
   p.path = path;
@@ -149,14 +585,19 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   p.N = N;
   p.Hq = Hq;
   p.Hkv = Hkv;
+  p.G = Hq / Hkv;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.scale_log2 = scale * kLog2e;
-  const dim3 grid(static_cast<unsigned>((max_pages * kPage + kKeys - 1) / kKeys), Hkv, B);
+  CUtensorMap km, kr;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(num_pages) * kPage};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
+  const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
+  if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&kr, k_cache, 3, dims, strides, box_run))
+    return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 128 ? launch_pdl(weight_kernel<128>, grid, dim3(kKeys), 0, s, p)
-                                 : launch_pdl(weight_kernel<64>, grid, dim3(kKeys), 0, s, p);
-  return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
+  return D == 128 ? launch_weight<128>(km, kr, p, sms, s) : launch_weight<64>(km, kr, p, sms, s);
 }
 
 }  // namespace
