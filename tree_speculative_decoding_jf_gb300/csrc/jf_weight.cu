@@ -7,23 +7,27 @@
 // every key is independent: no reduction crosses keys.
 //
 // The scores are taken transposed, S^T = K Q^T: a 128-key tile is the A operand, a block of
-// up to 128 query rows (row = k * G + head in group) the B operand, and a TMEM lane is a
-// key.  So the thread that owns a lane owns its key: it adds its probabilities in registers
-// over all row blocks and writes the key's weight once.  K is read once, nothing is merged
-// between CTAs, and the order of every sum is fixed.
+// query rows the B operand (whole nodes of G rows, at most 128 rows; row = k * G + head in
+// group), and a TMEM lane is a key.  So the thread that owns a lane owns its key: it adds
+// its probabilities in registers over all row blocks and writes the key's weight once.  K
+// is read once, nothing is merged between CTAs, and the order of every sum is fixed.
 //
-// Work: the tiles of all (sequence, kv-head) pairs lie end to end, a tile weighted by its
-// row blocks, and each CTA (one per SM) takes an equal range.  Up to four consecutive tiles
-// of a pair form a group that shares every row block loaded; with one row block (a verified
-// path) it stays in shared memory for the whole run of the pair.
+// Work: the key tiles of all sequences lie end to end, a tile weighted by its row blocks,
+// and are cut into (SMs / kv-heads) equal ranges; the CTAs of a range (one per kv-head, side
+// by side) walk the same tokens together, so the 256-byte rows that they read lie next to
+// each other.  Up to four consecutive tiles of a sequence form a group that shares every
+// row block loaded; with one row block (a verified path) it stays in shared memory for the
+// whole run of the sequence.
 //
-// Roles (768 threads):
-//   warp 0       K tiles by TMA into a ring, page ids one tile ahead; pages past the end
-//                and malformed ids load as zeros.
+// Roles (640 threads):
+//   warp 0       K tiles by TMA into a ring, page ids four to eight tiles ahead; pages past
+//                the end and malformed ids load as zeros.
 //   warp 1       allocates TMEM, issues the MMAs.
-//   warps 4..7   gather the query rows (path, heads, packed layouts) with 16-byte
-//                asynchronous copies into the swizzled B layout, and the rows' lse.
-//   warps 8..23  four warpgroups, one per TMEM slot (128 columns): tile c of the CTA goes
+//   warps 2, 3   query rows, one warp per stage: a full block of a chain as one TMA box
+//                per 64-column half, else one box per (node, half), and the rows' lse.
+//                (Gathered with 16-byte asynchronous copies instead, a block took 13,000
+//                cycles to issue beside the polling warps.)
+//   warps 4..19  four warpgroups, one per TMEM slot (128 columns): tile c of the CTA goes
 //                to slot c % 4.
 // Slots past a block's rows and rows whose lse is -inf get zero queries and lse = +inf, so
 // they add exp(-inf) = 0.  Keys past the sequence's end are lanes whose sum is dropped:
@@ -46,8 +50,8 @@ constexpr int kPagesPerTile = kKeyTile / kPage;
 constexpr int kRowBlock = 128;
 constexpr int kSlots = 4;                 // TMEM slots = epilogue warpgroups
 constexpr int kGroup = kSlots;            // key tiles that share a loaded row block
-constexpr int kThreads = 768;
-constexpr int kQWarp = 4, kEpiWarp = 8;   // first warps of the two roles
+constexpr int kThreads = 640;
+constexpr int kQWarp = 2, kEpiWarp = 4;   // first warps of the two roles
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -58,7 +62,8 @@ struct Cfg {
   // 160 KB of K in flight, far above the ~45 KB an SM needs to cover the latency of HBM at
   // its share of the bandwidth, and a group's four tiles plus the next one for D = 128.
   static constexpr int kKStages = D == 128 ? 5 : 10;
-  static constexpr int kQStages = 2;
+  static constexpr int kQStages = 2;          // one producer warp each
+  static constexpr int kLseStages = 3;        // held until the probabilities are added
   static constexpr int kQOff = kKStages * kTileBytes;
   static constexpr int kSmemBytes = kQOff + kQStages * kTileBytes + 1024;
 };
@@ -76,6 +81,7 @@ struct WeightParams {
   int32_t* dev_err;
   long long T;
   int B, N, Hq, Hkv, G, max_pages, num_pages;
+  int nodes;                  // nodes of a full row block: 128 / G
   float scale_log2;
 };
 
@@ -109,7 +115,7 @@ __device__ __forceinline__ SeqInfo seq_info(const WeightParams& p, int b) {
   s.R = R;
   s.L = P + R;
   s.tiles = (s.L + kKeyTile - 1) / kKeyTile;
-  s.blocks = (R * p.G + kRowBlock - 1) / kRowBlock;
+  s.blocks = (R + p.nodes - 1) / p.nodes;
   // A tile with one or two row blocks costs its 32 KB from HBM, one with more its blocks.
   s.unit = s.blocks == 0 ? 1 : max(2, s.blocks);
   return s;
@@ -121,36 +127,37 @@ struct Range {
   int b;
 };
 
-// Calls f(b, g, first tile, tiles, info) for every run of tiles of one (sequence, kv-head)
-// in the range, in order, until f returns false.
+// Calls f(b, first tile, tiles, info) for every sequence's run of tiles in the range, in
+// order, until f returns false.
 template <typename F>
 __device__ __forceinline__ void for_each_run(const WeightParams& p, const Range& r, F f) {
   long long base = r.base;
   for (int b = r.b; b < p.B && base < r.x1; ++b) {
     const SeqInfo s = seq_info(p, b);
-    const int every = s.tiles * p.Hkv;
     const long long lo = r.x0 - base, hi = r.x1 - base;
     int i = lo <= 0 ? 0 : static_cast<int>((lo + s.unit - 1) / s.unit);
     const long long last = (hi + s.unit - 1) / s.unit;
-    const int end = last < every ? static_cast<int>(last) : every;
-    while (i < end) {
-      const int g = i / s.tiles, t0 = i - g * s.tiles, n = min(s.tiles - t0, end - i);
-      if (!f(b, g, t0, n, s)) return;
-      i += n;
-    }
-    base += static_cast<long long>(every) * s.unit;
+    const int end = last < s.tiles ? static_cast<int>(last) : s.tiles;
+    if (i < end && !f(b, i, end - i, s)) return;
+    base += static_cast<long long>(s.tiles) * s.unit;
   }
 }
 
 // Rows of earlier positions than the group's first key do not see it: the first row block
 // that does.
-__device__ __forceinline__ int first_block(const SeqInfo& s, int tile, int G) {
-  return max(0, tile * kKeyTile - s.P) * G / kRowBlock;
+__device__ __forceinline__ int first_block(const SeqInfo& s, int tile, int nodes) {
+  return max(0, tile * kKeyTile - s.P) / nodes;
+}
+
+// Columns (rows of Q) that block qb's MMAs compute: a multiple of 32.
+__device__ __forceinline__ int block_cols(const SeqInfo& s, int qb, int nodes, int G) {
+  return (min(nodes, s.R - qb * nodes) * G + 31) & ~31;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     weight_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap_run,
+                  const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap_node,
                   const WeightParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -159,9 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* k_s = sm;
   uint8_t* q_s = sm + C::kQOff;
   __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages];
-  __shared__ uint64_t q_full[C::kQStages], q_empty[C::kQStages];
+  __shared__ uint64_t q_full[C::kQStages], q_empty[C::kQStages], q_raw[C::kQStages];
+  __shared__ uint64_t l_full[C::kLseStages], l_empty[C::kLseStages];
   __shared__ uint64_t s_full[kSlots], s_empty[kSlots], fin;
-  __shared__ __align__(16) float s_nlse[C::kQStages][kRowBlock];   // -lse in log2 units
+  __shared__ __align__(16) float s_nlse[C::kLseStages][kRowBlock];   // -lse in log2 units
   __shared__ long long s_scan[kThreads / 32];
   __shared__ Range s_range;
   __shared__ uint32_t tmem_slot;
@@ -175,8 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::kQStages; ++i) {
-      mbar_init(&q_full[i], 128);
-      mbar_init(&q_empty[i], 1 + 4 * kSlots);   // the MMAs and every epilogue warp
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_raw[i], 1);
+    }
+    for (int i = 0; i < C::kLseStages; ++i) {
+      mbar_init(&l_full[i], 32);
+      mbar_init(&l_empty[i], 4 * kSlots);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s_full[i], 1);
@@ -187,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&kmap_run);
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&qmap_node);
   }
   grid_dependency_wait();
 
@@ -195,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (b >= p.B) return 0;
     const SeqInfo s = seq_info(p, b);
     if (s.bits && blockIdx.x == 0) report(p.dev_err, s.bits);
-    return static_cast<long long>(s.tiles) * p.Hkv * s.unit;
+    return static_cast<long long>(s.tiles) * s.unit;
   };
   auto scan = [&](long long mine, long long* excl) -> long long {   // returns the block's sum
     long long incl = mine;
@@ -220,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mine = cost_of(b0 + tid);
     total += scan(mine, &excl);
   }
-  const long long x0 = total * blockIdx.x / gridDim.x, x1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int g = blockIdx.x % p.Hkv, part = blockIdx.x / p.Hkv, parts = gridDim.x / p.Hkv;
+  const long long x0 = total * part / parts, x1 = total * (part + 1) / parts;
   if (x0 == x1) {
     grid_dependents_launch();
     return;
@@ -242,33 +258,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Range range = s_range;
   const uint32_t tmem = tmem_slot;
   const uint64_t wlim = kWaitLimitNs;
-  const int G = p.G;
+  const int G = p.G, nodes = p.nodes;
 
   if (warp == 0) {
     // ================================================================ K producer
     int issued = 0, bits = 0;
-    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
+    for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
       if (s.blocks == 0) return true;
       const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
-      auto page_of = [&](int tile) -> int {   // num_pages: loads as zeros
-        const int pl = tile * kPagesPerTile + lane;
-        if (lane >= kPagesPerTile || tile >= t0 + n || pl * kPage >= s.L) return p.num_pages;
-        const int page = __ldg(bt + pl);
-        if (page >= 0 && page < p.num_pages) return page;
-        bits |= JF_DEVERR_BAD_PAGE;
-        return p.num_pages;
+      // Lane l holds page l % 8 of tile l / 8 of a batch of four tiles; the next batch is
+      // asked for when a batch's first tile is issued.  num_pages: loads as zeros.
+      auto pages_of = [&](int tile4) -> int {
+        const int pl = tile4 * kPagesPerTile + lane;
+        if (tile4 + lane / kPagesPerTile >= t0 + n || pl * kPage >= s.L) return p.num_pages;
+        return __ldg(bt + pl);
       };
-      int next = page_of(t0);
+      int now = 0, next = pages_of(t0);
       for (int tile = t0; tile < t0 + n; ++tile) {
-        const int mine_page = next;
-        next = page_of(tile + 1);
+        const int sub = (tile - t0) % 4;
+        if (sub == 0) {
+          now = next;
+          next = pages_of(tile + 4);
+          if (now < 0 || now > p.num_pages) {
+            bits |= JF_DEVERR_BAD_PAGE;
+            now = p.num_pages;
+          } else if (now == p.num_pages && tile + lane / kPagesPerTile < t0 + n &&
+                     (tile * kPagesPerTile + lane) * kPage < s.L) {
+            bits |= JF_DEVERR_BAD_PAGE;
+          }
+        }
         const int st = issued % C::kKStages;
         if (!wait_warp(&k_empty[st], (static_cast<uint32_t>(issued / C::kKStages) & 1u) ^ 1u, abort, wlim)) {
           if (lane == 0) set_abort(abort, p.dev_err);
           return false;
         }
-        const int page = __shfl_sync(0xffffffffu, mine_page, lane % kPagesPerTile);
-        const int page0 = __shfl_sync(0xffffffffu, mine_page, 0);
+        const int page = __shfl_sync(0xffffffffu, now, sub * kPagesPerTile + lane % kPagesPerTile);
+        const int page0 = __shfl_sync(0xffffffffu, page, 0);
         const bool together = __all_sync(0xffffffffu, page == page0 + lane % kPagesPerTile) &&
                               page0 + kPagesPerTile <= p.num_pages;
         if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
@@ -315,10 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(&s_full[slot]);
       return true;
     };
-    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
-      const int rows = s.R * G;
+    for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
       if (s.blocks == 1) {
-        const int cols = (rows + 31) & ~31;
+        const int cols = block_cols(s, 0, nodes, G);
         const int qs = q_no % C::kQStages;
         if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
         for (int i = 0; i < n; ++i, ++tile_no, ++k_no) {
@@ -334,9 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i0 = 0; i0 < n; i0 += kGroup) {
         const int m = min(kGroup, n - i0);
-        const int qb0 = first_block(s, t0 + i0, G);
+        const int qb0 = first_block(s, t0 + i0, nodes);
         for (int qb = qb0; qb < s.blocks; ++qb, ++q_no) {
-          const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
+          const int cols = block_cols(s, qb, nodes, G);
           const int qs = q_no % C::kQStages;
           if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
           for (int i = 0; i < m; ++i) {
@@ -362,67 +386,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kQWarp && warp < kEpiWarp) {
     // ================================================================ query rows
-    constexpr int kVecs = D / 8;              // 16-byte vectors of a row
-    constexpr int kRowsPerPass = 128 / kVecs;
-    const int qt = tid - kQWarp * 32;
-    int q_no = 0, bits = 0;
-    // Loads the rows of block qb of (b, g) into the next stage.
-    auto load = [&](int b, int g, const SeqInfo& s, int qb) -> bool {
-      const int qs = q_no % C::kQStages;
-      const bool ok = wait_warp(&q_empty[qs], (static_cast<uint32_t>(q_no / C::kQStages) & 1u) ^ 1u, abort, wlim);
-      ++q_no;
-      if (!ok && lane == 0) set_abort(abort, p.dev_err);
-      const int rows = s.R * G;
-      const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
-      auto node_of = [&](int j) -> int {      // -1: no such row
-        const int k = j / G;
-        if (j >= rows) return -1;
+    constexpr int kVecs = 8;                  // 16-byte vectors of a row's half
+    const int stage = warp - kQWarp;
+    int q_no = 0, mine = 0, raw_no = 0, bits = 0;
+    uint8_t* dst = q_s + stage * C::kTileBytes;
+    auto zero_row = [&](int r, int c) {       // vector c of row r, all halves
+      for (int hh = 0; hh < C::kHalves; ++hh)
+        *reinterpret_cast<uint4*>(dst + hh * C::kHalfBytes + r * 128 + (c << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    // Loads block qb of sequence b if it is this warp's turn.
+    auto load = [&](int b, const SeqInfo& s, int qb) -> bool {
+      const int no = q_no++;
+      if (no % C::kQStages != stage) return true;
+      const int n0 = qb * nodes, nb = min(nodes, s.R - n0), rows = nb * G, cols = block_cols(s, qb, nodes, G);
+      auto node_at = [&](int k) -> int {      // -1: malformed
         const int node = p.path == nullptr ? k : __ldg(p.path + static_cast<size_t>(b) * p.N + k);
         if (node >= 0 && node < s.n) return node;
         bits |= JF_DEVERR_BAD_PATH;
         return -1;
       };
-      uint8_t* dst = q_s + qs * C::kTileBytes;
-      if (ok) {
-        for (int r0 = 0; r0 < cols; r0 += kRowsPerPass) {
-          const int r = r0 + qt / kVecs, c = qt % kVecs;
-          const int j = qb * kRowBlock + r, node = node_of(j);
-          const uint16_t* src = p.q + (static_cast<size_t>(s.row0 + max(node, 0)) * p.Hq + g * G + j % G) * D + c * 8;
-          const uint32_t to = smem_u32(dst + (c / 8) * C::kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src),
-                       "r"(node >= 0 ? 16 : 0) : "memory");
-        }
-        const int j = qb * kRowBlock + qt, node = qt < cols ? node_of(j) : -1;
-        float nl = -INFINITY;
+      // Four rows a lane: their lse, asked for before the stage is free.
+      float nl[kRowBlock / 32];
+      bool dead = false;
+#pragma unroll
+      for (int u = 0; u < kRowBlock / 32; ++u) {
+        const int r = u * 32 + lane, k = r / G, h = g * G + r - k * G;
+        nl[u] = -INFINITY;
+        if (r >= rows) continue;
+        const int node = node_at(n0 + k);
         if (node >= 0) {
-          const int h = g * G + j % G;
           const float lse = p.cu != nullptr ? __ldg(p.lse + static_cast<size_t>(h) * p.T + s.row0 + node)
                                             : __ldg(p.lse + (static_cast<size_t>(b) * p.Hq + h) * p.N + node);
-          if (lse != -INFINITY) nl = -lse * kLog2e;
+          if (lse != -INFINITY) nl[u] = -lse * kLog2e;
         }
-        s_nlse[qs][qt] = nl;
+        dead |= nl[u] == -INFINITY;           // (lse = +inf as well: it adds nothing)
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!named_bar_and(1, 128, ok)) return false;   // all four warps go on, or none
-      // A row with no lse adds nothing whatever its query holds.
-      for (int r0 = 0; r0 < cols; r0 += kRowsPerPass) {
-        const int r = r0 + qt / kVecs, c = qt % kVecs;
-        if (s_nlse[qs][r] == -INFINITY)
-          *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4)) =
-              make_uint4(0u, 0u, 0u, 0u);
+      const int ls = no % C::kLseStages;
+      if (!wait_warp(&q_empty[stage], (static_cast<uint32_t>(no / C::kQStages) & 1u) ^ 1u, abort, wlim) ||
+          !wait_warp(&l_empty[ls], (static_cast<uint32_t>(no / C::kLseStages) & 1u) ^ 1u, abort, wlim)) {
+        if (lane == 0) set_abort(abort, p.dev_err);
+        return false;
       }
+      ++mine;
+#pragma unroll
+      for (int u = 0; u < kRowBlock / 32; ++u) s_nlse[ls][u * 32 + lane] = nl[u];
+      for (int i = lane; i < (cols - rows) * kVecs; i += 32) zero_row(rows + i / kVecs, i % kVecs);
       fence_proxy_async_smem();
-      mbar_arrive(&q_full[qs]);
+      // A block with rows that add nothing lands on a barrier of its own: those rows are
+      // zeroed before the MMA warp hears of it, whatever their queries hold.
+      const bool rare = __any_sync(0xffffffffu, dead);
+      uint64_t* bar = rare ? &q_raw[stage] : &q_full[stage];
+      const bool whole = p.path == nullptr && nb == nodes;
+      int boxes = nb;
+      if (p.path != nullptr) {
+        boxes = 0;
+        for (int v = 0; v < nb; v += 32)
+          boxes += __popc(__ballot_sync(0xffffffffu, v + lane < nb && node_at(n0 + v + lane) >= 0));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * G * 128 * C::kHalves));
+      __syncwarp();
+      const int c3 = p.cu != nullptr ? 0 : b, base = p.cu != nullptr ? static_cast<int>(s.row0) : 0;
+      if (whole) {
+        if (lane < C::kHalves)
+          tma_load_4d(dst + lane * C::kHalfBytes, &qmap, bar, lane * 64, g * G, base + n0, c3);
+      } else {
+        for (int v = lane; v < nb; v += 32) {
+          const int node = node_at(n0 + v);
+          if (node < 0) continue;
+          for (int hh = 0; hh < C::kHalves; ++hh)
+            tma_load_4d(dst + hh * C::kHalfBytes + v * G * 128, &qmap_node, bar, hh * 64, g * G, base + node, c3);
+        }
+      }
+      mbar_arrive(&l_full[ls]);
+      if (rare) {
+        const bool ok = wait_warp(bar, static_cast<uint32_t>(raw_no++) & 1u, abort, wlim);
+        if (!ok) {
+          if (lane == 0) set_abort(abort, p.dev_err);
+          return false;
+        }
+#pragma unroll
+        for (int u = 0; u < kRowBlock / 32; ++u)
+          if (u * 32 + lane < rows && nl[u] == -INFINITY)
+            for (int c = 0; c < kVecs; ++c) zero_row(u * 32 + lane, c);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[stage]);
+      }
       return true;
     };
-    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
-      if (s.blocks == 1) return load(b, g, s, 0);
+    for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
+      if (s.blocks == 1) return load(b, s, 0);
       for (int i0 = 0; i0 < n; i0 += kGroup)
-        for (int qb = first_block(s, t0 + i0, G); qb < s.blocks; ++qb)
-          if (!load(b, g, s, qb)) return false;
+        for (int qb = first_block(s, t0 + i0, nodes); qb < s.blocks; ++qb)
+          if (!load(b, s, qb)) return false;
       return true;
     });
     if (bits) report(p.dev_err, bits);
+    __syncwarp();
+    if (lane == 0 && mine > 0) {              // the last copies have landed before the CTA exits
+      int zero = 0;
+      mbar_wait(&q_full[stage], static_cast<uint32_t>(mine - 1) & 1u, &zero);
+    }
   } else if (warp >= kEpiWarp) {
     // ================================================================ probabilities
     const int slot = (warp - kEpiWarp) / 4;
@@ -436,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return false;
     };
     // Adds the block's probabilities to acc; row j of the block counts if j >= j_min.
-    auto add_block = [&](int qs, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
+    auto add_block = [&](int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
       if (!wait_warp(&s_full[slot], phase, abort, wlim)) return false;
       phase ^= 1u;
       __syncwarp();                           // lane 0 waited for the rows' lse, too
@@ -446,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sv[32];
         tmem_ld32(s_addr + c0, sv);
         tmem_ld_wait(sv);
-        const float4* nl = reinterpret_cast<const float4*>(&s_nlse[qs][c0]);
+        const float4* nl = reinterpret_cast<const float4*>(&s_nlse[ls][c0]);
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           const float4 l = nl[v];
@@ -469,36 +534,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&s_empty[slot]);
       return true;
     };
-    auto old_weight = [&](int b, int g, int t, const SeqInfo& s) -> float {
+    auto old_weight = [&](int b, int t, const SeqInfo& s) -> float {
       const size_t at = (static_cast<size_t>(b) * p.Hkv + g) * (static_cast<size_t>(p.max_pages) * kPage) + t;
       return t < s.P && p.weight != nullptr ? p.weight[at] : 0.f;
     };
-    auto write = [&](int b, int g, int t, const SeqInfo& s, float old, const uint64_t (&acc)[2]) {
+    auto write = [&](int b, int t, const SeqInfo& s, float old, const uint64_t (&acc)[2]) {
       float a, c, d, e;
       f2_split(acc[0], a, c);
       f2_split(acc[1], d, e);
       const size_t at = (static_cast<size_t>(b) * p.Hkv + g) * (static_cast<size_t>(p.max_pages) * kPage) + t;
       if (t < s.L) p.weight_out[at] = old + ((a + c) + (d + e));
     };
-    for_each_run(p, range, [&](int b, int g, int t0, int n, const SeqInfo& s) -> bool {
-      const int rows = s.R * G;
+    for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
       if (s.blocks <= 1) {
-        const int cols = (rows + 31) & ~31;
-        const int qs = q_no % C::kQStages;
+        const int cols = block_cols(s, 0, nodes, G);
+        const int ls = q_no % C::kLseStages;
         if (s.blocks == 1 &&
-            !wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim))
+            !wait_warp(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim))
           return fail();
         for (int i = 0; i < n; ++i, ++tile_no) {
           if (tile_no % kSlots != slot) continue;
           const int t = (t0 + i) * kKeyTile + key;
-          const float old = old_weight(b, g, t, s);
+          const float old = old_weight(b, t, s);
           uint64_t acc[2] = {0ull, 0ull};
-          if (s.blocks == 1 && !add_block(qs, cols, max(t - s.P, 0) * G, acc)) return fail();
-          write(b, g, t, s, old, acc);
+          if (s.blocks == 1 && !add_block(ls, cols, max(t - s.P, 0) * G, acc)) return fail();
+          write(b, t, s, old, acc);
         }
         if (s.blocks == 1) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&q_empty[qs]);
+          if (lane == 0) mbar_arrive(&l_empty[ls]);
           ++q_no;
         }
         return true;
@@ -508,19 +572,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my = (slot - tile_no % kSlots + kSlots) % kSlots;   // this slot's tile of the group
         const int t = (t0 + i0 + my) * kKeyTile + key;
         float old = 0.f;
-        if (my < m) old = old_weight(b, g, t, s);
+        if (my < m) old = old_weight(b, t, s);
         uint64_t acc[2] = {0ull, 0ull};
-        for (int qb = first_block(s, t0 + i0, G); qb < s.blocks; ++qb, ++q_no) {
-          const int qs = q_no % C::kQStages;
-          if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+        for (int qb = first_block(s, t0 + i0, nodes); qb < s.blocks; ++qb, ++q_no) {
+          const int ls = q_no % C::kLseStages;
+          if (!wait_warp(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim)) return fail();
           if (my < m) {
-            const int cols = (min(kRowBlock, rows - qb * kRowBlock) + 31) & ~31;
-            if (!add_block(qs, cols, max(t - s.P, 0) * G - qb * kRowBlock, acc)) return fail();
+            if (!add_block(ls, block_cols(s, qb, nodes, G), (max(t - s.P, 0) - qb * nodes) * G, acc)) return fail();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&q_empty[qs]);
+          if (lane == 0) mbar_arrive(&l_empty[ls]);
         }
-        if (my < m) write(b, g, t, s, old, acc);
+        if (my < m) write(b, t, s, old, acc);
         tile_no += m;
       }
       return true;
@@ -533,12 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-jf_status launch_weight(const CUtensorMap& km, const CUtensorMap& kr, const WeightParams& p, int sms,
-                        cudaStream_t s) {
+jf_status launch_weight(const CUtensorMap& km, const CUtensorMap& kr, const CUtensorMap& qm,
+                        const CUtensorMap& qn, const WeightParams& p, int sms, cudaStream_t s) {
   static SmemAttr attr;
   if (!attr.ensure(weight_kernel<D>, Cfg<D>::kSmemBytes)) return JF_ERR_CUDA;
-  const cudaError_t e = launch_pdl(weight_kernel<D>, dim3(static_cast<unsigned>(sms)), dim3(kThreads),
-                                   Cfg<D>::kSmemBytes, s, km, kr, p);
+  const int ranges = std::max(1, sms / p.Hkv);
+  const cudaError_t e = launch_pdl(weight_kernel<D>, dim3(static_cast<unsigned>(ranges * p.Hkv)), dim3(kThreads),
+                                   Cfg<D>::kSmemBytes, s, km, kr, qm, qn, p);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
@@ -586,6 +650,7 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
+  p.nodes = kRowBlock / p.G;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.scale_log2 = scale * kLog2e;
@@ -596,8 +661,18 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
   if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&kr, k_cache, 3, dims, strides, box_run))
     return JF_ERR_CUDA;
+  CUtensorMap qm, qn;
+  const cuuint64_t rows = cu != nullptr ? static_cast<cuuint64_t>(T) : static_cast<cuuint64_t>(N);
+  const cuuint64_t qdims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), rows,
+                               cu != nullptr ? 1u : static_cast<cuuint64_t>(B)};
+  const cuuint64_t qstrides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2,
+                                  rows * Hq * D * 2};
+  const cuuint32_t qbox[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.nodes), 1};
+  const cuuint32_t qbox_node[4] = {64, static_cast<cuuint32_t>(p.G), 1, 1};
+  if (!encode(&qm, q, 4, qdims, qstrides, qbox) || !encode(&qn, q, 4, qdims, qstrides, qbox_node)) return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return D == 128 ? launch_weight<128>(km, kr, p, sms, s) : launch_weight<64>(km, kr, p, sms, s);
+  return D == 128 ? launch_weight<128>(km, kr, qm, qn, p, sms, s)
+                  : launch_weight<64>(km, kr, qm, qn, p, sms, s);
 }
 
 }  // namespace
