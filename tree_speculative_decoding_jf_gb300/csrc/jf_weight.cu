@@ -19,16 +19,18 @@
 // row block loaded; with one row block (a verified path) it stays in shared memory for the
 // whole run of the sequence.
 //
-// Roles (640 threads):
-//   warp 0       K tiles by TMA into a ring, page ids four to eight tiles ahead; pages past
-//                the end and malformed ids load as zeros.
-//   warp 1       allocates TMEM, issues the MMAs.
-//   warps 2, 3   query rows, one warp per stage: a full block of a chain as one TMA box
-//                per 64-column half, else one box per (node, half), and the rows' lse.
-//                (Gathered with 16-byte asynchronous copies instead, a block took 13,000
-//                cycles to issue beside the polling warps.)
-//   warps 4..19  four warpgroups, one per TMEM slot (128 columns): tile c of the CTA goes
-//                to slot c % 4.
+// Roles (512 threads):
+//   warp 0         allocates TMEM, issues the MMAs.
+//   warps 2, 3     query rows, one warp per stage: a full block of a chain as one TMA box
+//                  per 64-column half, else one box per (node, half), and the rows' lse.
+//                  (Gathered with 16-byte asynchronous copies instead, a block took 13,000
+//                  cycles to issue beside the polling warps.)
+//   warps 4..11    two warpgroups with two TMEM slots (128 columns) each: tile c of the CTA
+//                  goes to slot c % 4, so one slot is refilled while the other is read.
+//   warps 12..15   K tiles by TMA into a ring, a quarter of every tile's pages each (issued
+//                  from 16 lanes of one warp, a tile's boxes took 1400 cycles to go out,
+//                  more than its share of the HBM bandwidth); page ids four to eight tiles
+//                  ahead; pages past the end and malformed ids load as zeros.
 // Slots past a block's rows and rows whose lse is -inf get zero queries and lse = +inf, so
 // they add exp(-inf) = 0.  Keys past the sequence's end are lanes whose sum is dropped:
 // whatever their page slots hold stays in their lane.
@@ -48,10 +50,11 @@ constexpr int kPage = 16;
 constexpr int kKeyTile = 128;
 constexpr int kPagesPerTile = kKeyTile / kPage;
 constexpr int kRowBlock = 128;
-constexpr int kSlots = 4;                 // TMEM slots = epilogue warpgroups
+constexpr int kSlots = 4;                 // TMEM slots, two for each epilogue warpgroup
 constexpr int kGroup = kSlots;            // key tiles that share a loaded row block
-constexpr int kThreads = 640;
-constexpr int kQWarp = 2, kEpiWarp = 4;   // first warps of the two roles
+constexpr int kThreads = 512;
+constexpr int kQWarp = 2, kEpiWarp = 4, kKWarp = 12;   // first warps of the roles
+constexpr int kKWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -154,9 +157,52 @@ __device__ __forceinline__ int block_cols(const SeqInfo& s, int qb, int nodes, i
   return (min(nodes, s.R - qb * nodes) * G + 31) & ~31;
 }
 
+// Adds 16 columns' probabilities 2^(s * c + nlse) to acc; MASKED: only columns j >= j_min.
+// (One instantiation with the test inside has a branch every four columns, which keeps the
+// compiler from overlapping them: 237 cycles for each four instead of about 20.)
+template <bool MASKED>
+__device__ __forceinline__ void add16(const uint32_t (&sv)[16], const float* nlse, int j_min, uint64_t c2,
+                                      uint64_t (&acc)[2]) {
+  const float4* nl = reinterpret_cast<const float4*>(nlse);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float4 l = nl[v];
+    float x0, x1, x2, x3;
+    f2_split(ffma2(f2(__uint_as_float(sv[4 * v]), __uint_as_float(sv[4 * v + 1])), c2, f2(l.x, l.y)), x0, x1);
+    f2_split(ffma2(f2(__uint_as_float(sv[4 * v + 2]), __uint_as_float(sv[4 * v + 3])), c2, f2(l.z, l.w)), x2, x3);
+    if constexpr (MASKED) {
+      x0 = 4 * v + 0 < j_min ? -INFINITY : x0;
+      x1 = 4 * v + 1 < j_min ? -INFINITY : x1;
+      x2 = 4 * v + 2 < j_min ? -INFINITY : x2;
+      x3 = 4 * v + 3 < j_min ? -INFINITY : x3;
+    }
+    acc[0] = fadd2(acc[0], f2(fast_exp2(x0), fast_exp2(x1)));
+    acc[1] = fadd2(acc[1], f2(fast_exp2(x2), fast_exp2(x3)));
+  }
+}
+
+// All columns of a slot (a multiple of 32); the next 16 travel from TMEM while 16 are
+// worked on.
+template <bool MASKED>
+__device__ __forceinline__ void add_columns(uint32_t addr, const float* nlse, int cols, int j_min, uint64_t c2,
+                                            uint64_t (&acc)[2]) {
+  uint32_t sa[16], sb[16];
+  tmem_ld16(addr, sa);
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    tmem_ld_wait16(sa);
+    tmem_ld16(addr + c + 16, sb);
+    add16<MASKED>(sa, nlse + c, j_min - c, c2, acc);
+    tmem_ld_wait16(sb);
+    tmem_ld16(addr + min(c + 32, cols - 32), sa);   // (the last one is not used)
+    add16<MASKED>(sb, nlse + c + 16, j_min - c - 16, c2, acc);
+  }
+  tmem_ld_wait16(sa);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    weight_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap_run,
+    weight_kernel(const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap_node,
                   const WeightParams p) {
   using C = Cfg<D>;
@@ -179,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::kKStages; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], kKWarps);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::kQStages; ++i) {
@@ -189,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::kLseStages; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], 4 * kSlots);
+      mbar_init(&l_empty[i], 8);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s_full[i], 1);
@@ -199,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&kmap_run);
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&qmap_node);
   }
@@ -248,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (run + excl <= x0 && x0 < run + excl + mine) s_range = Range{x0, x1, run + excl, b0 + tid};
     run += all;
   }
-  if (warp == 1) {
+  if (warp == 0) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -260,8 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t wlim = kWaitLimitNs;
   const int G = p.G, nodes = p.nodes;
 
-  if (warp == 0) {
-    // ================================================================ K producer
+  if (warp >= kKWarp) {
+    // ================================================================ K producers
+    constexpr int kMine = kPagesPerTile / kKWarps;          // pages of a tile for this warp
+    const int quarter = warp - kKWarp;
     int issued = 0, bits = 0;
     for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
       if (s.blocks == 0) return true;
@@ -288,24 +335,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int st = issued % C::kKStages;
-        if (!wait_warp(&k_empty[st], (static_cast<uint32_t>(issued / C::kKStages) & 1u) ^ 1u, abort, wlim)) {
+        if (!wait_lanes(&k_empty[st], (static_cast<uint32_t>(issued / C::kKStages) & 1u) ^ 1u, abort, wlim)) {
           if (lane == 0) set_abort(abort, p.dev_err);
           return false;
         }
-        const int page = __shfl_sync(0xffffffffu, now, sub * kPagesPerTile + lane % kPagesPerTile);
-        const int page0 = __shfl_sync(0xffffffffu, page, 0);
-        const bool together = __all_sync(0xffffffffu, page == page0 + lane % kPagesPerTile) &&
-                              page0 + kPagesPerTile <= p.num_pages;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
-        __syncwarp();
-        uint8_t* dst = k_s + st * C::kTileBytes;
-        if (together) {                       // eight consecutive pages: one box per half
-          if (lane < C::kHalves)
-            tma_load_3d(dst + lane * C::kHalfBytes, &kmap_run, &k_full[st], lane * 64, g, page0 * kPage);
-        } else if (lane < kPagesPerTile * C::kHalves) {
-          const int pq = lane % kPagesPerTile, hh = lane / kPagesPerTile;
-          tma_load_3d(dst + hh * C::kHalfBytes + pq * (kPage * 128), &kmap, &k_full[st], hh * 64, g,
-                      page * kPage);
+        uint8_t* dst = k_s + st * C::kTileBytes + quarter * kMine * (kPage * 128);
+        elect_arrive_expect_tx(&k_full[st], C::kTileBytes / kKWarps);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int page = __shfl_sync(0xffffffffu, now, sub * kPagesPerTile + quarter * kMine + i);
+#pragma unroll
+          for (int hh = 0; hh < C::kHalves; ++hh)
+            elect_tma_load_3d(dst + hh * C::kHalfBytes + i * (kPage * 128), &kmap, &k_full[st], hh * 64, g,
+                              page * kPage);
         }
         ++issued;
       }
@@ -318,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = max(0, issued - C::kKStages); i < issued; ++i)
         mbar_wait(&k_full[i % C::kKStages], static_cast<uint32_t>(i / C::kKStages) & 1u, &zero);
     }
-  } else if (warp == 1) {
+  } else if (warp == 0) {
     // ================================================================ MMA issuer
     const uint64_t dk = desc_sw128(smem_u32(k_s), 16, 1024);
     const uint64_t dq = desc_sw128(smem_u32(q_s), 16, 1024);
@@ -330,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // S^T of K stage k_at and row block q_at into a slot.
     auto issue = [&](int k_at, int q_at, int slot, int cols) -> bool {
-      if (!wait_warp(&s_empty[slot], (free_phase >> slot) & 1u, abort, wlim)) return false;
+      if (!wait_lanes(&s_empty[slot], (free_phase >> slot) & 1u, abort, wlim)) return false;
       free_phase ^= 1u << slot;
       tc_fence_after();
       mma_ss_tile<D / 16>(tmem + slot * kRowBlock,
@@ -344,10 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.blocks == 1) {
         const int cols = block_cols(s, 0, nodes, G);
         const int qs = q_no % C::kQStages;
-        if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+        if (!wait_lanes(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
         for (int i = 0; i < n; ++i, ++tile_no, ++k_no) {
           const int st = k_no % C::kKStages;
-          if (!wait_warp(&k_full[st], static_cast<uint32_t>(k_no / C::kKStages) & 1u, abort, wlim) ||
+          if (!wait_lanes(&k_full[st], static_cast<uint32_t>(k_no / C::kKStages) & 1u, abort, wlim) ||
               !issue(st, qs, tile_no % kSlots, cols))
             return fail();
           mma_commit(&k_empty[st]);
@@ -362,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int qb = qb0; qb < s.blocks; ++qb, ++q_no) {
           const int cols = block_cols(s, qb, nodes, G);
           const int qs = q_no % C::kQStages;
-          if (!wait_warp(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
+          if (!wait_lanes(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
           for (int i = 0; i < m; ++i) {
             const int st = (k_no + i) % C::kKStages;
             if (qb == qb0 &&
-                !wait_warp(&k_full[st], static_cast<uint32_t>((k_no + i) / C::kKStages) & 1u, abort, wlim))
+                !wait_lanes(&k_full[st], static_cast<uint32_t>((k_no + i) / C::kKStages) & 1u, abort, wlim))
               return fail();
             if (!issue(st, qs, (tile_no + i) % kSlots, cols)) return fail();
             if (qb == s.blocks - 1) mma_commit(&k_empty[st]);
@@ -422,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dead |= nl[u] == -INFINITY;           // (lse = +inf as well: it adds nothing)
       }
       const int ls = no % C::kLseStages;
-      if (!wait_warp(&q_empty[stage], (static_cast<uint32_t>(no / C::kQStages) & 1u) ^ 1u, abort, wlim) ||
-          !wait_warp(&l_empty[ls], (static_cast<uint32_t>(no / C::kLseStages) & 1u) ^ 1u, abort, wlim)) {
+      if (!wait_lanes(&q_empty[stage], (static_cast<uint32_t>(no / C::kQStages) & 1u) ^ 1u, abort, wlim) ||
+          !wait_lanes(&l_empty[ls], (static_cast<uint32_t>(no / C::kLseStages) & 1u) ^ 1u, abort, wlim)) {
         if (lane == 0) set_abort(abort, p.dev_err);
         return false;
       }
@@ -460,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_arrive(&l_full[ls]);
       if (rare) {
-        const bool ok = wait_warp(bar, static_cast<uint32_t>(raw_no++) & 1u, abort, wlim);
+        const bool ok = wait_lanes(bar, static_cast<uint32_t>(raw_no++) & 1u, abort, wlim);
         if (!ok) {
           if (lane == 0) set_abort(abort, p.dev_err);
           return false;
@@ -488,47 +530,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int zero = 0;
       mbar_wait(&q_full[stage], static_cast<uint32_t>(mine - 1) & 1u, &zero);
     }
-  } else if (warp >= kEpiWarp) {
+  } else if (warp >= kEpiWarp && warp < kKWarp) {
     // ================================================================ probabilities
-    const int slot = (warp - kEpiWarp) / 4;
+    const int wg = (warp - kEpiWarp) / 4;     // slots wg and wg + 2
     const int key = (warp & 3) * 32 + lane;   // TMEM lane = key of the tile
-    const uint32_t s_addr = tmem + slot * kRowBlock + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
     int tile_no = 0, q_no = 0;
-    uint32_t phase = 0;
+    uint32_t phases = 0;                      // parity to wait for on s_full, per slot
     auto fail = [&]() -> bool {
       if (lane == 0) set_abort(abort, p.dev_err);
       return false;
     };
     // Adds the block's probabilities to acc; row j of the block counts if j >= j_min.
-    auto add_block = [&](int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
-      if (!wait_warp(&s_full[slot], phase, abort, wlim)) return false;
-      phase ^= 1u;
-      __syncwarp();                           // lane 0 waited for the rows' lse, too
+    auto add_block = [&](int slot, int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
+      if (!wait_lanes(&s_full[slot], (phases >> slot) & 1u, abort, wlim)) return false;
+      phases ^= 1u << slot;
       tc_fence_after();
-      const bool all = __all_sync(0xffffffffu, j_min <= 0);
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        uint32_t sv[32];
-        tmem_ld32(s_addr + c0, sv);
-        tmem_ld_wait(sv);
-        const float4* nl = reinterpret_cast<const float4*>(&s_nlse[ls][c0]);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const float4 l = nl[v];
-          float x0, x1, x2, x3;
-          f2_split(ffma2(f2(__uint_as_float(sv[4 * v]), __uint_as_float(sv[4 * v + 1])), c2, f2(l.x, l.y)), x0, x1);
-          f2_split(ffma2(f2(__uint_as_float(sv[4 * v + 2]), __uint_as_float(sv[4 * v + 3])), c2, f2(l.z, l.w)), x2, x3);
-          if (!all) {
-            const int j = c0 + 4 * v;
-            if (j + 0 < j_min) x0 = -INFINITY;
-            if (j + 1 < j_min) x1 = -INFINITY;
-            if (j + 2 < j_min) x2 = -INFINITY;
-            if (j + 3 < j_min) x3 = -INFINITY;
-          }
-          acc[0] = fadd2(acc[0], f2(fast_exp2(x0), fast_exp2(x1)));
-          acc[1] = fadd2(acc[1], f2(fast_exp2(x2), fast_exp2(x3)));
-        }
-      }
+      if (__all_sync(0xffffffffu, j_min <= 0))
+        add_columns<false>(t_addr + slot * kRowBlock, s_nlse[ls], cols, j_min, c2, acc);
+      else
+        add_columns<true>(t_addr + slot * kRowBlock, s_nlse[ls], cols, j_min, c2, acc);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[slot]);
@@ -546,44 +568,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < s.L) p.weight_out[at] = old + ((a + c) + (d + e));
     };
     for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
-      if (s.blocks <= 1) {
-        const int cols = block_cols(s, 0, nodes, G);
-        const int ls = q_no % C::kLseStages;
-        if (s.blocks == 1 &&
-            !wait_warp(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim))
-          return fail();
-        for (int i = 0; i < n; ++i, ++tile_no) {
-          if (tile_no % kSlots != slot) continue;
-          const int t = (t0 + i) * kKeyTile + key;
-          const float old = old_weight(b, t, s);
-          uint64_t acc[2] = {0ull, 0ull};
-          if (s.blocks == 1 && !add_block(ls, cols, max(t - s.P, 0) * G, acc)) return fail();
-          write(b, t, s, old, acc);
-        }
-        if (s.blocks == 1) {
+      // With one row block its lse stays for the whole run.
+      const bool one = s.blocks == 1;
+      for (int i0 = 0; i0 < n; i0 += kGroup) {
+        const int m = min(kGroup, n - i0);
+        const int ia = (tile_no ^ wg) & 1, ib = ia + 2;     // this warpgroup's tiles of the group
+        const int ta = (t0 + i0 + ia) * kKeyTile + key, tb = ta + 2 * kKeyTile;
+        const int slot_a = (tile_no + ia) % kSlots, slot_b = (tile_no + ib) % kSlots;
+        float old_a = 0.f, old_b = 0.f;
+        if (ia < m) old_a = old_weight(b, ta, s);
+        if (ib < m) old_b = old_weight(b, tb, s);
+        uint64_t acc_a[2] = {0ull, 0ull}, acc_b[2] = {0ull, 0ull};
+        for (int qb = first_block(s, t0 + i0, nodes); qb < s.blocks; ++qb) {
+          const int ls = q_no % C::kLseStages;
+          if ((!one || i0 == 0) &&
+              !wait_lanes(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim))
+            return fail();
+          const int cols = block_cols(s, qb, nodes, G);
+          if (ia < m && !add_block(slot_a, ls, cols, (max(ta - s.P, 0) - qb * nodes) * G, acc_a)) return fail();
+          if (ib < m && !add_block(slot_b, ls, cols, (max(tb - s.P, 0) - qb * nodes) * G, acc_b)) return fail();
+          if (one && i0 + kGroup < n) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[ls]);
           ++q_no;
         }
-        return true;
-      }
-      for (int i0 = 0; i0 < n; i0 += kGroup) {
-        const int m = min(kGroup, n - i0);
-        const int my = (slot - tile_no % kSlots + kSlots) % kSlots;   // this slot's tile of the group
-        const int t = (t0 + i0 + my) * kKeyTile + key;
-        float old = 0.f;
-        if (my < m) old = old_weight(b, t, s);
-        uint64_t acc[2] = {0ull, 0ull};
-        for (int qb = first_block(s, t0 + i0, nodes); qb < s.blocks; ++qb, ++q_no) {
-          const int ls = q_no % C::kLseStages;
-          if (!wait_warp(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim)) return fail();
-          if (my < m) {
-            if (!add_block(ls, block_cols(s, qb, nodes, G), (max(t - s.P, 0) - qb * nodes) * G, acc)) return fail();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&l_empty[ls]);
-        }
-        if (my < m) write(b, t, s, old, acc);
+        if (ia < m) write(b, ta, s, old_a, acc_a);
+        if (ib < m) write(b, tb, s, old_b, acc_b);
         tile_no += m;
       }
       return true;
@@ -592,17 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   grid_dependents_launch();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
-jf_status launch_weight(const CUtensorMap& km, const CUtensorMap& kr, const CUtensorMap& qm,
-                        const CUtensorMap& qn, const WeightParams& p, int sms, cudaStream_t s) {
+jf_status launch_weight(const CUtensorMap& km, const CUtensorMap& qm, const CUtensorMap& qn,
+                        const WeightParams& p, int sms, cudaStream_t s) {
   static SmemAttr attr;
   if (!attr.ensure(weight_kernel<D>, Cfg<D>::kSmemBytes)) return JF_ERR_CUDA;
   const int ranges = std::max(1, sms / p.Hkv);
   const cudaError_t e = launch_pdl(weight_kernel<D>, dim3(static_cast<unsigned>(ranges * p.Hkv)), dim3(kThreads),
-                                   Cfg<D>::kSmemBytes, s, km, kr, qm, qn, p);
+                                   Cfg<D>::kSmemBytes, s, km, qm, qn, p);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
@@ -654,13 +664,12 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.scale_log2 = scale * kLog2e;
-  CUtensorMap km, kr;
+  CUtensorMap km;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
                               static_cast<cuuint64_t>(num_pages) * kPage};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
-  const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
-  if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&kr, k_cache, 3, dims, strides, box_run))
-    return JF_ERR_CUDA;
+  const cuuint32_t box[3] = {64, 1, kPage};
+  if (!encode(&km, k_cache, 3, dims, strides, box)) return JF_ERR_CUDA;
   CUtensorMap qm, qn;
   const cuuint64_t rows = cu != nullptr ? static_cast<cuuint64_t>(T) : static_cast<cuuint64_t>(N);
   const cuuint64_t qdims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), rows,
@@ -671,8 +680,7 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   const cuuint32_t qbox_node[4] = {64, static_cast<cuuint32_t>(p.G), 1, 1};
   if (!encode(&qm, q, 4, qdims, qstrides, qbox) || !encode(&qn, q, 4, qdims, qstrides, qbox_node)) return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return D == 128 ? launch_weight<128>(km, kr, qm, qn, p, sms, s)
-                  : launch_weight<64>(km, kr, qm, qn, p, sms, s);
+  return D == 128 ? launch_weight<128>(km, qm, qn, p, sms, s) : launch_weight<64>(km, qm, qn, p, sms, s);
 }
 
 }  // namespace
