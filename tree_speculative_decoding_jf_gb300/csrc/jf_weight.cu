@@ -20,7 +20,9 @@
 // whole run of the sequence.
 //
 // Roles (512 threads):
-//   warp 0         allocates TMEM, issues the MMAs.
+//   warps 0, 1     issue the MMAs of the even and the odd tiles (warp 0 allocates TMEM): one
+//                  warp's waits and bookkeeping, some 500 cycles a tile, pass while the
+//                  other's eight MMAs run.
 //   warps 2, 3     query rows, one warp per stage: a full block of a chain as one TMA box
 //                  per 64-column half, else one box per (node, half), and the rows' lse.
 //                  (Gathered with 16-byte asynchronous copies instead, a block took 13,000
@@ -65,6 +67,11 @@ struct Cfg {
   // 160 KB of K in flight, far above the ~45 KB an SM needs to cover the latency of HBM at
   // its share of the bandwidth, and a group's four tiles plus the next one for D = 128.
   static constexpr int kKStages = D == 128 ? 5 : 10;
+  // Barriers of the ring: twice the stages, so that every barrier belongs to tiles of one
+  // parity and thus to one MMA warp.  (With one a stage, a warp may come to wait for the
+  // phase after one that the other warp's tile has not completed, and a parity wait takes
+  // the phase before that for its own.)
+  static constexpr int kKBars = 2 * kKStages;
   static constexpr int kQStages = 2;          // one producer warp each
   static constexpr int kLseStages = 3;        // held until the probabilities are added
   static constexpr int kQOff = kKStages * kTileBytes;
@@ -211,12 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            ~static_cast<uintptr_t>(1023));
   uint8_t* k_s = sm;
   uint8_t* q_s = sm + C::kQOff;
-  __shared__ uint64_t k_full[C::kKStages], k_empty[C::kKStages];
+  __shared__ uint64_t k_full[C::kKBars], k_empty[C::kKBars];
   __shared__ uint64_t q_full[C::kQStages], q_empty[C::kQStages], q_raw[C::kQStages];
   __shared__ uint64_t l_full[C::kLseStages], l_empty[C::kLseStages];
   __shared__ uint64_t s_full[kSlots], s_empty[kSlots], fin;
   __shared__ __align__(16) float s_nlse[C::kLseStages][kRowBlock];   // -lse in log2 units
-  __shared__ long long s_scan[kThreads / 32];
   __shared__ Range s_range;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -224,13 +230,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < C::kKStages; ++i) {
+    for (int i = 0; i < C::kKBars; ++i) {
       mbar_init(&k_full[i], kKWarps);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::kQStages; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);
       mbar_init(&q_raw[i], 1);
     }
     for (int i = 0; i < C::kLseStages; ++i) {
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
     }
-    mbar_init(&fin, 1);
+    mbar_init(&fin, 2);
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
@@ -257,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s.bits && blockIdx.x == 0) report(p.dev_err, s.bits);
     return static_cast<long long>(s.tiles) * s.unit;
   };
+  long long* s_scan = reinterpret_cast<long long*>(&s_nlse[0][0]);   // not in use yet
   auto scan = [&](long long mine, long long* excl) -> long long {   // returns the block's sum
     long long incl = mine;
 #pragma unroll
@@ -334,19 +341,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             bits |= JF_DEVERR_BAD_PAGE;
           }
         }
-        const int st = issued % C::kKStages;
-        if (!wait_lanes(&k_empty[st], (static_cast<uint32_t>(issued / C::kKStages) & 1u) ^ 1u, abort, wlim)) {
+        const int st = issued % C::kKStages, before = issued - C::kKStages;   // the stage's last tile
+        if (before >= 0 && !wait_lanes(&k_empty[before % C::kKBars], static_cast<uint32_t>(before / C::kKBars) & 1u,
+                                       abort, wlim)) {
           if (lane == 0) set_abort(abort, p.dev_err);
           return false;
         }
+        uint64_t* full = &k_full[issued % C::kKBars];
         uint8_t* dst = k_s + st * C::kTileBytes + quarter * kMine * (kPage * 128);
-        elect_arrive_expect_tx(&k_full[st], C::kTileBytes / kKWarps);
+        elect_arrive_expect_tx(full, C::kTileBytes / kKWarps);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
           const int page = __shfl_sync(0xffffffffu, now, sub * kPagesPerTile + quarter * kMine + i);
 #pragma unroll
           for (int hh = 0; hh < C::kHalves; ++hh)
-            elect_tma_load_3d(dst + hh * C::kHalfBytes + i * (kPage * 128), &kmap, &k_full[st], hh * 64, g,
+            elect_tma_load_3d(dst + hh * C::kHalfBytes + i * (kPage * 128), &kmap, full, hh * 64, g,
                               page * kPage);
         }
         ++issued;
@@ -358,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {                          // no copy is still landing when the CTA exits
       int zero = 0;
       for (int i = max(0, issued - C::kKStages); i < issued; ++i)
-        mbar_wait(&k_full[i % C::kKStages], static_cast<uint32_t>(i / C::kKStages) & 1u, &zero);
+        mbar_wait(&k_full[i % C::kKBars], static_cast<uint32_t>(i / C::kKBars) & 1u, &zero);
     }
-  } else if (warp == 0) {
+  } else if (warp < kQWarp) {
     // ================================================================ MMA issuer
     const uint64_t dk = desc_sw128(smem_u32(k_s), 16, 1024);
     const uint64_t dq = desc_sw128(smem_u32(q_s), 16, 1024);
-    int tile_no = 0, k_no = 0, q_no = 0;      // tiles, K stages and row blocks so far
+    int tile_no = 0, q_no = 0;                // tiles and row blocks so far
     uint32_t free_phase = (1u << kSlots) - 1u;  // parity to wait for on s_empty, per slot
     auto fail = [&]() -> bool {
       if (lane == 0) set_abort(abort, p.dev_err);
@@ -383,40 +392,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
-      if (s.blocks == 1) {
-        const int cols = block_cols(s, 0, nodes, G);
-        const int qs = q_no % C::kQStages;
-        if (!wait_lanes(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
-        for (int i = 0; i < n; ++i, ++tile_no, ++k_no) {
-          const int st = k_no % C::kKStages;
-          if (!wait_lanes(&k_full[st], static_cast<uint32_t>(k_no / C::kKStages) & 1u, abort, wlim) ||
-              !issue(st, qs, tile_no % kSlots, cols))
-            return fail();
-          mma_commit(&k_empty[st]);
-        }
-        mma_commit(&q_empty[qs]);
-        ++q_no;
-        return true;
-      }
+      if (s.blocks == 0) return true;
+      const bool one = s.blocks == 1;         // its block stays for the whole run
       for (int i0 = 0; i0 < n; i0 += kGroup) {
-        const int m = min(kGroup, n - i0);
+        const int m = min(kGroup, n - i0), ia = (tile_no ^ warp) & 1;
+        const int na = tile_no + ia, nb = na + 2;           // this warp's tiles of the group
+        const int ka = na % C::kKBars, kb = nb % C::kKBars;
+        const uint32_t pa = static_cast<uint32_t>(na / C::kKBars) & 1u;
+        const uint32_t pb = static_cast<uint32_t>(nb / C::kKBars) & 1u;
+        const int sa = na % kSlots, sb = nb % kSlots;
         const int qb0 = first_block(s, t0 + i0, nodes);
-        for (int qb = qb0; qb < s.blocks; ++qb, ++q_no) {
+        for (int qb = qb0; qb < s.blocks; ++qb) {
+          const bool last = qb == s.blocks - 1;
           const int cols = block_cols(s, qb, nodes, G);
           const int qs = q_no % C::kQStages;
-          if (!wait_lanes(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim)) return fail();
-          for (int i = 0; i < m; ++i) {
-            const int st = (k_no + i) % C::kKStages;
-            if (qb == qb0 &&
-                !wait_lanes(&k_full[st], static_cast<uint32_t>((k_no + i) / C::kKStages) & 1u, abort, wlim))
-              return fail();
-            if (!issue(st, qs, (tile_no + i) % kSlots, cols)) return fail();
-            if (qb == s.blocks - 1) mma_commit(&k_empty[st]);
+          if ((!one || i0 == 0) &&
+              !wait_lanes(&q_full[qs], static_cast<uint32_t>(q_no / C::kQStages) & 1u, abort, wlim))
+            return fail();
+          if (ia < m) {
+            if (qb == qb0 && !wait_lanes(&k_full[ka], pa, abort, wlim)) return fail();
+            if (!issue(na % C::kKStages, qs, sa, cols)) return fail();
+            if (last) mma_commit(&k_empty[ka]);
           }
+          if (ia + 2 < m) {
+            if (qb == qb0 && !wait_lanes(&k_full[kb], pb, abort, wlim)) return fail();
+            if (!issue(nb % C::kKStages, qs, sb, cols)) return fail();
+            if (last) mma_commit(&k_empty[kb]);
+          }
+          if (one && i0 + kGroup < n) break;
           mma_commit(&q_empty[qs]);
+          ++q_no;
         }
         tile_no += m;
-        if (s.blocks > 0) k_no += m;
       }
       return true;
     });
@@ -568,6 +575,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < s.L) p.weight_out[at] = old + ((a + c) + (d + e));
     };
     for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
+      if (s.blocks == 0) {                    // no rows: the old weights, nothing from the tensor cores
+        for (int i = wg; i < n; i += 2) {
+          const int t = (t0 + i) * kKeyTile + key;
+          const uint64_t none[2] = {0ull, 0ull};
+          write(b, t, s, old_weight(b, t, s), none);
+        }
+        return true;
+      }
       // With one row block its lse stays for the whole run.
       const bool one = s.blocks == 1;
       for (int i0 = 0; i0 < n; i0 += kGroup) {
