@@ -19,7 +19,7 @@
 // row block loaded; with one row block (a verified path) it stays in shared memory for the
 // whole run of the sequence.
 //
-// Roles (512 threads):
+// Roles (768 threads):
 //   warps 0, 1     issue the MMAs of the even and the odd tiles (warp 0 allocates TMEM): one
 //                  warp's waits and bookkeeping, some 500 cycles a tile, pass while the
 //                  other's eight MMAs run.
@@ -27,9 +27,11 @@
 //                  per 64-column half, else one box per (node, half), and the rows' lse.
 //                  (Gathered with 16-byte asynchronous copies instead, a block took 13,000
 //                  cycles to issue beside the polling warps.)
-//   warps 4..11    two warpgroups with two TMEM slots (128 columns) each: tile c of the CTA
-//                  goes to slot c % 4, so one slot is refilled while the other is read.
-//   warps 12..15   K tiles by TMA into a ring, a quarter of every tile's pages each (issued
+//   warps 4..19    four warpgroups, one per TMEM slot (128 columns): tile c of the CTA goes
+//                  to slot c % 4.  (Two warpgroups with two slots each leave a scheduler
+//                  with two such warps and their latencies: 136 us against 122 on a 512-row
+//                  window over 2 x 16K keys.)
+//   warps 20..23   K tiles by TMA into a ring, a quarter of every tile's pages each (issued
 //                  from 16 lanes of one warp, a tile's boxes took 1400 cycles to go out,
 //                  more than its share of the HBM bandwidth); page ids four to eight tiles
 //                  ahead; pages past the end and malformed ids load as zeros.
@@ -52,10 +54,10 @@ constexpr int kPage = 16;
 constexpr int kKeyTile = 128;
 constexpr int kPagesPerTile = kKeyTile / kPage;
 constexpr int kRowBlock = 128;
-constexpr int kSlots = 4;                 // TMEM slots, two for each epilogue warpgroup
+constexpr int kSlots = 4;                 // TMEM slots = epilogue warpgroups
 constexpr int kGroup = kSlots;            // key tiles that share a loaded row block
-constexpr int kThreads = 512;
-constexpr int kQWarp = 2, kEpiWarp = 4, kKWarp = 12;   // first warps of the roles
+constexpr int kThreads = 768;
+constexpr int kQWarp = 2, kEpiWarp = 4, kKWarp = 20;   // first warps of the roles
 constexpr int kKWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < C::kLseStages; ++i) {
       mbar_init(&l_full[i], 32);
-      mbar_init(&l_empty[i], 8);
+      mbar_init(&l_empty[i], 4 * kSlots);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s_full[i], 1);
@@ -539,20 +541,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kEpiWarp && warp < kKWarp) {
     // ================================================================ probabilities
-    const int wg = (warp - kEpiWarp) / 4;     // slots wg and wg + 2
+    const int slot = (warp - kEpiWarp) / 4;   // this warpgroup's
     const int key = (warp & 3) * 32 + lane;   // TMEM lane = key of the tile
     const uint32_t t_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
     int tile_no = 0, q_no = 0;
-    uint32_t phases = 0;                      // parity to wait for on s_full, per slot
+    uint32_t phase = 0;                       // parity to wait for on s_full
     auto fail = [&]() -> bool {
       if (lane == 0) set_abort(abort, p.dev_err);
       return false;
     };
     // Adds the block's probabilities to acc; row j of the block counts if j >= j_min.
-    auto add_block = [&](int slot, int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
-      if (!wait_lanes(&s_full[slot], (phases >> slot) & 1u, abort, wlim)) return false;
-      phases ^= 1u << slot;
+    auto add_block = [&](int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
+      if (!wait_lanes(&s_full[slot], phase, abort, wlim)) return false;
+      phase ^= 1u;
       tc_fence_after();
       if (__all_sync(0xffffffffu, j_min <= 0))
         add_columns<false>(t_addr + slot * kRowBlock, s_nlse[ls], cols, j_min, c2, acc);
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for_each_run(p, range, [&](int b, int t0, int n, const SeqInfo& s) -> bool {
       if (s.blocks == 0) {                    // no rows: the old weights, nothing from the tensor cores
-        for (int i = wg; i < n; i += 2) {
+        for (int i = slot; i < n; i += kSlots) {
           const int t = (t0 + i) * kKeyTile + key;
           const uint64_t none[2] = {0ull, 0ull};
           write(b, t, s, old_weight(b, t, s), none);
@@ -587,28 +589,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool one = s.blocks == 1;
       for (int i0 = 0; i0 < n; i0 += kGroup) {
         const int m = min(kGroup, n - i0);
-        const int ia = (tile_no ^ wg) & 1, ib = ia + 2;     // this warpgroup's tiles of the group
-        const int ta = (t0 + i0 + ia) * kKeyTile + key, tb = ta + 2 * kKeyTile;
-        const int slot_a = (tile_no + ia) % kSlots, slot_b = (tile_no + ib) % kSlots;
-        float old_a = 0.f, old_b = 0.f;
-        if (ia < m) old_a = old_weight(b, ta, s);
-        if (ib < m) old_b = old_weight(b, tb, s);
-        uint64_t acc_a[2] = {0ull, 0ull}, acc_b[2] = {0ull, 0ull};
+        const int i = (slot - tile_no) & (kSlots - 1);      // this warpgroup's tile of the group
+        const int t = (t0 + i0 + i) * kKeyTile + key;
+        float old = 0.f;
+        if (i < m) old = old_weight(b, t, s);
+        uint64_t acc[2] = {0ull, 0ull};
         for (int qb = first_block(s, t0 + i0, nodes); qb < s.blocks; ++qb) {
           const int ls = q_no % C::kLseStages;
           if ((!one || i0 == 0) &&
               !wait_lanes(&l_full[ls], static_cast<uint32_t>(q_no / C::kLseStages) & 1u, abort, wlim))
             return fail();
           const int cols = block_cols(s, qb, nodes, G);
-          if (ia < m && !add_block(slot_a, ls, cols, (max(ta - s.P, 0) - qb * nodes) * G, acc_a)) return fail();
-          if (ib < m && !add_block(slot_b, ls, cols, (max(tb - s.P, 0) - qb * nodes) * G, acc_b)) return fail();
+          if (i < m && !add_block(ls, cols, (max(t - s.P, 0) - qb * nodes) * G, acc)) return fail();
           if (one && i0 + kGroup < n) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&l_empty[ls]);
           ++q_no;
         }
-        if (ia < m) write(b, ta, s, old_a, acc_a);
-        if (ib < m) write(b, tb, s, old_b, acc_b);
+        if (i < m) write(b, t, s, old, acc);
         tile_no += m;
       }
       return true;
