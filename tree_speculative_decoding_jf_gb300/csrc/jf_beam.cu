@@ -15,27 +15,15 @@ constexpr int kMaxK = 64;
 // ------------------------------------------------------------------------ candidates
 //
 // Within a beam the pairs rank as the logits do, so a slice of a row contributes at most
-// its K greatest logits.  A thread's 16-byte vectors stay in registers: the slice's maximum,
-// its sum of exponentials and its candidates come from one read.  The K-th greatest of the
-// 256 threads' maxima is a value that K logits of the slice reach, so only logits at or
-// above it are looked at again.
+// its K greatest logits.  A thread's 16-byte vectors stay packed in registers: the slice's
+// maximum, its sum of exponentials and its candidates come from one read of the logits,
+// which is all that bounds the call (bytes / HBM bandwidth).  The K-th greatest of 32 (or,
+// for K > 16, 256) groups' maxima is a value that K logits of the slice reach, so only
+// vectors that reach it are looked at logit by logit.
 constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kCandCap = 512;
-
-template <typename T>
-struct Vec;
-template <>
-struct Vec<uint16_t> {
-  static constexpr int kN = 8;
-};
-template <>
-struct Vec<float> {
-  static constexpr int kN = 4;
-};
-
-__device__ __forceinline__ float logit(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-__device__ __forceinline__ float logit(float x) { return x; }
+constexpr uint32_t kNegInfKey = 0x007fffffu;   // logit_key(-inf)
 
 // Orders as the value does; NaN lowest, -0 == +0.
 __device__ __forceinline__ uint32_t logit_key(float x) {
@@ -49,6 +37,44 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
+template <typename T>
+struct Row;
+template <>
+struct Row<uint16_t> {                    // bf16
+  static constexpr int kN = 8;            // logits of a 16-byte vector
+  static constexpr uint32_t kNone = 0xff80ff80u;   // -inf, -inf
+  static __device__ __forceinline__ float get(const uint4& v, int c) {
+    const uint32_t w = (&v.x)[c >> 1];
+    return __uint_as_float((c & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+  static __device__ __forceinline__ void put(uint4& v, int c, uint16_t x) {
+    uint32_t& w = (&v.x)[c >> 1];
+    w = (c & 1) ? ((w & 0xffffu) | (static_cast<uint32_t>(x) << 16)) : ((w & 0xffff0000u) | x);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <>
+struct Row<float> {
+  static constexpr int kN = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  static __device__ __forceinline__ float get(const uint4& v, int c) { return __uint_as_float((&v.x)[c]); }
+  static __device__ __forceinline__ void put(uint4& v, int c, float x) { (&v.x)[c] = __float_as_uint(x); }
+  static __device__ __forceinline__ float vmax(const uint4& v) {
+    return fmaxf(fmaxf(get(v, 0), get(v, 1)), fmaxf(get(v, 2), get(v, 3)));
+  }
+};
+
+__device__ __forceinline__ float to_float(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float to_float(float x) { return x; }
+
 struct BeamParams {
   const void* logits;
   const float* score;
@@ -59,140 +85,164 @@ struct BeamParams {
   int32_t* new_finished;
   float2* stats;          // [rows][chunks]: maximum, sum of exp(x - maximum)
   uint64_t* cand;         // [rows][chunks][K]: logit key << 32 | ~token, descending; 0 = none
-  int W, V, K, eos, chunks, chunk_len;
+  int W, V, K, eos, chunks, chunk_vecs;
 };
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamParams p) {
-  constexpr int VN = Vec<T>::kN;
+__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamParams p) {
+  using R = Row<T>;
+  constexpr int VN = R::kN;
   __shared__ uint32_t s_max[kScanThreads];
-  __shared__ float s_f[kScanWarps];
   __shared__ float s_sum[kScanWarps];
-  __shared__ uint32_t s_thr;
   __shared__ int s_n;
   __shared__ uint64_t s_cand[kCandCap];
   __shared__ uint64_t s_best[kScanWarps];
   grid_dependency_wait();
   const int chunk = blockIdx.x % p.chunks, row = blockIdx.x / p.chunks;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* out = p.cand + (static_cast<size_t>(row) * p.chunks + chunk) * p.K;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
+  uint64_t* out = p.cand + (static_cast<size_t>(row) * p.chunks + chunk) * K;
   if ((p.finished != nullptr && p.finished[row] != 0) || p.score[row] == -INFINITY) {
     grid_dependents_launch();
     return;                               // the merge makes this beam's pairs itself
   }
+  // Vectors start at the 16-byte boundary at or below the row's first logit: logit e of the
+  // row is element e + off of the vectors.  Vectors that reach over either end of the row
+  // are read logit by logit.
   const T* x = static_cast<const T*>(p.logits) + static_cast<size_t>(row) * p.V;
-  const int v_lo = chunk * p.chunk_len, v_hi = min(p.V, v_lo + p.chunk_len);
-
-  float v[NV][VN];
-  const bool vec_ok = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-  float m = -INFINITY;
-  uint32_t best = 0u;
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const int vec0 = chunk * p.chunk_vecs;
+  auto first_of = [&](int i) { return (vec0 + i * kScanThreads + tid) * VN - off; };
+  uint4 v[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int at = v_lo + (i * kScanThreads + tid) * VN;
-    if (vec_ok && at + VN <= v_hi) {
-      const uint4 raw = *reinterpret_cast<const uint4*>(x + at);
-      const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-      for (int c = 0; c < VN; ++c) v[i][c] = logit(e[c]);
+    const int at = first_of(i);
+    const bool mine = i * kScanThreads + tid < p.chunk_vecs;
+    if (mine && at >= 0 && at + VN <= p.V) {
+      v[i] = __ldg(reinterpret_cast<const uint4*>(x + at));
     } else {
+      v[i] = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+      if (mine) {
 #pragma unroll
-      for (int c = 0; c < VN; ++c) v[i][c] = at + c < v_hi ? logit(x[at + c]) : -INFINITY;
+        for (int c = 0; c < VN; ++c)
+          if (at + c >= 0 && at + c < p.V) R::put(v[i], c, x[at + c]);
+      }
     }
   }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) m = fmaxf(m, R::vmax(v[i]));
+  const uint32_t best = logit_key(m);
+  s_max[tid] = best;
+  if (tid == 0) s_n = 0;
+  __syncthreads();
+  // Every warp: the slice's maximum and the K-th greatest group maximum to 16 bits (a lower
+  // bound), bit by bit.
+  uint32_t mx[kScanWarps], gmax = 0u;
+#pragma unroll
+  for (int i = 0; i < kScanWarps; ++i) {
+    mx[i] = s_max[i * 32 + lane];
+    gmax = max(gmax, mx[i]);
+  }
+  const uint32_t top = __reduce_max_sync(0xffffffffu, gmax);
+  uint32_t thr = 0u;
+  if (K <= 16) {
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t at = thr | (1u << bit);
+      if (__popc(__ballot_sync(0xffffffffu, gmax >= at)) >= K) thr = at;
+    }
+  } else {
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t at = thr | (1u << bit);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kScanWarps; ++i) n += mx[i] >= at;
+      if (__reduce_add_sync(0xffffffffu, n) >= K) thr = at;
+    }
+  }
+  // A bound of -inf (a slice with few allowed tokens): collect what lies above it, the rest
+  // of the list is the first tokens at -inf.
+  const bool sparse = thr <= kNegInfKey;
+  if (sparse) thr = kNegInfKey + 1u;
+  const float M = key_logit(top), ref = M == -INFINITY ? 0.f : M;
+  const uint64_t neg = f2(-ref, -ref), l2e = f2(1.4426950408889634f, 1.4426950408889634f);
+  uint64_t acc = 0ull, acc1 = 0ull;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int c = 0; c < VN; ++c) m = fmaxf(m, v[i][c]);
-  best = logit_key(m);
-  s_max[tid] = best;
-  float wm = m;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  if (lane == 0) s_f[warp] = wm;
-  if (tid == 0) s_n = 0;
-  __syncthreads();
-  float M = s_f[0];
-  for (int i = 1; i < kScanWarps; ++i) M = fmaxf(M, s_f[i]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float part = 0.f;
-#pragma unroll
-    for (int c = 0; c < VN; ++c) part += exp2f((v[i][c] - ref) * 1.4426950408889634f);
-    sum += part;
-  }
+    for (int c = 0; c < VN; c += 4) {
+      float a, b, d, e;
+      f2_split(fmul2(fadd2(f2(R::get(v[i], c), R::get(v[i], c + 1)), neg), l2e), a, b);
+      f2_split(fmul2(fadd2(f2(R::get(v[i], c + 2), R::get(v[i], c + 3)), neg), l2e), d, e);
+      acc = fadd2(acc, f2(fast_exp2(a), fast_exp2(b)));
+      acc1 = fadd2(acc1, f2(fast_exp2(d), fast_exp2(e)));
+    }
+  float a, b;
+  f2_split(fadd2(acc, acc1), a, b);
+  float sum = a + b;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
-  // The K-th greatest thread maximum, bit by bit (warp 0, eight maxima a lane).
-  if (warp == 0) {
-    uint32_t mx[kScanWarps];
-#pragma unroll
-    for (int i = 0; i < kScanWarps; ++i) mx[i] = s_max[i * 32 + lane];
-    uint32_t thr = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t tryv = thr | (1u << bit);
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < kScanWarps; ++i) n += mx[i] >= tryv;
-      if (__reduce_add_sync(0xffffffffu, n) >= p.K) thr = tryv;
-    }
-    if (lane == 0) s_thr = thr;
-  }
-  __syncthreads();
-  const uint32_t thr = s_thr;
-  if (tid == 0) {
-    float s = 0.f;
-    for (int i = 0; i < kScanWarps; ++i) s += s_sum[i];
-    p.stats[static_cast<size_t>(row) * p.chunks + chunk] = make_float2(M, s);
-  }
   if (best >= thr) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      if (logit_key(R::vmax(v[i])) < thr) continue;
 #pragma unroll
       for (int c = 0; c < VN; ++c) {
-        const int at = v_lo + (i * kScanThreads + tid) * VN + c;
-        const uint32_t key = logit_key(v[i][c]);
-        if (key >= thr && at < v_hi) {
-          const int n = atomicAdd(&s_n, 1);
-          if (n < kCandCap) s_cand[n] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
-        }
+        const int at = first_of(i) + c;
+        const uint32_t key = logit_key(R::get(v[i], c));
+        if (key < thr || at < 0 || at >= p.V) continue;
+        const int n = atomicAdd(&s_n, 1);
+        if (n < kCandCap) s_cand[n] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
       }
+    }
   }
   __syncthreads();
   const int n = s_n;
+  if (tid == 0) {
+    float t = 0.f;
+    for (int i = 0; i < kScanWarps; ++i) t += s_sum[i];
+    p.stats[static_cast<size_t>(row) * p.chunks + chunk] = make_float2(M, t);
+  }
   if (n <= kCandCap) {
-    for (int i = tid; i < max(n, p.K); i += kScanThreads) {
-      if (i >= n) {
-        out[i] = 0ull;                    // a slice shorter than K
-        continue;
-      }
+    for (int i = tid; i < n; i += kScanThreads) {
       const uint64_t mine = s_cand[i];
       int r = 0;
       for (int j = 0; j < n; ++j) r += s_cand[j] > mine;
-      if (r < p.K) out[r] = mine;
+      if (r < K) out[r] = mine;
     }
-  } else {                                // ties: K rounds over the whole slice
-    uint64_t last = ~0ull;
-    for (int r = 0; r < p.K; ++r) {
-      uint64_t top = 0ull;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < VN; ++c) {
-          const int at = v_lo + (i * kScanThreads + tid) * VN + c;
-          const uint64_t e = (static_cast<uint64_t>(logit_key(v[i][c])) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
-          if (at < v_hi && e < last && e > top) top = e;
+    if (n < K) {                          // sparse, or a slice shorter than K
+      const int lo = max(0, vec0 * VN - off), hi = min(p.V, (vec0 + p.chunk_vecs) * VN - off);
+      if (warp == 0) {
+        int at = n;
+        for (int t0 = lo; t0 < hi && at < K && sparse; t0 += 32) {
+          const int t = t0 + lane;
+          const bool none = t < hi && to_float(x[t]) == -INFINITY;
+          const uint32_t ms = __ballot_sync(0xffffffffu, none);
+          const int r = at + __popc(ms & ((1u << lane) - 1u));
+          if (none && r < K)
+            out[r] = (static_cast<uint64_t>(kNegInfKey) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
+          at += __popc(ms);
         }
+        for (int r = min(at, K) + lane; r < K; r += 32) out[r] = 0ull;
+      }
+    }
+  } else {                                // many equal logits: K rounds over the whole slice
+    const int lo = max(0, vec0 * VN - off), hi = min(p.V, (vec0 + p.chunk_vecs) * VN - off);
+    uint64_t last = ~0ull;
+    for (int r = 0; r < K; ++r) {
+      uint64_t most = 0ull;
+      for (int t = lo + tid; t < hi; t += kScanThreads) {
+        const uint64_t e = (static_cast<uint64_t>(logit_key(to_float(x[t]))) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
+        if (e < last && e > most) most = e;
+      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) s_best[warp] = top;
+      for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      if (lane == 0) s_best[warp] = most;
       __syncthreads();
-      for (int i = 0; i < kScanWarps; ++i) top = max(top, s_best[i]);
-      if (tid == 0) out[r] = top;
-      last = top;
+      for (int i = 0; i < kScanWarps; ++i) most = max(most, s_best[i]);
+      if (tid == 0) out[r] = most;
+      last = most;
       __syncthreads();
     }
   }
@@ -220,42 +270,54 @@ __device__ __forceinline__ double key_score(uint64_t k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 512;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeCand = 4096;          // candidates held on chip when they fit
 
 // One CTA per prompt.  A list is a slice's candidates in descending order.  The K-th best
 // of the lists' first `first` entries bounds the K-th best pair from below; since pairs
 // rank strictly, at most K lists reach the bound, so the survivors are at most K * K.
+// Bound by its chain of small steps: the statistics and all candidates are fetched
+// together, one warp a beam forms the log-sum-exp.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
-  extern __shared__ uint64_t s_raw[];
+  extern __shared__ uint64_t s_dyn[];
   __shared__ int s_n;
   __shared__ Pair s_bound;
   grid_dependency_wait();
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = p.W, K = p.K, lists = W * p.chunks;
   const int first = min(K, (K + lists - 1) / lists), heads = lists * first;
-  double* s_off = reinterpret_cast<double*>(s_raw);                // [W]: score - lse
+  const bool held = static_cast<long long>(lists) * K <= kMergeCand;
+  double* s_off = reinterpret_cast<double*>(s_dyn);                // [W]: score - lse
   int* s_kind = reinterpret_cast<int*>(s_off + W);                 // [W]: 0 live, 1 finished, 2 dead
-  uint64_t* s_key = reinterpret_cast<uint64_t*>(s_off + W + (W + 1) / 2);
+  uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_off + W + (W + 1) / 2);
+  uint64_t* s_key = s_cand + (held ? lists * K : 0);
   const int room = max(heads, K * K);
   uint32_t* s_flat = reinterpret_cast<uint32_t*>(s_key + room);
-  for (int w = tid; w < W; w += kMergeThreads) {
+  const uint64_t* cand = p.cand + static_cast<size_t>(b) * lists * K;
+  if (held)                               // (lists of beams that are not live are not used)
+    for (int i = tid; i < lists * K; i += kMergeThreads) s_cand[i] = cand[i];
+  for (int w = warp; w < W; w += kMergeWarps) {
     const int row = b * W + w;
     const float sc = p.score[row];
-    if (p.finished != nullptr && p.finished[row] != 0) {
-      s_kind[w] = 1;
-      s_off[w] = sc;
-    } else if (sc == -INFINITY) {
-      s_kind[w] = 2;
-      s_off[w] = -INFINITY;
-    } else {
+    const bool over = p.finished != nullptr && p.finished[row] != 0;
+    double off = sc;
+    if (!over && sc != -INFINITY) {
       const float2* st = p.stats + static_cast<size_t>(row) * p.chunks;
       float M = -INFINITY;
-      for (int c = 0; c < p.chunks; ++c) M = fmaxf(M, st[c].x);
+      for (int c = lane; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       double Z = 0.0;
       if (M != -INFINITY)
-        for (int c = 0; c < p.chunks; ++c) Z += static_cast<double>(st[c].y) * exp(static_cast<double>(st[c].x) - M);
-      s_kind[w] = 0;
-      s_off[w] = static_cast<double>(sc) - (M == -INFINITY ? 0.0 : static_cast<double>(M) + log(Z));
+        for (int c = lane; c < p.chunks; c += 32) Z += static_cast<double>(st[c].y) * exp(static_cast<double>(st[c].x) - M);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
+      if (M != -INFINITY) off -= static_cast<double>(M) + log(Z);
+    }
+    if (lane == 0) {
+      s_kind[w] = over ? 1 : (sc == -INFINITY ? 2 : 0);
+      s_off[w] = off;
     }
   }
   if (tid == 0) s_n = 0;
@@ -263,10 +325,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   // Entry j of a list.  Beams that are not live offer their pairs in the first chunk's list:
   // a finished one its end token at its own score, then tokens at -inf in rising order.
   auto entry = [&](int list, int j, Pair& e) -> bool {
-    const int w = list / p.chunks, c = list % p.chunks;
+    const int w = list / p.chunks, c = list - w * p.chunks;
     const uint32_t base = static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V);
     if (s_kind[w] == 0) {
-      const uint64_t r = p.cand[(static_cast<size_t>(b) * lists + list) * K + j];
+      const uint64_t r = held ? s_cand[list * K + j] : cand[static_cast<size_t>(list) * K + j];
       if (r == 0ull) return false;
       const float x = key_logit(static_cast<uint32_t>(r >> 32));
       e.key = score_key(x == -INFINITY ? -INFINITY : s_off[w] + static_cast<double>(x));
@@ -308,7 +370,6 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   }
   __syncthreads();
   const Pair bound = s_bound;
-  __syncthreads();
   for (int l = tid; l < lists; l += kMergeThreads)
     for (int j = 0; j < K; ++j) {
       Pair e;
@@ -408,22 +469,22 @@ __global__ void __launch_bounds__(kForkThreads)
 // ------------------------------------------------------------------------ host
 
 struct BeamPlan {
-  int nv;          // vectors a thread holds
-  int chunks, chunk_len;
+  int nv;                  // vectors a thread holds
+  int chunks, chunk_vecs;  // slices of a row, 16-byte vectors of a slice
 };
 
-// Sixteen vectors a thread hide the most latency per CTA; with few rows shorter slices
-// spread one row over more SMs.
-bool plan_beam(long long rows, int V, int dtype, int sms, BeamPlan* pl) {
+// Eight vectors a thread (16,384 bf16 logits a CTA) while that gives every SM a CTA; with
+// few rows, shorter slices spread a row over more SMs.  Slices of a row are equally long.
+// One vector more than the logits fill: a row may start inside one.
+void plan_beam(long long rows, int V, int dtype, int sms, BeamPlan* pl) {
   const int vn = dtype == JF_DTYPE_BF16 ? 8 : 4;
-  pl->nv = 8;
-  for (int nv = 8; nv >= 2; nv /= 2) {
+  const long long vecs = (static_cast<long long>(V) + vn - 1) / vn + 1;
+  for (int nv = 8; nv >= 1; nv /= 2) {
     pl->nv = nv;
-    pl->chunk_len = nv * kScanThreads * vn;
-    pl->chunks = static_cast<int>((static_cast<long long>(V) + pl->chunk_len - 1) / pl->chunk_len);
+    pl->chunks = static_cast<int>((vecs + nv * kScanThreads - 1) / (nv * kScanThreads));
+    pl->chunk_vecs = static_cast<int>((vecs + pl->chunks - 1) / pl->chunks);
     if (rows * pl->chunks >= sms) break;
   }
-  return true;
 }
 
 bool beam_sizes_ok(int32_t B, int32_t W, int32_t V, int32_t K) {
@@ -444,7 +505,8 @@ cudaError_t launch_scan(const BeamParams& p, int nv, unsigned grid, cudaStream_t
   switch (nv) {
     case 8: return launch_pdl(beam_scan_kernel<T, 8>, dim3(grid), dim3(kScanThreads), 0, s, p);
     case 4: return launch_pdl(beam_scan_kernel<T, 4>, dim3(grid), dim3(kScanThreads), 0, s, p);
-    default: return launch_pdl(beam_scan_kernel<T, 2>, dim3(grid), dim3(kScanThreads), 0, s, p);
+    case 2: return launch_pdl(beam_scan_kernel<T, 2>, dim3(grid), dim3(kScanThreads), 0, s, p);
+    default: return launch_pdl(beam_scan_kernel<T, 1>, dim3(grid), dim3(kScanThreads), 0, s, p);
   }
 }
 
@@ -458,8 +520,9 @@ extern "C" size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V,
       (dtype != JF_DTYPE_BF16 && dtype != JF_DTYPE_F32))
     return static_cast<size_t>(-1);
   const int sms = current_sm_count();
+  if (sms <= 0) return static_cast<size_t>(-1);
   BeamPlan pl;
-  if (sms <= 0 || !plan_beam(static_cast<long long>(B) * W, V, dtype, sms, &pl)) return static_cast<size_t>(-1);
+  plan_beam(static_cast<long long>(B) * W, V, dtype, sms, &pl);
   return beam_workspace(pl, static_cast<long long>(B) * W, K);
 }
 
@@ -501,10 +564,12 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   p.K = K;
   p.eos = eos_token;
   p.chunks = pl.chunks;
-  p.chunk_len = pl.chunk_len;
+  p.chunk_vecs = pl.chunk_vecs;
   const int lists = W * pl.chunks, first = std::min(K, (K + lists - 1) / lists);
   const size_t room = std::max(static_cast<size_t>(lists) * first, static_cast<size_t>(K) * K);
-  const size_t smem = sizeof(double) * (W + (W + 1) / 2) + room * (sizeof(uint64_t) + sizeof(uint32_t));
+  const size_t held = static_cast<long long>(lists) * K <= kMergeCand ? static_cast<size_t>(lists) * K : 0;
+  const size_t smem = sizeof(double) * (W + (W + 1) / 2) + held * sizeof(uint64_t) +
+                      room * (sizeof(uint64_t) + sizeof(uint32_t));
   if (smem > 200 * 1024) return JF_ERR_UNSUPPORTED;
   static SmemAttr attr;
   if (!attr.ensure(beam_merge_kernel, 200 * 1024)) return JF_ERR_CUDA;
