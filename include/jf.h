@@ -626,7 +626,7 @@ jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
  *              initialisation.
  * s is ranked in 64 bits, with logsumexp from per-slice fp32 sums of exponentials (relative
  * error about 1e-7): pairs of different beams closer than that may come in either order.
- * Limits: 1 <= K <= 64, 1 <= W <= 64, K <= W * V, W * V < 2^31, B * W < 2^20.
+ * Limits: 1 <= K <= 64, 1 <= W <= 64, K <= W * V <= 2^26, B * W < 2^20.
  */
 size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K, int32_t dtype);
 jf_status jf_beam_select(const void* logits, int32_t dtype, const float* score,

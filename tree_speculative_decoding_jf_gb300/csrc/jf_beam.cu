@@ -273,12 +273,36 @@ __device__ __forceinline__ double key_score(uint64_t k) {
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeCand = 4096;          // candidates held on chip when they fit
+constexpr int kSpare = 8;                 // lists over K that may pass the bound
 
-// One CTA per prompt.  A list is a slice's candidates in descending order.  The K-th best
-// of the lists' first `first` entries bounds the K-th best pair from below; since pairs
-// rank strictly, at most K lists reach the bound, so the survivors are at most K * K.
-// Bound by its chain of small steps: the statistics and all candidates are fetched
-// together, one warp a beam forms the log-sum-exp.
+__device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float x_lo) {
+  const float s = hi + x, t = s - hi;
+  lo += x_lo + ((hi - (s - t)) + (x - t));
+  hi = s;
+}
+
+// log(z), z >= 1, to about 1e-11: one Newton step y + (z e^-y - 1) from the fp32 logarithm,
+// with e^-y = 2^k e^r, |r| <= 0.35, and the Taylor series of e^r to the ninth power in
+// Estrin's order.  A dependent fp64 instruction takes some 100 cycles here, so the chain's
+// length (13) is what counts; the library's exp and log took 11,000 cycles together.
+__device__ __forceinline__ double log_fp64(double z) {
+  const float y = logf(static_cast<float>(z));
+  const float k = rintf(y * 1.44269504f);
+  const double r = fma(static_cast<double>(k), 0.69314718055994530942, -static_cast<double>(y));
+  const double r2 = r * r, r4 = r2 * r2;
+  const double a = fma(r, 1.0, 1.0), b = fma(r, 1.0 / 6, 1.0 / 2), c = fma(r, 1.0 / 120, 1.0 / 24),
+               d = fma(r, 1.0 / 5040, 1.0 / 720), e = fma(r, 1.0 / 362880, 1.0 / 40320);
+  const double lo = fma(r2, b, a), hi = fma(r2, d, c);
+  const double er = fma(r4, fma(r4, e, hi), lo);
+  const double back = z * __hiloint2double((1023 - static_cast<int>(k)) << 20, 0);   // z 2^-k
+  return static_cast<double>(y) + fma(back, er, -1.0);
+}
+
+// One CTA per prompt.  A list is a slice's candidates in descending order.  The lists' first
+// `first` entries (their heads) bound the K-th best pair from below: a value that at least K
+// heads reach, found on the upper 32 bits of their keys, passes few lists, and only those
+// are looked at further.  The call is a chain of small dependent steps; each is spread over
+// a warp's lanes.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   extern __shared__ uint64_t s_dyn[];
   __shared__ int s_n;
@@ -288,12 +312,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   const int W = p.W, K = p.K, lists = W * p.chunks;
   const int first = min(K, (K + lists - 1) / lists), heads = lists * first;
   const bool held = static_cast<long long>(lists) * K <= kMergeCand;
+  const int room = (K + kSpare) * K;
   double* s_off = reinterpret_cast<double*>(s_dyn);                // [W]: score - lse
   int* s_kind = reinterpret_cast<int*>(s_off + W);                 // [W]: 0 live, 1 finished, 2 dead
   uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_off + W + (W + 1) / 2);
-  uint64_t* s_key = s_cand + (held ? lists * K : 0);
-  const int room = max(heads, K * K);
-  uint32_t* s_flat = reinterpret_cast<uint32_t*>(s_key + room);
+  uint64_t* s_head = s_cand + (held ? lists * K : 0);              // [heads]
+  uint64_t* s_key = s_head + heads;                                // [room]: survivors
+  uint32_t* s_hflat = reinterpret_cast<uint32_t*>(s_key + room);   // [heads]
+  uint32_t* s_flat = s_hflat + heads;                              // [room]
   const uint64_t* cand = p.cand + static_cast<size_t>(b) * lists * K;
   if (held)                               // (lists of beams that are not live are not used)
     for (int i = tid; i < lists * K; i += kMergeThreads) s_cand[i] = cand[i];
@@ -308,12 +334,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       for (int c = lane; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      double Z = 0.0;
-      if (M != -INFINITY)
-        for (int c = lane; c < p.chunks; c += 32) Z += static_cast<double>(st[c].y) * exp(static_cast<double>(st[c].x) - M);
+      if (M != -INFINITY) {
+        float hi = 0.f, lo = 0.f;
+        for (int c = lane; c < p.chunks; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
-      if (M != -INFINITY) off -= static_cast<double>(M) + log(Z);
+        for (int o = 16; o; o >>= 1) {
+          const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
+          two_sum(hi, lo, x, y);
+        }
+        off -= static_cast<double>(M) + log_fp64(static_cast<double>(hi) + lo);
+      }
     }
     if (lane == 0) {
       s_kind[w] = over ? 1 : (sc == -INFINITY ? 2 : 0);
@@ -353,42 +383,86 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     e.flat = base + static_cast<uint32_t>(j);
     return true;
   };
+  // s_head is 0 where a list has no such entry: no pair's key is 0 (that of NaN).
   for (int i = tid; i < heads; i += kMergeThreads) {
     Pair e;
     const bool ok = entry(i / first, i % first, e);
-    s_key[i] = ok ? e.key : 0ull;
-    s_flat[i] = ok ? e.flat : 0xffffffffu;
-  }
-  if (tid == 0) s_bound = Pair{0ull, 0xffffffffu};      // fewer than K heads: everything passes
-  __syncthreads();
-  for (int i = tid; i < heads; i += kMergeThreads) {
-    const Pair mine{s_key[i], s_flat[i]};
-    if (mine.flat == 0xffffffffu) continue;
-    int r = 0;
-    for (int j = 0; j < heads; ++j) r += before(Pair{s_key[j], s_flat[j]}, mine);
-    if (r == K - 1) s_bound = mine;
+    s_head[i] = ok ? (e.key == 0ull ? 1ull : e.key) : 0ull;
+    s_hflat[i] = ok ? e.flat : 0xffffffffu;
   }
   __syncthreads();
-  const Pair bound = s_bound;
-  for (int l = tid; l < lists; l += kMergeThreads)
-    for (int j = 0; j < K; ++j) {
-      Pair e;
-      if (!entry(l, j, e) || before(bound, e)) break;
-      const int n = atomicAdd(&s_n, 1);
-      if (n < room) {
-        s_key[n] = e.key;
-        s_flat[n] = e.flat;
+  // Every warp for itself: a value of the keys' upper words that K heads reach, bit by bit
+  // from the first bit in which they differ, good enough once at most kSpare more reach it.
+  const uint32_t* head_hi = reinterpret_cast<const uint32_t*>(s_head) + 1;
+  uint32_t top = 0u, low = 0xffffffffu;
+  int valid = 0;
+  for (int i = lane; i < heads; i += 32) {
+    if (s_head[i] == 0ull) continue;
+    const uint32_t h = head_hi[2 * i];
+    top = max(top, h);
+    low = min(low, h);
+    ++valid;
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  low = __reduce_min_sync(0xffffffffu, low);
+  valid = __reduce_add_sync(0xffffffffu, valid);
+  uint32_t thr = 0u;                      // fewer than K heads: everything passes
+  bool exact = false;                     // the bound is s_bound, not thr
+  if (valid >= K) {
+    int reach = valid;
+    const int bits = 32 - __clz(top ^ low);
+    thr = bits == 32 ? 0u : (top >> bits) << bits;
+    for (int bit = bits - 1; bit >= 0 && reach > K + kSpare; --bit) {
+      const uint32_t at = thr | (1u << bit);
+      int n = 0;
+      for (int i = lane; i < heads; i += 32) n += s_head[i] != 0ull && head_hi[2 * i] >= at;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n >= K) {
+        thr = at;
+        reach = n;
       }
     }
+    exact = reach > K + kSpare;
+  }
+  if (exact) {                            // many equal heads: the K-th itself
+    for (int i = warp; i < heads; i += kMergeWarps) {
+      const Pair mine{s_head[i], s_hflat[i]};
+      int r = 0;
+      for (int j = lane; j < heads; j += 32) r += before(Pair{s_head[j], s_hflat[j]}, mine);
+      r = __reduce_add_sync(0xffffffffu, r);
+      if (r == K - 1 && mine.key != 0ull && lane == 0) s_bound = mine;
+    }
+    __syncthreads();                      // (uniform: every warp found the same)
+  }
+  const Pair bound = exact ? s_bound : Pair{static_cast<uint64_t>(thr) << 32, 0xffffffffu};
+  for (int l = warp; l < lists; l += kMergeWarps) {
+    const uint64_t h = s_head[l * first];
+    if (h == 0ull || before(bound, Pair{h, s_hflat[l * first]})) continue;
+    for (int j0 = 0; j0 < K; j0 += 32) {
+      Pair e;
+      const int j = j0 + lane;
+      const bool in = j < K && entry(l, j, e) && !before(bound, Pair{e.key == 0ull ? 1ull : e.key, e.flat});
+      const uint32_t ms = __ballot_sync(0xffffffffu, in);
+      int at = 0;
+      if (lane == 0 && ms != 0u) at = atomicAdd(&s_n, __popc(ms));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(ms & ((1u << lane) - 1u));
+      if (in && at < room) {
+        s_key[at] = e.key;
+        s_flat[at] = e.flat;
+      }
+      if (ms != 0xffffffffu) break;       // a list descends
+    }
+  }
   __syncthreads();
   const int n = min(s_n, room);
-  for (int i = tid; i < n; i += kMergeThreads) {
+  for (int i = warp; i < n; i += kMergeWarps) {
     const Pair mine{s_key[i], s_flat[i]};
     int r = 0;
-    for (int j = 0; j < n; ++j) r += before(Pair{s_key[j], s_flat[j]}, mine);
-    if (r >= K) continue;
+    for (int j = lane; j < n; j += 32) r += before(Pair{s_key[j], s_flat[j]}, mine);
+    r = __reduce_add_sync(0xffffffffu, r);
+    if (r >= K || lane != 0) continue;
     const int w = static_cast<int>(mine.flat / static_cast<uint32_t>(p.V));
-    const int v = static_cast<int>(mine.flat % static_cast<uint32_t>(p.V));
+    const int v = static_cast<int>(mine.flat - static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V));
     const size_t o = static_cast<size_t>(b) * K + r;
     p.parent[o] = w;
     p.token[o] = v;
@@ -491,7 +565,7 @@ bool beam_sizes_ok(int32_t B, int32_t W, int32_t V, int32_t K) {
   return B >= 1 && W >= 1 && V >= 1 && K >= 1;
 }
 bool beam_supported(int32_t B, int32_t W, int32_t V, int32_t K) {
-  return K <= kMaxK && W <= kMaxK && static_cast<long long>(W) * V < (1ll << 31) &&
+  return K <= kMaxK && W <= kMaxK && static_cast<long long>(W) * V <= (1ll << 26) &&
          static_cast<long long>(K) <= static_cast<long long>(W) * V &&
          static_cast<long long>(B) * W < (1ll << 20);
 }
@@ -566,11 +640,10 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   p.chunks = pl.chunks;
   p.chunk_vecs = pl.chunk_vecs;
   const int lists = W * pl.chunks, first = std::min(K, (K + lists - 1) / lists);
-  const size_t room = std::max(static_cast<size_t>(lists) * first, static_cast<size_t>(K) * K);
+  const size_t room = static_cast<size_t>(lists) * first + static_cast<size_t>(K + kSpare) * K;
   const size_t held = static_cast<long long>(lists) * K <= kMergeCand ? static_cast<size_t>(lists) * K : 0;
   const size_t smem = sizeof(double) * (W + (W + 1) / 2) + held * sizeof(uint64_t) +
                       room * (sizeof(uint64_t) + sizeof(uint32_t));
-  if (smem > 200 * 1024) return JF_ERR_UNSUPPORTED;
   static SmemAttr attr;
   if (!attr.ensure(beam_merge_kernel, 200 * 1024)) return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
