@@ -88,6 +88,17 @@ struct BeamParams {
   int W, V, K, eos, chunks, chunk_vecs;
 };
 
+// A vector that reaches over an end of its row: the logits inside, -inf for the others.
+template <typename T>
+__device__ __noinline__ uint4 row_end(const T* x, int at, int V) {
+  using R = Row<T>;
+  uint4 r = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+#pragma unroll
+  for (int c = 0; c < R::kN; ++c)
+    if (at + c >= 0 && at + c < V) R::put(r, c, x[at + c]);
+  return r;
+}
+
 template <typename T, int NV>
 __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamParams p) {
   using R = Row<T>;
@@ -112,22 +123,15 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   const int vec0 = chunk * p.chunk_vecs;
   auto first_of = [&](int i) { return (vec0 + i * kScanThreads + tid) * VN - off; };
+  auto load = [&](int i) -> uint4 {
+    const int at = first_of(i);
+    if (i * kScanThreads + tid >= p.chunk_vecs) return make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+    if (at >= 0 && at + VN <= p.V) return __ldg(reinterpret_cast<const uint4*>(x + at));
+    return row_end(x, at, p.V);
+  };
   uint4 v[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = first_of(i);
-    const bool mine = i * kScanThreads + tid < p.chunk_vecs;
-    if (mine && at >= 0 && at + VN <= p.V) {
-      v[i] = __ldg(reinterpret_cast<const uint4*>(x + at));
-    } else {
-      v[i] = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
-      if (mine) {
-#pragma unroll
-        for (int c = 0; c < VN; ++c)
-          if (at + c >= 0 && at + c < p.V) R::put(v[i], c, x[at + c]);
-      }
-    }
-  }
+  for (int i = 0; i < NV; ++i) v[i] = load(i);
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) m = fmaxf(m, R::vmax(v[i]));
@@ -183,14 +187,17 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
+  // The few threads that reach the bound read their vectors again (from L2): unrolled over
+  // the registers this code was most of the kernel's, and fetching it held up every warp.
   if (best >= thr) {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NV; ++i) {
-      if (logit_key(R::vmax(v[i])) < thr) continue;
+      const uint4 w = load(i);
+      if (logit_key(R::vmax(w)) < thr) continue;
 #pragma unroll
       for (int c = 0; c < VN; ++c) {
         const int at = first_of(i) + c;
-        const uint32_t key = logit_key(R::get(v[i], c));
+        const uint32_t key = logit_key(R::get(w, c));
         if (key < thr || at < 0 || at >= p.V) continue;
         const int n = atomicAdd(&s_n, 1);
         if (n < kCandCap) s_cand[n] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
@@ -305,7 +312,8 @@ __device__ __forceinline__ double log_fp64(double z) {
 // a warp's lanes.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   extern __shared__ uint64_t s_dyn[];
-  __shared__ int s_n;
+  __shared__ int s_n, s_reach;
+  __shared__ uint32_t s_thr;
   __shared__ Pair s_bound;
   grid_dependency_wait();
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -318,25 +326,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_off + W + (W + 1) / 2);
   uint64_t* s_head = s_cand + (held ? lists * K : 0);              // [heads]
   uint64_t* s_key = s_head + heads;                                // [room]: survivors
-  uint32_t* s_hflat = reinterpret_cast<uint32_t*>(s_key + room);   // [heads]
+  // Upper words of the keys, padded with 0 to whole 16-byte vectors.
+  uint32_t* s_hhi = reinterpret_cast<uint32_t*>((reinterpret_cast<uintptr_t>(s_key + room) + 15) & ~static_cast<uintptr_t>(15));
+  uint32_t* s_hi = s_hhi + (heads + 3) / 4 * 4;
+  uint32_t* s_hflat = s_hi + (room + 3) / 4 * 4;                   // [heads]
   uint32_t* s_flat = s_hflat + heads;                              // [room]
   const uint64_t* cand = p.cand + static_cast<size_t>(b) * lists * K;
   if (held)                               // (lists of beams that are not live are not used)
-    for (int i = tid; i < lists * K; i += kMergeThreads) s_cand[i] = cand[i];
+    for (int i = tid; i < lists * K; i += kMergeThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(s_cand + i)), "l"(cand + i) : "memory");
   for (int w = warp; w < W; w += kMergeWarps) {
     const int row = b * W + w;
+    // (asked for together; those of a beam that is not live are not used)
+    const float2* st = p.stats + static_cast<size_t>(row) * p.chunks;
+    const float2 mine = lane < p.chunks ? st[lane] : make_float2(-INFINITY, 0.f);
     const float sc = p.score[row];
     const bool over = p.finished != nullptr && p.finished[row] != 0;
     double off = sc;
     if (!over && sc != -INFINITY) {
-      const float2* st = p.stats + static_cast<size_t>(row) * p.chunks;
-      float M = -INFINITY;
-      for (int c = lane; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
+      float M = mine.x;
+      for (int c = lane + 32; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       if (M != -INFINITY) {
-        float hi = 0.f, lo = 0.f;
-        for (int c = lane; c < p.chunks; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
+        float hi = mine.y * expf(mine.x - M), lo = 0.f;
+        for (int c = lane + 32; c < p.chunks; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
@@ -350,7 +364,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       s_off[w] = off;
     }
   }
-  if (tid == 0) s_n = 0;
+  if (tid == 0) {
+    s_n = 0;
+    s_thr = 0xffffffffu;
+    s_reach = 0;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   // Entry j of a list.  Beams that are not live offer their pairs in the first chunk's list:
   // a finished one its end token at its own score, then tokens at -inf in rising order.
@@ -384,46 +403,40 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     return true;
   };
   // s_head is 0 where a list has no such entry: no pair's key is 0 (that of NaN).
-  for (int i = tid; i < heads; i += kMergeThreads) {
+  for (int i = tid; i < (heads + 3) / 4 * 4; i += kMergeThreads) {
     Pair e;
-    const bool ok = entry(i / first, i % first, e);
-    s_head[i] = ok ? (e.key == 0ull ? 1ull : e.key) : 0ull;
-    s_hflat[i] = ok ? e.flat : 0xffffffffu;
+    const bool ok = i < heads && entry(i / first, i % first, e);
+    const uint64_t k = ok ? (e.key == 0ull ? 1ull : e.key) : 0ull;
+    s_hhi[i] = static_cast<uint32_t>(k >> 32);
+    if (i < heads) {
+      s_head[i] = k;
+      s_hflat[i] = ok ? e.flat : 0xffffffffu;
+    }
   }
   __syncthreads();
-  // Every warp for itself: a value of the keys' upper words that K heads reach, bit by bit
-  // from the first bit in which they differ, good enough once at most kSpare more reach it.
-  const uint32_t* head_hi = reinterpret_cast<const uint32_t*>(s_head) + 1;
-  uint32_t top = 0u, low = 0xffffffffu;
-  int valid = 0;
-  for (int i = lane; i < heads; i += 32) {
-    if (s_head[i] == 0ull) continue;
-    const uint32_t h = head_hi[2 * i];
-    top = max(top, h);
-    low = min(low, h);
-    ++valid;
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  low = __reduce_min_sync(0xffffffffu, low);
-  valid = __reduce_add_sync(0xffffffffu, valid);
-  uint32_t thr = 0u;                      // fewer than K heads: everything passes
-  bool exact = false;                     // the bound is s_bound, not thr
-  if (valid >= K) {
-    int reach = valid;
-    const int bits = 32 - __clz(top ^ low);
-    thr = bits == 32 ? 0u : (top >> bits) << bits;
-    for (int bit = bits - 1; bit >= 0 && reach > K + kSpare; --bit) {
-      const uint32_t at = thr | (1u << bit);
-      int n = 0;
-      for (int i = lane; i < heads; i += 32) n += s_head[i] != 0ull && head_hi[2 * i] >= at;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (n >= K) {
-        thr = at;
-        reach = n;
-      }
+  // Upper words of the array above x, and equal to it.
+  auto count = [&](const uint32_t* hi, int n, uint32_t x, int& above, int& equal) {
+    above = equal = 0;
+#pragma unroll 4
+    for (int j = 0; j < (n + 3) / 4; ++j) {
+      const uint4 h = reinterpret_cast<const uint4*>(hi)[j];
+      above += (h.x > x) + (h.y > x) + (h.z > x) + (h.w > x);
+      equal += (h.x == x) + (h.y == x) + (h.z == x) + (h.w == x);
     }
-    exact = reach > K + kSpare;
+  };
+  // The K-th greatest upper word of the heads; 0 with fewer than K of them: all pass.
+  for (int i = tid; i < heads; i += kMergeThreads) {
+    if (s_head[i] == 0ull) continue;
+    int above, equal;
+    count(s_hhi, heads, s_hhi[i], above, equal);
+    if (above < K && above + equal >= K) {
+      s_thr = s_hhi[i];                   // (the same value from each that writes)
+      s_reach = above + equal;
+    }
   }
+  __syncthreads();
+  const uint32_t thr = s_reach == 0 ? 0u : s_thr;
+  const bool exact = s_reach > K + kSpare;   // the bound is s_bound, not thr
   if (exact) {                            // many equal heads: the K-th itself
     for (int i = warp; i < heads; i += kMergeWarps) {
       const Pair mine{s_head[i], s_hflat[i]};
@@ -432,7 +445,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       r = __reduce_add_sync(0xffffffffu, r);
       if (r == K - 1 && mine.key != 0ull && lane == 0) s_bound = mine;
     }
-    __syncthreads();                      // (uniform: every warp found the same)
+    __syncthreads();
   }
   const Pair bound = exact ? s_bound : Pair{static_cast<uint64_t>(thr) << 32, 0xffffffffu};
   for (int l = warp; l < lists; l += kMergeWarps) {
@@ -449,18 +462,26 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       if (in && at < room) {
         s_key[at] = e.key;
         s_flat[at] = e.flat;
+        s_hi[at] = static_cast<uint32_t>(e.key >> 32);
       }
       if (ms != 0xffffffffu) break;       // a list descends
     }
   }
   __syncthreads();
   const int n = min(s_n, room);
-  for (int i = warp; i < n; i += kMergeWarps) {
+  for (int i = tid; i < n; i += kMergeThreads) {
+    int r, equal;
+    const uint32_t hi = s_hi[i];
+    count(s_hi, n / 4 * 4, hi, r, equal);
+    for (int j = n / 4 * 4; j < n; ++j) {
+      r += s_hi[j] > hi;
+      equal += s_hi[j] == hi;
+    }
+    if (r >= K) continue;
     const Pair mine{s_key[i], s_flat[i]};
-    int r = 0;
-    for (int j = lane; j < n; j += 32) r += before(Pair{s_key[j], s_flat[j]}, mine);
-    r = __reduce_add_sync(0xffffffffu, r);
-    if (r >= K || lane != 0) continue;
+    if (equal > 1)
+      for (int j = 0; j < n; ++j) r += s_hi[j] == hi && before(Pair{s_key[j], s_flat[j]}, mine);
+    if (r >= K) continue;
     const int w = static_cast<int>(mine.flat / static_cast<uint32_t>(p.V));
     const int v = static_cast<int>(mine.flat - static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V));
     const size_t o = static_cast<size_t>(b) * K + r;
@@ -643,9 +664,9 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   const size_t room = static_cast<size_t>(lists) * first + static_cast<size_t>(K + kSpare) * K;
   const size_t held = static_cast<long long>(lists) * K <= kMergeCand ? static_cast<size_t>(lists) * K : 0;
   const size_t smem = sizeof(double) * (W + (W + 1) / 2) + held * sizeof(uint64_t) +
-                      room * (sizeof(uint64_t) + sizeof(uint32_t));
+                      room * (sizeof(uint64_t) + 2 * sizeof(uint32_t)) + 64;
   static SmemAttr attr;
-  if (!attr.ensure(beam_merge_kernel, 200 * 1024)) return JF_ERR_CUDA;
+  if (!attr.ensure(beam_merge_kernel, 220 * 1024)) return JF_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(rows * pl.chunks);
   cudaError_t e = dtype == JF_DTYPE_BF16 ? launch_scan<uint16_t>(p, pl.nv, grid, s)
