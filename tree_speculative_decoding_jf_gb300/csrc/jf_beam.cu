@@ -10,19 +10,23 @@ namespace jf {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kMaxK = 64;
+constexpr int kMaxK = 64;                 // most beams, and most continuations
+constexpr float kLog2e = 1.4426950408889634f;
 
-// ------------------------------------------------------------------------ candidates
+// ------------------------------------------------------------------------ scan
 //
-// Within a beam the pairs rank as the logits do, so a slice of a row contributes at most
-// its K greatest logits.  A thread's 16-byte vectors stay packed in registers: the slice's
-// maximum, its sum of exponentials and its candidates come from one read of the logits,
-// which is all that bounds the call (bytes / HBM bandwidth).  The K-th greatest of 32 (or,
-// for K > 16, 256) groups' maxima is a value that K logits of the slice reach, so only
-// vectors that reach it are looked at logit by logit.
-constexpr int kScanThreads = 256;
+// The K best pairs of a prompt lie in few places.  The scan streams the logits once and
+// keeps, for every block of some 1024 logits, only the greatest, beside the slice's maximum
+// and sum of exponentials for the log-sum-exp.  The K-th best of the blocks' best pairs
+// bounds the K-th best pair from below, so the merge reads again only the blocks that reach
+// it: about K of them.  The scan has no barrier, no shared memory and no candidates; HBM
+// bounds it.  (Collecting candidates while streaming cost a threshold, a compaction and a
+// ranking per slice: 36 us with a CTA a slice, 50 us with a warp a slice, on 256 rows of
+// 151,936 bf16 logits, whose bytes take 11.7 us.)
+constexpr int kScanThreads = 128;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kCandCap = 512;
+constexpr int kStep = 4;                       // 16-byte vectors a lane holds at a time
+constexpr int kStepVecs = 32 * kStep;          // vectors of a warp's step
 constexpr uint32_t kNegInfKey = 0x007fffffu;   // logit_key(-inf)
 
 // Orders as the value does; NaN lowest, -0 == +0.
@@ -83,9 +87,26 @@ struct BeamParams {
   int32_t* token;
   float* new_score;
   int32_t* new_finished;
-  float2* stats;          // [rows][chunks]: maximum, sum of exp(x - maximum)
-  uint64_t* cand;         // [rows][chunks][K]: logit key << 32 | ~token, descending; 0 = none
-  int W, V, K, eos, chunks, chunk_vecs;
+  float2* stats;          // [rows][slices]: maximum, sum of exp(x - maximum)
+  uint32_t* best;         // [rows][blocks]: key of a block's greatest logit
+  int W, V, K, eos;
+  int slices, slice_blocks;   // slices of a row (a warp each), blocks of a slice
+  int blocks, block_vecs;     // blocks of a row, 16-byte vectors of a block
+  int total;                  // rows * slices
+};
+
+// A row as 16-byte vectors, the first of which starts at the boundary at or below the row's
+// first logit: logit e of the row is element e + off of the vectors.  Vectors that reach
+// over either end of the row are read logit by logit.
+template <typename T>
+struct RowVecs {
+  const T* x;
+  int off, V;
+  __device__ RowVecs(const void* logits, int row, int V_) : x(static_cast<const T*>(logits) + static_cast<size_t>(row) * V_), V(V_) {
+    off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  }
+  __device__ __forceinline__ int first(int vec) const { return vec * Row<T>::kN - off; }
+  __device__ __forceinline__ uint4 load(int vec) const;
 };
 
 // A vector that reaches over an end of its row: the logits inside, -inf for the others.
@@ -99,166 +120,85 @@ __device__ __noinline__ uint4 row_end(const T* x, int at, int V) {
   return r;
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamParams p) {
+template <typename T>
+__device__ __forceinline__ uint4 RowVecs<T>::load(int vec) const {
+  const int at = first(vec);
+  if (at >= 0 && at + Row<T>::kN <= V) return __ldg(reinterpret_cast<const uint4*>(x + at));
+  return row_end(x, at, V);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const BeamParams p) {
   using R = Row<T>;
   constexpr int VN = R::kN;
-  __shared__ uint32_t s_max[kScanThreads];
-  __shared__ float s_sum[kScanWarps];
-  __shared__ int s_n;
-  __shared__ uint64_t s_cand[kCandCap];
-  __shared__ uint64_t s_best[kScanWarps];
   grid_dependency_wait();
-  const int chunk = blockIdx.x % p.chunks, row = blockIdx.x / p.chunks;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
-  uint64_t* out = p.cand + (static_cast<size_t>(row) * p.chunks + chunk) * K;
-  if ((p.finished != nullptr && p.finished[row] != 0) || p.score[row] == -INFINITY) {
+  const int lane = threadIdx.x & 31, slice = blockIdx.x * kScanWarps + (threadIdx.x >> 5);
+  const int row = slice / p.slices, part = slice - row * p.slices;
+  // (the merge makes the pairs of beams that are not live itself)
+  if (slice >= p.total || (p.finished != nullptr && p.finished[row] != 0) || p.score[row] == -INFINITY) {
     grid_dependents_launch();
-    return;                               // the merge makes this beam's pairs itself
+    return;
   }
-  // Vectors start at the 16-byte boundary at or below the row's first logit: logit e of the
-  // row is element e + off of the vectors.  Vectors that reach over either end of the row
-  // are read logit by logit.
-  const T* x = static_cast<const T*>(p.logits) + static_cast<size_t>(row) * p.V;
-  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-  const int vec0 = chunk * p.chunk_vecs;
-  auto first_of = [&](int i) { return (vec0 + i * kScanThreads + tid) * VN - off; };
-  auto load = [&](int i) -> uint4 {
-    const int at = first_of(i);
-    if (i * kScanThreads + tid >= p.chunk_vecs) return make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
-    if (at >= 0 && at + VN <= p.V) return __ldg(reinterpret_cast<const uint4*>(x + at));
-    return row_end(x, at, p.V);
-  };
-  uint4 v[NV];
+  const RowVecs<T> r(p.logits, row, p.V);
+  const int b0 = part * p.slice_blocks, b1 = min(p.blocks, b0 + p.slice_blocks);
+  const int vec0 = b0 * p.block_vecs + lane, steps = (b1 - b0) * (p.block_vecs / kStepVecs);
+  const int block_steps = p.block_vecs / kStepVecs;
+  uint32_t* best = p.best + static_cast<size_t>(row) * p.blocks + b0;
+  float m = -INFINITY, sum = 0.f;         // of this lane
+  uint32_t greatest = 0u;                 // of this lane, in the block
+  uint4 next[kStep];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = load(i);
-  float m = -INFINITY;
+  for (int u = 0; u < kStep; ++u) next[u] = r.load(vec0 + u * 32);
+#pragma unroll 1
+  for (int i = 0, left = block_steps; i < steps; ++i) {
+    uint4 v[kStep];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) m = fmaxf(m, R::vmax(v[i]));
-  const uint32_t best = logit_key(m);
-  s_max[tid] = best;
-  if (tid == 0) s_n = 0;
-  __syncthreads();
-  // Every warp: the slice's maximum and the K-th greatest group maximum to 16 bits (a lower
-  // bound), bit by bit.
-  uint32_t mx[kScanWarps], gmax = 0u;
+    for (int u = 0; u < kStep; ++u) v[u] = next[u];
+    if (i + 1 < steps) {
 #pragma unroll
-  for (int i = 0; i < kScanWarps; ++i) {
-    mx[i] = s_max[i * 32 + lane];
-    gmax = max(gmax, mx[i]);
+      for (int u = 0; u < kStep; ++u) next[u] = r.load(vec0 + (i + 1) * kStepVecs + u * 32);
+    }
+    const float mine = fmaxf(fmaxf(R::vmax(v[0]), R::vmax(v[1])), fmaxf(R::vmax(v[2]), R::vmax(v[3])));
+    greatest = max(greatest, logit_key(mine));
+    if (--left == 0) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, greatest);
+      if (lane == 0) *best = top;
+      ++best;
+      greatest = 0u;
+      left = block_steps;
+    }
+    const float up = fmaxf(m, mine), ref = up == -INFINITY ? 0.f : up;
+    if (up > m) sum *= fast_exp2((m - ref) * kLog2e);
+    m = up;
+    const uint64_t neg = f2(-ref, -ref), l2e = f2(kLog2e, kLog2e);
+    uint64_t acc = 0ull, acc1 = 0ull;
+#pragma unroll
+    for (int u = 0; u < kStep; ++u)
+#pragma unroll
+      for (int c = 0; c < VN; c += 4) {
+        float a, b, d, e;
+        f2_split(fmul2(fadd2(f2(R::get(v[u], c), R::get(v[u], c + 1)), neg), l2e), a, b);
+        f2_split(fmul2(fadd2(f2(R::get(v[u], c + 2), R::get(v[u], c + 3)), neg), l2e), d, e);
+        acc = fadd2(acc, f2(fast_exp2(a), fast_exp2(b)));
+        acc1 = fadd2(acc1, f2(fast_exp2(d), fast_exp2(e)));
+      }
+    float a, b;
+    f2_split(fadd2(acc, acc1), a, b);
+    sum += a + b;
   }
-  const uint32_t top = __reduce_max_sync(0xffffffffu, gmax);
-  uint32_t thr = 0u;
-  if (K <= 16) {
+  float M = m;
 #pragma unroll
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t at = thr | (1u << bit);
-      if (__popc(__ballot_sync(0xffffffffu, gmax >= at)) >= K) thr = at;
-    }
-  } else {
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t at = thr | (1u << bit);
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < kScanWarps; ++i) n += mx[i] >= at;
-      if (__reduce_add_sync(0xffffffffu, n) >= K) thr = at;
-    }
-  }
-  // A bound of -inf (a slice with few allowed tokens): collect what lies above it, the rest
-  // of the list is the first tokens at -inf.
-  const bool sparse = thr <= kNegInfKey;
-  if (sparse) thr = kNegInfKey + 1u;
-  const float M = key_logit(top), ref = M == -INFINITY ? 0.f : M;
-  const uint64_t neg = f2(-ref, -ref), l2e = f2(1.4426950408889634f, 1.4426950408889634f);
-  uint64_t acc = 0ull, acc1 = 0ull;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int c = 0; c < VN; c += 4) {
-      float a, b, d, e;
-      f2_split(fmul2(fadd2(f2(R::get(v[i], c), R::get(v[i], c + 1)), neg), l2e), a, b);
-      f2_split(fmul2(fadd2(f2(R::get(v[i], c + 2), R::get(v[i], c + 3)), neg), l2e), d, e);
-      acc = fadd2(acc, f2(fast_exp2(a), fast_exp2(b)));
-      acc1 = fadd2(acc1, f2(fast_exp2(d), fast_exp2(e)));
-    }
-  float a, b;
-  f2_split(fadd2(acc, acc1), a, b);
-  float sum = a + b;
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  sum *= m == -INFINITY ? 0.f : fast_exp2((m - M) * kLog2e);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  // The few threads that reach the bound read their vectors again (from L2): unrolled over
-  // the registers this code was most of the kernel's, and fetching it held up every warp.
-  if (best >= thr) {
-#pragma unroll 1
-    for (int i = 0; i < NV; ++i) {
-      const uint4 w = load(i);
-      if (logit_key(R::vmax(w)) < thr) continue;
-#pragma unroll
-      for (int c = 0; c < VN; ++c) {
-        const int at = first_of(i) + c;
-        const uint32_t key = logit_key(R::get(w, c));
-        if (key < thr || at < 0 || at >= p.V) continue;
-        const int n = atomicAdd(&s_n, 1);
-        if (n < kCandCap) s_cand[n] = (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(at));
-      }
-    }
-  }
-  __syncthreads();
-  const int n = s_n;
-  if (tid == 0) {
-    float t = 0.f;
-    for (int i = 0; i < kScanWarps; ++i) t += s_sum[i];
-    p.stats[static_cast<size_t>(row) * p.chunks + chunk] = make_float2(M, t);
-  }
-  if (n <= kCandCap) {
-    for (int i = tid; i < n; i += kScanThreads) {
-      const uint64_t mine = s_cand[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += s_cand[j] > mine;
-      if (r < K) out[r] = mine;
-    }
-    if (n < K) {                          // sparse, or a slice shorter than K
-      const int lo = max(0, vec0 * VN - off), hi = min(p.V, (vec0 + p.chunk_vecs) * VN - off);
-      if (warp == 0) {
-        int at = n;
-        for (int t0 = lo; t0 < hi && at < K && sparse; t0 += 32) {
-          const int t = t0 + lane;
-          const bool none = t < hi && to_float(x[t]) == -INFINITY;
-          const uint32_t ms = __ballot_sync(0xffffffffu, none);
-          const int r = at + __popc(ms & ((1u << lane) - 1u));
-          if (none && r < K)
-            out[r] = (static_cast<uint64_t>(kNegInfKey) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
-          at += __popc(ms);
-        }
-        for (int r = min(at, K) + lane; r < K; r += 32) out[r] = 0ull;
-      }
-    }
-  } else {                                // many equal logits: K rounds over the whole slice
-    const int lo = max(0, vec0 * VN - off), hi = min(p.V, (vec0 + p.chunk_vecs) * VN - off);
-    uint64_t last = ~0ull;
-    for (int r = 0; r < K; ++r) {
-      uint64_t most = 0ull;
-      for (int t = lo + tid; t < hi; t += kScanThreads) {
-        const uint64_t e = (static_cast<uint64_t>(logit_key(to_float(x[t]))) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
-        if (e < last && e > most) most = e;
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-      if (lane == 0) s_best[warp] = most;
-      __syncthreads();
-      for (int i = 0; i < kScanWarps; ++i) most = max(most, s_best[i]);
-      if (tid == 0) out[r] = most;
-      last = most;
-      __syncthreads();
-    }
-  }
+  if (lane == 0) p.stats[slice] = make_float2(M, sum);
   grid_dependents_launch();
 }
 
 // ------------------------------------------------------------------------ merge
 
-// A pair's rank: score (as ordered 64 bits), then the lower flat index.
+// A pair's rank: score (as ordered 64 bits), then the lower flat index w * V + v.
 struct Pair {
   uint64_t key;
   uint32_t flat;
@@ -279,8 +219,9 @@ __device__ __forceinline__ double key_score(uint64_t k) {
 
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeCand = 4096;          // candidates held on chip when they fit
-constexpr int kSpare = 8;                 // lists over K that may pass the bound
+constexpr int kMergeBlocks = 8192;        // blocks of a prompt: 8 bytes of shared memory each
+constexpr int kBins = 1024;
+constexpr int kListCap = kMaxK + 32;      // pairs a warp collects before it cuts back to K
 
 __device__ __forceinline__ void two_sum(float& hi, float& lo, float x, float x_lo) {
   const float s = hi + x, t = s - hi;
@@ -305,52 +246,79 @@ __device__ __forceinline__ double log_fp64(double z) {
   return static_cast<double>(y) + fma(back, er, -1.0);
 }
 
-// One CTA per prompt.  A list is a slice's candidates in descending order.  The lists' first
-// `first` entries (their heads) bound the K-th best pair from below: a value that at least K
-// heads reach, found on the upper 32 bits of their keys, passes few lists, and only those
-// are looked at further.  The call is a chain of small dependent steps; each is spread over
-// a warp's lanes.
+// Sorts a warp's n <= kListCap pairs and keeps the first K; returns their number.
+__device__ __noinline__ int cut_back(uint64_t* key, uint32_t* flat, int n, int K) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kMine = kListCap / 32;
+  Pair e[kMine];
+  int r[kMine];
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {
+    const int i = u * 32 + lane;
+    e[u] = i < n ? Pair{key[i], flat[i]} : Pair{0ull, 0u};
+    r[u] = 0;
+  }
+  for (int j = 0; j < n; ++j) {
+    const Pair x{key[j], flat[j]};
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) r[u] += before(x, e[u]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < kMine; ++u)
+    if (u * 32 + lane < n && r[u] < K) {
+      key[r[u]] = e[u].key;
+      flat[r[u]] = e[u].flat;
+    }
+  __syncwarp();
+  return min(n, K);
+}
+
+// fp32 score as an ordered word.
+__device__ __forceinline__ uint32_t score_word(float off, float x) { return logit_key(off + x); }
+
+// One CTA per prompt: the log-sum-exp of every beam (a warp each), the bound from the blocks'
+// best pairs, the pairs of the blocks that reach it, their ranking.  The bound is formed on
+// fp32 scores, off + x with off rounded: each is off by at most 2^-24 (|off| + |score|), so
+// the bound is lowered by four times that, and the pairs are ranked by their 64-bit scores.
+// A chain of small dependent steps bounds the call.
+template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
-  extern __shared__ uint64_t s_dyn[];
-  __shared__ int s_n, s_reach;
-  __shared__ uint32_t s_thr;
-  __shared__ Pair s_bound;
+  using R = Row<T>;
+  constexpr int VN = R::kN;
+  extern __shared__ uint32_t s_dyn[];     // [heads]: score words, then [heads]: blocks that pass
+  __shared__ double s_off[kMaxK];         // score - lse
+  __shared__ int s_kind[kMaxK];           // 0 live, 1 finished, 2 without a score
+  __shared__ uint32_t s_hist[kBins];
+  __shared__ uint64_t s_key[kMergeWarps][kListCap];
+  __shared__ uint32_t s_flat[kMergeWarps][kListCap];
+  __shared__ uint64_t s_all_key[kMergeWarps * kMaxK + kMaxK];
+  __shared__ __align__(16) uint32_t s_all_hi[kMergeWarps * kMaxK + kMaxK];
+  __shared__ uint32_t s_all_flat[kMergeWarps * kMaxK + kMaxK];
+  __shared__ uint32_t s_range[2], s_warp[kMergeWarps];
+  __shared__ int s_bin, s_pass, s_n;
+  __shared__ float s_most;                // greatest |off| of a live beam
   grid_dependency_wait();
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int W = p.W, K = p.K, lists = W * p.chunks;
-  const int first = min(K, (K + lists - 1) / lists), heads = lists * first;
-  const bool held = static_cast<long long>(lists) * K <= kMergeCand;
-  const int room = (K + kSpare) * K;
-  double* s_off = reinterpret_cast<double*>(s_dyn);                // [W]: score - lse
-  int* s_kind = reinterpret_cast<int*>(s_off + W);                 // [W]: 0 live, 1 finished, 2 dead
-  uint64_t* s_cand = reinterpret_cast<uint64_t*>(s_off + W + (W + 1) / 2);
-  uint64_t* s_head = s_cand + (held ? lists * K : 0);              // [heads]
-  uint64_t* s_key = s_head + heads;                                // [room]: survivors
-  // Upper words of the keys, padded with 0 to whole 16-byte vectors.
-  uint32_t* s_hhi = reinterpret_cast<uint32_t*>((reinterpret_cast<uintptr_t>(s_key + room) + 15) & ~static_cast<uintptr_t>(15));
-  uint32_t* s_hi = s_hhi + (heads + 3) / 4 * 4;
-  uint32_t* s_hflat = s_hi + (room + 3) / 4 * 4;                   // [heads]
-  uint32_t* s_flat = s_hflat + heads;                              // [room]
-  const uint64_t* cand = p.cand + static_cast<size_t>(b) * lists * K;
-  if (held)                               // (lists of beams that are not live are not used)
-    for (int i = tid; i < lists * K; i += kMergeThreads)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(s_cand + i)), "l"(cand + i) : "memory");
+  const int W = p.W, K = p.K, heads = W * p.blocks;
+  uint32_t* s_word = s_dyn;
+  uint32_t* s_list = s_dyn + heads;
   for (int w = warp; w < W; w += kMergeWarps) {
     const int row = b * W + w;
     // (asked for together; those of a beam that is not live are not used)
-    const float2* st = p.stats + static_cast<size_t>(row) * p.chunks;
-    const float2 mine = lane < p.chunks ? st[lane] : make_float2(-INFINITY, 0.f);
+    const float2* st = p.stats + static_cast<size_t>(row) * p.slices;
+    const float2 mine = lane < p.slices ? st[lane] : make_float2(-INFINITY, 0.f);
     const float sc = p.score[row];
     const bool over = p.finished != nullptr && p.finished[row] != 0;
     double off = sc;
     if (!over && sc != -INFINITY) {
       float M = mine.x;
-      for (int c = lane + 32; c < p.chunks; c += 32) M = fmaxf(M, st[c].x);
+      for (int c = lane + 32; c < p.slices; c += 32) M = fmaxf(M, st[c].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       if (M != -INFINITY) {
         float hi = mine.y * expf(mine.x - M), lo = 0.f;
-        for (int c = lane + 32; c < p.chunks; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
+        for (int c = lane + 32; c < p.slices; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
@@ -365,130 +333,193 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     }
   }
   if (tid == 0) {
+    s_range[0] = 0xffffffffu;
+    s_range[1] = 0u;
+    s_pass = 0;
     s_n = 0;
-    s_thr = 0xffffffffu;
-    s_reach = 0;
+    s_bin = -1;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (int i = tid; i < kBins; i += kMergeThreads) s_hist[i] = 0u;
   __syncthreads();
-  // Entry j of a list.  Beams that are not live offer their pairs in the first chunk's list:
-  // a finished one its end token at its own score, then tokens at -inf in rising order.
-  auto entry = [&](int list, int j, Pair& e) -> bool {
-    const int w = list / p.chunks, c = list - w * p.chunks;
-    const uint32_t base = static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V);
-    if (s_kind[w] == 0) {
-      const uint64_t r = held ? s_cand[list * K + j] : cand[static_cast<size_t>(list) * K + j];
-      if (r == 0ull) return false;
-      const float x = key_logit(static_cast<uint32_t>(r >> 32));
-      e.key = score_key(x == -INFINITY ? -INFINITY : s_off[w] + static_cast<double>(x));
-      e.flat = base + (0xffffffffu - static_cast<uint32_t>(r));
-      return true;
-    }
-    if (c != 0) return false;
-    if (s_kind[w] == 1) {
-      if (j == 0) {
-        e.key = score_key(s_off[w]);
-        e.flat = base + static_cast<uint32_t>(p.eos);
-        return true;
-      }
-      const int v = j - 1 + (j - 1 >= p.eos ? 1 : 0);
-      if (v >= p.V) return false;
-      e.key = score_key(-INFINITY);
-      e.flat = base + static_cast<uint32_t>(v);
-      return true;
-    }
-    if (j >= p.V) return false;
-    e.key = score_key(-INFINITY);
-    e.flat = base + static_cast<uint32_t>(j);
-    return true;
-  };
-  // s_head is 0 where a list has no such entry: no pair's key is 0 (that of NaN).
-  for (int i = tid; i < (heads + 3) / 4 * 4; i += kMergeThreads) {
-    Pair e;
-    const bool ok = i < heads && entry(i / first, i % first, e);
-    const uint64_t k = ok ? (e.key == 0ull ? 1ull : e.key) : 0ull;
-    s_hhi[i] = static_cast<uint32_t>(k >> 32);
-    if (i < heads) {
-      s_head[i] = k;
-      s_hflat[i] = ok ? e.flat : 0xffffffffu;
-    }
-  }
-  __syncthreads();
-  // Upper words of the array above x, and equal to it.
-  auto count = [&](const uint32_t* hi, int n, uint32_t x, int& above, int& equal) {
-    above = equal = 0;
-#pragma unroll 4
-    for (int j = 0; j < (n + 3) / 4; ++j) {
-      const uint4 h = reinterpret_cast<const uint4*>(hi)[j];
-      above += (h.x > x) + (h.y > x) + (h.z > x) + (h.w > x);
-      equal += (h.x == x) + (h.y == x) + (h.z == x) + (h.w == x);
-    }
-  };
-  // The K-th greatest upper word of the heads; 0 with fewer than K of them: all pass.
+  // Score words of the blocks' best pairs; 0 where a block has no pair above -inf.  A
+  // finished beam's only pair goes straight into the final list.
+  uint32_t low = 0xffffffffu, high = 0u;
   for (int i = tid; i < heads; i += kMergeThreads) {
-    if (s_head[i] == 0ull) continue;
-    int above, equal;
-    count(s_hhi, heads, s_hhi[i], above, equal);
-    if (above < K && above + equal >= K) {
-      s_thr = s_hhi[i];                   // (the same value from each that writes)
-      s_reach = above + equal;
-    }
-  }
-  __syncthreads();
-  const uint32_t thr = s_reach == 0 ? 0u : s_thr;
-  const bool exact = s_reach > K + kSpare;   // the bound is s_bound, not thr
-  if (exact) {                            // many equal heads: the K-th itself
-    for (int i = warp; i < heads; i += kMergeWarps) {
-      const Pair mine{s_head[i], s_hflat[i]};
-      int r = 0;
-      for (int j = lane; j < heads; j += 32) r += before(Pair{s_head[j], s_hflat[j]}, mine);
-      r = __reduce_add_sync(0xffffffffu, r);
-      if (r == K - 1 && mine.key != 0ull && lane == 0) s_bound = mine;
-    }
-    __syncthreads();
-  }
-  const Pair bound = exact ? s_bound : Pair{static_cast<uint64_t>(thr) << 32, 0xffffffffu};
-  for (int l = warp; l < lists; l += kMergeWarps) {
-    const uint64_t h = s_head[l * first];
-    if (h == 0ull || before(bound, Pair{h, s_hflat[l * first]})) continue;
-    for (int j0 = 0; j0 < K; j0 += 32) {
-      Pair e;
-      const int j = j0 + lane;
-      const bool in = j < K && entry(l, j, e) && !before(bound, Pair{e.key == 0ull ? 1ull : e.key, e.flat});
-      const uint32_t ms = __ballot_sync(0xffffffffu, in);
-      int at = 0;
-      if (lane == 0 && ms != 0u) at = atomicAdd(&s_n, __popc(ms));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(ms & ((1u << lane) - 1u));
-      if (in && at < room) {
-        s_key[at] = e.key;
-        s_flat[at] = e.flat;
-        s_hi[at] = static_cast<uint32_t>(e.key >> 32);
+    const int w = i / p.blocks;
+    uint32_t word = 0u;
+    if (s_kind[w] == 0) {
+      const uint32_t k = p.best[static_cast<size_t>(b) * heads + i];
+      if (k > kNegInfKey) word = score_word(static_cast<float>(s_off[w]), key_logit(k));
+      if (word != 0u) {
+        low = min(low, word);
+        high = max(high, word);
       }
-      if (ms != 0xffffffffu) break;       // a list descends
+    }
+    s_word[i] = word;
+  }
+  for (int w = tid; w < W; w += kMergeThreads)
+    if (s_kind[w] == 1 && s_off[w] != -INFINITY) {
+      const int n = atomicAdd(&s_n, 1);
+      s_all_key[n] = score_key(s_off[w]);
+      s_all_hi[n] = static_cast<uint32_t>(s_all_key[n] >> 32);
+      s_all_flat[n] = static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(p.eos);
+    }
+  if (warp == 0) {
+    float most = 0.f;
+    for (int w = lane; w < W; w += 32)
+      if (s_kind[w] == 0) most = fmaxf(most, fabsf(static_cast<float>(s_off[w])));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) s_most = most;
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    atomicMin(&s_range[0], low);
+    atomicMax(&s_range[1], high);
+  }
+  __syncthreads();
+  // The K-th greatest word's step of a histogram over their range; its lower end is the
+  // bound.  With fewer than K words everything passes.
+  low = s_range[0];
+  high = s_range[1];
+  uint32_t bound = 1u;
+  if (low <= high) {
+    const int shift = max(0, 32 - __clz(high - low) - 10);
+    for (int i = tid; i < heads; i += kMergeThreads)
+      if (s_word[i] != 0u) atomicAdd(&s_hist[(s_word[i] - low) >> shift], 1u);
+    __syncthreads();
+    const uint32_t c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid], both = c0 + c1;
+    uint32_t incl = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    uint32_t above = incl - both;
+    for (int v = 0; v < warp; ++v) above += s_warp[v];
+    const uint32_t want = static_cast<uint32_t>(K);
+    if (above < want && above + c0 >= want) s_bin = kBins - 1 - 2 * tid;
+    else if (above + c0 < want && above + both >= want) s_bin = kBins - 2 - 2 * tid;
+    __syncthreads();
+    if (s_bin >= 0) {
+      const float at = key_logit(low + (static_cast<uint32_t>(s_bin) << shift));
+      bound = max(1u, logit_key(at - 2.3841858e-7f * (s_most + fabsf(at))));
+    }
+  }
+  for (int i = tid; i < heads; i += kMergeThreads)
+    if (s_word[i] >= bound) s_list[atomicAdd(&s_pass, 1)] = i;
+  __syncthreads();
+  const int pass = s_pass;
+  uint64_t* key = s_key[warp];
+  uint32_t* flat = s_flat[warp];
+  int n = 0;
+  Pair last{0ull, 0xffffffffu};           // the K-th pair so far: what does not rank before it is out
+  for (int i = warp; i < pass; i += kMergeWarps) {
+    const int id = s_list[i], w = id / p.blocks, block = id - w * p.blocks;
+    const double off = s_off[w];
+    const float off32 = static_cast<float>(off);
+    const RowVecs<T> r(p.logits, b * W + w, p.V);
+    for (int v0 = 0; v0 < p.block_vecs; v0 += kStepVecs) {
+      uint4 v[kStep];
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) v[u] = r.load(block * p.block_vecs + v0 + u * 32 + lane);
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) {
+        const bool some = score_word(off32, R::vmax(v[u])) >= bound;
+        if (!__any_sync(0xffffffffu, some)) continue;
+        const int first = r.first(block * p.block_vecs + v0 + u * 32 + lane);
+#pragma unroll 1
+        for (int c = 0; c < VN; ++c) {
+          // (component c of the vector, without indexing registers)
+          const uint32_t word = (VN == 8 ? c >> 1 : c) & 2 ? ((VN == 8 ? c >> 1 : c) & 1 ? v[u].w : v[u].z)
+                                                          : ((VN == 8 ? c >> 1 : c) & 1 ? v[u].y : v[u].x);
+          const float x = __uint_as_float(VN == 8 ? ((c & 1) ? (word & 0xffff0000u) : (word << 16)) : word);
+          const int token = first + c;
+          bool in = x != -INFINITY && score_word(off32, x) >= bound && token >= 0 && token < p.V;
+          if (!__any_sync(0xffffffffu, in)) continue;
+          Pair e{0ull, 0u};
+          if (in) {
+            e = Pair{score_key(off + static_cast<double>(x)), static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(token)};
+            in = before(e, last);
+          }
+          if (n + 32 > kListCap) {
+            n = cut_back(key, flat, n, K);
+            last = Pair{key[K - 1], flat[K - 1]};      // (n was above kMaxK)
+            in = in && before(e, last);
+          }
+          const uint32_t ms = __ballot_sync(0xffffffffu, in);
+          if (in) {
+            const int to = n + __popc(ms & ((1u << lane) - 1u));
+            key[to] = e.key;
+            flat[to] = e.flat;
+          }
+          n += __popc(ms);
+          __syncwarp();
+        }
+      }
+    }
+  }
+  if (n > K) n = cut_back(key, flat, n, K);
+  if (n > 0) {
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&s_n, n);
+    at = __shfl_sync(0xffffffffu, at, 0);
+    for (int i = lane; i < n; i += 32) {
+      s_all_key[at + i] = key[i];
+      s_all_hi[at + i] = static_cast<uint32_t>(key[i] >> 32);
+      s_all_flat[at + i] = flat[i];
     }
   }
   __syncthreads();
-  const int n = min(s_n, room);
-  for (int i = tid; i < n; i += kMergeThreads) {
-    int r, equal;
-    const uint32_t hi = s_hi[i];
-    count(s_hi, n / 4 * 4, hi, r, equal);
-    for (int j = n / 4 * 4; j < n; ++j) {
-      r += s_hi[j] > hi;
-      equal += s_hi[j] == hi;
-    }
-    if (r >= K) continue;
-    const Pair mine{s_key[i], s_flat[i]};
-    if (equal > 1)
-      for (int j = 0; j < n; ++j) r += s_hi[j] == hi && before(Pair{s_key[j], s_flat[j]}, mine);
-    if (r >= K) continue;
-    const int w = static_cast<int>(mine.flat / static_cast<uint32_t>(p.V));
-    const int v = static_cast<int>(mine.flat - static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V));
-    const size_t o = static_cast<size_t>(b) * K + r;
+  const int all = s_n;
+  auto put = [&](int rank, uint32_t flat_at, float score) {
+    const int w = static_cast<int>(flat_at / static_cast<uint32_t>(p.V));
+    const int v = static_cast<int>(flat_at - static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V));
+    const size_t o = static_cast<size_t>(b) * K + rank;
     p.parent[o] = w;
     p.token[o] = v;
-    p.new_score[o] = static_cast<float>(key_score(mine.key));
+    p.new_score[o] = score;
     if (p.new_finished != nullptr) p.new_finished[o] = (s_kind[w] == 1 || v == p.eos) ? 1 : 0;
+  };
+  for (int i = tid; i < all; i += kMergeThreads) {
+    const uint32_t hi = s_all_hi[i];
+    int rank = 0, equal = 0;
+#pragma unroll 4
+    for (int j = 0; j < all / 4; ++j) {
+      const uint4 h = reinterpret_cast<const uint4*>(s_all_hi)[j];
+      rank += (h.x > hi) + (h.y > hi) + (h.z > hi) + (h.w > hi);
+      equal += (h.x == hi) + (h.y == hi) + (h.z == hi) + (h.w == hi);
+    }
+    for (int j = all / 4 * 4; j < all; ++j) {
+      rank += s_all_hi[j] > hi;
+      equal += s_all_hi[j] == hi;
+    }
+    if (rank >= K) continue;
+    const Pair mine{s_all_key[i], s_all_flat[i]};
+    if (equal > 1)
+      for (int j = 0; j < all; ++j) rank += s_all_hi[j] == hi && before(Pair{s_all_key[j], s_all_flat[j]}, mine);
+    if (rank < K) put(rank, mine.flat, static_cast<float>(key_score(mine.key)));
+  }
+  // Fewer than K pairs above -inf: the rest are the first pairs at -inf (each live beam has
+  // fewer than K others, so they come early).
+  if (all < K && warp == 0) {
+    int at = all;
+    for (int w = 0; w < W && at < K; ++w) {
+      const T* x = static_cast<const T*>(p.logits) + static_cast<size_t>(b * W + w) * p.V;
+      for (int t0 = 0; t0 < p.V && at < K; t0 += 32) {
+        const int t = t0 + lane;
+        bool none = t < p.V;
+        if (s_kind[w] == 0) none = none && to_float(x[t]) == -INFINITY;
+        else if (s_kind[w] == 1) none = none && (t != p.eos || s_off[w] == -INFINITY);
+        const uint32_t ms = __ballot_sync(0xffffffffu, none);
+        const int rank = at + __popc(ms & ((1u << lane) - 1u));
+        if (none && rank < K) put(rank, static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(t), -INFINITY);
+        at += __popc(ms);
+      }
+    }
   }
   grid_dependents_launch();
 }
@@ -564,22 +595,23 @@ __global__ void __launch_bounds__(kForkThreads)
 // ------------------------------------------------------------------------ host
 
 struct BeamPlan {
-  int nv;                  // vectors a thread holds
-  int chunks, chunk_vecs;  // slices of a row, 16-byte vectors of a slice
+  int blocks, block_vecs;     // blocks of a row, vectors of a block
+  int slices, slice_blocks;   // slices of a row (a warp each), blocks of a slice
 };
 
-// Eight vectors a thread (16,384 bf16 logits a CTA) while that gives every SM a CTA; with
-// few rows, shorter slices spread a row over more SMs.  Slices of a row are equally long.
-// One vector more than the logits fill: a row may start inside one.
-void plan_beam(long long rows, int V, int dtype, int sms, BeamPlan* pl) {
+// A block is one step of a warp, 128 vectors, more where a prompt would have more than
+// kMergeBlocks.  A slice is eight blocks while that gives every SM 16 warps; with few rows,
+// shorter ones spread a row over more SMs.  One vector more than the logits fill: a row may
+// start inside one.
+void plan_beam(long long rows, int W, int V, int dtype, int sms, BeamPlan* pl) {
   const int vn = dtype == JF_DTYPE_BF16 ? 8 : 4;
   const long long vecs = (static_cast<long long>(V) + vn - 1) / vn + 1;
-  for (int nv = 8; nv >= 1; nv /= 2) {
-    pl->nv = nv;
-    pl->chunks = static_cast<int>((vecs + nv * kScanThreads - 1) / (nv * kScanThreads));
-    pl->chunk_vecs = static_cast<int>((vecs + pl->chunks - 1) / pl->chunks);
-    if (rows * pl->chunks >= sms) break;
-  }
+  pl->block_vecs = kStepVecs;
+  while (W * ((vecs + pl->block_vecs - 1) / pl->block_vecs) > kMergeBlocks) pl->block_vecs *= 2;
+  pl->blocks = static_cast<int>((vecs + pl->block_vecs - 1) / pl->block_vecs);
+  for (pl->slice_blocks = 8; pl->slice_blocks > 1; pl->slice_blocks /= 2)
+    if (rows * ((pl->blocks + pl->slice_blocks - 1) / pl->slice_blocks) >= 16ll * sms) break;
+  pl->slices = (pl->blocks + pl->slice_blocks - 1) / pl->slice_blocks;
 }
 
 bool beam_sizes_ok(int32_t B, int32_t W, int32_t V, int32_t K) {
@@ -591,18 +623,19 @@ bool beam_supported(int32_t B, int32_t W, int32_t V, int32_t K) {
          static_cast<long long>(B) * W < (1ll << 20);
 }
 
-size_t beam_workspace(const BeamPlan& pl, long long rows, int K) {
-  return static_cast<size_t>(rows) * pl.chunks * (sizeof(float2) + sizeof(uint64_t) * K);
+size_t beam_workspace(const BeamPlan& pl, long long rows) {
+  return static_cast<size_t>(rows) * (pl.slices * sizeof(float2) + pl.blocks * sizeof(uint32_t));
 }
 
 template <typename T>
-cudaError_t launch_scan(const BeamParams& p, int nv, unsigned grid, cudaStream_t s) {
-  switch (nv) {
-    case 8: return launch_pdl(beam_scan_kernel<T, 8>, dim3(grid), dim3(kScanThreads), 0, s, p);
-    case 4: return launch_pdl(beam_scan_kernel<T, 4>, dim3(grid), dim3(kScanThreads), 0, s, p);
-    case 2: return launch_pdl(beam_scan_kernel<T, 2>, dim3(grid), dim3(kScanThreads), 0, s, p);
-    default: return launch_pdl(beam_scan_kernel<T, 1>, dim3(grid), dim3(kScanThreads), 0, s, p);
-  }
+cudaError_t launch_beam(const BeamParams& p, int B, cudaStream_t s) {
+  static SmemAttr attr;
+  if (!attr.ensure(beam_merge_kernel<T>, 2 * sizeof(uint32_t) * kMergeBlocks)) return cudaErrorUnknown;
+  const dim3 grid(static_cast<unsigned>((p.total + kScanWarps - 1) / kScanWarps));
+  const cudaError_t e = launch_pdl(beam_scan_kernel<T>, grid, dim3(kScanThreads), 0, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(beam_merge_kernel<T>, dim3(static_cast<unsigned>(B)), dim3(kMergeThreads),
+                    2 * sizeof(uint32_t) * p.W * p.blocks, s, p);
 }
 
 }  // namespace
@@ -617,8 +650,8 @@ extern "C" size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V,
   const int sms = current_sm_count();
   if (sms <= 0) return static_cast<size_t>(-1);
   BeamPlan pl;
-  plan_beam(static_cast<long long>(B) * W, V, dtype, sms, &pl);
-  return beam_workspace(pl, static_cast<long long>(B) * W, K);
+  plan_beam(static_cast<long long>(B) * W, W, V, dtype, sms, &pl);
+  return beam_workspace(pl, static_cast<long long>(B) * W);
 }
 
 extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const float* score,
@@ -641,9 +674,9 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * W;
   BeamPlan pl;
-  plan_beam(rows, V, dtype, sms, &pl);
-  if (rows * pl.chunks >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
-  if (workspace_bytes < beam_workspace(pl, rows, K)) return JF_ERR_WORKSPACE_TOO_SMALL;
+  plan_beam(rows, W, V, dtype, sms, &pl);
+  if (rows * pl.slices >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  if (workspace_bytes < beam_workspace(pl, rows)) return JF_ERR_WORKSPACE_TOO_SMALL;
   BeamParams p;
   p.logits = logits;
   p.score = score;
@@ -652,27 +685,19 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   p.token = token;
   p.new_score = new_score;
   p.new_finished = new_finished;
-  p.cand = static_cast<uint64_t*>(workspace);
-  p.stats = reinterpret_cast<float2*>(p.cand + static_cast<size_t>(rows) * pl.chunks * K);
+  p.stats = static_cast<float2*>(workspace);
+  p.best = reinterpret_cast<uint32_t*>(p.stats + static_cast<size_t>(rows) * pl.slices);
   p.W = W;
   p.V = V;
   p.K = K;
   p.eos = eos_token;
-  p.chunks = pl.chunks;
-  p.chunk_vecs = pl.chunk_vecs;
-  const int lists = W * pl.chunks, first = std::min(K, (K + lists - 1) / lists);
-  const size_t room = static_cast<size_t>(lists) * first + static_cast<size_t>(K + kSpare) * K;
-  const size_t held = static_cast<long long>(lists) * K <= kMergeCand ? static_cast<size_t>(lists) * K : 0;
-  const size_t smem = sizeof(double) * (W + (W + 1) / 2) + held * sizeof(uint64_t) +
-                      room * (sizeof(uint64_t) + 2 * sizeof(uint32_t)) + 64;
-  static SmemAttr attr;
-  if (!attr.ensure(beam_merge_kernel, 220 * 1024)) return JF_ERR_CUDA;
+  p.slices = pl.slices;
+  p.slice_blocks = pl.slice_blocks;
+  p.blocks = pl.blocks;
+  p.block_vecs = pl.block_vecs;
+  p.total = static_cast<int>(rows * pl.slices);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(rows * pl.chunks);
-  cudaError_t e = dtype == JF_DTYPE_BF16 ? launch_scan<uint16_t>(p, pl.nv, grid, s)
-                                         : launch_scan<float>(p, pl.nv, grid, s);
-  if (e == cudaSuccess)
-    e = launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(B)), dim3(kMergeThreads), smem, s, p);
+  const cudaError_t e = dtype == JF_DTYPE_BF16 ? launch_beam<uint16_t>(p, B, s) : launch_beam<float>(p, B, s);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
