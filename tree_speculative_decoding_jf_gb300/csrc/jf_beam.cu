@@ -277,17 +277,22 @@ __device__ __noinline__ int cut_back(uint64_t* key, uint32_t* flat, int n, int K
 // fp32 score as an ordered word.
 __device__ __forceinline__ uint32_t score_word(float off, float x) { return logit_key(off + x); }
 
-// One CTA per prompt: the log-sum-exp of every beam (a warp each), the bound from the blocks'
-// best pairs, the pairs of the blocks that reach it, their ranking.  The bound is formed on
-// fp32 scores, off + x with off rounded: each is off by at most 2^-24 (|off| + |score|), so
-// the bound is lowered by four times that, and the pairs are ranked by their 64-bit scores.
-// A chain of small dependent steps bounds the call.
+// One CTA per prompt: the log-sum-exp of every beam, the bound from the blocks' best pairs,
+// the pairs of the blocks that reach it, their ranking.  A chain of small dependent steps
+// bounds the call, so half the warps form the bound from fp32 scores while the others take
+// the fp64 logarithms that the ranking wants.  An fp32 score, off + x, is off by at most
+// 2^-24 times the sizes of what its roundings round (score and M of the beam, the logarithm,
+// off, and the score itself) and 2^-22 for logf (below 25): the bound is lowered by four
+// times as much.
+constexpr int kBoundThreads = kMergeThreads / 2;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   using R = Row<T>;
   constexpr int VN = R::kN;
   extern __shared__ uint32_t s_dyn[];     // [heads]: score words, then [heads]: blocks that pass
   __shared__ double s_off[kMaxK];         // score - lse
+  __shared__ float s_off32[kMaxK], s_mag[kMaxK];
+  __shared__ float s_stat[3][kMaxK];      // maximum, and sum of exponentials in two parts
   __shared__ int s_kind[kMaxK];           // 0 live, 1 finished, 2 without a score
   __shared__ uint32_t s_hist[kBins];
   __shared__ uint64_t s_key[kMergeWarps][kListCap];
@@ -295,14 +300,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   __shared__ uint64_t s_all_key[kMergeWarps * kMaxK + kMaxK];
   __shared__ __align__(16) uint32_t s_all_hi[kMergeWarps * kMaxK + kMaxK];
   __shared__ uint32_t s_all_flat[kMergeWarps * kMaxK + kMaxK];
-  __shared__ uint32_t s_range[2], s_warp[kMergeWarps];
+  __shared__ uint32_t s_range[2], s_warp[kBoundThreads / 32];
   __shared__ int s_bin, s_pass, s_n;
-  __shared__ float s_most;                // greatest |off| of a live beam
   grid_dependency_wait();
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = p.W, K = p.K, heads = W * p.blocks;
   uint32_t* s_word = s_dyn;
   uint32_t* s_list = s_dyn + heads;
+  const uint32_t* best = p.best + static_cast<size_t>(b) * heads;
+  for (int i = tid; i < heads; i += kMergeThreads)    // (those of beams that are not live are not used)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_word + i)), "l"(best + i) : "memory");
   for (int w = warp; w < W; w += kMergeWarps) {
     const int row = b * W + w;
     // (asked for together; those of a beam that is not live are not used)
@@ -310,26 +317,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     const float2 mine = lane < p.slices ? st[lane] : make_float2(-INFINITY, 0.f);
     const float sc = p.score[row];
     const bool over = p.finished != nullptr && p.finished[row] != 0;
-    double off = sc;
+    float M = -INFINITY, hi = 0.f, lo = 0.f, off = sc, mag = 0.f;
     if (!over && sc != -INFINITY) {
-      float M = mine.x;
+      M = mine.x;
       for (int c = lane + 32; c < p.slices; c += 32) M = fmaxf(M, st[c].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       if (M != -INFINITY) {
-        float hi = mine.y * expf(mine.x - M), lo = 0.f;
+        hi = mine.y * expf(mine.x - M);
         for (int c = lane + 32; c < p.slices; c += 32) two_sum(hi, lo, st[c].y * expf(st[c].x - M), 0.f);
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
           two_sum(hi, lo, x, y);
         }
-        off -= static_cast<double>(M) + log_fp64(static_cast<double>(hi) + lo);
+        off = sc - (M + logf(hi));
+        mag = fabsf(sc) + 2.f * fabsf(M) + 32.f;
       }
     }
     if (lane == 0) {
       s_kind[w] = over ? 1 : (sc == -INFINITY ? 2 : 0);
-      s_off[w] = off;
+      s_off32[w] = off;
+      s_mag[w] = mag;
+      s_stat[0][w] = M;
+      s_stat[1][w] = hi;
+      s_stat[2][w] = lo;
     }
   }
   if (tid == 0) {
@@ -340,78 +352,93 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     s_bin = -1;
   }
   for (int i = tid; i < kBins; i += kMergeThreads) s_hist[i] = 0u;
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // Score words of the blocks' best pairs; 0 where a block has no pair above -inf.  A
-  // finished beam's only pair goes straight into the final list.
-  uint32_t low = 0xffffffffu, high = 0u;
-  for (int i = tid; i < heads; i += kMergeThreads) {
-    const int w = i / p.blocks;
-    uint32_t word = 0u;
-    if (s_kind[w] == 0) {
-      const uint32_t k = p.best[static_cast<size_t>(b) * heads + i];
-      if (k > kNegInfKey) word = score_word(static_cast<float>(s_off[w]), key_logit(k));
-      if (word != 0u) {
-        low = min(low, word);
-        high = max(high, word);
+  if (tid >= kBoundThreads) {
+    // fp64 offsets; a finished beam's only pair goes straight into the final list.
+    for (int w = warp - kBoundThreads / 32; w < W; w += kMergeWarps / 2)
+      if (lane == 0) {
+        double off = p.score[b * W + w];
+        if (s_kind[w] == 0 && s_stat[0][w] != -INFINITY)
+          off -= static_cast<double>(s_stat[0][w]) + log_fp64(static_cast<double>(s_stat[1][w]) + s_stat[2][w]);
+        s_off[w] = off;
+        if (s_kind[w] == 1 && off != -INFINITY) {
+          const int n = atomicAdd(&s_n, 1);
+          s_all_key[n] = score_key(off);
+          s_all_hi[n] = static_cast<uint32_t>(s_all_key[n] >> 32);
+          s_all_flat[n] = static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(p.eos);
+        }
       }
+  } else {
+    // Score words of the blocks' best pairs; 0 where a block has no pair above -inf.
+    uint32_t low = 0xffffffffu, high = 0u;
+    for (int i = tid; i < heads; i += kBoundThreads) {
+      const int w = i / p.blocks;
+      const uint32_t k = s_word[i];
+      uint32_t word = 0u;
+      if (s_kind[w] == 0 && k > kNegInfKey) {
+        word = score_word(s_off32[w], key_logit(k));
+        if (word != 0u) {
+          low = min(low, word);
+          high = max(high, word);
+        }
+      }
+      s_word[i] = word;
     }
-    s_word[i] = word;
-  }
-  for (int w = tid; w < W; w += kMergeThreads)
-    if (s_kind[w] == 1 && s_off[w] != -INFINITY) {
-      const int n = atomicAdd(&s_n, 1);
-      s_all_key[n] = score_key(s_off[w]);
-      s_all_hi[n] = static_cast<uint32_t>(s_all_key[n] >> 32);
-      s_all_flat[n] = static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(p.eos);
-    }
-  if (warp == 0) {
-    float most = 0.f;
-    for (int w = lane; w < W; w += 32)
-      if (s_kind[w] == 0) most = fmaxf(most, fabsf(static_cast<float>(s_off[w])));
+    float most = 0.f;                     // greatest sum of what is rounded, of a live beam
+    for (int w = lane; w < W; w += 32) most = fmaxf(most, s_mag[w] + fabsf(s_kind[w] == 0 ? s_off32[w] : 0.f));
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (lane == 0) s_most = most;
-  }
-  low = __reduce_min_sync(0xffffffffu, low);
-  high = __reduce_max_sync(0xffffffffu, high);
-  if (lane == 0) {
-    atomicMin(&s_range[0], low);
-    atomicMax(&s_range[1], high);
-  }
-  __syncthreads();
-  // The K-th greatest word's step of a histogram over their range; its lower end is the
-  // bound.  With fewer than K words everything passes.
-  low = s_range[0];
-  high = s_range[1];
-  uint32_t bound = 1u;
-  if (low <= high) {
-    const int shift = max(0, 32 - __clz(high - low) - 10);
-    for (int i = tid; i < heads; i += kMergeThreads)
-      if (s_word[i] != 0u) atomicAdd(&s_hist[(s_word[i] - low) >> shift], 1u);
-    __syncthreads();
-    const uint32_t c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid], both = c0 + c1;
-    uint32_t incl = both;
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) {
+      atomicMin(&s_range[0], low);
+      atomicMax(&s_range[1], high);
+    }
+    named_bar(1, kBoundThreads);
+    // The K-th greatest word's step of a histogram over their range; its lower end is the
+    // bound.  With fewer than K words everything passes.
+    low = s_range[0];
+    high = s_range[1];
+    uint32_t bound = 1u;
+    if (low <= high) {
+      constexpr int kMine = kBins / kBoundThreads;
+      const int shift = max(0, 32 - __clz(high - low) - 10);
+      for (int i = tid; i < heads; i += kBoundThreads)
+        if (s_word[i] != 0u) atomicAdd(&s_hist[(s_word[i] - low) >> shift], 1u);
+      named_bar(1, kBoundThreads);
+      const int top = kBins - 1 - kMine * tid;
+      uint32_t c[kMine], all = 0u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      for (int i = 0; i < kMine; ++i) all += c[i] = s_hist[top - i];
+      uint32_t incl = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      named_bar(1, kBoundThreads);
+      uint32_t above = incl - all;
+      for (int v = 0; v < warp; ++v) above += s_warp[v];
+      const uint32_t want = static_cast<uint32_t>(K);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (above < want && above + c[i] >= want) s_bin = top - i;
+        above += c[i];
+      }
+      named_bar(1, kBoundThreads);
+      if (s_bin >= 0) {
+        const float at = key_logit(low + (static_cast<uint32_t>(s_bin) << shift));
+        bound = max(1u, logit_key(at - 2.3841858e-7f * (most + fabsf(at)) - 9.5367432e-7f));
+      }
     }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    uint32_t above = incl - both;
-    for (int v = 0; v < warp; ++v) above += s_warp[v];
-    const uint32_t want = static_cast<uint32_t>(K);
-    if (above < want && above + c0 >= want) s_bin = kBins - 1 - 2 * tid;
-    else if (above + c0 < want && above + both >= want) s_bin = kBins - 2 - 2 * tid;
-    __syncthreads();
-    if (s_bin >= 0) {
-      const float at = key_logit(low + (static_cast<uint32_t>(s_bin) << shift));
-      bound = max(1u, logit_key(at - 2.3841858e-7f * (s_most + fabsf(at))));
-    }
+    for (int i = tid; i < heads; i += kBoundThreads)
+      if (s_word[i] >= bound) s_list[atomicAdd(&s_pass, 1)] = i;
+    if (tid == 0) s_range[0] = bound;
   }
-  for (int i = tid; i < heads; i += kMergeThreads)
-    if (s_word[i] >= bound) s_list[atomicAdd(&s_pass, 1)] = i;
   __syncthreads();
+  const uint32_t bound = s_range[0];
   const int pass = s_pass;
   uint64_t* key = s_key[warp];
   uint32_t* flat = s_flat[warp];
@@ -420,7 +447,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   for (int i = warp; i < pass; i += kMergeWarps) {
     const int id = s_list[i], w = id / p.blocks, block = id - w * p.blocks;
     const double off = s_off[w];
-    const float off32 = static_cast<float>(off);
+    const float off32 = s_off32[w];
     const RowVecs<T> r(p.logits, b * W + w, p.V);
     for (int v0 = 0; v0 < p.block_vecs; v0 += kStepVecs) {
       uint4 v[kStep];
@@ -428,24 +455,28 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       for (int u = 0; u < kStep; ++u) v[u] = r.load(block * p.block_vecs + v0 + u * 32 + lane);
 #pragma unroll
       for (int u = 0; u < kStep; ++u) {
-        const bool some = score_word(off32, R::vmax(v[u])) >= bound;
-        if (!__any_sync(0xffffffffu, some)) continue;
+        uint32_t some = __ballot_sync(0xffffffffu, score_word(off32, R::vmax(v[u])) >= bound);
         const int first = r.first(block * p.block_vecs + v0 + u * 32 + lane);
-#pragma unroll 1
-        for (int c = 0; c < VN; ++c) {
-          // (component c of the vector, without indexing registers)
-          const uint32_t word = (VN == 8 ? c >> 1 : c) & 2 ? ((VN == 8 ? c >> 1 : c) & 1 ? v[u].w : v[u].z)
-                                                          : ((VN == 8 ? c >> 1 : c) & 1 ? v[u].y : v[u].x);
-          const float x = __uint_as_float(VN == 8 ? ((c & 1) ? (word & 0xffff0000u) : (word << 16)) : word);
-          const int token = first + c;
+        // One passing vector (there are few) after the other, a lane a logit.
+        for (; some != 0u; some &= some - 1u) {
+          const int src = __ffs(some) - 1;
+          uint4 t;
+          t.x = __shfl_sync(0xffffffffu, v[u].x, src);
+          t.y = __shfl_sync(0xffffffffu, v[u].y, src);
+          t.z = __shfl_sync(0xffffffffu, v[u].z, src);
+          t.w = __shfl_sync(0xffffffffu, v[u].w, src);
+          const int token = __shfl_sync(0xffffffffu, first, src) + lane;
+          float x = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < VN; ++c)
+            if (lane == c) x = R::get(t, c);
           bool in = x != -INFINITY && score_word(off32, x) >= bound && token >= 0 && token < p.V;
-          if (!__any_sync(0xffffffffu, in)) continue;
           Pair e{0ull, 0u};
           if (in) {
             e = Pair{score_key(off + static_cast<double>(x)), static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(token)};
             in = before(e, last);
           }
-          if (n + 32 > kListCap) {
+          if (n + VN > kListCap) {
             n = cut_back(key, flat, n, K);
             last = Pair{key[K - 1], flat[K - 1]};      // (n was above kMaxK)
             in = in && before(e, last);
