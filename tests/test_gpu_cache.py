@@ -296,6 +296,26 @@ def test_select_long_rows(jf, rows):
     run_select(jf, w, L, 30000 if rows == 1 else 5000, 4, 100)
 
 
+@pytest.mark.parametrize("kind", ["weights", "few values", "one value"])
+def test_select_rows_past_shared_memory(jf, kind):
+    """Slices that a cluster of eight cannot hold on chip."""
+    rng = np.random.default_rng(2)
+    n = 450000
+    w = rng.standard_normal((2, 1, n)).astype(np.float32)
+    if kind != "weights":
+        w = np.floor(w * 2) if kind == "few values" else np.zeros_like(w)
+    err = new_err()
+    L = np.array([n, 300], np.int32)
+    keep, kept = jf.select_kept_keys(dev(w), dev(L), 100000, sink=3, recent=50, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and kept.tolist() == [100000, 300]
+    mid = w[0, 0, 3:n - 50]
+    order = np.lexsort((np.arange(len(mid)), -mid.astype(np.float64)))[:100000 - 53] + 3
+    want = np.sort(np.concatenate([np.arange(3), order, np.arange(n - 50, n)]))
+    assert (keep[0, 0].cpu().numpy() == want).all()
+    assert (keep[1, 0, :300].cpu().numpy() == np.arange(300)).all() and (keep[1, 0, 300:] == -1).all()
+
+
 def test_select_clamps_lengths(jf):
     w = np.random.default_rng(0).random((2, 2, 64)).astype(np.float32)
     err = new_err()

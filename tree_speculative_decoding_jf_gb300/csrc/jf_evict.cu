@@ -14,16 +14,19 @@ constexpr int kPage = 16;
 // ------------------------------------------------------------------------ selection
 
 // One thread-block cluster per (sequence, kv-head) row; its CTAs take equal slices of the
-// row.  Weights become 32-bit keys that order as the weights do.  The budget's smallest
-// kept key is found by counting: the keys' range is cut into 2048 equal steps, the step
-// that holds the wanted rank becomes the next range, and after at most three counts it is
-// one value (2^32 = 2^11 * 2^11 * 2^10).  Equal keys are then taken by position.
+// row and keep them on chip as 32-bit keys that order as the weights do, so the weights are
+// read once.  The smallest kept key is found by counting: the keys' range is cut into 1024
+// steps, and the step that holds the wanted rank usually holds few enough keys to list and
+// rank directly; otherwise it becomes the next range, down to one value (2^32 in four
+// counts), of which the first by position stay.  What bounds the call is the number of such
+// row-wide steps and their barriers, not the 8 bytes a key.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelItems = 16;                               // keys a thread holds
-constexpr int kSelTile = kSelThreads * kSelItems;           // keys a CTA holds at once
-constexpr int kBins = 2048;
-constexpr int kBinBits = 11;
+constexpr int kSelSlice = 8192;           // keys of a CTA's slice, while a cluster of 8 suffices
+constexpr int kSelMost = 200 * 1024 / 4;  // keys that fit on chip; longer slices are read again
+constexpr int kBinBits = 10;
+constexpr int kBins = 1 << kBinBits;
+constexpr int kSelList = 1024;            // listed keys of a row
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   uint32_t u = __float_as_uint(w);
@@ -32,34 +35,38 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ void row_sync(int C) {
-  if (C == 1) __syncthreads();
-  else cluster_sync();
-}
-
 __device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
-__device__ __forceinline__ uint32_t peer_u32(const uint32_t* local, int rank, int C) {
-  return C == 1 ? *local : dsmem_ld_u32(dsmem_addr(local, rank));
-}
-
+template <bool ONE>   // a cluster of one CTA
 __global__ void __launch_bounds__(kSelThreads, 2)
     select_kernel(const float* __restrict__ weight, const int32_t* __restrict__ seq_len, int Hkv,
-                  int cap, int sink, int recent, int budget, int C, int32_t* __restrict__ keep,
-                  int32_t* __restrict__ kept_len, int32_t* dev_err) {
-  __shared__ uint32_t s_hist[kBins];      // this CTA's counts
-  __shared__ uint32_t s_tot[kBins];       // the row's counts
-  __shared__ uint32_t s_red[4];           // min, max (later kept, equal) of this CTA
+                  int cap, int sink, int recent, int budget, int C, int resident,
+                  int32_t* __restrict__ keep, int32_t* __restrict__ kept_len, int32_t* dev_err) {
+  extern __shared__ uint32_t s_keys[];                      // this CTA's slice
+  __shared__ uint32_t s_hist[2][kBins];                     // this CTA's counts (two rounds' in turn)
+  __shared__ uint32_t s_range[2];                           // min, max of this CTA
+  __shared__ uint32_t s_count[3];                           // above the step, in it, listed (this CTA)
   __shared__ uint32_t s_warp[2][kSelWarps];
-  __shared__ uint32_t s_bin[3];           // the chosen step, keys above it, keys in it
+  __shared__ uint32_t s_bin[3];                             // the step, keys above it, keys in it
+  __shared__ uint64_t s_list[kSelList];                     // key << 32 | ~position, this CTA's
+  __shared__ uint64_t s_all[kSelList];                      // the row's
+  __shared__ uint64_t s_cut;
   grid_dependency_wait();
-  const int rank = C == 1 ? 0 : static_cast<int>(cluster_ctarank());
+  const int rank = ONE ? 0 : static_cast<int>(cluster_ctarank());
   const int row = blockIdx.x / C, b = row / Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto row_sync = [&]() {
+    if constexpr (ONE) __syncthreads();
+    else cluster_sync();
+  };
+  auto peer = [&](const uint32_t* local, int r) -> uint32_t {
+    if constexpr (ONE) return *local;
+    else return dsmem_ld_u32(dsmem_addr(local, r));
+  };
   int L = seq_len[b];
   if (L < 0 || L > cap) {
     if (tid == 0 && rank == 0 && row % Hkv == 0) report(dev_err, JF_DEVERR_BAD_PREFIX);
@@ -73,214 +80,201 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     return;
   }
   const float* w = weight + static_cast<size_t>(row) * cap;
-  const int lo_t = sink, hi_t = L - recent;                 // positions that compete
-  const int want = budget - sink - recent;                  // >= 0, < hi_t - lo_t
+  const uint32_t want = static_cast<uint32_t>(budget - sink - recent);   // of the keys that compete
   const int per = ((L + C - 1) / C + 31) & ~31;             // slice of this CTA
   const int t_lo = min(L, rank * per), t_hi = min(L, t_lo + per);
-  const int ntiles = (per + kSelTile - 1) / kSelTile;
+  const int c_lo = max(t_lo, min(sink, t_hi)), c_hi = max(c_lo, min(t_hi, L - recent));   // its competing part
+  auto key_of = [&](int t) -> uint32_t { return resident ? s_keys[t - t_lo] : weight_key(w[t]); };
 
-  uint32_t key[kSelItems];
-  int seg_lo = 0, seg_n = 0;              // this warp's run of the tile
-  auto load = [&](int tile) {
-    const int a = t_lo + tile * kSelTile, n = max(0, min(kSelTile, t_hi - a));
-    const int seg = (((n + kSelWarps - 1) / kSelWarps) + 31) & ~31;
-    seg_lo = a + min(n, warp * seg);
-    seg_n = max(0, min(seg, n - warp * seg));
-#pragma unroll
-    for (int i = 0; i < kSelItems; ++i) {
-      const int e = i * 32 + lane;
-      key[i] = e < seg_n ? weight_key(w[seg_lo + e]) : 0u;
-    }
-  };
-  auto competes = [&](int i) -> bool {
-    const int e = i * 32 + lane, t = seg_lo + e;
-    return e < seg_n && t >= lo_t && t < hi_t;
-  };
-
-  uint32_t T = 0xffffffffu, need = 0;     // kept: key > T, and the first `need` keys == T
-  if (want > 0) {
-    uint32_t kmin = 0xffffffffu, kmax = 0u;
-    for (int tile = 0; tile < ntiles; ++tile) {
-      load(tile);
-#pragma unroll
-      for (int i = 0; i < kSelItems; ++i)
-        if (competes(i)) {
-          kmin = min(kmin, key[i]);
-          kmax = max(kmax, key[i]);
-        }
-    }
-    kmin = __reduce_min_sync(0xffffffffu, kmin);
-    kmax = __reduce_max_sync(0xffffffffu, kmax);
-    if (tid == 0) {
-      s_red[0] = 0xffffffffu;
-      s_red[1] = 0u;
-    }
-    __syncthreads();
-    if (lane == 0) {
-      atomicMin(&s_red[0], kmin);
-      atomicMax(&s_red[1], kmax);
-    }
-    row_sync(C);
-    for (int r = 0; r < C; ++r) {
-      kmin = min(kmin, peer_u32(&s_red[0], r, C));
-      kmax = max(kmax, peer_u32(&s_red[1], r, C));
-    }
-    const uint32_t range = kmax - kmin;
-    uint32_t lo = kmin, last = range;     // keys of the current range: lo .. lo + last
-    int s = max(0, 32 - __clz(range) - kBinBits);
-    need = static_cast<uint32_t>(want);
-    for (;;) {
-      for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0u;
-      __syncthreads();
-      for (int tile = 0; tile < ntiles; ++tile) {
-        if (ntiles > 1) load(tile);
-#pragma unroll
-        for (int i = 0; i < kSelItems; ++i)
-          if (competes(i) && key[i] >= lo && key[i] - lo <= last) atomicAdd(&s_hist[(key[i] - lo) >> s], 1u);
-      }
-      const uint32_t* tot = s_hist;
-      row_sync(C);
-      if (C > 1) {                        // every CTA forms the row's counts for itself
-        for (int i = tid; i < kBins; i += kSelThreads) {
-          uint32_t v = 0;
-          for (int r = 0; r < C; ++r) v += peer_u32(&s_hist[i], r, C);
-          s_tot[i] = v;
-        }
-        cluster_sync();                   // s_hist is read by nobody any more
-        tot = s_tot;
-      }
-      // Four steps a thread, thread 0 the highest: the step where the count from above
-      // reaches `need`.
-      uint32_t c[4], mine = 0;
-      const int top = kBins - 1 - tid * 4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mine += c[i] = tot[top - i];
-      uint32_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) s_warp[0][warp] = incl;
-      __syncthreads();
-      uint32_t above = incl - mine;
-      for (int v = 0; v < warp; ++v) above += s_warp[0][v];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (above < need && above + c[i] >= need) {
-          s_bin[0] = top - i;
-          s_bin[1] = above;
-          s_bin[2] = c[i];
-        }
-        above += c[i];
-      }
-      __syncthreads();
-      const uint32_t bin = s_bin[0];
-      need -= s_bin[1];
-      lo += bin << s;
-      if (s == 0) {
-        T = lo;
-        break;
-      }
-      if (s_bin[2] == need && lo > 0) {   // the whole step stays
-        T = lo - 1;
-        need = 0;
-        break;
-      }
-      last = min(last - (bin << s), (1u << s) - 1u);
-      s = max(0, s - kBinBits);
+  // ---- the slice, and the range of the competing keys
+  if (tid < 2) s_range[tid] = tid == 0 ? 0xffffffffu : 0u;
+  uint32_t kmin = 0xffffffffu, kmax = 0u;
+#pragma unroll 8
+  for (int t = t_lo + tid; t < t_hi; t += kSelThreads) {
+    const uint32_t k = weight_key(w[t]);
+    if (resident) s_keys[t - t_lo] = k;
+    if (t >= c_lo && t < c_hi) {
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
     }
   }
+  for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0u;
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  __syncthreads();
+  if (lane == 0) {
+    atomicMin(&s_range[0], kmin);
+    atomicMax(&s_range[1], kmax);
+  }
+  row_sync();
+  for (int r = 0; r < C; ++r) {
+    kmin = min(kmin, peer(&s_range[0], r));
+    kmax = max(kmax, peer(&s_range[1], r));
+  }
 
-  // Kept keys (forced ones among them) and keys equal to T, per CTA.
-  auto classify = [&](int i, bool& above, bool& equal) {
-    const int e = i * 32 + lane, t = seg_lo + e;
-    const bool in = e < seg_n, mid = t >= lo_t && t < hi_t;
-    above = in && (!mid || (want > 0 && key[i] > T));
-    equal = in && mid && need > 0 && key[i] == T;
-  };
-  uint32_t n_above = 0, n_equal = 0;
-  for (int tile = 0; tile < ntiles; ++tile) {
-    if (ntiles > 1 || want == 0) load(tile);
+  // ---- kept: keys above lo + last; of the keys lo .. lo + last (the step), `need`
+  uint32_t lo = kmin, last = kmax - kmin, need = want;
+  int shift = max(0, 32 - __clz(last) - kBinBits);
+  bool listed = false;
+  if (want == 0u) {                       // nothing that competes stays
+    lo = 0xffffffffu;
+    last = 0u;
+  }
+  for (int round = 0; want > 0u; ++round) {
+    uint32_t* hist = s_hist[round & 1];
+#pragma unroll 4
+    for (int t = c_lo + tid; t < c_hi; t += kSelThreads) {
+      const uint32_t d = key_of(t) - lo;
+      if (d <= last) atomicAdd(&hist[d >> shift], 1u);
+    }
+    row_sync();
+    // The step where the count from above reaches `need`: two steps a thread, thread 0 the
+    // highest.
+    const int top = kBins - 1 - 2 * tid;
+    uint32_t c0 = 0u, c1 = 0u;
+    for (int r = 0; r < C; ++r) {
+      c0 += peer(&hist[top], r);
+      c1 += peer(&hist[top - 1], r);
+    }
+    for (int i = tid; i < kBins; i += kSelThreads) s_hist[(round & 1) ^ 1][i] = 0u;   // (read by nobody now)
+    uint32_t incl = c0 + c1;
 #pragma unroll
-    for (int i = 0; i < kSelItems; ++i) {
-      bool a, q;
-      classify(i, a, q);
-      n_above += a;
-      n_equal += q;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_warp[0][warp] = incl;
+    __syncthreads();
+    uint32_t above = incl - c0 - c1;
+    for (int v = 0; v < warp; ++v) above += s_warp[0][v];
+    if (above < need && above + c0 >= need) {
+      s_bin[0] = top;
+      s_bin[1] = above;
+      s_bin[2] = c0;
+    } else if (above + c0 < need && above + c0 + c1 >= need) {
+      s_bin[0] = top - 1;
+      s_bin[1] = above + c0;
+      s_bin[2] = c1;
+    }
+    __syncthreads();
+    need -= s_bin[1];
+    lo += s_bin[0] << shift;
+    last = min(last - (s_bin[0] << shift), (1u << shift) - 1u);
+    listed = s_bin[2] <= kSelList;
+    if (listed || shift == 0) break;
+    shift = max(0, shift - kBinBits);
+  }
+
+  // ---- counts: forced keys and keys above the step, keys in it; the latter listed
+  const int seg = ((t_hi - t_lo + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int seg_lo = min(t_hi, t_lo + warp * seg), seg_hi = min(t_hi, seg_lo + seg);
+  auto forced = [&](int t) -> bool { return t < c_lo || t >= c_hi; };
+  if (tid == 0) s_count[2] = 0u;
+  __syncthreads();
+  uint32_t n_above = 0u, n_in = 0u;
+#pragma unroll 4
+  for (int t = seg_lo + lane; t < seg_hi; t += 32) {
+    if (forced(t)) {
+      ++n_above;
+      continue;
+    }
+    const uint32_t k = key_of(t);
+    if (k < lo) continue;
+    if (k - lo > last) {
+      ++n_above;
+    } else if (want > 0u) {
+      ++n_in;
+      if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
     }
   }
   n_above = __reduce_add_sync(0xffffffffu, n_above);
-  n_equal = __reduce_add_sync(0xffffffffu, n_equal);
-  __syncthreads();
+  n_in = __reduce_add_sync(0xffffffffu, n_in);
   if (lane == 0) {
     s_warp[0][warp] = n_above;
-    s_warp[1][warp] = n_equal;
+    s_warp[1][warp] = n_in;
   }
   __syncthreads();
   if (tid < 2) {
-    uint32_t v = 0;
+    uint32_t v = 0u;
     for (int i = 0; i < kSelWarps; ++i) v += s_warp[tid][i];
-    s_red[2 + tid] = v;
+    s_count[tid] = v;
   }
-  row_sync(C);
-  uint32_t base_above = 0, base_equal = 0;
-  for (int r = 0; r < rank; ++r) {
-    base_above += peer_u32(&s_red[2], r, C);
-    base_equal += peer_u32(&s_red[3], r, C);
+  row_sync();
+  uint32_t at = 0u, in_before = 0u, all = 0u;               // kept and in-step keys of earlier CTAs
+  for (int r = 0; r < C; ++r) {
+    const uint32_t a = peer(&s_count[0], r), n = peer(&s_count[1], r);
+    if (r < rank) {
+      at += a;
+      in_before += n;
+    }
+    if (listed) {                         // the row's list, in any order
+      for (uint32_t i = tid; i < n; i += kSelThreads) {
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(&s_list[i]);
+        reinterpret_cast<uint32_t*>(&s_all[all + i])[0] = peer(e, r);
+        reinterpret_cast<uint32_t*>(&s_all[all + i])[1] = peer(e + 1, r);
+      }
+    }
+    all += n;
+  }
+  for (int v = 0; v < warp; ++v) {
+    at += s_warp[0][v];
+    in_before += s_warp[1][v];
+  }
+  uint64_t cut = ~0ull;
+  if (listed) {                           // the step's keys that stay: `cut` and what ranks before it
+    __syncthreads();
+    for (uint32_t i = tid; i < all; i += kSelThreads) {
+      const uint64_t e = s_all[i];
+      uint32_t before = 0u;
+#pragma unroll 8
+      for (uint32_t j = 0; j < all; ++j) before += s_all[j] > e;
+      if (before == need - 1u) s_cut = e;
+    }
+    __syncthreads();
+    cut = s_cut;
+    uint32_t n = 0u;
+    for (uint32_t i = lane; i < all; i += 32) {
+      const uint64_t e = s_all[i];
+      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(seg_lo);
+    }
+    at += __reduce_add_sync(0xffffffffu, n);
+  } else {                                // one value: the first by position stay
+    at += min(need, in_before);
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int tile = 0; tile < ntiles; ++tile) {
-    if (ntiles > 1) {
-      load(tile);
-      n_above = n_equal = 0;
-#pragma unroll
-      for (int i = 0; i < kSelItems; ++i) {
-        bool a, q;
-        classify(i, a, q);
-        n_above += a;
-        n_equal += q;
+  for (int t0 = seg_lo; t0 < seg_hi; t0 += 32) {
+    const int t = t0 + lane;
+    bool stay = false, in = false;
+    if (t < seg_hi) {
+      if (forced(t)) {
+        stay = true;
+      } else {
+        const uint32_t k = key_of(t);
+        if (k >= lo) {
+          in = want > 0u && k - lo <= last;
+          stay = in ? listed && ((static_cast<uint64_t>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t))) >= cut
+                    : k - lo > last;
+        }
       }
-      n_above = __reduce_add_sync(0xffffffffu, n_above);
-      n_equal = __reduce_add_sync(0xffffffffu, n_equal);
-      __syncthreads();
-      if (lane == 0) {
-        s_warp[0][warp] = n_above;
-        s_warp[1][warp] = n_equal;
-      }
-      __syncthreads();
     }
-    uint32_t at_above = base_above, at_equal = base_equal;
-    for (int v = 0; v < kSelWarps; ++v) {
-      if (v < warp) {
-        at_above += s_warp[0][v];
-        at_equal += s_warp[1][v];
-      }
-      base_above += s_warp[0][v];
-      base_equal += s_warp[1][v];
+    if (!listed) {
+      const uint32_t mi = __ballot_sync(0xffffffffu, in);
+      if (in) stay = in_before + __popc(mi & below) < need;
+      in_before += __popc(mi);
     }
-    uint32_t at = at_above + min(need, at_equal);
-#pragma unroll
-    for (int i = 0; i < kSelItems; ++i) {
-      if (i * 32 >= seg_n) break;
-      bool a, q;
-      classify(i, a, q);
-      const uint32_t mq = __ballot_sync(0xffffffffu, q);
-      const bool stay = a || (q && at_equal + __popc(mq & below) < need);
-      const uint32_t ms = __ballot_sync(0xffffffffu, stay);
-      if (stay) out[at + __popc(ms & below)] = seg_lo + i * 32 + lane;
-      at += __popc(ms);
-      at_equal += __popc(mq);
-    }
+    const uint32_t ms = __ballot_sync(0xffffffffu, stay);
+    if (stay) out[at + __popc(ms & below)] = t;
+    at += __popc(ms);
   }
   grid_dependents_launch();
-  if (C > 1) cluster_sync();              // nobody leaves while its counts may be read
+  if constexpr (!ONE) cluster_sync();     // nobody leaves while its lists may be read
 }
 
 // ------------------------------------------------------------------------ eviction
 
 constexpr int kEvictThreads = 256;
-constexpr int kEvictRows = 8;             // rows a thread has in flight
+constexpr int kEvictHeld = 4;             // 16-byte vectors a thread moves at a time
+constexpr int kEvictWeights = 8;          // weights a thread moves at a time
 
 struct EvictParams {
   uint16_t* k_cache;
@@ -294,19 +288,32 @@ struct EvictParams {
   float* weight_out;
   int32_t* dev_err;
   int Hkv, D, budget, max_pages, num_pages;
-  int slices, splits;         // byte slices of a row; ranges of rows (1 in place)
   int kv_in_place, weight_in_place;
 };
 
-// One CTA moves one byte slice of K or V of one kv-head (the last CTA of a head: the
-// weights), over its range of kept rows.  In place the rows go in rising order: because
-// keep[j] >= j rises strictly, row j's new place lies below every later row's old one, so
-// reading a batch whole before writing it gives the sequential result.
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
+// One CTA moves one byte slice (VECS 16-byte vectors) of K or V of one kv-head (the last CTA
+// of a head: the weights), over its range of kept rows; bound by the bytes, read once and
+// written once.
+//
+// In place the rows go in rising order, in batches, by one CTA a slice (32-byte pieces of
+// the rows would spread further, but share the 64-byte accesses of HBM).  keep[j] >= j rises
+// strictly, so a row's new place lies below every later row's old one: reading a batch
+// whole before any of it is written gives the sequential result, and the next batch may be
+// read before this one is written.  Into other pages, whole rows move in any order and the
+// rows are split over CTAs.
+//
+// A row's pool rows (page * 16 + slot) are looked up once, by one thread, two batches ahead.
+template <int VECS>
+__global__ void __launch_bounds__(kEvictThreads, 4) evict_kernel(const EvictParams p) {
+  constexpr int kRows = kEvictThreads / VECS;               // rows a pass of the CTA touches
+  constexpr int kBatch = kRows * kEvictHeld;
+  static_assert(kBatch <= kEvictThreads, "a thread looks up one row of a batch");
+  // Four: a slot is written again only when every thread is done with its last batch.
+  __shared__ int s_src[4][kBatch], s_dst[4][kBatch];
   grid_dependency_wait();
-  const int parts = 2 * p.slices + (p.weight_out != nullptr ? 1 : 0);
+  const int slices = p.D / 8 / VECS, parts = 2 * slices + (p.weight_out != nullptr ? 1 : 0);
   const int part = blockIdx.x % parts, row = blockIdx.x / parts;
-  const int b = row / p.Hkv, g = row % p.Hkv;
+  const int b = row / p.Hkv, g = row % p.Hkv, tid = threadIdx.x;
   const int cap = p.max_pages * kPage;
   int bits = 0;
   int L = p.seq_len[b], n = p.kept_len[b];
@@ -315,70 +322,90 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   if (n < 0 || n > min(L, p.budget)) bits |= JF_DEVERR_BAD_PATH;
   n = max(0, min(n, min(L, p.budget)));
   const int32_t* keep = p.keep + static_cast<size_t>(row) * p.budget;
-  const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
-  const int32_t* nt = p.new_table + static_cast<size_t>(b) * p.max_pages;
-  const int span = (n + p.splits - 1) / p.splits;
-  const int j0 = min(n, static_cast<int>(blockIdx.y) * span), j1 = min(n, j0 + span);
+  // Ranges of whole batches, so that CTAs differ by at most one.
+  const int batches = (n + kBatch - 1) / kBatch, splits = gridDim.y;
+  const int j0 = static_cast<int>(static_cast<long long>(batches) * blockIdx.y / splits) * kBatch;
+  const int j1 = min(n, static_cast<int>(static_cast<long long>(batches) * (blockIdx.y + 1) / splits) * kBatch);
   auto source = [&](int j) -> int {       // -1: a malformed entry
-    const int t = keep[j];
-    if (t < j || t >= L || (j > 0 && t <= keep[j - 1])) return -1;
-    return t;
+    const int t = keep[j], before = j > 0 ? keep[j - 1] : -1;
+    if (t >= j && t < L && t > before) return t;
+    bits |= JF_DEVERR_BAD_PATH;
+    return -1;
   };
-  if (part == 2 * p.slices) {
+  if (part == 2 * slices) {
     const float* w = p.weight + static_cast<size_t>(row) * cap;
     float* wo = p.weight_out + static_cast<size_t>(row) * cap;
-    for (int base = j0; base < j1; base += kEvictThreads * kEvictRows) {
-      float v[kEvictRows];
-      int t[kEvictRows];
+    // (in place, one CTA goes through all rows in order)
+    const int w0 = p.weight_in_place ? 0 : j0, w1 = p.weight_in_place ? (blockIdx.y == 0 ? n : 0) : j1;
+    for (int base = w0; base < w1; base += kEvictThreads * kEvictWeights) {
+      float v[kEvictWeights];
+      int t[kEvictWeights];
 #pragma unroll
-      for (int u = 0; u < kEvictRows; ++u) {
-        const int j = base + u * kEvictThreads + threadIdx.x;
-        t[u] = j < j1 ? source(j) : -1;
+      for (int u = 0; u < kEvictWeights; ++u) {
+        const int j = base + u * kEvictThreads + tid;
+        t[u] = j < w1 ? source(j) : -1;
         if (t[u] >= 0) v[u] = w[t[u]];
-        else if (j < j1) bits |= JF_DEVERR_BAD_PATH;
       }
       if (p.weight_in_place) __syncthreads();
 #pragma unroll
-      for (int u = 0; u < kEvictRows; ++u)
-        if (t[u] >= 0) wo[base + u * kEvictThreads + threadIdx.x] = v[u];
+      for (int u = 0; u < kEvictWeights; ++u)
+        if (t[u] >= 0) wo[base + u * kEvictThreads + tid] = v[u];
       if (p.weight_in_place) __syncthreads();
     }
   } else {
-    uint16_t* cache = part < p.slices ? p.k_cache : p.v_cache;
-    const int vecs = p.D / 8 / p.slices;  // 16-byte vectors of a slice
-    const int rows = kEvictThreads / vecs;
-    const int r = threadIdx.x / vecs;
-    const int col = (part % p.slices) * vecs + threadIdx.x % vecs;
-    auto at = [&](int page, int t) -> uint4* {
-      return reinterpret_cast<uint4*>(cache + ((static_cast<size_t>(page) * kPage + t % kPage) * p.Hkv + g) * p.D) + col;
-    };
-    for (int base = j0; base < j1; base += rows * kEvictRows) {
-      uint4 v[kEvictRows];
-      uint4* to[kEvictRows];
-#pragma unroll
-      for (int u = 0; u < kEvictRows; ++u) {
-        const int j = base + u * rows + r;
-        to[u] = nullptr;
-        if (j >= j1) continue;
+    uint4* cache = reinterpret_cast<uint4*>(part < slices ? p.k_cache : p.v_cache);
+    const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
+    const int32_t* nt = p.new_table + static_cast<size_t>(b) * p.max_pages;
+    const int r = tid / VECS, col = (part % slices) * VECS + tid % VECS;
+    const int row_vecs = p.D / 8;
+    // Pool rows of row j of a batch into its slot of s_src / s_dst; -1: not moved.
+    auto look_up = [&](int base, int slot) {
+      if (tid >= kBatch) return;
+      const int j = base + tid;
+      int from = -1, to = -1;
+      if (j < j1) {
         const int t = source(j);
-        if (t < 0) {
-          bits |= JF_DEVERR_BAD_PATH;
-          continue;
+        if (t >= 0 && !(p.kv_in_place && t == j)) {
+          const int ps = bt[t / kPage], pd = nt[j / kPage];
+          if (ps >= 0 && ps < p.num_pages && pd >= 0 && pd < p.num_pages) {
+            from = ps * kPage + t % kPage;
+            to = pd * kPage + j % kPage;
+          } else {
+            bits |= JF_DEVERR_BAD_PAGE;
+          }
         }
-        const int ps = bt[t / kPage], pd = nt[j / kPage];
-        if (ps < 0 || ps >= p.num_pages || pd < 0 || pd >= p.num_pages) {
-          bits |= JF_DEVERR_BAD_PAGE;
-          continue;
-        }
-        if (p.kv_in_place && t == j) continue;
-        to[u] = at(pd, j);
-        v[u] = *at(ps, t);
       }
-      if (p.kv_in_place) __syncthreads();
+      s_src[slot][tid] = from;
+      s_dst[slot][tid] = to;
+    };
+    auto vec_at = [&](int pool_row) -> uint4* {
+      return cache + (static_cast<size_t>(pool_row) * p.Hkv + g) * row_vecs + col;
+    };
+    uint4 v[kEvictHeld], next[kEvictHeld];
+    auto read = [&](int slot, uint4 (&x)[kEvictHeld]) {
 #pragma unroll
-      for (int u = 0; u < kEvictRows; ++u)
-        if (to[u] != nullptr) *to[u] = v[u];
-      if (p.kv_in_place) __syncthreads();
+      for (int u = 0; u < kEvictHeld; ++u) {
+        const int from = s_src[slot][u * kRows + r];
+        if (from >= 0) x[u] = *vec_at(from);
+      }
+    };
+    look_up(j0, 0);
+    look_up(j0 + kBatch, 1);
+    __syncthreads();
+    read(0, next);
+    int slot = 0;
+    for (int base = j0; base < j1; base += kBatch) {
+#pragma unroll
+      for (int u = 0; u < kEvictHeld; ++u) v[u] = next[u];
+      look_up(base + 2 * kBatch, (slot + 2) & 3);
+      read((slot + 1) & 3, next);
+      __syncthreads();                    // every thread has read this batch, and the one after
+#pragma unroll
+      for (int u = 0; u < kEvictHeld; ++u) {
+        const int to = s_dst[slot][u * kRows + r];
+        if (to >= 0) *vec_at(to) = v[u];
+      }
+      slot = (slot + 1) & 3;
     }
   }
   if (bits) report(p.dev_err, bits);
@@ -403,23 +430,32 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * Hkv;
+  // The smallest cluster whose slices stay at kSelSlice keys; with few rows, more CTAs a row
+  // while the machine has room for them.
   int C = 1;
-  while (C < 8 && (capacity > C * kSelTile || (rows * C * 2 <= sms && capacity > C * 2048))) C *= 2;
+  while (C < 8 && (capacity > C * kSelSlice || (rows * C * 2 <= sms && capacity > C * 2048))) C *= 2;
+  const int slice = ((capacity + C - 1) / C + 31) & ~31;
+  const int resident = slice <= kSelMost;
+  const size_t smem = resident ? static_cast<size_t>(slice) * sizeof(uint32_t) : 0;
+  auto* kernel = C == 1 ? select_kernel<true> : select_kernel<false>;
+  static SmemAttr attr1, attr;
+  if (!(C == 1 ? attr1 : attr).ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, weight, seq_len, Hkv, capacity, sink,
-                                           recent, budget, C, keep, kept_len, dev_err);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, weight, seq_len, Hkv, capacity, sink, recent,
+                                           budget, C, resident, keep, kept_len, dev_err);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
@@ -459,10 +495,19 @@ extern "C" jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* bl
   p.budget = budget;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
-  p.slices = 4;
-  p.splits = 1;
-  const unsigned parts = 2 * p.slices + (weight_out != nullptr ? 1 : 0);
-  const cudaError_t e = launch_pdl(evict_kernel, dim3(static_cast<unsigned>(B) * Hkv * parts, p.splits),
-                                   dim3(kEvictThreads), 0, reinterpret_cast<cudaStream_t>(stream), p);
+  // In place: 64-byte slices, one CTA each.  Into other pages: whole rows, split so that
+  // every SM gets about eight CTAs (two rounds of the four that fit).
+  const int vecs = p.kv_in_place ? 4 : D / 8;
+  const int batch = kEvictThreads / vecs * kEvictHeld;
+  const unsigned parts = 2 * (D / 8 / vecs) + (weight_out != nullptr ? 1 : 0);
+  const long long units = static_cast<long long>(B) * Hkv * parts;
+  long long splits = 1;
+  if (!p.kv_in_place)
+    splits = std::max<long long>(1, std::min<long long>((budget + batch - 1) / batch, (8ll * sms + units - 1) / units));
+  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(std::min<long long>(splits, 65535)));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = vecs == 4   ? launch_pdl(evict_kernel<4>, grid, dim3(kEvictThreads), 0, s, p)
+                        : vecs == 8 ? launch_pdl(evict_kernel<8>, grid, dim3(kEvictThreads), 0, s, p)
+                                    : launch_pdl(evict_kernel<16>, grid, dim3(kEvictThreads), 0, s, p);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
