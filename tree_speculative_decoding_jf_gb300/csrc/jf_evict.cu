@@ -27,6 +27,8 @@ constexpr int kSelMost = 200 * 1024 / 4;  // keys that fit on chip; longer slice
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kSelList = 1024;            // listed keys of a row
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kForced = 0xffffffffu; // above every weight's key
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   uint32_t u = __float_as_uint(w);
@@ -41,10 +43,10 @@ __device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
   return v;
 }
 
-template <bool ONE>   // a cluster of one CTA
-__global__ void __launch_bounds__(kSelThreads, 2)
+template <bool ONE, bool RESIDENT>   // a cluster of one CTA; slices fit on chip
+__global__ void __launch_bounds__(kSelThreads, 3)
     select_kernel(const float* __restrict__ weight, const int32_t* __restrict__ seq_len, int Hkv,
-                  int cap, int sink, int recent, int budget, int C, int resident,
+                  int cap, int sink, int recent, int budget, int C,
                   int32_t* __restrict__ keep, int32_t* __restrict__ kept_len, int32_t* dev_err) {
   extern __shared__ uint32_t s_keys[];                      // this CTA's slice
   __shared__ uint32_t s_hist[2][kBins];                     // this CTA's counts (two rounds' in turn)
@@ -63,9 +65,17 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     if constexpr (ONE) __syncthreads();
     else cluster_sync();
   };
-  auto peer = [&](const uint32_t* local, int r) -> uint32_t {
-    if constexpr (ONE) return *local;
-    else return dsmem_ld_u32(dsmem_addr(local, r));
+  // The word in every CTA of the row (0 past the last), all on their way at once.
+  auto peers = [&](const uint32_t* local, uint32_t (&v)[kMaxCluster], uint32_t none) {
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      v[r] = none;
+      if constexpr (ONE) {
+        if (r == 0) v[r] = *local;
+      } else {
+        if (r < C) v[r] = dsmem_ld_u32(dsmem_addr(local, r));
+      }
+    }
   };
   int L = seq_len[b];
   if (L < 0 || L > cap) {
@@ -84,19 +94,25 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   const int per = ((L + C - 1) / C + 31) & ~31;             // slice of this CTA
   const int t_lo = min(L, rank * per), t_hi = min(L, t_lo + per);
   const int c_lo = max(t_lo, min(sink, t_hi)), c_hi = max(c_lo, min(t_hi, L - recent));   // its competing part
-  auto key_of = [&](int t) -> uint32_t { return resident ? s_keys[t - t_lo] : weight_key(w[t]); };
+  // Keys that stay whatever they are (the first `sink`, the last `recent`) count as kForced.
+  // Positions below are offsets in the slice.
+  const int n_slice = t_hi - t_lo, e_lo = c_lo - t_lo, e_hi = c_hi - t_lo;
+  const float* ws = w + t_lo;
+  auto key_of = [&](int e) -> uint32_t {
+    if constexpr (RESIDENT) return s_keys[e];
+    else return e >= e_lo && e < e_hi ? weight_key(ws[e]) : kForced;
+  };
 
   // ---- the slice, and the range of the competing keys
   if (tid < 2) s_range[tid] = tid == 0 ? 0xffffffffu : 0u;
   uint32_t kmin = 0xffffffffu, kmax = 0u;
 #pragma unroll 8
-  for (int t = t_lo + tid; t < t_hi; t += kSelThreads) {
-    const uint32_t k = weight_key(w[t]);
-    if (resident) s_keys[t - t_lo] = k;
-    if (t >= c_lo && t < c_hi) {
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
-    }
+  for (int e = tid; e < n_slice; e += kSelThreads) {
+    uint32_t k = weight_key(ws[e]);
+    const bool in = e >= e_lo && e < e_hi;
+    kmin = min(kmin, in ? k : 0xffffffffu);
+    kmax = max(kmax, in ? k : 0u);
+    if constexpr (RESIDENT) s_keys[e] = in ? k : kForced;
   }
   for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0u;
   kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -107,24 +123,27 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     atomicMax(&s_range[1], kmax);
   }
   row_sync();
-  for (int r = 0; r < C; ++r) {
-    kmin = min(kmin, peer(&s_range[0], r));
-    kmax = max(kmax, peer(&s_range[1], r));
-  }
+  uint32_t from[kMaxCluster];
+  peers(&s_range[0], from, 0xffffffffu);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) kmin = min(kmin, from[r]);
+  peers(&s_range[1], from, 0u);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) kmax = max(kmax, from[r]);
 
   // ---- kept: keys above lo + last; of the keys lo .. lo + last (the step), `need`
   uint32_t lo = kmin, last = kmax - kmin, need = want;
   int shift = max(0, 32 - __clz(last) - kBinBits);
   bool listed = false;
-  if (want == 0u) {                       // nothing that competes stays
-    lo = 0xffffffffu;
+  if (want == 0u) {                       // nothing that competes stays: the step is empty
+    lo = kForced - 1u;
     last = 0u;
   }
   for (int round = 0; want > 0u; ++round) {
     uint32_t* hist = s_hist[round & 1];
 #pragma unroll 4
-    for (int t = c_lo + tid; t < c_hi; t += kSelThreads) {
-      const uint32_t d = key_of(t) - lo;
+    for (int e = e_lo + tid; e < e_hi; e += kSelThreads) {
+      const uint32_t d = key_of(e) - lo;
       if (d <= last) atomicAdd(&hist[d >> shift], 1u);
     }
     row_sync();
@@ -132,10 +151,12 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     // highest.
     const int top = kBins - 1 - 2 * tid;
     uint32_t c0 = 0u, c1 = 0u;
-    for (int r = 0; r < C; ++r) {
-      c0 += peer(&hist[top], r);
-      c1 += peer(&hist[top - 1], r);
-    }
+    peers(&hist[top], from, 0u);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) c0 += from[r];
+    peers(&hist[top - 1], from, 0u);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) c1 += from[r];
     for (int i = tid; i < kBins; i += kSelThreads) s_hist[(round & 1) ^ 1][i] = 0u;   // (read by nobody now)
     uint32_t incl = c0 + c1;
 #pragma unroll
@@ -166,25 +187,20 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   }
 
   // ---- counts: forced keys and keys above the step, keys in it; the latter listed
-  const int seg = ((t_hi - t_lo + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int seg_lo = min(t_hi, t_lo + warp * seg), seg_hi = min(t_hi, seg_lo + seg);
-  auto forced = [&](int t) -> bool { return t < c_lo || t >= c_hi; };
+  const int seg = ((n_slice + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int seg_lo = min(n_slice, warp * seg), seg_hi = min(n_slice, seg_lo + seg);
+  const uint32_t hi = lo + last;
   if (tid == 0) s_count[2] = 0u;
   __syncthreads();
   uint32_t n_above = 0u, n_in = 0u;
+  const uint32_t not_first = 0xffffffffu - static_cast<uint32_t>(t_lo);   // ~position of offset 0
 #pragma unroll 4
-  for (int t = seg_lo + lane; t < seg_hi; t += 32) {
-    if (forced(t)) {
-      ++n_above;
-      continue;
-    }
-    const uint32_t k = key_of(t);
-    if (k < lo) continue;
-    if (k - lo > last) {
-      ++n_above;
-    } else if (want > 0u) {
+  for (int e = seg_lo + lane; e < seg_hi; e += 32) {
+    const uint32_t k = key_of(e);
+    n_above += k > hi;
+    if (k - lo <= last) {
       ++n_in;
-      if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t));
+      if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(k) << 32) | (not_first - static_cast<uint32_t>(e));
     }
   }
   n_above = __reduce_add_sync(0xffffffffu, n_above);
@@ -196,74 +212,76 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   __syncthreads();
   if (tid < 2) {
     uint32_t v = 0u;
+#pragma unroll
     for (int i = 0; i < kSelWarps; ++i) v += s_warp[tid][i];
     s_count[tid] = v;
   }
   row_sync();
-  uint32_t at = 0u, in_before = 0u, all = 0u;               // kept and in-step keys of earlier CTAs
-  for (int r = 0; r < C; ++r) {
-    const uint32_t a = peer(&s_count[0], r), n = peer(&s_count[1], r);
-    if (r < rank) {
-      at += a;
-      in_before += n;
-    }
-    if (listed) {                         // the row's list, in any order
-      for (uint32_t i = tid; i < n; i += kSelThreads) {
-        const uint32_t* e = reinterpret_cast<const uint32_t*>(&s_list[i]);
-        reinterpret_cast<uint32_t*>(&s_all[all + i])[0] = peer(e, r);
-        reinterpret_cast<uint32_t*>(&s_all[all + i])[1] = peer(e + 1, r);
-      }
-    }
-    all += n;
-  }
+  uint32_t at = 0u, in_before = 0u;       // kept and in-step keys before this warp's segment
+  peers(&s_count[0], from, 0u);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < rank) at += from[r];
+  peers(&s_count[1], from, 0u);
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < rank) in_before += from[r];
   for (int v = 0; v < warp; ++v) {
     at += s_warp[0][v];
     in_before += s_warp[1][v];
   }
   uint64_t cut = ~0ull;
   if (listed) {                           // the step's keys that stay: `cut` and what ranks before it
+    uint32_t all = 0u;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      for (uint32_t i = tid; i < from[r]; i += kSelThreads) {
+        if constexpr (ONE) {
+          s_all[all + i] = s_list[i];
+        } else {
+          const uint32_t* e = reinterpret_cast<const uint32_t*>(&s_list[i]);
+          const uint32_t a = dsmem_ld_u32(dsmem_addr(e, r)), c = dsmem_ld_u32(dsmem_addr(e + 1, r));
+          s_all[all + i] = (static_cast<uint64_t>(c) << 32) | a;
+        }
+      }
+      all += from[r];
+    }
     __syncthreads();
-    for (uint32_t i = tid; i < all; i += kSelThreads) {
+    for (uint32_t i = warp; i < all; i += kSelWarps) {
       const uint64_t e = s_all[i];
       uint32_t before = 0u;
-#pragma unroll 8
-      for (uint32_t j = 0; j < all; ++j) before += s_all[j] > e;
-      if (before == need - 1u) s_cut = e;
+      for (uint32_t j = lane; j < all; j += 32) before += s_all[j] > e;
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (before == need - 1u && lane == 0) s_cut = e;
     }
     __syncthreads();
     cut = s_cut;
     uint32_t n = 0u;
     for (uint32_t i = lane; i < all; i += 32) {
       const uint64_t e = s_all[i];
-      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(seg_lo);
+      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(t_lo + seg_lo);
     }
     at += __reduce_add_sync(0xffffffffu, n);
   } else {                                // one value: the first by position stay
     at += min(need, in_before);
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int t0 = seg_lo; t0 < seg_hi; t0 += 32) {
-    const int t = t0 + lane;
-    bool stay = false, in = false;
-    if (t < seg_hi) {
-      if (forced(t)) {
-        stay = true;
-      } else {
-        const uint32_t k = key_of(t);
-        if (k >= lo) {
-          in = want > 0u && k - lo <= last;
-          stay = in ? listed && ((static_cast<uint64_t>(k) << 32) | (0xffffffffu - static_cast<uint32_t>(t))) >= cut
-                    : k - lo > last;
-        }
-      }
-    }
-    if (!listed) {
-      const uint32_t mi = __ballot_sync(0xffffffffu, in);
-      if (in) stay = in_before + __popc(mi & below) < need;
+#pragma unroll 4
+  for (int e0 = seg_lo; e0 < seg_hi; e0 += 32) {
+    const int e = e0 + lane;
+    uint32_t k = 0u;                      // (past the end: below everything that stays)
+    bool live = e < seg_hi;
+    if (live) k = key_of(e);
+    bool stay = live && k > hi;
+    const bool in = live && k - lo <= last;
+    const uint32_t mi = __ballot_sync(0xffffffffu, in);
+    if (mi != 0u) {
+      if (listed) stay = stay || (in && ((static_cast<uint64_t>(k) << 32) | (not_first - static_cast<uint32_t>(e))) >= cut);
+      else stay = stay || (in && in_before + __popc(mi & below) < need);
       in_before += __popc(mi);
     }
     const uint32_t ms = __ballot_sync(0xffffffffu, stay);
-    if (stay) out[at + __popc(ms & below)] = t;
+    if (stay) out[at + __popc(ms & below)] = t_lo + e;
     at += __popc(ms);
   }
   grid_dependents_launch();
@@ -437,9 +455,12 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   const int slice = ((capacity + C - 1) / C + 31) & ~31;
   const int resident = slice <= kSelMost;
   const size_t smem = resident ? static_cast<size_t>(slice) * sizeof(uint32_t) : 0;
-  auto* kernel = C == 1 ? select_kernel<true> : select_kernel<false>;
-  static SmemAttr attr1, attr;
-  if (!(C == 1 ? attr1 : attr).ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
+  // (a slice of a single CTA is at most 8192 keys, so it always fits)
+  auto* kernel = C == 1 ? select_kernel<true, true> : resident ? select_kernel<false, true> : select_kernel<false, false>;
+  if (resident) {
+    static SmemAttr attr1, attr;
+    if (!(C == 1 ? attr1 : attr).ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
   cfg.blockDim = dim3(kSelThreads);
@@ -455,7 +476,7 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, weight, seq_len, Hkv, capacity, sink, recent,
-                                           budget, C, resident, keep, kept_len, dev_err);
+                                           budget, C, keep, kept_len, dev_err);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
