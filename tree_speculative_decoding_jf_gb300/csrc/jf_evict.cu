@@ -18,21 +18,26 @@ constexpr int kPage = 16;
 // read once.  The smallest kept key is found by counting: the keys' range is cut into 1024
 // steps, and the step that holds the wanted rank usually holds few enough keys to list and
 // rank directly; otherwise it becomes the next range, down to one value (2^32 in four
-// counts), of which the first by position stay.  What bounds the call is the number of such
-// row-wide steps and their barriers, not the 8 bytes a key.
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelSlice = 8192;           // keys of a CTA's slice, while a cluster of 8 suffices
+// counts), of which the first by position stay.
+//
+// What bounds the call is not the 8 bytes a key but the instructions a key (four passes over
+// shared memory, four keys at a time) and, for few rows, the barriers between the steps.
+// Keys that stay whatever they are (the first `sink`, the last `recent`) become kForced,
+// above every weight, and the padding 0, below every one, so no pass tests positions.
+constexpr int kSelSlice = 8192;           // keys of a CTA's slice with 512 threads, ..
+constexpr int kSelSliceMany = 32768;      // .. with 1024
 constexpr int kSelMost = 200 * 1024 / 4;  // keys that fit on chip; longer slices are read again
+constexpr int kSelPad = 128;              // a slice fills whole 128-key runs of a warp
 constexpr int kBinBits = 10;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kSelList = 1024;            // listed keys of a row
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kForced = 0xffffffffu; // above every weight's key
+constexpr uint32_t kNone = 0u;            // below every weight's key
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   uint32_t u = __float_as_uint(w);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;           // NaN: below everything
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 1u;           // NaN: below every number
   if (u == 0x80000000u) u = 0u;                             // -0 == +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -43,16 +48,18 @@ __device__ __forceinline__ uint32_t dsmem_ld_u32(uint32_t addr) {
   return v;
 }
 
-template <bool ONE, bool RESIDENT>   // a cluster of one CTA; slices fit on chip
-__global__ void __launch_bounds__(kSelThreads, 3)
+// ONE: a cluster of one CTA; RESIDENT: the slices fit on chip.
+template <int THREADS, bool ONE, bool RESIDENT>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
     select_kernel(const float* __restrict__ weight, const int32_t* __restrict__ seq_len, int Hkv,
-                  int cap, int sink, int recent, int budget, int C,
-                  int32_t* __restrict__ keep, int32_t* __restrict__ kept_len, int32_t* dev_err) {
-  extern __shared__ uint32_t s_keys[];                      // this CTA's slice
+                  int cap, int sink, int recent, int budget, int C, int32_t* __restrict__ keep,
+                  int32_t* __restrict__ kept_len, int32_t* dev_err) {
+  constexpr int kWarps = THREADS / 32, kMine = kBins / THREADS;
+  extern __shared__ uint4 s_keys[];                         // this CTA's slice, four keys each
   __shared__ uint32_t s_hist[2][kBins];                     // this CTA's counts (two rounds' in turn)
   __shared__ uint32_t s_range[2];                           // min, max of this CTA
   __shared__ uint32_t s_count[3];                           // above the step, in it, listed (this CTA)
-  __shared__ uint32_t s_warp[2][kSelWarps];
+  __shared__ uint32_t s_warp[2][kWarps];
   __shared__ uint32_t s_bin[3];                             // the step, keys above it, keys in it
   __shared__ uint64_t s_list[kSelList];                     // key << 32 | ~position, this CTA's
   __shared__ uint64_t s_all[kSelList];                      // the row's
@@ -65,15 +72,16 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     if constexpr (ONE) __syncthreads();
     else cluster_sync();
   };
-  // The word in every CTA of the row (0 past the last), all on their way at once.
-  auto peers = [&](const uint32_t* local, uint32_t (&v)[kMaxCluster], uint32_t none) {
+  // The word in every CTA of the row (`none` past the last), all on their way at once.
+  uint32_t from[kMaxCluster];
+  auto peers = [&](const uint32_t* local, uint32_t none) {
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
-      v[r] = none;
+      from[r] = none;
       if constexpr (ONE) {
-        if (r == 0) v[r] = *local;
+        if (r == 0) from[r] = *local;
       } else {
-        if (r < C) v[r] = dsmem_ld_u32(dsmem_addr(local, r));
+        if (r < C) from[r] = dsmem_ld_u32(dsmem_addr(local, r));
       }
     }
   };
@@ -85,36 +93,54 @@ __global__ void __launch_bounds__(kSelThreads, 3)
   int32_t* out = keep + static_cast<size_t>(row) * budget;
   if (tid == 0 && rank == 0 && row % Hkv == 0) kept_len[b] = min(L, budget);
   if (L <= budget) {                      // everything stays
-    for (int j = rank * kSelThreads + tid; j < budget; j += C * kSelThreads) out[j] = j < L ? j : -1;
+    for (int j = rank * THREADS + tid; j < budget; j += C * THREADS) out[j] = j < L ? j : -1;
     grid_dependents_launch();
     return;
   }
-  const float* w = weight + static_cast<size_t>(row) * cap;
   const uint32_t want = static_cast<uint32_t>(budget - sink - recent);   // of the keys that compete
-  const int per = ((L + C - 1) / C + 31) & ~31;             // slice of this CTA
-  const int t_lo = min(L, rank * per), t_hi = min(L, t_lo + per);
-  const int c_lo = max(t_lo, min(sink, t_hi)), c_hi = max(c_lo, min(t_hi, L - recent));   // its competing part
-  // Keys that stay whatever they are (the first `sink`, the last `recent`) count as kForced.
-  // Positions below are offsets in the slice.
-  const int n_slice = t_hi - t_lo, e_lo = c_lo - t_lo, e_hi = c_hi - t_lo;
-  const float* ws = w + t_lo;
-  auto key_of = [&](int e) -> uint32_t {
-    if constexpr (RESIDENT) return s_keys[e];
-    else return e >= e_lo && e < e_hi ? weight_key(ws[e]) : kForced;
+  const int per = ((L + C - 1) / C + kSelPad - 1) / kSelPad * kSelPad;   // slice of this CTA
+  const int t_lo = min(L, rank * per), n_slice = min(L, t_lo + per) - t_lo;
+  const int c_lo = sink - t_lo, c_hi = L - recent - t_lo;   // its competing part, as offsets
+  const float* ws = weight + static_cast<size_t>(row) * cap + t_lo;
+  auto load_key = [&](int e) -> uint32_t {
+    if (e >= n_slice) return kNone;
+    return e >= c_lo && e < c_hi ? weight_key(ws[e]) : kForced;
   };
+  auto load4 = [&](int i) -> uint4 {
+    return make_uint4(load_key(4 * i), load_key(4 * i + 1), load_key(4 * i + 2), load_key(4 * i + 3));
+  };
+  auto keys4 = [&](int i) -> uint4 {
+    if constexpr (RESIDENT) return s_keys[i];
+    else return load4(i);
+  };
+  // Runs of 128 keys, which the warps take in order.
+  const int runs = (n_slice + kSelPad - 1) / kSelPad, vecs = runs * (kSelPad / 4);
 
   // ---- the slice, and the range of the competing keys
   if (tid < 2) s_range[tid] = tid == 0 ? 0xffffffffu : 0u;
   uint32_t kmin = 0xffffffffu, kmax = 0u;
-#pragma unroll 8
-  for (int e = tid; e < n_slice; e += kSelThreads) {
-    uint32_t k = weight_key(ws[e]);
-    const bool in = e >= e_lo && e < e_hi;
-    kmin = min(kmin, in ? k : 0xffffffffu);
-    kmax = max(kmax, in ? k : 0u);
-    if constexpr (RESIDENT) s_keys[e] = in ? k : kForced;
+  const bool wide = (reinterpret_cast<uintptr_t>(ws) & 15u) == 0;
+#pragma unroll 4
+  for (int i = tid; i < vecs; i += THREADS) {
+    uint4 k;
+    if (wide && 4 * i >= c_lo && 4 * i + 4 <= min(c_hi, n_slice)) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(ws) + i);
+      k = make_uint4(weight_key(f.x), weight_key(f.y), weight_key(f.z), weight_key(f.w));
+      kmin = min(min(kmin, min(k.x, k.y)), min(k.z, k.w));
+      kmax = max(max(kmax, max(k.x, k.y)), max(k.z, k.w));
+    } else {
+      k = load4(i);
+      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e[c] != kForced && e[c] != kNone) {
+          kmin = min(kmin, e[c]);
+          kmax = max(kmax, e[c]);
+        }
+    }
+    if constexpr (RESIDENT) s_keys[i] = k;
   }
-  for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0u;
+  for (int i = tid; i < kBins; i += THREADS) s_hist[0][i] = 0u;
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   __syncthreads();
@@ -123,11 +149,10 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     atomicMax(&s_range[1], kmax);
   }
   row_sync();
-  uint32_t from[kMaxCluster];
-  peers(&s_range[0], from, 0xffffffffu);
+  peers(&s_range[0], 0xffffffffu);
 #pragma unroll
   for (int r = 0; r < kMaxCluster; ++r) kmin = min(kmin, from[r]);
-  peers(&s_range[1], from, 0u);
+  peers(&s_range[1], 0u);
 #pragma unroll
   for (int r = 0; r < kMaxCluster; ++r) kmax = max(kmax, from[r]);
 
@@ -141,24 +166,33 @@ __global__ void __launch_bounds__(kSelThreads, 3)
   }
   for (int round = 0; want > 0u; ++round) {
     uint32_t* hist = s_hist[round & 1];
-#pragma unroll 4
-    for (int e = e_lo + tid; e < e_hi; e += kSelThreads) {
-      const uint32_t d = key_of(e) - lo;
+    auto tally = [&](uint32_t k) {
+      const uint32_t d = k - lo;
       if (d <= last) atomicAdd(&hist[d >> shift], 1u);
+    };
+#pragma unroll 2
+    for (int i = tid; i < vecs; i += THREADS) {
+      const uint4 k = keys4(i);
+      tally(k.x);
+      tally(k.y);
+      tally(k.z);
+      tally(k.w);
     }
     row_sync();
-    // The step where the count from above reaches `need`: two steps a thread, thread 0 the
+    // The step where the count from above reaches `need`: kMine steps a thread, thread 0 the
     // highest.
-    const int top = kBins - 1 - 2 * tid;
-    uint32_t c0 = 0u, c1 = 0u;
-    peers(&hist[top], from, 0u);
+    const int top = kBins - 1 - kMine * tid;
+    uint32_t c[kMine], mine = 0u;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) c0 += from[r];
-    peers(&hist[top - 1], from, 0u);
+    for (int i = 0; i < kMine; ++i) {
+      c[i] = 0u;
+      peers(&hist[top - i], 0u);
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) c1 += from[r];
-    for (int i = tid; i < kBins; i += kSelThreads) s_hist[(round & 1) ^ 1][i] = 0u;   // (read by nobody now)
-    uint32_t incl = c0 + c1;
+      for (int r = 0; r < kMaxCluster; ++r) c[i] += from[r];
+      mine += c[i];
+    }
+    for (int i = tid; i < kBins; i += THREADS) s_hist[(round & 1) ^ 1][i] = 0u;   // (read by nobody now)
+    uint32_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -166,16 +200,16 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     }
     if (lane == 31) s_warp[0][warp] = incl;
     __syncthreads();
-    uint32_t above = incl - c0 - c1;
+    uint32_t above = incl - mine;
     for (int v = 0; v < warp; ++v) above += s_warp[0][v];
-    if (above < need && above + c0 >= need) {
-      s_bin[0] = top;
-      s_bin[1] = above;
-      s_bin[2] = c0;
-    } else if (above + c0 < need && above + c0 + c1 >= need) {
-      s_bin[0] = top - 1;
-      s_bin[1] = above + c0;
-      s_bin[2] = c1;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (above < need && above + c[i] >= need) {
+        s_bin[0] = top - i;
+        s_bin[1] = above;
+        s_bin[2] = c[i];
+      }
+      above += c[i];
     }
     __syncthreads();
     need -= s_bin[1];
@@ -187,20 +221,25 @@ __global__ void __launch_bounds__(kSelThreads, 3)
   }
 
   // ---- counts: forced keys and keys above the step, keys in it; the latter listed
-  const int seg = ((n_slice + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int seg_lo = min(n_slice, warp * seg), seg_hi = min(n_slice, seg_lo + seg);
+  const int per_warp = (runs + kWarps - 1) / kWarps;
+  const int v_lo = min(runs, warp * per_warp) * 32, v_hi = min(runs, (warp + 1) * per_warp) * 32;
   const uint32_t hi = lo + last;
+  const uint32_t not_first = 0xffffffffu - static_cast<uint32_t>(t_lo);   // ~position of offset 0
   if (tid == 0) s_count[2] = 0u;
   __syncthreads();
   uint32_t n_above = 0u, n_in = 0u;
-  const uint32_t not_first = 0xffffffffu - static_cast<uint32_t>(t_lo);   // ~position of offset 0
-#pragma unroll 4
-  for (int e = seg_lo + lane; e < seg_hi; e += 32) {
-    const uint32_t k = key_of(e);
-    n_above += k > hi;
-    if (k - lo <= last) {
-      ++n_in;
-      if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(k) << 32) | (not_first - static_cast<uint32_t>(e));
+#pragma unroll 2
+  for (int i = v_lo + lane; i < v_hi; i += 32) {
+    const uint4 k = keys4(i);
+    n_above += (k.x > hi) + (k.y > hi) + (k.z > hi) + (k.w > hi);
+    if (k.x - lo <= last || k.y - lo <= last || k.z - lo <= last || k.w - lo <= last) {
+      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e[c] - lo <= last) {
+          ++n_in;
+          if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(e[c]) << 32) | (not_first - static_cast<uint32_t>(4 * i + c));
+        }
     }
   }
   n_above = __reduce_add_sync(0xffffffffu, n_above);
@@ -213,16 +252,16 @@ __global__ void __launch_bounds__(kSelThreads, 3)
   if (tid < 2) {
     uint32_t v = 0u;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) v += s_warp[tid][i];
+    for (int i = 0; i < kWarps; ++i) v += s_warp[tid][i];
     s_count[tid] = v;
   }
   row_sync();
-  uint32_t at = 0u, in_before = 0u;       // kept and in-step keys before this warp's segment
-  peers(&s_count[0], from, 0u);
+  uint32_t at = 0u, in_before = 0u;       // kept and in-step keys before this warp's runs
+  peers(&s_count[0], 0u);
 #pragma unroll
   for (int r = 0; r < kMaxCluster; ++r)
     if (r < rank) at += from[r];
-  peers(&s_count[1], from, 0u);
+  peers(&s_count[1], 0u);
 #pragma unroll
   for (int r = 0; r < kMaxCluster; ++r)
     if (r < rank) in_before += from[r];
@@ -235,7 +274,7 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     uint32_t all = 0u;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
-      for (uint32_t i = tid; i < from[r]; i += kSelThreads) {
+      for (uint32_t i = tid; i < from[r]; i += THREADS) {
         if constexpr (ONE) {
           s_all[all + i] = s_list[i];
         } else {
@@ -247,7 +286,7 @@ __global__ void __launch_bounds__(kSelThreads, 3)
       all += from[r];
     }
     __syncthreads();
-    for (uint32_t i = warp; i < all; i += kSelWarps) {
+    for (uint32_t i = warp; i < all; i += kWarps) {
       const uint64_t e = s_all[i];
       uint32_t before = 0u;
       for (uint32_t j = lane; j < all; j += 32) before += s_all[j] > e;
@@ -259,30 +298,52 @@ __global__ void __launch_bounds__(kSelThreads, 3)
     uint32_t n = 0u;
     for (uint32_t i = lane; i < all; i += 32) {
       const uint64_t e = s_all[i];
-      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(t_lo + seg_lo);
+      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(t_lo + 4 * v_lo);
     }
     at += __reduce_add_sync(0xffffffffu, n);
   } else {                                // one value: the first by position stay
     at += min(need, in_before);
   }
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int e0 = seg_lo; e0 < seg_hi; e0 += 32) {
-    const int e = e0 + lane;
-    uint32_t k = 0u;                      // (past the end: below everything that stays)
-    bool live = e < seg_hi;
-    if (live) k = key_of(e);
-    bool stay = live && k > hi;
-    const bool in = live && k - lo <= last;
-    const uint32_t mi = __ballot_sync(0xffffffffu, in);
-    if (mi != 0u) {
-      if (listed) stay = stay || (in && ((static_cast<uint64_t>(k) << 32) | (not_first - static_cast<uint32_t>(e))) >= cut);
-      else stay = stay || (in && in_before + __popc(mi & below) < need);
-      in_before += __popc(mi);
+  // ---- the kept positions, in order: a lane's four are consecutive
+#pragma unroll 2
+  for (int i = v_lo + lane; i < v_hi; i += 32) {
+    const uint4 k = keys4(i);
+    const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+    uint32_t stay = 0u, in = 0u;          // a bit a key
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      stay |= static_cast<uint32_t>(e[c] > hi) << c;
+      in |= static_cast<uint32_t>(e[c] - lo <= last) << c;
     }
-    const uint32_t ms = __ballot_sync(0xffffffffu, stay);
-    if (stay) out[at + __popc(ms & below)] = t_lo + e;
-    at += __popc(ms);
+    const uint32_t below = (1u << lane) - 1u;
+    if (__any_sync(0xffffffffu, in != 0u)) {
+      uint32_t before = 0u, all = 0u;     // in-step keys of earlier lanes, of all
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t m = __ballot_sync(0xffffffffu, (in >> c) & 1u);
+        before += __popc(m & below);
+        all += __popc(m);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if ((in >> c) & 1u) {
+          const uint64_t x = (static_cast<uint64_t>(e[c]) << 32) | (not_first - static_cast<uint32_t>(4 * i + c));
+          if (listed ? x >= cut : in_before + before < need) stay |= 1u << c;
+          ++before;
+        }
+      in_before += all;
+    }
+    uint32_t to = at, all = 0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t m = __ballot_sync(0xffffffffu, (stay >> c) & 1u);
+      to += __popc(m & below);
+      all += __popc(m);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if ((stay >> c) & 1u) out[to++] = t_lo + 4 * i + c;
+    at += all;
   }
   grid_dependents_launch();
   if constexpr (!ONE) cluster_sync();     // nobody leaves while its lists may be read
@@ -448,23 +509,29 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * Hkv;
-  // The smallest cluster whose slices stay at kSelSlice keys; with few rows, more CTAs a row
-  // while the machine has room for them.
+  // With rows for half the SMs or more, a row is one CTA of 1024 threads while it fits (44 us
+  // against 61 us in clusters of four on 256 rows of 32K: no exchange between CTAs, fewer
+  // barriers a key).  With fewer rows, 512 threads and the smallest cluster whose slices
+  // stay at kSelSlice keys, or more CTAs while the machine has room for them.
+  const bool many = rows * 2 >= sms;
+  const int slice_most = many ? kSelSliceMany : kSelSlice;
   int C = 1;
-  while (C < 8 && (capacity > C * kSelSlice || (rows * C * 2 <= sms && capacity > C * 2048))) C *= 2;
-  const int slice = ((capacity + C - 1) / C + 31) & ~31;
-  const int resident = slice <= kSelMost;
-  const size_t smem = resident ? static_cast<size_t>(slice) * sizeof(uint32_t) : 0;
-  // (a slice of a single CTA is at most 8192 keys, so it always fits)
-  auto* kernel = C == 1 ? select_kernel<true, true> : resident ? select_kernel<false, true> : select_kernel<false, false>;
+  while (C < kMaxCluster && (capacity > C * slice_most || (!many && rows * C * 2 <= sms && capacity > C * 2048))) C *= 2;
+  const int slice = ((capacity + C - 1) / C + kSelPad - 1) / kSelPad * kSelPad;
+  const bool resident = slice <= kSelMost;
+  // (a slice of a single CTA always fits)
+  auto* kernel = many ? (C == 1 ? select_kernel<1024, true, true> : resident ? select_kernel<1024, false, true>
+                                                                            : select_kernel<1024, false, false>)
+                      : (C == 1 ? select_kernel<512, true, true> : resident ? select_kernel<512, false, true>
+                                                                           : select_kernel<512, false, false>);
   if (resident) {
-    static SmemAttr attr1, attr;
-    if (!(C == 1 ? attr1 : attr).ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
+    static SmemAttr attr[4];
+    if (!attr[(many ? 2 : 0) + (C == 1 ? 1 : 0)].ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(many ? 1024 : 512);
+  cfg.dynamicSmemBytes = resident ? static_cast<size_t>(slice) * sizeof(uint32_t) : 0;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
