@@ -103,7 +103,7 @@ def _load():
     lib.jf_tree_verify_sampled_packed.restype = ctypes.c_int
     lib.jf_attention_weight.argtypes = [P, P, P, P, P, P, P, P] + [i32] * 8 + [f32, P, P, P]
     lib.jf_attention_weight.restype = ctypes.c_int
-    lib.jf_attention_weight_packed.argtypes = [P, P, P, P, P, P, P, P, P] + [i32] * 9 + [f32, P, P, P]
+    lib.jf_attention_weight_packed.argtypes = [P] * 9 + [i32] * 9 + [f32, P, P, P]
     lib.jf_attention_weight_packed.restype = ctypes.c_int
     lib.jf_select_kept.argtypes = [P, P] + [i32] * 6 + [P, P, P, P]
     lib.jf_select_kept.restype = ctypes.c_int
@@ -632,20 +632,35 @@ def jf_build_draft_tree_ragged(draft_logits, K, N, budget, cand_token, cand_logp
         _ptr(dev_err), _stream(stream)))
 
 
-def _need_all(dtype_shapes, dev_err=None):
-    """Checks of the cache and beam calls: _need for each (name, tensor, dtype, shape) whose
-    tensor is given, and one device, the current one, for all of them."""
-    cur = torch.cuda.current_device()
-    for name, t, dtype, shape in dtype_shapes:
+def _on_stream(specs, dev_err, stream) -> int:
+    """Checks of the cache and beam calls, quick where all is well: (name, tensor, dtype,
+    shape) of every tensor given, and one device, the current one, for all of them (an error
+    says what _need says).  Returns the stream's handle."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+        cur = stream.device_index
+    else:
+        cur = torch.cuda.current_device()
+    for name, t, dtype, shape in specs:
         if t is None:
             continue
-        _need(t, name, dtype, shape)
-        if t.device.index != cur:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{cur}")
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and
+                t.is_contiguous() and (shape is None or t.shape == shape)):
+            _need(t, name, dtype, shape)
+        if t.get_device() != cur:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{cur}")
     if dev_err is not None:
         _need(dev_err, "dev_err", torch.int32, (1,))
-        if dev_err.device.index != cur:
-            raise ValueError(f"dev_err is on cuda:{dev_err.device.index}, the current device is cuda:{cur}")
+        if dev_err.get_device() != cur:
+            raise ValueError(f"dev_err is on cuda:{dev_err.get_device()}, the current device "
+                             f"is cuda:{cur}")
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t):
+    """Address of an optional tensor for a call whose arguments are declared as pointers."""
+    return None if t is None else t.data_ptr()
 
 
 def jf_attention_weight(q, k_cache, block_table, prefix_len, lse, weight_out, scale, path=None,
@@ -657,17 +672,17 @@ def jf_attention_weight(q, k_cache, block_table, prefix_len, lse, weight_out, sc
     if D2 != D:
         raise ValueError("q and k_cache head dims differ")
     wshape = (B, Hkv, max_pages * page)
-    _need_all((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
-               ("block_table", block_table, torch.int32, (B, max_pages)),
-               ("prefix_len", prefix_len, torch.int32, (B,)),
-               ("lse", lse, torch.float32, (B, Hq, N)), ("path", path, torch.int32, (B, N)),
-               ("accept_len", accept_len, torch.int32, (B,)),
-               ("weight", weight, torch.float32, wshape),
-               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+                     ("block_table", block_table, torch.int32, (B, max_pages)),
+                     ("prefix_len", prefix_len, torch.int32, (B,)),
+                     ("lse", lse, torch.float32, (B, Hq, N)), ("path", path, torch.int32, (B, N)),
+                     ("accept_len", accept_len, torch.int32, (B,)),
+                     ("weight", weight, torch.float32, wshape),
+                     ("weight_out", weight_out, torch.float32, wshape)), dev_err, stream)
     _check("jf_attention_weight", _lib.jf_attention_weight(
-        _ptr(q), _ptr(k_cache), _ptr(block_table), _ptr(prefix_len), _ptr(path), _ptr(accept_len),
-        _ptr(lse), _ptr(weight), B, N, Hq, Hkv, D, page, max_pages, num_pages, float(scale),
-        _ptr(weight_out), _ptr(dev_err), _stream(stream)))
+        _at(q), _at(k_cache), _at(block_table), _at(prefix_len), _at(path), _at(accept_len),
+        _at(lse), _at(weight), B, N, Hq, Hkv, D, page, max_pages, num_pages, float(scale),
+        _at(weight_out), _at(dev_err), on))
 
 
 def jf_attention_weight_packed(q, k_cache, block_table, prefix_len, cu_seqlens, lse, weight_out,
@@ -680,18 +695,18 @@ def jf_attention_weight_packed(q, k_cache, block_table, prefix_len, cu_seqlens, 
     if D2 != D:
         raise ValueError("q and k_cache head dims differ")
     wshape = (B, Hkv, max_pages * page)
-    _need_all((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
-               ("block_table", block_table, torch.int32, None),
-               ("prefix_len", prefix_len, torch.int32, (B,)),
-               ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)),
-               ("lse", lse, torch.float32, (Hq, T)), ("path", path, torch.int32, (B, N_max)),
-               ("accept_len", accept_len, torch.int32, (B,)),
-               ("weight", weight, torch.float32, wshape),
-               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+                     ("block_table", block_table, torch.int32, None),
+                     ("prefix_len", prefix_len, torch.int32, (B,)),
+                     ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)),
+                     ("lse", lse, torch.float32, (Hq, T)), ("path", path, torch.int32, (B, N_max)),
+                     ("accept_len", accept_len, torch.int32, (B,)),
+                     ("weight", weight, torch.float32, wshape),
+                     ("weight_out", weight_out, torch.float32, wshape)), dev_err, stream)
     _check("jf_attention_weight_packed", _lib.jf_attention_weight_packed(
-        _ptr(q), _ptr(k_cache), _ptr(block_table), _ptr(prefix_len), _ptr(cu_seqlens), _ptr(path),
-        _ptr(accept_len), _ptr(lse), _ptr(weight), B, N_max, T, Hq, Hkv, D, page, max_pages,
-        num_pages, float(scale), _ptr(weight_out), _ptr(dev_err), _stream(stream)))
+        _at(q), _at(k_cache), _at(block_table), _at(prefix_len), _at(cu_seqlens), _at(path),
+        _at(accept_len), _at(lse), _at(weight), B, N_max, T, Hq, Hkv, D, page, max_pages,
+        num_pages, float(scale), _at(weight_out), _at(dev_err), on))
 
 
 def jf_select_kept(weight, seq_len, keep, kept_len, sink=0, recent=0, dev_err=None,
@@ -699,12 +714,13 @@ def jf_select_kept(weight, seq_len, keep, kept_len, sink=0, recent=0, dev_err=No
     """The positions a cache of keep.shape[-1] keys keeps (see include/jf.h)."""
     B, Hkv, capacity = weight.shape
     budget = keep.shape[-1]
-    _need_all((("weight", weight, torch.float32, None), ("seq_len", seq_len, torch.int32, (B,)),
-               ("keep", keep, torch.int32, (B, Hkv, budget)),
-               ("kept_len", kept_len, torch.int32, (B,))), dev_err)
+    on = _on_stream((("weight", weight, torch.float32, None),
+                     ("seq_len", seq_len, torch.int32, (B,)),
+                     ("keep", keep, torch.int32, (B, Hkv, budget)),
+                     ("kept_len", kept_len, torch.int32, (B,))), dev_err, stream)
     _check("jf_select_kept", _lib.jf_select_kept(
-        _ptr(weight), _ptr(seq_len), B, Hkv, capacity, int(sink), int(recent), budget, _ptr(keep),
-        _ptr(kept_len), _ptr(dev_err), _stream(stream)))
+        _at(weight), _at(seq_len), B, Hkv, capacity, int(sink), int(recent), budget, _at(keep),
+        _at(kept_len), _at(dev_err), on))
 
 
 def jf_evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_block_table=None,
@@ -714,19 +730,19 @@ def jf_evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_bloc
     B, max_pages = block_table.shape
     budget = keep.shape[-1]
     wshape = (B, Hkv, max_pages * page)
-    _need_all((("k_cache", k_cache, torch.bfloat16, None),
-               ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
-               ("block_table", block_table, torch.int32, None),
-               ("seq_len", seq_len, torch.int32, (B,)),
-               ("keep", keep, torch.int32, (B, Hkv, budget)),
-               ("kept_len", kept_len, torch.int32, (B,)),
-               ("new_block_table", new_block_table, torch.int32, (B, max_pages)),
-               ("weight", weight, torch.float32, wshape),
-               ("weight_out", weight_out, torch.float32, wshape)), dev_err)
+    on = _on_stream((("k_cache", k_cache, torch.bfloat16, None),
+                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+                     ("block_table", block_table, torch.int32, None),
+                     ("seq_len", seq_len, torch.int32, (B,)),
+                     ("keep", keep, torch.int32, (B, Hkv, budget)),
+                     ("kept_len", kept_len, torch.int32, (B,)),
+                     ("new_block_table", new_block_table, torch.int32, (B, max_pages)),
+                     ("weight", weight, torch.float32, wshape),
+                     ("weight_out", weight_out, torch.float32, wshape)), dev_err, stream)
     _check("jf_evict_kv", _lib.jf_evict_kv(
-        _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_len), _ptr(keep), _ptr(kept_len),
-        _ptr(new_block_table), _ptr(weight), _ptr(weight_out), B, Hkv, D, budget, page, max_pages,
-        num_pages, _ptr(dev_err), _stream(stream)))
+        _at(k_cache), _at(v_cache), _at(block_table), _at(seq_len), _at(keep), _at(kept_len),
+        _at(new_block_table), _at(weight), _at(weight_out), B, Hkv, D, budget, page, max_pages,
+        num_pages, _at(dev_err), on))
 
 
 def jf_beam_select_workspace_size(B, W, V, K, dtype) -> int:
@@ -742,16 +758,17 @@ def jf_beam_select(logits, score, parent, token, new_score, workspace, finished=
     B, W, V = logits.shape
     K = parent.shape[-1]
     dt = _logit_dtype(logits)
-    _need_all((("logits", logits, logits.dtype, None), ("score", score, torch.float32, (B, W)),
-               ("finished", finished, torch.int32, (B, W)),
-               ("parent", parent, torch.int32, (B, K)), ("token", token, torch.int32, (B, K)),
-               ("new_score", new_score, torch.float32, (B, K)),
-               ("new_finished", new_finished, torch.int32, (B, K)),
-               ("workspace", workspace, torch.uint8, None)))
+    on = _on_stream((("logits", logits, logits.dtype, None),
+                     ("score", score, torch.float32, (B, W)),
+                     ("finished", finished, torch.int32, (B, W)),
+                     ("parent", parent, torch.int32, (B, K)), ("token", token, torch.int32, (B, K)),
+                     ("new_score", new_score, torch.float32, (B, K)),
+                     ("new_finished", new_finished, torch.int32, (B, K)),
+                     ("workspace", workspace, torch.uint8, None)), None, stream)
     _check("jf_beam_select", _lib.jf_beam_select(
-        _ptr(logits), dt, _ptr(score), _ptr(finished), int(eos_token), B, W, V, K, _ptr(parent),
-        _ptr(token), _ptr(new_score), _ptr(new_finished), _ptr(workspace), workspace.numel(),
-        _stream(stream)))
+        _at(logits), dt, _at(score), _at(finished), int(eos_token), B, W, V, K, _at(parent),
+        _at(token), _at(new_score), _at(new_finished), _at(workspace), workspace.numel(),
+        on))
 
 
 def jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page,
@@ -763,18 +780,18 @@ def jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_pag
     if B < 1 or rows % B != 0:
         raise ValueError(f"block_table has {rows} rows, not a multiple of {B} prompts")
     W = rows // B
-    _need_all((("k_cache", k_cache, torch.bfloat16, None),
-               ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
-               ("block_table", block_table, torch.int32, None),
-               ("prefix_len", prefix_len, torch.int32, (B * W,)),
-               ("parent", parent, torch.int32, (B, K)),
-               ("fresh_page", fresh_page, torch.int32, (B, K)),
-               ("new_block_table", new_block_table, torch.int32, (B * K, max_pages)),
-               ("new_prefix_len", new_prefix_len, torch.int32, (B * K,))), dev_err)
+    on = _on_stream((("k_cache", k_cache, torch.bfloat16, None),
+                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+                     ("block_table", block_table, torch.int32, None),
+                     ("prefix_len", prefix_len, torch.int32, (B * W,)),
+                     ("parent", parent, torch.int32, (B, K)),
+                     ("fresh_page", fresh_page, torch.int32, (B, K)),
+                     ("new_block_table", new_block_table, torch.int32, (B * K, max_pages)),
+                     ("new_prefix_len", new_prefix_len, torch.int32, (B * K,))), dev_err, stream)
     _check("jf_beam_fork_kv", _lib.jf_beam_fork_kv(
-        _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(prefix_len), _ptr(parent),
-        _ptr(fresh_page), B, W, K, Hkv, D, page, max_pages, num_pages, _ptr(new_block_table),
-        _ptr(new_prefix_len), _ptr(dev_err), _stream(stream)))
+        _at(k_cache), _at(v_cache), _at(block_table), _at(prefix_len), _at(parent),
+        _at(fresh_page), B, W, K, Hkv, D, page, max_pages, num_pages, _at(new_block_table),
+        _at(new_prefix_len), _at(dev_err), on))
 
 
 # ----------------------------------------------------------------------------- conveniences
@@ -947,11 +964,12 @@ def beam_select(logits, score, K, finished=None, eos_token=-1, stream=None):
     """(parent, token, score, finished), each [B][K]: the K best continuations of every prompt."""
     B, W, V = logits.shape
     dev = logits.device
-    parent = torch.empty((B, K), dtype=torch.int32, device=dev)
-    token = torch.empty((B, K), dtype=torch.int32, device=dev)
+    parent, token, new_finished = torch.empty((3, B, K), dtype=torch.int32, device=dev).unbind(0)
     new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
-    new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
     ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
+    if stream is not None:    # the workspace is given back to the current stream's allocator
+        ws.record_stream(stream if hasattr(stream, "cuda_stream")
+                         else torch.cuda.ExternalStream(int(stream)))
     jf_beam_select(logits, score, parent, token, new_score, ws, finished, eos_token, new_finished,
                    stream)
     return parent, token, new_score, new_finished
