@@ -636,25 +636,21 @@ def _on_stream(specs, dev_err, stream) -> int:
     """Checks of the cache and beam calls, quick where all is well: (name, tensor, dtype,
     shape) of every tensor given, and one device, the current one, for all of them (an error
     says what _need says).  Returns the stream's handle."""
-    if stream is None:
-        stream = torch.cuda.current_stream()
-        cur = stream.device_index
-    else:
-        cur = torch.cuda.current_device()
+    cur = torch.cuda.current_device()
     for name, t, dtype, shape in specs:
         if t is None:
             continue
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cur and
                 t.is_contiguous() and (shape is None or t.shape == shape)):
-            _need(t, name, dtype, shape)
-        if t.get_device() != cur:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{cur}")
+            continue
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
     if dev_err is not None:
         _need(dev_err, "dev_err", torch.int32, (1,))
         if dev_err.get_device() != cur:
-            raise ValueError(f"dev_err is on cuda:{dev_err.get_device()}, the current device "
-                             f"is cuda:{cur}")
+            raise ValueError(f"dev_err is on {dev_err.device}, the current device is cuda:{cur}")
+    if stream is None:        # the handle of torch.cuda.current_stream(), without the object
+        return torch._C._cuda_getCurrentRawStream(cur)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -964,7 +960,9 @@ def beam_select(logits, score, K, finished=None, eos_token=-1, stream=None):
     """(parent, token, score, finished), each [B][K]: the K best continuations of every prompt."""
     B, W, V = logits.shape
     dev = logits.device
-    parent, token, new_finished = torch.empty((3, B, K), dtype=torch.int32, device=dev).unbind(0)
+    parent = torch.empty((B, K), dtype=torch.int32, device=dev)
+    token = torch.empty((B, K), dtype=torch.int32, device=dev)
+    new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
     new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
     ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
     if stream is not None:    # the workspace is given back to the current stream's allocator
