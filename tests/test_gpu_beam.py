@@ -110,6 +110,40 @@ def test_masked_tokens_and_ties(jf, dtype):
         run_beams(jf, logits, score, K, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_logits_of_beams_that_are_not_live_are_not_read(jf, dtype):
+    rng = np.random.default_rng(15)
+    B, W, V, K = 2, 4, 3001, 9
+    logits = 2 * rng.standard_normal((B, W, V))
+    score = -rng.random((B, W)) - 1
+    finished = np.zeros((B, W), np.int32)
+    finished[0, 1] = 1
+    score[1, 2:] = -np.inf
+    t = torch.from_numpy(logits.astype(np.float32)).to(dtype)
+    clean = t.float().numpy().copy()
+    t[0, 1], t[1, 2], t[1, 3] = float("nan"), float("inf"), float("nan")
+    got = jf.beam_select(t.cuda(), dev(score.astype(np.float32)), K, finished=dev(finished), eos_token=5)
+    torch.cuda.synchronize()
+    check_beams(clean, score.astype(np.float32), finished, 5, got, K)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scores_of_every_size(jf, dtype):
+    """Sharp and flat rows, logits and scores far from zero: the fp32 bound of the merge stays
+    below the K-th pair."""
+    rng = np.random.default_rng(16)
+    B, W, V, K = 6, 3, 9001, 12
+    logits = rng.standard_normal((B, W, V))
+    logits[0] *= 30.0                          # almost all probability on one token
+    logits[1] += 60.0
+    logits[2] -= 60.0
+    logits[3] *= 1e-3
+    logits[4, :, 17] = 200.0
+    score = -rng.random((B, W)) * 3
+    score[1], score[5] = score[1] - 300.0, score[5] + 50.0
+    run_beams(jf, logits, score, K, dtype=dtype)
+
+
 def test_unaligned_logits(jf):
     """A logits tensor that starts two bytes past a 16-byte boundary."""
     rng = np.random.default_rng(7)
@@ -120,6 +154,27 @@ def test_unaligned_logits(jf):
     got = jf.beam_select(view, dev(score), K)
     torch.cuda.synchronize()
     check_beams(view.float().cpu().numpy(), score, None, -1, got, K)
+
+
+def test_beams_and_fork_on_a_given_stream(jf):
+    rng = np.random.default_rng(18)
+    logits = dev((2 * rng.standard_normal((3, 4, 20000))).astype(np.float32))
+    score = dev((-rng.random((3, 4))).astype(np.float32))
+    want = jf.beam_select(logits, score, 6)
+    pool, _, fresh = fork_case(3, 3, 4, 6, 2, 64, rng.integers(1, 60, 12), 5)
+    table, lens = dev(pool.table), dev(rng.integers(1, 60, 12).astype(np.int32))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = jf.beam_select(logits, score, 6, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ta, la = jf.beam_fork_kv(pool.k.cuda(), pool.v.cuda(), table, lens, want[0], dev(fresh))
+    torch.cuda.synchronize()
+    k, v = pool.k.cuda(), pool.v.cuda()
+    torch.cuda.synchronize()
+    tb, lb = jf.beam_fork_kv(k, v, table, lens, want[0], dev(fresh), stream=s)
+    s.synchronize()
+    assert torch.equal(ta, tb) and torch.equal(la, lb)
 
 
 def test_beams_in_a_graph(jf):

@@ -246,6 +246,29 @@ def test_weight_on_another_stream_and_in_a_graph(jf):
         assert torch.equal(out, want)
 
 
+def test_calls_on_a_given_stream(jf):
+    """stream= instead of the current stream, for every call of the cache."""
+    c = weight_case(11, [500, 300], [4, 2], 8, 8, 2, 64, True)
+    kw = dict(path=c["path"], accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    args = (c["q"], c["k"], c["table"], c["prefix"], c["lse"])
+    want_w = jf.accumulate_attention_weight(*args, out=c["out"].clone(), **kw)
+    lens = c["prefix"] + c["accept_len"] + 1
+    want_keep, want_len = jf.select_kept_keys(want_w, lens, 100, sink=1, recent=5)
+    k1, v1 = c["k"].clone(), c["k"].clone()
+    jf.evict_kv(k1, v1, c["table"], lens, want_keep, want_len, weight=want_w.clone())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out, k2, v2 = c["out"].clone(), c["k"].clone(), c["k"].clone()
+    keep, kept = torch.empty_like(want_keep), torch.empty_like(want_len)
+    torch.cuda.synchronize()
+    jf.accumulate_attention_weight(*args, out=out, stream=s, **kw)
+    jf.jf_select_kept(out, lens, keep, kept, 1, 5, stream=s)
+    jf.evict_kv(k2, v2, c["table"], lens, keep, kept, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want_w) and torch.equal(keep, want_keep) and torch.equal(kept, want_len)
+    assert torch.equal(k1.view(torch.int16), k2.view(torch.int16)) and torch.equal(v1.view(torch.int16), v2.view(torch.int16))
+
+
 # ------------------------------------------------------------------------------- kept positions
 
 def run_select(jf, w, L, budget, sink, recent):
@@ -283,6 +306,37 @@ def test_select_special_values(jf):
     w = np.pad(w, ((0, 0), (0, 0), (0, 8)))
     for budget, sink, recent in ((400, 5, 7), (1, 0, 0), (999, 0, 0), (12, 5, 7)):
         run_select(jf, w, [n, n - 3], budget, sink, recent)
+
+
+@pytest.mark.parametrize("cap", [1003, 4097, 333])
+def test_select_rows_off_sixteen_bytes(jf, cap):
+    """Rows that start at any 4-byte offset, and a tensor that does."""
+    rng = np.random.default_rng(cap)
+    w = rng.standard_normal((3, 5, cap)).astype(np.float32)
+    run_select(jf, w, [cap, cap - 1, cap // 2], cap // 3, 3, 9)
+    flat = torch.zeros(w.size + 1, device="cuda")
+    view = flat[1:].view(w.shape)
+    view.copy_(dev(w))
+    L = np.array([cap, cap - 2, 7], np.int32)
+    keep, kept = jf.select_kept_keys(view, dev(L), 40, sink=1, recent=2)
+    want, want_len = ref.select_kept(w, L, 1, 2, 40)
+    assert (keep.cpu().numpy() == want).all() and (kept.cpu().numpy() == want_len).all()
+
+
+@pytest.mark.parametrize("rows", [80, 200])
+def test_select_many_rows(jf, rows):
+    """A row a CTA, short and longer than one CTA holds."""
+    rng = np.random.default_rng(rows)
+    w = np.exp(rng.standard_normal((rows // 4, 4, 3000 if rows == 80 else 40000))).astype(np.float32)
+    n = w.shape[2]
+    if rows == 200:                            # (the reference sorts every row: a few of them)
+        w[1:] = w[:1]
+        L = np.full(rows // 4, n, np.int32)
+        keep, _ = jf.select_kept_keys(dev(w), dev(L), 7000, sink=2, recent=30)
+        want, _ = ref.select_kept(w[:1], L[:1], 2, 30, 7000)
+        assert (keep.cpu().numpy() == want).all()
+    else:
+        run_select(jf, w, [n - 100 * i for i in range(rows // 4)], 700, 2, 30)
 
 
 @pytest.mark.parametrize("rows", [1, 40])
