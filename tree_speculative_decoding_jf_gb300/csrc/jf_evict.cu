@@ -351,7 +351,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
 
 // ------------------------------------------------------------------------ eviction
 
-constexpr int kEvictThreads = 256;
 constexpr int kEvictHeld = 4;             // 16-byte vectors a thread moves at a time
 constexpr int kEvictWeights = 8;          // weights a thread moves at a time
 
@@ -382,11 +381,11 @@ struct EvictParams {
 // rows are split over CTAs.
 //
 // A row's pool rows (page * 16 + slot) are looked up once, by one thread, two batches ahead.
-template <int VECS>
-__global__ void __launch_bounds__(kEvictThreads, 4) evict_kernel(const EvictParams p) {
-  constexpr int kRows = kEvictThreads / VECS;               // rows a pass of the CTA touches
+template <int VECS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_kernel(const EvictParams p) {
+  constexpr int kRows = THREADS / VECS;               // rows a pass of the CTA touches
   constexpr int kBatch = kRows * kEvictHeld;
-  static_assert(kBatch <= kEvictThreads, "a thread looks up one row of a batch");
+  static_assert(kBatch <= THREADS, "a thread looks up one row of a batch");
   // Four: a slot is written again only when every thread is done with its last batch.
   __shared__ int s_src[4][kBatch], s_dst[4][kBatch];
   grid_dependency_wait();
@@ -416,19 +415,19 @@ __global__ void __launch_bounds__(kEvictThreads, 4) evict_kernel(const EvictPara
     float* wo = p.weight_out + static_cast<size_t>(row) * cap;
     // (in place, one CTA goes through all rows in order)
     const int w0 = p.weight_in_place ? 0 : j0, w1 = p.weight_in_place ? (blockIdx.y == 0 ? n : 0) : j1;
-    for (int base = w0; base < w1; base += kEvictThreads * kEvictWeights) {
+    for (int base = w0; base < w1; base += THREADS * kEvictWeights) {
       float v[kEvictWeights];
       int t[kEvictWeights];
 #pragma unroll
       for (int u = 0; u < kEvictWeights; ++u) {
-        const int j = base + u * kEvictThreads + tid;
+        const int j = base + u * THREADS + tid;
         t[u] = j < w1 ? source(j) : -1;
         if (t[u] >= 0) v[u] = w[t[u]];
       }
       if (p.weight_in_place) __syncthreads();
 #pragma unroll
       for (int u = 0; u < kEvictWeights; ++u)
-        if (t[u] >= 0) wo[base + u * kEvictThreads + tid] = v[u];
+        if (t[u] >= 0) wo[base + u * THREADS + tid] = v[u];
       if (p.weight_in_place) __syncthreads();
     }
   } else {
@@ -583,10 +582,12 @@ extern "C" jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* bl
   p.budget = budget;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
-  // In place: 64-byte slices, one CTA each.  Into other pages: whole rows, split so that
-  // every SM gets about eight CTAs (two rounds of the four that fit).
-  const int vecs = p.kv_in_place ? 4 : D / 8;
-  const int batch = kEvictThreads / vecs * kEvictHeld;
+  // In place: 64-byte slices, one CTA of 512 threads each (few CTAs, so each holds more on
+  // its way: 103 us against 134 us with 256 threads on 16384 of 33024 keys, 8 x 4 heads).
+  // Into other pages: whole rows, split so that every SM gets about eight CTAs (two rounds
+  // of the four that fit).
+  const int vecs = p.kv_in_place ? 4 : D / 8, threads = p.kv_in_place ? 512 : 256;
+  const int batch = threads / vecs * kEvictHeld;
   const unsigned parts = 2 * (D / 8 / vecs) + (weight_out != nullptr ? 1 : 0);
   const long long units = static_cast<long long>(B) * Hkv * parts;
   long long splits = 1;
@@ -594,8 +595,8 @@ extern "C" jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* bl
     splits = std::max<long long>(1, std::min<long long>((budget + batch - 1) / batch, (8ll * sms + units - 1) / units));
   const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(std::min<long long>(splits, 65535)));
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = vecs == 4   ? launch_pdl(evict_kernel<4>, grid, dim3(kEvictThreads), 0, s, p)
-                        : vecs == 8 ? launch_pdl(evict_kernel<8>, grid, dim3(kEvictThreads), 0, s, p)
-                                    : launch_pdl(evict_kernel<16>, grid, dim3(kEvictThreads), 0, s, p);
+  const cudaError_t e = vecs == 4   ? launch_pdl(evict_kernel<4, 512>, grid, dim3(threads), 0, s, p)
+                        : vecs == 8 ? launch_pdl(evict_kernel<8, 256>, grid, dim3(threads), 0, s, p)
+                                    : launch_pdl(evict_kernel<16, 256>, grid, dim3(threads), 0, s, p);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
