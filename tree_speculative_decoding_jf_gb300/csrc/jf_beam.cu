@@ -16,8 +16,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ------------------------------------------------------------------------ scan
 //
 // The K best pairs of a prompt lie in few places.  The scan streams the logits once and
-// keeps, for every block of some 1024 logits, only the greatest, beside the slice's maximum
-// and sum of exponentials for the log-sum-exp.  The K-th best of the blocks' best pairs
+// keeps, for every block of logits (1024 in bf16; fewer where a prompt has few), only the
+// greatest, beside the slice's maximum and sum of exponentials for the log-sum-exp.  The K-th best of the blocks' best pairs
 // bounds the K-th best pair from below, so the merge reads again only the blocks that reach
 // it: about K of them.  The scan has no barrier, no shared memory and no candidates; HBM
 // bounds it.  (Collecting candidates while streaming cost a threshold, a compaction and a
@@ -90,7 +90,8 @@ struct BeamParams {
   float2* stats;          // [rows][slices]: maximum, sum of exp(x - maximum)
   uint32_t* best;         // [rows][blocks]: key of a block's greatest logit
   int W, V, K, eos;
-  int slices, slice_blocks;   // slices of a row (a warp each), blocks of a slice
+  int slices, slice_steps;    // slices of a row (a warp each), steps of a slice
+  int steps;                  // steps of a row
   int blocks, block_vecs;     // blocks of a row, 16-byte vectors of a block
   int total;                  // rows * slices
 };
@@ -127,23 +128,25 @@ __device__ __forceinline__ uint4 RowVecs<T>::load(int vec) const {
   return row_end(x, at, V);
 }
 
-template <typename T>
+template <typename T, bool SMALL>       // SMALL: blocks of part of a step's vectors
 __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const BeamParams p) {
   using R = Row<T>;
   constexpr int VN = R::kN;
   grid_dependency_wait();
+  grid_dependents_launch();               // the merge's blocks may take their places; it waits for this grid
   const int lane = threadIdx.x & 31, slice = blockIdx.x * kScanWarps + (threadIdx.x >> 5);
   const int row = slice / p.slices, part = slice - row * p.slices;
   // (the merge makes the pairs of beams that are not live itself)
   if (slice >= p.total || (p.finished != nullptr && p.finished[row] != 0) || p.score[row] == -INFINITY) {
-    grid_dependents_launch();
     return;
   }
   const RowVecs<T> r(p.logits, row, p.V);
-  const int b0 = part * p.slice_blocks, b1 = min(p.blocks, b0 + p.slice_blocks);
-  const int vec0 = b0 * p.block_vecs + lane, steps = (b1 - b0) * (p.block_vecs / kStepVecs);
-  const int block_steps = p.block_vecs / kStepVecs;
-  uint32_t* best = p.best + static_cast<size_t>(row) * p.blocks + b0;
+  const int step0 = part * p.slice_steps, steps = min(p.slice_steps, p.steps - step0);
+  const int vec0 = step0 * kStepVecs + lane;
+  // (a slice holds whole blocks)
+  const int block_steps = max(1, p.block_vecs / kStepVecs);
+  uint32_t* best = p.best + static_cast<size_t>(row) * p.blocks;
+  int block = step0 / block_steps;
   float m = -INFINITY, sum = 0.f;         // of this lane
   uint32_t greatest = 0u;                 // of this lane, in the block
   uint4 next[kStep];
@@ -159,13 +162,23 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const BeamPa
       for (int u = 0; u < kStep; ++u) next[u] = r.load(vec0 + (i + 1) * kStepVecs + u * 32);
     }
     const float mine = fmaxf(fmaxf(R::vmax(v[0]), R::vmax(v[1])), fmaxf(R::vmax(v[2]), R::vmax(v[3])));
-    greatest = max(greatest, logit_key(mine));
-    if (--left == 0) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, greatest);
-      if (lane == 0) *best = top;
-      ++best;
-      greatest = 0u;
-      left = block_steps;
+    if constexpr (SMALL) {                // 32, 8 or 1 vectors
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) {
+        uint32_t top = logit_key(R::vmax(v[u]));
+        for (int o = 1; o < p.block_vecs; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int at = (vec0 + i * kStepVecs + u * 32) / p.block_vecs;
+        if ((lane & (p.block_vecs - 1)) == 0 && at < p.blocks) best[at] = top;
+      }
+    } else {
+      greatest = max(greatest, logit_key(mine));
+      if (--left == 0) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, greatest);
+        if (lane == 0) best[block] = top;
+        ++block;
+        greatest = 0u;
+        left = block_steps;
+      }
     }
     const float up = fmaxf(m, mine), ref = up == -INFINITY ? 0.f : up;
     if (up > m) sum *= fast_exp2((m - ref) * kLog2e);
@@ -193,7 +206,6 @@ __global__ void __launch_bounds__(kScanThreads, 8) beam_scan_kernel(const BeamPa
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) p.stats[slice] = make_float2(M, sum);
-  grid_dependents_launch();
 }
 
 // ------------------------------------------------------------------------ merge
@@ -452,7 +464,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     for (int v0 = 0; v0 < p.block_vecs; v0 += kStepVecs) {
       uint4 v[kStep];
 #pragma unroll
-      for (int u = 0; u < kStep; ++u) v[u] = r.load(block * p.block_vecs + v0 + u * 32 + lane);
+      for (int u = 0; u < kStep; ++u) {
+        const int i_vec = v0 + u * 32 + lane;
+        v[u] = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+        if (i_vec < p.block_vecs) v[u] = r.load(block * p.block_vecs + i_vec);
+      }
 #pragma unroll
       for (int u = 0; u < kStep; ++u) {
         uint32_t some = __ballot_sync(0xffffffffu, score_word(off32, R::vmax(v[u])) >= bound);
@@ -627,22 +643,30 @@ __global__ void __launch_bounds__(kForkThreads)
 
 struct BeamPlan {
   int blocks, block_vecs;     // blocks of a row, vectors of a block
-  int slices, slice_blocks;   // slices of a row (a warp each), blocks of a slice
+  int steps;                  // 128-vector steps of a row (whole blocks)
+  int slices, slice_steps;    // slices of a row (a warp each), steps of a slice
 };
 
-// A block is one step of a warp, 128 vectors, more where a prompt would have more than
-// kMergeBlocks.  A slice is eight blocks while that gives every SM 16 warps; with few rows,
-// shorter ones spread a row over more SMs.  One vector more than the logits fill: a row may
-// start inside one.
-void plan_beam(long long rows, int W, int V, int dtype, int sms, BeamPlan* pl) {
+// A block is one step of a warp, 128 vectors; more where a prompt would have more than
+// kMergeBlocks, and 32, 8 or 1 vectors where it would have fewer than 8 K, since the bound
+// comes from the K-th best block (6000 logits in 6 blocks, K = 20: 60 us in the merge, which
+// then had to look at every logit).  A slice is eight steps while that gives every SM 16
+// warps; with few rows, shorter ones spread a row over more SMs.  One vector more than the
+// logits fill: a row may start inside one.
+void plan_beam(long long rows, int W, int V, int K, int dtype, int sms, BeamPlan* pl) {
   const int vn = dtype == JF_DTYPE_BF16 ? 8 : 4;
   const long long vecs = (static_cast<long long>(V) + vn - 1) / vn + 1;
+  auto blocks_of = [&](int block_vecs) { return (vecs + block_vecs - 1) / block_vecs; };
   pl->block_vecs = kStepVecs;
-  while (W * ((vecs + pl->block_vecs - 1) / pl->block_vecs) > kMergeBlocks) pl->block_vecs *= 2;
-  pl->blocks = static_cast<int>((vecs + pl->block_vecs - 1) / pl->block_vecs);
-  for (pl->slice_blocks = 8; pl->slice_blocks > 1; pl->slice_blocks /= 2)
-    if (rows * ((pl->blocks + pl->slice_blocks - 1) / pl->slice_blocks) >= 16ll * sms) break;
-  pl->slices = (pl->blocks + pl->slice_blocks - 1) / pl->slice_blocks;
+  while (W * blocks_of(pl->block_vecs) > kMergeBlocks) pl->block_vecs *= 2;
+  while (pl->block_vecs > 1 && pl->block_vecs <= kStepVecs && W * blocks_of(pl->block_vecs) < 8ll * K)
+    pl->block_vecs = pl->block_vecs > 8 ? pl->block_vecs / 4 : 1;
+  pl->blocks = static_cast<int>(blocks_of(pl->block_vecs));
+  const int block_steps = std::max(1, pl->block_vecs / kStepVecs);
+  pl->steps = static_cast<int>((vecs + kStepVecs - 1) / kStepVecs + block_steps - 1) / block_steps * block_steps;
+  for (pl->slice_steps = 8 * block_steps; pl->slice_steps > block_steps; pl->slice_steps /= 2)
+    if (rows * ((pl->steps + pl->slice_steps - 1) / pl->slice_steps) >= 16ll * sms) break;
+  pl->slices = (pl->steps + pl->slice_steps - 1) / pl->slice_steps;
 }
 
 bool beam_sizes_ok(int32_t B, int32_t W, int32_t V, int32_t K) {
@@ -663,7 +687,9 @@ cudaError_t launch_beam(const BeamParams& p, int B, cudaStream_t s) {
   static SmemAttr attr;
   if (!attr.ensure(beam_merge_kernel<T>, 2 * sizeof(uint32_t) * kMergeBlocks)) return cudaErrorUnknown;
   const dim3 grid(static_cast<unsigned>((p.total + kScanWarps - 1) / kScanWarps));
-  const cudaError_t e = launch_pdl(beam_scan_kernel<T>, grid, dim3(kScanThreads), 0, s, p);
+  const cudaError_t e = p.block_vecs < kStepVecs
+                            ? launch_pdl(beam_scan_kernel<T, true>, grid, dim3(kScanThreads), 0, s, p)
+                            : launch_pdl(beam_scan_kernel<T, false>, grid, dim3(kScanThreads), 0, s, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(beam_merge_kernel<T>, dim3(static_cast<unsigned>(B)), dim3(kMergeThreads),
                     2 * sizeof(uint32_t) * p.W * p.blocks, s, p);
@@ -681,7 +707,7 @@ extern "C" size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V,
   const int sms = current_sm_count();
   if (sms <= 0) return static_cast<size_t>(-1);
   BeamPlan pl;
-  plan_beam(static_cast<long long>(B) * W, W, V, dtype, sms, &pl);
+  plan_beam(static_cast<long long>(B) * W, W, V, K, dtype, sms, &pl);
   return beam_workspace(pl, static_cast<long long>(B) * W);
 }
 
@@ -705,7 +731,7 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * W;
   BeamPlan pl;
-  plan_beam(rows, W, V, dtype, sms, &pl);
+  plan_beam(rows, W, V, K, dtype, sms, &pl);
   if (rows * pl.slices >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   if (workspace_bytes < beam_workspace(pl, rows)) return JF_ERR_WORKSPACE_TOO_SMALL;
   BeamParams p;
@@ -723,7 +749,8 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
   p.K = K;
   p.eos = eos_token;
   p.slices = pl.slices;
-  p.slice_blocks = pl.slice_blocks;
+  p.slice_steps = pl.slice_steps;
+  p.steps = pl.steps;
   p.blocks = pl.blocks;
   p.block_vecs = pl.block_vecs;
   p.total = static_cast<int>(rows * pl.slices);
