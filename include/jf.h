@@ -59,7 +59,7 @@ typedef enum { JF_DTYPE_BF16 = 0, JF_DTYPE_F32 = 1 } jf_dtype;
 #define JF_DEVERR_BAD_PREFIX 0x4 /* prefix_len < 0 or prefix_len + N > max_pages * page */
 #define JF_DEVERR_BAD_TOKEN 0x8  /* draft token (non-root node) outside [0, V)          */
 #define JF_DEVERR_TIMEOUT 0x10   /* an in-kernel wait gave up after its time limit      */
-#define JF_DEVERR_BAD_PATH 0x20  /* accepted path / length malformed (KV compaction)     */
+#define JF_DEVERR_BAD_PATH 0x20  /* accepted path, kept positions or beam parent malformed */
 #define JF_DEVERR_BAD_TREE_LEN 0x40 /* tree_len[b] outside [1, N], or a bad packed span   */
 
 /* Largest tree (nodes per sequence) any call accepts. */
