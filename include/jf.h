@@ -617,8 +617,9 @@ jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
  *   parent int32 [B][K] (w), token int32 [B][K] (v), new_score float [B][K] (s, rounded to
  *   fp32), new_finished int32 [B][K] (1 where the parent had finished or v == eos_token;
  *   may be NULL).
- *   logits     [B][W][V] bf16 or fp32 (dtype); -inf marks a token that may not be chosen,
- *              NaN and +inf leave the outputs of that prompt unspecified.
+ *   logits     [B][W][V] bf16 or fp32 (dtype); -inf marks a token that may not be chosen;
+ *              with NaN or +inf the prompt's outputs are unspecified, but every parent and
+ *              token is in range (entries without a pair: 0, 0 and a NaN score).
  *   score      float [B][W]; must not be new_score.
  *   finished   int32 [B][W] or NULL; must not be new_finished.  eos_token: -1 for none, in
  *              [0, V) where finished is given.

@@ -128,6 +128,34 @@ def test_logits_of_beams_that_are_not_live_are_not_read(jf, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nan_and_inf_logits_leave_no_stale_output(jf, dtype, bad):
+    """A prompt with NaN or +inf gives pairs in range, whatever the outputs held, and the
+    prompts beside it their own results."""
+    rng = np.random.default_rng(21)
+    B, W, V, K = 4, 2, 3001, 7
+    logits = 2 * rng.standard_normal((B, W, V))
+    score = (-rng.random((B, W)) - 1).astype(np.float32)
+    t = torch.from_numpy(logits.astype(np.float32)).to(dtype)
+    clean = t.float().numpy().copy()
+    t[0] = bad                                 # everywhere
+    t[1, 1, 5] = bad                           # in one logit
+    t[2, :, 17] = bad                          # in one logit of every beam
+    ws = torch.empty(jf.jf_beam_select_workspace_size(B, W, V, K, jf._logit_dtype(t)), dtype=torch.uint8, device="cuda")
+    out = [torch.full((B, K), -(1 << 30), dtype=torch.int32, device="cuda") for _ in range(2)]
+    new_score = torch.full((B, K), 1e30, device="cuda")
+    new_fin = torch.full((B, K), 77, dtype=torch.int32, device="cuda")
+    jf.jf_beam_select(t.cuda(), dev(score), *out, new_score, ws, new_finished=new_fin)
+    torch.cuda.synchronize()
+    parent, token = (x.cpu().numpy() for x in out)
+    assert ((parent >= 0) & (parent < W)).all() and ((token >= 0) & (token < V)).all()
+    assert (new_score.cpu().numpy() != np.float32(1e30)).all()
+    assert np.isin(new_fin.cpu().numpy(), (0, 1)).all()
+    good = slice(3, 4)
+    check_beams(clean[good], score[good], None, -1, [x[good] for x in (*out, new_score, new_fin)], K)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_scores_of_every_size(jf, dtype):
     """Sharp and flat rows, logits and scores far from zero: the fp32 bound of the merge stays
     below the K-th pair."""

@@ -572,6 +572,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
         at += __popc(ms);
       }
     }
+    // (left only where NaN or +inf took a beam's pairs away: nothing stale is left behind)
+    for (int rank = at + lane; rank < K; rank += 32) put(rank, 0u, __int_as_float(0x7fffffff));
   }
   grid_dependents_launch();
 }
