@@ -269,6 +269,49 @@ def test_calls_on_a_given_stream(jf):
     assert torch.equal(k1.view(torch.int16), k2.view(torch.int16)) and torch.equal(v1.view(torch.int16), v2.view(torch.int16))
 
 
+def test_tensors_of_a_call_on_a_given_stream(jf):
+    """What a call makes for itself is made on its stream: a busy current stream neither clears
+    the result late nor loses the contents of memory that it still reads."""
+    c = weight_case(12, [500, 300], [4, 2], 8, 8, 2, 64, True)
+    kw = dict(path=c["path"], accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    args = (c["q"], c["k"], c["table"], c["prefix"], c["lse"])
+    want = jf.accumulate_attention_weight(*args, **kw)
+    lens = c["prefix"] + c["accept_len"] + 1
+    want_keep, want_len = jf.select_kept_keys(want, lens, 100, sink=1, recent=5)
+    logits, score = torch.randn(2, 3, 4000, device="cuda"), torch.zeros(2, 3, device="cuda")
+    want_beams = jf.beam_select(logits, score, 5)
+    fresh = torch.arange(10, dtype=torch.int32, device="cuda").view(2, 5)
+    table = torch.arange(10, 28, dtype=torch.int32, device="cuda").view(6, 3)
+    cache = [torch.randn(28, 16, 2, 64, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    plen = torch.full((6,), 20, dtype=torch.int32, device="cuda")
+    want_fork = jf.beam_fork_kv(*(x.clone() for x in cache), table, plen, want_beams[0], fresh)
+    s = torch.cuda.Stream()
+
+    def check(call, wants):
+        """call(), with the current stream asleep before it reads tensors like call's."""
+        held = [torch.full_like(w, 3) for w in wants for _ in range(4)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        copies = [h.clone() for h in held]
+        del held                               # its memory is free to the current stream
+        got = call()
+        s.synchronize()
+        torch.cuda.synchronize()
+        for g, w in zip(got, wants):
+            assert torch.equal(g, w)
+        for x in copies:
+            assert (x == 3).all()
+
+    check(lambda: [jf.accumulate_attention_weight(*args, stream=s, **kw)], [want])
+    check(lambda: jf.select_kept_keys(want, lens, 100, sink=1, recent=5, stream=s), [want_keep, want_len])
+    check(lambda: jf.beam_select(logits, score, 5, stream=s), list(want_beams))
+    check(lambda: jf.beam_select(logits, score, 5, stream=s.cuda_stream), list(want_beams))
+    check(lambda: jf.beam_fork_kv(*cache, table, plen, want_beams[0], fresh, stream=s), list(want_fork))
+    got = jf.select_kept_keys(want, lens, 100, sink=1, recent=5, stream=0)   # the default stream
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want_keep) and torch.equal(got[1], want_len)
+
+
 # ------------------------------------------------------------------------------- kept positions
 
 def run_select(jf, w, L, budget, sink, recent):

@@ -9,6 +9,7 @@ also allocate the outputs (with torch) before calling the same entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -654,6 +655,17 @@ def _on_stream(specs, dev_err, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made_on(stream):
+    """Where a call makes tensors of its own: on its stream, so that their memory's earlier
+    users, a fill and the kernels follow each other."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _at(t):
     """Address of an optional tensor for a call whose arguments are declared as pointers."""
     return None if t is None else t.data_ptr()
@@ -925,7 +937,8 @@ def accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path=N
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = torch.zeros((B, Hkv, max_pages * page), dtype=torch.float32, device=q.device)
+        with _made_on(stream):
+            out = torch.zeros((B, Hkv, max_pages * page), dtype=torch.float32, device=q.device)
     if cu_seqlens is None:
         jf_attention_weight(q, k_cache, block_table, prefix_len, lse, out, scale, path, accept_len,
                             weight, dev_err, stream)
@@ -939,8 +952,9 @@ def accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path=N
 def select_kept_keys(weight, seq_len, budget, sink=0, recent=0, dev_err=None, stream=None):
     """(keep [B][Hkv][budget], kept_len [B]): the positions that stay, by weight."""
     B, Hkv, _ = weight.shape
-    keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weight.device)
-    kept_len = torch.empty((B,), dtype=torch.int32, device=weight.device)
+    with _made_on(stream):
+        keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weight.device)
+        kept_len = torch.empty((B,), dtype=torch.int32, device=weight.device)
     jf_select_kept(weight, seq_len, keep, kept_len, sink, recent, dev_err, stream)
     return keep, kept_len
 
@@ -960,14 +974,12 @@ def beam_select(logits, score, K, finished=None, eos_token=-1, stream=None):
     """(parent, token, score, finished), each [B][K]: the K best continuations of every prompt."""
     B, W, V = logits.shape
     dev = logits.device
-    parent = torch.empty((B, K), dtype=torch.int32, device=dev)
-    token = torch.empty((B, K), dtype=torch.int32, device=dev)
-    new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
-    new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
-    ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
-    if stream is not None:    # the workspace is given back to the current stream's allocator
-        ws.record_stream(stream if hasattr(stream, "cuda_stream")
-                         else torch.cuda.ExternalStream(int(stream)))
+    with _made_on(stream):
+        parent = torch.empty((B, K), dtype=torch.int32, device=dev)
+        token = torch.empty((B, K), dtype=torch.int32, device=dev)
+        new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
+        new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
+        ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
     jf_beam_select(logits, score, parent, token, new_score, ws, finished, eos_token, new_finished,
                    stream)
     return parent, token, new_score, new_finished
@@ -977,9 +989,10 @@ def beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, 
                  stream=None):
     """(block_table [B * K][max_pages], prefix_len [B * K]) of the new beams."""
     B, K = parent.shape
-    new_table = torch.empty((B * K, block_table.shape[1]), dtype=torch.int32,
-                            device=block_table.device)
-    new_len = torch.empty((B * K,), dtype=torch.int32, device=block_table.device)
+    with _made_on(stream):
+        new_table = torch.empty((B * K, block_table.shape[1]), dtype=torch.int32,
+                                device=block_table.device)
+        new_len = torch.empty((B * K,), dtype=torch.int32, device=block_table.device)
     jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, new_table,
                     new_len, dev_err, stream)
     return new_table, new_len
