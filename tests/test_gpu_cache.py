@@ -413,6 +413,44 @@ def test_select_rows_past_shared_memory(jf, kind):
     assert (keep[1, 0, :300].cpu().numpy() == np.arange(300)).all() and (keep[1, 0, 300:] == -1).all()
 
 
+@pytest.mark.parametrize("rows,n", [(1, 300000), (1, 393216), (80, 300000), (80, 400000)])
+@pytest.mark.parametrize("kind", ["weights", "few values"])
+def test_select_the_longest_slices(jf, rows, n, kind):
+    """Slices at and past what fits on chip, for few rows and for many."""
+    rng = np.random.default_rng(n + rows)
+    w = rng.standard_normal(n).astype(np.float32)
+    if kind == "few values":
+        w = np.floor(w * 2)
+    budget, sink, recent = 100000, 3, 50
+    err = new_err()
+    keep, kept = jf.select_kept_keys(dev(w).expand(rows, 1, n).contiguous(), dev(np.full(rows, n, np.int32)),
+                                     budget, sink=sink, recent=recent, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and (kept == budget).all()
+    mid = w[sink:n - recent].astype(np.float64)
+    order = np.lexsort((np.arange(len(mid)), -mid))[:budget - sink - recent] + sink
+    want = np.sort(np.concatenate([np.arange(sink), order, np.arange(n - recent, n)]))
+    assert (keep.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("rows", [1, 80])
+@pytest.mark.parametrize("equal", [1, 255, 256, 257, 2000])
+def test_select_equal_keys_at_the_border(jf, rows, equal):
+    """`equal` keys of one value, of which some stay, around the number that is listed."""
+    rng = np.random.default_rng(equal)
+    n = 20000
+    w = rng.random(n) + 2.0
+    w[rng.permutation(n)[:n // 2]] -= 2.0      # below 1
+    at = rng.permutation(n)[:equal]
+    w[at] = 1.5
+    w = w.astype(np.float32)
+    above = int((w > 1.5).sum())
+    for b in {above + 1, above + (equal + 1) // 2, above + equal}:
+        keep, _ = jf.select_kept_keys(dev(w).expand(rows, 1, n).contiguous(), dev(np.full(rows, n, np.int32)), b)
+        want, _ = ref.select_kept(w[None, None], np.array([n], np.int32), 0, 0, b)
+        assert (keep.cpu().numpy() == want).all()
+
+
 def test_select_clamps_lengths(jf):
     w = np.random.default_rng(0).random((2, 2, 64)).astype(np.float32)
     err = new_err()

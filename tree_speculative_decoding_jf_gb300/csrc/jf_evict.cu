@@ -16,21 +16,25 @@ constexpr int kPage = 16;
 // One thread-block cluster per (sequence, kv-head) row; its CTAs take equal slices of the
 // row and keep them on chip as 32-bit keys that order as the weights do, so the weights are
 // read once.  The smallest kept key is found by counting: the keys' range is cut into 1024
-// steps, and the step that holds the wanted rank usually holds few enough keys to list and
-// rank directly; otherwise it becomes the next range, down to one value (2^32 in four
-// counts), of which the first by position stay.
+// steps (2048 with 1024 threads), and the step that holds the wanted rank usually holds few
+// enough keys to list and rank directly; otherwise it becomes the next range, down to one
+// value (2^32 in four counts), of which the first by position stay.  (A count of a row of
+// 32K takes 5,500 cycles; ranking a list goes with its square, 50,000 cycles at 1000 keys.)
+// Then one pass makes a bit a key, and a thread a 32-key word puts the kept offsets together
+// on chip, from where they are written side by side.
 //
-// What bounds the call is not the 8 bytes a key but the instructions a key (four passes over
-// shared memory, four keys at a time) and, for few rows, the barriers between the steps.
+// What bounds the call is not the 8 bytes a key but, for a row of 32K in one CTA, in cycles:
+// the load 10,800, the counts 4,700, the bits 4,000, the list 1,700, the positions 4,300;
+// for few rows, the barriers between the steps.  256 rows of 32K: 30 us, of which the 256
+// CTAs on 152 SMs take two rounds.  (With a second pass of ballots for the positions, 1024
+// steps and lists of 1024: 40 us, and 87 us where a step held 700 keys.)
 // Keys that stay whatever they are (the first `sink`, the last `recent`) become kForced,
 // above every weight, and the padding 0, below every one, so no pass tests positions.
 constexpr int kSelSlice = 8192;           // keys of a CTA's slice with 512 threads, ..
 constexpr int kSelSliceMany = 32768;      // .. with 1024
-constexpr int kSelMost = 200 * 1024 / 4;  // keys that fit on chip; longer slices are read again
+constexpr int kSelMost = 192 * 1024 / 4;  // keys that fit on chip; longer slices are read again
 constexpr int kSelPad = 128;              // a slice fills whole 128-key runs of a warp
-constexpr int kBinBits = 10;
-constexpr int kBins = 1 << kBinBits;
-constexpr int kSelList = 1024;            // listed keys of a row
+constexpr int kSelList = 256;             // listed keys of a row
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kForced = 0xffffffffu; // above every weight's key
 constexpr uint32_t kNone = 0u;            // below every weight's key
@@ -54,16 +58,21 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
     select_kernel(const float* __restrict__ weight, const int32_t* __restrict__ seq_len, int Hkv,
                   int cap, int sink, int recent, int budget, int C, int32_t* __restrict__ keep,
                   int32_t* __restrict__ kept_len, int32_t* dev_err) {
-  constexpr int kWarps = THREADS / 32, kMine = kBins / THREADS;
+  constexpr int kWarps = THREADS / 32, kMine = 2, kBins = kMine * THREADS;   // steps of a count
+  constexpr int kBinBits = THREADS == 512 ? 10 : 11;
+  static_assert(kBins == 1 << kBinBits, "a step each");
   extern __shared__ uint4 s_keys[];                         // this CTA's slice, four keys each
   __shared__ uint32_t s_hist[2][kBins];                     // this CTA's counts (two rounds' in turn)
   __shared__ uint32_t s_range[2];                           // min, max of this CTA
-  __shared__ uint32_t s_count[3];                           // above the step, in it, listed (this CTA)
+  __shared__ uint32_t s_count[4];                           // this CTA's: above the step, in it, listed; listed before it that stay
   __shared__ uint32_t s_warp[2][kWarps];
   __shared__ uint32_t s_bin[3];                             // the step, keys above it, keys in it
   __shared__ uint64_t s_list[kSelList];                     // key << 32 | ~position, this CTA's
   __shared__ uint64_t s_all[kSelList];                      // the row's
+  __shared__ __align__(16) uint32_t s_in[RESIDENT ? kSelMost / 32 : 1];  // a bit a key: in the step
   __shared__ uint64_t s_cut;
+  __shared__ __align__(16) uint32_t s_mask[RESIDENT ? kSelMost / 32 : 1];   // a bit a key: it stays
+  __shared__ uint32_t s_scan[kWarps];
   grid_dependency_wait();
   const int rank = ONE ? 0 : static_cast<int>(cluster_ctarank());
   const int row = blockIdx.x / C, b = row / Hkv;
@@ -119,26 +128,37 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
   // ---- the slice, and the range of the competing keys
   if (tid < 2) s_range[tid] = tid == 0 ? 0xffffffffu : 0u;
   uint32_t kmin = 0xffffffffu, kmax = 0u;
+  // Vectors [va, vb) hold competing keys alone: four loads a thread on their way at once (a
+  // test inside the loop kept them apart: 13,700 cycles a row of 32K; eight at once gain
+  // nothing).
   const bool wide = (reinterpret_cast<uintptr_t>(ws) & 15u) == 0;
-#pragma unroll 4
-  for (int i = tid; i < vecs; i += THREADS) {
-    uint4 k;
-    if (wide && 4 * i >= c_lo && 4 * i + 4 <= min(c_hi, n_slice)) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(ws) + i);
-      k = make_uint4(weight_key(f.x), weight_key(f.y), weight_key(f.z), weight_key(f.w));
-      kmin = min(min(kmin, min(k.x, k.y)), min(k.z, k.w));
-      kmax = max(max(kmax, max(k.x, k.y)), max(k.z, k.w));
-    } else {
-      k = load4(i);
-      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+  const int va = wide ? min(vecs, (max(c_lo, 0) + 3) / 4) : 0;
+  const int vb = wide ? max(va, max(min(c_hi, n_slice), 0) / 4) : 0;
+  for (int j = tid; j < va + vecs - vb; j += THREADS) {     // the others, first: their latency passes under the bulk
+    const int i = j < va ? j : j - va + vb;
+    const uint4 k = load4(i);
+    const uint32_t e[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (e[c] != kForced && e[c] != kNone) {
-          kmin = min(kmin, e[c]);
-          kmax = max(kmax, e[c]);
-        }
-    }
+    for (int c = 0; c < 4; ++c)
+      if (e[c] != kForced && e[c] != kNone) {
+        kmin = min(kmin, e[c]);
+        kmax = max(kmax, e[c]);
+      }
     if constexpr (RESIDENT) s_keys[i] = k;
+  }
+  for (int i0 = va + tid; i0 < vb; i0 += THREADS * 4) {
+    float4 f[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * THREADS < vb) f[u] = __ldg(reinterpret_cast<const float4*>(ws) + i0 + u * THREADS);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * THREADS < vb) {
+        const uint4 k = make_uint4(weight_key(f[u].x), weight_key(f[u].y), weight_key(f[u].z), weight_key(f[u].w));
+        kmin = min(min(kmin, min(k.x, k.y)), min(k.z, k.w));
+        kmax = max(max(kmax, max(k.x, k.y)), max(k.z, k.w));
+        if constexpr (RESIDENT) s_keys[i0 + u * THREADS] = k;
+      }
   }
   for (int i = tid; i < kBins; i += THREADS) s_hist[0][i] = 0u;
   kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -201,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
     if (lane == 31) s_warp[0][warp] = incl;
     __syncthreads();
     uint32_t above = incl - mine;
-    for (int v = 0; v < warp; ++v) above += s_warp[0][v];
+    above += __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[0][lane] : 0u);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       if (above < need && above + c[i] >= need) {
@@ -220,130 +240,251 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 3 : 1)
     shift = max(0, shift - kBinBits);
   }
 
-  // ---- counts: forced keys and keys above the step, keys in it; the latter listed
-  const int per_warp = (runs + kWarps - 1) / kWarps;
-  const int v_lo = min(runs, warp * per_warp) * 32, v_hi = min(runs, (warp + 1) * per_warp) * 32;
-  const uint32_t hi = lo + last;
-  const uint32_t not_first = 0xffffffffu - static_cast<uint32_t>(t_lo);   // ~position of offset 0
-  if (tid == 0) s_count[2] = 0u;
-  __syncthreads();
-  uint32_t n_above = 0u, n_in = 0u;
-#pragma unroll 2
-  for (int i = v_lo + lane; i < v_hi; i += 32) {
-    const uint4 k = keys4(i);
-    n_above += (k.x > hi) + (k.y > hi) + (k.z > hi) + (k.w > hi);
-    if (k.x - lo <= last || k.y - lo <= last || k.z - lo <= last || k.w - lo <= last) {
-      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (e[c] - lo <= last) {
-          ++n_in;
-          if (listed) s_list[atomicAdd(&s_count[2], 1u)] = (static_cast<uint64_t>(e[c]) << 32) | (not_first - static_cast<uint32_t>(4 * i + c));
-        }
-    }
-  }
-  n_above = __reduce_add_sync(0xffffffffu, n_above);
-  n_in = __reduce_add_sync(0xffffffffu, n_in);
-  if (lane == 0) {
-    s_warp[0][warp] = n_above;
-    s_warp[1][warp] = n_in;
-  }
-  __syncthreads();
-  if (tid < 2) {
-    uint32_t v = 0u;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += s_warp[tid][i];
-    s_count[tid] = v;
-  }
-  row_sync();
-  uint32_t at = 0u, in_before = 0u;       // kept and in-step keys before this warp's runs
-  peers(&s_count[0], 0u);
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < rank) at += from[r];
-  peers(&s_count[1], 0u);
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < rank) in_before += from[r];
-  for (int v = 0; v < warp; ++v) {
-    at += s_warp[0][v];
-    in_before += s_warp[1][v];
-  }
-  uint64_t cut = ~0ull;
-  if (listed) {                           // the step's keys that stay: `cut` and what ranks before it
+  // Every CTA's listed keys into s_all; returns their number.
+  auto gather_lists = [&]() -> uint32_t {
+    peers(&s_count[2], 0u);
     uint32_t all = 0u;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       for (uint32_t i = tid; i < from[r]; i += THREADS) {
-        if constexpr (ONE) {
-          s_all[all + i] = s_list[i];
-        } else {
-          const uint32_t* e = reinterpret_cast<const uint32_t*>(&s_list[i]);
-          const uint32_t a = dsmem_ld_u32(dsmem_addr(e, r)), c = dsmem_ld_u32(dsmem_addr(e + 1, r));
-          s_all[all + i] = (static_cast<uint64_t>(c) << 32) | a;
-        }
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(&s_list[i]);
+        const uint32_t a = dsmem_ld_u32(dsmem_addr(e, r)), c = dsmem_ld_u32(dsmem_addr(e + 1, r));
+        s_all[all + i] = (static_cast<uint64_t>(c) << 32) | a;
       }
       all += from[r];
     }
-    __syncthreads();
-    for (uint32_t i = warp; i < all; i += kWarps) {
-      const uint64_t e = s_all[i];
-      uint32_t before = 0u;
-      for (uint32_t j = lane; j < all; j += 32) before += s_all[j] > e;
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (before == need - 1u && lane == 0) s_cut = e;
-    }
-    __syncthreads();
-    cut = s_cut;
-    uint32_t n = 0u;
-    for (uint32_t i = lane; i < all; i += 32) {
-      const uint64_t e = s_all[i];
-      n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(t_lo + 4 * v_lo);
-    }
-    at += __reduce_add_sync(0xffffffffu, n);
-  } else {                                // one value: the first by position stay
-    at += min(need, in_before);
-  }
-  // ---- the kept positions, in order: a lane's four are consecutive
+    return all;
+  };
+  const uint32_t hi = lo + last;
+  const uint32_t not_first = 0xffffffffu - static_cast<uint32_t>(t_lo);   // ~position of offset 0
+  auto entry = [&](uint32_t k, int e) -> uint64_t {   // of offset e in a list
+    return (static_cast<uint64_t>(k) << 32) | (not_first - static_cast<uint32_t>(e));
+  };
+  if (tid == 0) s_count[2] = s_count[3] = 0u;
+  __syncthreads();
+  if constexpr (RESIDENT) {
+    // ---- a bit a key: forced or above the step; keys in the step are listed, or (equal keys
+    // without number) get bits of their own.  From here on the keys are not read again.
+    uint8_t* up8 = reinterpret_cast<uint8_t*>(s_mask);
+    uint32_t n_above = 0u, n_in = 0u;
 #pragma unroll 2
-  for (int i = v_lo + lane; i < v_hi; i += 32) {
-    const uint4 k = keys4(i);
-    const uint32_t e[4] = {k.x, k.y, k.z, k.w};
-    uint32_t stay = 0u, in = 0u;          // a bit a key
+    for (int i = tid; i < vecs; i += THREADS) {
+      const uint4 k = s_keys[i];
+      const uint32_t up = static_cast<uint32_t>(k.x > hi) | (k.y > hi) << 1 | (k.z > hi) << 2 | (k.w > hi) << 3;
+      const uint32_t in = static_cast<uint32_t>(k.x - lo <= last) | (k.y - lo <= last) << 1 |
+                          (k.z - lo <= last) << 2 | (k.w - lo <= last) << 3;
+      const uint32_t up_next = __shfl_down_sync(0xffffffffu, up, 1);
+      if ((lane & 1) == 0) up8[i >> 1] = static_cast<uint8_t>(up | up_next << 4);
+      if constexpr (!ONE) n_above += __popc(up);
+      if (listed) {
+        const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+        if (in != 0u)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      stay |= static_cast<uint32_t>(e[c] > hi) << c;
-      in |= static_cast<uint32_t>(e[c] - lo <= last) << c;
+          for (int c = 0; c < 4; ++c)
+            if ((in >> c) & 1u) s_list[atomicAdd(&s_count[2], 1u)] = entry(e[c], 4 * i + c);
+      } else {
+        const uint32_t in_next = __shfl_down_sync(0xffffffffu, in, 1);
+        if ((lane & 1) == 0) reinterpret_cast<uint8_t*>(s_in)[i >> 1] = static_cast<uint8_t>(in | in_next << 4);
+        if constexpr (!ONE) n_in += __popc(in);
+      }
     }
-    const uint32_t below = (1u << lane) - 1u;
-    if (__any_sync(0xffffffffu, in != 0u)) {
-      uint32_t before = 0u, all = 0u;     // in-step keys of earlier lanes, of all
+    uint32_t at = 0u, in_before = 0u;     // kept and in-step keys of earlier CTAs, then threads
+    if constexpr (ONE) {
+      __syncthreads();
+    } else {
+      n_above = __reduce_add_sync(0xffffffffu, n_above);
+      n_in = __reduce_add_sync(0xffffffffu, n_in);
+      if (lane == 0) {
+        s_warp[0][warp] = n_above;
+        s_warp[1][warp] = n_in;
+      }
+      __syncthreads();
+      if (tid < 2) {
+        uint32_t v = 0u;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) v += s_warp[tid][i];
+        s_count[tid] = v;
+      }
+      row_sync();
+      peers(&s_count[0], 0u);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < rank) at += from[r];
+      peers(&s_count[1], 0u);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < rank) in_before += from[r];
+    }
+    if (listed) {                         // of the step's keys, those with fewer than `need` before them stay
+      const uint64_t* list = s_list;
+      uint32_t all = 0u;
+      if constexpr (ONE) {
+        all = s_count[2];
+      } else {
+        list = s_all;
+        all = gather_lists();
+        __syncthreads();
+      }
+      for (uint32_t i = warp; i < all; i += kWarps) {
+        const uint64_t x = list[i];
+        uint32_t before = 0u;
+        for (uint32_t j = lane; j < all; j += 32) before += list[j] > x;
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (before < need && lane == 0) {
+          const int e = static_cast<int>(not_first - static_cast<uint32_t>(x));   // offset in this slice
+          if (e < 0) atomicAdd(&s_count[3], 1u);
+          else if (e < n_slice) atomicOr(&s_mask[e >> 5], 1u << (e & 31));
+        }
+      }
+      __syncthreads();
+      at += s_count[3];
+    }
+    // ---- the kept offsets in order, gathered on chip, and written
+    const int words = vecs / 8, mine = (words + THREADS - 1) / THREADS;
+    const int w0 = min(words, tid * mine), w1 = min(words, w0 + mine);
+    uint32_t sum = 0u;                    // kept keys, and in-step ones << 16 (a slice has fewer than 2^16)
+    for (int w = w0; w < w1; ++w) sum += __popc(s_mask[w]) + (listed ? 0u : __popc(s_in[w]) << 16);
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    const uint32_t of_warp = lane < kWarps ? s_scan[lane] : 0u;
+    const uint32_t prior = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0u);
+    const uint32_t total = __reduce_add_sync(0xffffffffu, of_warp);
+    uint32_t* offs = reinterpret_cast<uint32_t*>(s_keys);
+    // Kept keys before in-step ones of rank n: all above, and the first `need` of the step.
+    uint32_t n = in_before + (prior >> 16);
+    const uint32_t in_kept = min(need, in_before);
+    uint32_t to = (prior & 0xffffu) + (listed ? 0u : min(need, n) - in_kept);
+    for (int w = w0; w < w1; ++w) {
+      uint32_t m = s_mask[w];
+      if (!listed) {
+        uint32_t q = s_in[w];
+        for (; q != 0u && n < need; ++n, q &= q - 1u) m |= q & (0u - q);
+      }
+      for (; m != 0u; m &= m - 1u) offs[to++] = 32u * w + __ffs(m) - 1u;
+    }
+    uint32_t kept = total & 0xffffu;
+    if (!listed) {
+      kept += min(need, in_before + (total >> 16)) - in_kept;
+      at += in_kept;
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < kept; i += THREADS) out[at + i] = t_lo + static_cast<int>(offs[i]);
+  } else {
+    // ---- longer slices, whose keys are read again.  Counts: forced keys and keys above the
+    // step, keys in it; the latter listed
+    const int per_warp = (runs + kWarps - 1) / kWarps;
+    const int v_lo = min(runs, warp * per_warp) * 32, v_hi = min(runs, (warp + 1) * per_warp) * 32;
+    uint32_t n_above = 0u, n_in = 0u;
+#pragma unroll 2
+    for (int i = v_lo + lane; i < v_hi; i += 32) {
+      const uint4 k = keys4(i);
+      n_above += (k.x > hi) + (k.y > hi) + (k.z > hi) + (k.w > hi);
+      if (k.x - lo <= last || k.y - lo <= last || k.z - lo <= last || k.w - lo <= last) {
+        const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (e[c] - lo <= last) {
+            ++n_in;
+            if (listed) s_list[atomicAdd(&s_count[2], 1u)] = entry(e[c], 4 * i + c);
+          }
+      }
+    }
+    n_above = __reduce_add_sync(0xffffffffu, n_above);
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
+    if (lane == 0) {
+      s_warp[0][warp] = n_above;
+      s_warp[1][warp] = n_in;
+    }
+    __syncthreads();
+    if (tid < 2) {
+      uint32_t v = 0u;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += s_warp[tid][i];
+      s_count[tid] = v;
+    }
+    row_sync();
+    uint32_t at = 0u, in_before = 0u;       // kept and in-step keys before this warp's runs
+    peers(&s_count[0], 0u);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < rank) at += from[r];
+    peers(&s_count[1], 0u);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < rank) in_before += from[r];
+    for (int v = 0; v < warp; ++v) {
+      at += s_warp[0][v];
+      in_before += s_warp[1][v];
+    }
+    uint64_t cut = ~0ull;
+    if (listed) {                           // the step's keys that stay: `cut` and what ranks before it
+      const uint32_t all = gather_lists();
+      __syncthreads();
+      for (uint32_t i = warp; i < all; i += kWarps) {
+        const uint64_t e = s_all[i];
+        uint32_t before = 0u;
+        for (uint32_t j = lane; j < all; j += 32) before += s_all[j] > e;
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (before == need - 1u && lane == 0) s_cut = e;
+      }
+      __syncthreads();
+      cut = s_cut;
+      uint32_t n = 0u;
+      for (uint32_t i = lane; i < all; i += 32) {
+        const uint64_t e = s_all[i];
+        n += e >= cut && 0xffffffffu - static_cast<uint32_t>(e) < static_cast<uint32_t>(t_lo + 4 * v_lo);
+      }
+      at += __reduce_add_sync(0xffffffffu, n);
+    } else {                                // one value: the first by position stay
+      at += min(need, in_before);
+    }
+    // ---- the kept positions, in order: a lane's four are consecutive
+#pragma unroll 2
+    for (int i = v_lo + lane; i < v_hi; i += 32) {
+      const uint4 k = keys4(i);
+      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+      uint32_t stay = 0u, in = 0u;          // a bit a key
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t m = __ballot_sync(0xffffffffu, (in >> c) & 1u);
-        before += __popc(m & below);
+        stay |= static_cast<uint32_t>(e[c] > hi) << c;
+        in |= static_cast<uint32_t>(e[c] - lo <= last) << c;
+      }
+      const uint32_t below = (1u << lane) - 1u;
+      if (__any_sync(0xffffffffu, in != 0u)) {
+        uint32_t before = 0u, all = 0u;     // in-step keys of earlier lanes, of all
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t m = __ballot_sync(0xffffffffu, (in >> c) & 1u);
+          before += __popc(m & below);
+          all += __popc(m);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((in >> c) & 1u) {
+            const uint64_t x = entry(e[c], 4 * i + c);
+            if (listed ? x >= cut : in_before + before < need) stay |= 1u << c;
+            ++before;
+          }
+        in_before += all;
+      }
+      uint32_t to = at, all = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t m = __ballot_sync(0xffffffffu, (stay >> c) & 1u);
+        to += __popc(m & below);
         all += __popc(m);
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if ((in >> c) & 1u) {
-          const uint64_t x = (static_cast<uint64_t>(e[c]) << 32) | (not_first - static_cast<uint32_t>(4 * i + c));
-          if (listed ? x >= cut : in_before + before < need) stay |= 1u << c;
-          ++before;
-        }
-      in_before += all;
+        if ((stay >> c) & 1u) out[to++] = t_lo + 4 * i + c;
+      at += all;
     }
-    uint32_t to = at, all = 0u;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t m = __ballot_sync(0xffffffffu, (stay >> c) & 1u);
-      to += __popc(m & below);
-      all += __popc(m);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if ((stay >> c) & 1u) out[to++] = t_lo + 4 * i + c;
-    at += all;
   }
   grid_dependents_launch();
   if constexpr (!ONE) cluster_sync();     // nobody leaves while its lists may be read
@@ -508,9 +649,9 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * Hkv;
-  // With rows for half the SMs or more, a row is one CTA of 1024 threads while it fits (44 us
-  // against 61 us in clusters of four on 256 rows of 32K: no exchange between CTAs, fewer
-  // barriers a key).  With fewer rows, 512 threads and the smallest cluster whose slices
+  // With rows for half the SMs or more, a row is one CTA of 1024 threads while it fits (30 us
+  // against 42 us in clusters of two and 54 in clusters of four with 512 threads each, on 256
+  // rows of 32K: no exchange between CTAs, fewer barriers a key).  With fewer rows, 512 threads and the smallest cluster whose slices
   // stay at kSelSlice keys, or more CTAs while the machine has room for them.
   const bool many = rows * 2 >= sms;
   const int slice_most = many ? kSelSliceMany : kSelSlice;
