@@ -9,7 +9,6 @@ also allocate the outputs (with torch) before calling the same entry points.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -655,11 +654,9 @@ def _on_stream(specs, dev_err, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _made_on(stream):
-    """Where a call makes tensors of its own: on its stream, so that their memory's earlier
-    users, a fill and the kernels follow each other."""
-    if stream is None:
-        return contextlib.nullcontext()
+def _as_current(stream):
+    """The context in which stream is the current one.  Calls that make tensors run in it:
+    their memory's earlier users, a fill and the kernels then follow each other."""
     if not isinstance(stream, torch.cuda.Stream):
         handle = int(getattr(stream, "cuda_stream", stream))
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
@@ -937,8 +934,12 @@ def accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path=N
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        with _made_on(stream):
-            out = torch.zeros((B, Hkv, max_pages * page), dtype=torch.float32, device=q.device)
+        if stream is not None:
+            with _as_current(stream):
+                return accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path,
+                                                   accept_len, weight, scale, cu_seqlens, None,
+                                                   dev_err)
+        out = torch.zeros((B, Hkv, max_pages * page), dtype=torch.float32, device=q.device)
     if cu_seqlens is None:
         jf_attention_weight(q, k_cache, block_table, prefix_len, lse, out, scale, path, accept_len,
                             weight, dev_err, stream)
@@ -951,11 +952,13 @@ def accumulate_attention_weight(q, k_cache, block_table, prefix_len, lse, path=N
 
 def select_kept_keys(weight, seq_len, budget, sink=0, recent=0, dev_err=None, stream=None):
     """(keep [B][Hkv][budget], kept_len [B]): the positions that stay, by weight."""
+    if stream is not None:
+        with _as_current(stream):
+            return select_kept_keys(weight, seq_len, budget, sink, recent, dev_err)
     B, Hkv, _ = weight.shape
-    with _made_on(stream):
-        keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weight.device)
-        kept_len = torch.empty((B,), dtype=torch.int32, device=weight.device)
-    jf_select_kept(weight, seq_len, keep, kept_len, sink, recent, dev_err, stream)
+    keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weight.device)
+    kept_len = torch.empty((B,), dtype=torch.int32, device=weight.device)
+    jf_select_kept(weight, seq_len, keep, kept_len, sink, recent, dev_err)
     return keep, kept_len
 
 
@@ -972,27 +975,30 @@ def evict_kv(k_cache, v_cache, block_table, seq_len, keep, kept_len, new_block_t
 
 def beam_select(logits, score, K, finished=None, eos_token=-1, stream=None):
     """(parent, token, score, finished), each [B][K]: the K best continuations of every prompt."""
+    if stream is not None:
+        with _as_current(stream):
+            return beam_select(logits, score, K, finished, eos_token)
     B, W, V = logits.shape
     dev = logits.device
-    with _made_on(stream):
-        parent = torch.empty((B, K), dtype=torch.int32, device=dev)
-        token = torch.empty((B, K), dtype=torch.int32, device=dev)
-        new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
-        new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
-        ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
-    jf_beam_select(logits, score, parent, token, new_score, ws, finished, eos_token, new_finished,
-                   stream)
+    parent = torch.empty((B, K), dtype=torch.int32, device=dev)
+    token = torch.empty((B, K), dtype=torch.int32, device=dev)
+    new_finished = torch.empty((B, K), dtype=torch.int32, device=dev)
+    new_score = torch.empty((B, K), dtype=torch.float32, device=dev)
+    ws = _workspace(jf_beam_select_workspace_size(B, W, V, K, _logit_dtype(logits)), dev)
+    jf_beam_select(logits, score, parent, token, new_score, ws, finished, eos_token, new_finished)
     return parent, token, new_score, new_finished
 
 
 def beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, dev_err=None,
                  stream=None):
     """(block_table [B * K][max_pages], prefix_len [B * K]) of the new beams."""
+    if stream is not None:
+        with _as_current(stream):
+            return beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, dev_err)
     B, K = parent.shape
-    with _made_on(stream):
-        new_table = torch.empty((B * K, block_table.shape[1]), dtype=torch.int32,
-                                device=block_table.device)
-        new_len = torch.empty((B * K,), dtype=torch.int32, device=block_table.device)
+    new_table = torch.empty((B * K, block_table.shape[1]), dtype=torch.int32,
+                            device=block_table.device)
+    new_len = torch.empty((B * K,), dtype=torch.int32, device=block_table.device)
     jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, new_table,
-                    new_len, dev_err, stream)
+                    new_len, dev_err)
     return new_table, new_len
