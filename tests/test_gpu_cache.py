@@ -433,6 +433,20 @@ def test_select_the_longest_slices(jf, rows, n, kind):
     assert (keep.cpu().numpy() == want).all()
 
 
+@pytest.mark.parametrize("n", [8192, 8193, 20480, 20481, 32768, 32769, 65536, 81921])
+@pytest.mark.parametrize("rows", [1, 200])
+def test_select_at_the_borders_of_the_forms(jf, rows, n):
+    """The longest rows that each form takes, and one key more, for few rows and for many."""
+    rng = np.random.default_rng(n)
+    w = np.exp(2 * rng.standard_normal(n)).astype(np.float32)
+    cap = (n + 15) // 16 * 16
+    full = torch.zeros(rows, 1, cap, device="cuda")
+    full[:, 0, :n] = dev(w)
+    keep, kept = jf.select_kept_keys(full, dev(np.full(rows, n, np.int32)), n // 3, sink=4, recent=37)
+    want, _ = ref.select_kept(w[None, None], np.array([n], np.int32), 4, 37, n // 3)
+    assert (kept == n // 3).all() and (keep.cpu().numpy() == want).all()
+
+
 @pytest.mark.parametrize("rows", [1, 80])
 @pytest.mark.parametrize("equal", [1, 255, 256, 257, 2000])
 def test_select_equal_keys_at_the_border(jf, rows, equal):

@@ -26,12 +26,13 @@ constexpr int kPage = 16;
 // What bounds the call is not the 8 bytes a key but, for a row of 32K in one CTA, in cycles:
 // the load 10,800, the counts 4,700, the bits 4,000, the list 1,700, the positions 4,300;
 // for few rows, the barriers between the steps.  256 rows of 32K: 30 us, of which the 256
-// CTAs on 152 SMs take two rounds.  (With a second pass of ballots for the positions, 1024
+// CTAs on 152 SMs take two rounds; 8 rows of 2304: 5.8 us, one call after the other.  (With a second pass of ballots for the positions, 1024
 // steps and lists of 1024: 40 us, and 87 us where a step held 700 keys.)
 // Keys that stay whatever they are (the first `sink`, the last `recent`) become kForced,
 // above every weight, and the padding 0, below every one, so no pass tests positions.
-constexpr int kSelSlice = 8192;           // keys of a CTA's slice with 512 threads, ..
-constexpr int kSelSliceMany = 32768;      // .. with 1024
+constexpr int kSelShort = 8192;           // keys of a row that 512 threads take alone, ..
+constexpr int kSelTwo = 20480;            // .. where two such CTAs share an SM, ..
+constexpr int kSelRow = 32768;            // .. that 1024 threads take alone
 constexpr int kSelMost = 192 * 1024 / 4;  // keys that fit on chip; longer slices are read again
 constexpr int kSelPad = 128;              // a slice fills whole 128-key runs of a warp
 constexpr int kSelList = 256;             // listed keys of a row
@@ -649,28 +650,32 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
   const long long rows = static_cast<long long>(B) * Hkv;
-  // With rows for half the SMs or more, a row is one CTA of 1024 threads while it fits (30 us
-  // against 42 us in clusters of two and 54 in clusters of four with 512 threads each, on 256
-  // rows of 32K: no exchange between CTAs, fewer barriers a key).  With fewer rows, 512 threads and the smallest cluster whose slices
-  // stay at kSelSlice keys, or more CTAs while the machine has room for them.
-  const bool many = rows * 2 >= sms;
-  const int slice_most = many ? kSelSliceMany : kSelSlice;
+  // A row up to kSelRow is one CTA: no exchanges.  Short ones take 512 threads (8 rows of
+  // 2304: 5.8 us against 6.2 with 1024 and 9.1 in clusters of two; 256 rows, 7.0 against 11.6),
+  // longer ones 1024 (80 rows of 16384: 10.1 against 12.1), unless there are more rows than
+  // SMs and two CTAs of 512 fit on each (256 rows of 16384: 16.2 against 19.3; of 20480: 19.8
+  // against 21.8).
+  // Longer rows are clusters of CTAs of 512 threads, with slices up to kSelTwo (256 rows of
+  // 64K: 84 us in fours, 92 in twos, 87 in twos of 1024 threads; 200 rows of 40000: 46 in
+  // twos, 56 in fours); of eight only where every CTA has an SM of its own (8 rows of
+  // 128K: 18 us against 25 in fours of 1024; but 32 rows: 28 against 22 in fours).
   int C = 1;
-  while (C < kMaxCluster && (capacity > C * slice_most || (!many && rows * C * 2 <= sms && capacity > C * 2048))) C *= 2;
+  if (capacity > kSelRow)
+    while (C < kMaxCluster && (capacity > C * kSelRow || (capacity > C * kSelTwo && (C < 4 || rows * 2 * C <= sms)))) C *= 2;
+  const bool wide = C == 1 && capacity > (rows > sms ? kSelTwo : kSelShort);
   const int slice = ((capacity + C - 1) / C + kSelPad - 1) / kSelPad * kSelPad;
   const bool resident = slice <= kSelMost;
-  // (a slice of a single CTA always fits)
-  auto* kernel = many ? (C == 1 ? select_kernel<1024, true, true> : resident ? select_kernel<1024, false, true>
-                                                                            : select_kernel<1024, false, false>)
-                      : (C == 1 ? select_kernel<512, true, true> : resident ? select_kernel<512, false, true>
-                                                                           : select_kernel<512, false, false>);
+  auto* kernel = wide       ? select_kernel<1024, true, true>
+                 : C == 1   ? select_kernel<512, true, true>
+                 : resident ? select_kernel<512, false, true>
+                            : select_kernel<512, false, false>;
   if (resident) {
-    static SmemAttr attr[4];
-    if (!attr[(many ? 2 : 0) + (C == 1 ? 1 : 0)].ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
+    static SmemAttr attr[3];
+    if (!attr[wide ? 2 : C == 1 ? 1 : 0].ensure(kernel, kSelMost * sizeof(uint32_t))) return JF_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
-  cfg.blockDim = dim3(many ? 1024 : 512);
+  cfg.blockDim = dim3(wide ? 1024 : 512);
   cfg.dynamicSmemBytes = resident ? static_cast<size_t>(slice) * sizeof(uint32_t) : 0;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attrs[2];
