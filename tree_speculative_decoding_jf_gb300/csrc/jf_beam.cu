@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   uint32_t* s_word = s_dyn;
   uint32_t* s_list = s_dyn + heads;
   const uint32_t* best = p.best + static_cast<size_t>(b) * heads;
+#pragma unroll 1
   for (int i = tid; i < heads; i += kMergeThreads)    // (those of beams that are not live are not used)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_word + i)), "l"(best + i) : "memory");
   for (int w = warp; w < W; w += kMergeWarps) {
@@ -383,9 +384,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       }
   } else {
     // Score words of the blocks' best pairs; 0 where a block has no pair above -inf.
+    // i / blocks for i < 2^13: the product's excess, i (recip - 2^32 / blocks), stays below
+    // 2^32 / blocks.  (This and the loops left rolled, since every step's code is fetched and
+    // run once: 14.9 -> 14.3 us a call on 1 x 4 x 151936.)
+    const uint32_t recip = 0xffffffffu / static_cast<uint32_t>(p.blocks) + 1u;
     uint32_t low = 0xffffffffu, high = 0u;
+#pragma unroll 1
     for (int i = tid; i < heads; i += kBoundThreads) {
-      const int w = i / p.blocks;
+      const int w = p.blocks == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), recip));
       const uint32_t k = s_word[i];
       uint32_t word = 0u;
       if (s_kind[w] == 0 && k > kNegInfKey) {
@@ -416,6 +422,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     if (low <= high) {
       constexpr int kMine = kBins / kBoundThreads;
       const int shift = max(0, 32 - __clz(high - low) - 10);
+#pragma unroll 1
       for (int i = tid; i < heads; i += kBoundThreads)
         if (s_word[i] != 0u) atomicAdd(&s_hist[(s_word[i] - low) >> shift], 1u);
       named_bar(1, kBoundThreads);
@@ -445,6 +452,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
         bound = max(1u, logit_key(at - 2.3841858e-7f * (most + fabsf(at)) - 9.5367432e-7f));
       }
     }
+#pragma unroll 1
     for (int i = tid; i < heads; i += kBoundThreads)
       if (s_word[i] >= bound) s_list[atomicAdd(&s_pass, 1)] = i;
     if (tid == 0) s_range[0] = bound;
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   for (int i = tid; i < all; i += kMergeThreads) {
     const uint32_t hi = s_all_hi[i];
     int rank = 0, equal = 0;
-#pragma unroll 4
+#pragma unroll 1
     for (int j = 0; j < all / 4; ++j) {
       const uint4 h = reinterpret_cast<const uint4*>(s_all_hi)[j];
       rank += (h.x > hi) + (h.y > hi) + (h.z > hi) + (h.w > hi);
