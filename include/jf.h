@@ -568,7 +568,7 @@ jf_status jf_attention_weight_packed(const void* q, const void* k_cache, const i
  *   keep      int32 [B][Hkv][budget]: the kept positions in rising order, then -1.
  *   kept_len  int32 [B]: min(L_b, budget).
  * Limits: sink, recent >= 0, 1 <= budget, sink + recent <= budget; capacity and budget
- * up to 2^30.
+ * up to 2^30; keep and kept_len must not overlap seq_len (JF_ERR_INVALID_ARGUMENT).
  */
 jf_status jf_select_kept(const float* weight, const int32_t* seq_len, int32_t B, int32_t Hkv,
                          int32_t capacity, int32_t sink, int32_t recent, int32_t budget,

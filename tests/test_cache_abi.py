@@ -51,6 +51,18 @@ def test_select_refusals(lib):
                        (4, (1 << 30) + 1, 3), (7, (1 << 30) + 1, 3), (2, 1 << 28, 3)])
 
 
+def test_select_refuses_lengths_in_place(lib):
+    """Other heads' blocks read the lengths while the first head's writes the kept ones."""
+    fn = lib.jf_select_kept
+    fn.argtypes = [P, P] + [i32] * 6 + [P, P, P, P]
+    at = ctypes.c_void_p
+    #       w     len          B  H  cap  sink rec budget keep kept
+    args = [FAKE, at(0x20000), 4, 2, 100, 4, 10, 50, at(0x30000), at(0x40000), None, None]
+    refused(fn, args, [(9, at(0x20000), 1),              # kept_len is seq_len
+                       (9, at(0x2000C), 1), (9, at(0x1FFF4), 1),     # it shares one element
+                       (8, at(0x20000), 1), (8, at(0x20000 - 4 * 4 * 2 * 50 + 4), 1)])   # so does keep
+
+
 def test_evict_refusals(lib):
     fn = lib.jf_evict_kv
     fn.argtypes = [P] * 9 + [i32] * 7 + [P, P]

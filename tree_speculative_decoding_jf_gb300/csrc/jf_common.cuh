@@ -14,6 +14,12 @@ inline bool aligned_to(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
 
+// Whether two arrays share a byte.
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
 inline jf_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }

@@ -647,9 +647,15 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
     return JF_ERR_INVALID_ARGUMENT;
   if (capacity > (1 << 30) || budget > (1 << 30) || static_cast<long long>(B) * Hkv > (1ll << 27))
     return JF_ERR_UNSUPPORTED;
+  // (every CTA of a sequence reads its length, at a time of its own; CTAs of one cluster that
+  // saw different ones would wait for each other)
+  const long long rows = static_cast<long long>(B) * Hkv;
+  const size_t len_bytes = sizeof(int32_t) * static_cast<size_t>(B);
+  if (overlap(kept_len, len_bytes, seq_len, len_bytes) ||
+      overlap(keep, sizeof(int32_t) * static_cast<size_t>(rows) * static_cast<size_t>(budget), seq_len, len_bytes))
+    return JF_ERR_INVALID_ARGUMENT;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  const long long rows = static_cast<long long>(B) * Hkv;
   // A row up to kSelRow is one CTA: no exchanges.  Short ones take 512 threads (8 rows of
   // 2304: 5.8 us against 6.2 with 1024 and 9.1 in clusters of two; 256 rows, 7.0 against 11.6),
   // longer ones 1024 (80 rows of 16384: 10.1 against 12.1), unless there are more rows than
