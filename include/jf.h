@@ -530,8 +530,8 @@ jf_status jf_compact_accepted_kv(void* k_cache, void* v_cache, const int32_t* bl
  *   lse          float [B][Hq][N], written by the attention call for the same keys.  A row
  *                whose lse is -inf attended to nothing and adds nothing.
  *   weight       float [B][Hkv][max_pages * page_size], or NULL for zero.
- *   weight_out   the same shape; may be weight itself.  Positions t >= P_b + R_b are left
- *                as they were.
+ *   weight_out   the same shape; may be weight itself, and must not otherwise overlap it.
+ *                Positions t >= P_b + R_b are left as they were.
  *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + R_b past the block table),
  *                _BAD_PATH (accept_len or a path entry out of range), _BAD_PAGE, _TIMEOUT,
  *                and _BAD_TREE_LEN for the packed call.  May be NULL.
@@ -620,8 +620,8 @@ jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
  *   logits     [B][W][V] bf16 or fp32 (dtype); -inf marks a token that may not be chosen;
  *              with NaN or +inf the prompt's outputs are unspecified, but every parent and
  *              token is in range (entries without a pair: 0, 0 and a NaN score).
- *   score      float [B][W]; must not be new_score.
- *   finished   int32 [B][W] or NULL; must not be new_finished.  eos_token: -1 for none, in
+ *   score      float [B][W]; must not overlap new_score.
+ *   finished   int32 [B][W] or NULL; must not overlap new_finished.  eos_token: -1 for none, in
  *              [0, V) where finished is given.
  *   workspace  at least jf_beam_select_workspace_size(...) bytes, 8-byte aligned, no
  *              initialisation.
@@ -647,8 +647,8 @@ jf_status jf_beam_select(const void* logits, int32_t dtype, const float* score,
  *   parent            int32 [B][K] as written by jf_beam_select.
  *   fresh_page        int32 [B][K]: distinct pages that no sequence uses.  Where P fills the
  *                     whole block table none is used.
- *   new_block_table   int32 [B * K][max_pages]; new_prefix_len int32 [B * K].  Must not be
- *                     block_table and prefix_len.
+ *   new_block_table   int32 [B * K][max_pages]; new_prefix_len int32 [B * K].  Must not
+ *                     overlap block_table and prefix_len.
  *   dev_err           JF_DEVERR_BAD_PATH (parent; the beam then gets length 0 and no pages),
  *                     _BAD_PREFIX (the same), _BAD_PAGE.  May be NULL.
  * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned.

@@ -101,6 +101,34 @@ def test_beam_fork_refusals(lib):
              (10, 96, 3), (11, 8, 3), (0, ODD, 7), (1, ODD, 7)])
 
 
+def test_arrays_that_overlap_in_part_are_refused(lib):
+    """An output whose blocks write where others still read."""
+    at = ctypes.c_void_p
+    fn = lib.jf_attention_weight
+    fn.argtypes = [P] * 8 + [i32] * 8 + [f32, P, P, P]
+    w, n = 0x100000, 4 * 2 * 8 * 160           # weight [2][8][160]
+    args = [FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, at(w), 2, 16, 32, 8, 128, 16, 10, 10, 0.1, at(2 * w), None, None]
+    refused(fn, args, [(17, at(w + 4), 1), (17, at(w + n - 4), 1), (17, at(w - n + 4), 1)])
+    fn = lib.jf_attention_weight_packed
+    fn.argtypes = [P] * 9 + [i32] * 9 + [f32, P, P, P]
+    args = [FAKE] * 8 + [at(w), 2, 16, 20, 32, 8, 128, 16, 10, 10, 0.1, at(2 * w), None, None]
+    refused(fn, args, [(19, at(w + n - 4), 1)])
+    fn = lib.jf_evict_kv
+    fn.argtypes = [P] * 9 + [i32] * 7 + [P, P]
+    args = [FAKE, FAKE, FAKE, OTHER, FAKE, FAKE, None, at(w), at(2 * w), 2, 8, 128, 20, 16, 10, 10, None, None]
+    refused(fn, args, [(8, at(w + 4), 1), (8, at(w + n - 4), 1), (8, at(w - n + 4), 1)])
+    fn = lib.jf_beam_select
+    fn.argtypes = [P, i32, P, P, i32, i32, i32, i32, i32, P, P, P, P, P, sz, P]
+    s, f = 0x30000, 0x40000                    # score and finished [2][4], the outputs [2][8]
+    args = [FAKE, 0, at(s), at(f), 5, 2, 4, 100, 8, FAKE, FAKE, at(0x50000), at(0x60000), at(0x70000), 1 << 20, None]
+    refused(fn, args, [(11, at(s + 28), 1), (11, at(s - 60), 1), (12, at(f + 28), 1), (12, at(f - 60), 1)])
+    fn = lib.jf_beam_fork_kv
+    fn.argtypes = [P] * 6 + [i32] * 8 + [P, P, P, P]
+    t, m = 0x30000, 0x40000                    # block_table [8][10], prefix_len [8]; the new ones [6][10], [6]
+    args = [FAKE, FAKE, at(t), at(m), FAKE, FAKE, 2, 4, 3, 2, 128, 16, 10, 10, at(0x50000), at(0x60000), None, None]
+    refused(fn, args, [(14, at(t + 4 * 79), 1), (14, at(t - 4 * 59), 1), (15, at(m + 28), 1), (15, at(m - 20), 1)])
+
+
 @pytest.mark.gpu
 def test_wrappers_refuse_bad_tensors():
     from tree_speculative_decoding_jf_gb300 import jf

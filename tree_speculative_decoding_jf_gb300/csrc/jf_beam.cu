@@ -739,8 +739,12 @@ extern "C" jf_status jf_beam_select(const void* logits, int32_t dtype, const flo
     return JF_ERR_INVALID_ARGUMENT;
   if (eos_token < -1 || eos_token >= V || (finished != nullptr && eos_token < 0))
     return JF_ERR_INVALID_ARGUMENT;
-  if (new_score == score || (finished != nullptr && new_finished == finished)) return JF_ERR_INVALID_ARGUMENT;
   if (!beam_supported(B, W, V, K)) return JF_ERR_UNSUPPORTED;
+  // (one prompt's block writes while another's still reads)
+  const size_t beams = sizeof(int32_t) * static_cast<size_t>(B) * W, pairs = sizeof(int32_t) * static_cast<size_t>(B) * K;
+  if (overlap(new_score, pairs, score, beams) ||
+      (finished != nullptr && new_finished != nullptr && overlap(new_finished, pairs, finished, beams)))
+    return JF_ERR_INVALID_ARGUMENT;
   if (!aligned_to(logits, dtype == JF_DTYPE_BF16 ? 2 : 4) || !aligned_to(workspace, 8)) return JF_ERR_MISALIGNED;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
@@ -786,9 +790,13 @@ extern "C" jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t
       parent == nullptr || fresh_page == nullptr || new_block_table == nullptr || new_prefix_len == nullptr)
     return JF_ERR_INVALID_ARGUMENT;
   if (B < 1 || W < 1 || K < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1) return JF_ERR_INVALID_ARGUMENT;
-  if (new_block_table == block_table || new_prefix_len == prefix_len) return JF_ERR_INVALID_ARGUMENT;
   if ((D != 64 && D != 128) || page_size != kPage || Hkv > 65535 || max_pages > (1 << 26)) return JF_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * std::max(W, K) >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  // (one beam's blocks write while another's still read)
+  const size_t olds = sizeof(int32_t) * static_cast<size_t>(B) * W, news = sizeof(int32_t) * static_cast<size_t>(B) * K;
+  if (overlap(new_block_table, news * max_pages, block_table, olds * max_pages) ||
+      overlap(new_prefix_len, news, prefix_len, olds))
+    return JF_ERR_INVALID_ARGUMENT;
   if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16)) return JF_ERR_MISALIGNED;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;

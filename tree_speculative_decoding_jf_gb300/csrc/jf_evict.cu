@@ -713,6 +713,9 @@ extern "C" jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* bl
   if ((D != 64 && D != 128) || page_size != kPage) return JF_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hkv > (1ll << 26) || max_pages > (1 << 26) || budget > (1 << 30))
     return JF_ERR_UNSUPPORTED;
+  const size_t weight_bytes = sizeof(float) * static_cast<size_t>(B) * Hkv * max_pages * kPage;
+  if (weight != nullptr && weight != weight_out && overlap(weight, weight_bytes, weight_out, weight_bytes))
+    return JF_ERR_INVALID_ARGUMENT;
   if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16)) return JF_ERR_MISALIGNED;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;

@@ -657,6 +657,9 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
     return JF_ERR_UNSUPPORTED;
   if (cu != nullptr && T < 1) return JF_ERR_INVALID_ARGUMENT;
   if (cu != nullptr && static_cast<long long>(T) + N >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  const size_t weight_bytes = sizeof(float) * static_cast<size_t>(B) * Hkv * max_pages * kPage;
+  if (weight != nullptr && weight != weight_out && overlap(weight, weight_bytes, weight_out, weight_bytes))
+    return JF_ERR_INVALID_ARGUMENT;
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16)) return JF_ERR_MISALIGNED;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
