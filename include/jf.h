@@ -592,8 +592,8 @@ jf_status jf_select_kept(const float* weight, const int32_t* seq_len, int32_t B,
  *                    same array, and must not otherwise overlap.
  *   dev_err          JF_DEVERR_BAD_PREFIX (seq_len), _BAD_PATH (kept_len or keep malformed),
  *                    _BAD_PAGE.  May be NULL.
- * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned, kept_len != seq_len (the
- * arrays).
+ * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned, num_pages * page_size < 2^31,
+ * kept_len != seq_len (the arrays).
  */
 jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
                       const int32_t* seq_len, const int32_t* keep, const int32_t* kept_len,

@@ -75,6 +75,14 @@ def test_evict_refusals(lib):
                        (0, ODD, 7), (1, ODD, 7)])
 
 
+def test_evict_refuses_pools_whose_rows_pass_32_bits(lib):
+    """Pool rows (page * 16 + slot) are 32-bit: a row past them would silently stay in place."""
+    fn = lib.jf_evict_kv
+    fn.argtypes = [P] * 9 + [i32] * 7 + [P, P]
+    args = [FAKE, FAKE, FAKE, OTHER, FAKE, FAKE, None, None, None, 1, 2, 128, 20, 16, 10, 10, None, None]
+    refused(fn, args, [(15, 1 << 27, 3), (15, 0x7FFFFFFF, 3)])
+
+
 def test_beam_select_refusals(lib):
     size = lib.jf_beam_select_workspace_size
     size.argtypes, size.restype = [i32] * 5, sz

@@ -711,7 +711,8 @@ extern "C" jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* bl
   if (B < 1 || Hkv < 1 || budget < 1 || max_pages < 1 || num_pages < 1) return JF_ERR_INVALID_ARGUMENT;
   if (kept_len == seq_len) return JF_ERR_INVALID_ARGUMENT;
   if ((D != 64 && D != 128) || page_size != kPage) return JF_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hkv > (1ll << 26) || max_pages > (1 << 26) || budget > (1 << 30))
+  if (static_cast<long long>(B) * Hkv > (1ll << 26) || max_pages > (1 << 26) || budget > (1 << 30) ||
+      static_cast<long long>(num_pages) * kPage >= (1ll << 31))
     return JF_ERR_UNSUPPORTED;
   const size_t weight_bytes = sizeof(float) * static_cast<size_t>(B) * Hkv * max_pages * kPage;
   if (weight != nullptr && weight != weight_out && overlap(weight, weight_bytes, weight_out, weight_bytes))
