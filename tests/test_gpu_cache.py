@@ -312,6 +312,77 @@ def test_tensors_of_a_call_on_a_given_stream(jf):
     assert torch.equal(got[0], want_keep) and torch.equal(got[1], want_len)
 
 
+@pytest.mark.parametrize("prefix,rows,N,Hq,Hkv,D,path", [
+    ([200, 70], [5, 3], 8, 12, 4, 64, True),               # G = 3: rows do not fill 32 columns
+    ([300], [45], 64, 6, 2, 128, False),                   # 135 rows: a full block of 126 and a rest
+    ([130, 9], [1, 1], 1, 8, 2, 128, False),               # one token
+])
+def test_weight_of_keys_with_infinities(jf, prefix, rows, N, Hq, Hkv, D, path):
+    """A cached key whose scores are all -inf receives nothing: its weight and the others' stay
+    what they are without it."""
+    c = weight_case(31, prefix, rows, N, Hq, Hkv, D, path)
+    c["q"][..., 5] = c["q"][..., 5].abs() + 0.25            # (the lse is an input like any other)
+    lse = torch.full_like(c["lse"], 6.0)
+    k = c["k"].clone()
+    at = [(b, t) for b, P in enumerate(prefix) for t in (0, P // 2, P - 1)]
+    for b, t in at:
+        k[c["table"][b, t // PAGE].long(), t % PAGE, :, 5] = -float("inf")
+    got = jf.accumulate_attention_weight(c["q"], k, c["table"], c["prefix"], lse, path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"].clone())
+    plain = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], lse, path=c["path"],
+                                           accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                           out=c["out"].clone())
+    want = plain.clone()
+    for b, t in at:
+        want[b, :, t] = c["weight"][b, :, t]
+    assert torch.equal(got, want)
+    # +inf with these lse is an infinite weight for the rows that see the key, and for no other key
+    b, t = len(prefix) - 1, prefix[-1] // 2
+    k = c["k"].clone()
+    k[c["table"][b, t // PAGE].long(), t % PAGE, :, 5] = float("inf")
+    got = jf.accumulate_attention_weight(c["q"], k, c["table"], c["prefix"], lse, path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"].clone())
+    assert torch.isposinf(got[b, :, t]).all()
+    plain[b, :, t] = float("inf")
+    assert torch.equal(got, plain)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (12, 4, 128), (4, 4, 128)])
+def test_weight_where_dead_rows_alone_see_nan(jf, Hq, Hkv, D):
+    """Keys (NaN here) that only rows with an lse of -inf see keep their weight: a padded
+    sequence whose rows attended to nothing, and the later rows of another."""
+    prefix, rows = [90, 40, 0], [6, 4, 2]
+    dead = {(0, 4), (0, 5)} | {(b, k) for b in (1, 2) for k in range(4)}
+    c = weight_case(32, prefix, rows, 8, Hq, Hkv, D, True, dead_rows=dead)
+    k = c["k"].clone()
+    seen = [(0, 94), (0, 95)] + [(1, t) for t in range(44)] + [(2, 0), (2, 1)]
+    for b, t in seen:
+        k[c["table"][b, t // PAGE].long(), t % PAGE] = float("nan")
+    c["q"][1, c["path"][1, 2].long()] = float("nan")       # a dead row's query may hold anything
+    got = jf.accumulate_attention_weight(c["q"], k, c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"])
+    close(got, c["want"], c["tol"])
+    for b, t in seen:
+        assert torch.equal(got[b, :, t], c["weight"][b, :, t] if t < prefix[b] else torch.zeros(Hkv, device="cuda"))
+
+
+def test_weight_of_nan_keys_is_nan(jf):
+    """A NaN key that a live row sees is a NaN weight, at its own position alone."""
+    c = weight_case(33, [300], [5], 8, 12, 4, 128, True)
+    k = c["k"].clone()
+    k[c["table"][0, 130 // PAGE].long(), 130 % PAGE, 1, 7] = float("nan")
+    got = jf.accumulate_attention_weight(c["q"], k, c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"])
+    want, tol = c["want"].copy(), c["tol"]
+    assert torch.isnan(got[0, 1, 130])
+    got[0, 1, 130] = want[0, 1, 130] = 0.0
+    close(got, want, tol)
+
+
 # ------------------------------------------------------------------------------- kept positions
 
 def run_select(jf, w, L, budget, sink, recent):

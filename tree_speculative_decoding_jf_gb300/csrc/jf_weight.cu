@@ -40,8 +40,12 @@
 // window, whose products take 71: 114 without the MMAs, 103 without the exponentials, 79 with
 // the TMEM loads and the waits alone).
 // Slots past a block's rows and rows whose lse is -inf get zero queries and lse = +inf, so
-// they add exp(-inf) = 0.  Keys past the sequence's end are lanes whose sum is dropped:
-// whatever their page slots hold stays in their lane.
+// they add exp(-inf) = 0.  Only with an infinity or a NaN in the key is such a score not zero
+// but NaN (0 * inf): one such column of the block tells, and its warp then leaves them all out
+// (122 against 119 us on the window, nothing on the others; testing every column of a block
+// that has any, 82 against 57 us on a window of three heads a group).
+// Keys past the sequence's end are lanes whose sum is dropped: whatever their page slots hold
+// stays in their lane.
 // All waits are bounded; on a timeout the CTA records JF_DEVERR_TIMEOUT, drains its copies
 // and MMAs, frees TMEM and returns.
 #include <algorithm>
@@ -170,7 +174,8 @@ __device__ __forceinline__ int block_cols(const SeqInfo& s, int qb, int nodes, i
   return (min(nodes, s.R - qb * nodes) * G + 31) & ~31;
 }
 
-// Adds 16 columns' probabilities 2^(s * c + nlse) to acc; MASKED: only columns j >= j_min.
+// Adds 16 columns' probabilities 2^(s * c + nlse) to acc; MASKED: only columns j >= j_min of
+// rows that add something (nlse above -inf), whatever the others' scores are.
 // (One instantiation with the test inside has a branch every four columns, which keeps the
 // compiler from overlapping them: 237 cycles for each four instead of about 20.)
 template <bool MASKED>
@@ -184,10 +189,10 @@ __device__ __forceinline__ void add16(const uint32_t (&sv)[16], const float* nls
     f2_split(ffma2(f2(__uint_as_float(sv[4 * v]), __uint_as_float(sv[4 * v + 1])), c2, f2(l.x, l.y)), x0, x1);
     f2_split(ffma2(f2(__uint_as_float(sv[4 * v + 2]), __uint_as_float(sv[4 * v + 3])), c2, f2(l.z, l.w)), x2, x3);
     if constexpr (MASKED) {
-      x0 = 4 * v + 0 < j_min ? -INFINITY : x0;
-      x1 = 4 * v + 1 < j_min ? -INFINITY : x1;
-      x2 = 4 * v + 2 < j_min ? -INFINITY : x2;
-      x3 = 4 * v + 3 < j_min ? -INFINITY : x3;
+      x0 = 4 * v + 0 < j_min || l.x == -INFINITY ? -INFINITY : x0;
+      x1 = 4 * v + 1 < j_min || l.y == -INFINITY ? -INFINITY : x1;
+      x2 = 4 * v + 2 < j_min || l.z == -INFINITY ? -INFINITY : x2;
+      x3 = 4 * v + 3 < j_min || l.w == -INFINITY ? -INFINITY : x3;
     }
     acc[0] = fadd2(acc[0], f2(fast_exp2(x0), fast_exp2(x1)));
     acc[1] = fadd2(acc[1], f2(fast_exp2(x2), fast_exp2(x3)));
@@ -229,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t l_full[C::kLseStages], l_empty[C::kLseStages];
   __shared__ uint64_t s_full[kSlots], s_empty[kSlots], fin;
   __shared__ __align__(16) float s_nlse[C::kLseStages][kRowBlock];   // -lse in log2 units
+  __shared__ int s_idle[C::kLseStages];       // a column of the block that adds nothing; kRowBlock: none
   __shared__ Range s_range;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Four rows a lane: their lse, asked for before the stage is free.
       float nl[kRowBlock / 32];
-      bool dead = false;
+      int dead = kRowBlock;                   // a row that adds nothing
 #pragma unroll
       for (int u = 0; u < kRowBlock / 32; ++u) {
         const int r = u * 32 + lane, k = r / G, h = g * G + r - k * G;
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             : __ldg(p.lse + (static_cast<size_t>(b) * p.Hq + h) * p.N + node);
           if (lse != -INFINITY) nl[u] = -lse * kLog2e;
         }
-        dead |= nl[u] == -INFINITY;           // (lse = +inf as well: it adds nothing)
+        if (nl[u] == -INFINITY) dead = r;     // (lse = +inf as well: it adds nothing)
       }
       const int ls = no % C::kLseStages;
       if (!wait_lanes(&q_empty[stage], (static_cast<uint32_t>(no / C::kQStages) & 1u) ^ 1u, abort, wlim) ||
@@ -485,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++mine;
 #pragma unroll
       for (int u = 0; u < kRowBlock / 32; ++u) s_nlse[ls][u * 32 + lane] = nl[u];
+      const int idle = __reduce_min_sync(0xffffffffu, dead);
+      const bool rare = idle < kRowBlock;
+      if (lane == 0) s_idle[ls] = rows < cols ? rows : idle;
       for (int i = lane; i < (cols - rows) * kVecs; i += 32) zero_row(rows + i / kVecs, i % kVecs);
       fence_proxy_async_smem();
       // A block with rows that add nothing lands on a barrier of its own: those rows are
       // zeroed before the MMA warp hears of it, whatever their queries hold.
-      const bool rare = __any_sync(0xffffffffu, dead);
       uint64_t* bar = rare ? &q_raw[stage] : &q_full[stage];
       const bool whole = p.path == nullptr && nb == nodes;
       int boxes = nb;
@@ -557,10 +565,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // Adds the block's probabilities to acc; row j of the block counts if j >= j_min.
     auto add_block = [&](int ls, int cols, int j_min, uint64_t (&acc)[2]) -> bool {
+      const int idle = s_idle[ls];            // (the same in every lane; so is the branch, as the load wants it)
       if (!wait_lanes(&s_full[slot], phase, abort, wlim)) return false;
       phase ^= 1u;
       tc_fence_after();
-      if (__all_sync(0xffffffffu, j_min <= 0))
+      uint32_t zero = 0u;
+      if (idle < kRowBlock) zero = tmem_ld1(t_addr + slot * kRowBlock + idle);
+      if (__all_sync(0xffffffffu, j_min <= 0 & __uint_as_float(zero) == 0.f))
         add_columns<false>(t_addr + slot * kRowBlock, s_nlse[ls], cols, j_min, c2, acc);
       else
         add_columns<true>(t_addr + slot * kRowBlock, s_nlse[ls], cols, j_min, c2, acc);
