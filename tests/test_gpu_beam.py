@@ -278,3 +278,43 @@ def test_fork_reports_bad_input_and_stays_in_bounds(jf):
             assert (table[j].cpu().numpy() == want_table[j]).all() and new_len[j].item() == want_len[j]
         if what in ("parent", "len"):
             assert new_len[2].item() == 0 and (table[2] == -1).all()
+
+
+@pytest.mark.parametrize("low", ["lowest", -1e30, -1e12])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_masks_of_the_lowest_value(jf, dtype, low):
+    """Tokens masked with a finite value: a beam that has nothing else spreads its score evenly,
+    score - log V each, and does not outrank one with tokens of its own.  Scores against
+    (score - log sum exp(x - max)) + (x - max) in 64 bits, where nothing large cancels; the
+    fp32 sum of the exponentials is within 2^-17 of it (with u = 2^-24: 29 u for a slice of
+    one step and 6 u for each of up to five, 2.25 u times the unmasked logits' span, below 16;
+    masked ones underflow), and new_score is rounded once more."""
+    low = torch.finfo(dtype).min if low == "lowest" else low
+    rng = np.random.default_rng(41)
+    B, W, V, K = 4, 3, 5003, 20
+    logits = rng.standard_normal((B, W, V)) * 2
+    allowed = rng.permutation(V)[:7]
+    logits[0, 1] = low                         # all masked, beside two beams that are not
+    logits[1] = low                            # a prompt with nothing else
+    keep = logits[2, :, allowed].copy()
+    logits[2] = low                            # seven tokens allowed in each beam
+    logits[2, :, allowed] = keep
+    logits[3, 0] = low
+    logits[3, 1, ::2] = low
+    score = np.array([[-1.0, -1.0, -2.5], [-1.0, -0.5, -3.0], [-2.0, -1.0, -4.0], [-0.25, -9.0, -1.0]], np.float32)
+    t = torch.from_numpy(logits.astype(np.float32)).to(dtype)
+    parent, token, new_score, _ = (x.cpu().numpy() for x in jf.beam_select(t.cuda(), dev(score), K))
+    x = t.double().numpy()
+    d = x - x.max(-1, keepdims=True)
+    s = (score.astype(np.float64)[..., None] - np.log(np.exp(d).sum(-1, keepdims=True))) + d
+    tol = 2.0 ** -17
+    for b in range(B):
+        flat = s[b].reshape(-1)
+        order = np.lexsort((np.arange(flat.size), -flat))[:K]
+        pick = parent[b].astype(np.int64) * V + token[b]
+        assert len(set(pick.tolist())) == K
+        assert (np.abs(flat[pick] - flat[order]) <= 2 * tol + 2.0 ** -50 * np.abs(flat[order])).all(), b
+        assert (np.abs(new_score[b] - flat[pick]) <= tol + 2.0 ** -24 * np.abs(flat[pick])).all(), b
+        for w in range(W):                     # in a beam: by logit, then by token
+            mine = pick[parent[b] == w]
+            assert (mine == np.lexsort((np.arange(V), -x[b, w]))[:len(mine)] + w * V).all(), (b, w)

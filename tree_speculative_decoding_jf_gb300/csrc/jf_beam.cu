@@ -286,25 +286,29 @@ __device__ __noinline__ int cut_back(uint64_t* key, uint32_t* flat, int n, int K
   return min(n, K);
 }
 
-// fp32 score as an ordered word.
-__device__ __forceinline__ uint32_t score_word(float off, float x) { return logit_key(off + x); }
+// A pair's score is off + (x - M), with its beam's off = score - log(sum exp(x - M)) and greatest
+// logit M: x - M is small where it counts, however far from zero the logits are.  (With M in off
+// instead, a beam whose tokens are all masked with the type's lowest value loses its score and its
+// logarithm to the rounding of M, and outranks the others.)  Here in fp32, as an ordered word.
+__device__ __forceinline__ uint32_t score_word(float off, float M, float x) { return logit_key(off + (x - M)); }
 
 // One CTA per prompt: the log-sum-exp of every beam, the bound from the blocks' best pairs,
 // the pairs of the blocks that reach it, their ranking.  A chain of small dependent steps
 // bounds the call, so half the warps form the bound from fp32 scores while the others take
-// the fp64 logarithms that the ranking wants.  An fp32 score, off + x, is off by at most
-// 2^-24 times the sizes of what its roundings round (score and M of the beam, the logarithm,
-// off, and the score itself) and 2^-22 for logf (below 25): the bound is lowered by four
-// times as much.
+// the fp64 logarithms that the ranking wants.  An fp32 score s is off by 2^-24 times the sizes
+// of what is rounded (off, x - M, which is at most |off| + |s|, and s) and 2^-19 for logf (below
+// 25): in all 2^-23 (|off| + |s|) + 2^-19.  A pair among the K best may stand below the K-th
+// block's word by twice that, so the bound is lowered by 2^-22 (|score| + 32 + |off| + |s|) and
+// a little more.
 constexpr int kBoundThreads = kMergeThreads / 2;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
   using R = Row<T>;
   constexpr int VN = R::kN;
   extern __shared__ uint32_t s_dyn[];     // [heads]: score words, then [heads]: blocks that pass
-  __shared__ double s_off[kMaxK];         // score - lse
+  __shared__ double s_off[kMaxK];         // score - log of the sum
   __shared__ float s_off32[kMaxK], s_mag[kMaxK];
-  __shared__ float s_stat[3][kMaxK];      // maximum, and sum of exponentials in two parts
+  __shared__ float s_stat[3][kMaxK];      // maximum (0 without logits above -inf), sum of exponentials in two parts
   __shared__ int s_kind[kMaxK];           // 0 live, 1 finished, 2 without a score
   __shared__ uint32_t s_hist[kBins];
   __shared__ uint64_t s_key[kMergeWarps][kListCap];
@@ -344,15 +348,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
           const float x = __shfl_xor_sync(0xffffffffu, hi, o), y = __shfl_xor_sync(0xffffffffu, lo, o);
           two_sum(hi, lo, x, y);
         }
-        off = sc - (M + logf(hi));
-        mag = fabsf(sc) + 2.f * fabsf(M) + 32.f;
+        off = sc - logf(hi);
+        mag = fabsf(sc) + 32.f;
       }
     }
     if (lane == 0) {
       s_kind[w] = over ? 1 : (sc == -INFINITY ? 2 : 0);
       s_off32[w] = off;
       s_mag[w] = mag;
-      s_stat[0][w] = M;
+      s_stat[0][w] = M == -INFINITY ? 0.f : M;
       s_stat[1][w] = hi;
       s_stat[2][w] = lo;
     }
@@ -372,8 +376,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     for (int w = warp - kBoundThreads / 32; w < W; w += kMergeWarps / 2)
       if (lane == 0) {
         double off = p.score[b * W + w];
-        if (s_kind[w] == 0 && s_stat[0][w] != -INFINITY)
-          off -= static_cast<double>(s_stat[0][w]) + log_fp64(static_cast<double>(s_stat[1][w]) + s_stat[2][w]);
+        if (s_kind[w] == 0 && s_stat[1][w] != 0.f)
+          off -= log_fp64(static_cast<double>(s_stat[1][w]) + s_stat[2][w]);
         s_off[w] = off;
         if (s_kind[w] == 1 && off != -INFINITY) {
           const int n = atomicAdd(&s_n, 1);
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       const uint32_t k = s_word[i];
       uint32_t word = 0u;
       if (s_kind[w] == 0 && k > kNegInfKey) {
-        word = score_word(s_off32[w], key_logit(k));
+        word = score_word(s_off32[w], s_stat[0][w], key_logit(k));
         if (word != 0u) {
           low = min(low, word);
           high = max(high, word);
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   for (int i = warp; i < pass; i += kMergeWarps) {
     const int id = s_list[i], w = id / p.blocks, block = id - w * p.blocks;
     const double off = s_off[w];
-    const float off32 = s_off32[w];
+    const float off32 = s_off32[w], M = s_stat[0][w];
     const RowVecs<T> r(p.logits, b * W + w, p.V);
     for (int v0 = 0; v0 < p.block_vecs; v0 += kStepVecs) {
       uint4 v[kStep];
@@ -481,9 +485,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       for (int u = 0; u < kStep; ++u) {
         const float most = R::vmax(v[u]);
         const int first = r.first(block * p.block_vecs + v0 + u * 32 + lane);
-        bool look = score_word(off32, most) >= bound;
+        bool look = score_word(off32, M, most) >= bound;
         if (look && last.key != 0ull)         // (many equal logits: nothing here ranks before the K-th)
-          look = before(Pair{score_key(off + static_cast<double>(most)),
+          look = before(Pair{score_key(off + (static_cast<double>(most) - M)),
                              static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(max(first, 0))}, last);
         uint32_t some = __ballot_sync(0xffffffffu, look);
         // One passing vector (there are few) after the other, a lane a logit.
@@ -499,10 +503,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
 #pragma unroll
           for (int c = 0; c < VN; ++c)
             if (lane == c) x = R::get(t, c);
-          bool in = x != -INFINITY && score_word(off32, x) >= bound && token >= 0 && token < p.V;
+          bool in = x != -INFINITY && score_word(off32, M, x) >= bound && token >= 0 && token < p.V;
           Pair e{0ull, 0u};
           if (in) {
-            e = Pair{score_key(off + static_cast<double>(x)), static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(token)};
+            e = Pair{score_key(off + (static_cast<double>(x) - M)), static_cast<uint32_t>(w) * static_cast<uint32_t>(p.V) + static_cast<uint32_t>(token)};
             in = before(e, last);
           }
           if (n + VN > kListCap) {
