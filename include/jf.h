@@ -649,8 +649,9 @@ jf_status jf_beam_select(const void* logits, int32_t dtype, const float* score,
  *                     whole block table none is used.
  *   new_block_table   int32 [B * K][max_pages]; new_prefix_len int32 [B * K].  Must not
  *                     overlap block_table and prefix_len.
- *   dev_err           JF_DEVERR_BAD_PATH (parent; the beam then gets length 0 and no pages),
- *                     _BAD_PREFIX (the same), _BAD_PAGE.  May be NULL.
+ *   dev_err           JF_DEVERR_BAD_PATH (parent), _BAD_PREFIX, _BAD_PAGE (a page of the
+ *                     parent's tokens, or fresh_page where one is used): the beam then gets
+ *                     length 0 and no pages.  May be NULL.
  * Limits: D in {64, 128}, page_size 16, caches 16-byte aligned.
  */
 jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_table,

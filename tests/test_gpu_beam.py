@@ -318,3 +318,38 @@ def test_masks_of_the_lowest_value(jf, dtype, low):
         for w in range(W):                     # in a beam: by logit, then by token
             mine = pick[parent[b] == w]
             assert (mine == np.lexsort((np.arange(V), -x[b, w]))[:len(mine)] + w * V).all(), (b, w)
+
+
+@pytest.mark.parametrize("what", ["fresh past", "fresh below", "fresh unused slots", "partial", "full"])
+def test_fork_of_bad_pages_leaves_no_tokens(jf, what):
+    """A beam whose pages are not in the pool gets length 0 and no pages, like one with a bad
+    parent: a caller that reads dev_err late does not attend over what it was not given."""
+    lens = np.array([20, 33, 37, 48], np.int32)
+    pool, parent, fresh = fork_case(4, 2, 2, 2, 2, 64, lens, 4)
+    parent[:] = [[0, 1], [0, 1]]
+    fr, tb, beam = fresh.copy(), pool.table.copy(), 2
+    if what == "fresh past":
+        fr[1, 0] = pool.k.shape[0]
+    elif what == "fresh below":
+        fr[1, 0] = -1
+    elif what == "fresh unused slots":         # 48 tokens: the fresh page takes no copy, the next token does
+        fr[1, 1], beam = -2, 3
+    elif what == "partial":
+        tb[2, 2] = -1
+    else:
+        tb[2, 1] = pool.k.shape[0] + 7
+    k, v, err = pool.k.cuda(), pool.v.cuda(), new_err()
+    table, new_len = jf.beam_fork_kv(k, v, dev(tb), dev(lens), dev(parent), dev(fr), dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == jf.DEVERR_BAD_PAGE
+    want_table, want_len, copies = ref.beam_fork(pool.table, lens, parent, fresh)
+    want_table[beam], want_len[beam] = -1, 0
+    assert (table.cpu().numpy() == want_table).all() and (new_len.cpu().numpy() == want_len).all()
+    for cache, got in ((pool.k, k), (pool.v, v)):          # the other beams' copies; nothing outside fresh pages
+        bits = cache.view(torch.int16).clone()
+        for to, frm, slots in copies:
+            bits[to, :slots] = cache.view(torch.int16)[frm, :slots]
+        out = got.view(torch.int16).cpu()
+        own = int(fresh[1, beam - 2])
+        rows = [i for i in range(len(bits)) if i != own]
+        assert torch.equal(out[rows], bits[rows])

@@ -630,29 +630,38 @@ __global__ void __launch_bounds__(kForkThreads)
   const int32_t* bt = block_table + (static_cast<size_t>(b) * W + w) * max_pages;
   const int full = len / kPage, slots = len % kPage;
   const int fresh = fresh_page[j];
+  const int from = full < max_pages && slots > 0 ? bt[full] : 0;
+  auto bad = [&](int page) { return page < 0 || page >= num_pages; };
+  const bool stop = full < max_pages && (bad(fresh) || bad(from));
   if (lead) {
-    for (int i = tid; i < max_pages; i += kForkThreads) nt[i] = i < full ? bt[i] : (i == full ? fresh : -1);
-    if (tid == 0) new_len[j] = len;
+    bool wrong = stop;
+    for (int i = tid; i < max_pages; i += kForkThreads) {
+      const int page = i < full ? bt[i] : (i == full ? fresh : -1);
+      wrong |= i < full && bad(page);
+      nt[i] = page;
+    }
+    wrong = __syncthreads_or(wrong);
+    if (wrong)                            // as for a bad parent: nothing that a later call could read
+      for (int i = tid; i < max_pages; i += kForkThreads) nt[i] = -1;
+    if (tid == 0) {
+      if (wrong) report(dev_err, JF_DEVERR_BAD_PAGE);
+      new_len[j] = wrong ? 0 : len;
+    }
   }
-  if (full < max_pages) {
-    const int from = slots > 0 ? bt[full] : 0;
-    if (fresh < 0 || fresh >= num_pages || from < 0 || from >= num_pages) {
-      if (lead && tid == 0) report(dev_err, JF_DEVERR_BAD_PAGE);
-    } else if (slots > 0) {
-      const int n = slots * row_vecs, span = (n + parts - 1) / parts;
-      const int lo = min(n, part * span), hi = min(n, lo + span);
-      uint16_t* cache = is_v ? v_cache : k_cache;
-      const uint4* src = reinterpret_cast<const uint4*>(cache) + static_cast<size_t>(from) * kPage * row_vecs;
-      uint4* dst = reinterpret_cast<uint4*>(cache) + static_cast<size_t>(fresh) * kPage * row_vecs;
-      for (int i0 = lo + tid; i0 < hi; i0 += kForkThreads * 4) {
-        uint4 v[4];
+  if (full < max_pages && !stop && slots > 0) {
+    const int n = slots * row_vecs, span = (n + parts - 1) / parts;
+    const int lo = min(n, part * span), hi = min(n, lo + span);
+    uint16_t* cache = is_v ? v_cache : k_cache;
+    const uint4* src = reinterpret_cast<const uint4*>(cache) + static_cast<size_t>(from) * kPage * row_vecs;
+    uint4* dst = reinterpret_cast<uint4*>(cache) + static_cast<size_t>(fresh) * kPage * row_vecs;
+    for (int i0 = lo + tid; i0 < hi; i0 += kForkThreads * 4) {
+      uint4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (i0 + u * kForkThreads < hi) v[u] = src[i0 + u * kForkThreads];
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kForkThreads < hi) v[u] = src[i0 + u * kForkThreads];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (i0 + u * kForkThreads < hi) dst[i0 + u * kForkThreads] = v[u];
-      }
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kForkThreads < hi) dst[i0 + u * kForkThreads] = v[u];
     }
   }
   grid_dependents_launch();
