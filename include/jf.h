@@ -625,8 +625,12 @@ jf_status jf_evict_kv(void* k_cache, void* v_cache, const int32_t* block_table,
  *              [0, V) where finished is given.
  *   workspace  at least jf_beam_select_workspace_size(...) bytes, 8-byte aligned, no
  *              initialisation.
- * s is ranked in 64 bits, with logsumexp from per-slice fp32 sums of exponentials (relative
- * error about 1e-7): pairs of different beams closer than that may come in either order.
+ * s is ranked in 64 bits, as (score - log(sum)) + (logit - the beam's greatest), with the sum
+ * of the exponentials formed in fp32 per slice: its relative error, which is s's absolute one,
+ * is at most (80 ceil(W V / 2^21) + 3 span) 2^-24, span being the beam's greatest finite logit
+ * less its least (90 at most: what is further below adds nothing).  Pairs of different beams
+ * closer than twice that may come in either order, and not the same one in another batch: the
+ * slices go by the sizes of the call and the device.  Within a beam the order is exact.
  * Limits: 1 <= K <= 64, 1 <= W <= 64, K <= W * V <= 2^26, B * W < 2^20.
  */
 size_t jf_beam_select_workspace_size(int32_t B, int32_t W, int32_t V, int32_t K, int32_t dtype);

@@ -353,3 +353,32 @@ def test_fork_of_bad_pages_leaves_no_tokens(jf, what):
         own = int(fresh[1, beam - 2])
         rows = [i for i in range(len(bits)) if i != own]
         assert torch.equal(out[rows], bits[rows])
+
+
+@pytest.mark.parametrize("B,W,V", [(1, 4, 151936), (16, 8, 50257), (3, 2, 1001), (1, 16, 262144)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scores_of_many_equal_logits(jf, dtype, B, W, V):
+    """Rows of one value far below a few others, whose roundings all go the same way: scores
+    within the stated error of logsumexp, (80 ceil(W V / 2^21) + 3 span) 2^-24, and the
+    rounding of the fp32 score."""
+    rng = np.random.default_rng(V + W)
+    K = 4
+    logits = np.empty((B, W, V), np.float32)
+    logits[:] = -rng.uniform(9.0, 17.0, (B, W, 1))
+    logits[..., V // 3] = 0.25
+    logits[..., 2 * V // 3] = rng.uniform(-3.0, 0.0, (B, W))
+    score = (-3 * rng.random((B, W)) - 1).astype(np.float32)
+    t = torch.from_numpy(logits).to(dtype)
+    parent, token, new_score, _ = (x.cpu().numpy() for x in jf.beam_select(t.cuda(), dev(score), K))
+    x = t.double().numpy()
+    worst = 0.0
+    for b in range(B):
+        d = x[b] - x[b].max(-1, keepdims=True)
+        s = (score[b].astype(np.float64)[:, None] - np.log(np.exp(d).sum(-1, keepdims=True))) + d
+        span = -d.min()
+        tol = (80 * -(-W * V // 2 ** 21) + 3 * span) * 2.0 ** -24
+        a = s[parent[b], token[b]]
+        e = np.sort(s.reshape(-1))[::-1][:K]
+        worst = max(worst, float(np.abs(new_score[b] - a).max()))
+        assert (np.abs(a - e) <= 2 * tol).all(), b
+        assert (np.abs(new_score[b] - a) <= tol + 2.0 ** -24 * np.abs(a)).all(), (b, worst)
