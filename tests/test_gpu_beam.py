@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import cache_reference as ref
-from test_gpu_cache import Pool, dev, new_err
+from test_gpu_cache import Pool, dev, new_err, on_its_stream
 
 pytestmark = pytest.mark.gpu
 
@@ -382,3 +382,67 @@ def test_scores_of_many_equal_logits(jf, dtype, B, W, V):
         worst = max(worst, float(np.abs(new_score[b] - a).max()))
         assert (np.abs(a - e) <= 2 * tol).all(), b
         assert (np.abs(new_score[b] - a) <= tol + 2.0 ** -24 * np.abs(a)).all(), (b, worst)
+
+
+def test_beam_calls_wait_for_their_stream(jf):
+    rng = np.random.default_rng(19)
+    B, W, V, K = 3, 4, 20000, 6
+    logits = dev((2 * rng.standard_normal((B, W, V))).astype(np.float32))
+    score = dev((-rng.random((B, W))).astype(np.float32))
+    want = jf.beam_select(logits, score, K)
+    ws = torch.empty(jf.jf_beam_select_workspace_size(B, W, V, K, jf._logit_dtype(logits)), dtype=torch.uint8,
+                     device="cuda")
+    out = [torch.full_like(x, -9) for x in want]
+    on_its_stream(lambda s: jf.jf_beam_select(logits, score, out[0], out[1], out[2], ws, new_finished=out[3], stream=s),
+                  out, list(want))
+
+
+def test_fork_on_a_given_stream_copies_its_pages(jf):
+    rng = np.random.default_rng(20)
+    B, W, K, cap = 3, 4, 6, 5
+    lens = rng.integers(1, cap * 16, B * W)
+    pool, parent, fresh = fork_case(20, B, W, K, 2, 64, lens, cap)
+    want_table, want_len, copies = ref.beam_fork(pool.table, lens, parent, fresh)
+    want = [dev(want_table), dev(want_len)]
+    for cache in (pool.k, pool.v):
+        bits = cache.view(torch.int16).clone()
+        for to, frm, slots in copies:
+            bits[to, :slots] = cache.view(torch.int16)[frm, :slots]
+        want.append(bits.cuda())
+    err, outs = new_err(), [torch.full_like(want[0], -9), torch.full_like(want[1], -9), pool.k.cuda(), pool.v.cuda()]
+    args = (dev(pool.table), dev(lens.astype(np.int32)), dev(parent), dev(fresh))
+    on_its_stream(lambda s: jf.jf_beam_fork_kv(outs[2], outs[3], *args, outs[0], outs[1], dev_err=err, stream=s),
+                  outs, want)
+    assert err.item() == 0
+
+
+def test_beams_that_share_a_context_in_a_graph(jf):
+    """Selection and fork of one step, captured once and replayed."""
+    rng = np.random.default_rng(22)
+    B, W, cap = 2, 5, 6
+    lens = rng.integers(1, cap * 16, B * W)
+    pool, _, fresh = fork_case(22, B, W, W, 2, 128, lens, cap)
+    logits = dev((2 * rng.standard_normal((B, W, 4001))).astype(np.float32)).to(torch.bfloat16)
+    score = dev((-rng.random((B, W))).astype(np.float32))
+    table, plen, fr, err = dev(pool.table), dev(lens.astype(np.int32)), dev(fresh), new_err()
+    k, v = pool.k.cuda(), pool.v.cuda()
+
+    def step():
+        picked = jf.beam_select(logits, score, W)
+        return (*picked, *jf.beam_fork_kv(k, v, table, plen, picked[0], fr, dev_err=err))
+
+    want = [x.clone() for x in (*step(), k, v)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        k.copy_(pool.k)
+        v.copy_(pool.v)
+        for x in got:
+            x.fill_(-9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        for a, b in zip((*got, k, v), want):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))

@@ -667,3 +667,180 @@ def test_pages_past_four_gigabytes(jf):
     assert err.item() == 0 and nl.tolist() == [20, 20]
     assert nt.tolist() == [[139999, 139000, -1, -1], [139999, 138000, -1, -1]]
     assert torch.equal(k[139000, :4], k[3, :4]) and torch.equal(v[138000, :4], v[3, :4])
+
+
+# ------------------------------------------------------------------- shapes and layouts of the weight
+
+@pytest.mark.parametrize("Hq,Hkv,D,prefix,sizes", [
+    (32, 8, 128, [200, 0, 77], [75, 3, 130]),              # 32 rows a block: two and four full ones and rests
+    (12, 4, 64, [131, 40, 9], [100, 1, 87]),               # 42 rows a block
+    (40, 8, 128, [16, 300], [51, 52]),                     # 25 rows a block
+    (8, 8, 64, [5, 128], [300, 129]),                      # 128 rows a block
+])
+def test_weight_packed_rows_without_a_path(jf, Hq, Hkv, D, prefix, sizes):
+    """Every packed row counts: full blocks of rows at offsets that are no multiple of a block."""
+    c = weight_case(60 + Hq, prefix, sizes, max(sizes), Hq, Hkv, D, False)
+    at = torch.cat([torch.arange(n) + b * max(sizes) for b, n in enumerate(sizes)]).cuda()
+    q = c["q"].flatten(0, 1)[at].contiguous()
+    lse = c["lse"].transpose(0, 1).flatten(1)[:, at].contiguous()
+    cu, err = dev(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)), new_err()
+    got = jf.accumulate_attention_weight(q, c["k"], c["table"], c["prefix"], lse, cu_seqlens=cu, weight=c["weight"],
+                                         scale=c["scale"], out=c["out"], dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(got, c["want"], c["tol"])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(12, 4, 64), (32, 8, 128)])
+def test_weight_packed_scattered_paths(jf, Hq, Hkv, D):
+    """Accepted nodes anywhere in each packed tree, against the 64-bit sums and the padded call's bits."""
+    sizes, prefix, rows, N = [9, 41, 30], [100, 3, 700], [4, 37, 1], 41
+    c = weight_case(70 + Hq, prefix, rows, N, Hq, Hkv, D, True)
+    rng = np.random.default_rng(Hq)
+    qn, kn = c["q"].double().cpu().numpy(), c["pool"].k.double().numpy()
+    lse = torch.from_numpy((rng.random(c["lse"].shape) + 5).astype(np.float32)).cuda()
+    paths, want, tol = np.full((3, N), -1, np.int32), np.empty_like(c["want"]), np.empty_like(c["tol"])
+    before = c["out"].cpu().numpy()
+    for b, (n, r) in enumerate(zip(sizes, rows)):
+        paths[b, :r] = np.concatenate([[0], np.sort(rng.permutation(n - 1)[:r - 1]) + 1])
+        want[b], tol[b] = ref.attention_weight(qn[b], kn, c["pool"].table[b], prefix[b], paths[b, :r].astype(np.int64),
+                                               lse[b].cpu().numpy(), c["weight"][b].cpu().numpy(), before[b], c["scale"])
+    kw = dict(path=dev(paths), accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    pad = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], lse, out=c["out"].clone(), **kw)
+    at = torch.cat([torch.arange(n) + b * N for b, n in enumerate(sizes)]).cuda()
+    cu, err = dev(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)), new_err()
+    got = jf.accumulate_attention_weight(c["q"].flatten(0, 1)[at].contiguous(), c["k"], c["table"], c["prefix"],
+                                         lse.transpose(0, 1).flatten(1)[:, at].contiguous(), cu_seqlens=cu,
+                                         out=c["out"].clone(), dev_err=err, **kw)
+    assert err.item() == 0 and torch.equal(got, pad)
+    close(got, want, tol)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,path", [
+    (66, 2, 64, True), (66, 2, 128, False), (128, 2, 128, True), (71, 1, 64, False), (71, 1, 128, True),
+    (128, 1, 64, False), (256, 2, 128, True),              # 33, 64, 71 and 128 heads a kv-head
+])
+def test_weight_of_wide_groups(jf, Hq, Hkv, D, path):
+    prefix, rows, N = [140, 0, 33], [7, 2, 9], 9
+    if not path:
+        rows = [9, 9, 9]
+    c = weight_case(80 + Hq, prefix, rows, N, Hq, Hkv, D, path)
+    err = new_err()
+    got = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"] if path else None, weight=c["weight"],
+                                         scale=c["scale"], out=c["out"], dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(got, c["want"], c["tol"])
+
+
+@pytest.mark.parametrize("heads", [40, 80, 160])
+def test_weight_of_many_kv_heads(jf, heads):
+    """Kv-heads that do not divide the SMs, and more of them than SMs."""
+    c = weight_case(90 + heads, [300, 15], [5, 2], 6, heads, heads, 64, True)
+    err = new_err()
+    got = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"], dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(got, c["want"], c["tol"])
+
+
+@pytest.mark.parametrize("B", [769, 1600])
+def test_weight_of_many_sequences(jf, B):
+    """More sequences than a block has threads: their costs are scanned in several passes."""
+    rng = np.random.default_rng(B)
+    prefix = [int(x) for x in rng.integers(0, 60, B)]
+    prefix[-1] = 400                                       # the last one spans several tiles
+    rows = [int(x) for x in rng.integers(0, 3, B)]
+    rows[-1] = 2
+    c = weight_case(B, prefix, rows, 2, 4, 2, 64, True)
+    err = new_err()
+    got = jf.accumulate_attention_weight(c["q"], c["k"], c["table"], c["prefix"], c["lse"], path=c["path"],
+                                         accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"],
+                                         out=c["out"], dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    close(got, c["want"], c["tol"])
+
+
+# --------------------------------------------------------------------------- order of work
+
+def on_its_stream(call, outs, wants):
+    """call(stream) does its work on stream, behind what is queued there: while that stream
+    sleeps, the outputs are what they were.  (A first call before: loading a kernel and growing
+    the pool of memory wait for the device.)"""
+    s = torch.cuda.Stream()
+    was, seen = [o.clone() for o in outs], [o.clone() for o in outs]
+    call(s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, was):
+        o.copy_(w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    call(s)
+    for to, o in zip(seen, outs):                          # on the current stream
+        to.copy_(o)
+    torch.cuda.current_stream().synchronize()
+    asleep = not s.query()
+    s.synchronize()
+    assert asleep, "the stream woke too early to tell"
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))   # noqa: E731
+    assert all(same(a, b) for a, b in zip(seen, was))
+    assert all(same(a, b) for a, b in zip(outs, wants))
+
+
+def test_cache_calls_wait_for_their_stream(jf):
+    c = weight_case(13, [500, 300], [4, 2], 8, 8, 2, 64, True)
+    kw = dict(path=c["path"], accept_len=c["accept_len"], weight=c["weight"], scale=c["scale"])
+    args = (c["q"], c["k"], c["table"], c["prefix"], c["lse"])
+    want = jf.accumulate_attention_weight(*args, out=c["out"].clone(), **kw)
+    out = c["out"].clone()
+    on_its_stream(lambda s: jf.accumulate_attention_weight(*args, out=out, stream=s, **kw), [out], [want])
+    lens = c["prefix"] + c["accept_len"] + 1
+    keep, kept = jf.select_kept_keys(want, lens, 100, sink=1, recent=5)
+    k2, l2 = torch.full_like(keep, -9), torch.full_like(kept, -9)
+    on_its_stream(lambda s: jf.jf_select_kept(want, lens, k2, l2, 1, 5, stream=s), [k2, l2], [keep, kept])
+    k_old, v_old = c["k"], torch.randn_like(c["k"])
+    kv, w = [k_old.clone(), v_old.clone()], want.clone()
+    jf.evict_kv(*kv, c["table"], lens, keep, kept, weight=w)
+    torch.cuda.synchronize()
+    mine = [k_old.clone(), v_old.clone(), want.clone()]
+    on_its_stream(lambda s: jf.evict_kv(mine[0], mine[1], c["table"], lens, keep, kept, weight=mine[2], stream=s),
+                  mine, [*kv, w])
+
+
+def test_eviction_in_a_graph(jf):
+    """Weight, choice and move of one step, captured once and replayed over restored caches."""
+    c = weight_case(14, [900, 640, 7], [4, 2, 1], 8, 8, 2, 128, True)
+    lens = c["prefix"] + c["accept_len"] + 1
+    k, v, w = c["k"].clone(), c["k"].flip(0).contiguous(), c["weight"].clone()
+    err = new_err()
+
+    def step():
+        jf.accumulate_attention_weight(c["q"], k, c["table"], c["prefix"], c["lse"], path=c["path"],
+                                       accept_len=c["accept_len"], weight=w, scale=c["scale"], out=w, dev_err=err)
+        keep, kept = jf.select_kept_keys(w, lens, 300, sink=2, recent=20, dev_err=err)
+        jf.evict_kv(k, v, c["table"], lens, keep, kept, weight=w, dev_err=err)
+        return keep, kept
+
+    def restore():
+        k.copy_(c["k"])
+        v.copy_(c["k"].flip(0))
+        w.copy_(c["weight"])
+
+    want = [x.clone() for x in (*step(), k, v, w)]
+    restore()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        for a, b in zip((*got, k, v, w), want):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
