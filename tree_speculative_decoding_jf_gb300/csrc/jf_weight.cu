@@ -89,7 +89,6 @@ struct Cfg {
 };
 
 struct WeightParams {
-  const uint16_t* q;
   const int32_t* block_table;
   const int32_t* prefix_len;
   const int32_t* path;        // or null: row k is node k
@@ -675,7 +674,6 @@ jf_status attention_weight_call(const void* q, const void* k_cache, const int32_
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
   WeightParams p;
-  p.q = static_cast<const uint16_t*>(q);
   p.block_table = block_table;
   p.prefix_len = prefix_len;
   p.path = path;
