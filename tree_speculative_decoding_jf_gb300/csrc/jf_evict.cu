@@ -663,8 +663,9 @@ extern "C" jf_status jf_select_kept(const float* weight, const int32_t* seq_len,
   // against 21.8).
   // Longer rows are clusters of CTAs of 512 threads, with slices up to kSelTwo (256 rows of
   // 64K: 84 us in fours, 92 in twos, 87 in twos of 1024 threads; 200 rows of 40000: 46 in
-  // twos, 56 in fours); of eight only where every CTA has an SM of its own (8 rows of
-  // 128K: 18 us against 25 in fours of 1024; but 32 rows: 28 against 22 in fours).
+  // twos, 56 in fours); of eight where every CTA has an SM of its own (8 rows of 128K: 18 us
+  // against 25 in fours of 1024; but 32 rows: 28 against 22 in fours), and past 4 kSelRow keys
+  // whatever their number, so that a slice stays within kSelRow as long as it can.
   int C = 1;
   if (capacity > kSelRow)
     while (C < kMaxCluster && (capacity > C * kSelRow || (capacity > C * kSelTwo && (C < 4 || rows * 2 * C <= sms)))) C *= 2;

@@ -15,7 +15,8 @@
 // Work: the key tiles of all sequences lie end to end, a tile weighted by its row blocks,
 // and are cut into (SMs / kv-heads) equal ranges; the CTAs of a range (one per kv-head, side
 // by side) walk the same tokens together, so the 256-byte rows that they read lie next to
-// each other.  Up to four consecutive tiles of a sequence form a group that shares every
+// each other.  (Rounded down: of 152 SMs, 32 kv-heads use 128, 40 use 120 and 80 use 80, and
+// more than 152 kv-heads take a second round.)  Up to four consecutive tiles of a sequence form a group that shares every
 // row block loaded; with one row block (a verified path) it stays in shared memory for the
 // whole run of the sequence.
 //
@@ -36,9 +37,10 @@
 //                  more than its share of the HBM bandwidth); page ids four to eight tiles
 //                  ahead; pages past the end and malformed ids load as zeros.
 // What bounds it: HBM with few rows (54 us for 8 x 32K keys, 32/4 heads, whose bytes take 41);
-// with many, the round trip of a slot from scores to probabilities and back (124 us for the
-// window, whose products take 71: 114 without the MMAs, 103 without the exponentials, 79 with
-// the TMEM loads and the waits alone).
+// with many, the instructions of the probabilities: the window took 124 us, whose products
+// take 71, and still 114 without the MMAs, or without MMAs and TMEM loads, but 87 when the
+// reads of -lse went as well (103 without the exponentials, 79 with the TMEM loads and the
+// waits alone).
 // Slots past a block's rows and rows whose lse is -inf get zero queries and lse = +inf, so
 // they add exp(-inf) = 0.  Only with an infinity or a NaN in the key is such a score not zero
 // but NaN (0 * inf): one such column of the block tells, and its warp then leaves them all out
