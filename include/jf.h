@@ -59,7 +59,7 @@ typedef enum { JF_DTYPE_BF16 = 0, JF_DTYPE_F32 = 1 } jf_dtype;
 #define JF_DEVERR_BAD_PREFIX 0x4 /* prefix_len < 0 or prefix_len + N > max_pages * page */
 #define JF_DEVERR_BAD_TOKEN 0x8  /* draft token (non-root node) outside [0, V)          */
 #define JF_DEVERR_TIMEOUT 0x10   /* an in-kernel wait gave up after its time limit      */
-#define JF_DEVERR_BAD_PATH 0x20  /* accepted path, kept positions or beam parent malformed */
+#define JF_DEVERR_BAD_PATH 0x20  /* accepted path, kept positions, beam parent, grammar or count row malformed */
 #define JF_DEVERR_BAD_TREE_LEN 0x40 /* tree_len[b] outside [1, N], or a bad packed span   */
 
 /* Largest tree (nodes per sequence) any call accepts. */
@@ -664,6 +664,142 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
                           int32_t D, int32_t page_size, int32_t max_pages, int32_t num_pages,
                           int32_t* new_block_table, int32_t* new_prefix_len, int32_t* dev_err,
                           jf_stream_t stream);
+
+/* ---------------------------------------------------------------- around a step
+ * What a decoding step does between the model's projections and the calls above: heads are
+ * rotated and the new keys and values enter the cache before the attention; logits are
+ * adjusted before verification or beam selection, from token counts that are brought up to
+ * date after it.  The pages take these for granted (they plug into a serving engine, explainer
+ * §3); the calls follow the engine-independent definitions below.
+ *
+ * jf_rotate_append_kv -- rotary positions for the step's queries and keys, and the append of
+ * its keys and values to the paged cache.  For token i of sequence b (a tree node, or a token
+ * of a prompt chunk):
+ *   1. with q_norm / k_norm, every query / key head x becomes x / sqrt(mean(x^2) + norm_eps) *
+ *      weight;
+ *   2. with freq, pair f < R / 2 of the head's first R = rotary_dim elements, (x[f], x[f + R / 2])
+ *      or, interleaved, (x[2 f], x[2 f + 1]), turns by a = pos * freq[f]:
+ *      rotary_scale * (x cos a - y sin a, y cos a + x sin a); the elements from R on stay;
+ *   3. query heads are written to q_out, key and value heads (values as they are) to position
+ *      P_b + i of sequence b's pages.
+ * Arithmetic is fp32 with one rounding to bf16 at the end; the angle is formed modulo one turn in
+ * 64 bits (its fraction of a turn is off by about 2^-52 |pos freq / 2 pi| + 2^-25), so far positions
+ * cost no precision.
+ *   q, k, v      bf16, token rows of [Hq][D], [Hkv][D], [Hkv][D]; consecutive tokens
+ *                (row b * N + i) lie *_stride elements apart, so the three may be views of one
+ *                projection's output.  q and q_out may both be NULL (keys and values only).
+ *   pos          int32 [B][N], as from jf_build_tree_mask; any value.  NULL without freq.
+ *   freq         double [R / 2], radians per position, or NULL for no rotation.  Frequencies
+ *                scaled for long contexts are the caller's to compute.
+ *   rotary_scale a factor on the rotated elements (1, or a long-context method's).
+ *   q_norm, k_norm  bf16 [D] or NULL.
+ *   block_table, prefix_len, tree_len (may be NULL)  as in jf_tree_attention and its _ragged
+ *                form; tokens i >= tree_len[b] are neither read nor written.
+ *   q_out        bf16 [B][N][Hq][D]; may be q itself when q_stride == Hq * D.  Must not overlap
+ *                k, v or, in another way, q; the caches must not overlap any input.
+ *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + n_b past the block table: the sequence's
+ *                keys and values are not written), _BAD_PAGE (the token's are not written),
+ *                _BAD_TREE_LEN.  May be NULL.
+ * Limits: D in {64, 128}; R a multiple of 16, 16 <= R <= D; page_size 16; B * N + N < 2^31; num_pages *
+ * page_size < 2^31; the arrays 16-byte aligned and strides multiples of 8; N may exceed JF_MAX_NODES.
+ * jf_rotate_append_kv_packed takes the packed layout: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
+ * pos [T], q_out [T][Hq][D].
+ */
+jf_status jf_rotate_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* pos,
+                              const double* freq, int32_t rotary_dim, int32_t interleaved,
+                              float rotary_scale, const void* q_norm, const void* k_norm,
+                              float norm_eps, const int32_t* block_table,
+                              const int32_t* prefix_len, const int32_t* tree_len, int32_t B,
+                              int32_t N, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                              int32_t max_pages, int32_t num_pages, void* q_out, void* k_cache,
+                              void* v_cache, int32_t* dev_err, jf_stream_t stream);
+jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const int32_t* pos, const double* freq, int32_t rotary_dim,
+                                     int32_t interleaved, float rotary_scale, const void* q_norm,
+                                     const void* k_norm, float norm_eps,
+                                     const int32_t* block_table, const int32_t* prefix_len,
+                                     const int32_t* cu_seqlens, int32_t B, int32_t N_max,
+                                     int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t page_size, int32_t max_pages, int32_t num_pages,
+                                     void* q_out, void* k_cache, void* v_cache, int32_t* dev_err,
+                                     jf_stream_t stream);
+
+/*
+ * jf_adjust_logits -- penalties for repeated tokens, biases and grammar masks on the logits of
+ * the tree's nodes, before jf_tree_verify, jf_tree_verify_sampled or jf_beam_select.  With
+ *   c    = times token v was generated before node i of sequence b's tree: the count's times
+ *          plus the drafted tokens draft[b][j] == v of the nodes j >= 1 on i's branch (mask bit j
+ *          of i; the root's token is an emitted one, so the count has it),
+ *   seen = c > 0, or the count has v in the prompt:
+ *     x = logits[b][i][v];
+ *     seen:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *     c > 0: x = x - presence[b] - frequency[b] * c
+ *     out[b][i][v] = allowed ? x + bias[b][v] : masked
+ *   logits       [B][N][V], bf16 or fp32 (dtype); out: the same type, or fp32 from bf16
+ *                (out_dtype).  out may be logits itself when the types are equal (unchanged
+ *                values are then not written) and must not otherwise overlap an input.
+ *   count        int32 [B][V] as kept by jf_count_tokens, or NULL for none.
+ *   draft, mask  int32 [B][N] and uint64 [B][N][W] as in jf_build_tree_mask, or both NULL: no
+ *                drafted tokens count.
+ *   bias         float [B][V] or NULL.
+ *   allowed      uint32 [n_allowed][ceil(V / 32)]: bit v & 31 of word v >> 5 set where token v
+ *                is allowed, or NULL.  allowed_row int32 [B][N]: the node's row, -1 for a node
+ *                without a grammar; NULL: row b * N + i (packed: the node's row).
+ *                The logits of forbidden tokens need not be finite.
+ *   repetition, presence, frequency  float [B], NULL for 1, 0 and 0.  repetition > 0.
+ *   masked       what forbidden tokens get, rounded to the output's type: -INFINITY, or a finite
+ *                value for calls that want finite logits.  A row whose grammar forbids every
+ *                token is masked throughout.
+ *   tree_len     int32 [B] or NULL; rows i >= tree_len[b] are neither read nor written.
+ *   dev_err      JF_DEVERR_BAD_TOKEN (a drafted token outside [0, V): not counted), _BAD_PATH
+ *                (an allowed_row outside [-1, n_allowed): no grammar), _BAD_TREE_LEN.
+ * Arithmetic is fp32 with one rounding at the end.
+ * Limits: 1 <= N <= JF_MAX_NODES, B * N * V <= 2^40.  V a multiple of 8 with 16-byte aligned arrays
+ * is read and written 16 bytes at a time, anything else element by element.
+ * jf_adjust_logits_packed takes rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1: logits, out [T][V],
+ * draft, allowed_row [T], mask [T][W].
+ */
+jf_status jf_adjust_logits(const void* logits, int32_t dtype, const int32_t* count,
+                           const int32_t* draft, const uint64_t* mask, const float* bias,
+                           const uint32_t* allowed, const int32_t* allowed_row,
+                           int32_t n_allowed, const float* repetition, const float* presence,
+                           const float* frequency, float masked, const int32_t* tree_len,
+                           int32_t B, int32_t N, int32_t V, void* out, int32_t out_dtype,
+                           int32_t* dev_err, jf_stream_t stream);
+jf_status jf_adjust_logits_packed(const void* logits, int32_t dtype, const int32_t* count,
+                                  const int32_t* draft, const uint64_t* mask, const float* bias,
+                                  const uint32_t* allowed, const int32_t* allowed_row,
+                                  int32_t n_allowed, const float* repetition,
+                                  const float* presence, const float* frequency, float masked,
+                                  const int32_t* cu_seqlens, int32_t B, int32_t N_max, int32_t T,
+                                  int32_t V, void* out, int32_t out_dtype, int32_t* dev_err,
+                                  jf_stream_t stream);
+
+/*
+ * jf_count_tokens -- the token counts of jf_adjust_logits: an entry is the times a token was
+ * generated, plus JF_COUNT_PROMPT if it is in the prompt.
+ *   count_out[b] = count[row[b]] with sequence b's tokens added: +1 each or, with prompt != 0,
+ *   JF_COUNT_PROMPT set.  The tokens are token[b][k], k < length[b]; with a path,
+ *   token[b][path[b][k]], 1 <= k <= length[b] (draft, path and accept_len of a verification);
+ *   and extra[b] (the bonus token; -1 for none).
+ *   count      int32 [rows_in][V], or NULL for zeros.
+ *   row        int32 [B] (the new beams' parents, as rows of count) or NULL: row b.
+ *   token      int32 [B][N]; path int32 [B][N] or NULL; length int32 [B] or NULL (all N; a path
+ *              needs it); extra int32 [B] or NULL.
+ *   count_out  int32 [B][V]; may be count itself without row: only the tokens' entries are then
+ *              touched.  Must not otherwise overlap an input.
+ *   dev_err    JF_DEVERR_BAD_TOKEN (outside [0, V)), _BAD_PATH (a path entry, its length or a row
+ *              out of range; a bad row counts as zeros), _BAD_TREE_LEN (length outside [0, N],
+ *              clamped).  May be NULL.
+ * Limits: B <= 65535; 2^30 - 1 times a token.
+ */
+#define JF_COUNT_PROMPT (1 << 30)
+jf_status jf_count_tokens(const int32_t* count, const int32_t* row, int32_t rows_in,
+                          const int32_t* token, const int32_t* path, const int32_t* length,
+                          const int32_t* extra, int32_t prompt, int32_t B, int32_t N, int32_t V,
+                          int32_t* count_out, int32_t* dev_err, jf_stream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

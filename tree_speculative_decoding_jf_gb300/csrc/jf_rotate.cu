@@ -1,0 +1,362 @@
+// jf_rotate.cu -- rotary positions for a step's queries and keys, and the append of its keys
+// and values to the paged cache.
+//
+// For every token: each query and key head is normalised (optional: x / sqrt(mean x^2 + eps) *
+// w), its pairs (x, y) are turned by the angle pos * freq[f],
+//     (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
+// and rounded to bf16 once; query heads go to q_out, key and value heads to slot P_b + i of the
+// sequence's pages.
+//
+// Angles.  Only the fraction of a turn matters, and with integer positions it can be formed
+// exactly modulo one turn: freq / 2 pi as a 64-bit fixed-point fraction of a turn, multiplied
+// by the position in 64-bit integer arithmetic (which wraps at whole turns), is off by at most
+// |pos| 2^-64 turns plus the 2^-52 relative rounding of freq / 2 pi.  The signed fraction is
+// then rounded to fp32 once, so a position of a million costs no more error than position 1;
+// pos * freq in fp32 would be off by up to 2^-24 * pos radians.
+//
+// Bound: bytes.  Every head row is read and written once, so a thread owns the two 16-byte
+// chunks of a head that a half-split pair needs (chunks t and t + R / 16), D / 16 threads a
+// head; the cosines and sines of a token are formed once per block and read from shared memory
+// by all its heads.
+#include <cmath>
+
+#include "jf_common.cuh"
+
+namespace jf {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kRotThreads = 256;
+
+struct RotateParams {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;   // elements between consecutive tokens
+  const int32_t* pos;
+  const double* freq;                       // null: nothing is rotated
+  const uint16_t *q_norm, *k_norm;          // null: not normalised
+  const int32_t *block_table, *prefix_len, *tree_len, *cu;
+  uint16_t *q_out, *k_cache, *v_cache;
+  int32_t* dev_err;
+  long long rows;                           // tokens of the call's arrays (padding included)
+  int B, N, Hq, Hkv, R, max_pages, num_pages;
+  float scale, eps;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
+  x[0] = bf_lo(w.x); x[1] = bf_hi(w.x); x[2] = bf_lo(w.y); x[3] = bf_hi(w.y);
+  x[4] = bf_lo(w.z); x[5] = bf_hi(w.z); x[6] = bf_lo(w.w); x[7] = bf_hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+// The sequence whose packed span holds `row`: the last b with cu[b] <= row, found by the whole
+// warp, 32 probes a round (one round up to 32 sequences, two up to 1024).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, long long row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = B;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lane * step;
+    const bool below = at < len && cu[lo + at] <= row;
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    const int skip = max(n - 1, 0) * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  return lo;
+}
+
+// Fraction of a turn per position, as a 64-bit fixed-point number (whole turns dropped).
+__device__ __forceinline__ uint64_t fixed_turns(double freq) {
+  double t = freq * 0.15915494309189533577;   // 1 / (2 pi)
+  t -= floor(t);
+  return __double2ull_rn(t * 18446744073709551616.0);
+}
+
+// TB tokens per block.  INTER: pairs (2 f, 2 f + 1) instead of (f, f + R / 2).
+template <int D, bool INTER, int TB>
+__global__ void __launch_bounds__(kRotThreads) rotate_append_kernel(const RotateParams p) {
+  constexpr int kLanes = D / 16;            // threads per head row
+  constexpr int kSlots = kRotThreads / kLanes;
+  __shared__ float2 s_cs[TB][D / 2];        // (cos, sin) * scale
+  __shared__ long long s_cache[TB];         // cache row of the token, -1: none
+  __shared__ int s_live[TB];
+  __shared__ int s_pos[TB];
+  grid_dependency_wait();
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row0 = static_cast<long long>(blockIdx.x) * TB;
+  const int cap = p.max_pages * kPage;
+  if (blockIdx.x == 0) {                    // every sequence's span and length are judged once
+    for (int b = threadIdx.x; b < p.B; b += kRotThreads) {
+      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.rows);
+      if (!sp.ok) report(p.dev_err, JF_DEVERR_BAD_TREE_LEN);
+      const int P = p.prefix_len[b];
+      if (P < 0 || P > cap - sp.n) report(p.dev_err, JF_DEVERR_BAD_PREFIX);
+    }
+  }
+  if (warp < TB) {
+    const long long row = row0 + warp;
+    bool live = row < p.rows;
+    long long at = -1;
+    if (live) {                             // warp-uniform
+      const int b = p.cu != nullptr ? find_sequence(p.cu, p.B, row) : static_cast<int>(row / p.N);
+      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.rows);
+      const long long i = row - sp.row0;
+      live = i >= 0 && i < sp.n;
+      if (live && lane == 0) {
+        const int P = p.prefix_len[b];
+        if (P >= 0 && P <= cap - sp.n) {
+          const int t = P + static_cast<int>(i);
+          const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + t / kPage];
+          if (page >= 0 && page < p.num_pages)
+            at = static_cast<long long>(page) * kPage + t % kPage;
+          else
+            report(p.dev_err, JF_DEVERR_BAD_PAGE);
+        }
+      }
+    }
+    if (lane == 0) {
+      s_live[warp] = live ? 1 : 0;
+      s_cache[warp] = at;
+      s_pos[warp] = live && p.freq != nullptr ? p.pos[row] : 0;
+    }
+  }
+  __syncthreads();
+  const int pairs = p.freq != nullptr ? p.R / 2 : 0;
+  for (int e = threadIdx.x; e < TB * pairs; e += kRotThreads) {
+    const int tok = e / pairs, f = e % pairs;
+    const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(s_pos[tok])) * fixed_turns(p.freq[f]);
+    // signed fraction of a turn in [-1/2, 1/2), in units of pi: [-1, 1)
+    const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;   // 2^-63
+    float s, c;
+    sincospif(x, &s, &c);
+    s_cs[tok][f] = make_float2(c * p.scale, s * p.scale);
+  }
+  __syncthreads();
+
+  // Thread t of a head: the rotated chunks t and t + R / 16, or two of the chunks behind R.
+  const int t = threadIdx.x % kLanes;
+  const int half = p.freq != nullptr ? p.R / 16 : 0;
+  const bool turns = t < half;
+  const int c0 = turns ? t : 2 * half + 2 * (t - half);
+  const int c1 = turns ? t + half : c0 + 1;
+  const int heads = p.Hq + 2 * p.Hkv;
+#pragma unroll
+  for (int tok = 0; tok < TB; ++tok) {
+    if (!s_live[tok]) continue;             // block-uniform
+    const long long row = row0 + tok;
+    const long long at = s_cache[tok];
+    float cs[8], sn[8];
+    if (turns) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // half: the eight pairs of chunk t; interleaved: four pairs of each chunk
+        const int f = !INTER ? 8 * t + e : (e < 4 ? 4 * c0 + e : 4 * c1 + e - 4);
+        const float2 v = s_cs[tok][f];
+        cs[e] = v.x;
+        sn[e] = v.y;
+      }
+    }
+    for (int h0 = 0; h0 < heads; h0 += kSlots) {
+      const int h = h0 + threadIdx.x / kLanes;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+      const bool act = h < heads && (is_q || at >= 0);
+      const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
+      uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+      uint4* dst = nullptr;
+      if (act) {
+        const uint16_t* src = is_q ? p.q + row * p.q_stride
+                                   : (is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride);
+        const uint4* s4 = reinterpret_cast<const uint4*>(src + hh * D);
+        w0 = s4[c0];
+        w1 = s4[c1];
+        uint16_t* d = is_q ? p.q_out + (row * p.Hq + hh) * D
+                           : (is_v ? p.v_cache : p.k_cache) + (at * p.Hkv + hh) * D;
+        dst = reinterpret_cast<uint4*>(d);
+      }
+      const uint16_t* norm = is_v ? nullptr : (is_q ? p.q_norm : p.k_norm);
+      float x[8], y[8];
+      unpack8(w0, x);
+      unpack8(w1, y);
+      if (p.q_norm != nullptr || p.k_norm != nullptr) {     // uniform: the shuffles need every lane
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (norm != nullptr) {
+          const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+          float u0[8], u1[8];
+          unpack8(reinterpret_cast<const uint4*>(norm)[c0], u0);
+          unpack8(reinterpret_cast<const uint4*>(norm)[c1], u1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] *= inv * u0[e];
+            y[e] *= inv * u1[e];
+          }
+        }
+      }
+      if (!act) continue;
+      if (!is_v && (turns || norm != nullptr)) {
+        if (turns) {
+          if (!INTER) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float a = x[e], b = y[e];
+              x[e] = a * cs[e] - b * sn[e];
+              y[e] = b * cs[e] + a * sn[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float a = x[2 * e], b = x[2 * e + 1];
+              x[2 * e] = a * cs[e] - b * sn[e];
+              x[2 * e + 1] = b * cs[e] + a * sn[e];
+              a = y[2 * e];
+              b = y[2 * e + 1];
+              y[2 * e] = a * cs[4 + e] - b * sn[4 + e];
+              y[2 * e + 1] = b * cs[4 + e] + a * sn[4 + e];
+            }
+          }
+        }
+        w0 = pack8(x);
+        w1 = pack8(y);
+      }
+      dst[c0] = w0;
+      dst[c1] = w1;
+    }
+  }
+  grid_dependents_launch();
+}
+
+template <int D>
+cudaError_t launch_rotate(const RotateParams& p, bool inter, int tb, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.rows + tb - 1) / tb));
+  const dim3 block(kRotThreads);
+  if (tb == 1)
+    return inter ? launch_pdl(rotate_append_kernel<D, true, 1>, grid, block, 0, s, p)
+                 : launch_pdl(rotate_append_kernel<D, false, 1>, grid, block, 0, s, p);
+  return inter ? launch_pdl(rotate_append_kernel<D, true, 4>, grid, block, 0, s, p)
+               : launch_pdl(rotate_append_kernel<D, false, 4>, grid, block, 0, s, p);
+}
+
+jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool packed, long long T,
+                      jf_stream_t stream) {
+  if (p.k == nullptr || p.v == nullptr || p.block_table == nullptr || p.prefix_len == nullptr ||
+      p.k_cache == nullptr || p.v_cache == nullptr || (p.q == nullptr) != (p.q_out == nullptr))
+    return JF_ERR_INVALID_ARGUMENT;
+  if (p.freq != nullptr && p.pos == nullptr) return JF_ERR_INVALID_ARGUMENT;
+  if (p.q == nullptr) p.Hq = 0;
+  if (p.B < 1 || p.N < 1 || p.Hkv < 1 || (p.q != nullptr && p.Hq < 1) || p.max_pages < 1 ||
+      p.num_pages < 1 || !std::isfinite(p.scale) || !(p.eps >= 0.f) || !std::isfinite(p.eps))
+    return JF_ERR_INVALID_ARGUMENT;
+  if (packed && T < 1) return JF_ERR_INVALID_ARGUMENT;
+  if (D != 64 && D != 128) return JF_ERR_UNSUPPORTED;
+  if (page_size != kPage) return JF_ERR_UNSUPPORTED;
+  if (p.freq != nullptr && (p.R < 16 || p.R > D || p.R % 16 != 0)) return JF_ERR_UNSUPPORTED;
+  if (p.Hq > (1 << 20) || p.Hkv > (1 << 20)) return JF_ERR_UNSUPPORTED;
+  p.rows = packed ? T : static_cast<long long>(p.B) * p.N;
+  if (p.rows + p.N >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p.max_pages) * kPage > (1ll << 30)) return JF_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p.num_pages) * kPage >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  const long long qw = static_cast<long long>(p.Hq) * D, kw = static_cast<long long>(p.Hkv) * D;
+  if (p.k_stride < kw || p.v_stride < kw || (p.q != nullptr && p.q_stride < qw)) return JF_ERR_INVALID_ARGUMENT;
+  const long long max_stride = 1ll << 31;     // rows * stride stays far inside 64 bits
+  if (p.k_stride > max_stride || p.v_stride > max_stride || (p.q != nullptr && p.q_stride > max_stride))
+    return JF_ERR_UNSUPPORTED;
+  if (!aligned_to(p.k, 16) || !aligned_to(p.v, 16) || !aligned_to(p.q, 16) || !aligned_to(p.q_out, 16) ||
+      !aligned_to(p.k_cache, 16) || !aligned_to(p.v_cache, 16) || !aligned_to(p.q_norm, 16) ||
+      !aligned_to(p.k_norm, 16) || !aligned_to(p.freq, 8) || p.k_stride % 8 != 0 || p.v_stride % 8 != 0 ||
+      (p.q != nullptr && p.q_stride % 8 != 0))
+    return JF_ERR_MISALIGNED;
+  // Outputs must not overlap what other blocks still read; q_out may be q itself.
+  const size_t rows = static_cast<size_t>(p.rows);
+  const size_t kb = ((rows - 1) * p.k_stride + kw) * 2, vb = ((rows - 1) * p.v_stride + kw) * 2;
+  const size_t qb = p.q != nullptr ? ((rows - 1) * p.q_stride + qw) * 2 : 0, ob = rows * qw * 2;
+  const size_t cb = static_cast<size_t>(p.num_pages) * kPage * kw * 2;
+  if (overlap(p.k_cache, cb, p.v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
+  for (void* out : {static_cast<void*>(p.k_cache), static_cast<void*>(p.v_cache)}) {
+    if (overlap(out, cb, p.k, kb) || overlap(out, cb, p.v, vb)) return JF_ERR_INVALID_ARGUMENT;
+    if (p.q != nullptr && (overlap(out, cb, p.q, qb) || overlap(out, cb, p.q_out, ob)))
+      return JF_ERR_INVALID_ARGUMENT;
+  }
+  if (p.q != nullptr) {
+    if (overlap(p.q_out, ob, p.k, kb) || overlap(p.q_out, ob, p.v, vb)) return JF_ERR_INVALID_ARGUMENT;
+    if (overlap(p.q_out, ob, p.q, qb) && !(p.q_out == p.q && p.q_stride == qw)) return JF_ERR_INVALID_ARGUMENT;
+  }
+  const int sms = current_sm_count();
+  if (sms <= 0) return JF_ERR_CUDA;
+  const int tb = p.rows <= 4ll * sms ? 1 : 4;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 128 ? launch_rotate<128>(p, inter, tb, s) : launch_rotate<64>(p, inter, tb, s);
+  return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
+}
+
+RotateParams rotate_params(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int32_t* pos, const double* freq, int32_t R,
+                           float scale, const void* q_norm, const void* k_norm, float eps,
+                           const int32_t* block_table, const int32_t* prefix_len, int32_t B, int32_t N,
+                           int32_t Hq, int32_t Hkv, int32_t max_pages, int32_t num_pages, void* q_out,
+                           void* k_cache, void* v_cache, int32_t* dev_err) {
+  RotateParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+  p.pos = pos; p.freq = freq; p.R = R; p.scale = scale;
+  p.q_norm = static_cast<const uint16_t*>(q_norm);
+  p.k_norm = static_cast<const uint16_t*>(k_norm);
+  p.eps = eps;
+  p.block_table = block_table; p.prefix_len = prefix_len;
+  p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.max_pages = max_pages; p.num_pages = num_pages;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_cache = static_cast<uint16_t*>(k_cache);
+  p.v_cache = static_cast<uint16_t*>(v_cache);
+  p.dev_err = dev_err;
+  return p;
+}
+
+}  // namespace
+}  // namespace jf
+
+extern "C" jf_status jf_rotate_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* v, int64_t v_stride, const int32_t* pos,
+                                         const double* freq, int32_t rotary_dim, int32_t interleaved,
+                                         float rotary_scale, const void* q_norm, const void* k_norm,
+                                         float norm_eps, const int32_t* block_table,
+                                         const int32_t* prefix_len, const int32_t* tree_len, int32_t B,
+                                         int32_t N, int32_t Hq, int32_t Hkv, int32_t D,
+                                         int32_t page_size, int32_t max_pages, int32_t num_pages,
+                                         void* q_out, void* k_cache, void* v_cache, int32_t* dev_err,
+                                         jf_stream_t stream) {
+  jf::RotateParams p = jf::rotate_params(q, q_stride, k, k_stride, v, v_stride, pos, freq, rotary_dim,
+                                         rotary_scale, q_norm, k_norm, norm_eps, block_table, prefix_len, B,
+                                         N, Hq, Hkv, max_pages, num_pages, q_out, k_cache, v_cache, dev_err);
+  p.tree_len = tree_len;
+  return jf::rotate_call(p, D, page_size, interleaved != 0, false, 0, stream);
+}
+
+extern "C" jf_status jf_rotate_append_kv_packed(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    const int32_t* pos, const double* freq, int32_t rotary_dim, int32_t interleaved, float rotary_scale,
+    const void* q_norm, const void* k_norm, float norm_eps, const int32_t* block_table,
+    const int32_t* prefix_len, const int32_t* cu_seqlens, int32_t B, int32_t N_max, int32_t T, int32_t Hq,
+    int32_t Hkv, int32_t D, int32_t page_size, int32_t max_pages, int32_t num_pages, void* q_out,
+    void* k_cache, void* v_cache, int32_t* dev_err, jf_stream_t stream) {
+  if (cu_seqlens == nullptr) return JF_ERR_INVALID_ARGUMENT;
+  jf::RotateParams p = jf::rotate_params(q, q_stride, k, k_stride, v, v_stride, pos, freq, rotary_dim,
+                                         rotary_scale, q_norm, k_norm, norm_eps, block_table, prefix_len, B,
+                                         N_max, Hq, Hkv, max_pages, num_pages, q_out, k_cache, v_cache,
+                                         dev_err);
+  p.cu = cu_seqlens;
+  return jf::rotate_call(p, D, page_size, interleaved != 0, true, T, stream);
+}

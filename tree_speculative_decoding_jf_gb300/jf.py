@@ -10,6 +10,7 @@ also allocate the outputs (with torch) before calling the same entry points.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -28,6 +29,7 @@ DEVERR_BAD_TOKEN, DEVERR_TIMEOUT, DEVERR_BAD_PATH = 0x8, 0x10, 0x20
 DEVERR_BAD_TREE_LEN = 0x40
 MAX_NODES = 4096
 PAGE_SIZE = 16
+COUNT_PROMPT = 1 << 30
 
 
 class JFError(RuntimeError):
@@ -115,6 +117,19 @@ def _load():
     lib.jf_beam_select.restype = ctypes.c_int
     lib.jf_beam_fork_kv.argtypes = [P, P, P, P, P, P] + [i32] * 8 + [P, P, P, P]
     lib.jf_beam_fork_kv.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    rotate = [P, i64, P, i64, P, i64, P, P, i32, i32, f32, P, P, f32, P, P, P]
+    lib.jf_rotate_append_kv.argtypes = rotate + [i32] * 8 + [P, P, P, P, P]
+    lib.jf_rotate_append_kv.restype = ctypes.c_int
+    lib.jf_rotate_append_kv_packed.argtypes = rotate + [i32] * 9 + [P, P, P, P, P]
+    lib.jf_rotate_append_kv_packed.restype = ctypes.c_int
+    adjust = [P, i32, P, P, P, P, P, P, i32, P, P, P, f32, P]
+    lib.jf_adjust_logits.argtypes = adjust + [i32] * 3 + [P, i32, P, P]
+    lib.jf_adjust_logits.restype = ctypes.c_int
+    lib.jf_adjust_logits_packed.argtypes = adjust + [i32] * 4 + [P, i32, P, P]
+    lib.jf_adjust_logits_packed.restype = ctypes.c_int
+    lib.jf_count_tokens.argtypes = [P, P, i32, P, P, P, P, i32, i32, i32, i32, P, P, P]
+    lib.jf_count_tokens.restype = ctypes.c_int
     return lib
 
 
@@ -799,6 +814,144 @@ def jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_pag
         _at(new_prefix_len), _at(dev_err), on))
 
 
+def _token_rows(name, t, lead) -> int:
+    """Elements between consecutive tokens of a bf16 [..., H, D] tensor whose heads are
+    contiguous and whose token rows lie evenly apart (a slice of a projection's output)."""
+    H, D = t.shape[-2:]
+    strides = t.stride()
+    if D > 1 and strides[-1] != 1 or H > 1 and strides[-2] != D:
+        raise ValueError(f"{name} must have contiguous heads")
+    if len(lead) == 1:
+        return strides[0] if lead[0] > 1 else H * D
+    B, N = lead
+    if N == 1:
+        return strides[0] if B > 1 else H * D
+    if B > 1 and strides[0] != N * strides[1]:
+        raise ValueError(f"the token rows of {name} must lie evenly apart")
+    return strides[1]
+
+
+def _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, lead, q_out, pos, freq, interleaved,
+                 rotary_scale, q_norm, k_norm, norm_eps, tree_len, cu_seqlens, N_max, dev_err, stream):
+    num_pages, page, Hkv, D = k_cache.shape
+    B, max_pages = block_table.shape
+    cur = torch.cuda.current_device()
+    strides = []
+    for name, t, H in (("q", q, None if q is None else q.shape[-2]), ("k", k, Hkv), ("v", v, Hkv)):
+        if t is None:
+            strides.append(0)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if tuple(t.shape) != tuple(lead) + (H, D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(lead) + (H, D)}")
+        if t.get_device() != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+        strides.append(_token_rows(name, t, lead))
+    Hq = 0 if q is None else q.shape[-2]
+    R = 0 if freq is None else 2 * freq.numel()
+    specs = (("k_cache", k_cache, torch.bfloat16, None), ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+             ("block_table", block_table, torch.int32, None), ("prefix_len", prefix_len, torch.int32, (B,)),
+             ("pos", pos, torch.int32, lead), ("freq", freq, torch.float64, (R // 2,)),
+             ("q_norm", q_norm, torch.bfloat16, (D,)), ("k_norm", k_norm, torch.bfloat16, (D,)),
+             ("q_out", q_out, torch.bfloat16, tuple(lead) + (Hq, D)),
+             ("tree_len", tree_len, torch.int32, (B,)), ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
+    on = _on_stream(specs, dev_err, stream)
+    first = (_at(q), strides[0], _at(k), strides[1], _at(v), strides[2], _at(pos), _at(freq), R,
+             1 if interleaved else 0, float(rotary_scale), _at(q_norm), _at(k_norm), float(norm_eps),
+             _at(block_table), _at(prefix_len))
+    last = (Hq, Hkv, D, page, max_pages, num_pages, _at(q_out), _at(k_cache), _at(v_cache), _at(dev_err), on)
+    if cu_seqlens is None:
+        _check("jf_rotate_append_kv", _lib.jf_rotate_append_kv(*first, _at(tree_len), B, lead[1], *last))
+    else:
+        _check("jf_rotate_append_kv_packed", _lib.jf_rotate_append_kv_packed(
+            *first, _at(cu_seqlens), B, N_max, lead[0], *last))
+
+
+def jf_rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, q_out, pos=None, freq=None,
+                        interleaved=False, rotary_scale=1.0, q_norm=None, k_norm=None, norm_eps=1e-6,
+                        tree_len=None, dev_err=None, stream=None) -> None:
+    """Rotates a step's queries [B][N][Hq][D] and keys [B][N][Hkv][D] and appends its keys and
+    values to the paged cache (see include/jf.h).  q, k and v may be slices of one projection's
+    output; q and q_out may be None."""
+    B = block_table.shape[0]
+    if k.dim() != 4 or k.shape[0] != B:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, N, Hkv, D)")
+    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, (B, k.shape[1]), q_out, pos, freq,
+                 interleaved, rotary_scale, q_norm, k_norm, norm_eps, tree_len, None, None, dev_err, stream)
+
+
+def jf_rotate_append_kv_packed(q, k, v, k_cache, v_cache, block_table, prefix_len, cu_seqlens, N_max, q_out,
+                               pos=None, freq=None, interleaved=False, rotary_scale=1.0, q_norm=None,
+                               k_norm=None, norm_eps=1e-6, dev_err=None, stream=None) -> None:
+    """jf_rotate_append_kv on packed rows: q [T][Hq][D], k and v [T][Hkv][D], pos [T]."""
+    if k.dim() != 3:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (T, Hkv, D)")
+    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, (k.shape[0],), q_out, pos, freq,
+                 interleaved, rotary_scale, q_norm, k_norm, norm_eps, None, cu_seqlens, int(N_max), dev_err, stream)
+
+
+def jf_adjust_logits(logits, out, count=None, draft=None, mask=None, bias=None, allowed=None, allowed_row=None,
+                     repetition=None, presence=None, frequency=None, masked=float("-inf"), tree_len=None,
+                     dev_err=None, stream=None) -> None:
+    """Penalties, biases and grammar masks on logits [B][N][V] (see include/jf.h); out has their
+    type or float32 and may be logits."""
+    B, N, V = logits.shape
+    _adjust_call(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
+                 masked, tree_len, None, B, N, dev_err, stream)
+
+
+def jf_adjust_logits_packed(logits, out, cu_seqlens, N_max, count=None, draft=None, mask=None, bias=None,
+                            allowed=None, allowed_row=None, repetition=None, presence=None, frequency=None,
+                            masked=float("-inf"), dev_err=None, stream=None) -> None:
+    """jf_adjust_logits on packed rows: logits [T][V], draft and allowed_row [T], mask [T][W]."""
+    T, V = logits.shape
+    _adjust_call(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
+                 masked, None, cu_seqlens, cu_seqlens.shape[0] - 1, int(N_max), dev_err, stream)
+
+
+def _adjust_call(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
+                 masked, tree_len, cu_seqlens, B, N, dev_err, stream):
+    V = logits.shape[-1]
+    lead = tuple(logits.shape[:-1])
+    dt, odt = _logit_dtype(logits), _logit_dtype(out)
+    n_allowed = 0 if allowed is None else allowed.shape[0]
+    if allowed is not None and allowed_row is None and n_allowed != logits.numel() // max(V, 1):
+        raise ValueError(f"allowed has {n_allowed} rows, one for each of {logits.numel() // max(V, 1)} nodes is expected")
+    on = _on_stream((("logits", logits, logits.dtype, None), ("out", out, out.dtype, logits.shape),
+                     ("count", count, torch.int32, (B, V)), ("draft", draft, torch.int32, lead),
+                     ("mask", mask, torch.int64, lead + ((N + 63) // 64,)), ("bias", bias, torch.float32, (B, V)),
+                     ("allowed", allowed, torch.int32, (n_allowed, (V + 31) // 32)),
+                     ("allowed_row", allowed_row, torch.int32, lead),
+                     ("repetition", repetition, torch.float32, (B,)), ("presence", presence, torch.float32, (B,)),
+                     ("frequency", frequency, torch.float32, (B,)), ("tree_len", tree_len, torch.int32, (B,)),
+                     ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))), dev_err, stream)
+    first = (_at(logits), dt, _at(count), _at(draft), _at(mask), _at(bias), _at(allowed), _at(allowed_row), n_allowed,
+             _at(repetition), _at(presence), _at(frequency), float(masked))
+    last = (V, _at(out), odt, _at(dev_err), on)
+    if cu_seqlens is None:
+        _check("jf_adjust_logits", _lib.jf_adjust_logits(*first, _at(tree_len), B, N, *last))
+    else:
+        _check("jf_adjust_logits_packed", _lib.jf_adjust_logits_packed(*first, _at(cu_seqlens), B, N, lead[0], *last))
+
+
+def jf_count_tokens(count, token, count_out, path=None, length=None, extra=None, row=None, prompt=False,
+                    dev_err=None, stream=None) -> None:
+    """Adds a step's tokens to the counts that jf_adjust_logits reads (see include/jf.h)."""
+    B, N = token.shape
+    V = count_out.shape[-1]
+    rows_in = 0 if count is None else count.shape[0]
+    on = _on_stream((("count", count, torch.int32, (rows_in, V)), ("token", token, torch.int32, None),
+                     ("count_out", count_out, torch.int32, (B, V)), ("path", path, torch.int32, (B, N)),
+                     ("length", length, torch.int32, (B,)), ("extra", extra, torch.int32, (B,)),
+                     ("row", row, torch.int32, (B,))), dev_err, stream)
+    _check("jf_count_tokens", _lib.jf_count_tokens(
+        _at(count), _at(row), rows_in, _at(token), _at(path), _at(length), _at(extra), 1 if prompt else 0, B, N, V,
+        _at(count_out), _at(dev_err), on))
+
+
 # ----------------------------------------------------------------------------- conveniences
 
 def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
@@ -1002,3 +1155,94 @@ def beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, 
     jf_beam_fork_kv(k_cache, v_cache, block_table, prefix_len, parent, fresh_page, new_table,
                     new_len, dev_err)
     return new_table, new_len
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, device="cuda"):
+    """(freq, rotary_scale) for rotate_append_kv: float64 [rotary_dim / 2] radians per position,
+    base^(-2 f / rotary_dim), and the factor on the rotated elements.  scaling for contexts longer
+    than the model was trained on: None; ("linear", factor), every frequency divided by factor; or
+    ("yarn", factor, trained_length), which divides the frequencies that turn less than once in
+    trained_length positions, keeps those that turn more than 32 times, goes over between them in a
+    linear ramp over the pair's index, and scales by 0.1 ln(factor) + 1."""
+    f = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    freq = float(base) ** -f
+    if scaling is None:
+        return freq.to(device), 1.0
+    kind, factor = scaling[0], float(scaling[1])
+    if not factor >= 1.0:
+        raise ValueError(f"the scaling factor must be at least 1, got {factor}")
+    if kind == "linear":
+        return (freq / factor).to(device), 1.0
+    if kind != "yarn":
+        raise ValueError(f"unknown rotary scaling {kind!r}")
+    length = float(scaling[2])
+
+    def pair_of(turns):        # the (fractional) pair that turns so often in trained_length positions
+        return rotary_dim * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+    low = max(math.floor(pair_of(32.0)), 0)
+    high = min(math.ceil(pair_of(1.0)), rotary_dim - 1)
+    ramp = ((torch.arange(rotary_dim // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+    return (freq / factor * ramp + freq * (1.0 - ramp)).to(device), 0.1 * math.log(factor) + 1.0
+
+
+def rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, pos=None, freq=None, interleaved=False,
+                     rotary_scale=1.0, q_norm=None, k_norm=None, norm_eps=1e-6, tree_len=None, cu_seqlens=None,
+                     N_max=None, out=None, dev_err=None, stream=None):
+    """Appends the step's keys and values to the cache and returns its rotated queries (written to
+    out if given; padding rows of a new tensor are zero).  q [B][N][Hq][D], or [T][Hq][D] with
+    cu_seqlens (N_max: the longest sequence's rows, by default T)."""
+    if out is None and q is not None:
+        if stream is not None:
+            with _as_current(stream):
+                return rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, pos, freq, interleaved,
+                                        rotary_scale, q_norm, k_norm, norm_eps, tree_len, cu_seqlens, N_max, None,
+                                        dev_err)
+        make = torch.empty if tree_len is None and cu_seqlens is None else torch.zeros
+        out = make(q.shape, dtype=q.dtype, device=q.device)
+    if cu_seqlens is None:
+        jf_rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, out, pos, freq, interleaved,
+                            rotary_scale, q_norm, k_norm, norm_eps, tree_len, dev_err, stream)
+    else:
+        jf_rotate_append_kv_packed(q, k, v, k_cache, v_cache, block_table, prefix_len, cu_seqlens,
+                                   k.shape[0] if N_max is None else N_max, out, pos, freq, interleaved, rotary_scale,
+                                   q_norm, k_norm, norm_eps, dev_err, stream)
+    return out
+
+
+def adjust_logits(logits, count=None, draft=None, mask=None, bias=None, allowed=None, allowed_row=None,
+                  repetition=None, presence=None, frequency=None, masked=float("-inf"), tree_len=None,
+                  cu_seqlens=None, N_max=None, out=None, dev_err=None, stream=None):
+    """The logits under penalties, biases and grammar masks: written to out if given (out may be
+    logits), else to a new tensor, whose padding rows are zero.  With cu_seqlens the rows are packed;
+    N_max is then the largest tree (by default what mask's width allows, or without one the rows)."""
+    if out is None:
+        if stream is not None:
+            with _as_current(stream):
+                return adjust_logits(logits, count, draft, mask, bias, allowed, allowed_row, repetition, presence,
+                                     frequency, masked, tree_len, cu_seqlens, N_max, None, dev_err)
+        make = torch.empty if tree_len is None and cu_seqlens is None else torch.zeros
+        out = make(logits.shape, dtype=logits.dtype, device=logits.device)
+    if cu_seqlens is None:
+        jf_adjust_logits(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
+                         masked, tree_len, dev_err, stream)
+    else:
+        if N_max is None:
+            N_max = min(logits.shape[0], MAX_NODES) if mask is None else 64 * mask.shape[-1]
+        jf_adjust_logits_packed(logits, out, cu_seqlens, N_max, count, draft, mask, bias, allowed, allowed_row,
+                                repetition, presence, frequency, masked, dev_err, stream)
+    return out
+
+
+def count_tokens(count, token, path=None, length=None, extra=None, row=None, prompt=False, V=None, out=None,
+                 dev_err=None, stream=None):
+    """The counts with a step's tokens added, in place (out=count), in out, or in a new tensor.
+    count None: zeros, over a vocabulary of V tokens (or out's)."""
+    if out is None:
+        if stream is not None:
+            with _as_current(stream):
+                return count_tokens(count, token, path, length, extra, row, prompt, V, None, dev_err)
+        size = count.shape[-1] if count is not None else int(V)
+        out = torch.empty((token.shape[0], size), dtype=torch.int32, device=token.device)
+    jf_count_tokens(count, token, out, path, length, extra, row, prompt, dev_err, stream)
+    return out
