@@ -9,13 +9,13 @@
 //     v forbidden by the node's grammar row: x = masked.
 //
 // Bound: bytes (logits read and written once).  A block owns a slice of 2048 tokens, eight per
-// thread, for a run of rows of one sequence: what depends on the sequence alone (counts and
-// bias, 8 bytes a token) becomes one multiplier choice and one addend per token in registers
-// and serves all rows of the run, so a row costs its logits, its output and one grammar bit a
-// token.  Logits of eight tokens that the grammar forbids are not read.  A branch's drafted
-// tokens are few and fall into few slices: a bitmap of the nodes whose token lies in the slice
-// is formed once, ANDed with each row's ancestor mask, and only rows with a hit walk the hits,
-// each hit counted by the thread that owns the token (no atomics, no shared table).
+// thread, for a run of up to 16 rows of one sequence.  Few of the tokens change (a prompt's, the
+// generated and drafted ones, those with a bias), so the rows are first copied under their grammar
+// bits, as words, without unpacking a value; logits of eight tokens that the grammar forbids are
+// not read.  Then the slice's changed tokens, listed once for the run from the counts, the biases
+// and the drafted tokens, are computed one (row, token) pair a thread and written over the copy.
+// A branch's drafted tokens: a bitmap of the nodes whose token lies in the slice is ANDed with the
+// rows' ancestor masks in shared memory, and only rows with a hit walk theirs.
 #include <algorithm>
 #include <cmath>
 
@@ -28,6 +28,7 @@ constexpr int kAdjThreads = 256;
 constexpr int kPer = 8;                        // tokens per thread
 constexpr int kSlice = kAdjThreads * kPer;
 constexpr int kMaxRun = 16;                    // rows per block at most
+constexpr int kAdjBlocks = 5;                  // resident blocks per SM
 constexpr int kPromptFlag = JF_COUNT_PROMPT;
 
 struct AdjustParams {
@@ -79,87 +80,179 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+
+// Eight logits of a thread on their way from input to output: bf16 that stays bf16 travels as
+// the words it was read in, so values that nothing changes are neither unpacked nor rounded.
+template <typename TI, typename TO>
+struct Chunk {
+  float x[kPer];
+  __device__ __forceinline__ void load(const TI* p) { load8(p, x); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+  }
+  __device__ __forceinline__ float get(int at) const {
+    float y = x[0];
+#pragma unroll
+    for (int e = 1; e < kPer; ++e) y = at == e ? +x[e] : +y;     // values, not places: x stays in registers
+    return y;
+  }
+  __device__ __forceinline__ void put(int at, float y) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = at == e ? +y : +x[e];
+  }
+  __device__ __forceinline__ void forbid(uint32_t ok, float masked) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = (ok >> e) & 1u ? x[e] : masked;
+  }
+  __device__ __forceinline__ void store(TO* p) const { store8(p, x); }
+};
+__device__ __forceinline__ uint32_t pick(bool c, uint32_t a, uint32_t b) {   // by value: what it picks from stays in registers
+  uint32_t r;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tselp.b32 %0, %1, %2, p;\n\t}" : "=r"(r) : "r"(a), "r"(b), "r"(c ? 1u : 0u));
+  return r;
 }
+template <>
+struct Chunk<uint16_t, uint16_t> {
+  uint32_t w0, w1, w2, w3;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w0 = v.x; w1 = v.y; w2 = v.z; w3 = v.w;
+  }
+  __device__ __forceinline__ void zero() { w0 = w1 = w2 = w3 = 0u; }
+  __device__ __forceinline__ float get(int at) const {
+    const uint32_t v = pick(at & 4, pick(at & 2, w3, w2), pick(at & 2, w1, w0));
+    return __uint_as_float(pick(at & 1, v & 0xFFFF0000u, v << 16));
+  }
+  __device__ __forceinline__ void put(int at, float y) {
+    const uint32_t bits = pack2(y, y), half = pick(at & 1, 0xFFFF0000u, 0x0000FFFFu);   // the bits to replace
+    const int at2 = at >> 1;
+    w0 ^= (w0 ^ bits) & pick(at2 == 0, half, 0u);
+    w1 ^= (w1 ^ bits) & pick(at2 == 1, half, 0u);
+    w2 ^= (w2 ^ bits) & pick(at2 == 2, half, 0u);
+    w3 ^= (w3 ^ bits) & pick(at2 == 3, half, 0u);
+  }
+  static __device__ __forceinline__ uint32_t under(uint32_t w, uint32_t ok2, uint32_t m) {
+    const uint32_t keep = (ok2 & 1u) * 0xFFFFu | ((ok2 >> 1) & 1u) * 0xFFFF0000u;      // where the token is allowed
+    return (w & keep) | (m & ~keep);
+  }
+  __device__ __forceinline__ void forbid(uint32_t ok, float masked) {
+    const uint32_t m = pack2(masked, masked);
+    w0 = under(w0, ok, m);
+    w1 = under(w1, ok >> 2, m);
+    w2 = under(w2, ok >> 4, m);
+    w3 = under(w3, ok >> 6, m);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w0, w1, w2, w3);
+  }
+};
 
 // VEC: a thread's eight tokens are consecutive and every row starts at a 16-byte boundary (V a
 // multiple of 8).  Otherwise they lie kAdjThreads apart, so that a warp's accesses of one
 // element each still cover whole sectors.
 template <typename TI, typename TO, bool VEC>
-__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustParams p) {
-  __shared__ unsigned long long s_hit[JF_MAX_NODES / 64];   // nodes whose token lies in the slice
-  __shared__ int s_any;
+__global__ void __launch_bounds__(kAdjThreads, kAdjBlocks) adjust_kernel(const AdjustParams p) {
+  __shared__ float s_add[kPer][kAdjThreads];   // a token's addend, for its own thread alone
+  __shared__ uint32_t s_drafted[kSlice / 32];  // tokens that a node of the tree drafts,
+  __shared__ uint16_t s_list[kSlice];          // listed
+  __shared__ int s_grammar[kMaxRun];           // the rows' grammar rows, -1: none
+  __shared__ uint32_t s_rows;                  // rows with a drafted token of the slice on their branch
+  __shared__ int s_any, s_listed;
+  extern __shared__ unsigned long long s_dyn[];
   grid_dependency_wait();
-  const int tid = threadIdx.x;
-  long long bid = blockIdx.x;
-  const int slice = static_cast<int>(bid % p.slices);
-  bid /= p.slices;
-  const int run = static_cast<int>(bid % p.runs);
-  const int b = static_cast<int>(bid / p.runs);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const unsigned per = static_cast<unsigned>(p.slices) * static_cast<unsigned>(p.runs);
+  const int b = static_cast<int>(blockIdx.x / per);
+  const unsigned rem = blockIdx.x - static_cast<unsigned>(b) * per;
+  const int run = static_cast<int>(rem / static_cast<unsigned>(p.slices));
+  const int slice = static_cast<int>(rem - static_cast<unsigned>(run) * static_cast<unsigned>(p.slices));
   const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
   if (!sp.ok && slice == 0 && run == 0 && tid == 0) report(p.dev_err, JF_DEVERR_BAD_TREE_LEN);
-  const int i0 = run * p.run, i1 = min(i0 + p.run, sp.n);
-  if (i0 >= i1) return;                        // block-uniform
+  const int i0 = run * p.run, rows = min(p.run, sp.n - i0);
+  if (rows <= 0) return;                       // block-uniform
   const int v0 = slice * kSlice;
   const int vmine = VEC ? v0 + tid * kPer : v0 + tid;        // first token of this thread
   constexpr int kStep = VEC ? 1 : kAdjThreads;               // to its next one
-
-  // What depends on the sequence alone.
+  const size_t base = static_cast<size_t>(b) * p.V;
   const float rep = p.repetition != nullptr ? p.repetition[b] : 1.f;
   const float pres = p.presence != nullptr ? p.presence[b] : 0.f;
   const float freq = p.frequency != nullptr ? p.frequency[b] : 0.f;
-  float add[kPer];                             // bias - presence - frequency * c
-  float sub[kPer];                             // bias alone
-  int c[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) c[e] = 0, sub[e] = 0.f;
-  const size_t base = static_cast<size_t>(b) * p.V;
-  if (VEC) {
-    if (vmine < p.V) {
-      if (p.count != nullptr) {
-        const int4 a = *reinterpret_cast<const int4*>(p.count + base + vmine);
-        const int4 d = *reinterpret_cast<const int4*>(p.count + base + vmine + 4);
-        c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-        c[4] = d.x; c[5] = d.y; c[6] = d.z; c[7] = d.w;
-      }
-      if (p.bias != nullptr) load8(p.bias + base + vmine, sub);
+
+  if (p.allowed != nullptr && tid < rows) {
+    const long long row = sp.row0 + i0 + tid;
+    long long at = p.allowed_row != nullptr ? p.allowed_row[row] : row;
+    if (at < 0 || at >= p.n_allowed) {
+      if (at != -1 && slice == 0) report(p.dev_err, JF_DEVERR_BAD_PATH);
+      at = -1;
     }
-  } else {
+    s_grammar[tid] = static_cast<int>(at);
+  }
+  if (tid < kSlice / 32) s_drafted[tid] = 0;
+  if (tid == 0) s_any = 0, s_rows = 0;
+
+  // What the history changes: marked tokens, the seen ones among them, and their addends.
+  uint32_t mark = 0, seen = 0;
+  if (p.count != nullptr || p.bias != nullptr) {
+    int c[kPer];
+    float bias[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) c[e] = 0, bias[e] = 0.f;
+    if (VEC) {
+      if (vmine < p.V) {
+        if (p.count != nullptr) {
+          const int4 a = *reinterpret_cast<const int4*>(p.count + base + vmine);
+          const int4 d = *reinterpret_cast<const int4*>(p.count + base + vmine + 4);
+          c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+          c[4] = d.x; c[5] = d.y; c[6] = d.z; c[7] = d.w;
+        }
+        if (p.bias != nullptr) load8(p.bias + base + vmine, bias);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int v = vmine + e * kStep;
+        if (v < p.V) {
+          if (p.count != nullptr) c[e] = p.count[base + v];
+          if (p.bias != nullptr) bias[e] = p.bias[base + v];
+        }
+      }
+    }
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      const int v = vmine + e * kStep;
-      if (v < p.V) {
-        if (p.count != nullptr) c[e] = p.count[base + v];
-        if (p.bias != nullptr) sub[e] = p.bias[base + v];
-      }
+      const int n = c[e] & (kPromptFlag - 1);
+      seen |= (c[e] != 0 ? 1u : 0u) << e;
+      mark |= (c[e] != 0 || bias[e] != 0.f ? 1u : 0u) << e;
+      s_add[e][tid] = n > 0 ? bias[e] - fmaf(freq, static_cast<float>(n), pres) : bias[e];
     }
   }
-  uint32_t seen = 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int n = c[e] & (kPromptFlag - 1);
-    seen |= (c[e] != 0 ? 1u : 0u) << e;
-    add[e] = n > 0 ? sub[e] - fmaf(freq, static_cast<float>(n), pres) : sub[e];
-  }
+  __syncthreads();
 
-  // Nodes whose drafted token lies in this slice.
-  bool hits = false;
+  // Nodes whose drafted token lies in this slice, the rows that have one on their branch, and the
+  // tokens' list.  Drafted tokens leave the marks: they are done row by row at the end.
+  const int words64 = (sp.n + 63) / 64;
+  unsigned long long* s_hit = s_dyn;           // [W] the nodes
+  unsigned long long* s_branch = s_dyn + p.W;  // [run][W] and the row's ancestors
+  uint16_t* s_at = reinterpret_cast<uint16_t*>(s_dyn + static_cast<size_t>(p.W) * (1 + p.run));   // [N] a node's place
+  bool any = false;
   if (p.draft != nullptr) {
-    if (tid == 0) s_any = 0;
-    __syncthreads();
     int bad = 0;
     const int words32 = (sp.n + 31) / 32;
     for (int w = tid >> 5; w < words32; w += kAdjThreads / 32) {
-      const int j = w * 32 + (tid & 31);
+      const int j = w * 32 + lane;
       bool in = false;
       if (j >= 1 && j < sp.n) {
         const int tok = p.draft[sp.row0 + j];
         if (tok < 0 || tok >= p.V) bad = 1;
         else in = tok >= v0 && tok - v0 < kSlice;
+        if (in) {
+          const int o = tok - v0;
+          s_at[j] = static_cast<uint16_t>(o);
+          atomicOr(&s_drafted[o >> 5], 1u << (o & 31));
+        }
       }
       const uint32_t m = __ballot_sync(0xffffffffu, in);
-      if ((tid & 31) == 0) {
+      if (lane == 0) {
         reinterpret_cast<uint32_t*>(s_hit)[w] = m;
         if (m != 0) s_any = 1;
       }
@@ -167,103 +260,140 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustParams 
     if (tid == 0 && (words32 & 1)) reinterpret_cast<uint32_t*>(s_hit)[words32] = 0;
     if (bad) report(p.dev_err, JF_DEVERR_BAD_TOKEN);
     __syncthreads();
-    hits = s_any != 0;
-  }
-
-  for (int i = i0; i < i1; ++i) {
-    const size_t row = static_cast<size_t>(sp.row0 + i);
-    // Grammar bits of the thread's tokens.
-    uint32_t ok = 0xFFu;
-    if (p.allowed != nullptr) {
-      const long long ar = p.allowed_row != nullptr ? p.allowed_row[row] : static_cast<long long>(row);
-      if (ar >= 0 && ar < p.n_allowed) {
-        const uint32_t* aw = p.allowed + static_cast<size_t>(ar) * p.words;
-        if (VEC) {
-          if (vmine < p.V) ok = reinterpret_cast<const uint8_t*>(aw)[vmine >> 3];
-        } else {
-          ok = 0;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            const int v = vmine + e * kStep;
-            if (v < p.V) ok |= ((aw[v >> 5] >> (v & 31)) & 1u) << e;
-          }
-        }
-      } else if (ar != -1 && tid == 0 && slice == 0) {
-        report(p.dev_err, JF_DEVERR_BAD_PATH);
-      }
-    }
-    // Drafted tokens of the branch, counted by their owners.
-    float ad[kPer];
-    uint32_t sn = seen;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) ad[e] = add[e];
-    if (hits) {
-      int extra[kPer];
-      bool any = false;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) extra[e] = 0;
-      const int words64 = (sp.n + 63) / 64;
-      for (int w = 0; w < words64; ++w) {
+    any = s_any != 0;                          // block-uniform
+    if (any) {
+      for (int e = tid; e < rows * words64; e += kAdjThreads) {
+        const int u = e / words64, w = e % words64;
         unsigned long long m = s_hit[w];
-        if (m != 0) m &= p.mask[row * p.W + w];
-        while (m != 0) {
-          const int j = w * 64 + __ffsll(static_cast<long long>(m)) - 1;
-          m &= m - 1;
-          const int o = p.draft[sp.row0 + j] - v0;
-          if ((VEC ? o / kPer : o % kAdjThreads) == tid) {
-            const int at = VEC ? o % kPer : o / kAdjThreads;
-            any = true;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) extra[e] += at == e ? 1 : 0;
-          }
-        }
+        if (m != 0) m &= p.mask[static_cast<size_t>(sp.row0 + i0 + u) * p.W + w];
+        s_branch[u * p.W + w] = m;
+        if (m != 0) atomicOr(&s_rows, 1u << u);
       }
-      if (any) {
+      if (tid < 32) {                          // lane l lists tokens 64 l .. 64 l + 63
+        unsigned long long d = static_cast<unsigned long long>(s_drafted[2 * lane + 1]) << 32 | s_drafted[2 * lane];
+        const int mine = __popcll(d);
+        int upto = mine;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          if (extra[e] > 0) {
-            const int n = (c[e] & (kPromptFlag - 1)) + extra[e];
-            sn |= 1u << e;
-            ad[e] = sub[e] - fmaf(freq, static_cast<float>(n), pres);
-          }
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
         }
+        if (lane == 31) s_listed = upto;
+        for (int at = upto - mine; d != 0; d &= d - 1)
+          s_list[at++] = static_cast<uint16_t>(64 * lane + __ffsll(static_cast<long long>(d)) - 1);
       }
-    }
-    const TI* src = static_cast<const TI*>(p.logits) + row * p.V;
-    TO* dst = static_cast<TO*>(p.out) + row * p.V;
-    float x[kPer];
-    if (VEC) {
-      if (vmine >= p.V) continue;
-      if (ok != 0) {
-        load8(src + vmine, x);
+      if (VEC) {
+        mark &= ~static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(s_drafted)[tid]);
       } else {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+        for (int e = 0; e < kPer; ++e) {
+          const int o = e * kAdjThreads + tid;
+          mark &= ~(((s_drafted[o >> 5] >> (o & 31)) & 1u) << e);
+        }
       }
-    } else {
+    }
+  }
+
+  // x under a seen token's repetition penalty.
+  auto repeated = [&](float x) { return x > 0.f ? x / rep : x * rep; };
+  const size_t first = static_cast<size_t>(sp.row0 + i0) * p.V;
+  const TI* logits = static_cast<const TI*>(p.logits) + first;     // the run's rows
+  TO* out = static_cast<TO*>(p.out) + first;
+  if constexpr (VEC) {
+    if (vmine < p.V) {
+      constexpr int kRows = sizeof(Chunk<TI, TO>) <= 16 ? 4 : 2;     // rows whose reads overlap
+      const uint8_t* bits = reinterpret_cast<const uint8_t*>(p.allowed) + (vmine >> 3);
+      for (int u0 = 0; u0 < rows; u0 += kRows) {
+        uint32_t ok[kRows];
+        Chunk<TI, TO> x[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          ok[k] = u0 + k < rows ? 0xFFu : 0u;
+          if (p.allowed != nullptr && u0 + k < rows) {
+            const int gr = s_grammar[u0 + k];
+            if (gr >= 0) ok[k] = bits[static_cast<size_t>(gr) * p.words * 4];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          if (ok[k] != 0) x[k].load(logits + static_cast<size_t>(u0 + k) * p.V + vmine);
+          else x[k].zero();                    // logits that the grammar forbids are not read
+        }
+        for (uint32_t m = mark; m != 0; m &= m - 1) {
+          const int e = __ffs(static_cast<int>(m)) - 1;
+          const float add = s_add[e][tid];
+          const bool again = (seen >> e) & 1u;
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            if (!((ok[k] >> e) & 1u)) continue;
+            float y = x[k].get(e);
+            if (again) y = repeated(y);
+            x[k].put(e, y + add);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          if (u0 + k >= rows || (p.in_place && ok[k] == 0xFFu && mark == 0)) continue;
+          if (ok[k] != 0xFFu) x[k].forbid(ok[k], p.masked);
+          x[k].store(out + static_cast<size_t>(u0 + k) * p.V + vmine);
+        }
+      }
+    }
+  } else {
+    for (int u = 0; u < rows; ++u) {
+      const int gr = p.allowed != nullptr ? s_grammar[u] : -1;
+      const uint32_t* words = p.allowed + static_cast<size_t>(max(gr, 0)) * p.words;
+      const size_t at = static_cast<size_t>(u) * p.V;
+      uint32_t ok = 0;
+      float y[kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         const int v = vmine + e * kStep;
-        x[e] = v < p.V && ((ok >> e) & 1u) ? load1<TI>(src + v) : 0.f;
+        if (v < p.V) ok |= (gr >= 0 ? (words[v >> 5] >> (v & 31)) & 1u : 1u) << e;
       }
-    }
-    bool same = ok == 0xFFu && sn == 0;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      same = same && ad[e] == 0.f;
-      if ((sn >> e) & 1u) x[e] = x[e] > 0.f ? x[e] / rep : x[e] * rep;
-      x[e] += ad[e];
-      if (!((ok >> e) & 1u)) x[e] = p.masked;
-    }
-    if (p.in_place && same) continue;          // the eight values stay as they are
-    if (VEC) {
-      store8(dst + vmine, x);
-    } else {
+      for (int e = 0; e < kPer; ++e) y[e] = (ok >> e) & 1u ? load1<TI>(logits + at + vmine + e * kStep) : p.masked;
+      if ((mark & ok) != 0) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          if (!((mark & ok) >> e & 1u)) continue;
+          if ((seen >> e) & 1u) y[e] = repeated(y[e]);
+          y[e] += s_add[e][tid];
+        }
+      }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         const int v = vmine + e * kStep;
-        if (v < p.V) store1(dst + v, x[e]);
+        if (v < p.V && !(p.in_place && (ok & ~mark) >> e & 1u)) store1(out + at + v, y[e]);
       }
+    }
+  }
+  if (any) {
+    // The drafted tokens of the slice, one (row, token) pair a thread.
+    __syncthreads();
+    const int n = s_listed;
+    const uint32_t hit_rows = s_rows;
+    for (int q = tid; q < n * rows; q += kAdjThreads) {
+      const int u = q / n, o = s_list[q - u * n], v = v0 + o;
+      const int gr = p.allowed != nullptr ? s_grammar[u] : -1;
+      if (gr >= 0 && !((p.allowed[static_cast<size_t>(gr) * p.words + (v >> 5)] >> (v & 31)) & 1u)) continue;
+      const int c = p.count != nullptr ? p.count[base + v] : 0;
+      const float bias = p.bias != nullptr ? p.bias[base + v] : 0.f;
+      const float x = load1<TI>(logits + static_cast<size_t>(u) * p.V + v);
+      int times = c & (kPromptFlag - 1);
+      bool again = c != 0;
+      if ((hit_rows >> u) & 1u) {              // on this row's branch?
+        for (int w = 0; w < words64; ++w) {
+          for (unsigned long long m = s_branch[u * p.W + w]; m != 0; m &= m - 1) {
+            const bool mine = s_at[w * 64 + __ffsll(static_cast<long long>(m)) - 1] == o;
+            times += mine ? 1 : 0;
+            again = again || mine;
+          }
+        }
+      }
+      if (!again && bias == 0.f) continue;
+      const float add = times > 0 ? bias - fmaf(freq, static_cast<float>(times), pres) : bias;
+      store1(out + static_cast<size_t>(u) * p.V + v, (again ? repeated(x) : x) + add);
     }
   }
   grid_dependents_launch();
@@ -299,27 +429,27 @@ jf_status adjust_call(AdjustParams p, int32_t dtype, int32_t out_dtype, bool pac
   if (sms <= 0) return JF_ERR_CUDA;
   p.W = (p.N + 63) / 64;
   p.slices = (p.V + kSlice - 1) / kSlice;
-  // Rows per block: 16, so that counts and bias cost half a byte a logit at most, fewer while
-  // the grid would leave SMs short of blocks.
-  p.run = kMaxRun < p.N ? kMaxRun : p.N;
-  while (p.run > 1 && static_cast<long long>(p.B) * p.slices * ((p.N + p.run - 1) / p.run) < 8ll * sms) p.run = (p.run + 1) / 2;
+  if (static_cast<long long>(p.B) * p.N * p.slices > 0x7FFFFFFFll) return JF_ERR_UNSUPPORTED;
+  // Rows per block: 16, so that what a block does once weighs little, fewer while the grid would
+  // leave SMs short of blocks.
+  p.run = std::min(kMaxRun, p.N);
+  while (p.run > 1 && static_cast<long long>(p.B) * p.slices * ((p.N + p.run - 1) / p.run) < 2ll * sms) p.run = (p.run + 1) / 2;
   p.runs = (p.N + p.run - 1) / p.run;
-  const long long grid = static_cast<long long>(p.B) * p.runs * p.slices;
-  if (grid > 0x7FFFFFFFll) return JF_ERR_UNSUPPORTED;
   const bool vec = p.V % 8 == 0 && aligned_to(p.logits, 16) && aligned_to(p.out, 16) && aligned_to(p.count, 16) &&
                    aligned_to(p.bias, 16);
-  const dim3 g(static_cast<unsigned>(grid)), t(kAdjThreads);
+  const dim3 g(static_cast<unsigned>(p.B * p.runs * p.slices)), t(kAdjThreads);
+  const size_t smem = p.draft != nullptr ? static_cast<size_t>(p.W) * 8 * (1 + p.run) + static_cast<size_t>(p.N) * 2 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == JF_DTYPE_F32)
-    e = vec ? launch_pdl(adjust_kernel<float, float, true>, g, t, 0, s, p)
-            : launch_pdl(adjust_kernel<float, float, false>, g, t, 0, s, p);
+    e = vec ? launch_pdl(adjust_kernel<float, float, true>, g, t, smem, s, p)
+            : launch_pdl(adjust_kernel<float, float, false>, g, t, smem, s, p);
   else if (out_dtype == JF_DTYPE_F32)
-    e = vec ? launch_pdl(adjust_kernel<uint16_t, float, true>, g, t, 0, s, p)
-            : launch_pdl(adjust_kernel<uint16_t, float, false>, g, t, 0, s, p);
+    e = vec ? launch_pdl(adjust_kernel<uint16_t, float, true>, g, t, smem, s, p)
+            : launch_pdl(adjust_kernel<uint16_t, float, false>, g, t, smem, s, p);
   else
-    e = vec ? launch_pdl(adjust_kernel<uint16_t, uint16_t, true>, g, t, 0, s, p)
-            : launch_pdl(adjust_kernel<uint16_t, uint16_t, false>, g, t, 0, s, p);
+    e = vec ? launch_pdl(adjust_kernel<uint16_t, uint16_t, true>, g, t, smem, s, p)
+            : launch_pdl(adjust_kernel<uint16_t, uint16_t, false>, g, t, smem, s, p);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 

@@ -26,7 +26,9 @@ namespace jf {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kRotThreads = 256;
+constexpr int kMaxThreads = 512;
+constexpr long long kFewRows = 16;          // per SM: up to there a block takes one token
+constexpr int kTokens = 4;                  // tokens per block once every SM has blocks enough
 
 struct RotateParams {
   const uint16_t *q, *k, *v;
@@ -57,21 +59,45 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
+// Where a token belongs: its sequence, the sequence's span and its prefix length.
+struct Home {
+  int b, P;
+  SeqSpan sp;
+};
+
 // The sequence whose packed span holds `row`: the last b with cu[b] <= row, found by the whole
-// warp, 32 probes a round (one round up to 32 sequences, two up to 1024).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, long long row) {
+// warp, 32 probes a round (one round up to 32 sequences, two up to 1024).  The last round's
+// probes bring the spans' ends and the prefix lengths along, so they cost no further trip.
+__device__ __forceinline__ Home packed_home(const RotateParams& p, long long row) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, len = B;
-  while (len > 1) {
+  int lo = 0, len = p.B;
+  while (len > 32) {
     const int step = (len + 31) / 32;
     const int at = lane * step;
-    const bool below = at < len && cu[lo + at] <= row;
-    const int n = __popc(__ballot_sync(0xffffffffu, below));
-    const int skip = max(n - 1, 0) * step;
+    const bool below = at < len && p.cu[lo + at] <= row;
+    const int skip = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0) * step;
     lo += skip;
     len = min(step, len - skip);
   }
-  return lo;
+  const int at = lo + min(lane, len - 1);
+  const int r0 = p.cu[at], r1 = p.cu[at + 1], P = p.prefix_len[at];
+  const int sel = max(__popc(__ballot_sync(0xffffffffu, lane < len && r0 <= row)) - 1, 0);
+  Home h;
+  h.b = lo + sel;
+  h.P = __shfl_sync(0xffffffffu, P, sel);
+  const long long a = __shfl_sync(0xffffffffu, r0, sel), e = __shfl_sync(0xffffffffu, r1, sel);
+  h.sp.ok = a >= 0 && e <= p.rows && e - a >= 1 && e - a <= p.N;
+  h.sp.row0 = h.sp.ok ? a : 0;
+  h.sp.n = h.sp.rows = h.sp.ok ? static_cast<int>(e - a) : 0;
+  return h;
+}
+
+__device__ __forceinline__ Home padded_home(const RotateParams& p, long long row) {
+  Home h;
+  h.b = static_cast<int>(row / p.N);
+  h.P = p.prefix_len[h.b];
+  h.sp = seq_span(nullptr, p.tree_len, h.b, p.N, p.rows);
+  return h;
 }
 
 // Fraction of a turn per position, as a 64-bit fixed-point number (whole turns dropped).
@@ -81,67 +107,21 @@ __device__ __forceinline__ uint64_t fixed_turns(double freq) {
   return __double2ull_rn(t * 18446744073709551616.0);
 }
 
-// TB tokens per block.  INTER: pairs (2 f, 2 f + 1) instead of (f, f + R / 2).
+// TB tokens per block.  INTER: pairs (2 f, 2 f + 1) instead of (f, f + R / 2).  A block has a
+// thread for each pair of chunks of a token's heads (up to kMaxThreads: more heads take more
+// rounds), and its first loads, all TB tokens at once, are on their way before it looks up pages
+// and forms angles, whose chain of dependent reads they hide.
 template <int D, bool INTER, int TB>
-__global__ void __launch_bounds__(kRotThreads) rotate_append_kernel(const RotateParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 2) rotate_append_kernel(const RotateParams p) {
   constexpr int kLanes = D / 16;            // threads per head row
-  constexpr int kSlots = kRotThreads / kLanes;
   __shared__ float2 s_cs[TB][D / 2];        // (cos, sin) * scale
   __shared__ long long s_cache[TB];         // cache row of the token, -1: none
   __shared__ int s_live[TB];
-  __shared__ int s_pos[TB];
   grid_dependency_wait();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row0 = static_cast<long long>(blockIdx.x) * TB;
   const int cap = p.max_pages * kPage;
-  if (blockIdx.x == 0) {                    // every sequence's span and length are judged once
-    for (int b = threadIdx.x; b < p.B; b += kRotThreads) {
-      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.rows);
-      if (!sp.ok) report(p.dev_err, JF_DEVERR_BAD_TREE_LEN);
-      const int P = p.prefix_len[b];
-      if (P < 0 || P > cap - sp.n) report(p.dev_err, JF_DEVERR_BAD_PREFIX);
-    }
-  }
-  if (warp < TB) {
-    const long long row = row0 + warp;
-    bool live = row < p.rows;
-    long long at = -1;
-    if (live) {                             // warp-uniform
-      const int b = p.cu != nullptr ? find_sequence(p.cu, p.B, row) : static_cast<int>(row / p.N);
-      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.rows);
-      const long long i = row - sp.row0;
-      live = i >= 0 && i < sp.n;
-      if (live && lane == 0) {
-        const int P = p.prefix_len[b];
-        if (P >= 0 && P <= cap - sp.n) {
-          const int t = P + static_cast<int>(i);
-          const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + t / kPage];
-          if (page >= 0 && page < p.num_pages)
-            at = static_cast<long long>(page) * kPage + t % kPage;
-          else
-            report(p.dev_err, JF_DEVERR_BAD_PAGE);
-        }
-      }
-    }
-    if (lane == 0) {
-      s_live[warp] = live ? 1 : 0;
-      s_cache[warp] = at;
-      s_pos[warp] = live && p.freq != nullptr ? p.pos[row] : 0;
-    }
-  }
-  __syncthreads();
-  const int pairs = p.freq != nullptr ? p.R / 2 : 0;
-  for (int e = threadIdx.x; e < TB * pairs; e += kRotThreads) {
-    const int tok = e / pairs, f = e % pairs;
-    const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(s_pos[tok])) * fixed_turns(p.freq[f]);
-    // signed fraction of a turn in [-1/2, 1/2), in units of pi: [-1, 1)
-    const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;   // 2^-63
-    float s, c;
-    sincospif(x, &s, &c);
-    s_cs[tok][f] = make_float2(c * p.scale, s * p.scale);
-  }
-  __syncthreads();
 
   // Thread t of a head: the rotated chunks t and t + R / 16, or two of the chunks behind R.
   const int t = threadIdx.x % kLanes;
@@ -150,54 +130,104 @@ __global__ void __launch_bounds__(kRotThreads) rotate_append_kernel(const Rotate
   const int c0 = turns ? t : 2 * half + 2 * (t - half);
   const int c1 = turns ? t + half : c0 + 1;
   const int heads = p.Hq + 2 * p.Hkv;
+  const int slots = blockDim.x / kLanes;
+  uint4 w0[TB], w1[TB];
+  auto load = [&](int h) {
+    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+    const uint16_t* src = is_q ? p.q : (is_v ? p.v : p.k);
+    const long long stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
+    const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
 #pragma unroll
-  for (int tok = 0; tok < TB; ++tok) {
-    if (!s_live[tok]) continue;             // block-uniform
-    const long long row = row0 + tok;
-    const long long at = s_cache[tok];
-    float cs[8], sn[8];
-    if (turns) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // half: the eight pairs of chunk t; interleaved: four pairs of each chunk
-        const int f = !INTER ? 8 * t + e : (e < 4 ? 4 * c0 + e : 4 * c1 + e - 4);
-        const float2 v = s_cs[tok][f];
-        cs[e] = v.x;
-        sn[e] = v.y;
+    for (int k = 0; k < TB; ++k) {
+      w0[k] = w1[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < heads && row0 + k < p.rows) {      // padding rows exist too; what they hold is dropped
+        const uint4* s4 = reinterpret_cast<const uint4*>(src + (row0 + k) * stride + hh * D);
+        w0[k] = s4[c0];
+        w1[k] = s4[c1];
       }
     }
-    for (int h0 = 0; h0 < heads; h0 += kSlots) {
-      const int h = h0 + threadIdx.x / kLanes;
-      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-      const bool act = h < heads && (is_q || at >= 0);
-      const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
-      uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
-      uint4* dst = nullptr;
-      if (act) {
-        const uint16_t* src = is_q ? p.q + row * p.q_stride
-                                   : (is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride);
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + hh * D);
-        w0 = s4[c0];
-        w1 = s4[c1];
-        uint16_t* d = is_q ? p.q_out + (row * p.Hq + hh) * D
-                           : (is_v ? p.v_cache : p.k_cache) + (at * p.Hkv + hh) * D;
-        dst = reinterpret_cast<uint4*>(d);
+  };
+  load(threadIdx.x / kLanes);
+  auto weight = [&](int h) -> const uint16_t* {       // of head h, null: not normalised
+    return h < p.Hq ? p.q_norm : (h < p.Hq + p.Hkv ? p.k_norm : nullptr);
+  };
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  auto load_weight = [&](int h) {
+    const uint4* w = reinterpret_cast<const uint4*>(weight(h));
+    if (w != nullptr) n0 = w[c0], n1 = w[c1];
+  };
+  if (TB == 1) load_weight(threadIdx.x / kLanes);     // with more tokens a block the registers go to their rows
+
+  if (blockIdx.x == 0) {                    // every sequence's span and length are judged once
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.rows);
+      if (!sp.ok) report(p.dev_err, JF_DEVERR_BAD_TREE_LEN);
+      const int P = p.prefix_len[b];
+      if (P < 0 || P > cap - sp.n) report(p.dev_err, JF_DEVERR_BAD_PREFIX);
+    }
+  }
+  const int warps = blockDim.x >> 5;
+  for (int k = warps - 1 - warp; k < TB; k += warps) {      // the last warps: the first ones form angles
+    const long long row = row0 + k;
+    bool live = row < p.rows;
+    long long at = -1;
+    if (live) {                             // warp-uniform
+      const Home h = p.cu != nullptr ? packed_home(p, row) : padded_home(p, row);
+      const long long i = row - h.sp.row0;
+      live = i >= 0 && i < h.sp.n;
+      if (live && lane == 0 && h.P >= 0 && h.P <= cap - h.sp.n) {
+        const int pt = h.P + static_cast<int>(i);
+        const int page = p.block_table[static_cast<size_t>(h.b) * p.max_pages + pt / kPage];
+        if (page >= 0 && page < p.num_pages)
+          at = static_cast<long long>(page) * kPage + pt % kPage;
+        else
+          report(p.dev_err, JF_DEVERR_BAD_PAGE);
       }
-      const uint16_t* norm = is_v ? nullptr : (is_q ? p.q_norm : p.k_norm);
+    }
+    if (lane == 0) {
+      s_live[k] = live ? 1 : 0;
+      s_cache[k] = at;
+    }
+  }
+  const int pairs = p.freq != nullptr ? p.R / 2 : 0;
+  for (int e = threadIdx.x; e < TB * pairs; e += blockDim.x) {
+    const int k = e / pairs, f = e % pairs;
+    const long long pos = row0 + k < p.rows ? p.pos[row0 + k] : 0;
+    const uint64_t turn = static_cast<uint64_t>(pos) * fixed_turns(p.freq[f]);
+    // signed fraction of a turn in [-1/2, 1/2), in units of pi: [-1, 1)
+    const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;   // 2^-63
+    float s, c;
+    sincospif(x, &s, &c);
+    s_cs[k][f] = make_float2(c * p.scale, s * p.scale);
+  }
+  __syncthreads();
+
+  const bool any_norm = p.q_norm != nullptr || p.k_norm != nullptr;
+  for (int h0 = 0; h0 < heads; h0 += slots) {
+    const int h = h0 + threadIdx.x / kLanes;
+    if (h0 > 0) load(h);
+    if (h0 > 0 || TB > 1) load_weight(h);
+    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+    const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
+    const bool norm = weight(h) != nullptr;
+#pragma unroll
+    for (int k = 0; k < TB; ++k) {
+      if (!s_live[k]) continue;             // block-uniform
+      const long long at = s_cache[k];
       float x[8], y[8];
-      unpack8(w0, x);
-      unpack8(w1, y);
-      if (p.q_norm != nullptr || p.k_norm != nullptr) {     // uniform: the shuffles need every lane
+      unpack8(w0[k], x);
+      unpack8(w1[k], y);
+      if (any_norm) {                       // uniform: the shuffles need every lane
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (norm != nullptr) {
+        if (norm) {
           const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
           float u0[8], u1[8];
-          unpack8(reinterpret_cast<const uint4*>(norm)[c0], u0);
-          unpack8(reinterpret_cast<const uint4*>(norm)[c1], u1);
+          unpack8(n0, u0);
+          unpack8(n1, u1);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             x[e] *= inv * u0[e];
@@ -205,34 +235,33 @@ __global__ void __launch_bounds__(kRotThreads) rotate_append_kernel(const Rotate
           }
         }
       }
-      if (!act) continue;
-      if (!is_v && (turns || norm != nullptr)) {
-        if (turns) {
+      if (h >= heads || !(is_q || at >= 0)) continue;
+      if (!is_v && turns) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // half: the eight pairs of chunk t; interleaved: four pairs of each chunk
+          const int f = !INTER ? 8 * t + e : (e < 4 ? 4 * c0 + e : 4 * c1 + e - 4);
+          const float2 cs = s_cs[k][f];
           if (!INTER) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = x[e], b = y[e];
-              x[e] = a * cs[e] - b * sn[e];
-              y[e] = b * cs[e] + a * sn[e];
-            }
+            const float a = x[e], b = y[e];
+            x[e] = a * cs.x - b * cs.y;
+            y[e] = b * cs.x + a * cs.y;
           } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = a * cs[e] - b * sn[e];
-              x[2 * e + 1] = b * cs[e] + a * sn[e];
-              a = y[2 * e];
-              b = y[2 * e + 1];
-              y[2 * e] = a * cs[4 + e] - b * sn[4 + e];
-              y[2 * e + 1] = b * cs[4 + e] + a * sn[4 + e];
-            }
+            float* z = e < 4 ? x + 2 * e : y + 2 * (e - 4);
+            const float a = z[0], b = z[1];
+            z[0] = a * cs.x - b * cs.y;
+            z[1] = b * cs.x + a * cs.y;
           }
         }
-        w0 = pack8(x);
-        w1 = pack8(y);
       }
-      dst[c0] = w0;
-      dst[c1] = w1;
+      if (!is_v && (turns || norm)) {
+        w0[k] = pack8(x);
+        w1[k] = pack8(y);
+      }
+      uint16_t* d = is_q ? p.q_out + ((row0 + k) * p.Hq + hh) * D
+                         : (is_v ? p.v_cache : p.k_cache) + (at * p.Hkv + hh) * D;
+      reinterpret_cast<uint4*>(d)[c0] = w0[k];
+      reinterpret_cast<uint4*>(d)[c1] = w1[k];
     }
   }
   grid_dependents_launch();
@@ -241,12 +270,14 @@ __global__ void __launch_bounds__(kRotThreads) rotate_append_kernel(const Rotate
 template <int D>
 cudaError_t launch_rotate(const RotateParams& p, bool inter, int tb, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.rows + tb - 1) / tb));
-  const dim3 block(kRotThreads);
+  const int need = (p.Hq + 2 * p.Hkv) * (D / 16);
+  const int rounds = (need + kMaxThreads - 1) / kMaxThreads;
+  const dim3 block(static_cast<unsigned>(((need + rounds - 1) / rounds + 31) / 32 * 32));
   if (tb == 1)
     return inter ? launch_pdl(rotate_append_kernel<D, true, 1>, grid, block, 0, s, p)
                  : launch_pdl(rotate_append_kernel<D, false, 1>, grid, block, 0, s, p);
-  return inter ? launch_pdl(rotate_append_kernel<D, true, 4>, grid, block, 0, s, p)
-               : launch_pdl(rotate_append_kernel<D, false, 4>, grid, block, 0, s, p);
+  return inter ? launch_pdl(rotate_append_kernel<D, true, kTokens>, grid, block, 0, s, p)
+               : launch_pdl(rotate_append_kernel<D, false, kTokens>, grid, block, 0, s, p);
 }
 
 jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool packed, long long T,
@@ -295,7 +326,7 @@ jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool pac
   }
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  const int tb = p.rows <= 4ll * sms ? 1 : 4;
+  const int tb = p.rows <= kFewRows * sms ? 1 : kTokens;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? launch_rotate<128>(p, inter, tb, s) : launch_rotate<64>(p, inter, tb, s);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;

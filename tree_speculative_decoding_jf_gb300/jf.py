@@ -831,37 +831,46 @@ def _token_rows(name, t, lead) -> int:
     return strides[1]
 
 
+def _heads(name, t, lead, H, D, cur) -> int:
+    """Checks one of q, k and v, quickly where all is well; the elements between its tokens."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == cur and t.shape == lead + (H, D):
+        s = t.stride()
+        if s[-1] == 1 and s[-2] == D:
+            if len(s) == 3:
+                if lead[0] > 1:
+                    return s[0]
+            elif lead[1] > 1 and (lead[0] == 1 or s[0] == lead[1] * s[1]):
+                return s[1]
+        return _token_rows(name, t, lead)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != lead + (H, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + (H, D)}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
 def _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, lead, q_out, pos, freq, interleaved,
                  rotary_scale, q_norm, k_norm, norm_eps, tree_len, cu_seqlens, N_max, dev_err, stream):
     num_pages, page, Hkv, D = k_cache.shape
     B, max_pages = block_table.shape
     cur = torch.cuda.current_device()
-    strides = []
-    for name, t, H in (("q", q, None if q is None else q.shape[-2]), ("k", k, Hkv), ("v", v, Hkv)):
-        if t is None:
-            strides.append(0)
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if tuple(t.shape) != tuple(lead) + (H, D):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(lead) + (H, D)}")
-        if t.get_device() != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
-        strides.append(_token_rows(name, t, lead))
+    k_stride = _heads("k", k, lead, Hkv, D, cur)
+    v_stride = _heads("v", v, lead, Hkv, D, cur)
+    q_stride = 0 if q is None else _heads("q", q, lead, q.shape[-2], D, cur)
     Hq = 0 if q is None else q.shape[-2]
     R = 0 if freq is None else 2 * freq.numel()
     specs = (("k_cache", k_cache, torch.bfloat16, None), ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
              ("block_table", block_table, torch.int32, None), ("prefix_len", prefix_len, torch.int32, (B,)),
              ("pos", pos, torch.int32, lead), ("freq", freq, torch.float64, (R // 2,)),
              ("q_norm", q_norm, torch.bfloat16, (D,)), ("k_norm", k_norm, torch.bfloat16, (D,)),
-             ("q_out", q_out, torch.bfloat16, tuple(lead) + (Hq, D)),
+             ("q_out", q_out, torch.bfloat16, lead + (Hq, D)),
              ("tree_len", tree_len, torch.int32, (B,)), ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
     on = _on_stream(specs, dev_err, stream)
-    first = (_at(q), strides[0], _at(k), strides[1], _at(v), strides[2], _at(pos), _at(freq), R,
-             1 if interleaved else 0, float(rotary_scale), _at(q_norm), _at(k_norm), float(norm_eps),
-             _at(block_table), _at(prefix_len))
+    first = (_at(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _at(pos), _at(freq), R,
+             1 if interleaved else 0, rotary_scale, _at(q_norm), _at(k_norm), norm_eps,
+             block_table.data_ptr(), prefix_len.data_ptr())
     last = (Hq, Hkv, D, page, max_pages, num_pages, _at(q_out), _at(k_cache), _at(v_cache), _at(dev_err), on)
     if cu_seqlens is None:
         _check("jf_rotate_append_kv", _lib.jf_rotate_append_kv(*first, _at(tree_len), B, lead[1], *last))
