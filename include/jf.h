@@ -61,6 +61,7 @@ typedef enum { JF_DTYPE_BF16 = 0, JF_DTYPE_F32 = 1 } jf_dtype;
 #define JF_DEVERR_TIMEOUT 0x10   /* an in-kernel wait gave up after its time limit      */
 #define JF_DEVERR_BAD_PATH 0x20  /* accepted path, kept positions, beam parent, grammar or count row malformed */
 #define JF_DEVERR_BAD_TREE_LEN 0x40 /* tree_len[b] outside [1, N], or a bad packed span   */
+#define JF_DEVERR_BAD_GROUP 0x80 /* group_start is no partition, or shared_pages out of range */
 
 /* Largest tree (nodes per sequence) any call accepts. */
 #define JF_MAX_NODES 4096
@@ -725,6 +726,56 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
                                      int32_t page_size, int32_t max_pages, int32_t num_pages,
                                      void* q_out, void* k_cache, void* v_cache, int32_t* dev_err,
                                      jf_stream_t stream);
+
+/*
+ * jf_tree_attention_shared -- jf_tree_attention for sequences that share a long prefix, whose keys
+ * and values are then read once for all of them: the beams of a prompt, which share full pages
+ * after jf_beam_fork_kv, requests behind one system prompt, samples of one prompt.
+ *   group_start  int32 [n_groups + 1], 0 = group_start[0] <= .. <= group_start[n_groups] = B: group
+ *                u holds the sequences group_start[u] .. group_start[u + 1] - 1.
+ *   shared_pages int32 [n_groups]: the first S = page_size * shared_pages[u] keys of group u's
+ *                sequences are the same.  They are read through the block-table row of its first
+ *                sequence; the entries below shared_pages[u] of the other rows are not read.  At
+ *                most floor(P_b / page_size) of each of its sequences; 0: nothing is shared.
+ *   q, k_cache, v_cache, block_table, prefix_len, mask, scale, out, lse
+ *                as in jf_tree_attention, whose results these are (merged in another order).
+ *                out must not overlap q or the caches.
+ *   tree_len     int32 [B] or NULL: ragged trees as in jf_tree_attention_ragged, but rows
+ *                i >= tree_len[b] of out and lse are left as they were.
+ *   workspace    at least jf_tree_attention_shared_workspace_size(...) bytes, 16-byte aligned, no
+ *                initialisation.  Calls that overlap need one each.
+ *   dev_err      JF_DEVERR_BAD_GROUP (group_start is not such a partition: no row is computed, out and
+ *                lse are unspecified; or shared_pages[u] < 0 or past the block table, then clamped),
+ *                _BAD_PREFIX (P_b < S or P_b + n_b past the block table), _BAD_PAGE,
+ *                _BAD_TREE_LEN, _TIMEOUT.  May be NULL.
+ * The order of every sum is fixed by the call's sizes and data: the same call gives the same bits.
+ * Limits: as jf_tree_attention, and B <= 4096, 1 <= n_groups <= B.
+ * jf_tree_attention_shared_packed takes the packed layout (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
+ * q and out [T][Hq][D], mask [T][W], lse [Hq][T]); a bad span may spoil the rows of its group.
+ * The workspace size takes T = 0 for the padded call, the number of packed rows otherwise.
+ */
+size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, int32_t T, int32_t n_groups,
+                                               int32_t Hq, int32_t Hkv, int32_t D,
+                                               int32_t max_pages, int32_t page_size);
+jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* prefix_len,
+                                   const int32_t* tree_len, const uint64_t* mask,
+                                   const int32_t* group_start, const int32_t* shared_pages,
+                                   int32_t n_groups, int32_t B, int32_t N, int32_t Hq,
+                                   int32_t Hkv, int32_t D, int32_t page_size, int32_t max_pages,
+                                   int32_t num_pages, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                   jf_stream_t stream);
+jf_status jf_tree_attention_shared_packed(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_table, const int32_t* prefix_len,
+                                          const int32_t* cu_seqlens, const uint64_t* mask,
+                                          const int32_t* group_start, const int32_t* shared_pages,
+                                          int32_t n_groups, int32_t B, int32_t N_max, int32_t T,
+                                          int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                                          int32_t max_pages, int32_t num_pages, float scale,
+                                          void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, int32_t* dev_err,
+                                          jf_stream_t stream);
 
 /*
  * jf_adjust_logits -- penalties for repeated tokens, biases and grammar masks on the logits of

@@ -102,6 +102,27 @@ def test_count_refusals(lib):
                        (11, ctypes.c_void_p((6 << 32) + 2), 7)])
 
 
+def test_shared_refusals(lib):
+    fn = lib.jf_tree_attention_shared
+    fn.argtypes = [P] * 9 + [i32] * 9 + [f32, P, P, P, sz, P, P]
+    #       q      k      v      bt     pfx    tl    mask   gs     sp     ng B  N   Hq  Hkv D   pg  mp  np  scale
+    args = [at(1), at(2), at(3), at(4), at(5), None, at(6), at(7), at(8), 2, 4, 16, 32, 8, 128, 16, 10, 99, 0.1,
+            # out   lse   ws      bytes    err  stream
+            at(9), None, at(10), 1 << 40, None, None]
+    refused(fn, args, [(0, None, 1), (1, None, 1), (2, None, 1), (3, None, 1), (4, None, 1), (6, None, 1), (7, None, 1),
+                       (8, None, 1), (19, None, 1), (9, 0, 1), (9, 5, 1), (10, 0, 1), (11, 0, 1), (12, 0, 1), (13, 0, 1),
+                       (16, 0, 1), (17, 0, 1), (18, 0.0, 1), (18, float("nan"), 1), (18, float("inf"), 1),
+                       (17, 1 << 27, 3), ((10, 9), (4097, 1), 3), (11, 4097, 3), (12, 33, 3), (13, 5, 3), (14, 96, 3),
+                       (15, 32, 3), ((11, 16), (17, 1), 3), ((12, 13), (256, 1), 3),
+                       (0, ctypes.c_void_p((1 << 32) + 8), 7), (1, ctypes.c_void_p((2 << 32) + 8), 7),
+                       (19, ctypes.c_void_p((9 << 32) + 8), 7), (6, ctypes.c_void_p((6 << 32) + 4), 7),
+                       (19, at(1), 1), (19, at(2), 1), (19, ctypes.c_void_p((3 << 32) + 16), 1)])
+    fn = lib.jf_tree_attention_shared_packed
+    fn.argtypes = [P] * 9 + [i32] * 10 + [f32, P, P, P, sz, P, P]
+    args = args[:5] + [at(11)] + args[6:12] + [40] + args[12:]
+    refused(fn, args, [(5, None, 1), (12, 0, 1), (12, 0x7FFFFFF8, 3)])
+
+
 @pytest.fixture(scope="module")
 def jf():
     from tree_speculative_decoding_jf_gb300 import build

@@ -1,0 +1,1017 @@
+// jf_shared.cu -- tree-causal paged attention for sequences that share a long prefix.
+//
+// The sequences of a group have their first S keys in common (the same pages: a prompt's beams
+// after a fork, requests behind one system prompt).  A softmax over a set of keys is the merge
+// of softmaxes over its parts: with (O_x, l_x) the output and log-sum-exp over part x,
+//     l = log sum_x exp(l_x),   O = sum_x exp(l_x - l) O_x.
+// So each group's shared keys are attended to once by the rows of all its sequences together
+// (they lie one after the other in q, so they are one long list of nodes), and each sequence's
+// own keys (from S on, its tree included) by its own rows; the parts merge at the end.  Shared
+// K/V are read once per row tile group of the group instead of once per sequence, and rows fill
+// the 128-row tensor-core tile that a single sequence's G rows leave nearly empty.
+//
+// Work.  A unit is a group's shared part or a sequence's own part; an item is a unit, a
+// kv-head and a row-tile group (NT tiles of 128 rows).  Items lie end to end, T key tiles plus
+// kSwitch for the change of item, and are cut into one equal range per SM: lengths and group
+// sizes are data, so every CTA forms the same schedule from them.  A range's pieces of items are
+// walked with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer,
+// MMA issuer, vouchers, softmax warpgroups, all counters running over the range's tiles as one
+// sequence).  Every piece leaves normalised fp32 rows and their log-sum-exp: whole items in the
+// rows' own slots (shared and own part apart), items that a range boundary cuts in the range's
+// slots 0 (cut at its start) and 1; the first piece of an item tells each of its rows where its
+// pieces are.  The merge kernel, one warp a row, reads that and adds up.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "jf_attention.cuh"
+#include "jf_common.cuh"
+#include "jf_sm100.cuh"
+#include "jf_tensormap.cuh"
+
+namespace jf {
+namespace {
+
+constexpr int kSwitch = 1;          // cost of a change of item, in key tiles
+constexpr int kSharedMaxB = 4096;   // the schedule is formed in shared memory
+
+struct SharedParams {
+  const int32_t *block_table, *prefix_len, *tree_len, *cu, *group_start, *shared_pages;
+  const uint64_t* mask;
+  uint16_t* out;
+  float* lse;
+  float* ws_o;       // [2 * rows + 2 * ranges * R][D]: shared parts, own parts, cut pieces
+  float* ws_lse;     // the same rows' log-sum-exp (log2 domain)
+  int4* ws_desc;     // [2][rows]: first piece's row, pieces, second piece's row
+  int32_t* dev_err;
+  long long T;       // packed nodes
+  int B, N, Hq, Hkv, G, W, max_pages, num_pages, n_groups, ranges;
+  int rows;          // (node, query head) rows
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------------ the schedule
+
+// Keys that group u's sequences share: none when it has one sequence (nothing to share).
+__device__ __forceinline__ int group_keys(const SharedParams& p, int u, int b0, int b1) {
+  if (b1 - b0 < 2) return 0;
+  return max(0, min(p.shared_pages[u], (p.max_pages * kPage - p.N) / kPage)) * kPage;
+}
+
+// One unit: rows f0 .. f0 + nr - 1 of q's nodes attend to keys key0 .. L - 1 of block-table row
+// bt, T tiles; mpc row-tile groups.  Keys below P are visible to every row.
+struct Unit {
+  int f0, nr, key0, P, L, T, mpc, bt;
+};
+
+template <int NT>
+__device__ __forceinline__ Unit make_unit(const SharedParams& p, int b, int b0, int b1, int S) {
+  Unit t;
+  const int cap = p.max_pages * kPage;
+  if (b < 0) {                       // the group's shared keys
+    t.bt = b0;
+    t.key0 = 0;
+    t.P = t.L = S;
+    if (p.cu == nullptr) {
+      t.f0 = b0 * p.N;
+      t.nr = (b1 - b0) * p.N;
+    } else {
+      const long long r0 = p.cu[b0], r1 = p.cu[b1];
+      const bool ok = r0 >= 0 && r1 <= p.T && r1 >= r0;
+      t.f0 = ok ? static_cast<int>(r0) : 0;
+      t.nr = ok ? static_cast<int>(r1 - r0) : 0;
+    }
+  } else {
+    const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+    t.bt = b;
+    t.key0 = S;
+    t.P = max(S, min(p.prefix_len[b], cap - sp.n));
+    t.L = t.P + sp.n;
+    t.f0 = static_cast<int>(sp.row0);
+    t.nr = sp.n;
+  }
+  t.mpc = static_cast<int>((static_cast<long long>(t.nr) * p.G + NT * kRowTile - 1) / (NT * kRowTile));
+  t.T = t.nr > 0 ? (t.L - t.key0 + kKeyTile - 1) / kKeyTile : 0;
+  return t;
+}
+
+struct Schedule {
+  int lo, hi;        // this range, in positions
+  int q, rem;        // range v starts at v * q + min(v, rem)
+  int tiles;         // key tiles in the range
+  int u, b, off;     // the unit at lo (b < 0: shared) and lo's offset in it
+  __device__ int range_of(int x) const {
+    const int big = rem * (q + 1);
+    return x < big ? x / (q + 1) : rem + (x - big) / q;
+  }
+};
+
+// Every thread of the block calls it; scratch: 4 * (3 * n_groups + 2 * B + 1) bytes at least.  Unit
+// order: group by group, its shared part (if any), then its sequences.
+template <int NT>
+__device__ __noinline__ void make_schedule(const SharedParams& p, int v, int32_t* err, int* scratch, Schedule* out) {
+  const int ng = p.n_groups, B = p.B, U = ng + B, tid = threadIdx.x, nth = blockDim.x;
+  int* gs = scratch;                 // [ng + 1]
+  int* cost = gs + ng + 1;           // [U] positions of the unit
+  int* items = cost + U;             // [U]
+  __shared__ long long s_scan[32];
+  __shared__ int s_items[32];
+  for (int u = tid; u <= ng; u += nth) gs[u] = p.group_start[u];
+  if (tid == 0) out->tiles = 0, out->lo = out->hi = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int u = tid; u < ng; u += nth) bad = bad || gs[u] > gs[u + 1];
+  if (tid == 0) bad = bad || gs[0] != 0 || gs[ng] != B;
+  if (__syncthreads_or(bad)) {       // no work at all: group_start is not a partition
+    if (tid == 0 && err != nullptr) report(err, JF_DEVERR_BAD_GROUP);
+    return;
+  }
+  const int cap = p.max_pages * kPage;
+  for (int e = tid; e < U; e += nth) {
+    // unit e: u + gs[u] is group u's shared unit
+    int u = 0, hi = ng;
+    while (hi - u > 1) {
+      const int mid = (u + hi) >> 1;
+      if (mid + gs[mid] <= e) u = mid; else hi = mid;
+    }
+    const int b = e - u - 1 - 0;     // u + gs[u] + 1 + (b - gs[u]) = e
+    const int b0 = gs[u], b1 = gs[u + 1];
+    const int S = group_keys(p, u, b0, b1);
+    const bool shared = e == u + b0;
+    if (err != nullptr) {
+      if (shared && (p.shared_pages[u] < 0 || (S != p.shared_pages[u] * static_cast<long long>(kPage) && b1 - b0 >= 2)))
+        report(err, JF_DEVERR_BAD_GROUP);
+      if (!shared) {
+        const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+        if (!sp.ok) report(err, JF_DEVERR_BAD_TREE_LEN);
+        const int P = p.prefix_len[b];
+        if (P < S || P > cap - sp.n) report(err, JF_DEVERR_BAD_PREFIX);
+      }
+    }
+    int n = 0, c = 0;
+    if (!shared || S > 0) {
+      const Unit t = make_unit<NT>(p, shared ? -1 : b, b0, b1, S);
+      n = p.Hkv * t.mpc;
+      c = n * (t.T + kSwitch);
+      if (t.T == 0) n = c = 0;
+    }
+    cost[e] = c;
+    items[e] = n;
+  }
+  __syncthreads();
+  // Block-wide sums over contiguous chunks of units.
+  const int chunk = (U + nth - 1) / nth;
+  const int e0 = min(U, tid * chunk), e1 = min(U, e0 + chunk);
+  long long mine = 0;
+  int mine_items = 0;
+  for (int e = e0; e < e1; ++e) mine += cost[e], mine_items += items[e];
+  long long upto = mine;
+  int upto_items = mine_items;
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    const int z = __shfl_up_sync(0xffffffffu, upto_items, o);
+    if (lane >= o) upto += y, upto_items += z;
+  }
+  if (lane == 31) s_scan[warp] = upto, s_items[warp] = upto_items;
+  __syncthreads();
+  long long total = 0;
+  int total_items = 0;
+  for (int w = 0; w < (nth + 31) / 32; ++w) {
+    if (w < warp) upto += s_scan[w], upto_items += s_items[w];
+    total += s_scan[w];
+    total_items += s_items[w];
+  }
+  const int q = static_cast<int>(total / p.ranges), rem = static_cast<int>(total - static_cast<long long>(q) * p.ranges);
+  const long long lo = static_cast<long long>(v) * q + min(v, rem), hi = lo + q + (v < rem ? 1 : 0);
+  // tiles before a position: the position less kSwitch per item completed before it
+  __shared__ int s_before[2];
+  if (tid == 0) {
+    s_before[0] = 0;
+    s_before[1] = static_cast<int>(total) - kSwitch * total_items;     // hi == total
+  }
+  __syncthreads();
+  const long long first = upto - mine;
+  const int first_items = upto_items - mine_items;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const long long x = k == 0 ? lo : hi;
+    if (x < first || x >= upto) continue;        // the position lies in another thread's chunk
+    long long at = first;
+    int done = first_items, e = e0;
+    while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
+    const int off = static_cast<int>(x - at);
+    const int per = cost[e] / items[e];          // T + kSwitch
+    const int item = off / per, in = off - item * per;
+    s_before[k] = static_cast<int>(x) - kSwitch * (done + item) - max(0, in - (per - kSwitch));
+    if (k == 0) {
+      int u = 0, h = ng;
+      while (h - u > 1) {
+        const int mid = (u + h) >> 1;
+        if (mid + gs[mid] <= e) u = mid; else h = mid;
+      }
+      out->u = u;
+      out->b = e == u + gs[u] ? -1 : e - u - 1;
+      out->off = off;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    out->lo = static_cast<int>(lo);
+    out->hi = static_cast<int>(hi);
+    out->q = q;
+    out->rem = rem;
+    out->tiles = lo < hi ? s_before[1] - s_before[0] : 0;
+  }
+}
+
+// One piece as the CTA's roles need it.  The producer, which runs ahead of the others, walks the
+// range and posts its pieces in a ring in shared memory; s_posted counts them.
+struct Piece {
+  int T;                   // key tiles
+  int first, P, L;         // the first key; keys below P are seen by every row, keys from L on by none
+  int node0, nrows;        // first node, and rows from it on (the item's row tiles hold fewer or as many)
+  int g, b;                // kv-head; sequence, -1 for a shared part
+  int slots;               // workspace row of a cut item's row 0
+  bool whole, direct, opens, alone;   // uncut; nothing to merge with; the item's first piece; no shared part
+  int n, second;           // a cut item's pieces, and workspace row of row 0 of the second
+};
+// A piece's slot is written once the S MMAs of the last tile of the piece before it are done: every
+// role has then left the pieces up to the third before it.
+constexpr int kPieces = 4;
+
+// The pieces of a range, one after the other.
+template <int NT>
+struct Walk {
+  const SharedParams& p;
+  int lo, hi;
+  int u, b, b0, b1, S;     // group, sequence (-1: shared part), the group's sequences, shared keys
+  int g, mp, x;            // kv-head, row-tile group, the item's position
+  int k0, k1;              // the piece: key tiles k0 .. k1 - 1 of the item
+  Unit t;
+
+  __device__ __forceinline__ Walk(const SharedParams& p_, const Schedule& s) : p(p_), lo(s.lo), hi(s.hi) {
+    u = s.u;
+    b = s.b;
+    b0 = p.group_start[u];
+    b1 = p.group_start[u + 1];
+    S = group_keys(p, u, b0, b1);
+    t = make_unit<NT>(p, b, b0, b1, S);
+    const int per = t.T + kSwitch, item = s.off / per;
+    g = item / t.mpc;
+    mp = item - g * t.mpc;
+    x = lo - (s.off - item * per);
+    settle();
+  }
+  __device__ __forceinline__ bool live() const { return x < hi; }
+  __device__ __forceinline__ void next() {
+    advance();
+    settle();
+  }
+  __device__ __forceinline__ Piece piece(const Schedule& s, int v) const {
+    constexpr int R = NT * kRowTile;
+    Piece c;
+    c.T = k1 - k0;
+    c.first = t.key0 + k0 * kKeyTile;
+    c.P = t.P;
+    c.L = t.L;
+    c.node0 = t.f0 + mp * R / p.G;
+    c.nrows = t.nr * p.G - mp * R;
+    c.g = g;
+    c.b = b;
+    c.whole = k0 == 0 && k1 == t.T;
+    c.alone = b >= 0 && S == 0;
+    c.direct = c.whole && c.alone;
+    c.opens = k0 == 0;
+    const int slot = x + k0 == lo ? 0 : 1;
+    c.slots = 2 * p.rows + (2 * v + slot) * R;
+    c.n = c.direct ? 0 : 1;
+    c.second = 0;
+    if (!c.whole && c.opens) {
+      const int va = s.range_of(x), vb = s.range_of(x + t.T - 1);
+      c.n = vb - va + 1;
+      c.second = 2 * p.rows + 2 * (va + 1) * R;
+    }
+    return c;
+  }
+
+ private:
+  // The first piece at or after the current item (a range may start or end in an item's switch).
+  __device__ __forceinline__ void settle() {
+    while (x < hi) {
+      k0 = max(lo - x, 0);
+      k1 = min(hi - x, t.T);
+      if (k0 < k1) return;
+      advance();
+    }
+  }
+  __device__ __noinline__ void next_unit() {
+    for (;;) {
+      b = b < 0 ? b0 : b + 1;
+      while (b >= b1) {
+        if (++u >= p.n_groups) {
+          x = INT_MAX;
+          return;
+        }
+        b0 = b1;
+        b1 = p.group_start[u + 1];
+        S = group_keys(p, u, b0, b1);
+        b = S > 0 ? -1 : b0;
+      }
+      t = make_unit<NT>(p, b, b0, b1, S);
+      if (t.T > 0) return;
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    x += t.T + kSwitch;
+    if (++mp < t.mpc) return;
+    mp = 0;
+    if (++g < p.Hkv) return;
+    g = 0;
+    if (x < hi) next_unit();
+  }
+};
+
+__device__ __forceinline__ void shared_count_add(int* c) {
+  asm volatile("red.release.cta.shared::cta.add.s32 [%0], 1;" ::"r"(smem_u32(c)) : "memory");
+}
+__device__ __forceinline__ int shared_count(int* c) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(c)) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool wait_shared_count(int* c, int target, volatile int* abort) {
+  if (shared_count(c) > target) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (shared_count(c) > target) return true;
+    if ((it & 255u) == 0u && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+
+// ------------------------------------------------------------------------ the parts
+
+template <int NT, int D>
+__global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
+    shared_attention_kernel(const __grid_constant__ CUtensorMap qmap,
+                            const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap,
+                            const __grid_constant__ CUtensorMap kmap_run,
+                            const __grid_constant__ CUtensorMap vmap_run,
+                            const __grid_constant__ SharedParams p) {
+  using C = Cfg<NT, D>;
+  constexpr int SK = C::kKStages;
+  constexpr int SV = C::kVStages;
+  constexpr uint64_t wlim = kWaitLimitNs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t q_full, o_full, fin;
+  __shared__ uint64_t k_full[SK], v_full[SV], step_done[kStepRing];
+  __shared__ uint64_t s_full[NT], p_full[NT];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ Piece s_piece[kPieces];
+  __shared__ int s_posted;                   // pieces posted
+  __shared__ int s_tails;                    // pieces whose V tail is ready
+  __shared__ int s_lo[NT];                   // current key tile of row tile t stores P in two parts
+  __shared__ Schedule s_sch;
+  volatile int* abort = &abort_flag;
+  uint8_t* q_s = sm + C::kQOff;
+  uint8_t* k_s = sm + C::kKOff;
+  uint8_t* v_s = sm + C::kVOff;
+  const int v = blockIdx.x;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&o_full, 1);
+    mbar_init(&fin, 1);
+    for (int st = 0; st < SK; ++st) mbar_init(&k_full[st], 1);
+    for (int st = 0; st < SV; ++st) mbar_init(&v_full[st], 1);
+    for (int st = 0; st < kStepRing; ++st) mbar_init(&step_done[st], 1);
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128 + 1);   // the softmax warpgroup + its data voucher
+    }
+    s_posted = 0;
+    s_tails = 0;
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&kmap_run);
+    tma_prefetch_desc(&vmap_run);
+  }
+  grid_dependency_wait();
+  make_schedule<NT>(p, v, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
+  fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int Wc = s_sch.tiles;
+  if (Wc <= 0) {                        // fewer tiles than ranges (or nothing to do)
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+    return;
+  }
+
+  if (warp < 4) {
+  if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  if (warp == 0) {
+    // ================================================================ TMA producer
+    constexpr int kLookahead = 4;
+    int k_issued = 0, v_issued = 0, q_issued = 0, bad = 0;
+    bool ok = true;
+    auto issue = [&](uint8_t* ring, const CUtensorMap* map, const CUtensorMap* map_run,
+                     uint64_t* full, int st, int page, int page0, int g, bool run) {
+      if (run) {
+        if (lane < C::kHalves)
+          tma_load_3d(ring + st * C::kTileBytes + lane * C::kHalfBytes, map_run, full, lane * 64, g,
+                      page0 * kPage);
+      } else if (lane < kPagesPerTile * C::kHalves) {
+        const int q = lane % kPagesPerTile, hh = lane / kPagesPerTile;
+        tma_load_3d(ring + st * C::kTileBytes + hh * C::kHalfBytes + q * (kPage * 128), map, full,
+                    hh * 64, g, page * kPage);
+      }
+    };
+    int jg0 = 0;
+    Walk<NT> w(p, s_sch);
+    for (int s = 0; w.live() && ok; ++s, w.next()) {
+      const int T = w.k1 - w.k0, L = w.t.L;
+      const int page0_of = w.t.key0 / kPage + w.k0 * kPagesPerTile;     // the piece's first page
+      const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages;
+      // this piece's Q, once the previous piece's S MMAs no longer read the buffer
+      int okq = 1;
+      if (lane == 0) {
+        const int rq = jg0 - 1;   // S of the previous piece's last tile: step record rq
+        if (s > 0 && !mbar_wait(&step_done[rq % kStepRing], static_cast<uint32_t>(rq / kStepRing) & 1u,
+                                abort, wlim)) {
+          okq = 0;
+        } else {
+          s_piece[s % kPieces] = w.piece(s_sch, v);
+          shared_count_add(&s_posted);
+          mbar_arrive_expect_tx(&q_full, NT * C::kTileBytes);
+          for (int t = 0; t < NT; ++t) {
+            const int node0 = w.t.f0 + ((w.mp * NT + t) * kRowTile) / p.G;
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              tma_load_3d(q_s + t * C::kTileBytes + hh * C::kHalfBytes, &qmap, &q_full, hh * 64,
+                          w.g * p.G, node0);
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, okq, 0)) { ok = false; break; }
+      q_issued = s + 1;
+      auto load_pid = [&](int j) -> int {
+        const int pl = page0_of + j * kPagesPerTile + lane;
+        if (lane >= kPagesPerTile || j >= T || pl * kPage >= L) return p.num_pages;
+        return __ldg(bt + pl);
+      };
+      int pid[kLookahead];
+#pragma unroll
+      for (int u = 0; u < kLookahead; ++u) pid[u] = load_pid(u);
+      for (int j = 0; j < T; ++j) {
+        const int jg = jg0 + j;
+        int mine = pid[0];
+        if (mine < 0 || mine > p.num_pages) { bad = 1; mine = p.num_pages; }
+        else if (mine == p.num_pages && lane < kPagesPerTile &&
+                 (page0_of + j * kPagesPerTile + lane) * kPage < L) bad = 1;
+        const int page = __shfl_sync(0xffffffffu, mine, lane % kPagesPerTile);
+        const int page0 = __shfl_sync(0xffffffffu, mine, 0);
+        const bool run = __all_sync(0xffffffffu, page == page0 + lane % kPagesPerTile);
+#pragma unroll
+        for (int u = 0; u < kLookahead - 1; ++u) pid[u] = pid[u + 1];
+        pid[kLookahead - 1] = load_pid(j + kLookahead);
+        const int sk = jg % SK, sv = jg % SV;
+        const int rec = jg - C::kStageLag;
+        int okl = 1;
+        if (lane == 0) {
+          if (rec >= 0 && !mbar_wait(&step_done[rec % kStepRing],
+                                     static_cast<uint32_t>(rec / kStepRing) & 1u, abort, wlim)) {
+            okl = 0;
+          } else {
+            mbar_arrive_expect_tx(&k_full[sk], C::kTileBytes);
+            mbar_arrive_expect_tx(&v_full[sv], C::kTileBytes);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, okl, 0)) { ok = false; break; }
+        issue(k_s, &kmap, &kmap_run, &k_full[sk], sk, page, page0, w.g, run);
+        k_issued = jg + 1;
+        issue(v_s, &vmap, &vmap_run, &v_full[sv], sv, page, page0, w.g, run);
+        v_issued = jg + 1;
+      }
+      if (!ok) break;
+      // V rows past the part's end in its last tile meet a zero probability: make them zero,
+      // then release the tile to the MMA issuer's voucher (every piece).
+      const int jl = jg0 + T - 1;
+      const int last_key0 = w.t.key0 + (w.k1 - 1) * kKeyTile;
+      if (last_key0 + kKeyTile > L) {
+        if (!wait_warp(&v_full[jl % SV], static_cast<uint32_t>(jl / SV) & 1u, abort, wlim)) { ok = false; break; }
+        const int r0 = L - last_key0;
+        uint8_t* vt = v_s + (jl % SV) * C::kTileBytes;
+        const int per_half = (kKeyTile - r0) * 8;
+        for (int c = lane; c < per_half * C::kHalves; c += 32) {
+          const int hh = c / per_half, rem = c % per_half;
+          *reinterpret_cast<uint4*>(vt + hh * C::kHalfBytes + (r0 + rem / 8) * 128 + (rem % 8) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) shared_count_add(&s_tails);
+      jg0 += T;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_err, JF_DEVERR_BAD_PAGE);
+    if (!ok && lane == 0) set_abort(abort, p.dev_err);
+    __syncwarp();
+    if (lane == 0) {                   // no copy may still be landing when the CTA exits
+      int zero = 0;
+      if (q_issued > 0) mbar_wait(&q_full, static_cast<uint32_t>(q_issued - 1) & 1u, &zero);
+      for (int j = max(0, k_issued - SK); j < k_issued; ++j)
+        mbar_wait(&k_full[j % SK], static_cast<uint32_t>(j / SK) & 1u, &zero);
+      for (int j = max(0, v_issued - SV); j < v_issued; ++j)
+        mbar_wait(&v_full[j % SV], static_cast<uint32_t>(j / SV) & 1u, &zero);
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    constexpr uint32_t idS = idesc_bf16(kRowTile, kKeyTile, false, false);
+    constexpr uint32_t idO = idesc_bf16(kRowTile, D, false, true);
+    const uint64_t dq = desc_sw128(smem_u32(q_s), 16, 1024);
+    const uint64_t dk = desc_sw128(smem_u32(k_s), 16, 1024);
+    const uint64_t dv = desc_sw128(smem_u32(v_s), C::kHalfBytes, 1024);
+    auto issue_s = [&](int t, int st) {
+      const uint64_t da = dq + static_cast<uint64_t>((t * C::kTileBytes) >> 4);
+      const uint64_t db = dk + static_cast<uint64_t>((st * C::kTileBytes) >> 4);
+      const uint32_t d_tmem = tmem + C::kTmemS + t * 128;
+      mma_ss_tile<D / 16>(d_tmem, da, db, idS);
+    };
+    auto issue_pv = [&](int t, int st, bool acc, bool lo) {
+      const uint64_t db = dv + static_cast<uint64_t>((st * C::kTileBytes) >> 4);
+      const uint32_t d_tmem = tmem + C::kTmemO + t * 128;
+      const uint32_t a_tmem = tmem + C::kTmemS + t * 128;
+      mma_ts_tile(d_tmem, a_tmem, db, idO, acc);
+      if (lo) issue_pv_lo(d_tmem, a_tmem, db, idO);
+    };
+    bool ok = wait_warp(&q_full, 0, abort, wlim) && wait_warp(&k_full[0], 0, abort, wlim);
+    if (ok) {
+      // The whole warp runs this loop; the MMA and commit wrappers issue from one elected lane.
+      tc_fence_after();
+      for (int t = 0; t < NT; ++t) {
+        issue_s(t, 0);
+        mma_commit(&s_full[t]);
+      }
+      mma_commit(&step_done[0]);
+      int jn[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) jn[t] = 0;
+      int left = NT * Wc;
+      uint32_t idle = 0;
+      uint64_t idle_since = 0;
+      while (left > 0) {
+        bool progressed = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int j = jn[t];
+          if (j >= Wc) continue;
+          if (__shfl_sync(0xffffffffu, mbar_try_wait(&p_full[t], static_cast<uint32_t>(j) & 1u) ? 1 : 0, 0) == 0)
+            continue;
+          bool last = true;
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+            if (u != t && jn[u] <= j) last = false;
+          tc_fence_after();
+          // s_lo[t] was written before the softmax's arrival on p_full[t]: lane 0 reads it
+          const bool lo = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_lo[t]), 0) != 0;
+          issue_pv(t, j % SV, j > 0, lo);
+          if (j + 1 < Wc) {
+            issue_s(t, (j + 1) % SK);
+            mma_commit(&s_full[t]);
+          }
+          if (last) mma_commit(&step_done[(j + 1) % kStepRing]);
+          jn[t] = j + 1;
+          --left;
+          progressed = true;
+        }
+        if (progressed) {
+          idle = 0;
+        } else {
+          if (idle == 0) idle_since = global_timer_ns();
+          if ((++idle & 255u) == 0u &&
+              __shfl_sync(0xffffffffu, (*abort || global_timer_ns() - idle_since > wlim) ? 1 : 0, 0) != 0) {
+            ok = false;
+            break;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) set_abort(abort, p.dev_err);
+    if (ok) mma_commit(&o_full);   // the range's last PV
+    mma_commit(&fin);   // all MMAs done before TMEM is released
+    {
+      int zero = 0;
+      wait_warp(&fin, 0, &zero, kWaitLimitNs);
+    }
+  } else if (warp >= 2 && warp < 2 + NT) {
+    // ================================================================ data vouchers
+    // The last arrival on p_full[t] for tile j: V tile j and K tile j + 1 have landed and, at a
+    // piece's last tile, its V tail and the next piece's Q.
+    const int t = warp - 2;
+    if (lane == 0) {
+      bool ready = wait_shared_count(&s_posted, 0, abort);
+      int s = 0, e = ready ? s_piece[0].T : 0;
+      for (int j = 0; j < Wc && ready; ++j) {
+        const bool last_of_piece = j + 1 == e;
+        ready = (j == 0 || mbar_wait(&p_full[t], static_cast<uint32_t>(j - 1) & 1u, abort, wlim)) &&
+                mbar_wait(&v_full[j % SV], static_cast<uint32_t>(j / SV) & 1u, abort, wlim) &&
+                (j + 1 >= Wc ||
+                 mbar_wait(&k_full[(j + 1) % SK], static_cast<uint32_t>((j + 1) / SK) & 1u, abort, wlim)) &&
+                (!last_of_piece || wait_shared_count(&s_tails, s, abort)) &&
+                (!last_of_piece || j + 1 >= Wc ||
+                 mbar_wait(&q_full, static_cast<uint32_t>(s + 1) & 1u, abort, wlim));
+        if (!ready) break;
+        mbar_arrive(&p_full[t]);
+        if (last_of_piece && j + 1 < Wc) {
+          ++s;
+          ready = wait_shared_count(&s_posted, s, abort);
+          if (ready) e += *reinterpret_cast<volatile int*>(&s_piece[s % kPieces].T);
+        }
+      }
+      if (!ready) set_abort(abort, p.dev_err);
+    }
+    __syncwarp();
+  }
+  } else {
+    if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ================================================================ softmax / epilogue
+    const int t = (warp >> 2) - 1;
+    const int wq = warp & 3;
+    const int rl = wq * 32 + lane;                       // row within the tile = TMEM lane
+    const int W = p.W;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + C::kTmemS + t * 128 + lane_off;
+    const uint32_t tO = tmem + C::kTmemO + t * 128 + lane_off;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int jg0 = 0;
+    for (int s = 0; jg0 < Wc && ok; ++s) {
+      int posted = 1;
+      if (lane == 0) posted = wait_shared_count(&s_posted, s, abort) ? 1 : 0;
+      posted = __shfl_sync(0xffffffffu, posted, 0);      // and what the lane acquired is the warp's
+      __syncwarp();
+      // (The piece is read where it is needed: registers belong to the scores.)
+      const volatile Piece& c = s_piece[s % kPieces];
+      const int T = posted ? c.T : 0;
+      const int r = t * kRowTile + rl;                   // row of the item
+      float m_run = -INFINITY;
+      float l = 0.f;
+      ok = posted != 0;
+      {
+        const int P = c.P, L = c.L, first = c.first;
+        const bool valid = r < c.nrows, tree = valid && c.b >= 0;
+        const uint64_t* mrow = p.mask + (static_cast<size_t>(c.node0) + (valid ? r / p.G : 0)) * W;
+        // Key tiles before jm hold keys that every row sees and nothing else.
+        const int jm = min(max((P - first) / kKeyTile, 0), T);
+        volatile int* lo_flag = &s_lo[t];
+        for (int j = 0; j < jm && ok; ++j)
+          ok = softmax_tile<false, false, D>(&s_full[t], static_cast<uint32_t>(jg0 + j) & 1u, abort, &p_full[t],
+                                             tS, tO, mrow, tree, W, first + j * kKeyTile, P, L, sl2, j > 0,
+                                             lo_flag, rl == 0, m_run, l, wlim);
+        // Rows with fewer than kSplitPrefix keys that all of them see: P in two bf16 parts.  (A
+        // shared part has no tree keys: its ancestor words are not read.)
+        if (P < kSplitPrefix) {
+          for (int j = jm; j < T && ok; ++j)
+            ok = softmax_tile<true, true, D>(&s_full[t], static_cast<uint32_t>(jg0 + j) & 1u, abort,
+                                             &p_full[t], tS, tO, mrow, tree, W, first + j * kKeyTile,
+                                             P, L, sl2, j > 0, lo_flag, rl == 0, m_run, l, wlim);
+        } else {
+          for (int j = jm; j < T && ok; ++j)
+            ok = softmax_tile<true, false, D>(&s_full[t], static_cast<uint32_t>(jg0 + j) & 1u, abort,
+                                              &p_full[t], tS, tO, mrow, tree, W, first + j * kKeyTile,
+                                              P, L, sl2, j > 0, lo_flag, rl == 0, m_run, l, wlim);
+        }
+      }
+      // A failed wait still reaches the warpgroup vote below (every warp must enter it).
+      if (!ok && lane == 0) set_abort(abort, p.dev_err);
+      // ---- the piece's rows, once its last PV is done: S of the next tile (committed after it)
+      // or, for the range's last piece, o_full.
+      const int je = jg0 + T;
+      const bool pv_done = ok && (je < Wc ? wait_warp(&s_full[t], static_cast<uint32_t>(je) & 1u, abort, wlim)
+                                          : wait_warp(&o_full, 0u, abort, wlim));
+      if (!named_bar_and(1 + t, 128, pv_done)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m_run + __log2f(l) : -INFINITY;
+      const bool valid = r < c.nrows, direct = c.direct;
+      const int row = (c.node0 + (valid ? r / p.G : 0)) * p.Hq + c.g * p.G + r % p.G;    // (node, head)
+      const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[32];
+        tmem_ld32(tO + k * 32, o);
+        tmem_ld_wait(o);
+        if (!valid) continue;
+        if (direct) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * D + k * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 y;
+            y.x = pack_bf16x2(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv);
+            y.y = pack_bf16x2(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv);
+            y.z = pack_bf16x2(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv);
+            y.w = pack_bf16x2(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv);
+            dst[q] = y;
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + static_cast<size_t>(prow) * D + k * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                                 __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        }
+      }
+      if (valid) {
+        if (direct) {
+          if (p.lse != nullptr) {
+            const int node = row / p.Hq, h = row - node * p.Hq;
+            p.lse[p.cu != nullptr ? static_cast<size_t>(h * p.T + node)
+                                  : (static_cast<size_t>(c.b) * p.Hq + h) * p.N + (node - c.b * p.N)] =
+                lse2 * 0.69314718055994531f;
+          }
+        } else {
+          p.ws_lse[prow] = lse2;
+        }
+        if (c.opens) {                 // where the item's pieces are
+          p.ws_desc[(c.b < 0 ? 0 : p.rows) + row] = make_int4(prow, c.n, c.second + r, 0);
+          if (c.alone) p.ws_desc[row] = make_int4(0, 0, 0, 0);
+        }
+      }
+      if (je < Wc) {                   // the next piece's first PV accumulates onto zero
+        uint32_t z[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) z[e] = 0u;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_st32(tO + c * 32, z);
+      }
+      jg0 += T;
+    }
+    if (!ok) set_abort(abort, p.dev_err);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  grid_dependents_launch();
+}
+
+// ------------------------------------------------------------------------ the merge
+
+// One warp per (node, query head) row: the pieces of its shared and own parts, listed by ws_desc,
+// merged by log-sum-exp.  Four pieces' rows are requested together.  What ws_desc says is
+// checked against the workspace: a malformed group_start leaves it unwritten.
+template <int D>
+__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int R, int total) {
+  constexpr int E = D / 32;
+  constexpr int kBatch = 4;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const long long rr = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (rr >= static_cast<long long>(p.B) * p.N * p.Hq) return;
+  const int h = static_cast<int>(rr % p.Hq);
+  const long long bi = rr / p.Hq;
+  const int i = static_cast<int>(bi % p.N), b = static_cast<int>(bi / p.N);
+  const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+  if (i >= sp.n) return;
+  const int row = static_cast<int>(sp.row0 + i) * p.Hq + h;
+  const int4 da = p.ws_desc[row], db = p.ws_desc[p.rows + row];
+  if (db.y == 0) return;                         // written by its only piece
+  auto bad = [&](const int4& d) {
+    return d.y < 0 || d.y > p.ranges || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
+           (d.y > 1 && (d.z < 0 || d.z + (d.y - 2) * 2 * R >= total));
+  };
+  if (bad(da) || bad(db)) return;
+  const int n = da.y + db.y;
+  auto piece = [&](int k) {                      // workspace row of piece k
+    const int4& d = k < da.y ? da : db;
+    const int at = k < da.y ? k : k - da.y;
+    return at == 0 ? d.x : d.z + (at - 1) * 2 * R;
+  };
+  float mx = -INFINITY;
+  for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.ws_lse[piece(k)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  float sum = 0.f;
+  for (int k0 = 0; k0 < n; k0 += kBatch) {
+    float l[kBatch], x[kBatch][E];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      l[k] = -INFINITY;
+      if (k0 + k < n) {
+        const int at = piece(k0 + k);
+        l[k] = p.ws_lse[at];
+        const float* src = p.ws_o + static_cast<size_t>(at) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          x[k][e] = y.x;
+          x[k][e + 1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (l[k] == -INFINITY) continue;           // no such piece, or it saw nothing
+      const float f = exp2f(l[k] - mx);
+      sum += f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, x[k][e], acc[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t y[E / 2];
+#pragma unroll
+  for (int e = 0; e < E; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  uint16_t* dst = p.out + static_cast<size_t>(row) * D + lane * E;
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = y[0];
+  if (p.lse != nullptr && lane == 0)
+    p.lse[lse_index(p.cu != nullptr, sp.row0, p.T, b, h, i, p.Hq, p.N)] =
+        (sum > 0.f ? mx + __log2f(sum) : -INFINITY) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------------ host side
+
+struct SharedPlan {
+  int NT, ranges;
+  long long rows, total;   // (node, head) rows; workspace rows
+  size_t ws_bytes;
+};
+
+constexpr int kMaxRanges = 1024;   // SMs that the 32-bit limits allow for
+
+// nodes: B * N padded, T packed.
+bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, int D, int max_pages,
+                      int page_size) {
+  if (B < 1 || B > kSharedMaxB || N < 1 || N > JF_MAX_NODES || nodes < 1 || Hq < 1 || Hkv < 1 || max_pages < 1) return false;
+  if (n_groups < 1 || n_groups > B || (D != 64 && D != 128) || page_size != kPage || Hq % Hkv != 0) return false;
+  const int G = Hq / Hkv;
+  if (G > kRowTile || (G & (G - 1)) != 0) return false;
+  if (static_cast<long long>(max_pages) * kPage < N || static_cast<long long>(max_pages) * kPage > (1ll << 30)) return false;
+  // workspace rows and positions of the schedule are 32-bit
+  const long long tiles = (static_cast<long long>(max_pages) * kPage + kKeyTile - 1) / kKeyTile + kSwitch + 1;
+  const long long groups = nodes * G / kRowTile + B + n_groups;
+  return 2 * nodes * Hq + 4 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
+         static_cast<long long>(B) * N * Hq < 8ll * INT_MAX;
+}
+
+SharedPlan plan_shared(long long nodes, int n_groups, int Hq, int Hkv, int D, int sms) {
+  SharedPlan pl;
+  // Two row tiles per CTA (each key tile loaded feeds both) when a group's rows fill more than one.
+  pl.NT = nodes * (Hq / Hkv) > static_cast<long long>(n_groups) * kRowTile ? 2 : 1;
+  pl.ranges = std::min(sms, kMaxRanges);
+  pl.rows = nodes * Hq;
+  pl.total = 2 * pl.rows + 2ll * pl.ranges * pl.NT * kRowTile;
+  pl.ws_bytes = static_cast<size_t>(pl.total) * (D + 1) * sizeof(float) +
+                static_cast<size_t>(2 * pl.rows) * sizeof(int4) + 64;
+  return pl;
+}
+
+template <int NT, int D>
+jf_status launch_shared(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
+                        const CUtensorMap& vr, const SharedParams& prm, int total, cudaStream_t s) {
+  using C = Cfg<NT, D>;
+  static_assert(C::kSmemBytes >= 4 * (5 * kSharedMaxB + 1), "the schedule's scratch fits");
+  static SmemAttr attr;
+  if (!attr.ensure(shared_attention_kernel<NT, D>, C::kSmemBytes)) return JF_ERR_CUDA;
+  if (launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
+                 C::kSmemBytes, s, qm, km, vm, kr, vr, prm) != cudaSuccess)
+    return JF_ERR_CUDA;
+  const long long warps = static_cast<long long>(prm.B) * prm.N * prm.Hq;
+  return launch_pdl(shared_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, prm,
+                    NT * kRowTile, total) == cudaSuccess
+             ? JF_OK
+             : JF_ERR_CUDA;
+}
+
+jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                      const int32_t* prefix_len, const int32_t* tree_len, const int32_t* cu, const uint64_t* mask,
+                      const int32_t* group_start, const int32_t* shared_pages, int32_t n_groups, int32_t B, int32_t N,
+                      int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size, int32_t max_pages,
+                      int32_t num_pages, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_err, jf_stream_t stream) {
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_table == nullptr || prefix_len == nullptr ||
+      mask == nullptr || group_start == nullptr || shared_pages == nullptr || out == nullptr)
+    return JF_ERR_INVALID_ARGUMENT;
+  if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || D < 1 || page_size < 1 || max_pages < 1 || num_pages < 1 ||
+      n_groups < 1 || n_groups > B || (cu != nullptr && T < 1) || !(scale > 0.f) || !std::isfinite(scale))
+    return JF_ERR_INVALID_ARGUMENT;
+  if (cu != nullptr && static_cast<long long>(T) + N >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * kPage >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
+  const long long nodes = cu != nullptr ? T : static_cast<long long>(B) * N;
+  if (!shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return JF_ERR_UNSUPPORTED;
+  if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
+      !aligned_to(mask, 8))
+    return JF_ERR_MISALIGNED;
+  const size_t qb = static_cast<size_t>(nodes) * Hq * D * 2, cb = static_cast<size_t>(num_pages) * kPage * Hkv * D * 2;
+  if (overlap(out, qb, q, qb) || overlap(out, qb, k_cache, cb) || overlap(out, qb, v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
+  const int sms = current_sm_count();
+  if (sms <= 0) return JF_ERR_CUDA;
+  const SharedPlan pl = plan_shared(nodes, n_groups, Hq, Hkv, D, sms);
+  if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return JF_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned_to(workspace, 16)) return JF_ERR_MISALIGNED;
+  const int G = Hq / Hkv;
+  CUtensorMap qm, km, vm, kr, vr;
+  {
+    // q as one list of nodes: sequences of a group follow each other
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(nodes)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kRowTile / G)};
+    if (!encode(&qm, q, 3, dims, strides, box)) return JF_ERR_CUDA;
+  }
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(num_pages) * kPage};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
+    const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
+    if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&vm, v_cache, 3, dims, strides, box) ||
+        !encode(&kr, k_cache, 3, dims, strides, box_run) || !encode(&vr, v_cache, 3, dims, strides, box_run))
+      return JF_ERR_CUDA;
+  }
+  SharedParams prm = {};
+  prm.block_table = block_table; prm.prefix_len = prefix_len; prm.tree_len = tree_len; prm.cu = cu;
+  prm.group_start = group_start; prm.shared_pages = shared_pages; prm.mask = mask;
+  prm.out = static_cast<uint16_t*>(out);
+  prm.lse = lse;
+  prm.ws_desc = static_cast<int4*>(workspace);
+  prm.ws_o = reinterpret_cast<float*>(prm.ws_desc + 2 * pl.rows);
+  prm.ws_lse = prm.ws_o + static_cast<size_t>(pl.total) * D;
+  prm.dev_err = dev_err;
+  prm.T = cu != nullptr ? T : 0;
+  prm.B = B; prm.N = N; prm.Hq = Hq; prm.Hkv = Hkv; prm.G = G; prm.W = (N + 63) / 64;
+  prm.max_pages = max_pages; prm.num_pages = num_pages; prm.n_groups = n_groups; prm.ranges = pl.ranges;
+  prm.rows = static_cast<int>(pl.rows);
+  prm.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int total = static_cast<int>(pl.total);
+  if (D == 128)
+    return pl.NT == 2 ? launch_shared<2, 128>(qm, km, vm, kr, vr, prm, total, s)
+                      : launch_shared<1, 128>(qm, km, vm, kr, vr, prm, total, s);
+  return pl.NT == 2 ? launch_shared<2, 64>(qm, km, vm, kr, vr, prm, total, s)
+                    : launch_shared<1, 64>(qm, km, vm, kr, vr, prm, total, s);
+}
+
+}  // namespace
+}  // namespace jf
+
+extern "C" size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, int32_t T, int32_t n_groups,
+                                                          int32_t Hq, int32_t Hkv, int32_t D, int32_t max_pages,
+                                                          int32_t page_size) {
+  const long long nodes = T > 0 ? T : static_cast<long long>(B) * N;
+  if (!jf::shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return static_cast<size_t>(-1);
+  const int sms = jf::current_sm_count();
+  return sms > 0 ? jf::plan_shared(nodes, n_groups, Hq, Hkv, D, sms).ws_bytes : static_cast<size_t>(-1);
+}
+
+extern "C" jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_table, const int32_t* prefix_len,
+                                              const int32_t* tree_len, const uint64_t* mask,
+                                              const int32_t* group_start, const int32_t* shared_pages,
+                                              int32_t n_groups, int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                                              int32_t D, int32_t page_size, int32_t max_pages, int32_t num_pages,
+                                              float scale, void* out, float* lse, void* workspace,
+                                              size_t workspace_bytes, int32_t* dev_err, jf_stream_t stream) {
+  return jf::shared_call(q, k_cache, v_cache, block_table, prefix_len, tree_len, nullptr, mask, group_start,
+                         shared_pages, n_groups, B, N, 0, Hq, Hkv, D, page_size, max_pages, num_pages, scale, out,
+                         lse, workspace, workspace_bytes, dev_err, stream);
+}
+
+extern "C" jf_status jf_tree_attention_shared_packed(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table, const int32_t* prefix_len,
+    const int32_t* cu_seqlens, const uint64_t* mask, const int32_t* group_start, const int32_t* shared_pages,
+    int32_t n_groups, int32_t B, int32_t N_max, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+    int32_t max_pages, int32_t num_pages, float scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, int32_t* dev_err, jf_stream_t stream) {
+  if (cu_seqlens == nullptr) return JF_ERR_INVALID_ARGUMENT;
+  return jf::shared_call(q, k_cache, v_cache, block_table, prefix_len, nullptr, cu_seqlens, mask, group_start,
+                         shared_pages, n_groups, B, N_max, T, Hq, Hkv, D, page_size, max_pages, num_pages, scale,
+                         out, lse, workspace, workspace_bytes, dev_err, stream);
+}

@@ -26,7 +26,7 @@ STATUS_NAMES = {0: "JF_OK", 1: "JF_ERR_INVALID_ARGUMENT", 2: "JF_ERR_INVALID_TRE
 JF_DTYPE_BF16, JF_DTYPE_F32 = 0, 1
 DEVERR_BAD_PARENT, DEVERR_BAD_PAGE, DEVERR_BAD_PREFIX = 0x1, 0x2, 0x4
 DEVERR_BAD_TOKEN, DEVERR_TIMEOUT, DEVERR_BAD_PATH = 0x8, 0x10, 0x20
-DEVERR_BAD_TREE_LEN = 0x40
+DEVERR_BAD_TREE_LEN, DEVERR_BAD_GROUP = 0x40, 0x80
 MAX_NODES = 4096
 PAGE_SIZE = 16
 COUNT_PROMPT = 1 << 30
@@ -123,6 +123,12 @@ def _load():
     lib.jf_rotate_append_kv.restype = ctypes.c_int
     lib.jf_rotate_append_kv_packed.argtypes = rotate + [i32] * 9 + [P, P, P, P, P]
     lib.jf_rotate_append_kv_packed.restype = ctypes.c_int
+    lib.jf_tree_attention_shared_workspace_size.argtypes = [i32] * 9
+    lib.jf_tree_attention_shared_workspace_size.restype = sz
+    lib.jf_tree_attention_shared.argtypes = [P] * 9 + [i32] * 9 + [f32, P, P, P, sz, P, P]
+    lib.jf_tree_attention_shared.restype = ctypes.c_int
+    lib.jf_tree_attention_shared_packed.argtypes = [P] * 9 + [i32] * 10 + [f32, P, P, P, sz, P, P]
+    lib.jf_tree_attention_shared_packed.restype = ctypes.c_int
     adjust = [P, i32, P, P, P, P, P, P, i32, P, P, P, f32, P]
     lib.jf_adjust_logits.argtypes = adjust + [i32] * 3 + [P, i32, P, P]
     lib.jf_adjust_logits.restype = ctypes.c_int
@@ -902,6 +908,65 @@ def jf_rotate_append_kv_packed(q, k, v, k_cache, v_cache, block_table, prefix_le
                  interleaved, rotary_scale, q_norm, k_norm, norm_eps, None, cu_seqlens, int(N_max), dev_err, stream)
 
 
+def jf_tree_attention_shared_workspace_size(B, N, n_groups, Hq, Hkv, D, max_pages, T=0, page_size=PAGE_SIZE) -> int:
+    """T: the rows of a packed call, 0 for a padded one."""
+    n = _lib.jf_tree_attention_shared_workspace_size(B, N, T, n_groups, Hq, Hkv, D, max_pages, page_size)
+    if n == SIZE_MAX:
+        raise JFError("jf_tree_attention_shared_workspace_size", 3)
+    return int(n)
+
+
+def jf_tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start, shared_pages, scale,
+                             out, workspace, lse=None, tree_len=None, dev_err=None, stream=None) -> None:
+    """jf_tree_attention with each group's shared prefix read once (see include/jf.h)."""
+    B, N, Hq, D = q.shape
+    num_pages, page, Hkv, D2 = k_cache.shape
+    max_pages = block_table.shape[1]
+    n_groups = shared_pages.shape[0]
+    if D2 != D:
+        raise ValueError("q and k_cache head dims differ")
+    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+                     ("block_table", block_table, torch.int32, (B, max_pages)),
+                     ("prefix_len", prefix_len, torch.int32, (B,)), ("tree_len", tree_len, torch.int32, (B,)),
+                     ("mask", mask, torch.int64, (B, N, (N + 63) // 64)),
+                     ("group_start", group_start, torch.int32, (n_groups + 1,)),
+                     ("shared_pages", shared_pages, torch.int32, None), ("out", out, torch.bfloat16, q.shape),
+                     ("lse", lse, torch.float32, (B, Hq, N)), ("workspace", workspace, torch.uint8, None)),
+                    dev_err, stream)
+    _check("jf_tree_attention_shared", _lib.jf_tree_attention_shared(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(),
+        _at(tree_len), mask.data_ptr(), group_start.data_ptr(), shared_pages.data_ptr(), n_groups, B, N, Hq, Hkv, D,
+        page, max_pages, num_pages, float(scale), out.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel(),
+        _at(dev_err), on))
+
+
+def jf_tree_attention_shared_packed(q, k_cache, v_cache, block_table, prefix_len, cu_seqlens, N_max, mask,
+                                    group_start, shared_pages, scale, out, workspace, lse=None, dev_err=None,
+                                    stream=None) -> None:
+    """jf_tree_attention_shared on packed rows: q and out [T][Hq][D], mask [T][W], lse [Hq][T]."""
+    T, Hq, D = q.shape
+    num_pages, page, Hkv, D2 = k_cache.shape
+    B, max_pages = block_table.shape
+    n_groups = shared_pages.shape[0]
+    if D2 != D:
+        raise ValueError("q and k_cache head dims differ")
+    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
+                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
+                     ("block_table", block_table, torch.int32, None), ("prefix_len", prefix_len, torch.int32, (B,)),
+                     ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)),
+                     ("mask", mask, torch.int64, (T, (N_max + 63) // 64)),
+                     ("group_start", group_start, torch.int32, (n_groups + 1,)),
+                     ("shared_pages", shared_pages, torch.int32, None), ("out", out, torch.bfloat16, q.shape),
+                     ("lse", lse, torch.float32, (Hq, T)), ("workspace", workspace, torch.uint8, None)),
+                    dev_err, stream)
+    _check("jf_tree_attention_shared_packed", _lib.jf_tree_attention_shared_packed(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(),
+        cu_seqlens.data_ptr(), mask.data_ptr(), group_start.data_ptr(), shared_pages.data_ptr(), n_groups, B, N_max, T,
+        Hq, Hkv, D, page, max_pages, num_pages, float(scale), out.data_ptr(), _at(lse), workspace.data_ptr(),
+        workspace.numel(), _at(dev_err), on))
+
+
 def jf_adjust_logits(logits, out, count=None, draft=None, mask=None, bias=None, allowed=None, allowed_row=None,
                      repetition=None, presence=None, frequency=None, masked=float("-inf"), tree_len=None,
                      dev_err=None, stream=None) -> None:
@@ -1217,6 +1282,44 @@ def rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, pos=Non
                                    k.shape[0] if N_max is None else N_max, out, pos, freq, interleaved, rotary_scale,
                                    q_norm, k_norm, norm_eps, dev_err, stream)
     return out
+
+
+def tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start, shared_pages, scale=None,
+                          with_lse=False, tree_len=None, cu_seqlens=None, N_max=None, out=None, lse=None,
+                          workspace=None, dev_err=None, stream=None):
+    """Attention of sequences in groups that share a prefix; out, or (out, lse) with with_lse or a
+    given lse.  New tensors' padding rows are zero.  With cu_seqlens the rows are packed; N_max is then
+    the largest tree (by default what mask's width allows)."""
+    with_lse = with_lse or lse is not None
+    if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
+        with _as_current(stream):
+            return tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start,
+                                         shared_pages, scale, with_lse, tree_len, cu_seqlens, N_max, out, lse,
+                                         workspace, dev_err)
+    Hq, D = q.shape[-2:]
+    B, max_pages = block_table.shape
+    if scale is None:
+        scale = D ** -0.5
+    packed = cu_seqlens is not None
+    if packed and N_max is None:
+        N_max = 64 * mask.shape[-1]
+    make = torch.zeros if packed or tree_len is not None else torch.empty
+    if out is None:
+        out = make(q.shape, dtype=q.dtype, device=q.device)
+    if with_lse and lse is None:
+        lse = make((Hq, q.shape[0]) if packed else (B, Hq, q.shape[1]), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        size = jf_tree_attention_shared_workspace_size(
+            B, N_max if packed else q.shape[1], shared_pages.shape[0], Hq, k_cache.shape[2], D, max_pages,
+            q.shape[0] if packed else 0, k_cache.shape[1])
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    if packed:
+        jf_tree_attention_shared_packed(q, k_cache, v_cache, block_table, prefix_len, cu_seqlens, N_max, mask,
+                                        group_start, shared_pages, scale, out, workspace, lse, dev_err, stream)
+    else:
+        jf_tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start, shared_pages, scale,
+                                 out, workspace, lse, tree_len, dev_err, stream)
+    return (out, lse) if with_lse else out
 
 
 def adjust_logits(logits, count=None, draft=None, mask=None, bias=None, allowed=None, allowed_row=None,
