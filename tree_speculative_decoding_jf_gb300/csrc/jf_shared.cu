@@ -12,7 +12,7 @@
 //
 // Work.  A unit is a group's shared part or a sequence's own part; an item is a unit, a
 // kv-head and a row-tile group (NT tiles of 128 rows).  Items lie end to end, T key tiles plus
-// kSwitch for the change of item, and are cut into one equal range per SM: lengths and group
+// X::SW for the change of item, and are cut into one equal range per SM: lengths and group
 // sizes are data, so every CTA forms the same schedule from them.  A range's pieces of items are
 // walked with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer,
 // MMA issuer, vouchers, softmax warpgroups, all counters running over the range's tiles as one
@@ -36,7 +36,12 @@
 namespace jf {
 namespace {
 
-constexpr int kSwitch = 1;          // cost of a change of item, in key tiles
+// How a kernel cuts its units: row tiles of R rows, key tiles of KT keys, and what a change of item
+// costs, in key tiles.
+template <int R_, int KT_, int SW_>
+struct Cut {
+  static constexpr int R = R_, KT = KT_, SW = SW_;
+};
 constexpr int kSharedMaxB = 4096;   // the schedule is formed in shared memory
 
 struct SharedParams {
@@ -46,13 +51,18 @@ struct SharedParams {
   float* lse;
   float* ws_o;       // [2 * rows + 2 * ranges * R][D]: shared parts, own parts, cut pieces
   float* ws_lse;     // the same rows' log-sum-exp (log2 domain)
-  int4* ws_desc;     // [2][rows]: first piece's row, pieces, second piece's row
+  int4* ws_desc;     // [2][rows]: first piece's row, pieces, second piece's row, rows from there to the next
   int32_t* dev_err;
   long long T;       // packed nodes
-  int B, N, Hq, Hkv, G, W, max_pages, num_pages, n_groups, ranges;
+  const uint16_t *q, *k_cache, *v_cache;     // the row kernel reads them directly
+  int B, N, Hq, Hkv, G, W, max_pages, num_pages, n_groups;
   int rows;          // (node, query head) rows
+  int kinds;         // units of this launch: kShared, kOwn or both
+  int ranges;        // of this launch
+  int cut0;          // first workspace row of its cut pieces
   float scale_log2;
 };
+constexpr int kShared = 1, kOwn = 2;
 
 // ------------------------------------------------------------------------ the schedule
 
@@ -68,7 +78,7 @@ struct Unit {
   int f0, nr, key0, P, L, T, mpc, bt;
 };
 
-template <int NT>
+template <typename X>
 __device__ __forceinline__ Unit make_unit(const SharedParams& p, int b, int b0, int b1, int S) {
   Unit t;
   const int cap = p.max_pages * kPage;
@@ -94,8 +104,8 @@ __device__ __forceinline__ Unit make_unit(const SharedParams& p, int b, int b0, 
     t.f0 = static_cast<int>(sp.row0);
     t.nr = sp.n;
   }
-  t.mpc = static_cast<int>((static_cast<long long>(t.nr) * p.G + NT * kRowTile - 1) / (NT * kRowTile));
-  t.T = t.nr > 0 ? (t.L - t.key0 + kKeyTile - 1) / kKeyTile : 0;
+  t.mpc = static_cast<int>((static_cast<long long>(t.nr) * p.G + X::R - 1) / X::R);
+  t.T = t.nr > 0 ? (t.L - t.key0 + X::KT - 1) / X::KT : 0;
   return t;
 }
 
@@ -110,18 +120,23 @@ struct Schedule {
   }
 };
 
-// Every thread of the block calls it; scratch: 4 * (3 * n_groups + 2 * B + 1) bytes at least.  Unit
-// order: group by group, its shared part (if any), then its sequences.
-template <int NT>
-__device__ __noinline__ void make_schedule(const SharedParams& p, int v, int32_t* err, int* scratch, Schedule* out) {
+// The ranges v0 .. v0 + TEAMS - 1 of the launch.  Every thread of the block calls it; scratch: 4 * (3 *
+// n_groups + 2 * B + 1) bytes at least.  Unit order: group by group, its shared part (if any), then
+// its sequences.  Units of kinds that the launch does not do cost nothing.
+template <typename X, int TEAMS>
+__device__ __noinline__ void make_schedule(const SharedParams& p, int v0, int32_t* err, int* scratch, Schedule* out) {
   const int ng = p.n_groups, B = p.B, U = ng + B, tid = threadIdx.x, nth = blockDim.x;
   int* gs = scratch;                 // [ng + 1]
   int* cost = gs + ng + 1;           // [U] positions of the unit
   int* items = cost + U;             // [U]
   __shared__ long long s_scan[32];
   __shared__ int s_items[32];
+  __shared__ int s_before[TEAMS][2]; // tiles before a range's ends: the position less SW per item completed
   for (int u = tid; u <= ng; u += nth) gs[u] = p.group_start[u];
-  if (tid == 0) out->tiles = 0, out->lo = out->hi = 0;
+  if (tid < TEAMS) {
+    out[tid].tiles = out[tid].lo = out[tid].hi = 0;
+    s_before[tid][0] = s_before[tid][1] = 0;
+  }
   __syncthreads();
   bool bad = false;
   for (int u = tid; u < ng; u += nth) bad = bad || gs[u] > gs[u + 1];
@@ -130,16 +145,18 @@ __device__ __noinline__ void make_schedule(const SharedParams& p, int v, int32_t
     if (tid == 0 && err != nullptr) report(err, JF_DEVERR_BAD_GROUP);
     return;
   }
-  const int cap = p.max_pages * kPage;
-  for (int e = tid; e < U; e += nth) {
-    // unit e: u + gs[u] is group u's shared unit
+  auto group_of = [&](int e) {       // of unit e: unit u + gs[u] is group u's shared part
     int u = 0, hi = ng;
     while (hi - u > 1) {
       const int mid = (u + hi) >> 1;
       if (mid + gs[mid] <= e) u = mid; else hi = mid;
     }
-    const int b = e - u - 1 - 0;     // u + gs[u] + 1 + (b - gs[u]) = e
-    const int b0 = gs[u], b1 = gs[u + 1];
+    return u;
+  };
+  const int cap = p.max_pages * kPage;
+  for (int e = tid; e < U; e += nth) {
+    const int u = group_of(e), b0 = gs[u], b1 = gs[u + 1];
+    const int b = e - u - 1;
     const int S = group_keys(p, u, b0, b1);
     const bool shared = e == u + b0;
     if (err != nullptr) {
@@ -153,10 +170,10 @@ __device__ __noinline__ void make_schedule(const SharedParams& p, int v, int32_t
       }
     }
     int n = 0, c = 0;
-    if (!shared || S > 0) {
-      const Unit t = make_unit<NT>(p, shared ? -1 : b, b0, b1, S);
+    if (shared ? S > 0 && (p.kinds & kShared) : (p.kinds & kOwn) != 0) {
+      const Unit t = make_unit<X>(p, shared ? -1 : b, b0, b1, S);
       n = p.Hkv * t.mpc;
-      c = n * (t.T + kSwitch);
+      c = n * (t.T + X::SW);
       if (t.T == 0) n = c = 0;
     }
     cost[e] = c;
@@ -188,45 +205,34 @@ __device__ __noinline__ void make_schedule(const SharedParams& p, int v, int32_t
     total_items += s_items[w];
   }
   const int q = static_cast<int>(total / p.ranges), rem = static_cast<int>(total - static_cast<long long>(q) * p.ranges);
-  const long long lo = static_cast<long long>(v) * q + min(v, rem), hi = lo + q + (v < rem ? 1 : 0);
-  // tiles before a position: the position less kSwitch per item completed before it
-  __shared__ int s_before[2];
-  if (tid == 0) {
-    s_before[0] = 0;
-    s_before[1] = static_cast<int>(total) - kSwitch * total_items;     // hi == total
-  }
-  __syncthreads();
-  const long long first = upto - mine;
-  const int first_items = upto_items - mine_items;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const long long x = k == 0 ? lo : hi;
-    if (x < first || x >= upto) continue;        // the position lies in another thread's chunk
-    long long at = first;
-    int done = first_items, e = e0;
+  const int first = static_cast<int>(upto - mine), last = static_cast<int>(upto);
+  for (int k = 0; k < 2 * TEAMS; ++k) {
+    const int v = v0 + (k >> 1) + (k & 1), x = v * q + min(v, rem);      // start of range v0 + k / 2, or its end
+    if (x >= total && tid == 0 && (k & 1)) s_before[k >> 1][1] = static_cast<int>(total) - X::SW * total_items;
+    if (x < first || x >= last) continue;        // the position lies in another thread's chunk
+    int at = first, done = upto_items - mine_items, e = e0;
     while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
-    const int off = static_cast<int>(x - at);
-    const int per = cost[e] / items[e];          // T + kSwitch
+    const int off = x - at;
+    const int per = cost[e] / items[e];          // T + SW
     const int item = off / per, in = off - item * per;
-    s_before[k] = static_cast<int>(x) - kSwitch * (done + item) - max(0, in - (per - kSwitch));
-    if (k == 0) {
-      int u = 0, h = ng;
-      while (h - u > 1) {
-        const int mid = (u + h) >> 1;
-        if (mid + gs[mid] <= e) u = mid; else h = mid;
-      }
-      out->u = u;
-      out->b = e == u + gs[u] ? -1 : e - u - 1;
-      out->off = off;
+    s_before[k >> 1][k & 1] = x - X::SW * (done + item) - max(0, in - (per - X::SW));
+    if ((k & 1) == 0) {
+      const int u = group_of(e);
+      Schedule& o = out[k >> 1];
+      o.u = u;
+      o.b = e == u + gs[u] ? -1 : e - u - 1;
+      o.off = off;
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    out->lo = static_cast<int>(lo);
-    out->hi = static_cast<int>(hi);
-    out->q = q;
-    out->rem = rem;
-    out->tiles = lo < hi ? s_before[1] - s_before[0] : 0;
+  if (tid < TEAMS) {
+    const int v = v0 + tid;
+    Schedule& o = out[tid];
+    o.lo = v * q + min(v, rem);
+    o.hi = (v + 1) * q + min(v + 1, rem);
+    o.q = q;
+    o.rem = rem;
+    o.tiles = o.lo < o.hi ? s_before[tid][1] - s_before[tid][0] : 0;
   }
 }
 
@@ -244,9 +250,33 @@ struct Piece {
 // A piece's slot is written once the S MMAs of the last tile of the piece before it are done: every
 // role has then left the pieces up to the third before it.
 constexpr int kPieces = 4;
+// A change of item costs the tcgen05 kernel about four tiles' time: the next item's Q and K arrive, the
+// rows leave TMEM.
+template <int NT>
+using TileCut = Cut<NT * kRowTile, kKeyTile, 4>;
+
+// What a piece leaves beside a row's output: its log-sum-exp and, from the item's first piece, where
+// the row's pieces are (stride: workspace rows from the second piece to the third, and so on).
+__device__ __forceinline__ void write_row_facts(const SharedParams& p, const Piece& c, int row, int prow, int r,
+                                                float lse2, int stride) {
+  if (c.direct) {
+    if (p.lse != nullptr) {
+      const int node = row / p.Hq, h = row - node * p.Hq;
+      p.lse[p.cu != nullptr ? static_cast<size_t>(h * p.T + node)
+                            : (static_cast<size_t>(c.b) * p.Hq + h) * p.N + (node - c.b * p.N)] =
+          lse2 * 0.69314718055994531f;
+    }
+  } else {
+    p.ws_lse[prow] = lse2;
+  }
+  if (c.opens) {
+    p.ws_desc[(c.b < 0 ? 0 : p.rows) + row] = make_int4(prow, c.n, c.second + r, stride);
+    if (c.alone) p.ws_desc[row] = make_int4(0, 0, 0, 0);
+  }
+}
 
 // The pieces of a range, one after the other.
-template <int NT>
+template <typename X>
 struct Walk {
   const SharedParams& p;
   int lo, hi;
@@ -261,8 +291,8 @@ struct Walk {
     b0 = p.group_start[u];
     b1 = p.group_start[u + 1];
     S = group_keys(p, u, b0, b1);
-    t = make_unit<NT>(p, b, b0, b1, S);
-    const int per = t.T + kSwitch, item = s.off / per;
+    t = make_unit<X>(p, b, b0, b1, S);
+    const int per = t.T + X::SW, item = s.off / per;
     g = item / t.mpc;
     mp = item - g * t.mpc;
     x = lo - (s.off - item * per);
@@ -274,10 +304,10 @@ struct Walk {
     settle();
   }
   __device__ __forceinline__ Piece piece(const Schedule& s, int v) const {
-    constexpr int R = NT * kRowTile;
+    constexpr int R = X::R;
     Piece c;
     c.T = k1 - k0;
-    c.first = t.key0 + k0 * kKeyTile;
+    c.first = t.key0 + k0 * X::KT;
     c.P = t.P;
     c.L = t.L;
     c.node0 = t.f0 + mp * R / p.G;
@@ -289,13 +319,13 @@ struct Walk {
     c.direct = c.whole && c.alone;
     c.opens = k0 == 0;
     const int slot = x + k0 == lo ? 0 : 1;
-    c.slots = 2 * p.rows + (2 * v + slot) * R;
+    c.slots = p.cut0 + (2 * v + slot) * R;
     c.n = c.direct ? 0 : 1;
     c.second = 0;
     if (!c.whole && c.opens) {
       const int va = s.range_of(x), vb = s.range_of(x + t.T - 1);
       c.n = vb - va + 1;
-      c.second = 2 * p.rows + 2 * (va + 1) * R;
+      c.second = p.cut0 + 2 * (va + 1) * R;
     }
     return c;
   }
@@ -313,6 +343,7 @@ struct Walk {
   __device__ __noinline__ void next_unit() {
     for (;;) {
       b = b < 0 ? b0 : b + 1;
+      if (!(p.kinds & kOwn)) b = b1;     // shared parts alone: on to the next group
       while (b >= b1) {
         if (++u >= p.n_groups) {
           x = INT_MAX;
@@ -321,14 +352,14 @@ struct Walk {
         b0 = b1;
         b1 = p.group_start[u + 1];
         S = group_keys(p, u, b0, b1);
-        b = S > 0 ? -1 : b0;
+        b = S > 0 && (p.kinds & kShared) ? -1 : ((p.kinds & kOwn) ? b0 : b1);
       }
-      t = make_unit<NT>(p, b, b0, b1, S);
+      t = make_unit<X>(p, b, b0, b1, S);
       if (t.T > 0) return;
     }
   }
   __device__ __forceinline__ void advance() {
-    x += t.T + kSwitch;
+    x += t.T + X::SW;
     if (++mp < t.mpc) return;
     mp = 0;
     if (++g < p.Hkv) return;
@@ -411,7 +442,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     tma_prefetch_desc(&vmap_run);
   }
   grid_dependency_wait();
-  make_schedule<NT>(p, v, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
+  grid_dependents_launch();             // the own parts' kernel may run beside this one; others wait for it
+  make_schedule<TileCut<NT>, 1>(p, v, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
   fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
   if (warp == 1) {
     tmem_alloc(&tmem_slot, C::kTmemCols);
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
       }
     };
     int jg0 = 0;
-    Walk<NT> w(p, s_sch);
+    Walk<TileCut<NT>> w(p, s_sch);
     for (int s = 0; w.live() && ok; ++s, w.next()) {
       const int T = w.k1 - w.k0, L = w.t.L;
       const int page0_of = w.t.key0 / kPage + w.k0 * kPagesPerTile;     // the piece's first page
@@ -521,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         if (!wait_warp(&v_full[jl % SV], static_cast<uint32_t>(jl / SV) & 1u, abort, wlim)) { ok = false; break; }
         const int r0 = L - last_key0;
         uint8_t* vt = v_s + (jl % SV) * C::kTileBytes;
-        const int per_half = (kKeyTile - r0) * 8;
+        const int per_half = (-r0 & (kPage - 1)) * 8;     // to the page's end: later pages came as zeros
         for (int c = lane; c < per_half * C::kHalves; c += 32) {
           const int hh = c / per_half, rem = c % per_half;
           *reinterpret_cast<uint4*>(vt + hh * C::kHalfBytes + (r0 + rem / 8) * 128 + (rem % 8) * 16) =
@@ -744,22 +776,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                                  __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
         }
       }
-      if (valid) {
-        if (direct) {
-          if (p.lse != nullptr) {
-            const int node = row / p.Hq, h = row - node * p.Hq;
-            p.lse[p.cu != nullptr ? static_cast<size_t>(h * p.T + node)
-                                  : (static_cast<size_t>(c.b) * p.Hq + h) * p.N + (node - c.b * p.N)] =
-                lse2 * 0.69314718055994531f;
-          }
-        } else {
-          p.ws_lse[prow] = lse2;
-        }
-        if (c.opens) {                 // where the item's pieces are
-          p.ws_desc[(c.b < 0 ? 0 : p.rows) + row] = make_int4(prow, c.n, c.second + r, 0);
-          if (c.alone) p.ws_desc[row] = make_int4(0, 0, 0, 0);
-        }
-      }
+      if (valid) write_row_facts(p, const_cast<const Piece&>(s_piece[s % kPieces]), row, prow, r, lse2, 2 * NT * kRowTile);
       if (je < Wc) {                   // the next piece's first PV accumulates onto zero
         uint32_t z[32];
 #pragma unroll
@@ -779,13 +796,252 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
   grid_dependents_launch();
 }
 
+// ------------------------------------------------------------------------ few rows
+
+// Units of few rows (a decode step's G rows of a sequence, the beams of a prompt) are bound by the K/V
+// stream and by the latency of an item, not by matrix products, so a team of MT warps takes a
+// range of its own, 16 rows a warp, with nothing shared and nothing to synchronise: K and V go from
+// global memory to registers as the fragments of 16 x 8 x 16 products, one page of 16 keys a
+// step, the next step's K under way during the softmax and its V during the next scores.  (The
+// warps of a team read the same K and V: the later ones find them in L1.)
+//   Scores: a thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of eight) are two
+//   k-steps' B fragments if Q's chunks are cut the same way: the order of the contraction is free.
+//   Output: column n of n-tile 8 h + j is d = 64 h + 8 n + j, so that a thread's V chunks (8 h' values at
+//   64 h + 8 (lane / 4) of keys 2 (lane % 4) + {0, 1, 8, 9}) hold its B fragments, two keys' values
+//   joined by a byte permute, and a thread ends with runs of eight consecutive d.
+constexpr int kRowWarps = 8;
+template <int MT>
+using RowCut = Cut<16 * MT, 64, 2>;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(32 * kRowWarps, 1) shared_rows_kernel(const __grid_constant__ SharedParams p) {
+  using X = RowCut<MT>;
+  constexpr int kTeams = kRowWarps / MT;
+  constexpr int kI = D / 32;            // 16-byte chunks of a row per thread (scores)
+  constexpr int kH = D / 64;            // 16-byte chunks of a V row per thread
+  extern __shared__ int s_scratch[];
+  __shared__ Schedule s_sch[kTeams];
+  if (p.kinds & kShared) {
+    grid_dependency_wait();
+  }                                     // else: beside the shared parts' kernel, which waited (see below)
+  grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / MT, tw = warp % MT;
+  const int v = blockIdx.x * kTeams + team;
+  make_schedule<X, kTeams>(p, blockIdx.x * kTeams, blockIdx.x == 0 && p.kinds == (kShared | kOwn) ? p.dev_err : nullptr,
+                           s_scratch, s_sch);
+  __syncthreads();
+  const Schedule& sch = s_sch[team];
+  if (sch.tiles > 0) {
+    const int q4 = lane & 3, r8 = lane >> 2;
+    int bad = 0;
+    for (Walk<X> w(p, sch); w.live(); w.next()) {
+      const Piece c = w.piece(sch, v);
+      if (tw * 16 >= c.nrows) continue;              // this warp has none of the item's rows
+      const int ra = tw * 16 + r8, rb = ra + 8;      // the thread's rows of the item
+      const bool va = ra < c.nrows, vb = rb < c.nrows;
+      const int na = c.node0 + (va ? ra / p.G : 0), nb = c.node0 + (vb ? rb / p.G : 0);
+      const int rowa = na * p.Hq + c.g * p.G + ra % p.G, rowb = nb * p.Hq + c.g * p.G + rb % p.G;
+      uint4 qa[kI], qb[kI];
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const int ch = q4 + 4 * i;
+        qa[i] = va ? reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(rowa) * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
+        qb[i] = vb ? reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(rowb) * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      const int end = min(c.L, c.first + c.T * X::KT);
+      const int steps = (end - c.first + kPage - 1) / kPage;
+      const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages + c.first / kPage;
+      const bool split = c.P < kSplitPrefix;         // rows with few keys: probabilities in two bf16 parts
+      float o[8 * kH][4];
+#pragma unroll
+      for (int j = 0; j < 8 * kH; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
+      int ids = -1;                                  // lane l: the page of step 32 * k + l
+      auto page_of = [&](int s) -> int {
+        if ((s & 31) == 0) {
+          ids = -1;
+          if (s + lane < steps) {
+            ids = __ldg(bt + s + lane);
+            if (ids < 0 || ids >= p.num_pages) {
+              ids = -1;
+              bad = 1;
+            }
+          }
+        }
+        return __shfl_sync(0xffffffffu, ids, s & 31);
+      };
+      uint4 kr[2][kI], vr[4][kH];
+      auto load_k = [&](int s, int page) {
+        const int key0 = c.first + s * kPage;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const bool in = page >= 0 && key0 + 8 * t + r8 < end;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.k_cache + ((static_cast<size_t>(max(page, 0)) * kPage + 8 * t + r8) * p.Hkv + c.g) * D);
+#pragma unroll
+          for (int i = 0; i < kI; ++i) kr[t][i] = in ? src[q4 + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      auto load_v = [&](int s, int page) {           // keys past the end: zero (their probability is, too)
+        const int key0 = c.first + s * kPage;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
+          const bool in = page >= 0 && key0 + key < end;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.v_cache + ((static_cast<size_t>(max(page, 0)) * kPage + key) * p.Hkv + c.g) * D);
+#pragma unroll
+          for (int h = 0; h < kH; ++h) vr[t][h] = in ? src[r8 + 8 * h] : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      int page = page_of(0);
+      load_k(0, page);
+      load_v(0, page);
+      for (int s = 0; s < steps; ++s) {
+        float x[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kI; ++i) {
+            mma_16816(x[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[t][i].x, kr[t][i].y);
+            mma_16816(x[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[t][i].z, kr[t][i].w);
+          }
+        }
+        const int key0 = c.first + s * kPage;
+        page = -1;
+        if (s + 1 < steps) {
+          page = page_of(s + 1);
+          load_k(s + 1, page);
+        }
+        if (key0 + kPage > c.P) {                    // tree keys, or keys past the end
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + 8 * t + 2 * q4 + e, j = key - c.P;
+              bool sa = key < end, sb = sa;
+              if (sa && j >= 0) {
+                sa = va && c.b >= 0 && ((p.mask[static_cast<size_t>(na) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
+                sb = vb && c.b >= 0 && ((p.mask[static_cast<size_t>(nb) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
+              }
+              if (!sa) x[t][e] = -INFINITY;
+              if (!sb) x[t][2 + e] = -INFINITY;
+            }
+        }
+        float ta = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+        float tb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+#pragma unroll
+        for (int k = 1; k < 4; k <<= 1) {
+          ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, k));
+          tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, k));
+        }
+        ta *= p.scale_log2;
+        tb *= p.scale_log2;
+        // The running maximum rises only by more than 2^8 (see jf_attention.cu): O is rescaled rarely.
+        const bool ua = ta > ma + kRescaleThreshold, ub = tb > mb + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, ua || ub)) {
+          const float fa = ua ? fast_exp2(ma - ta) : 1.f, fb = ub ? fast_exp2(mb - tb) : 1.f;
+          if (ua) ma = ta;
+          if (ub) mb = tb;
+          la *= fa;
+          lb *= fb;
+#pragma unroll
+          for (int j = 0; j < 8 * kH; ++j) {
+            o[j][0] *= fa; o[j][1] *= fa;
+            o[j][2] *= fb; o[j][3] *= fb;
+          }
+        }
+        const float oa = ma == -INFINITY ? 0.f : -ma, ob = mb == -INFINITY ? 0.f : -mb;
+        uint32_t pa[4], pl[4];                       // the A fragment of the probabilities, and of their rest
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float y0 = fast_exp2(fmaf(x[t][0], p.scale_log2, oa)), y1 = fast_exp2(fmaf(x[t][1], p.scale_log2, oa));
+          const float z0 = fast_exp2(fmaf(x[t][2], p.scale_log2, ob)), z1 = fast_exp2(fmaf(x[t][3], p.scale_log2, ob));
+          la += y0 + y1;
+          lb += z0 + z1;
+          pa[2 * t] = pack_bf16x2(y0, y1);
+          pa[2 * t + 1] = pack_bf16x2(z0, z1);
+          if (split) {
+            pl[2 * t] = pack_bf16x2(y0 - __uint_as_float(pa[2 * t] << 16), y1 - __uint_as_float(pa[2 * t] & 0xFFFF0000u));
+            pl[2 * t + 1] = pack_bf16x2(z0 - __uint_as_float(pa[2 * t + 1] << 16), z1 - __uint_as_float(pa[2 * t + 1] & 0xFFFF0000u));
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t w0 = j < 2 ? vr[0][h].x : (j < 4 ? vr[0][h].y : (j < 6 ? vr[0][h].z : vr[0][h].w));
+            const uint32_t w1 = j < 2 ? vr[1][h].x : (j < 4 ? vr[1][h].y : (j < 6 ? vr[1][h].z : vr[1][h].w));
+            const uint32_t w2 = j < 2 ? vr[2][h].x : (j < 4 ? vr[2][h].y : (j < 6 ? vr[2][h].z : vr[2][h].w));
+            const uint32_t w3 = j < 2 ? vr[3][h].x : (j < 4 ? vr[3][h].y : (j < 6 ? vr[3][h].z : vr[3][h].w));
+            const uint32_t b0 = __byte_perm(w0, w1, j & 1 ? 0x7632 : 0x5410);
+            const uint32_t b1 = __byte_perm(w2, w3, j & 1 ? 0x7632 : 0x5410);
+            mma_16816(o[8 * h + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
+            if (split) mma_16816(o[8 * h + j], pl[0], pl[1], pl[2], pl[3], b0, b1);
+          }
+        }
+        if (s + 1 < steps) load_v(s + 1, page);
+      }
+#pragma unroll
+      for (int k = 1; k < 4; k <<= 1) {
+        la += __shfl_xor_sync(0xffffffffu, la, k);
+        lb += __shfl_xor_sync(0xffffffffu, lb, k);
+      }
+      // ---- the piece's rows
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const bool ok = half == 0 ? va : vb;
+        const int r = half == 0 ? ra : rb, row = half == 0 ? rowa : rowb;
+        const float l = half == 0 ? la : lb, m = half == 0 ? ma : mb;
+        if (!ok) continue;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+        const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d0 = 64 * h + 8 * (2 * q4 + e), at = 2 * half + e;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = o[8 * h + j][at] * inv;
+            if (c.direct) {
+              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * D + d0) =
+                  make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + static_cast<size_t>(prow) * D + d0);
+              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          }
+        if (q4 == 0) write_row_facts(p, c, row, prow, r, lse2, 2 * X::R);
+      }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_err, JF_DEVERR_BAD_PAGE);
+  }
+  // A launch of own parts alone runs beside the shared parts' kernel (which lets it start once all its
+  // CTAs have seen their inputs): it must not be complete before that one is, for what follows
+  // waits for this one.
+  if (!(p.kinds & kShared)) grid_dependency_wait();
+}
+
 // ------------------------------------------------------------------------ the merge
 
 // One warp per (node, query head) row: the pieces of its shared and own parts, listed by ws_desc,
 // merged by log-sum-exp.  Four pieces' rows are requested together.  What ws_desc says is
 // checked against the workspace: a malformed group_start leaves it unwritten.
 template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int R, int total) {
+__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
   constexpr int E = D / 32;
   constexpr int kBatch = 4;
   grid_dependency_wait();
@@ -802,15 +1058,15 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   const int4 da = p.ws_desc[row], db = p.ws_desc[p.rows + row];
   if (db.y == 0) return;                         // written by its only piece
   auto bad = [&](const int4& d) {
-    return d.y < 0 || d.y > p.ranges || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
-           (d.y > 1 && (d.z < 0 || d.z + (d.y - 2) * 2 * R >= total));
+    return d.y < 0 || d.y > total || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
+           (d.y > 1 && (d.z < 0 || d.w < 0 || d.z + static_cast<long long>(d.y - 2) * d.w >= total));
   };
   if (bad(da) || bad(db)) return;
   const int n = da.y + db.y;
   auto piece = [&](int k) {                      // workspace row of piece k
     const int4& d = k < da.y ? da : db;
     const int at = k < da.y ? k : k - da.y;
-    return at == 0 ? d.x : d.z + (at - 1) * 2 * R;
+    return at == 0 ? d.x : d.z + (at - 1) * d.w;
   };
   float mx = -INFINITY;
   for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.ws_lse[piece(k)]);
@@ -861,12 +1117,16 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
 // ------------------------------------------------------------------------ host side
 
 struct SharedPlan {
-  int NT, ranges;
+  int tile_nt;             // row tiles per CTA of the tcgen05 kernel, 0: it is not used
+  int tile_kinds, tile_ranges, tile_cut0;
+  int row_mt;              // warps per team of the row kernel, 0: it is not used
+  int row_kinds, row_ranges, row_cut0;
   long long rows, total;   // (node, head) rows; workspace rows
   size_t ws_bytes;
 };
 
 constexpr int kMaxRanges = 1024;   // SMs that the 32-bit limits allow for
+constexpr int kRowKernelRows = 64; // rows of a unit up to which the row kernel takes it
 
 // nodes: B * N padded, T packed.
 bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, int D, int max_pages,
@@ -877,37 +1137,81 @@ bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int H
   if (G > kRowTile || (G & (G - 1)) != 0) return false;
   if (static_cast<long long>(max_pages) * kPage < N || static_cast<long long>(max_pages) * kPage > (1ll << 30)) return false;
   // workspace rows and positions of the schedule are 32-bit
-  const long long tiles = (static_cast<long long>(max_pages) * kPage + kKeyTile - 1) / kKeyTile + kSwitch + 1;
-  const long long groups = nodes * G / kRowTile + B + n_groups;
-  return 2 * nodes * Hq + 4 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
+  const long long tiles = static_cast<long long>(max_pages) * kPage / 64 + 5;
+  const long long groups = nodes * G / 16 + B + n_groups;
+  return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
          static_cast<long long>(B) * N * Hq < 8ll * INT_MAX;
 }
 
-SharedPlan plan_shared(long long nodes, int n_groups, int Hq, int Hkv, int D, int sms) {
-  SharedPlan pl;
-  // Two row tiles per CTA (each key tile loaded feeds both) when a group's rows fill more than one.
-  pl.NT = nodes * (Hq / Hkv) > static_cast<long long>(n_groups) * kRowTile ? 2 : 1;
-  pl.ranges = std::min(sms, kMaxRanges);
+// Which kernel takes which units.  Up to 64 rows a group (on average) the row kernel takes both parts:
+// the K/V stream bounds it.  Groups of more rows have their shared parts on the tcgen05 kernel, two
+// row tiles per CTA (each key tile loaded feeds both) once they fill more than one, and so have own
+// parts of more than 64 rows.
+SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, int D, int sms) {
+  SharedPlan pl = {};
+  const long long G = Hq / Hkv, group_rows = (nodes * G + n_groups - 1) / n_groups, own_rows = N * G;
+  sms = std::min(sms, kMaxRanges);
   pl.rows = nodes * Hq;
-  pl.total = 2 * pl.rows + 2ll * pl.ranges * pl.NT * kRowTile;
+  auto team = [](long long rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); };
+  if (group_rows <= kRowKernelRows) {
+    pl.row_mt = team(group_rows);
+    pl.row_kinds = kShared | kOwn;
+  } else {
+    pl.tile_nt = group_rows > kRowTile ? 2 : 1;
+    pl.tile_kinds = kShared;
+    if (own_rows <= kRowKernelRows) {
+      pl.row_mt = team(own_rows);
+      pl.row_kinds = kOwn;
+    } else {
+      pl.tile_kinds |= kOwn;
+    }
+  }
+  pl.total = 2 * pl.rows;
+  if (pl.tile_nt > 0) {
+    pl.tile_ranges = sms;
+    pl.tile_cut0 = static_cast<int>(pl.total);
+    pl.total += 2ll * pl.tile_ranges * pl.tile_nt * kRowTile;
+  }
+  if (pl.row_mt > 0) {
+    pl.row_ranges = sms * (kRowWarps / pl.row_mt);
+    pl.row_cut0 = static_cast<int>(pl.total);
+    pl.total += 2ll * pl.row_ranges * pl.row_mt * 16;
+  }
   pl.ws_bytes = static_cast<size_t>(pl.total) * (D + 1) * sizeof(float) +
                 static_cast<size_t>(2 * pl.rows) * sizeof(int4) + 64;
   return pl;
 }
 
 template <int NT, int D>
-jf_status launch_shared(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
-                        const CUtensorMap& vr, const SharedParams& prm, int total, cudaStream_t s) {
+jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
+                       const CUtensorMap& vr, const SharedParams& prm, cudaStream_t s) {
   using C = Cfg<NT, D>;
   static_assert(C::kSmemBytes >= 4 * (5 * kSharedMaxB + 1), "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_attention_kernel<NT, D>, C::kSmemBytes)) return JF_ERR_CUDA;
-  if (launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
-                 C::kSmemBytes, s, qm, km, vm, kr, vr, prm) != cudaSuccess)
-    return JF_ERR_CUDA;
+  return launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
+                    C::kSmemBytes, s, qm, km, vm, kr, vr, prm) == cudaSuccess
+             ? JF_OK
+             : JF_ERR_CUDA;
+}
+
+template <int D, int MT>
+jf_status launch_rows(const SharedParams& prm, cudaStream_t s) {
+  constexpr int kMost = 4 * (5 * kSharedMaxB + 1);
+  static SmemAttr attr;
+  if (!attr.ensure(shared_rows_kernel<D, MT>, kMost)) return JF_ERR_CUDA;
+  const size_t smem = 4 * (3 * static_cast<size_t>(prm.n_groups) + 2 * static_cast<size_t>(prm.B) + 1);
+  return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / (kRowWarps / MT))),
+                    dim3(32 * kRowWarps), smem, s, prm) == cudaSuccess
+             ? JF_OK
+             : JF_ERR_CUDA;
+}
+
+template <int D>
+jf_status launch_merge(const SharedParams& prm, int total, cudaStream_t s) {
   const long long warps = static_cast<long long>(prm.B) * prm.N * prm.Hq;
-  return launch_pdl(shared_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, prm,
-                    NT * kRowTile, total) == cudaSuccess
+  return launch_pdl(shared_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, prm, total) ==
+                 cudaSuccess
              ? JF_OK
              : JF_ERR_CUDA;
 }
@@ -935,7 +1239,7 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   if (overlap(out, qb, q, qb) || overlap(out, qb, k_cache, cb) || overlap(out, qb, v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  const SharedPlan pl = plan_shared(nodes, n_groups, Hq, Hkv, D, sms);
+  const SharedPlan pl = plan_shared(nodes, N, n_groups, Hq, Hkv, D, sms);
   if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return JF_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned_to(workspace, 16)) return JF_ERR_MISALIGNED;
   const int G = Hq / Hkv;
@@ -967,16 +1271,36 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   prm.dev_err = dev_err;
   prm.T = cu != nullptr ? T : 0;
   prm.B = B; prm.N = N; prm.Hq = Hq; prm.Hkv = Hkv; prm.G = G; prm.W = (N + 63) / 64;
-  prm.max_pages = max_pages; prm.num_pages = num_pages; prm.n_groups = n_groups; prm.ranges = pl.ranges;
+  prm.max_pages = max_pages; prm.num_pages = num_pages; prm.n_groups = n_groups;
+  prm.q = static_cast<const uint16_t*>(q);
+  prm.k_cache = static_cast<const uint16_t*>(k_cache);
+  prm.v_cache = static_cast<const uint16_t*>(v_cache);
   prm.rows = static_cast<int>(pl.rows);
   prm.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  jf_status st = JF_OK;
+  if (pl.tile_nt > 0) {
+    prm.kinds = pl.tile_kinds;
+    prm.ranges = pl.tile_ranges;
+    prm.cut0 = pl.tile_cut0;
+    if (D == 128)
+      st = pl.tile_nt == 2 ? launch_tiles<2, 128>(qm, km, vm, kr, vr, prm, s) : launch_tiles<1, 128>(qm, km, vm, kr, vr, prm, s);
+    else
+      st = pl.tile_nt == 2 ? launch_tiles<2, 64>(qm, km, vm, kr, vr, prm, s) : launch_tiles<1, 64>(qm, km, vm, kr, vr, prm, s);
+    if (st != JF_OK) return st;
+  }
+  if (pl.row_mt > 0) {
+    prm.kinds = pl.row_kinds;
+    prm.ranges = pl.row_ranges;
+    prm.cut0 = pl.row_cut0;
+    if (D == 128)
+      st = pl.row_mt == 1 ? launch_rows<128, 1>(prm, s) : (pl.row_mt == 2 ? launch_rows<128, 2>(prm, s) : launch_rows<128, 4>(prm, s));
+    else
+      st = pl.row_mt == 1 ? launch_rows<64, 1>(prm, s) : (pl.row_mt == 2 ? launch_rows<64, 2>(prm, s) : launch_rows<64, 4>(prm, s));
+    if (st != JF_OK) return st;
+  }
   const int total = static_cast<int>(pl.total);
-  if (D == 128)
-    return pl.NT == 2 ? launch_shared<2, 128>(qm, km, vm, kr, vr, prm, total, s)
-                      : launch_shared<1, 128>(qm, km, vm, kr, vr, prm, total, s);
-  return pl.NT == 2 ? launch_shared<2, 64>(qm, km, vm, kr, vr, prm, total, s)
-                    : launch_shared<1, 64>(qm, km, vm, kr, vr, prm, total, s);
+  return D == 128 ? launch_merge<128>(prm, total, s) : launch_merge<64>(prm, total, s);
 }
 
 }  // namespace
@@ -988,7 +1312,7 @@ extern "C" size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, 
   const long long nodes = T > 0 ? T : static_cast<long long>(B) * N;
   if (!jf::shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return static_cast<size_t>(-1);
   const int sms = jf::current_sm_count();
-  return sms > 0 ? jf::plan_shared(nodes, n_groups, Hq, Hkv, D, sms).ws_bytes : static_cast<size_t>(-1);
+  return sms > 0 ? jf::plan_shared(nodes, N, n_groups, Hq, Hkv, D, sms).ws_bytes : static_cast<size_t>(-1);
 }
 
 extern "C" jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache,
