@@ -54,7 +54,7 @@ struct SharedParams {
   int4* ws_desc;     // [2][rows]: first piece's row, pieces, second piece's row, rows from there to the next
   int32_t* dev_err;
   long long T;       // packed nodes
-  const uint16_t *q, *k_cache, *v_cache;     // the row kernel reads them directly
+  const uint16_t* q;
   int B, N, Hq, Hkv, G, W, max_pages, num_pages, n_groups;
   int rows;          // (node, query head) rows
   int kinds;         // units of this launch: kShared, kOwn or both
@@ -799,19 +799,31 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // ------------------------------------------------------------------------ few rows
 
 // Units of few rows (a decode step's G rows of a sequence, the beams of a prompt) are bound by the K/V
-// stream and by the latency of an item, not by matrix products, so a team of MT warps takes a
-// range of its own, 16 rows a warp, with nothing shared and nothing to synchronise: K and V go from
-// global memory to registers as the fragments of 16 x 8 x 16 products, one page of 16 keys a
-// step, the next step's K under way during the softmax and its V during the next scores.  (The
-// warps of a team read the same K and V: the later ones find them in L1.)
-//   Scores: a thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of eight) are two
-//   k-steps' B fragments if Q's chunks are cut the same way: the order of the contraction is free.
-//   Output: column n of n-tile 8 h + j is d = 64 h + 8 n + j, so that a thread's V chunks (8 h' values at
+// stream and by the latency of an item, not by matrix products.  A team of MT warps, 16 rows each,
+// takes a range of its own; a producer warp per team walks the range ahead of it, through item
+// changes too, and keeps a ring of key pages (K and V of 16 keys, by TMA) in flight: 24 pages of
+// 8 KB per SM at D = 128, some 190 KB, where the HBM rate needs about 40.
+//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of
+//   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
+//   contraction is free.
+//   Output: column n of n-tile 8 h + j is d = 64 h + 8 n + j, so that a thread's V chunks (8 values at
 //   64 h + 8 (lane / 4) of keys 2 (lane % 4) + {0, 1, 8, 9}) hold its B fragments, two keys' values
 //   joined by a byte permute, and a thread ends with runs of eight consecutive d.
-constexpr int kRowWarps = 8;
+constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
 template <int MT>
 using RowCut = Cut<16 * MT, 64, 2>;
+
+template <int D, int MT>
+struct RowCfg {
+  static constexpr int kTeams = kRowWarps / MT;
+  static constexpr int kHalves = D / 64;                      // 128-byte swizzle atoms per row
+  static constexpr int kHalfBytes = kPage * 128;              // one 64-column half of a page
+  static constexpr int kStageBytes = 2 * kHalves * kHalfBytes;     // K, then V
+  static constexpr int kStages = 24 * 8192 / kStageBytes / kTeams;
+  static constexpr int kPosts = 32;                           // piece slots: kStages + 2 at least
+  static_assert(kPosts >= kStages + 2, "a piece is read until its last step's successor ring is full");
+  static constexpr int kSmemBytes = kTeams * kStages * kStageBytes + 1024;
+};
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -822,176 +834,240 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(32 * kRowWarps, 1) shared_rows_kernel(const __grid_constant__ SharedParams p) {
+__global__ void __launch_bounds__(64 * kRowWarps, 1)
+    shared_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ SharedParams p) {
   using X = RowCut<MT>;
-  constexpr int kTeams = kRowWarps / MT;
+  using C = RowCfg<D, MT>;
+  constexpr int kTeams = C::kTeams, kS = C::kStages;
   constexpr int kI = D / 32;            // 16-byte chunks of a row per thread (scores)
-  constexpr int kH = D / 64;            // 16-byte chunks of a V row per thread
-  extern __shared__ int s_scratch[];
+  constexpr int kH = C::kHalves;
+  constexpr uint64_t wlim = kWaitLimitNs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
   __shared__ Schedule s_sch[kTeams];
-  if (p.kinds & kShared) {
-    grid_dependency_wait();
-  }                                     // else: beside the shared parts' kernel, which waited (see below)
+  __shared__ Piece s_post[kTeams][C::kPosts];
+  __shared__ uint64_t s_full[kTeams][kS], s_empty[kTeams][kS];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < kTeams; ++t)
+      for (int st = 0; st < kS; ++st) {
+        mbar_init(&s_full[t][st], 1);
+        mbar_init(&s_empty[t][st], MT);
+      }
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (p.kinds & kShared) grid_dependency_wait();    // else: beside the shared parts' kernel, which waited (see below)
   grid_dependents_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int team = warp / MT, tw = warp % MT;
-  const int v = blockIdx.x * kTeams + team;
   make_schedule<X, kTeams>(p, blockIdx.x * kTeams, blockIdx.x == 0 && p.kinds == (kShared | kOwn) ? p.dev_err : nullptr,
-                           s_scratch, s_sch);
+                           reinterpret_cast<int*>(sm), s_sch);
+  fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
   __syncthreads();
-  const Schedule& sch = s_sch[team];
-  if (sch.tiles > 0) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // 512 threads x 128 registers at launch: 56 * 256 + 200 * 256 = 128 * 512.
+  if (warp >= kRowWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // ================================================================ producers
+    const int team = warp - kRowWarps;
+    if (team < kTeams && s_sch[team].tiles > 0) {
+      const Schedule& sch = s_sch[team];
+      uint8_t* ring = sm + team * kS * C::kStageBytes;
+      int it = 0, posted = 0, bad = 0;
+      bool ok = true;
+      auto free_stage = [&] {           // lane 0: the stage of step `it` has been read by the whole team
+        return it < kS || mbar_wait(&s_empty[team][it % kS], static_cast<uint32_t>(it / kS - 1) & 1u, abort, wlim);
+      };
+      for (Walk<X> w(p, sch); w.live() && ok; w.next()) {
+        const int first = w.t.key0 + w.k0 * X::KT, end = min(w.t.L, w.t.key0 + w.k1 * X::KT);
+        const int steps = (end - first + kPage - 1) / kPage;
+        const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages + first / kPage;
+        int ids = p.num_pages;          // lane l: the page of step 32 * k + l
+        for (int s = 0; s < steps; ++s) {
+          if ((s & 31) == 0 && s + lane < steps) {
+            ids = __ldg(bt + s + lane);
+            if (ids < 0 || ids >= p.num_pages) {
+              ids = p.num_pages;        // out of bounds: TMA fills zeros
+              bad = 1;
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, s & 31);
+          int go = 1;
+          if (lane == 0) {
+            go = free_stage() ? 1 : 0;
+            if (go) {
+              if (s == 0) s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x * kTeams + team);
+              mbar_arrive_expect_tx(&s_full[team][it % kS], C::kStageBytes);
+            }
+          }
+          if (!__shfl_sync(0xffffffffu, go, 0)) {
+            ok = false;
+            break;
+          }
+          if (lane < 2 * kH) {          // K halves, then V halves
+            const int h = lane % kH;
+            tma_load_3d(ring + (it % kS) * C::kStageBytes + lane * C::kHalfBytes, lane < kH ? &kmap : &vmap,
+                        &s_full[team][it % kS], h * 64, w.g, page * kPage);
+          }
+          ++it;
+        }
+        ++posted;
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_err, JF_DEVERR_BAD_PAGE);
+      if (lane == 0) {
+        // No copy may still be landing when the block exits (before the end's phase: a barrier tells
+        // only its last phase).
+        int zero = 0;
+        for (int j = max(0, it - kS); j < it; ++j)
+          ok = mbar_wait(&s_full[team][j % kS], static_cast<uint32_t>(j / kS) & 1u, &zero) && ok;
+        if (ok && free_stage()) {       // the end: a piece without tiles, on a stage without data
+          s_post[team][posted % C::kPosts].T = 0;
+          mbar_arrive(&s_full[team][it % kS]);
+        } else {
+          set_abort(abort, p.dev_err);
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ================================================================ the teams
+    const int team = warp / MT, tw = warp % MT;
     const int q4 = lane & 3, r8 = lane >> 2;
-    int bad = 0;
-    for (Walk<X> w(p, sch); w.live(); w.next()) {
-      const Piece c = w.piece(sch, v);
-      if (tw * 16 >= c.nrows) continue;              // this warp has none of the item's rows
+    const uint8_t* ring = sm + team * kS * C::kStageBytes;
+    bool ok = s_sch[team].tiles > 0;
+    int it = 0;
+    for (int post = 0; ok; ++post) {
+      if (!wait_warp(&s_full[team][it % kS], static_cast<uint32_t>(it / kS) & 1u, abort, wlim)) break;
+      const Piece& c = s_post[team][post % C::kPosts];
+      const int T = c.T;
+      if (T == 0) break;
+      const int first = c.first, P = c.P, end = min(c.L, first + T * X::KT);
+      const int steps = (end - first + kPage - 1) / kPage;
       const int ra = tw * 16 + r8, rb = ra + 8;      // the thread's rows of the item
-      const bool va = ra < c.nrows, vb = rb < c.nrows;
+      const bool va = ra < c.nrows, vb = rb < c.nrows, some = tw * 16 < c.nrows;
       const int na = c.node0 + (va ? ra / p.G : 0), nb = c.node0 + (vb ? rb / p.G : 0);
-      const int rowa = na * p.Hq + c.g * p.G + ra % p.G, rowb = nb * p.Hq + c.g * p.G + rb % p.G;
       uint4 qa[kI], qb[kI];
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
         const int ch = q4 + 4 * i;
-        qa[i] = va ? reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(rowa) * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
-        qb[i] = vb ? reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(rowb) * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
+        const size_t rowa = static_cast<size_t>(na) * p.Hq + c.g * p.G + ra % p.G;
+        const size_t rowb = static_cast<size_t>(nb) * p.Hq + c.g * p.G + rb % p.G;
+        qa[i] = va ? reinterpret_cast<const uint4*>(p.q + rowa * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
+        qb[i] = vb ? reinterpret_cast<const uint4*>(p.q + rowb * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
       }
-      const int end = min(c.L, c.first + c.T * X::KT);
-      const int steps = (end - c.first + kPage - 1) / kPage;
-      const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages + c.first / kPage;
-      const bool split = c.P < kSplitPrefix;         // rows with few keys: probabilities in two bf16 parts
+      const bool split = P < kSplitPrefix;           // rows with few keys: probabilities in two bf16 parts
       float o[8 * kH][4];
 #pragma unroll
       for (int j = 0; j < 8 * kH; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
-      int ids = -1;                                  // lane l: the page of step 32 * k + l
-      auto page_of = [&](int s) -> int {
-        if ((s & 31) == 0) {
-          ids = -1;
-          if (s + lane < steps) {
-            ids = __ldg(bt + s + lane);
-            if (ids < 0 || ids >= p.num_pages) {
-              ids = -1;
-              bad = 1;
+      for (int s = 0; s < steps; ++s, ++it) {
+        if (s > 0 && !wait_warp(&s_full[team][it % kS], static_cast<uint32_t>(it / kS) & 1u, abort, wlim)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* kt = ring + (it % kS) * C::kStageBytes;
+        const uint8_t* vt = kt + kH * C::kHalfBytes;
+        const int key0 = first + s * kPage;
+        if (some) {                                  // warp-uniform
+          float x[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              const int ch = q4 + 4 * i;
+              const uint4 kr = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + r8) * 128 +
+                                                               (((ch & 7) ^ r8) << 4));
+              mma_16816(x[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr.x, kr.y);
+              mma_16816(x[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr.z, kr.w);
             }
           }
-        }
-        return __shfl_sync(0xffffffffu, ids, s & 31);
-      };
-      uint4 kr[2][kI], vr[4][kH];
-      auto load_k = [&](int s, int page) {
-        const int key0 = c.first + s * kPage;
+          if (key0 + kPage > P) {                    // tree keys, or keys past the end
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const bool in = page >= 0 && key0 + 8 * t + r8 < end;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.k_cache + ((static_cast<size_t>(max(page, 0)) * kPage + 8 * t + r8) * p.Hkv + c.g) * D);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int i = 0; i < kI; ++i) kr[t][i] = in ? src[q4 + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      auto load_v = [&](int s, int page) {           // keys past the end: zero (their probability is, too)
-        const int key0 = c.first + s * kPage;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
-          const bool in = page >= 0 && key0 + key < end;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.v_cache + ((static_cast<size_t>(max(page, 0)) * kPage + key) * p.Hkv + c.g) * D);
-#pragma unroll
-          for (int h = 0; h < kH; ++h) vr[t][h] = in ? src[r8 + 8 * h] : make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      int page = page_of(0);
-      load_k(0, page);
-      load_v(0, page);
-      for (int s = 0; s < steps; ++s) {
-        float x[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
-#pragma unroll
-          for (int i = 0; i < kI; ++i) {
-            mma_16816(x[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[t][i].x, kr[t][i].y);
-            mma_16816(x[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[t][i].z, kr[t][i].w);
-          }
-        }
-        const int key0 = c.first + s * kPage;
-        page = -1;
-        if (s + 1 < steps) {
-          page = page_of(s + 1);
-          load_k(s + 1, page);
-        }
-        if (key0 + kPage > c.P) {                    // tree keys, or keys past the end
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = key0 + 8 * t + 2 * q4 + e, j = key - c.P;
-              bool sa = key < end, sb = sa;
-              if (sa && j >= 0) {
-                sa = va && c.b >= 0 && ((p.mask[static_cast<size_t>(na) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
-                sb = vb && c.b >= 0 && ((p.mask[static_cast<size_t>(nb) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
+              for (int e = 0; e < 2; ++e) {
+                const int key = key0 + 8 * t + 2 * q4 + e, j = key - P;
+                bool sa = key < end, sb = sa;
+                if (sa && j >= 0) {
+                  sa = va && c.b >= 0 && ((p.mask[static_cast<size_t>(na) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
+                  sb = vb && c.b >= 0 && ((p.mask[static_cast<size_t>(nb) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
+                }
+                if (!sa) x[t][e] = -INFINITY;
+                if (!sb) x[t][2 + e] = -INFINITY;
               }
-              if (!sa) x[t][e] = -INFINITY;
-              if (!sb) x[t][2 + e] = -INFINITY;
+          }
+          float ta = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          float tb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+#pragma unroll
+          for (int k = 1; k < 4; k <<= 1) {
+            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, k));
+            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, k));
+          }
+          ta *= p.scale_log2;
+          tb *= p.scale_log2;
+          // The running maximum rises only by more than 2^8 (see jf_attention.cu): O is rescaled rarely.
+          const bool ua = ta > ma + kRescaleThreshold, ub = tb > mb + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, ua || ub)) {
+            const float fa = ua ? fast_exp2(ma - ta) : 1.f, fb = ub ? fast_exp2(mb - tb) : 1.f;
+            if (ua) ma = ta;
+            if (ub) mb = tb;
+            la *= fa;
+            lb *= fb;
+#pragma unroll
+            for (int j = 0; j < 8 * kH; ++j) {
+              o[j][0] *= fa; o[j][1] *= fa;
+              o[j][2] *= fb; o[j][3] *= fb;
             }
-        }
-        float ta = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float tb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+          }
+          const float oa = ma == -INFINITY ? 0.f : -ma, ob = mb == -INFINITY ? 0.f : -mb;
+          uint32_t pa[4], pl[4];                     // the A fragment of the probabilities, and of their rest
 #pragma unroll
-        for (int k = 1; k < 4; k <<= 1) {
-          ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, k));
-          tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, k));
-        }
-        ta *= p.scale_log2;
-        tb *= p.scale_log2;
-        // The running maximum rises only by more than 2^8 (see jf_attention.cu): O is rescaled rarely.
-        const bool ua = ta > ma + kRescaleThreshold, ub = tb > mb + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, ua || ub)) {
-          const float fa = ua ? fast_exp2(ma - ta) : 1.f, fb = ub ? fast_exp2(mb - tb) : 1.f;
-          if (ua) ma = ta;
-          if (ub) mb = tb;
-          la *= fa;
-          lb *= fb;
+          for (int t = 0; t < 2; ++t) {
+            const float y0 = fast_exp2(fmaf(x[t][0], p.scale_log2, oa)), y1 = fast_exp2(fmaf(x[t][1], p.scale_log2, oa));
+            const float z0 = fast_exp2(fmaf(x[t][2], p.scale_log2, ob)), z1 = fast_exp2(fmaf(x[t][3], p.scale_log2, ob));
+            la += y0 + y1;
+            lb += z0 + z1;
+            pa[2 * t] = pack_bf16x2(y0, y1);
+            pa[2 * t + 1] = pack_bf16x2(z0, z1);
+            pl[2 * t] = pl[2 * t + 1] = 0u;
+            if (split) {
+              pl[2 * t] = pack_bf16x2(y0 - __uint_as_float(pa[2 * t] << 16), y1 - __uint_as_float(pa[2 * t] & 0xFFFF0000u));
+              pl[2 * t + 1] = pack_bf16x2(z0 - __uint_as_float(pa[2 * t + 1] << 16), z1 - __uint_as_float(pa[2 * t + 1] & 0xFFFF0000u));
+            }
+          }
 #pragma unroll
-          for (int j = 0; j < 8 * kH; ++j) {
-            o[j][0] *= fa; o[j][1] *= fa;
-            o[j][2] *= fb; o[j][3] *= fb;
+          for (int h = 0; h < kH; ++h) {
+            uint4 vr[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {            // keys past the end: zero (their probability is, too)
+              const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
+              vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((r8 ^ (key & 7)) << 4));
+              if (key0 + key >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t w0 = j < 2 ? vr[0].x : (j < 4 ? vr[0].y : (j < 6 ? vr[0].z : vr[0].w));
+              const uint32_t w1 = j < 2 ? vr[1].x : (j < 4 ? vr[1].y : (j < 6 ? vr[1].z : vr[1].w));
+              const uint32_t w2 = j < 2 ? vr[2].x : (j < 4 ? vr[2].y : (j < 6 ? vr[2].z : vr[2].w));
+              const uint32_t w3 = j < 2 ? vr[3].x : (j < 4 ? vr[3].y : (j < 6 ? vr[3].z : vr[3].w));
+              const uint32_t b0 = __byte_perm(w0, w1, j & 1 ? 0x7632 : 0x5410);
+              const uint32_t b1 = __byte_perm(w2, w3, j & 1 ? 0x7632 : 0x5410);
+              mma_16816(o[8 * h + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
+              if (split) mma_16816(o[8 * h + j], pl[0], pl[1], pl[2], pl[3], b0, b1);
+            }
           }
         }
-        const float oa = ma == -INFINITY ? 0.f : -ma, ob = mb == -INFINITY ? 0.f : -mb;
-        uint32_t pa[4], pl[4];                       // the A fragment of the probabilities, and of their rest
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float y0 = fast_exp2(fmaf(x[t][0], p.scale_log2, oa)), y1 = fast_exp2(fmaf(x[t][1], p.scale_log2, oa));
-          const float z0 = fast_exp2(fmaf(x[t][2], p.scale_log2, ob)), z1 = fast_exp2(fmaf(x[t][3], p.scale_log2, ob));
-          la += y0 + y1;
-          lb += z0 + z1;
-          pa[2 * t] = pack_bf16x2(y0, y1);
-          pa[2 * t + 1] = pack_bf16x2(z0, z1);
-          if (split) {
-            pl[2 * t] = pack_bf16x2(y0 - __uint_as_float(pa[2 * t] << 16), y1 - __uint_as_float(pa[2 * t] & 0xFFFF0000u));
-            pl[2 * t + 1] = pack_bf16x2(z0 - __uint_as_float(pa[2 * t + 1] << 16), z1 - __uint_as_float(pa[2 * t + 1] & 0xFFFF0000u));
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t w0 = j < 2 ? vr[0][h].x : (j < 4 ? vr[0][h].y : (j < 6 ? vr[0][h].z : vr[0][h].w));
-            const uint32_t w1 = j < 2 ? vr[1][h].x : (j < 4 ? vr[1][h].y : (j < 6 ? vr[1][h].z : vr[1][h].w));
-            const uint32_t w2 = j < 2 ? vr[2][h].x : (j < 4 ? vr[2][h].y : (j < 6 ? vr[2][h].z : vr[2][h].w));
-            const uint32_t w3 = j < 2 ? vr[3][h].x : (j < 4 ? vr[3][h].y : (j < 6 ? vr[3][h].z : vr[3][h].w));
-            const uint32_t b0 = __byte_perm(w0, w1, j & 1 ? 0x7632 : 0x5410);
-            const uint32_t b1 = __byte_perm(w2, w3, j & 1 ? 0x7632 : 0x5410);
-            mma_16816(o[8 * h + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
-            if (split) mma_16816(o[8 * h + j], pl[0], pl[1], pl[2], pl[3], b0, b1);
-          }
-        }
-        if (s + 1 < steps) load_v(s + 1, page);
+        __syncwarp();                                // every lane has read the stage
+        if (lane == 0) mbar_arrive(&s_empty[team][it % kS]);
       }
+      if (!ok) break;
 #pragma unroll
       for (int k = 1; k < 4; k <<= 1) {
         la += __shfl_xor_sync(0xffffffffu, la, k);
@@ -1000,10 +1076,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) shared_rows_kernel(const __
       // ---- the piece's rows
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const bool ok = half == 0 ? va : vb;
-        const int r = half == 0 ? ra : rb, row = half == 0 ? rowa : rowb;
+        const bool mine = half == 0 ? va : vb;
+        const int r = half == 0 ? ra : rb;
+        const int row = (half == 0 ? na : nb) * p.Hq + c.g * p.G + r % p.G;
         const float l = half == 0 ? la : lb, m = half == 0 ? ma : mb;
-        if (!ok) continue;
+        if (!mine) continue;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
         const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
@@ -1027,7 +1104,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 1) shared_rows_kernel(const __
         if (q4 == 0) write_row_facts(p, c, row, prow, r, lse2, 2 * X::R);
       }
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_err, JF_DEVERR_BAD_PAGE);
+    if (!ok && s_sch[team].tiles > 0 && lane == 0) set_abort(abort, p.dev_err);
   }
   // A launch of own parts alone runs beside the shared parts' kernel (which lets it start once all its
   // CTAs have seen their inputs): it must not be complete before that one is, for what follows
@@ -1196,13 +1273,13 @@ jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUten
 }
 
 template <int D, int MT>
-jf_status launch_rows(const SharedParams& prm, cudaStream_t s) {
-  constexpr int kMost = 4 * (5 * kSharedMaxB + 1);
+jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const SharedParams& prm, cudaStream_t s) {
+  using C = RowCfg<D, MT>;
+  static_assert(C::kSmemBytes >= 4 * (5 * kSharedMaxB + 1), "the schedule's scratch fits");
   static SmemAttr attr;
-  if (!attr.ensure(shared_rows_kernel<D, MT>, kMost)) return JF_ERR_CUDA;
-  const size_t smem = 4 * (3 * static_cast<size_t>(prm.n_groups) + 2 * static_cast<size_t>(prm.B) + 1);
-  return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / (kRowWarps / MT))),
-                    dim3(32 * kRowWarps), smem, s, prm) == cudaSuccess
+  if (!attr.ensure(shared_rows_kernel<D, MT>, C::kSmemBytes)) return JF_ERR_CUDA;
+  return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / C::kTeams)),
+                    dim3(64 * kRowWarps), C::kSmemBytes, s, km, vm, prm) == cudaSuccess
              ? JF_OK
              : JF_ERR_CUDA;
 }
@@ -1273,8 +1350,6 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   prm.B = B; prm.N = N; prm.Hq = Hq; prm.Hkv = Hkv; prm.G = G; prm.W = (N + 63) / 64;
   prm.max_pages = max_pages; prm.num_pages = num_pages; prm.n_groups = n_groups;
   prm.q = static_cast<const uint16_t*>(q);
-  prm.k_cache = static_cast<const uint16_t*>(k_cache);
-  prm.v_cache = static_cast<const uint16_t*>(v_cache);
   prm.rows = static_cast<int>(pl.rows);
   prm.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1294,9 +1369,9 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
     prm.ranges = pl.row_ranges;
     prm.cut0 = pl.row_cut0;
     if (D == 128)
-      st = pl.row_mt == 1 ? launch_rows<128, 1>(prm, s) : (pl.row_mt == 2 ? launch_rows<128, 2>(prm, s) : launch_rows<128, 4>(prm, s));
+      st = pl.row_mt == 1 ? launch_rows<128, 1>(km, vm, prm, s) : (pl.row_mt == 2 ? launch_rows<128, 2>(km, vm, prm, s) : launch_rows<128, 4>(km, vm, prm, s));
     else
-      st = pl.row_mt == 1 ? launch_rows<64, 1>(prm, s) : (pl.row_mt == 2 ? launch_rows<64, 2>(prm, s) : launch_rows<64, 4>(prm, s));
+      st = pl.row_mt == 1 ? launch_rows<64, 1>(km, vm, prm, s) : (pl.row_mt == 2 ? launch_rows<64, 2>(km, vm, prm, s) : launch_rows<64, 4>(km, vm, prm, s));
     if (st != JF_OK) return st;
   }
   const int total = static_cast<int>(pl.total);
