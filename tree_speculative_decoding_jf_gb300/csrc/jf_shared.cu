@@ -27,6 +27,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "jf_attention.cuh"
 #include "jf_common.cuh"
@@ -120,16 +121,17 @@ struct Schedule {
   }
 };
 
-// The ranges v0 .. v0 + TEAMS - 1 of the launch.  Every thread of the block calls it; scratch: 4 * (3 *
+// The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it; scratch: 4 * (3 *
 // n_groups + 2 * B + 1) bytes at least.  Unit order: group by group, its shared part (if any), then
 // its sequences.  Units of kinds that the launch does not do cost nothing.
 template <typename X, int TEAMS>
-__device__ __noinline__ void make_schedule(const SharedParams& p, int v0, int32_t* err, int* scratch, Schedule* out) {
+__device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int vstep, int32_t* err, int* scratch,
+                                              Schedule* out) {
   const int ng = p.n_groups, B = p.B, U = ng + B, tid = threadIdx.x, nth = blockDim.x;
   int* gs = scratch;                 // [ng + 1]
   int* cost = gs + ng + 1;           // [U] positions of the unit
   int* items = cost + U;             // [U]
-  __shared__ long long s_scan[32];
+  __shared__ int s_scan[32];
   __shared__ int s_items[32];
   __shared__ int s_before[TEAMS][2]; // tiles before a range's ends: the position less SW per item completed
   for (int u = tid; u <= ng; u += nth) gs[u] = p.group_start[u];
@@ -183,32 +185,29 @@ __device__ __noinline__ void make_schedule(const SharedParams& p, int v0, int32_
   // Block-wide sums over contiguous chunks of units.
   const int chunk = (U + nth - 1) / nth;
   const int e0 = min(U, tid * chunk), e1 = min(U, e0 + chunk);
-  long long mine = 0;
-  int mine_items = 0;
+  int mine = 0, mine_items = 0;      // positions are 32-bit (a limit of the call)
   for (int e = e0; e < e1; ++e) mine += cost[e], mine_items += items[e];
-  long long upto = mine;
-  int upto_items = mine_items;
+  int upto = mine, upto_items = mine_items;
   const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
     const int z = __shfl_up_sync(0xffffffffu, upto_items, o);
     if (lane >= o) upto += y, upto_items += z;
   }
   if (lane == 31) s_scan[warp] = upto, s_items[warp] = upto_items;
   __syncthreads();
-  long long total = 0;
-  int total_items = 0;
+  int total = 0, total_items = 0;
   for (int w = 0; w < (nth + 31) / 32; ++w) {
     if (w < warp) upto += s_scan[w], upto_items += s_items[w];
     total += s_scan[w];
     total_items += s_items[w];
   }
-  const int q = static_cast<int>(total / p.ranges), rem = static_cast<int>(total - static_cast<long long>(q) * p.ranges);
-  const int first = static_cast<int>(upto - mine), last = static_cast<int>(upto);
+  const int q = total / p.ranges, rem = total - q * p.ranges;
+  const int first = upto - mine, last = upto;
   for (int k = 0; k < 2 * TEAMS; ++k) {
-    const int v = v0 + (k >> 1) + (k & 1), x = v * q + min(v, rem);      // start of range v0 + k / 2, or its end
-    if (x >= total && tid == 0 && (k & 1)) s_before[k >> 1][1] = static_cast<int>(total) - X::SW * total_items;
+    const int v = v0 + (k >> 1) * vstep + (k & 1), x = v * q + min(v, rem);      // start of the team's range, or its end
+    if (x >= total && tid == 0 && (k & 1)) s_before[k >> 1][1] = total - X::SW * total_items;
     if (x < first || x >= last) continue;        // the position lies in another thread's chunk
     int at = first, done = upto_items - mine_items, e = e0;
     while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
@@ -226,7 +225,7 @@ __device__ __noinline__ void make_schedule(const SharedParams& p, int v0, int32_
   }
   __syncthreads();
   if (tid < TEAMS) {
-    const int v = v0 + tid;
+    const int v = v0 + tid * vstep;
     Schedule& o = out[tid];
     o.lo = v * q + min(v, rem);
     o.hi = (v + 1) * q + min(v + 1, rem);
@@ -296,13 +295,10 @@ struct Walk {
     g = item / t.mpc;
     mp = item - g * t.mpc;
     x = lo - (s.off - item * per);
-    settle();
+    settle(false);
   }
   __device__ __forceinline__ bool live() const { return x < hi; }
-  __device__ __forceinline__ void next() {
-    advance();
-    settle();
-  }
+  __device__ __forceinline__ void next() { settle(true); }
   __device__ __forceinline__ Piece piece(const Schedule& s, int v) const {
     constexpr int R = X::R;
     Piece c;
@@ -331,17 +327,28 @@ struct Walk {
   }
 
  private:
-  // The first piece at or after the current item (a range may start or end in an item's switch).
-  __device__ __forceinline__ void settle() {
-    while (x < hi) {
+  // The first piece at or after the current item, or after it (a range may start or end in an item's
+  // switch).
+  __device__ __forceinline__ void settle(bool move) {
+    for (;; move = true) {
+      if (move) {
+        x += t.T + X::SW;
+        if (++mp >= t.mpc) {
+          mp = 0;
+          if (++g >= p.Hkv) {
+            g = 0;
+            if (x < hi) next_unit();
+          }
+        }
+      }
+      if (x >= hi) return;
       k0 = max(lo - x, 0);
       k1 = min(hi - x, t.T);
       if (k0 < k1) return;
-      advance();
     }
   }
-  __device__ __noinline__ void next_unit() {
-    for (;;) {
+  __device__ __forceinline__ void next_unit() {
+    do {
       b = b < 0 ? b0 : b + 1;
       if (!(p.kinds & kOwn)) b = b1;     // shared parts alone: on to the next group
       while (b >= b1) {
@@ -355,16 +362,7 @@ struct Walk {
         b = S > 0 && (p.kinds & kShared) ? -1 : ((p.kinds & kOwn) ? b0 : b1);
       }
       t = make_unit<X>(p, b, b0, b1, S);
-      if (t.T > 0) return;
-    }
-  }
-  __device__ __forceinline__ void advance() {
-    x += t.T + X::SW;
-    if (++mp < t.mpc) return;
-    mp = 0;
-    if (++g < p.Hkv) return;
-    g = 0;
-    if (x < hi) next_unit();
+    } while (t.T == 0);
   }
 };
 
@@ -443,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
   }
   grid_dependency_wait();
   grid_dependents_launch();             // the own parts' kernel may run beside this one; others wait for it
-  make_schedule<TileCut<NT>, 1>(p, v, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
+  make_schedule<TileCut<NT>, 1>(p, v, 1, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
   fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
   if (warp == 1) {
     tmem_alloc(&tmem_slot, C::kTmemCols);
@@ -864,7 +862,8 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
   }
   if (p.kinds & kShared) grid_dependency_wait();    // else: beside the shared parts' kernel, which waited (see below)
   grid_dependents_launch();
-  make_schedule<X, kTeams>(p, blockIdx.x * kTeams, blockIdx.x == 0 && p.kinds == (kShared | kOwn) ? p.dev_err : nullptr,
+  // (Consecutive ranges lie on different SMs: small calls reach them all.)
+  make_schedule<X, kTeams>(p, blockIdx.x, gridDim.x, blockIdx.x == 0 && p.kinds == (kShared | kOwn) ? p.dev_err : nullptr,
                            reinterpret_cast<int*>(sm), s_sch);
   fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
   __syncthreads();
@@ -901,7 +900,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
           if (lane == 0) {
             go = free_stage() ? 1 : 0;
             if (go) {
-              if (s == 0) s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x * kTeams + team);
+              if (s == 0) s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
               mbar_arrive_expect_tx(&s_full[team][it % kS], C::kStageBytes);
             }
           }
@@ -1114,81 +1113,141 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 
 // ------------------------------------------------------------------------ the merge
 
-// One warp per (node, query head) row: the pieces of its shared and own parts, listed by ws_desc,
-// merged by log-sum-exp.  Four pieces' rows are requested together.  What ws_desc says is
-// checked against the workspace: a malformed group_start leaves it unwritten.
-template <int D>
+// The pieces of a (node, query head) row's shared and own parts, listed by ws_desc, merged by
+// log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap; ROWS == 1, for few rows:
+// a block merges one, its warps taking every eighth piece.  What ws_desc says is checked against
+// the workspace: a malformed group_start leaves it unwritten.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
   constexpr int E = D / 32;
-  constexpr int kBatch = 4;
+  constexpr int kWarps = 8;
+  constexpr int kStep = ROWS == 1 ? kWarps : 1;       // pieces a warp skips
+  constexpr int kBatch = ROWS == 1 ? 4 : 2;           // pieces of a row whose reads overlap
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ float s_part[ROWS == 1 ? kWarps : 1][D + 2];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x & 31;
-  const long long rr = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (rr >= static_cast<long long>(p.B) * p.N * p.Hq) return;
-  const int h = static_cast<int>(rr % p.Hq);
-  const long long bi = rr / p.Hq;
-  const int i = static_cast<int>(bi % p.N), b = static_cast<int>(bi / p.N);
-  const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
-  if (i >= sp.n) return;
-  const int row = static_cast<int>(sp.row0 + i) * p.Hq + h;
-  const int4 da = p.ws_desc[row], db = p.ws_desc[p.rows + row];
-  if (db.y == 0) return;                         // written by its only piece
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long all = static_cast<long long>(p.B) * p.N * p.Hq;
+  const long long r0 = ROWS == 1 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * kWarps + warp) * ROWS;
+  int row[ROWS], n[ROWS];
+  int4 da[ROWS], db[ROWS];
+  long long out_lse[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const long long rr = r0 + k;
+    row[k] = -1;
+    if (rr < all) {
+      const int h = static_cast<int>(rr % p.Hq);
+      const int bi = static_cast<int>(rr / p.Hq), i = bi % p.N, b = bi / p.N;
+      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+      if (i < sp.n) {
+        row[k] = static_cast<int>(sp.row0 + i) * p.Hq + h;
+        out_lse[k] = static_cast<long long>(lse_index(p.cu != nullptr, sp.row0, p.T, b, h, i, p.Hq, p.N));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    da[k] = db[k] = make_int4(0, 0, 0, 0);
+    if (row[k] >= 0) {
+      da[k] = p.ws_desc[row[k]];
+      db[k] = p.ws_desc[p.rows + row[k]];
+    }
+  }
   auto bad = [&](const int4& d) {
     return d.y < 0 || d.y > total || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
            (d.y > 1 && (d.z < 0 || d.w < 0 || d.z + static_cast<long long>(d.y - 2) * d.w >= total));
   };
-  if (bad(da) || bad(db)) return;
-  const int n = da.y + db.y;
-  auto piece = [&](int k) {                      // workspace row of piece k
-    const int4& d = k < da.y ? da : db;
-    const int at = k < da.y ? k : k - da.y;
-    return at == 0 ? d.x : d.z + (at - 1) * d.w;
+  auto piece = [&](const int4& a, const int4& b, int k) {      // workspace row of piece k
+    const int at = k < a.y ? k : k - a.y;
+    const int x = k < a.y ? a.x : b.x, z = k < a.y ? a.z : b.z, w = k < a.y ? a.w : b.w;
+    return at == 0 ? x : z + (at - 1) * w;
   };
-  float mx = -INFINITY;
-  for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.ws_lse[piece(k)]);
+  float acc[ROWS][E], m[ROWS], sum[ROWS];
+  int most = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float acc[E];
+  for (int k = 0; k < ROWS; ++k) {
+    // db.y == 0: written by its only piece
+    n[k] = row[k] >= 0 && db[k].y != 0 && !bad(da[k]) && !bad(db[k]) ? da[k].y + db[k].y : 0;
+    most = max(most, n[k]);
+    m[k] = -INFINITY;
+    sum[k] = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float sum = 0.f;
-  for (int k0 = 0; k0 < n; k0 += kBatch) {
-    float l[kBatch], x[kBatch][E];
+    for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+  }
+  for (int j0 = ROWS == 1 ? warp : 0; j0 < most; j0 += kBatch * kStep) {
+    float l[ROWS][kBatch];
+    Vec x[ROWS][kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      l[k] = -INFINITY;
-      if (k0 + k < n) {
-        const int at = piece(k0 + k);
-        l[k] = p.ws_lse[at];
-        const float* src = p.ws_o + static_cast<size_t>(at) * D + lane * E;
+    for (int k = 0; k < ROWS; ++k)
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src + e);
-          x[k][e] = y.x;
-          x[k][e + 1] = y.y;
+      for (int j = 0; j < kBatch; ++j) {
+        l[k][j] = -INFINITY;
+        if (j0 + j * kStep < n[k]) {
+          const int at = piece(da[k], db[k], j0 + j * kStep);
+          l[k][j] = p.ws_lse[at];
+          x[k][j] = *reinterpret_cast<const Vec*>(p.ws_o + static_cast<size_t>(at) * D + lane * E);
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (l[k] == -INFINITY) continue;           // no such piece, or it saw nothing
-      const float f = exp2f(l[k] - mx);
-      sum += f;
+    for (int k = 0; k < ROWS; ++k) {
+      float top = m[k];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, x[k][e], acc[e]);
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, l[k][j]);
+      if (top == -INFINITY) continue;            // nothing yet that saw a key
+      const float f0 = m[k] == -INFINITY ? 0.f : exp2f(m[k] - top);
+      m[k] = top;
+      sum[k] *= f0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[k][e] *= f0;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (l[k][j] == -INFINITY) continue;
+        const float f = exp2f(l[k][j] - top);
+        const float* xs = reinterpret_cast<const float*>(&x[k][j]);
+        sum[k] += f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[k][e] = fmaf(f, xs[e], acc[k][e]);
+      }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t y[E / 2];
+  if constexpr (ROWS == 1) {
+    if (n[0] == 0) return;                       // block-uniform
 #pragma unroll
-  for (int e = 0; e < E; e += 2) y[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  uint16_t* dst = p.out + static_cast<size_t>(row) * D + lane * E;
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
-  else *reinterpret_cast<uint32_t*>(dst) = y[0];
-  if (p.lse != nullptr && lane == 0)
-    p.lse[lse_index(p.cu != nullptr, sp.row0, p.T, b, h, i, p.Hq, p.N)] =
-        (sum > 0.f ? mx + __log2f(sum) : -INFINITY) * 0.69314718055994531f;
+    for (int e = 0; e < E; ++e) s_part[warp][lane * E + e] = acc[0][e];
+    if (lane == 0) s_part[warp][D] = m[0], s_part[warp][D + 1] = sum[0];
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_part[w][D]);
+    m[0] = top;
+    sum[0] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[0][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (s_part[w][D] == -INFINITY) continue;
+      const float f = exp2f(s_part[w][D] - top);
+      sum[0] = fmaf(f, s_part[w][D + 1], sum[0]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[0][e] = fmaf(f, s_part[w][lane * E + e], acc[0][e]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    if (n[k] == 0) continue;
+    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    uint32_t y[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) y[e / 2] = pack_bf16x2(acc[k][e] * inv, acc[k][e + 1] * inv);
+    uint16_t* dst = p.out + static_cast<size_t>(row[k]) * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = y[0];
+    if (p.lse != nullptr && lane == 0)
+      p.lse[out_lse[k]] = (sum[k] > 0.f ? m[k] + __log2f(sum[k]) : -INFINITY) * 0.69314718055994531f;
+  }
 }
 
 // ------------------------------------------------------------------------ host side
@@ -1285,12 +1344,14 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 }
 
 template <int D>
-jf_status launch_merge(const SharedParams& prm, int total, cudaStream_t s) {
-  const long long warps = static_cast<long long>(prm.B) * prm.N * prm.Hq;
-  return launch_pdl(shared_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, s, prm, total) ==
-                 cudaSuccess
-             ? JF_OK
-             : JF_ERR_CUDA;
+jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
+  // A block a row while that keeps the SMs less than eight blocks deep, else two rows a warp.
+  const long long rows = static_cast<long long>(prm.B) * prm.N * prm.Hq;
+  const cudaError_t e =
+      rows <= 8ll * sms
+          ? launch_pdl(shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, prm, total)
+          : launch_pdl(shared_merge_kernel<D, 2>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, prm, total);
+  return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
 jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -1375,7 +1436,7 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
     if (st != JF_OK) return st;
   }
   const int total = static_cast<int>(pl.total);
-  return D == 128 ? launch_merge<128>(prm, total, s) : launch_merge<64>(prm, total, s);
+  return D == 128 ? launch_merge<128>(prm, total, sms, s) : launch_merge<64>(prm, total, sms, s);
 }
 
 }  // namespace
