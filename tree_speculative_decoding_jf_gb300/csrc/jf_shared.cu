@@ -67,10 +67,11 @@ constexpr int kShared = 1, kOwn = 2;
 
 // ------------------------------------------------------------------------ the schedule
 
-// Keys that group u's sequences share: none when it has one sequence (nothing to share).
-__device__ __forceinline__ int group_keys(const SharedParams& p, int u, int b0, int b1) {
+// Keys that a group's sequences share, of its shared_pages entry: none when it has one sequence
+// (nothing to share).
+__device__ __forceinline__ int group_keys(const SharedParams& p, int pages, int b0, int b1) {
   if (b1 - b0 < 2) return 0;
-  return max(0, min(p.shared_pages[u], (p.max_pages * kPage - p.N) / kPage)) * kPage;
+  return max(0, min(pages, (p.max_pages * kPage - p.N) / kPage)) * kPage;
 }
 
 // One unit: rows f0 .. f0 + nr - 1 of q's nodes attend to keys key0 .. L - 1 of block-table row
@@ -80,33 +81,38 @@ struct Unit {
 };
 
 template <typename X>
-__device__ __forceinline__ Unit make_unit(const SharedParams& p, int b, int b0, int b1, int S) {
-  Unit t;
-  const int cap = p.max_pages * kPage;
-  if (b < 0) {                       // the group's shared keys
-    t.bt = b0;
-    t.key0 = 0;
-    t.P = t.L = S;
-    if (p.cu == nullptr) {
-      t.f0 = b0 * p.N;
-      t.nr = (b1 - b0) * p.N;
-    } else {
-      const long long r0 = p.cu[b0], r1 = p.cu[b1];
-      const bool ok = r0 >= 0 && r1 <= p.T && r1 >= r0;
-      t.f0 = ok ? static_cast<int>(r0) : 0;
-      t.nr = ok ? static_cast<int>(r1 - r0) : 0;
-    }
-  } else {
-    const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
-    t.bt = b;
-    t.key0 = S;
-    t.P = max(S, min(p.prefix_len[b], cap - sp.n));
-    t.L = t.P + sp.n;
-    t.f0 = static_cast<int>(sp.row0);
-    t.nr = sp.n;
-  }
+__device__ __forceinline__ void cut_unit(const SharedParams& p, Unit& t) {
   t.mpc = static_cast<int>((static_cast<long long>(t.nr) * p.G + X::R - 1) / X::R);
   t.T = t.nr > 0 ? (t.L - t.key0 + X::KT - 1) / X::KT : 0;
+}
+template <typename X>
+__device__ __forceinline__ Unit shared_unit(const SharedParams& p, int b0, int b1, int S) {
+  Unit t;
+  t.bt = b0;
+  t.key0 = 0;
+  t.P = t.L = S;
+  if (p.cu == nullptr) {
+    t.f0 = b0 * p.N;
+    t.nr = (b1 - b0) * p.N;
+  } else {
+    const long long r0 = p.cu[b0], r1 = p.cu[b1];
+    const bool ok = r0 >= 0 && r1 <= p.T && r1 >= r0;
+    t.f0 = ok ? static_cast<int>(r0) : 0;
+    t.nr = ok ? static_cast<int>(r1 - r0) : 0;
+  }
+  cut_unit<X>(p, t);
+  return t;
+}
+template <typename X>
+__device__ __forceinline__ Unit own_unit(const SharedParams& p, int b, int S, int prefix, int row0, int n) {
+  Unit t;
+  t.bt = b;
+  t.key0 = S;
+  t.P = max(S, min(prefix, p.max_pages * kPage - n));
+  t.L = t.P + n;
+  t.f0 = row0;
+  t.nr = n;
+  cut_unit<X>(p, t);
   return t;
 }
 
@@ -121,20 +127,33 @@ struct Schedule {
   }
 };
 
-// The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it; scratch: 4 * (3 *
-// n_groups + 2 * B + 1) bytes at least.  Unit order: group by group, its shared part (if any), then
-// its sequences.  Units of kinds that the launch does not do cost nothing.
+// The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it;
+// scratch: 4 * (4 * n_groups + 4 * B + 1) bytes at least.  Unit order: group by group, its shared part
+// (if any), then its sequences.  Units of kinds that the launch does not do cost nothing.
 template <typename X, int TEAMS>
 __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int vstep, int32_t* err, int* scratch,
                                               Schedule* out) {
   const int ng = p.n_groups, B = p.B, U = ng + B, tid = threadIdx.x, nth = blockDim.x;
   int* gs = scratch;                 // [ng + 1]
-  int* cost = gs + ng + 1;           // [U] positions of the unit
+  int* sp = gs + ng + 1;             // [ng]
+  int* pl = sp + ng;                 // [B] prefix lengths
+  int* nn = pl + B;                  // [B] nodes, -1 for a bad packed span, n | kClamped for a clamped one
+  int* cost = nn + B;                // [U] positions of the unit
   int* items = cost + U;             // [U]
+  constexpr int kClamped = 1 << 30;
   __shared__ int s_scan[32];
   __shared__ int s_items[32];
   __shared__ int s_before[TEAMS][2]; // tiles before a range's ends: the position less SW per item completed
-  for (int u = tid; u <= ng; u += nth) gs[u] = p.group_start[u];
+  // One trip to memory for all that the schedule depends on.
+  for (int u = tid; u <= ng; u += nth) {
+    gs[u] = p.group_start[u];
+    if (u < ng) sp[u] = p.shared_pages[u];
+  }
+  for (int b = tid; b < B; b += nth) {
+    pl[b] = p.prefix_len[b];
+    const SeqSpan span = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+    nn[b] = span.n | (span.ok ? 0 : kClamped);
+  }
   if (tid < TEAMS) {
     out[tid].tiles = out[tid].lo = out[tid].hi = 0;
     s_before[tid][0] = s_before[tid][1] = 0;
@@ -159,24 +178,24 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   for (int e = tid; e < U; e += nth) {
     const int u = group_of(e), b0 = gs[u], b1 = gs[u + 1];
     const int b = e - u - 1;
-    const int S = group_keys(p, u, b0, b1);
+    const int S = group_keys(p, sp[u], b0, b1);
     const bool shared = e == u + b0;
+    const int n_b = shared ? 0 : nn[b] & ~kClamped;
     if (err != nullptr) {
-      if (shared && (p.shared_pages[u] < 0 || (S != p.shared_pages[u] * static_cast<long long>(kPage) && b1 - b0 >= 2)))
-        report(err, JF_DEVERR_BAD_GROUP);
-      if (!shared) {
-        const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
-        if (!sp.ok) report(err, JF_DEVERR_BAD_TREE_LEN);
-        const int P = p.prefix_len[b];
-        if (P < S || P > cap - sp.n) report(err, JF_DEVERR_BAD_PREFIX);
+      int bits = 0;
+      if (shared) {
+        if (sp[u] < 0 || (b1 - b0 >= 2 && S / kPage != sp[u])) bits |= JF_DEVERR_BAD_GROUP;
+      } else {
+        if (nn[b] & kClamped) bits |= JF_DEVERR_BAD_TREE_LEN;
+        if (pl[b] < S || pl[b] > cap - n_b) bits |= JF_DEVERR_BAD_PREFIX;
       }
+      if (bits) report(err, bits);
     }
     int n = 0, c = 0;
     if (shared ? S > 0 && (p.kinds & kShared) : (p.kinds & kOwn) != 0) {
-      const Unit t = make_unit<X>(p, shared ? -1 : b, b0, b1, S);
-      n = p.Hkv * t.mpc;
+      const Unit t = shared ? shared_unit<X>(p, b0, b1, S) : own_unit<X>(p, b, S, pl[b], 0, n_b);
+      n = t.T == 0 ? 0 : p.Hkv * t.mpc;
       c = n * (t.T + X::SW);
-      if (t.T == 0) n = c = 0;
     }
     cost[e] = c;
     items[e] = n;
@@ -197,12 +216,18 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   }
   if (lane == 31) s_scan[warp] = upto, s_items[warp] = upto_items;
   __syncthreads();
-  int total = 0, total_items = 0;
-  for (int w = 0; w < (nth + 31) / 32; ++w) {
-    if (w < warp) upto += s_scan[w], upto_items += s_items[w];
-    total += s_scan[w];
-    total_items += s_items[w];
+  const int warps = (nth + 31) / 32;
+  int all = lane < warps ? s_scan[lane] : 0, all_items = lane < warps ? s_items[lane] : 0;
+  const int own = all, own_items = all_items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, all, o);
+    const int z = __shfl_up_sync(0xffffffffu, all_items, o);
+    if (lane >= o) all += y, all_items += z;
   }
+  const int total = __shfl_sync(0xffffffffu, all, 31), total_items = __shfl_sync(0xffffffffu, all_items, 31);
+  upto += __shfl_sync(0xffffffffu, all - own, warp);
+  upto_items += __shfl_sync(0xffffffffu, all_items - own_items, warp);
   const int q = total / p.ranges, rem = total - q * p.ranges;
   const int first = upto - mine, last = upto;
   for (int k = 0; k < 2 * TEAMS; ++k) {
@@ -289,8 +314,8 @@ struct Walk {
     b = s.b;
     b0 = p.group_start[u];
     b1 = p.group_start[u + 1];
-    S = group_keys(p, u, b0, b1);
-    t = make_unit<X>(p, b, b0, b1, S);
+    S = group_keys(p, p.shared_pages[u], b0, b1);
+    load_unit();
     const int per = t.T + X::SW, item = s.off / per;
     g = item / t.mpc;
     mp = item - g * t.mpc;
@@ -358,11 +383,20 @@ struct Walk {
         }
         b0 = b1;
         b1 = p.group_start[u + 1];
-        S = group_keys(p, u, b0, b1);
+        S = group_keys(p, p.shared_pages[u], b0, b1);
         b = S > 0 && (p.kinds & kShared) ? -1 : ((p.kinds & kOwn) ? b0 : b1);
       }
-      t = make_unit<X>(p, b, b0, b1, S);
+      load_unit();
     } while (t.T == 0);
+  }
+  __device__ __forceinline__ void load_unit() {
+    if (b < 0) {
+      t = shared_unit<X>(p, b0, b1, S);
+    } else {
+      const int prefix = p.prefix_len[b];
+      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
+      t = own_unit<X>(p, b, S, prefix, static_cast<int>(sp.row0), sp.n);
+    }
   }
 };
 
@@ -809,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 //   joined by a byte permute, and a thread ends with runs of eight consecutive d.
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
 template <int MT>
-using RowCut = Cut<16 * MT, 64, 2>;
+using RowCut = Cut<16 * MT, MT == 1 ? 48 : 64, 2>;      // (a one-warp team's ring holds 48 keys)
 
 template <int D, int MT>
 struct RowCfg {
@@ -847,14 +881,17 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
   __shared__ Schedule s_sch[kTeams];
   __shared__ Piece s_post[kTeams][C::kPosts];
   __shared__ uint64_t s_full[kTeams][kS], s_empty[kTeams][kS];
+  __shared__ int s_posted[kTeams];
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
   if (threadIdx.x == 0) {
-    for (int t = 0; t < kTeams; ++t)
+    for (int t = 0; t < kTeams; ++t) {
       for (int st = 0; st < kS; ++st) {
         mbar_init(&s_full[t][st], 1);
         mbar_init(&s_empty[t][st], MT);
       }
+      s_posted[t] = 0;
+    }
     abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&kmap);
@@ -886,6 +923,10 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         const int first = w.t.key0 + w.k0 * X::KT, end = min(w.t.L, w.t.key0 + w.k1 * X::KT);
         const int steps = (end - first + kPage - 1) / kPage;
         const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages + first / kPage;
+        if (lane == 0) {                // its rows' Q can be read while its first page is under way
+          s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
+          shared_count_add(&s_posted[team]);
+        }
         int ids = p.num_pages;          // lane l: the page of step 32 * k + l
         for (int s = 0; s < steps; ++s) {
           if ((s & 31) == 0 && s + lane < steps) {
@@ -899,10 +940,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
           int go = 1;
           if (lane == 0) {
             go = free_stage() ? 1 : 0;
-            if (go) {
-              if (s == 0) s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
-              mbar_arrive_expect_tx(&s_full[team][it % kS], C::kStageBytes);
-            }
+            if (go) mbar_arrive_expect_tx(&s_full[team][it % kS], C::kStageBytes);
           }
           if (!__shfl_sync(0xffffffffu, go, 0)) {
             ok = false;
@@ -919,17 +957,12 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
       }
       if (__any_sync(0xffffffffu, bad) && lane == 0) report(p.dev_err, JF_DEVERR_BAD_PAGE);
       if (lane == 0) {
-        // No copy may still be landing when the block exits (before the end's phase: a barrier tells
-        // only its last phase).
-        int zero = 0;
+        s_post[team][posted % C::kPosts].T = 0;          // the end
+        shared_count_add(&s_posted[team]);
+        int zero = 0;                   // no copy may still be landing when the block exits
         for (int j = max(0, it - kS); j < it; ++j)
           ok = mbar_wait(&s_full[team][j % kS], static_cast<uint32_t>(j / kS) & 1u, &zero) && ok;
-        if (ok && free_stage()) {       // the end: a piece without tiles, on a stage without data
-          s_post[team][posted % C::kPosts].T = 0;
-          mbar_arrive(&s_full[team][it % kS]);
-        } else {
-          set_abort(abort, p.dev_err);
-        }
+        if (!ok) set_abort(abort, p.dev_err);
       }
       __syncwarp();
     }
@@ -940,9 +973,17 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     const int q4 = lane & 3, r8 = lane >> 2;
     const uint8_t* ring = sm + team * kS * C::kStageBytes;
     bool ok = s_sch[team].tiles > 0;
-    int it = 0;
+    int st = 0;                          // the ring's next stage, and the phase of its barrier
+    uint32_t phase = 0;
     for (int post = 0; ok; ++post) {
-      if (!wait_warp(&s_full[team][it % kS], static_cast<uint32_t>(it / kS) & 1u, abort, wlim)) break;
+      int there = 1;
+      if (lane == 0) there = wait_shared_count(&s_posted[team], post, abort) ? 1 : 0;
+      there = __shfl_sync(0xffffffffu, there, 0);
+      __syncwarp();                     // what the lane acquired is the warp's
+      if (!there) {
+        ok = false;
+        break;
+      }
       const Piece& c = s_post[team][post % C::kPosts];
       const int T = c.T;
       if (T == 0) break;
@@ -965,27 +1006,30 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 #pragma unroll
       for (int j = 0; j < 8 * kH; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
-      for (int s = 0; s < steps; ++s, ++it) {
-        if (s > 0 && !wait_warp(&s_full[team][it % kS], static_cast<uint32_t>(it / kS) & 1u, abort, wlim)) {
+      for (int s = 0; s < steps; ++s) {
+        if (!wait_lanes(&s_full[team][st], phase, abort, wlim)) {
           ok = false;
           break;
         }
-        const uint8_t* kt = ring + (it % kS) * C::kStageBytes;
+        const uint8_t* kt = ring + st * C::kStageBytes;
         const uint8_t* vt = kt + kH * C::kHalfBytes;
         const int key0 = first + s * kPage;
         if (some) {                                  // warp-uniform
           float x[2][4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+          for (int t = 0; t < 2; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kI; ++i) {
-              const int ch = q4 + 4 * i;
-              const uint4 kr = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + r8) * 128 +
-                                                               (((ch & 7) ^ r8) << 4));
-              mma_16816(x[t], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr.x, kr.y);
-              mma_16816(x[t], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr.z, kr.w);
-            }
+          for (int i = 0; i < kI; ++i) {
+            const int ch = q4 + 4 * i;
+            uint4 kr[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              kr[t] = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + r8) * 128 +
+                                                      (((ch & 7) ^ r8) << 4));
+            mma_16816(x[0], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[0].x, kr[0].y);
+            mma_16816(x[1], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[1].x, kr[1].y);
+            mma_16816(x[0], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[0].z, kr[0].w);
+            mma_16816(x[1], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[1].z, kr[1].w);
           }
           if (key0 + kPage > P) {                    // tree keys, or keys past the end
 #pragma unroll
@@ -1002,21 +1046,21 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
                 if (!sb) x[t][2 + e] = -INFINITY;
               }
           }
-          float ta = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-          float tb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+          // The running maximum rises only by more than 2^8 (see jf_attention.cu): O is rescaled rarely, and
+          // most pages need no maximum across the row's four lanes, only that no lane passes it.
+          const float ta = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1])) * p.scale_log2;
+          const float tb = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3])) * p.scale_log2;
+          if (__any_sync(0xffffffffu, ta > ma + kRescaleThreshold || tb > mb + kRescaleThreshold)) {
+            float ra2 = ta, rb2 = tb;
 #pragma unroll
-          for (int k = 1; k < 4; k <<= 1) {
-            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, k));
-            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, k));
-          }
-          ta *= p.scale_log2;
-          tb *= p.scale_log2;
-          // The running maximum rises only by more than 2^8 (see jf_attention.cu): O is rescaled rarely.
-          const bool ua = ta > ma + kRescaleThreshold, ub = tb > mb + kRescaleThreshold;
-          if (__any_sync(0xffffffffu, ua || ub)) {
-            const float fa = ua ? fast_exp2(ma - ta) : 1.f, fb = ub ? fast_exp2(mb - tb) : 1.f;
-            if (ua) ma = ta;
-            if (ub) mb = tb;
+            for (int k = 1; k < 4; k <<= 1) {
+              ra2 = fmaxf(ra2, __shfl_xor_sync(0xffffffffu, ra2, k));
+              rb2 = fmaxf(rb2, __shfl_xor_sync(0xffffffffu, rb2, k));
+            }
+            const bool ua = ra2 > ma + kRescaleThreshold, ub = rb2 > mb + kRescaleThreshold;
+            const float fa = ua ? fast_exp2(ma - ra2) : 1.f, fb = ub ? fast_exp2(mb - rb2) : 1.f;
+            if (ua) ma = ra2;
+            if (ub) mb = rb2;
             la *= fa;
             lb *= fb;
 #pragma unroll
@@ -1026,45 +1070,58 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             }
           }
           const float oa = ma == -INFINITY ? 0.f : -ma, ob = mb == -INFINITY ? 0.f : -mb;
-          uint32_t pa[4], pl[4];                     // the A fragment of the probabilities, and of their rest
+          uint32_t pa[4];                            // the A fragment of the probabilities
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float y0 = fast_exp2(fmaf(x[t][0], p.scale_log2, oa)), y1 = fast_exp2(fmaf(x[t][1], p.scale_log2, oa));
-            const float z0 = fast_exp2(fmaf(x[t][2], p.scale_log2, ob)), z1 = fast_exp2(fmaf(x[t][3], p.scale_log2, ob));
-            la += y0 + y1;
-            lb += z0 + z1;
-            pa[2 * t] = pack_bf16x2(y0, y1);
-            pa[2 * t + 1] = pack_bf16x2(z0, z1);
-            pl[2 * t] = pl[2 * t + 1] = 0u;
-            if (split) {
-              pl[2 * t] = pack_bf16x2(y0 - __uint_as_float(pa[2 * t] << 16), y1 - __uint_as_float(pa[2 * t] & 0xFFFF0000u));
-              pl[2 * t + 1] = pack_bf16x2(z0 - __uint_as_float(pa[2 * t + 1] << 16), z1 - __uint_as_float(pa[2 * t + 1] & 0xFFFF0000u));
+          for (int t = 0; t < 2; ++t) {              // which replace the scores
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[t][e] = fast_exp2(fmaf(x[t][e], p.scale_log2, oa));
+              x[t][2 + e] = fast_exp2(fmaf(x[t][2 + e], p.scale_log2, ob));
             }
+            la += x[t][0] + x[t][1];
+            lb += x[t][2] + x[t][3];
+            pa[2 * t] = pack_bf16x2(x[t][0], x[t][1]);
+            pa[2 * t + 1] = pack_bf16x2(x[t][2], x[t][3]);
           }
+          const bool tail = key0 + kPage > end;
+          auto pv = [&](const uint32_t (&a)[4]) {
 #pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            uint4 vr[4];
+            for (int h = 0; h < kH; ++h) {
+              uint4 vr[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {            // keys past the end: zero (their probability is, too)
-              const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
-              vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((r8 ^ (key & 7)) << 4));
-              if (key0 + key >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
+              for (int t = 0; t < 4; ++t) {
+                const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
+                vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((r8 ^ (key & 7)) << 4));
+              }
+              if (tail) {                            // keys past the end: zero (their probability is, too)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                  if (key0 + 2 * q4 + (t & 1) + 8 * (t >> 1) >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              auto two = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float (&d0)[4], float (&d1)[4]) {
+                mma_16816(d0, a[0], a[1], a[2], a[3], __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
+                mma_16816(d1, a[0], a[1], a[2], a[3], __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632));
+              };
+              two(vr[0].x, vr[1].x, vr[2].x, vr[3].x, o[8 * h + 0], o[8 * h + 1]);
+              two(vr[0].y, vr[1].y, vr[2].y, vr[3].y, o[8 * h + 2], o[8 * h + 3]);
+              two(vr[0].z, vr[1].z, vr[2].z, vr[3].z, o[8 * h + 4], o[8 * h + 5]);
+              two(vr[0].w, vr[1].w, vr[2].w, vr[3].w, o[8 * h + 6], o[8 * h + 7]);
             }
+          };
+          pv(pa);
+          if (split) {                               // and of what their rounding dropped
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t w0 = j < 2 ? vr[0].x : (j < 4 ? vr[0].y : (j < 6 ? vr[0].z : vr[0].w));
-              const uint32_t w1 = j < 2 ? vr[1].x : (j < 4 ? vr[1].y : (j < 6 ? vr[1].z : vr[1].w));
-              const uint32_t w2 = j < 2 ? vr[2].x : (j < 4 ? vr[2].y : (j < 6 ? vr[2].z : vr[2].w));
-              const uint32_t w3 = j < 2 ? vr[3].x : (j < 4 ? vr[3].y : (j < 6 ? vr[3].z : vr[3].w));
-              const uint32_t b0 = __byte_perm(w0, w1, j & 1 ? 0x7632 : 0x5410);
-              const uint32_t b1 = __byte_perm(w2, w3, j & 1 ? 0x7632 : 0x5410);
-              mma_16816(o[8 * h + j], pa[0], pa[1], pa[2], pa[3], b0, b1);
-              if (split) mma_16816(o[8 * h + j], pl[0], pl[1], pl[2], pl[3], b0, b1);
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t u0 = pa[2 * t], u1 = pa[2 * t + 1];
+              pa[2 * t] = pack_bf16x2(x[t][0] - __uint_as_float(u0 << 16), x[t][1] - __uint_as_float(u0 & 0xFFFF0000u));
+              pa[2 * t + 1] = pack_bf16x2(x[t][2] - __uint_as_float(u1 << 16), x[t][3] - __uint_as_float(u1 & 0xFFFF0000u));
             }
+            pv(pa);
           }
         }
         __syncwarp();                                // every lane has read the stage
-        if (lane == 0) mbar_arrive(&s_empty[team][it % kS]);
+        if (lane == 0) mbar_arrive(&s_empty[team][st]);
+        if (++st == kS) st = 0, phase ^= 1u;
       }
       if (!ok) break;
 #pragma unroll
@@ -1273,7 +1330,7 @@ bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int H
   if (G > kRowTile || (G & (G - 1)) != 0) return false;
   if (static_cast<long long>(max_pages) * kPage < N || static_cast<long long>(max_pages) * kPage > (1ll << 30)) return false;
   // workspace rows and positions of the schedule are 32-bit
-  const long long tiles = static_cast<long long>(max_pages) * kPage / 64 + 5;
+  const long long tiles = static_cast<long long>(max_pages) * kPage / 48 + 5;
   const long long groups = nodes * G / 16 + B + n_groups;
   return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
          static_cast<long long>(B) * N * Hq < 8ll * INT_MAX;
@@ -1322,7 +1379,7 @@ template <int NT, int D>
 jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
                        const CUtensorMap& vr, const SharedParams& prm, cudaStream_t s) {
   using C = Cfg<NT, D>;
-  static_assert(C::kSmemBytes >= 4 * (5 * kSharedMaxB + 1), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1), "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_attention_kernel<NT, D>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
@@ -1334,7 +1391,7 @@ jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUten
 template <int D, int MT>
 jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const SharedParams& prm, cudaStream_t s) {
   using C = RowCfg<D, MT>;
-  static_assert(C::kSmemBytes >= 4 * (5 * kSharedMaxB + 1), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1), "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_rows_kernel<D, MT>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / C::kTeams)),
