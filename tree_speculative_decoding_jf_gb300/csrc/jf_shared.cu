@@ -37,11 +37,11 @@
 namespace jf {
 namespace {
 
-// How a kernel cuts its units: row tiles of R rows, key tiles of KT keys, and what a change of item
-// costs, in key tiles.
-template <int R_, int KT_, int SW_>
+// How a kernel cuts its units: row tiles of R rows, key tiles of KT keys, what a change of item
+// costs, in key tiles, and the least that a range is cut for (small calls leave ranges empty).
+template <int R_, int KT_, int SW_, int LEAST_>
 struct Cut {
-  static constexpr int R = R_, KT = KT_, SW = SW_;
+  static constexpr int R = R_, KT = KT_, SW = SW_, LEAST = LEAST_;
 };
 constexpr int kSharedMaxB = 4096;   // the schedule is formed in shared memory
 
@@ -128,7 +128,7 @@ struct Schedule {
 };
 
 // The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it;
-// scratch: 4 * (4 * n_groups + 4 * B + 1) bytes at least.  Unit order: group by group, its shared part
+// scratch: 4 * (4 * n_groups + 4 * B + 2 * threads + 1) bytes at least.  Unit order: group by group, its shared part
 // (if any), then its sequences.  Units of kinds that the launch does not do cost nothing.
 template <typename X, int TEAMS>
 __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int vstep, int32_t* err, int* scratch,
@@ -140,6 +140,8 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   int* nn = pl + B;                  // [B] nodes, -1 for a bad packed span, n | kClamped for a clamped one
   int* cost = nn + B;                // [U] positions of the unit
   int* items = cost + U;             // [U]
+  int* s_first = items + U;          // [threads] positions and items before a thread's chunk
+  int* s_done = s_first + nth;
   constexpr int kClamped = 1 << 30;
   __shared__ int s_scan[32];
   __shared__ int s_items[32];
@@ -228,32 +230,50 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   const int total = __shfl_sync(0xffffffffu, all, 31), total_items = __shfl_sync(0xffffffffu, all_items, 31);
   upto += __shfl_sync(0xffffffffu, all - own, warp);
   upto_items += __shfl_sync(0xffffffffu, all_items - own_items, warp);
-  const int q = total / p.ranges, rem = total - q * p.ranges;
-  const int first = upto - mine, last = upto;
-  for (int k = 0; k < 2 * TEAMS; ++k) {
-    const int v = v0 + (k >> 1) * vstep + (k & 1), x = v * q + min(v, rem);      // start of the team's range, or its end
-    if (x >= total && tid == 0 && (k & 1)) s_before[k >> 1][1] = total - X::SW * total_items;
-    if (x < first || x >= last) continue;        // the position lies in another thread's chunk
-    int at = first, done = upto_items - mine_items, e = e0;
+  const int used = max(1, min(p.ranges, total / X::LEAST));
+  const int q = total / used, rem = total - q * used;
+  // A warp per position (the starts and ends of the teams' ranges): the chunk that holds it, by 32
+  // probes a trip, then the unit and the item.
+  s_first[tid] = upto - mine;
+  s_done[tid] = upto_items - mine_items;
+  __syncthreads();
+  for (int k = warp; k < 2 * TEAMS; k += warps) {
+    const int v = min(v0 + (k >> 1) * vstep + (k & 1), used), x = v * q + min(v, rem);
+    if (x >= total) {                // the end of the last range, or an empty one
+      if (lane == 0) s_before[k >> 1][k & 1] = total - X::SW * total_items;
+      continue;
+    }
+    int lo = 0, len = nth;           // the last thread whose chunk starts at or before x
+    while (len > 1) {
+      const int step = (len + 31) / 32, at = lane * step;
+      const bool below = at < len && s_first[lo + at] <= x;
+      const int skip = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0) * step;
+      lo += skip;
+      len = min(step, len - skip);
+    }
+    // (Chunks without positions share their start with the one that has it, which comes last.)
+    int at = s_first[lo], done = s_done[lo], e = lo * chunk;
     while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
     const int off = x - at;
     const int per = cost[e] / items[e];          // T + SW
     const int item = off / per, in = off - item * per;
-    s_before[k >> 1][k & 1] = x - X::SW * (done + item) - max(0, in - (per - X::SW));
-    if ((k & 1) == 0) {
-      const int u = group_of(e);
-      Schedule& o = out[k >> 1];
-      o.u = u;
-      o.b = e == u + gs[u] ? -1 : e - u - 1;
-      o.off = off;
+    if (lane == 0) {
+      s_before[k >> 1][k & 1] = x - X::SW * (done + item) - max(0, in - (per - X::SW));
+      if ((k & 1) == 0) {
+        const int u = group_of(e);
+        Schedule& o = out[k >> 1];
+        o.u = u;
+        o.b = e == u + gs[u] ? -1 : e - u - 1;
+        o.off = off;
+      }
     }
   }
   __syncthreads();
   if (tid < TEAMS) {
     const int v = v0 + tid * vstep;
     Schedule& o = out[tid];
-    o.lo = v * q + min(v, rem);
-    o.hi = (v + 1) * q + min(v + 1, rem);
+    o.lo = v < used ? v * q + min(v, rem) : total;
+    o.hi = v < used ? (v + 1) * q + min(v + 1, rem) : total;
     o.q = q;
     o.rem = rem;
     o.tiles = o.lo < o.hi ? s_before[tid][1] - s_before[tid][0] : 0;
@@ -276,8 +296,15 @@ struct Piece {
 constexpr int kPieces = 4;
 // A change of item costs the tcgen05 kernel about four tiles' time: the next item's Q and K arrive, the
 // rows leave TMEM.
+constexpr int kTileSwitch = 6;
 template <int NT>
-using TileCut = Cut<NT * kRowTile, kKeyTile, 4>;
+using TileCut = Cut<NT * kRowTile, kKeyTile, kTileSwitch, 1>;
+
+__device__ __forceinline__ void store_sector(float* p, const float (&y)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]),
+               "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+               : "memory");
+}
 
 // What a piece leaves beside a row's output: its log-sum-exp and, from the item's first piece, where
 // the row's pieces are (stride: workspace rows from the second piece to the third, and so on).
@@ -801,11 +828,16 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
             dst[q] = y;
           }
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.ws_o + static_cast<size_t>(prow) * D + k * 32);
+          // A lane's row is its own, so a store instruction touches 32 lines whatever its width: the
+          // widest one, a whole sector a lane.
+          float* dst = p.ws_o + static_cast<size_t>(prow) * D + k * 32;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                 __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+          for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * q + e]) * inv;
+            store_sector(dst + 8 * q, y);
+          }
         }
       }
       if (valid) write_row_facts(p, const_cast<const Piece&>(s_piece[s % kPieces]), row, prow, r, lse2, 2 * NT * kRowTile);
@@ -841,9 +873,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 //   Output: column n of n-tile 8 h + j is d = 64 h + 8 n + j, so that a thread's V chunks (8 values at
 //   64 h + 8 (lane / 4) of keys 2 (lane % 4) + {0, 1, 8, 9}) hold its B fragments, two keys' values
 //   joined by a byte permute, and a thread ends with runs of eight consecutive d.
+constexpr int kRowSwitch = 4;           // pages
+constexpr int kRowLeast = 4;
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
 template <int MT>
-using RowCut = Cut<16 * MT, MT == 1 ? 48 : 64, 2>;      // (a one-warp team's ring holds 48 keys)
+using RowCut = Cut<16 * MT, kPage, kRowSwitch, kRowLeast>;
 
 template <int D, int MT>
 struct RowCfg {
@@ -923,14 +957,15 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         const int first = w.t.key0 + w.k0 * X::KT, end = min(w.t.L, w.t.key0 + w.k1 * X::KT);
         const int steps = (end - first + kPage - 1) / kPage;
         const int32_t* bt = p.block_table + static_cast<size_t>(w.t.bt) * p.max_pages + first / kPage;
+        int ids = p.num_pages;          // lane l: the page of step 32 * k + l
+        if (lane < steps) ids = __ldg(bt + lane);
         if (lane == 0) {                // its rows' Q can be read while its first page is under way
           s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
           shared_count_add(&s_posted[team]);
         }
-        int ids = p.num_pages;          // lane l: the page of step 32 * k + l
         for (int s = 0; s < steps; ++s) {
           if ((s & 31) == 0 && s + lane < steps) {
-            ids = __ldg(bt + s + lane);
+            if (s > 0) ids = __ldg(bt + s + lane);
             if (ids < 0 || ids >= p.num_pages) {
               ids = p.num_pages;        // out of bounds: TMA fills zeros
               bad = 1;
@@ -1152,9 +1187,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
               *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * D + d0) =
                   make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
             } else {
-              float4* dst = reinterpret_cast<float4*>(p.ws_o + static_cast<size_t>(prow) * D + d0);
-              dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-              dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+              store_sector(p.ws_o + static_cast<size_t>(prow) * D + d0, y);
             }
           }
         if (q4 == 0) write_row_facts(p, c, row, prow, r, lse2, 2 * X::R);
@@ -1179,7 +1212,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   constexpr int E = D / 32;
   constexpr int kWarps = 8;
   constexpr int kStep = ROWS == 1 ? kWarps : 1;       // pieces a warp skips
-  constexpr int kBatch = ROWS == 1 ? 4 : 2;           // pieces of a row whose reads overlap
+  constexpr int kBatch = 4;                           // pieces of a row whose reads overlap
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ float s_part[ROWS == 1 ? kWarps : 1][D + 2];
   grid_dependency_wait();
@@ -1330,7 +1363,7 @@ bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int H
   if (G > kRowTile || (G & (G - 1)) != 0) return false;
   if (static_cast<long long>(max_pages) * kPage < N || static_cast<long long>(max_pages) * kPage > (1ll << 30)) return false;
   // workspace rows and positions of the schedule are 32-bit
-  const long long tiles = static_cast<long long>(max_pages) * kPage / 48 + 5;
+  const long long tiles = static_cast<long long>(max_pages) + 5;
   const long long groups = nodes * G / 16 + B + n_groups;
   return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
          static_cast<long long>(B) * N * Hq < 8ll * INT_MAX;
@@ -1371,7 +1404,7 @@ SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, in
     pl.total += 2ll * pl.row_ranges * pl.row_mt * 16;
   }
   pl.ws_bytes = static_cast<size_t>(pl.total) * (D + 1) * sizeof(float) +
-                static_cast<size_t>(2 * pl.rows) * sizeof(int4) + 64;
+                static_cast<size_t>(2 * pl.rows) * sizeof(int4) + 128;
   return pl;
 }
 
@@ -1379,7 +1412,7 @@ template <int NT, int D>
 jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
                        const CUtensorMap& vr, const SharedParams& prm, cudaStream_t s) {
   using C = Cfg<NT, D>;
-  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1025), "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_attention_kernel<NT, D>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
@@ -1391,7 +1424,7 @@ jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUten
 template <int D, int MT>
 jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const SharedParams& prm, cudaStream_t s) {
   using C = RowCfg<D, MT>;
-  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1025), "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_rows_kernel<D, MT>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / C::kTeams)),
@@ -1402,10 +1435,11 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 
 template <int D>
 jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
-  // A block a row while that keeps the SMs less than eight blocks deep, else two rows a warp.
+  // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
+  // pieces), else two rows a warp.
   const long long rows = static_cast<long long>(prm.B) * prm.N * prm.Hq;
   const cudaError_t e =
-      rows <= 8ll * sms
+      rows <= 32ll * sms
           ? launch_pdl(shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, prm, total)
           : launch_pdl(shared_merge_kernel<D, 2>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, prm, total);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
@@ -1460,9 +1494,10 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   prm.group_start = group_start; prm.shared_pages = shared_pages; prm.mask = mask;
   prm.out = static_cast<uint16_t*>(out);
   prm.lse = lse;
-  prm.ws_desc = static_cast<int4*>(workspace);
-  prm.ws_o = reinterpret_cast<float*>(prm.ws_desc + 2 * pl.rows);
-  prm.ws_lse = prm.ws_o + static_cast<size_t>(pl.total) * D;
+  // partial rows first, from a 128-byte boundary on
+  prm.ws_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 127) & ~static_cast<uintptr_t>(127));
+  prm.ws_desc = reinterpret_cast<int4*>(prm.ws_o + static_cast<size_t>(pl.total) * D);
+  prm.ws_lse = reinterpret_cast<float*>(prm.ws_desc + 2 * pl.rows);
   prm.dev_err = dev_err;
   prm.T = cu != nullptr ? T : 0;
   prm.B = B; prm.N = N; prm.Hq = Hq; prm.Hkv = Hkv; prm.G = G; prm.W = (N + 63) / 64;
