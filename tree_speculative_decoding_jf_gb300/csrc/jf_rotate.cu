@@ -18,6 +18,7 @@
 // chunks of a head that a half-split pair needs (chunks t and t + R / 16), D / 16 threads a
 // head; the cosines and sines of a token are formed once per block and read from shared memory
 // by all its heads.
+#include <algorithm>
 #include <cmath>
 
 #include "jf_common.cuh"
@@ -26,9 +27,10 @@ namespace jf {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kMaxThreads = 512;
-constexpr long long kFewRows = 16;          // per SM: up to there a block takes one token
-constexpr int kTokens = 4;                  // tokens per block once every SM has blocks enough
+constexpr int kMaxThreads = 384;
+constexpr int kAhead = 2;                   // tokens whose rows are on their way
+constexpr int kMaxChunk = 16;               // tokens whose facts a block settles at once
+constexpr int kBlocks = 8;                  // blocks per SM, resident or next in line
 
 struct RotateParams {
   const uint16_t *q, *k, *v;
@@ -41,6 +43,7 @@ struct RotateParams {
   int32_t* dev_err;
   long long rows;                           // tokens of the call's arrays (padding included)
   int B, N, Hq, Hkv, R, max_pages, num_pages;
+  int chunk;                                // tokens a block takes at a time
   float scale, eps;
 };
 
@@ -107,56 +110,33 @@ __device__ __forceinline__ uint64_t fixed_turns(double freq) {
   return __double2ull_rn(t * 18446744073709551616.0);
 }
 
-// TB tokens per block.  INTER: pairs (2 f, 2 f + 1) instead of (f, f + R / 2).  A block has a
-// thread for each pair of chunks of a token's heads (up to kMaxThreads: more heads take more
-// rounds), and its first loads, all TB tokens at once, are on their way before it looks up pages
-// and forms angles, whose chain of dependent reads they hide.
-template <int D, bool INTER, int TB>
+// A block takes `chunk` consecutive tokens at a time (blocks stride over the chunks).  It first settles
+// the chunk's facts, one chain of dependent reads for all its tokens: where each token's keys and
+// values go, and its cosines and sines, both into shared memory; then it streams the tokens' rows,
+// a thread for each pair of 16-byte chunks of a token's heads (up to kMaxThreads: more heads take
+// more rounds), the next tokens' rows being read while the current one's are turned.  The first
+// rows' reads go out before the facts'.  INTER: pairs (2 f, 2 f + 1) instead of (f, f + R / 2).
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kMaxThreads, 2) rotate_append_kernel(const RotateParams p) {
   constexpr int kLanes = D / 16;            // threads per head row
-  __shared__ float2 s_cs[TB][D / 2];        // (cos, sin) * scale
-  __shared__ long long s_cache[TB];         // cache row of the token, -1: none
-  __shared__ int s_live[TB];
+  __shared__ float2 s_cs[kMaxChunk][D / 2]; // (cos, sin) * scale: number e of thread t at e * kLanes + t
+  __shared__ long long s_cache[kMaxChunk];  // cache row of the token, -1: none
+  __shared__ int s_live[kMaxChunk];
   grid_dependency_wait();
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row0 = static_cast<long long>(blockIdx.x) * TB;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int cap = p.max_pages * kPage;
-
-  // Thread t of a head: the rotated chunks t and t + R / 16, or two of the chunks behind R.
+  // Thread t of a head: the rotated chunks t and t + R / 16, or two of the chunks behind R (the first
+  // ones of all such threads side by side, then the second ones).
   const int t = threadIdx.x % kLanes;
   const int half = p.freq != nullptr ? p.R / 16 : 0;
   const bool turns = t < half;
-  const int c0 = turns ? t : 2 * half + 2 * (t - half);
-  const int c1 = turns ? t + half : c0 + 1;
+  const int c0 = turns ? t : half + t;
+  const int c1 = turns ? t + half : c0 + kLanes - half;
   const int heads = p.Hq + 2 * p.Hkv;
   const int slots = blockDim.x / kLanes;
-  uint4 w0[TB], w1[TB];
-  auto load = [&](int h) {
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const uint16_t* src = is_q ? p.q : (is_v ? p.v : p.k);
-    const long long stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
-    const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
-#pragma unroll
-    for (int k = 0; k < TB; ++k) {
-      w0[k] = w1[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < heads && row0 + k < p.rows) {      // padding rows exist too; what they hold is dropped
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + (row0 + k) * stride + hh * D);
-        w0[k] = s4[c0];
-        w1[k] = s4[c1];
-      }
-    }
-  };
-  load(threadIdx.x / kLanes);
-  auto weight = [&](int h) -> const uint16_t* {       // of head h, null: not normalised
-    return h < p.Hq ? p.q_norm : (h < p.Hq + p.Hkv ? p.k_norm : nullptr);
-  };
-  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
-  auto load_weight = [&](int h) {
-    const uint4* w = reinterpret_cast<const uint4*>(weight(h));
-    if (w != nullptr) n0 = w[c0], n1 = w[c1];
-  };
-  if (TB == 1) load_weight(threadIdx.x / kLanes);     // with more tokens a block the registers go to their rows
+  const bool any_norm = p.q_norm != nullptr || p.k_norm != nullptr;
+  const int pairs = p.freq != nullptr ? p.R / 2 : 0;
 
   if (blockIdx.x == 0) {                    // every sequence's span and length are judged once
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
@@ -166,118 +146,134 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rotate_append_kernel(const Rot
       if (P < 0 || P > cap - sp.n) report(p.dev_err, JF_DEVERR_BAD_PREFIX);
     }
   }
-  const int warps = blockDim.x >> 5;
-  for (int k = warps - 1 - warp; k < TB; k += warps) {      // the last warps: the first ones form angles
-    const long long row = row0 + k;
-    bool live = row < p.rows;
-    long long at = -1;
-    if (live) {                             // warp-uniform
-      const Home h = p.cu != nullptr ? packed_home(p, row) : padded_home(p, row);
-      const long long i = row - h.sp.row0;
-      live = i >= 0 && i < h.sp.n;
-      if (live && lane == 0 && h.P >= 0 && h.P <= cap - h.sp.n) {
-        const int pt = h.P + static_cast<int>(i);
-        const int page = p.block_table[static_cast<size_t>(h.b) * p.max_pages + pt / kPage];
-        if (page >= 0 && page < p.num_pages)
-          at = static_cast<long long>(page) * kPage + pt % kPage;
-        else
-          report(p.dev_err, JF_DEVERR_BAD_PAGE);
+  for (long long row0 = static_cast<long long>(blockIdx.x) * p.chunk; row0 < p.rows;
+       row0 += static_cast<long long>(gridDim.x) * p.chunk) {
+    const int tokens = static_cast<int>(min(static_cast<long long>(p.chunk), p.rows - row0));
+    for (int h0 = 0; h0 < heads; h0 += slots) {
+      const int h = h0 + threadIdx.x / kLanes;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+      const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
+      const long long stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
+      const uint16_t* src = (is_q ? p.q : (is_v ? p.v : p.k)) + row0 * stride + static_cast<long long>(hh) * D;
+      uint4 w0[kAhead], w1[kAhead];
+      auto load = [&](int k, int to) {       // padding rows exist too; what they hold is dropped
+        if (h < heads && k < tokens) {
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + k * stride);
+          w0[to] = s4[c0];
+          w1[to] = s4[c1];
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        w0[k] = w1[k] = make_uint4(0u, 0u, 0u, 0u);
+        load(k, k);
       }
-    }
-    if (lane == 0) {
-      s_live[k] = live ? 1 : 0;
-      s_cache[k] = at;
-    }
-  }
-  const int pairs = p.freq != nullptr ? p.R / 2 : 0;
-  for (int e = threadIdx.x; e < TB * pairs; e += blockDim.x) {
-    const int k = e / pairs, f = e % pairs;
-    const long long pos = row0 + k < p.rows ? p.pos[row0 + k] : 0;
-    const uint64_t turn = static_cast<uint64_t>(pos) * fixed_turns(p.freq[f]);
-    // signed fraction of a turn in [-1/2, 1/2), in units of pi: [-1, 1)
-    const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;   // 2^-63
-    float s, c;
-    sincospif(x, &s, &c);
-    s_cs[k][f] = make_float2(c * p.scale, s * p.scale);
-  }
-  __syncthreads();
-
-  const bool any_norm = p.q_norm != nullptr || p.k_norm != nullptr;
-  for (int h0 = 0; h0 < heads; h0 += slots) {
-    const int h = h0 + threadIdx.x / kLanes;
-    if (h0 > 0) load(h);
-    if (h0 > 0 || TB > 1) load_weight(h);
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    const int hh = is_q ? h : (is_v ? h - p.Hq - p.Hkv : h - p.Hq);
-    const bool norm = weight(h) != nullptr;
+      const uint16_t* norm = is_v || h >= heads ? nullptr : (is_q ? p.q_norm : p.k_norm);
+      uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+      if (norm != nullptr) {
+        n0 = reinterpret_cast<const uint4*>(norm)[c0];
+        n1 = reinterpret_cast<const uint4*>(norm)[c1];
+      }
+      if (h0 == 0) {
+        __syncthreads();                     // the chunk before has been turned
+        for (int k = warps - 1 - warp; k < tokens; k += warps) {      // the last warps: the first ones form angles
+          const long long row = row0 + k;
+          const Home at_home = p.cu != nullptr ? packed_home(p, row) : padded_home(p, row);
+          const long long i = row - at_home.sp.row0;
+          const bool live = i >= 0 && i < at_home.sp.n;
+          if (lane == 0) {
+            long long at = -1;
+            if (live && at_home.P >= 0 && at_home.P <= cap - at_home.sp.n) {
+              const int pt = at_home.P + static_cast<int>(i);
+              const int page = p.block_table[static_cast<size_t>(at_home.b) * p.max_pages + pt / kPage];
+              if (page >= 0 && page < p.num_pages)
+                at = static_cast<long long>(page) * kPage + pt % kPage;
+              else
+                report(p.dev_err, JF_DEVERR_BAD_PAGE);
+            }
+            s_live[k] = live ? 1 : 0;
+            s_cache[k] = at;
+          }
+        }
+        for (int e = threadIdx.x; e < tokens * pairs; e += blockDim.x) {
+          const int k = e / pairs, f = e - k * pairs;
+          const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(p.pos[row0 + k])) * fixed_turns(p.freq[f]);
+          // signed fraction of a turn in [-1/2, 1/2), in units of pi: [-1, 1)
+          const float x = __ll2float_rn(static_cast<long long>(turn)) * 1.0842021724855044e-19f;   // 2^-63
+          float s, c;
+          sincospif(x, &s, &c);
+          // half: the eight pairs of chunk t; interleaved: four pairs each of chunks t and t + half
+          const int chunk = f >> 2;
+          const int tt = !INTER ? f >> 3 : (chunk < half ? chunk : chunk - half);
+          const int ee = !INTER ? f & 7 : (f & 3) + (chunk < half ? 0 : 4);
+          s_cs[k][ee * kLanes + tt] = make_float2(c * p.scale, s * p.scale);
+        }
+        __syncthreads();
+      }
+      for (int k = 0; k < tokens; ++k) {
+        const uint4 v0 = w0[0], v1 = w1[0];
 #pragma unroll
-    for (int k = 0; k < TB; ++k) {
-      if (!s_live[k]) continue;             // block-uniform
-      const long long at = s_cache[k];
-      float x[8], y[8];
-      unpack8(w0[k], x);
-      unpack8(w1[k], y);
-      if (any_norm) {                       // uniform: the shuffles need every lane
-        float ss = 0.f;
+        for (int u = 0; u < kAhead - 1; ++u) w0[u] = w0[u + 1], w1[u] = w1[u + 1];
+        load(k + kAhead, kAhead - 1);
+        if (!s_live[k]) continue;            // block-uniform
+        const long long at = s_cache[k];
+        float x[8], y[8];
+        unpack8(v0, x);
+        unpack8(v1, y);
+        if (any_norm) {                      // uniform: the shuffles need every lane
+          float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (norm) {
-          const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-          float u0[8], u1[8];
-          unpack8(n0, u0);
-          unpack8(n1, u1);
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (norm != nullptr) {
+            const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+            float u[8];
+            unpack8(n0, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inv * u[e];
+            unpack8(n1, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= inv * u[e];
+          }
+        }
+        if (h >= heads || !(is_q || at >= 0)) continue;
+        if (!is_v && turns) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] *= inv * u0[e];
-            y[e] *= inv * u1[e];
+            const float2 cs = s_cs[k][e * kLanes + t];
+            if (!INTER) {
+              const float a = x[e], b = y[e];
+              x[e] = a * cs.x - b * cs.y;
+              y[e] = b * cs.x + a * cs.y;
+            } else {
+              float* z = e < 4 ? x + 2 * e : y + 2 * (e - 4);
+              const float a = z[0], b = z[1];
+              z[0] = a * cs.x - b * cs.y;
+              z[1] = b * cs.x + a * cs.y;
+            }
           }
         }
+        uint16_t* d = is_q ? p.q_out + ((row0 + k) * p.Hq + hh) * D
+                           : (is_v ? p.v_cache : p.k_cache) + (at * p.Hkv + hh) * D;
+        const bool changed = !is_v && (turns || norm != nullptr);
+        reinterpret_cast<uint4*>(d)[c0] = changed ? pack8(x) : v0;
+        reinterpret_cast<uint4*>(d)[c1] = changed ? pack8(y) : v1;
       }
-      if (h >= heads || !(is_q || at >= 0)) continue;
-      if (!is_v && turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // half: the eight pairs of chunk t; interleaved: four pairs of each chunk
-          const int f = !INTER ? 8 * t + e : (e < 4 ? 4 * c0 + e : 4 * c1 + e - 4);
-          const float2 cs = s_cs[k][f];
-          if (!INTER) {
-            const float a = x[e], b = y[e];
-            x[e] = a * cs.x - b * cs.y;
-            y[e] = b * cs.x + a * cs.y;
-          } else {
-            float* z = e < 4 ? x + 2 * e : y + 2 * (e - 4);
-            const float a = z[0], b = z[1];
-            z[0] = a * cs.x - b * cs.y;
-            z[1] = b * cs.x + a * cs.y;
-          }
-        }
-      }
-      if (!is_v && (turns || norm)) {
-        w0[k] = pack8(x);
-        w1[k] = pack8(y);
-      }
-      uint16_t* d = is_q ? p.q_out + ((row0 + k) * p.Hq + hh) * D
-                         : (is_v ? p.v_cache : p.k_cache) + (at * p.Hkv + hh) * D;
-      reinterpret_cast<uint4*>(d)[c0] = w0[k];
-      reinterpret_cast<uint4*>(d)[c1] = w1[k];
     }
   }
   grid_dependents_launch();
 }
 
 template <int D>
-cudaError_t launch_rotate(const RotateParams& p, bool inter, int tb, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.rows + tb - 1) / tb));
+cudaError_t launch_rotate(const RotateParams& p, bool inter, int sms, cudaStream_t s) {
+  const long long chunks = (p.rows + p.chunk - 1) / p.chunk;
+  const dim3 grid(static_cast<unsigned>(std::min(chunks, static_cast<long long>(sms) * kBlocks)));
   const int need = (p.Hq + 2 * p.Hkv) * (D / 16);
   const int rounds = (need + kMaxThreads - 1) / kMaxThreads;
   const dim3 block(static_cast<unsigned>(((need + rounds - 1) / rounds + 31) / 32 * 32));
-  if (tb == 1)
-    return inter ? launch_pdl(rotate_append_kernel<D, true, 1>, grid, block, 0, s, p)
-                 : launch_pdl(rotate_append_kernel<D, false, 1>, grid, block, 0, s, p);
-  return inter ? launch_pdl(rotate_append_kernel<D, true, kTokens>, grid, block, 0, s, p)
-               : launch_pdl(rotate_append_kernel<D, false, kTokens>, grid, block, 0, s, p);
+  return inter ? launch_pdl(rotate_append_kernel<D, true>, grid, block, 0, s, p)
+               : launch_pdl(rotate_append_kernel<D, false>, grid, block, 0, s, p);
 }
 
 jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool packed, long long T,
@@ -326,9 +322,11 @@ jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool pac
   }
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  const int tb = p.rows <= kFewRows * sms ? 1 : kTokens;
+  // One token a block while that leaves no SM with more than kBlocks, then as many as it takes, up
+  // to kMaxChunk.
+  p.chunk = static_cast<int>(std::min<long long>(kMaxChunk, (p.rows + kBlocks * sms - 1) / (kBlocks * sms)));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 128 ? launch_rotate<128>(p, inter, tb, s) : launch_rotate<64>(p, inter, tb, s);
+  const cudaError_t e = D == 128 ? launch_rotate<128>(p, inter, sms, s) : launch_rotate<64>(p, inter, sms, s);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 

@@ -1474,20 +1474,21 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   const int G = Hq / Hkv;
   CUtensorMap qm, km, vm, kr, vr;
   {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(num_pages) * kPage};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
+    const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
+    if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&vm, v_cache, 3, dims, strides, box)) return JF_ERR_CUDA;
+    if (pl.tile_nt > 0 &&
+        (!encode(&kr, k_cache, 3, dims, strides, box_run) || !encode(&vr, v_cache, 3, dims, strides, box_run)))
+      return JF_ERR_CUDA;
+  }
+  if (pl.tile_nt > 0) {
     // q as one list of nodes: sequences of a group follow each other
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(nodes)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(kRowTile / G)};
     if (!encode(&qm, q, 3, dims, strides, box)) return JF_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv),
-                                static_cast<cuuint64_t>(num_pages) * kPage};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hkv) * D * 2};
-    const cuuint32_t box[3] = {64, 1, kPage}, box_run[3] = {64, 1, kKeyTile};
-    if (!encode(&km, k_cache, 3, dims, strides, box) || !encode(&vm, v_cache, 3, dims, strides, box) ||
-        !encode(&kr, k_cache, 3, dims, strides, box_run) || !encode(&vr, v_cache, 3, dims, strides, box_run))
-      return JF_ERR_CUDA;
   }
   SharedParams prm = {};
   prm.block_table = block_table; prm.prefix_len = prefix_len; prm.tree_len = tree_len; prm.cu = cu;

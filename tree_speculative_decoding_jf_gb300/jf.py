@@ -894,7 +894,7 @@ def jf_rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, q_ou
     B = block_table.shape[0]
     if k.dim() != 4 or k.shape[0] != B:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, N, Hkv, D)")
-    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, (B, k.shape[1]), q_out, pos, freq,
+    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, k.shape[:2], q_out, pos, freq,
                  interleaved, rotary_scale, q_norm, k_norm, norm_eps, tree_len, None, None, dev_err, stream)
 
 
@@ -904,7 +904,7 @@ def jf_rotate_append_kv_packed(q, k, v, k_cache, v_cache, block_table, prefix_le
     """jf_rotate_append_kv on packed rows: q [T][Hq][D], k and v [T][Hkv][D], pos [T]."""
     if k.dim() != 3:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (T, Hkv, D)")
-    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, (k.shape[0],), q_out, pos, freq,
+    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, k.shape[:1], q_out, pos, freq,
                  interleaved, rotary_scale, q_norm, k_norm, norm_eps, None, cu_seqlens, int(N_max), dev_err, stream)
 
 
@@ -1275,12 +1275,16 @@ def rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, pos=Non
         make = torch.empty if tree_len is None and cu_seqlens is None else torch.zeros
         out = make(q.shape, dtype=q.dtype, device=q.device)
     if cu_seqlens is None:
-        jf_rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, out, pos, freq, interleaved,
-                            rotary_scale, q_norm, k_norm, norm_eps, tree_len, dev_err, stream)
+        if k.dim() != 4 or k.shape[0] != block_table.shape[0]:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected ({block_table.shape[0]}, N, Hkv, D)")
+        lead = k.shape[:2]
     else:
-        jf_rotate_append_kv_packed(q, k, v, k_cache, v_cache, block_table, prefix_len, cu_seqlens,
-                                   k.shape[0] if N_max is None else N_max, out, pos, freq, interleaved, rotary_scale,
-                                   q_norm, k_norm, norm_eps, dev_err, stream)
+        if k.dim() != 3:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected (T, Hkv, D)")
+        lead = k.shape[:1]
+        N_max = int(lead[0] if N_max is None else N_max)
+    _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, lead, out, pos, freq, interleaved, rotary_scale,
+                 q_norm, k_norm, norm_eps, tree_len, cu_seqlens, N_max, dev_err, stream)
     return out
 
 
