@@ -867,12 +867,16 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // takes a range of its own; a producer warp per team walks the range ahead of it, through item
 // changes too, and keeps a ring of key pages (K and V of 16 keys, by TMA) in flight: 24 pages of
 // 8 KB per SM at D = 128, some 190 KB, where the HBM rate needs about 40.
-//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of
-//   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
-//   contraction is free.
-//   Output: column n of n-tile 8 h + j is d = 64 h + 8 n + j, so that a thread's V chunks (8 values at
-//   64 h + 8 (lane / 4) of keys 2 (lane % 4) + {0, 1, 8, 9}) hold its B fragments, two keys' values
-//   joined by a byte permute, and a thread ends with runs of eight consecutive d.
+//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row are two
+//   k-steps' B fragments if Q's chunks are cut the same way: the order of the contraction is free.
+//   Column n of an n-tile is key pi(n) = n / 2 + 4 (n % 2) of its eight.
+//   Output: column n of n-tile 8 h + j is d = 64 h + 8 pi(n) + j, so that a thread's V chunks (8 values
+//   at 64 h + 8 pi(lane / 4) of the keys lane % 4 + {0, 4, 8, 12} that its probabilities belong to)
+//   hold its B fragments, two keys' values joined by a byte permute, and a thread ends with runs
+//   of eight consecutive d.
+//   pi: eight lanes that read together (two of lane / 4, four of lane % 4) then meet all eight 16-byte
+//   bank groups, for K and for V; the shared-memory reads, 8 KB a warp and page, are what bounds a
+//   team of several warps (with the identity in its place K's took twice as long).
 constexpr int kRowSwitch = 4;           // pages
 constexpr int kRowLeast = 4;
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
@@ -1006,6 +1010,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     // ================================================================ the teams
     const int team = warp / MT, tw = warp % MT;
     const int q4 = lane & 3, r8 = lane >> 2;
+    const int pi8 = (r8 >> 1) | ((r8 & 1) << 2);
     const uint8_t* ring = sm + team * kS * C::kStageBytes;
     bool ok = s_sch[team].tiles > 0;
     int st = 0;                          // the ring's next stage, and the phase of its barrier
@@ -1036,7 +1041,10 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         qa[i] = va ? reinterpret_cast<const uint4*>(p.q + rowa * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
         qb[i] = vb ? reinterpret_cast<const uint4*>(p.q + rowb * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
       }
-      const bool split = P < kSplitPrefix;           // rows with few keys: probabilities in two bf16 parts
+      // Probabilities in two bf16 parts: for rows with few keys (see jf_attention.cuh), and in one-warp
+      // teams, where the K/V stream leaves time for it, always: rounding them to bf16 alone costs the
+      // output as much precision as its own rounding.
+      const bool split = MT == 1 || P < kSplitPrefix;
       float o[8 * kH][4];
 #pragma unroll
       for (int j = 0; j < 8 * kH; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -1059,8 +1067,8 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             uint4 kr[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-              kr[t] = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + r8) * 128 +
-                                                      (((ch & 7) ^ r8) << 4));
+              kr[t] = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + pi8) * 128 +
+                                                      (((ch & 7) ^ pi8) << 4));
             mma_16816(x[0], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[0].x, kr[0].y);
             mma_16816(x[1], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[1].x, kr[1].y);
             mma_16816(x[0], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[0].z, kr[0].w);
@@ -1071,7 +1079,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int key = key0 + 8 * t + 2 * q4 + e, j = key - P;
+                const int key = key0 + 8 * t + q4 + 4 * e, j = key - P;
                 bool sa = key < end, sb = sa;
                 if (sa && j >= 0) {
                   sa = va && c.b >= 0 && ((p.mask[static_cast<size_t>(na) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
@@ -1125,13 +1133,13 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
               uint4 vr[4];
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
-                const int key = 2 * q4 + (t & 1) + 8 * (t >> 1);
-                vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((r8 ^ (key & 7)) << 4));
+                const int key = q4 + 4 * t;
+                vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((pi8 ^ (key & 7)) << 4));
               }
               if (tail) {                            // keys past the end: zero (their probability is, too)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                  if (key0 + 2 * q4 + (t & 1) + 8 * (t >> 1) >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
+                  if (key0 + q4 + 4 * t >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
               }
               auto two = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float (&d0)[4], float (&d1)[4]) {
                 mma_16816(d0, a[0], a[1], a[2], a[3], __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
@@ -1179,7 +1187,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         for (int h = 0; h < kH; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int d0 = 64 * h + 8 * (2 * q4 + e), at = 2 * half + e;
+            const int d0 = 64 * h + 8 * (q4 + 4 * e), at = 2 * half + e;
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] = o[8 * h + j][at] * inv;
