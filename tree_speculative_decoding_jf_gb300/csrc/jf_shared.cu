@@ -867,16 +867,10 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // takes a range of its own; a producer warp per team walks the range ahead of it, through item
 // changes too, and keeps a ring of key pages (K and V of 16 keys, by TMA) in flight: 24 pages of
 // 8 KB per SM at D = 128, some 190 KB, where the HBM rate needs about 40.
-//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row are two
-//   k-steps' B fragments if Q's chunks are cut the same way: the order of the contraction is free.
-//   Column n of an n-tile is key pi(n) = n / 2 + 4 (n % 2) of its eight.
-//   Output: column n of n-tile 8 h + j is d = 64 h + 8 pi(n) + j, so that a thread's V chunks (8 values
-//   at 64 h + 8 pi(lane / 4) of the keys lane % 4 + {0, 4, 8, 12} that its probabilities belong to)
-//   hold its B fragments, two keys' values joined by a byte permute, and a thread ends with runs
-//   of eight consecutive d.
-//   pi: eight lanes that read together (two of lane / 4, four of lane % 4) then meet all eight 16-byte
-//   bank groups, for K and for V; the shared-memory reads, 8 KB a warp and page, are what bounds a
-//   team of several warps (with the identity in its place K's took twice as long).
+//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of
+//   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
+//   contraction is free.
+//   Output: V's fragments come transposed from shared memory (ldmatrix), two n-tiles at a time.
 constexpr int kRowSwitch = 4;           // pages
 constexpr int kRowLeast = 4;
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
@@ -901,6 +895,13 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
 }
 
 template <int D, int MT>
@@ -1010,7 +1011,6 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     // ================================================================ the teams
     const int team = warp / MT, tw = warp % MT;
     const int q4 = lane & 3, r8 = lane >> 2;
-    const int pi8 = (r8 >> 1) | ((r8 & 1) << 2);
     const uint8_t* ring = sm + team * kS * C::kStageBytes;
     bool ok = s_sch[team].tiles > 0;
     int st = 0;                          // the ring's next stage, and the phase of its barrier
@@ -1067,8 +1067,8 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             uint4 kr[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-              kr[t] = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + pi8) * 128 +
-                                                      (((ch & 7) ^ pi8) << 4));
+              kr[t] = *reinterpret_cast<const uint4*>(kt + (ch >> 3) * C::kHalfBytes + (8 * t + r8) * 128 +
+                                                      (((ch & 7) ^ r8) << 4));
             mma_16816(x[0], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[0].x, kr[0].y);
             mma_16816(x[1], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kr[1].x, kr[1].y);
             mma_16816(x[0], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kr[0].z, kr[0].w);
@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int key = key0 + 8 * t + q4 + 4 * e, j = key - P;
+                const int key = key0 + 8 * t + 2 * q4 + e, j = key - P;
                 bool sa = key < end, sb = sa;
                 if (sa && j >= 0) {
                   sa = va && c.b >= 0 && ((p.mask[static_cast<size_t>(na) * p.W + (j >> 6)] >> (j & 63)) & 1ull);
@@ -1127,28 +1127,28 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
             pa[2 * t + 1] = pack_bf16x2(x[t][2], x[t][3]);
           }
           const bool tail = key0 + kPage > end;
+          uint32_t keep0 = 0xFFFFFFFFu, keep1 = keep0;
+          if (tail) {
+            const int left = end - key0 - 2 * q4;    // of the thread's keys 2 q4, 2 q4 + 1, and eight further on
+            keep0 = left >= 2 ? 0xFFFFFFFFu : (left == 1 ? 0xFFFFu : 0u);
+            keep1 = left >= 10 ? 0xFFFFFFFFu : (left == 9 ? 0xFFFFu : 0u);
+          }
+          // Lane l's row of the four 8 x 8 blocks: key l % 16, the first (l < 16) or second d-tile of two.
+          const uint32_t vaddr = smem_u32(vt) + (lane & 15) * 128;
+          const int vx = (lane & 7) ^ (lane >> 4);   // chunk j + lane / 16, swizzled by the key
           auto pv = [&](const uint32_t (&a)[4]) {
 #pragma unroll
             for (int h = 0; h < kH; ++h) {
-              uint4 vr[4];
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const int key = q4 + 4 * t;
-                vr[t] = *reinterpret_cast<const uint4*>(vt + h * C::kHalfBytes + key * 128 + ((pi8 ^ (key & 7)) << 4));
+              for (int j = 0; j < 8; j += 2) {       // n-tiles 8 h + j and the next: d from 8 (8 h + j) on
+                uint32_t b0, b1, c0, c1;             // keys 0 .. 7 and 8 .. 15 of either
+                ldmatrix_x4_trans(b0, b1, c0, c1, vaddr + h * C::kHalfBytes + ((j ^ vx) << 4));
+                if (tail) {                          // keys past the end: zero (their probability is, too)
+                  b0 &= keep0; b1 &= keep1; c0 &= keep0; c1 &= keep1;
+                }
+                mma_16816(o[8 * h + j], a[0], a[1], a[2], a[3], b0, b1);
+                mma_16816(o[8 * h + j + 1], a[0], a[1], a[2], a[3], c0, c1);
               }
-              if (tail) {                            // keys past the end: zero (their probability is, too)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                  if (key0 + q4 + 4 * t >= end) vr[t] = make_uint4(0u, 0u, 0u, 0u);
-              }
-              auto two = [&](uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float (&d0)[4], float (&d1)[4]) {
-                mma_16816(d0, a[0], a[1], a[2], a[3], __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
-                mma_16816(d1, a[0], a[1], a[2], a[3], __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632));
-              };
-              two(vr[0].x, vr[1].x, vr[2].x, vr[3].x, o[8 * h + 0], o[8 * h + 1]);
-              two(vr[0].y, vr[1].y, vr[2].y, vr[3].y, o[8 * h + 2], o[8 * h + 3]);
-              two(vr[0].z, vr[1].z, vr[2].z, vr[3].z, o[8 * h + 4], o[8 * h + 5]);
-              two(vr[0].w, vr[1].w, vr[2].w, vr[3].w, o[8 * h + 6], o[8 * h + 7]);
             }
           };
           pv(pa);
@@ -1184,20 +1184,12 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
         const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
 #pragma unroll
-        for (int h = 0; h < kH; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d0 = 64 * h + 8 * (q4 + 4 * e), at = 2 * half + e;
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = o[8 * h + j][at] * inv;
-            if (c.direct) {
-              *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * D + d0) =
-                  make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-            } else {
-              store_sector(p.ws_o + static_cast<size_t>(prow) * D + d0, y);
-            }
-          }
+        for (int j = 0; j < 8 * kH; ++j) {           // four lanes write a sector of the row
+          const float y0 = o[j][2 * half] * inv, y1 = o[j][2 * half + 1] * inv;
+          const int d0 = 8 * j + 2 * q4;
+          if (c.direct) *reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(row) * D + d0) = pack_bf16x2(y0, y1);
+          else *reinterpret_cast<float2*>(p.ws_o + static_cast<size_t>(prow) * D + d0) = make_float2(y0, y1);
+        }
         if (q4 == 0) write_row_facts(p, c, row, prow, r, lse2, 2 * X::R);
       }
     }
