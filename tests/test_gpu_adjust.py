@@ -236,6 +236,28 @@ def test_malformed_inputs_are_reported(jf):
         assert err.item() == jf.DEVERR_BAD_TREE_LEN, cu
 
 
+def test_packed_rows_behind_the_last_sequence(jf):
+    w = make(2, 10, 600, torch.float32, seed=15, sizes=[10, 4])
+    B, N, V = w["shape"]
+    rows = lambda k: torch.cat([rows_of(w, w[k], "packed"), w[k].flatten(0, 1)[:6]]).cuda()  # noqa: E731
+    out = torch.full((20, V), -7.0, device="cuda")
+    jf.adjust_logits(rows("logits"), count=w["count"].cuda(), draft=rows("draft"), mask=rows("mask"), bias=w["bias"].cuda(),
+                     allowed=w["allowed"].cuda(), allowed_row=rows("allowed_row"), repetition=w["rep"].cuda(),
+                     presence=w["pres"].cuda(), frequency=w["freq"].cuda(),
+                     cu_seqlens=torch.tensor([0, 10, 14], dtype=torch.int32).cuda(), N_max=N, out=out)
+    assert (out[14:] == -7.0).all()
+    check(w, "packed", out[:14])
+
+
+def test_dense_bias_and_full_histories(jf):
+    """Every token changed: no part of a slice is a plain copy."""
+    for V, dt in ((4096, torch.bfloat16), (2500, torch.float32)):
+        w = make(2, 7, V, dt, seed=16)
+        w["bias"] = torch.randn(2, V, generator=torch.Generator().manual_seed(1)) + 3.0
+        w["count"] = w["count"] | ref.PROMPT
+        check(w, "padded", call(jf, w, "padded"))
+
+
 def test_refused_tensors(jf):
     w = make(1, 4, 64, torch.float32, seed=13)
     x = w["logits"].cuda()

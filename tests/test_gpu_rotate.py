@@ -228,6 +228,23 @@ def test_bad_spans_and_tree_lengths(jf):
     assert (out[0, 1:] == -7.0).all() and (out[2, 3:] == -7.0).all() and (out[1] != -7.0).any()
 
 
+def test_packed_rows_behind_the_last_sequence(jf):
+    w = make(3, 10, 4, 2, 64, [10, 4, 7], [3, 30, 0], seed=12, R=64, norm=True)
+    want, kw, vw = call(jf, w, "packed", False, 1.0)
+    B, N, Hq, Hkv, D = w["shape"]
+    x = torch.cat([w["qkv"].view(B, N, -1, D)[b, :n] for b, n in enumerate(w["sizes"])] + [torch.full((9, Hq + 2 * Hkv, D), float("nan")).to(torch.bfloat16)]).cuda()
+    pos = torch.cat([w["pos"][b, :n] for b, n in enumerate(w["sizes"])] + [torch.full((9,), 5, dtype=torch.int32)]).cuda()
+    q, k, v = x.split([Hq, Hkv, Hkv], dim=1)
+    out = torch.full(q.shape, -7.0, dtype=torch.bfloat16, device="cuda")
+    kc, vc = w["kc"].cuda(), w["vc"].cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    jf.rotate_append_kv(q, k, v, kc, vc, w["table"].cuda(), w["lens"].cuda(), pos=pos, freq=w["freq"].cuda(),
+                        q_norm=w["wq"].cuda(), k_norm=w["wk"].cuda(),
+                        cu_seqlens=torch.tensor([0, 10, 14, 21], dtype=torch.int32).cuda(), N_max=N, out=out, dev_err=err)
+    assert err.item() == 0 and (out[21:] == -7.0).all()
+    assert torch.equal(bits(out[:21]), bits(want)) and torch.equal(bits(kc), bits(kw)) and torch.equal(bits(vc), bits(vw))
+
+
 def test_pool_past_32_bit_offsets(jf):
     """A pool of more than 2^31 elements: its last page is written, and read from a far offset."""
     Hkv, D = 8, 128

@@ -159,6 +159,59 @@ def test_parts_and_groups(jf, case, layout):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+MORE = [
+    # groups, N, Hq, Hkv, D, shared pages, own tokens: 24 and 48 rows a group, 80 with 8 of a sequence's own
+    ([6], 1, 8, 2, 128, [21], [3, 0, 40, 17, 16, 100]),
+    ([7, 5], 1, 16, 4, 64, [9, 33], list(range(0, 120, 10))),
+    ([3, 3], 4, 8, 2, 128, [10, 3], [5, 0, 61, 200, 33, 2]),
+    ([2, 4], 4, 16, 4, 64, [40, 20], [15, 16, 17, 31, 32, 33]),
+    ([10], 2, 8, 2, 128, [15], [7 * b for b in range(10)]),
+    ([11, 9], 2, 4, 1, 64, [50, 4], [9 * b for b in range(20)]),
+    ([20], 1, 16, 2, 128, [37], [50 * b for b in range(20)]),
+]
+
+
+@pytest.mark.parametrize("layout", ["padded", "packed"])
+@pytest.mark.parametrize("case", range(len(MORE)))
+def test_rows_between(jf, case, layout):
+    groups, N, Hq, Hkv, D, pages, own = MORE[case]
+    w = make(groups, N, Hq, Hkv, D, pages, own, seed=100 + case)
+    err = new_err()
+    out, lse = call(jf, w, layout, err)
+    assert err.item() == 0
+    check(w, layout, out, lse)
+
+
+@pytest.mark.parametrize("groups,N,pages", [([2, 1], 5, [0, 0]), ([2, 2], 40, [0, 0]), ([40], 1, [0])])
+def test_rows_that_see_nothing(jf, groups, N, pages):
+    """An empty context and a mask without bits: zeros and -inf; rows beside them are as always."""
+    B = sum(groups)
+    w = make(groups, N, 8, 2, 64, pages, [0] * B, seed=60)
+    w["sees"][0, 0] = False
+    w["sees"][B - 1, N // 2] = False
+    w["mask"] = ref.pack_bits(w["sees"])
+    out, lse = call(jf, w, "padded")
+    for b, i in ((0, 0), (B - 1, N // 2)):
+        assert (out[b, i] == 0).all() and (lse[b, :, i] == -float("inf")).all()
+    keep = torch.ones((B, N), dtype=torch.bool)
+    keep[0, 0] = keep[B - 1, N // 2] = False
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse.transpose(1, 2)[keep.cuda()]).all()
+    check(w, "padded", out, lse, only={b for b in range(B) if keep[b].all()})
+
+
+def test_packed_rows_behind_the_last_sequence(jf):
+    w = make([3, 2], 6, 8, 2, 128, [9, 3], [4, 0, 70, 16, 8], seed=61)
+    B, N, Hq, Hkv, D = w["shape"]
+    q = torch.cat([w["q"].flatten(0, 1), torch.full((7, Hq, D), float("nan"), dtype=torch.bfloat16)]).cuda()
+    mask = torch.cat([w["mask"].flatten(0, 1), torch.zeros((7, 1), dtype=torch.int64)]).cuda()
+    out = torch.full(q.shape, -7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Hq, B * N + 7), -7.0, device="cuda")
+    jf.tree_attention_shared(q, w["kc"].cuda(), w["vc"].cuda(), w["table"].cuda(), ints(w["lens"]), mask, ints(w["start"]),
+                             ints(w["pages"]), cu_seqlens=ints(list(range(0, B * N + 1, N))), N_max=N, out=out, lse=lse)
+    assert (out[B * N:] == -7.0).all() and (lse[:, B * N:] == -7.0).all()
+    check(w, "packed", out[:B * N], lse[:, :B * N])
+
+
 @pytest.mark.parametrize("scale_q", [1e-3, 12.0])
 def test_flat_and_peaked_rows(jf, scale_q):
     """Parts whose log-sum-exps lie far apart, and the rescale of a risen maximum."""
@@ -270,8 +323,12 @@ def test_refused(jf):
                                  ints(w["start"]), ints(w["pages"]), out=q)
 
 
-def test_streams_graphs_and_workspaces(jf):
-    a = make([3], 2, 8, 2, 128, [20], [3, 4, 500], seed=58)
+@pytest.mark.parametrize("groups,N,own", [([3], 2, [3, 4, 500]), ([20], 1, [9 * b + 3 for b in range(20)]),
+                                          ([2, 3], 20, [2, 30, 4, 90, 6])])
+def test_streams_graphs_and_workspaces(jf, groups, N, own):
+    """Calls of one kernel, of two side by side, and of the one for many rows."""
+    Hq, pages = 16, [20] * len(groups)
+    a = make(groups, N, Hq, 2, 128, pages, own, seed=58)
     b = make([2, 2], 1, 8, 2, 128, [9, 30], [0, 44, 10, 2], seed=59)
     want = [call(jf, w, "padded") for w in (a, b)]
     sides = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -286,7 +343,7 @@ def test_streams_graphs_and_workspaces(jf):
     held = dict(k=a["kc"].cuda(), v=a["vc"].cuda(), t=a["table"].cuda(), n=ints(a["lens"]), m=a["mask"].cuda(),
                 g=ints(a["start"]), p=ints(a["pages"]))
     q, out, lse = torch.zeros(a["q"].shape, dtype=torch.bfloat16, device="cuda"), torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
-    ws = torch.empty(jf.jf_tree_attention_shared_workspace_size(3, 2, 1, 8, 2, 128, a["table"].shape[1]),
+    ws = torch.empty(jf.jf_tree_attention_shared_workspace_size(sum(groups), N, len(groups), Hq, 2, 128, a["table"].shape[1]),
                      dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
