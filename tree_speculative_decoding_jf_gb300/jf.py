@@ -30,6 +30,7 @@ DEVERR_BAD_TREE_LEN, DEVERR_BAD_GROUP = 0x40, 0x80
 MAX_NODES = 4096
 PAGE_SIZE = 16
 COUNT_PROMPT = 1 << 30
+_Tensor, _bf16, _f32, _i32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
 
 
 class JFError(RuntimeError):
@@ -684,6 +685,28 @@ def _as_current(stream):
     return torch.cuda.stream(stream)
 
 
+def _pointers(specs, dev_err, stream) -> list:
+    """_on_stream's checks for calls of many small arguments, with the addresses taken in the same
+    round: those of the tensors (None where none is given), dev_err's and the stream's handle."""
+    cur = torch._C._cuda_getDevice()
+    out = []
+    for name, t, dtype, shape in specs:
+        if t is None:
+            out.append(None)
+        elif (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == cur and t.is_contiguous() and
+              (shape is None or t.shape == shape)):
+            out.append(t.data_ptr())
+        else:
+            _need(t, name, dtype, shape)
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+    if dev_err is None and stream is None:
+        out += (None, torch._C._cuda_getCurrentRawStream(cur))
+    else:
+        on = _on_stream((), dev_err, stream)
+        out += (_at(dev_err), on)
+    return out
+
+
 def _at(t):
     """Address of an optional tensor for a call whose arguments are declared as pointers."""
     return None if t is None else t.data_ptr()
@@ -861,28 +884,37 @@ def _rotate_call(q, k, v, k_cache, v_cache, block_table, prefix_len, lead, q_out
                  rotary_scale, q_norm, k_norm, norm_eps, tree_len, cu_seqlens, N_max, dev_err, stream):
     num_pages, page, Hkv, D = k_cache.shape
     B, max_pages = block_table.shape
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     k_stride = _heads("k", k, lead, Hkv, D, cur)
     v_stride = _heads("v", v, lead, Hkv, D, cur)
-    q_stride = 0 if q is None else _heads("q", q, lead, q.shape[-2], D, cur)
-    Hq = 0 if q is None else q.shape[-2]
-    R = 0 if freq is None else 2 * freq.numel()
-    specs = (("k_cache", k_cache, torch.bfloat16, None), ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
-             ("block_table", block_table, torch.int32, None), ("prefix_len", prefix_len, torch.int32, (B,)),
-             ("pos", pos, torch.int32, lead), ("freq", freq, torch.float64, (R // 2,)),
-             ("q_norm", q_norm, torch.bfloat16, (D,)), ("k_norm", k_norm, torch.bfloat16, (D,)),
-             ("q_out", q_out, torch.bfloat16, lead + (Hq, D)),
-             ("tree_len", tree_len, torch.int32, (B,)), ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)))
-    on = _on_stream(specs, dev_err, stream)
-    first = (_at(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, _at(pos), _at(freq), R,
-             1 if interleaved else 0, rotary_scale, _at(q_norm), _at(k_norm), norm_eps,
-             block_table.data_ptr(), prefix_len.data_ptr())
-    last = (Hq, Hkv, D, page, max_pages, num_pages, _at(q_out), _at(k_cache), _at(v_cache), _at(dev_err), on)
-    if cu_seqlens is None:
-        _check("jf_rotate_append_kv", _lib.jf_rotate_append_kv(*first, _at(tree_len), B, lead[1], *last))
+    Hq = q_stride = R = 0
+    q_at = None
+    if q is not None:
+        Hq = q.shape[-2]
+        q_stride = _heads("q", q, lead, Hq, D, cur)
+        q_at = q.data_ptr()
+    if freq is not None:
+        R = 2 * freq.numel()
+    batch = (B,)
+    (k_to, v_to, table, lens, pos_at, freq_at, qn, kn, out, tl, cu, err, on) = _pointers(
+        (("k_cache", k_cache, _bf16, None), ("v_cache", v_cache, _bf16, k_cache.shape),
+         ("block_table", block_table, _i32, None), ("prefix_len", prefix_len, _i32, batch),
+         ("pos", pos, _i32, lead), ("freq", freq, torch.float64, None if freq is None else (R // 2,)),
+         ("q_norm", q_norm, _bf16, (D,)), ("k_norm", k_norm, _bf16, (D,)),
+         ("q_out", q_out, _bf16, None if q_out is None else lead + (Hq, D)), ("tree_len", tree_len, _i32, batch),
+         ("cu_seqlens", cu_seqlens, _i32, None if cu_seqlens is None else (B + 1,))), dev_err, stream)
+    if cu is None:
+        status = _lib.jf_rotate_append_kv(
+            q_at, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, pos_at, freq_at, R, 1 if interleaved else 0,
+            rotary_scale, qn, kn, norm_eps, table, lens, tl, B, lead[1], Hq, Hkv, D, page, max_pages, num_pages, out, k_to,
+            v_to, err, on)
+        if status:
+            _check("jf_rotate_append_kv", status)
     else:
         _check("jf_rotate_append_kv_packed", _lib.jf_rotate_append_kv_packed(
-            *first, _at(cu_seqlens), B, N_max, lead[0], *last))
+            q_at, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, pos_at, freq_at, R, 1 if interleaved else 0,
+            rotary_scale, qn, kn, norm_eps, table, lens, cu, B, N_max, lead[0], Hq, Hkv, D, page, max_pages, num_pages,
+            out, k_to, v_to, err, on))
 
 
 def jf_rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, q_out, pos=None, freq=None,
@@ -925,20 +957,16 @@ def jf_tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask,
     n_groups = shared_pages.shape[0]
     if D2 != D:
         raise ValueError("q and k_cache head dims differ")
-    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
-                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
-                     ("block_table", block_table, torch.int32, (B, max_pages)),
-                     ("prefix_len", prefix_len, torch.int32, (B,)), ("tree_len", tree_len, torch.int32, (B,)),
-                     ("mask", mask, torch.int64, (B, N, (N + 63) // 64)),
-                     ("group_start", group_start, torch.int32, (n_groups + 1,)),
-                     ("shared_pages", shared_pages, torch.int32, None), ("out", out, torch.bfloat16, q.shape),
-                     ("lse", lse, torch.float32, (B, Hq, N)), ("workspace", workspace, torch.uint8, None)),
-                    dev_err, stream)
+    (q_at, k_at, v_at, table, lens, tl, bits, starts, shared, o_at, l_at, ws, err, on) = _pointers(
+        (("q", q, _bf16, None), ("k_cache", k_cache, _bf16, None), ("v_cache", v_cache, _bf16, k_cache.shape),
+         ("block_table", block_table, _i32, (B, max_pages)), ("prefix_len", prefix_len, _i32, (B,)),
+         ("tree_len", tree_len, _i32, (B,)), ("mask", mask, torch.int64, (B, N, (N + 63) // 64)),
+         ("group_start", group_start, _i32, (n_groups + 1,)), ("shared_pages", shared_pages, _i32, None),
+         ("out", out, _bf16, q.shape), ("lse", lse, _f32, (B, Hq, N)), ("workspace", workspace, torch.uint8, None)),
+        dev_err, stream)
     _check("jf_tree_attention_shared", _lib.jf_tree_attention_shared(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(),
-        _at(tree_len), mask.data_ptr(), group_start.data_ptr(), shared_pages.data_ptr(), n_groups, B, N, Hq, Hkv, D,
-        page, max_pages, num_pages, float(scale), out.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel(),
-        _at(dev_err), on))
+        q_at, k_at, v_at, table, lens, tl, bits, starts, shared, n_groups, B, N, Hq, Hkv, D, page, max_pages, num_pages,
+        scale, o_at, l_at, ws, workspace.numel(), err, on))
 
 
 def jf_tree_attention_shared_packed(q, k_cache, v_cache, block_table, prefix_len, cu_seqlens, N_max, mask,
@@ -951,20 +979,16 @@ def jf_tree_attention_shared_packed(q, k_cache, v_cache, block_table, prefix_len
     n_groups = shared_pages.shape[0]
     if D2 != D:
         raise ValueError("q and k_cache head dims differ")
-    on = _on_stream((("q", q, torch.bfloat16, None), ("k_cache", k_cache, torch.bfloat16, None),
-                     ("v_cache", v_cache, torch.bfloat16, k_cache.shape),
-                     ("block_table", block_table, torch.int32, None), ("prefix_len", prefix_len, torch.int32, (B,)),
-                     ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,)),
-                     ("mask", mask, torch.int64, (T, (N_max + 63) // 64)),
-                     ("group_start", group_start, torch.int32, (n_groups + 1,)),
-                     ("shared_pages", shared_pages, torch.int32, None), ("out", out, torch.bfloat16, q.shape),
-                     ("lse", lse, torch.float32, (Hq, T)), ("workspace", workspace, torch.uint8, None)),
-                    dev_err, stream)
+    (q_at, k_at, v_at, table, lens, cu, bits, starts, shared, o_at, l_at, ws, err, on) = _pointers(
+        (("q", q, _bf16, None), ("k_cache", k_cache, _bf16, None), ("v_cache", v_cache, _bf16, k_cache.shape),
+         ("block_table", block_table, _i32, None), ("prefix_len", prefix_len, _i32, (B,)),
+         ("cu_seqlens", cu_seqlens, _i32, (B + 1,)), ("mask", mask, torch.int64, (T, (N_max + 63) // 64)),
+         ("group_start", group_start, _i32, (n_groups + 1,)), ("shared_pages", shared_pages, _i32, None),
+         ("out", out, _bf16, q.shape), ("lse", lse, _f32, (Hq, T)), ("workspace", workspace, torch.uint8, None)),
+        dev_err, stream)
     _check("jf_tree_attention_shared_packed", _lib.jf_tree_attention_shared_packed(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), prefix_len.data_ptr(),
-        cu_seqlens.data_ptr(), mask.data_ptr(), group_start.data_ptr(), shared_pages.data_ptr(), n_groups, B, N_max, T,
-        Hq, Hkv, D, page, max_pages, num_pages, float(scale), out.data_ptr(), _at(lse), workspace.data_ptr(),
-        workspace.numel(), _at(dev_err), on))
+        q_at, k_at, v_at, table, lens, cu, bits, starts, shared, n_groups, B, N_max, T, Hq, Hkv, D, page, max_pages,
+        num_pages, scale, o_at, l_at, ws, workspace.numel(), err, on))
 
 
 def jf_adjust_logits(logits, out, count=None, draft=None, mask=None, bias=None, allowed=None, allowed_row=None,
@@ -988,27 +1012,28 @@ def jf_adjust_logits_packed(logits, out, cu_seqlens, N_max, count=None, draft=No
 
 def _adjust_call(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
                  masked, tree_len, cu_seqlens, B, N, dev_err, stream):
-    V = logits.shape[-1]
-    lead = tuple(logits.shape[:-1])
+    shape = logits.shape
+    V, lead = shape[-1], shape[:-1]
     dt, odt = _logit_dtype(logits), _logit_dtype(out)
-    n_allowed = 0 if allowed is None else allowed.shape[0]
-    if allowed is not None and allowed_row is None and n_allowed != logits.numel() // max(V, 1):
-        raise ValueError(f"allowed has {n_allowed} rows, one for each of {logits.numel() // max(V, 1)} nodes is expected")
-    on = _on_stream((("logits", logits, logits.dtype, None), ("out", out, out.dtype, logits.shape),
-                     ("count", count, torch.int32, (B, V)), ("draft", draft, torch.int32, lead),
-                     ("mask", mask, torch.int64, lead + ((N + 63) // 64,)), ("bias", bias, torch.float32, (B, V)),
-                     ("allowed", allowed, torch.int32, (n_allowed, (V + 31) // 32)),
-                     ("allowed_row", allowed_row, torch.int32, lead),
-                     ("repetition", repetition, torch.float32, (B,)), ("presence", presence, torch.float32, (B,)),
-                     ("frequency", frequency, torch.float32, (B,)), ("tree_len", tree_len, torch.int32, (B,)),
-                     ("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))), dev_err, stream)
-    first = (_at(logits), dt, _at(count), _at(draft), _at(mask), _at(bias), _at(allowed), _at(allowed_row), n_allowed,
-             _at(repetition), _at(presence), _at(frequency), float(masked))
-    last = (V, _at(out), odt, _at(dev_err), on)
-    if cu_seqlens is None:
-        _check("jf_adjust_logits", _lib.jf_adjust_logits(*first, _at(tree_len), B, N, *last))
+    n_allowed = 0
+    if allowed is not None:
+        n_allowed = allowed.shape[0]
+        if allowed_row is None and n_allowed != lead.numel():
+            raise ValueError(f"allowed has {n_allowed} rows, one for each of {lead.numel()} nodes is expected")
+    batch = (B,)
+    (x, o, c, d, m, bi, al, ar, rep, pres, freq, tl, cu, err, on) = _pointers(
+        (("logits", logits, logits.dtype, None), ("out", out, out.dtype, shape), ("count", count, _i32, (B, V)),
+         ("draft", draft, _i32, lead), ("mask", mask, torch.int64, None if mask is None else lead + ((N + 63) // 64,)),
+         ("bias", bias, _f32, (B, V)), ("allowed", allowed, _i32, (n_allowed, (V + 31) // 32)),
+         ("allowed_row", allowed_row, _i32, lead), ("repetition", repetition, _f32, batch),
+         ("presence", presence, _f32, batch), ("frequency", frequency, _f32, batch), ("tree_len", tree_len, _i32, batch),
+         ("cu_seqlens", cu_seqlens, _i32, (B + 1,))), dev_err, stream)
+    if cu is None:
+        _check("jf_adjust_logits", _lib.jf_adjust_logits(
+            x, dt, c, d, m, bi, al, ar, n_allowed, rep, pres, freq, masked, tl, B, N, V, o, odt, err, on))
     else:
-        _check("jf_adjust_logits_packed", _lib.jf_adjust_logits_packed(*first, _at(cu_seqlens), B, N, lead[0], *last))
+        _check("jf_adjust_logits_packed", _lib.jf_adjust_logits_packed(
+            x, dt, c, d, m, bi, al, ar, n_allowed, rep, pres, freq, masked, cu, B, N, lead[0], V, o, odt, err, on))
 
 
 def jf_count_tokens(count, token, count_out, path=None, length=None, extra=None, row=None, prompt=False,
@@ -1017,13 +1042,12 @@ def jf_count_tokens(count, token, count_out, path=None, length=None, extra=None,
     B, N = token.shape
     V = count_out.shape[-1]
     rows_in = 0 if count is None else count.shape[0]
-    on = _on_stream((("count", count, torch.int32, (rows_in, V)), ("token", token, torch.int32, None),
-                     ("count_out", count_out, torch.int32, (B, V)), ("path", path, torch.int32, (B, N)),
-                     ("length", length, torch.int32, (B,)), ("extra", extra, torch.int32, (B,)),
-                     ("row", row, torch.int32, (B,))), dev_err, stream)
-    _check("jf_count_tokens", _lib.jf_count_tokens(
-        _at(count), _at(row), rows_in, _at(token), _at(path), _at(length), _at(extra), 1 if prompt else 0, B, N, V,
-        _at(count_out), _at(dev_err), on))
+    batch = (B,)
+    (c, t, o, pa, le, ex, ro, err, on) = _pointers(
+        (("count", count, _i32, (rows_in, V)), ("token", token, _i32, None), ("count_out", count_out, _i32, (B, V)),
+         ("path", path, _i32, (B, N)), ("length", length, _i32, batch), ("extra", extra, _i32, batch),
+         ("row", row, _i32, batch)), dev_err, stream)
+    _check("jf_count_tokens", _lib.jf_count_tokens(c, ro, rows_in, t, pa, le, ex, 1 if prompt else 0, B, N, V, o, err, on))
 
 
 # ----------------------------------------------------------------------------- conveniences
@@ -1340,8 +1364,9 @@ def adjust_logits(logits, count=None, draft=None, mask=None, bias=None, allowed=
         make = torch.empty if tree_len is None and cu_seqlens is None else torch.zeros
         out = make(logits.shape, dtype=logits.dtype, device=logits.device)
     if cu_seqlens is None:
-        jf_adjust_logits(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency,
-                         masked, tree_len, dev_err, stream)
+        B, N, _ = logits.shape
+        _adjust_call(logits, out, count, draft, mask, bias, allowed, allowed_row, repetition, presence, frequency, masked,
+                     tree_len, None, B, N, dev_err, stream)
     else:
         if N_max is None:
             N_max = min(logits.shape[0], MAX_NODES) if mask is None else 64 * mask.shape[-1]
