@@ -146,11 +146,14 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   __shared__ int s_scan[32];
   __shared__ int s_items[32];
   __shared__ int s_before[TEAMS][2]; // tiles before a range's ends: the position less SW per item completed
-  // One trip to memory for all that the schedule depends on.
+  // (Nothing here is unrolled: it runs once, and what it costs is mostly the instructions' own trip
+  // from memory.)  One trip for all the data that the schedule depends on.
+#pragma unroll 1
   for (int u = tid; u <= ng; u += nth) {
     gs[u] = p.group_start[u];
     if (u < ng) sp[u] = p.shared_pages[u];
   }
+#pragma unroll 1
   for (int b = tid; b < B; b += nth) {
     pl[b] = p.prefix_len[b];
     const SeqSpan span = seq_span(p.cu, p.tree_len, b, p.N, p.T);
@@ -162,6 +165,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   }
   __syncthreads();
   bool bad = false;
+#pragma unroll 1
   for (int u = tid; u < ng; u += nth) bad = bad || gs[u] > gs[u + 1];
   if (tid == 0) bad = bad || gs[0] != 0 || gs[ng] != B;
   if (__syncthreads_or(bad)) {       // no work at all: group_start is not a partition
@@ -170,6 +174,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   }
   auto group_of = [&](int e) {       // of unit e: unit u + gs[u] is group u's shared part
     int u = 0, hi = ng;
+#pragma unroll 1
     while (hi - u > 1) {
       const int mid = (u + hi) >> 1;
       if (mid + gs[mid] <= e) u = mid; else hi = mid;
@@ -177,6 +182,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
     return u;
   };
   const int cap = p.max_pages * kPage;
+#pragma unroll 1
   for (int e = tid; e < U; e += nth) {
     const int u = group_of(e), b0 = gs[u], b1 = gs[u + 1];
     const int b = e - u - 1;
@@ -207,10 +213,11 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   const int chunk = (U + nth - 1) / nth;
   const int e0 = min(U, tid * chunk), e1 = min(U, e0 + chunk);
   int mine = 0, mine_items = 0;      // positions are 32-bit (a limit of the call)
+#pragma unroll 1
   for (int e = e0; e < e1; ++e) mine += cost[e], mine_items += items[e];
   int upto = mine, upto_items = mine_items;
   const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, upto, o);
     const int z = __shfl_up_sync(0xffffffffu, upto_items, o);
@@ -221,7 +228,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   const int warps = (nth + 31) / 32;
   int all = lane < warps ? s_scan[lane] : 0, all_items = lane < warps ? s_items[lane] : 0;
   const int own = all, own_items = all_items;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, all, o);
     const int z = __shfl_up_sync(0xffffffffu, all_items, o);
@@ -237,6 +244,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   s_first[tid] = upto - mine;
   s_done[tid] = upto_items - mine_items;
   __syncthreads();
+#pragma unroll 1
   for (int k = warp; k < 2 * TEAMS; k += warps) {
     const int v = min(v0 + (k >> 1) * vstep + (k & 1), used), x = v * q + min(v, rem);
     if (x >= total) {                // the end of the last range, or an empty one
@@ -244,6 +252,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
       continue;
     }
     int lo = 0, len = nth;           // the last thread whose chunk starts at or before x
+#pragma unroll 1
     while (len > 1) {
       const int step = (len + 31) / 32, at = lane * step;
       const bool below = at < len && s_first[lo + at] <= x;
@@ -253,6 +262,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
     }
     // (Chunks without positions share their start with the one that has it, which comes last.)
     int at = s_first[lo], done = s_done[lo], e = lo * chunk;
+#pragma unroll 1
     while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
     const int off = x - at;
     const int per = cost[e] / items[e];          // T + SW
