@@ -28,9 +28,9 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kMaxThreads = 384;
-constexpr int kAhead = 2;                   // tokens whose rows are on their way
+constexpr int kAhead = 1;                   // tokens whose rows are on their way
 constexpr int kMaxChunk = 16;               // tokens whose facts a block settles at once
-constexpr int kBlocks = 8;                  // blocks per SM, resident or next in line
+constexpr int kBlocks = 4;                  // blocks per SM, resident or next in line
 
 struct RotateParams {
   const uint16_t *q, *k, *v;

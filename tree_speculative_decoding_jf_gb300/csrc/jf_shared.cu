@@ -1222,38 +1222,27 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
   constexpr int E = D / 32;
   constexpr int kWarps = 8;
   constexpr int kStep = ROWS == 1 ? kWarps : 1;       // pieces a warp skips
-  constexpr int kBatch = 4;                           // pieces of a row whose reads overlap
+  constexpr int kBatch = ROWS == 1 ? 4 : 2;           // pieces of a row whose reads overlap
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ float s_part[ROWS == 1 ? kWarps : 1][D + 2];
   grid_dependency_wait();
   grid_dependents_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long all = static_cast<long long>(p.B) * p.N * p.Hq;
   const long long r0 = ROWS == 1 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * kWarps + warp) * ROWS;
   int row[ROWS], n[ROWS];
   int4 da[ROWS], db[ROWS];
-  long long out_lse[ROWS];
+  bool live[ROWS];                 // of a sequence (its span or length is read beside the descriptors)
+  const int behind = p.cu != nullptr ? p.cu[p.B] : 0;
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     const long long rr = r0 + k;
-    row[k] = -1;
-    if (rr < all) {
-      const int h = static_cast<int>(rr % p.Hq);
-      const int bi = static_cast<int>(rr / p.Hq), i = bi % p.N, b = bi / p.N;
-      const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
-      if (i < sp.n) {
-        row[k] = static_cast<int>(sp.row0 + i) * p.Hq + h;
-        out_lse[k] = static_cast<long long>(lse_index(p.cu != nullptr, sp.row0, p.T, b, h, i, p.Hq, p.N));
-      }
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    da[k] = db[k] = make_int4(0, 0, 0, 0);
-    if (row[k] >= 0) {
-      da[k] = p.ws_desc[row[k]];
-      db[k] = p.ws_desc[p.rows + row[k]];
-    }
+    live[k] = rr < p.rows;
+    row[k] = live[k] ? static_cast<int>(rr) : 0;
+    da[k] = p.ws_desc[row[k]];
+    db[k] = p.ws_desc[p.rows + row[k]];
+    const int node = row[k] / p.Hq;
+    if (p.cu != nullptr) live[k] = live[k] && node < behind;
+    else if (p.tree_len != nullptr) live[k] = live[k] && node % p.N < seq_span(nullptr, p.tree_len, node / p.N, p.N, p.T).n;
   }
   auto bad = [&](const int4& d) {
     return d.y < 0 || d.y > total || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
@@ -1269,7 +1258,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     // db.y == 0: written by its only piece
-    n[k] = row[k] >= 0 && db[k].y != 0 && !bad(da[k]) && !bad(db[k]) ? da[k].y + db[k].y : 0;
+    n[k] = live[k] && db[k].y != 0 && !bad(da[k]) && !bad(db[k]) ? da[k].y + db[k].y : 0;
     most = max(most, n[k]);
     m[k] = -INFINITY;
     sum[k] = 0.f;
@@ -1345,8 +1334,12 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
     uint16_t* dst = p.out + static_cast<size_t>(row[k]) * D + lane * E;
     if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
     else *reinterpret_cast<uint32_t*>(dst) = y[0];
-    if (p.lse != nullptr && lane == 0)
-      p.lse[out_lse[k]] = (sum[k] > 0.f ? m[k] + __log2f(sum[k]) : -INFINITY) * 0.69314718055994531f;
+    if (p.lse != nullptr && lane == 0) {
+      const int node = row[k] / p.Hq, h = row[k] - node * p.Hq, b = node / p.N;
+      p.lse[p.cu != nullptr ? static_cast<size_t>(h) * p.T + node
+                            : (static_cast<size_t>(b) * p.Hq + h) * p.N + (node - b * p.N)] =
+          (sum[k] > 0.f ? m[k] + __log2f(sum[k]) : -INFINITY) * 0.69314718055994531f;
+    }
   }
 }
 
@@ -1447,7 +1440,7 @@ template <int D>
 jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
   // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
   // pieces), else two rows a warp.
-  const long long rows = static_cast<long long>(prm.B) * prm.N * prm.Hq;
+  const long long rows = prm.rows;
   const cudaError_t e =
       rows <= 32ll * sms
           ? launch_pdl(shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, prm, total)
