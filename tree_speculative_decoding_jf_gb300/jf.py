@@ -10,6 +10,7 @@ also allocate the outputs (with torch) before calling the same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -948,6 +949,12 @@ def jf_tree_attention_shared_workspace_size(B, N, n_groups, Hq, Hkv, D, max_page
     return int(n)
 
 
+@functools.lru_cache(maxsize=512)
+def _shared_workspace(device, *sizes) -> int:
+    """A workspace's bytes: they follow from the sizes and the current device alone."""
+    return jf_tree_attention_shared_workspace_size(*sizes)
+
+
 def jf_tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start, shared_pages, scale,
                              out, workspace, lse=None, tree_len=None, dev_err=None, stream=None) -> None:
     """jf_tree_attention with each group's shared prefix read once (see include/jf.h)."""
@@ -1324,23 +1331,25 @@ def tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, gr
             return tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start,
                                          shared_pages, scale, with_lse, tree_len, cu_seqlens, N_max, out, lse,
                                          workspace, dev_err)
-    Hq, D = q.shape[-2:]
+    shape = q.shape
+    Hq, D = shape[-2:]
     B, max_pages = block_table.shape
     if scale is None:
         scale = D ** -0.5
     packed = cu_seqlens is not None
     if packed and N_max is None:
         N_max = 64 * mask.shape[-1]
-    make = torch.zeros if packed or tree_len is not None else torch.empty
-    if out is None:
-        out = make(q.shape, dtype=q.dtype, device=q.device)
-    if with_lse and lse is None:
-        lse = make((Hq, q.shape[0]) if packed else (B, Hq, q.shape[1]), dtype=torch.float32, device=q.device)
+    if out is None or (with_lse and lse is None):
+        make = torch.zeros if packed or tree_len is not None else torch.empty
+        if out is None:
+            out = make(shape, dtype=q.dtype, device=q.device)
+        if with_lse and lse is None:
+            lse = make((Hq, shape[0]) if packed else (B, Hq, shape[1]), dtype=torch.float32, device=q.device)
     if workspace is None:
-        size = jf_tree_attention_shared_workspace_size(
-            B, N_max if packed else q.shape[1], shared_pages.shape[0], Hq, k_cache.shape[2], D, max_pages,
-            q.shape[0] if packed else 0, k_cache.shape[1])
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        page, Hkv = k_cache.shape[1:3]
+        N, T = (N_max, shape[0]) if packed else (shape[1], 0)
+        workspace = q.new_empty(_shared_workspace(torch._C._cuda_getDevice(), B, N, shared_pages.shape[0], Hq, Hkv, D,
+                                                  max_pages, T, page), dtype=torch.uint8)
     if packed:
         jf_tree_attention_shared_packed(q, k_cache, v_cache, block_table, prefix_len, cu_seqlens, N_max, mask,
                                         group_start, shared_pages, scale, out, workspace, lse, dev_err, stream)
