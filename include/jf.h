@@ -683,9 +683,9 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
  *      rotary_scale * (x cos a - y sin a, y cos a + x sin a); the elements from R on stay;
  *   3. query heads are written to q_out, key and value heads (values as they are) to position
  *      P_b + i of sequence b's pages.
- * Arithmetic is fp32 with one rounding to bf16 at the end; the angle is formed modulo one turn in
- * 64 bits (its fraction of a turn is off by about 2^-52 |pos freq / 2 pi| + 2^-25), so far positions
- * cost no precision.
+ * Arithmetic is fp32 (a normalised head's squares must sum within its range) with one rounding to
+ * bf16 at the end; the angle is formed modulo one turn in 64 bits (its fraction of a turn is off by
+ * about 2^-52 |pos freq / 2 pi| + 2^-25), so far positions cost no precision.
  *   q, k, v      bf16, token rows of [Hq][D], [Hkv][D], [Hkv][D]; consecutive tokens
  *                (row b * N + i) lie *_stride elements apart, so the three may be views of one
  *                projection's output.  q and q_out may both be NULL (keys and values only).
@@ -695,7 +695,8 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
  *   rotary_scale a factor on the rotated elements (1, or a long-context method's).
  *   q_norm, k_norm  bf16 [D] or NULL.
  *   block_table, prefix_len, tree_len (may be NULL)  as in jf_tree_attention and its _ragged
- *                form; tokens i >= tree_len[b] are neither read nor written.
+ *                form; tokens i >= tree_len[b] are neither written nor do they change anything.
+ *                Pages that take new tokens belong to one sequence (shared ones are forked first).
  *   q_out        bf16 [B][N][Hq][D]; may be q itself when q_stride == Hq * D.  Must not overlap
  *                k, v or, in another way, q; the caches must not overlap any input.
  *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + n_b past the block table: the sequence's

@@ -8,14 +8,17 @@
 //     c > 0: x -= presence + frequency * c;   x += bias[b][v]
 //     v forbidden by the node's grammar row: x = masked.
 //
-// Bound: bytes (logits read and written once).  A block owns a slice of 2048 tokens, eight per
-// thread, for a run of up to 16 rows of one sequence.  Few of the tokens change (a prompt's, the
-// generated and drafted ones, those with a bias), so the rows are first copied under their grammar
-// bits, as words, without unpacking a value; logits of eight tokens that the grammar forbids are
-// not read.  Then the slice's changed tokens, listed once for the run from the counts, the biases
-// and the drafted tokens, are computed one (row, token) pair a thread and written over the copy.
-// A branch's drafted tokens: a bitmap of the nodes whose token lies in the slice is ANDed with the
-// rows' ancestor masks in shared memory, and only rows with a hit walk theirs.
+// Bound: bytes (logits read and written once: 2048 rows of 151936 take 189 us at the copy rate; this
+// takes 235, 80% of it).  A block owns a slice of 2048 tokens, eight per thread, for a run of up to 16 rows of
+// one sequence, and passes over them once.  Few tokens change, so values travel as the words they were
+// read in: a thread turns its tokens' counts and biases into marks and addends once for the run,
+// takes the marked ones out of the words, computes them and puts them back, and forbids the rest by
+// bits; logits of eight tokens that the grammar forbids are not read.  (Computing every value took
+// 533 us; a copy and a second kernel over the marked tokens more than this one, for the second
+// touch of scattered sectors reaches HBM again.)
+// Drafted tokens differ from row to row: they are left out of the marks and done afterwards, one
+// (row, token) pair a thread.  A bitmap of the nodes whose token lies in the slice is ANDed with the
+// rows' ancestor masks, and only rows with a hit walk theirs.
 #include <algorithm>
 #include <cmath>
 
@@ -27,8 +30,8 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kPer = 8;                        // tokens per thread
 constexpr int kSlice = kAdjThreads * kPer;
-constexpr int kMaxRun = 16;                    // rows per block at most
-constexpr int kAdjBlocks = 5;                  // resident blocks per SM
+constexpr int kMaxRun = 16;                    // rows per block at most (2048 rows: 8 249 us, 16 236, 32 247)
+constexpr int kAdjBlocks = 5;                  // resident blocks per SM (4: 251 us, 5: 236, 6: 233, but 54 odd rows 9.5 -> 11.0)
 constexpr int kPromptFlag = JF_COUNT_PROMPT;
 
 struct AdjustParams {
@@ -431,7 +434,7 @@ jf_status adjust_call(AdjustParams p, int32_t dtype, int32_t out_dtype, bool pac
   p.slices = (p.V + kSlice - 1) / kSlice;
   if (static_cast<long long>(p.B) * p.N * p.slices > 0x7FFFFFFFll) return JF_ERR_UNSUPPORTED;
   // Rows per block: 16, so that what a block does once weighs little, fewer while the grid would
-  // leave SMs short of blocks.
+  // leave SMs short of two blocks (a chain of 16 rows of 151936: 7.4 us; short of one 8.2, of four 9.6).
   p.run = std::min(kMaxRun, p.N);
   while (p.run > 1 && static_cast<long long>(p.B) * p.slices * ((p.N + p.run - 1) / p.run) < 2ll * sms) p.run = (p.run + 1) / 2;
   p.runs = (p.N + p.run - 1) / p.run;

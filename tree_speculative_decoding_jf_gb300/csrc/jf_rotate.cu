@@ -17,7 +17,9 @@
 // Bound: bytes.  Every head row is read and written once, so a thread owns the two 16-byte
 // chunks of a head that a half-split pair needs (chunks t and t + R / 16), D / 16 threads a
 // head; the cosines and sines of a token are formed once per block and read from shared memory
-// by all its heads.
+// by all its heads.  Prompt chunks of 8 x 4096 tokens, 32 + 2 * 8 heads of 128: 144 us, 5.6 TB/s (82% of
+// the copy rate); eight trees of up to 256 nodes 12.6 us, a chain of 16 tokens 2.7 us, where the bound is
+// the chain of reads position -> angle and length -> page -> store.
 #include <algorithm>
 #include <cmath>
 
@@ -28,9 +30,9 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kMaxThreads = 384;
-constexpr int kAhead = 1;                   // tokens whose rows are on their way
+constexpr int kAhead = 1;                   // tokens whose rows are on their way (trees: 1 13.9 us, 2 15.9, 3 17.1: registers)
 constexpr int kMaxChunk = 16;               // tokens whose facts a block settles at once
-constexpr int kBlocks = 4;                  // blocks per SM, resident or next in line
+constexpr int kBlocks = 4;                  // blocks per SM, resident or next in line (trees: 4 12.6 us, 8 13.8; prompts alike)
 
 struct RotateParams {
   const uint16_t *q, *k, *v;

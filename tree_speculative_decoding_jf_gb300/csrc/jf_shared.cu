@@ -11,15 +11,25 @@
 // the 128-row tensor-core tile that a single sequence's G rows leave nearly empty.
 //
 // Work.  A unit is a group's shared part or a sequence's own part; an item is a unit, a
-// kv-head and a row-tile group (NT tiles of 128 rows).  Items lie end to end, T key tiles plus
-// X::SW for the change of item, and are cut into one equal range per SM: lengths and group
-// sizes are data, so every CTA forms the same schedule from them.  A range's pieces of items are
-// walked with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer,
-// MMA issuer, vouchers, softmax warpgroups, all counters running over the range's tiles as one
-// sequence).  Every piece leaves normalised fp32 rows and their log-sum-exp: whole items in the
-// rows' own slots (shared and own part apart), items that a range boundary cuts in the range's
-// slots 0 (cut at its start) and 1; the first piece of an item tells each of its rows where its
-// pieces are.  The merge kernel, one warp a row, reads that and adds up.
+// kv-head and a row tile.  Items lie end to end, T key tiles plus X::SW for the change of item,
+// and are cut into equal ranges: lengths and group sizes are data, so every CTA forms the same
+// schedule from them (3 to 4 us, mostly its instructions' way from memory) and walks its ranges.
+// Every piece leaves normalised fp32 rows and their log-sum-exp: whole items in the rows' own
+// slots (shared and own part apart), items that a range boundary cuts in the range's slots 0 (cut
+// at its start) and 1; the first piece of an item tells each of its rows where its pieces are.
+// The merge kernel reads that and adds up.
+//
+// Two kernels walk ranges.
+//   shared_attention_kernel: 256 rows (two tiles of 128) an item, tcgen05 products, one range per SM,
+//     with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer, MMA issuer,
+//     vouchers, softmax warpgroups, all counters running over the range's tiles as one sequence).
+//     A step of 128 keys takes 1.7 us, 78% of the tensor rate while it lasts: packed trees of 16
+//     sequences over 8K shared keys, 106 GFLOP, take 121 us in all (0.87 PFLOP/s; rows that fill their
+//     last tile in part, the prologue and the merge are the rest).
+//   shared_rows_kernel (below): 16 to 64 rows an item, bound by the K/V stream: 256 beams in 32
+//     groups over 4K keys take 91 us, 4.5 TB/s.
+// jf_tree_attention on the same inputs reads a prefix once per sequence and takes 566 us for the
+// beams, 695 us for 64 sequences over 32K shared keys (here 74).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -304,8 +314,8 @@ struct Piece {
 // A piece's slot is written once the S MMAs of the last tile of the piece before it are done: every
 // role has then left the pieces up to the third before it.
 constexpr int kPieces = 4;
-// A change of item costs the tcgen05 kernel about four tiles' time: the next item's Q and K arrive, the
-// rows leave TMEM.
+// A change of item costs the tcgen05 kernel four to six tiles' time: the next item's Q and K arrive, the
+// rows leave TMEM (16 trees: 2 161 us, 4 129, 6 130, 8 134).
 constexpr int kTileSwitch = 6;
 template <int NT>
 using TileCut = Cut<NT * kRowTile, kKeyTile, kTileSwitch, 1>;
@@ -881,8 +891,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 //   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
 //   contraction is free.
 //   Output: V's fragments come transposed from shared memory (ldmatrix), two n-tiles at a time.
-constexpr int kRowSwitch = 4;           // pages
-constexpr int kRowLeast = 4;
+// Its time is the latency of a page's chain (products, maximum, exponentials, products) at two warps a
+// scheduler: issue slots 42% busy, HBM 66%.  Two pages a step (103 us for 256 beams against 91), four
+// accumulators for the scores (93) and V's fragments kept for the second product (92) gained nothing.
+constexpr int kRowSwitch = 4;           // pages (256 beams: 2 98 us, 4 92, 8 102)
+constexpr int kRowLeast = 4;            // pages (4 beams over 2K keys: 1 17.2 us, 2 14.3, 4 13.6, 8 15.6)
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
 template <int MT>
 using RowCut = Cut<16 * MT, kPage, kRowSwitch, kRowLeast>;
@@ -1214,9 +1227,10 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 // ------------------------------------------------------------------------ the merge
 
 // The pieces of a (node, query head) row's shared and own parts, listed by ws_desc, merged by
-// log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap; ROWS == 1, for few rows:
-// a block merges one, its warps taking every eighth piece.  What ws_desc says is checked against
-// the workspace: a malformed group_start leaves it unwritten.
+// log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap (four rows for two: 144 us for
+// 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps taking every eighth piece.
+// Rows behind the last sequence keep what they hold.  What ws_desc says is checked against
+// the workspace: a malformed group_start or span leaves it unwritten.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
   constexpr int E = D / 32;
@@ -1373,9 +1387,10 @@ bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int H
 }
 
 // Which kernel takes which units.  Up to 64 rows a group (on average) the row kernel takes both parts:
-// the K/V stream bounds it.  Groups of more rows have their shared parts on the tcgen05 kernel, two
-// row tiles per CTA (each key tile loaded feeds both) once they fill more than one, and so have own
-// parts of more than 64 rows.
+// the K/V stream bounds it (four groups of 64 rows over 32K keys: 186 us, on the tcgen05 kernel 265; 32
+// rows fill two warps, 92 us for 256 beams against 125 with one warp twice).  Groups of more rows
+// have their shared parts on the tcgen05 kernel, two row tiles per CTA (each key tile loaded feeds
+// both) once they fill more than one, and so have own parts of more than 64 rows.
 SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, int D, int sms) {
   SharedPlan pl = {};
   const long long G = Hq / Hkv, group_rows = (nodes * G + n_groups - 1) / n_groups, own_rows = N * G;
@@ -1439,7 +1454,8 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 template <int D>
 jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
   // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
-  // pieces), else two rows a warp.
+  // pieces: 4 beams 13.6 us against 21.2, 64 requests 74 against 79), else two rows a warp (16 trees 131
+  // us against 189, 256 beams 92 against 108).
   const long long rows = prm.rows;
   const cudaError_t e =
       rows <= 32ll * sms
