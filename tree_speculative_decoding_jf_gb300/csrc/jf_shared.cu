@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // takes a range of its own; a producer warp per team walks the range ahead of it, through item
 // changes too, and keeps a ring of key pages (K and V of 16 keys, by TMA) in flight: 24 pages of
 // 8 KB per SM at D = 128, some 190 KB, where the HBM rate needs about 40.
-//   Scores: m16n8k16 products.  A thread's 16-byte chunks c = lane % 4 + 4 i of a K row (key lane / 4 of
+//   Scores: m16n8k16 products.  A thread's 16-byte chunks 2 (lane % 4) + {0, 1} of a K row (key lane / 4 of
 //   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
 //   contraction is free.
 //   Output: V's fragments come transposed from shared memory (ldmatrix), two n-tiles at a time.
@@ -1058,7 +1058,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
       uint4 qa[kI], qb[kI];
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const int ch = q4 + 4 * i;
+        const int ch = 2 * q4 + (i & 1) + 8 * (i >> 1);
         const size_t rowa = static_cast<size_t>(na) * p.Hq + c.g * p.G + ra % p.G;
         const size_t rowb = static_cast<size_t>(nb) * p.Hq + c.g * p.G + rb % p.G;
         qa[i] = va ? reinterpret_cast<const uint4*>(p.q + rowa * D)[ch] : make_uint4(0u, 0u, 0u, 0u);
@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
           for (int t = 0; t < 2; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
 #pragma unroll
           for (int i = 0; i < kI; ++i) {
-            const int ch = q4 + 4 * i;
+            const int ch = 2 * q4 + (i & 1) + 8 * (i >> 1);
             uint4 kr[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
