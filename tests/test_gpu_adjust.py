@@ -258,6 +258,42 @@ def test_dense_bias_and_full_histories(jf):
         check(w, "padded", call(jf, w, "padded"))
 
 
+def test_largest_tree(jf):
+    """4096 nodes: all words of the ancestor masks; a few rows are looked at."""
+    N = jf.MAX_NODES
+    w = make(1, N, 40, torch.float32, seed=18)
+    got = call(jf, w, "padded").cpu()
+    for i in (0, 1, 63, 64, 2047, 2048, 3333, N - 1):
+        want, tol = expected(w, 0, i, -INF, torch.float32)
+        assert ref.within(got[0, i], want, tol), i
+
+
+@pytest.mark.parametrize("V", [50000, 50001])
+def test_rows_past_32_bit_offsets(jf, V):
+    """More than 2^32 logits, in place: the last sequence's rows are adjusted, what has nothing to adjust stays."""
+    N, B = 4096, -(-(1 << 32) // (4096 * V)) + 1
+    few = 3                                         # rows of the last sequence that are looked at
+    w = make(1, few, V, torch.bfloat16, seed=19)
+    x = torch.zeros((B * N, V), dtype=torch.bfloat16, device="cuda")
+    x[-few:] = w["logits"][0].cuda()
+    cu = [N * b for b in range(B)] + [N * B - few, N * B]
+    rows = torch.full((N * B,), -1, dtype=torch.int32, device="cuda")
+    rows[-few:] = w["allowed_row"][0].cuda()
+    last = lambda k, fill: torch.cat([torch.full((B,) + w[k].shape[1:], fill, dtype=w[k].dtype), w[k]]).cuda()  # noqa: E731
+    draft = torch.zeros(N * B, dtype=torch.int32, device="cuda")
+    draft[-few:] = w["draft"][0].cuda()
+    mask = torch.zeros((N * B, N // 64), dtype=torch.int64, device="cuda")
+    mask[-few:, :1] = w["mask"][0].cuda()
+    err = new_err()
+    jf.adjust_logits(x, count=last("count", 0), draft=draft, mask=mask, bias=last("bias", 0.0), allowed=w["allowed"].cuda(),
+                     allowed_row=rows, repetition=last("rep", 1.0), presence=last("pres", 0.0), frequency=last("freq", 0.0),
+                     cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), N_max=N, out=x, dev_err=err)
+    assert err.item() == 0
+    check(w, "padded", x[-few:].view(1, few, V))
+    for at in range(0, B * N - few, N):             # (count_nonzero of it all would take an int64 copy)
+        assert not x[at:min(at + N, B * N - few)].any()
+
+
 def test_refused_tensors(jf):
     w = make(1, 4, 64, torch.float32, seed=13)
     x = w["logits"].cuda()
@@ -346,6 +382,28 @@ def test_counts(jf, B, N, V, kind):
         held = count.cuda()[:B].clone()
         assert jf.count_tokens(held, token.cuda(), out=held, **kw) is held
         assert torch.equal(held.cpu(), want) and err.item() == 0
+
+
+def test_counts_past_32_bit_offsets(jf):
+    """More than 2^32 entries: a new table from one row, and the last sequence's tokens in place."""
+    V = 70001
+    B = (1 << 32) // V + 2
+    token = torch.full((B, 2), 5, dtype=torch.int32, device="cuda")
+    token[-1] = torch.tensor([V - 1, 7], dtype=torch.int32)
+    one = torch.zeros((1, V), dtype=torch.int32, device="cuda")
+    one[0, 7] = 40
+    count = jf.count_tokens(one, token, row=torch.zeros(B, dtype=torch.int32, device="cuda"))
+    want = one[0].clone()
+    want[5] += 2
+    assert torch.equal(count[0], want) and torch.equal(count[-2], want)
+    want = one[0].clone()
+    want[7] += 1
+    want[V - 1] += 1
+    assert torch.equal(count[-1], want)
+    jf.count_tokens(count, token, out=count)
+    want[7] += 1
+    want[V - 1] += 1
+    assert torch.equal(count[-1], want) and int(count[-2, 5]) == 4
 
 
 def test_count_reports(jf):

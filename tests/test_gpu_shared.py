@@ -235,6 +235,44 @@ def test_many_sequences(jf):
         check(w, layout, out, lse, only=set(range(0, B, 7)))
 
 
+@pytest.mark.parametrize("groups", [[1] * 4096, [4096], [4] * 1024])
+def test_as_many_sequences_as_there_may_be(jf, groups):
+    w = make(groups, 1, 2, 1, 64, [2] * len(groups), [b % 19 for b in range(4096)], seed=61)
+    for layout in ("padded", "packed"):
+        out, lse = call(jf, w, layout)
+        check(w, layout, out, lse, only={0, 1, 2, 1023, 1024, 2047, 3000, 4094, 4095})
+
+
+@pytest.mark.parametrize("N,groups", [(1030, [2]), (4096, [1, 2])])
+def test_large_trees(jf, N, groups):
+    B = sum(groups)
+    w = make(groups, N, 2, 1, 64, [3] * len(groups), [5, 0, 40][:B], seed=62, sizes=[N, 1, N - 3][:B])
+    for layout in ("ragged", "packed"):
+        out, lse = call(jf, w, layout)
+        check(w, layout, out, lse)
+
+
+@pytest.mark.parametrize("groups,N", [([3, 2], 1), ([4], 20)])
+def test_pool_past_32_bit_offsets(jf, groups, N):
+    """The pages that are read lie at the end of a pool of more than 2^32 elements."""
+    w = make(groups, N, 16, 8, 128, [6] * len(groups), [3 + 30 * b for b in range(sum(groups))], seed=63)
+    out, lse = call(jf, w, "padded")
+    few = w["kc"].shape[0]
+    first = (1 << 32) // (PAGE * 8 * 128) + 3
+    pools = []
+    for x in (w["kc"], w["vc"]):
+        pool = torch.zeros((first + few, PAGE, 8, 128), dtype=torch.bfloat16, device="cuda")
+        pool[first:] = x.cuda()
+        pools.append(pool)
+    B, N, Hq, Hkv, D = w["shape"]
+    table = torch.where(w["table"] >= 0, w["table"] + first, w["table"]).cuda()
+    err = new_err()
+    far, far_lse = jf.tree_attention_shared(w["q"].cuda(), *pools, table, ints(w["lens"]), w["mask"].cuda(), ints(w["start"]),
+                                            ints(w["pages"]), with_lse=True, dev_err=err)
+    assert torch.equal(far, out) and torch.equal(far_lse, lse) and err.item() == 0
+    check(w, "padded", out, lse)
+
+
 def test_agrees_with_the_unshared_call(jf):
     w = make([4, 3], 9, 8, 2, 128, [30, 11], [0, 5, 77, 16, 300, 2, 1], seed=53)
     out, lse = call(jf, w, "padded")
