@@ -96,7 +96,7 @@ __device__ __forceinline__ void cut_unit(const SharedParams& p, Unit& t) {
   t.T = t.nr > 0 ? (t.L - t.key0 + X::KT - 1) / X::KT : 0;
 }
 template <typename X>
-__device__ __forceinline__ Unit shared_unit(const SharedParams& p, int b0, int b1, int S) {
+__device__ __forceinline__ Unit shared_unit(const SharedParams& p, int b0, int b1, int S, const int32_t* cu) {
   Unit t;
   t.bt = b0;
   t.key0 = 0;
@@ -105,7 +105,7 @@ __device__ __forceinline__ Unit shared_unit(const SharedParams& p, int b0, int b
     t.f0 = b0 * p.N;
     t.nr = (b1 - b0) * p.N;
   } else {
-    const long long r0 = p.cu[b0], r1 = p.cu[b1];
+    const long long r0 = cu[b0], r1 = cu[b1];
     const bool ok = r0 >= 0 && r1 <= p.T && r1 >= r0;
     t.f0 = ok ? static_cast<int>(r0) : 0;
     t.nr = ok ? static_cast<int>(r1 - r0) : 0;
@@ -137,9 +137,11 @@ struct Schedule {
   }
 };
 
-// The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it;
-// scratch: 4 * (4 * n_groups + 4 * B + 2 * threads + 1) bytes at least.  Unit order: group by group, its shared part
+// The ranges v0, v0 + vstep, .. (TEAMS of them) of the launch.  Every thread of the block calls it and
+// then waits for the block; scratch: schedule_bytes().  Unit order: group by group, its shared part
 // (if any), then its sequences.  Units of kinds that the launch does not do cost nothing.
+constexpr int schedule_bytes(int B, int n_groups) { return 4 * (4 * n_groups + 5 * B + 4); }
+
 template <typename X, int TEAMS>
 __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int vstep, int32_t* err, int* scratch,
                                               Schedule* out) {
@@ -147,38 +149,36 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   int* gs = scratch;                 // [ng + 1]
   int* sp = gs + ng + 1;             // [ng]
   int* pl = sp + ng;                 // [B] prefix lengths
-  int* nn = pl + B;                  // [B] nodes, -1 for a bad packed span, n | kClamped for a clamped one
-  int* cost = nn + B;                // [U] positions of the unit
-  int* items = cost + U;             // [U]
-  int* s_first = items + U;          // [threads] positions and items before a thread's chunk
-  int* s_done = s_first + nth;
+  int* nn = pl + B;                  // [B] nodes, with kClamped where a span or length is malformed
+  int* cost = nn + B;                // [U + 1] positions of the unit, then before it
+  int* items = cost + U + 1;         // [U + 1]
+  int* cs = items + U + 1;           // [B + 1] packed spans
   constexpr int kClamped = 1 << 30;
   __shared__ int s_scan[32];
   __shared__ int s_items[32];
-  __shared__ int s_before[TEAMS][2]; // tiles before a range's ends: the position less SW per item completed
   // (Nothing here is unrolled: it runs once, and what it costs is mostly the instructions' own trip
-  // from memory.)  One trip for all the data that the schedule depends on.
+  // from memory and the barriers.)  One trip for all the data that the schedule depends on.
+  bool bad = false;                  // group_start is not a partition
 #pragma unroll 1
-  for (int u = tid; u <= ng; u += nth) {
-    gs[u] = p.group_start[u];
-    if (u < ng) sp[u] = p.shared_pages[u];
+  for (int u = tid; u < ng; u += nth) {
+    const int g0 = p.group_start[u], g1 = p.group_start[u + 1];
+    gs[u] = g0;
+    sp[u] = p.shared_pages[u];
+    bad = bad || g0 > g1 || (u == 0 && g0 != 0) || (u == ng - 1 && g1 != B);
+    if (u == ng - 1) gs[ng] = g1;
   }
 #pragma unroll 1
   for (int b = tid; b < B; b += nth) {
     pl[b] = p.prefix_len[b];
     const SeqSpan span = seq_span(p.cu, p.tree_len, b, p.N, p.T);
     nn[b] = span.n | (span.ok ? 0 : kClamped);
+    if (p.cu != nullptr) {
+      cs[b] = p.cu[b];
+      if (b == B - 1) cs[B] = p.cu[B];
+    }
   }
-  if (tid < TEAMS) {
-    out[tid].tiles = out[tid].lo = out[tid].hi = 0;
-    s_before[tid][0] = s_before[tid][1] = 0;
-  }
-  __syncthreads();
-  bool bad = false;
-#pragma unroll 1
-  for (int u = tid; u < ng; u += nth) bad = bad || gs[u] > gs[u + 1];
-  if (tid == 0) bad = bad || gs[0] != 0 || gs[ng] != B;
-  if (__syncthreads_or(bad)) {       // no work at all: group_start is not a partition
+  if (tid < TEAMS) out[tid].tiles = out[tid].lo = out[tid].hi = 0;
+  if (__syncthreads_or(bad)) {       // no work at all
     if (tid == 0 && err != nullptr) report(err, JF_DEVERR_BAD_GROUP);
     return;
   }
@@ -192,8 +192,12 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
     return u;
   };
   const int cap = p.max_pages * kPage;
+  // A thread's units are consecutive, so that sums run over threads.
+  const int chunk = (U + nth - 1) / nth;
+  const int e0 = min(U, tid * chunk), e1 = min(U, e0 + chunk);
+  int mine = 0, mine_items = 0;      // positions are 32-bit (a limit of the call)
 #pragma unroll 1
-  for (int e = tid; e < U; e += nth) {
+  for (int e = e0; e < e1; ++e) {
     const int u = group_of(e), b0 = gs[u], b1 = gs[u + 1];
     const int b = e - u - 1;
     const int S = group_keys(p, sp[u], b0, b1);
@@ -211,20 +215,16 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
     }
     int n = 0, c = 0;
     if (shared ? S > 0 && (p.kinds & kShared) : (p.kinds & kOwn) != 0) {
-      const Unit t = shared ? shared_unit<X>(p, b0, b1, S) : own_unit<X>(p, b, S, pl[b], 0, n_b);
+      const Unit t = shared ? shared_unit<X>(p, b0, b1, S, cs) : own_unit<X>(p, b, S, pl[b], 0, n_b);
       n = t.T == 0 ? 0 : p.Hkv * t.mpc;
       c = n * (t.T + X::SW);
     }
     cost[e] = c;
     items[e] = n;
+    mine += c;
+    mine_items += n;
   }
-  __syncthreads();
-  // Block-wide sums over contiguous chunks of units.
-  const int chunk = (U + nth - 1) / nth;
-  const int e0 = min(U, tid * chunk), e1 = min(U, e0 + chunk);
-  int mine = 0, mine_items = 0;      // positions are 32-bit (a limit of the call)
-#pragma unroll 1
-  for (int e = e0; e < e1; ++e) mine += cost[e], mine_items += items[e];
+  // What lies before a thread's units: sums over its warp's lanes, then over the warps before it.
   int upto = mine, upto_items = mine_items;
   const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll 1
@@ -236,67 +236,54 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   if (lane == 31) s_scan[warp] = upto, s_items[warp] = upto_items;
   __syncthreads();
   const int warps = (nth + 31) / 32;
-  int all = lane < warps ? s_scan[lane] : 0, all_items = lane < warps ? s_items[lane] : 0;
-  const int own = all, own_items = all_items;
+  const int all = lane < warps ? s_scan[lane] : 0, all_items = lane < warps ? s_items[lane] : 0;
+  const int total = __reduce_add_sync(0xffffffffu, all);
+  const int total_items = __reduce_add_sync(0xffffffffu, all_items);
+  int first = upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? all : 0);
+  int first_items = upto_items - mine_items + __reduce_add_sync(0xffffffffu, lane < warp ? all_items : 0);
 #pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, all, o);
-    const int z = __shfl_up_sync(0xffffffffu, all_items, o);
-    if (lane >= o) all += y, all_items += z;
+  for (int e = e0; e < e1; ++e) {
+    const int c = cost[e], n = items[e];
+    cost[e] = first;
+    items[e] = first_items;
+    first += c;
+    first_items += n;
   }
-  const int total = __shfl_sync(0xffffffffu, all, 31), total_items = __shfl_sync(0xffffffffu, all_items, 31);
-  upto += __shfl_sync(0xffffffffu, all - own, warp);
-  upto_items += __shfl_sync(0xffffffffu, all_items - own_items, warp);
-  const int used = max(1, min(p.ranges, total / X::LEAST));
-  const int q = total / used, rem = total - q * used;
-  // A warp per position (the starts and ends of the teams' ranges): the chunk that holds it, by 32
-  // probes a trip, then the unit and the item.
-  s_first[tid] = upto - mine;
-  s_done[tid] = upto_items - mine_items;
+  if (tid == 0) cost[U] = total, items[U] = total_items;
   __syncthreads();
-#pragma unroll 1
-  for (int k = warp; k < 2 * TEAMS; k += warps) {
+  // Starts (even lanes) and ends of the teams' ranges: the unit that holds each, then the item.
+  if (warp == 0) {
+    const int used = max(1, min(p.ranges, total / X::LEAST));
+    const int q = total / used, rem = total - q * used;
+    const int k = min(lane, 2 * TEAMS - 1);
     const int v = min(v0 + (k >> 1) * vstep + (k & 1), used), x = v * q + min(v, rem);
-    if (x >= total) {                // the end of the last range, or an empty one
-      if (lane == 0) s_before[k >> 1][k & 1] = total - X::SW * total_items;
-      continue;
-    }
-    int lo = 0, len = nth;           // the last thread whose chunk starts at or before x
+    int before = total - X::SW * total_items;      // tiles before x: the position less SW per item completed
+    int e = 0, off = 0;
+    if (x < total) {
+      int hi = U;                    // (units without positions share theirs with the next one that has some)
 #pragma unroll 1
-    while (len > 1) {
-      const int step = (len + 31) / 32, at = lane * step;
-      const bool below = at < len && s_first[lo + at] <= x;
-      const int skip = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0) * step;
-      lo += skip;
-      len = min(step, len - skip);
-    }
-    // (Chunks without positions share their start with the one that has it, which comes last.)
-    int at = s_first[lo], done = s_done[lo], e = lo * chunk;
-#pragma unroll 1
-    while (x >= at + cost[e]) at += cost[e], done += items[e], ++e;
-    const int off = x - at;
-    const int per = cost[e] / items[e];          // T + SW
-    const int item = off / per, in = off - item * per;
-    if (lane == 0) {
-      s_before[k >> 1][k & 1] = x - X::SW * (done + item) - max(0, in - (per - X::SW));
-      if ((k & 1) == 0) {
-        const int u = group_of(e);
-        Schedule& o = out[k >> 1];
-        o.u = u;
-        o.b = e == u + gs[u] ? -1 : e - u - 1;
-        o.off = off;
+      while (hi - e > 1) {
+        const int mid = (e + hi) >> 1;
+        if (cost[mid] <= x) e = mid; else hi = mid;
       }
+      off = x - cost[e];
+      const int per = (cost[e + 1] - cost[e]) / (items[e + 1] - items[e]);     // T + SW
+      const int item = off / per, in = off - item * per;
+      before = x - X::SW * (items[e] + item) - max(0, in - (per - X::SW));
     }
-  }
-  __syncthreads();
-  if (tid < TEAMS) {
-    const int v = v0 + tid * vstep;
-    Schedule& o = out[tid];
-    o.lo = v < used ? v * q + min(v, rem) : total;
-    o.hi = v < used ? (v + 1) * q + min(v + 1, rem) : total;
-    o.q = q;
-    o.rem = rem;
-    o.tiles = o.lo < o.hi ? s_before[tid][1] - s_before[tid][0] : 0;
+    const int x1 = __shfl_down_sync(0xffffffffu, x, 1), before1 = __shfl_down_sync(0xffffffffu, before, 1);
+    if (lane < 2 * TEAMS && (lane & 1) == 0) {
+      const int u = group_of(e);
+      Schedule& o = out[lane >> 1];
+      o.u = u;
+      o.b = e == u + gs[u] ? -1 : e - u - 1;
+      o.off = off;
+      o.lo = v < used ? x : total;
+      o.hi = v < used ? x1 : total;
+      o.q = q;
+      o.rem = rem;
+      o.tiles = o.lo < o.hi ? before1 - before : 0;
+    }
   }
 }
 
@@ -438,7 +425,7 @@ struct Walk {
   }
   __device__ __forceinline__ void load_unit() {
     if (b < 0) {
-      t = shared_unit<X>(p, b0, b1, S);
+      t = shared_unit<X>(p, b0, b1, S, p.cu);
     } else {
       const int prefix = p.prefix_len[b];
       const SeqSpan sp = seq_span(p.cu, p.tree_len, b, p.N, p.T);
@@ -1430,7 +1417,7 @@ template <int NT, int D>
 jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& kr,
                        const CUtensorMap& vr, const SharedParams& prm, cudaStream_t s) {
   using C = Cfg<NT, D>;
-  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1025), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= schedule_bytes(kSharedMaxB, kSharedMaxB) + 1024, "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_attention_kernel<NT, D>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_attention_kernel<NT, D>, dim3(static_cast<unsigned>(prm.ranges)), dim3(C::kThreads),
@@ -1442,7 +1429,7 @@ jf_status launch_tiles(const CUtensorMap& qm, const CUtensorMap& km, const CUten
 template <int D, int MT>
 jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const SharedParams& prm, cudaStream_t s) {
   using C = RowCfg<D, MT>;
-  static_assert(C::kSmemBytes >= 4 * (8 * kSharedMaxB + 1025), "the schedule's scratch fits");
+  static_assert(C::kSmemBytes >= schedule_bytes(kSharedMaxB, kSharedMaxB) + 1024, "the schedule's scratch fits");
   static SmemAttr attr;
   if (!attr.ensure(shared_rows_kernel<D, MT>, C::kSmemBytes)) return JF_ERR_CUDA;
   return launch_pdl(shared_rows_kernel<D, MT>, dim3(static_cast<unsigned>(prm.ranges / C::kTeams)),
