@@ -1215,15 +1215,15 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 
 // The pieces of a (node, query head) row's shared and own parts, listed by ws_desc, merged by
 // log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap (four rows for two: 144 us for
-// 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps taking every eighth piece.
+// 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps sharing out the pieces.
 // Rows behind the last sequence keep what they hold.  What ws_desc says is checked against
 // the workspace: a malformed group_start or span leaves it unwritten.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
+template <int D, int ROWS, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
   constexpr int E = D / 32;
-  constexpr int kWarps = 8;
+  constexpr int kWarps = WARPS;
   constexpr int kStep = ROWS == 1 ? kWarps : 1;       // pieces a warp skips
-  constexpr int kBatch = ROWS == 1 ? 4 : 2;           // pieces of a row whose reads overlap
+  constexpr int kBatch = ROWS == 1 ? 6 : 2;           // pieces of a row whose reads overlap
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ float s_part[ROWS == 1 ? kWarps : 1][D + 2];
   grid_dependency_wait();
@@ -1441,13 +1441,14 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 template <int D>
 jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
   // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
-  // pieces: 4 beams 13.6 us against 21.2, 64 requests 74 against 79), else two rows a warp (16 trees 131
-  // us against 189, 256 beams 92 against 108).
+  // pieces: 4 beams 13.6 us against 21.2, 64 requests 74 against 79), of eight warps while all blocks
+  // are resident (4 beams 12.4, with four 13.7), else of four (64 requests 71.4, with eight 74.6); beyond
+  // that two rows a warp (16 trees 131 us against 189, 256 beams 92 against 108).
   const long long rows = prm.rows;
-  const cudaError_t e =
-      rows <= 32ll * sms
-          ? launch_pdl(shared_merge_kernel<D, 1>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, prm, total)
-          : launch_pdl(shared_merge_kernel<D, 2>, dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, s, prm, total);
+  const dim3 each(static_cast<unsigned>(rows)), half(static_cast<unsigned>((rows + 15) / 16));
+  const cudaError_t e = rows <= 4ll * sms    ? launch_pdl(shared_merge_kernel<D, 1, 8>, each, dim3(256), 0, s, prm, total)
+                        : rows <= 32ll * sms ? launch_pdl(shared_merge_kernel<D, 1, 4>, each, dim3(128), 0, s, prm, total)
+                                             : launch_pdl(shared_merge_kernel<D, 2, 8>, half, dim3(256), 0, s, prm, total);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
