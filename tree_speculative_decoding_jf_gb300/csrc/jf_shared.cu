@@ -302,7 +302,8 @@ struct Piece {
 // role has then left the pieces up to the third before it.
 constexpr int kPieces = 4;
 // A change of item costs the tcgen05 kernel four to six tiles' time: the next item's Q and K arrive, the
-// rows leave TMEM (16 trees: 2 161 us, 4 129, 6 130, 8 134).
+// rows leave TMEM (16 trees of up to 64 nodes: 3 130 us, 4 118, 5 119, 6 120; of up to 256: 4 317, 5 303,
+// 6 300; 128 beams in two groups over 16K keys: 4 69.6, 5 66.4, 6 63.9).
 constexpr int kTileSwitch = 6;
 template <int NT>
 using TileCut = Cut<NT * kRowTile, kKeyTile, kTileSwitch, 1>;
@@ -881,11 +882,14 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // Its time is the latency of a page's chain (products, maximum, exponentials, products) at two warps a
 // scheduler: issue slots 42% busy, HBM 66%.  Two pages a step (103 us for 256 beams against 91), four
 // accumulators for the scores (93) and V's fragments kept for the second product (92) gained nothing.
-constexpr int kRowSwitch = 4;           // pages (256 beams: 2 98 us, 4 92, 8 102)
+// A change of item, in pages: what it costs is the same for both head dimensions, a page at D = 64 half
+// (256 beams, D = 128: 2 98 us, 3 86, 4 88, 8 98; D = 64: 3 70, 4 66, 5 63; 16 groups of them: 3 73, 4 71, 5 74).
+template <int D>
+constexpr int kRowSwitch = D == 128 ? 3 : 4;
 constexpr int kRowLeast = 4;            // pages (4 beams over 2K keys: 1 17.2 us, 2 14.3, 4 13.6, 8 15.6)
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
-template <int MT>
-using RowCut = Cut<16 * MT, kPage, kRowSwitch, kRowLeast>;
+template <int D, int MT>
+using RowCut = Cut<16 * MT, kPage, kRowSwitch<D>, kRowLeast>;
 
 template <int D, int MT>
 struct RowCfg {
@@ -918,7 +922,7 @@ template <int D, int MT>
 __global__ void __launch_bounds__(64 * kRowWarps, 1)
     shared_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ SharedParams p) {
-  using X = RowCut<MT>;
+  using X = RowCut<D, MT>;
   using C = RowCfg<D, MT>;
   constexpr int kTeams = C::kTeams, kS = C::kStages;
   constexpr int kI = D / 32;            // 16-byte chunks of a row per thread (scores)
