@@ -13,7 +13,7 @@
 // Work.  A unit is a group's shared part or a sequence's own part; an item is a unit, a
 // kv-head and a row tile.  Items lie end to end, T key tiles plus X::SW for the change of item,
 // and are cut into equal ranges: lengths and group sizes are data, so every CTA forms the same
-// schedule from them (3 to 4 us, mostly its instructions' way from memory) and walks its ranges.
+// schedule from them (about 3 us, a chain of barriers and of shared-memory reads) and walks its ranges.
 // Every piece leaves normalised fp32 rows and their log-sum-exp: whole items in the rows' own
 // slots (shared and own part apart), items that a range boundary cuts in the range's slots 0 (cut
 // at its start) and 1; the first piece of an item tells each of its rows where its pieces are.
@@ -24,12 +24,12 @@
 //     with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer, MMA issuer,
 //     vouchers, softmax warpgroups, all counters running over the range's tiles as one sequence).
 //     A step of 128 keys takes 1.7 us, 78% of the tensor rate while it lasts: packed trees of 16
-//     sequences over 8K shared keys, 106 GFLOP, take 121 us in all (0.87 PFLOP/s; rows that fill their
+//     sequences over 8K shared keys, 106 GFLOP, take 120 us in all (0.89 PFLOP/s; rows that fill their
 //     last tile in part, the prologue and the merge are the rest).
 //   shared_rows_kernel (below): 16 to 64 rows an item, bound by the K/V stream: 256 beams in 32
-//     groups over 4K keys take 91 us, 4.5 TB/s.
+//     groups over 4K keys take 86 us, 4.7 TB/s.
 // jf_tree_attention on the same inputs reads a prefix once per sequence and takes 566 us for the
-// beams, 695 us for 64 sequences over 32K shared keys (here 74).
+// beams, 695 us for 64 sequences over 32K shared keys (here 72).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -877,10 +877,11 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 // 8 KB per SM at D = 128, some 190 KB, where the HBM rate needs about 40.
 //   Scores: m16n8k16 products.  A thread's 16-byte chunks 2 (lane % 4) + {0, 1} of a K row (key lane / 4 of
 //   eight) are two k-steps' B fragments if Q's chunks are cut the same way: the order of the
-//   contraction is free.
+//   contraction is free.  (Under the 128-byte swizzle the eight lanes of a phase then hit all banks; with
+//   chunks lane % 4 + 4 i two rows collide, 186 us for four groups of 64 rows over 32K keys against 181.)
 //   Output: V's fragments come transposed from shared memory (ldmatrix), two n-tiles at a time.
 // Its time is the latency of a page's chain (products, maximum, exponentials, products) at two warps a
-// scheduler: issue slots 42% busy, HBM 66%.  Two pages a step (103 us for 256 beams against 91), four
+// scheduler: issue slots 43% busy, HBM 69%.  Two pages a step (103 us for 256 beams against 91), four
 // accumulators for the scores (93) and V's fragments kept for the second product (92) gained nothing.
 // A change of item, in pages: what it costs is the same for both head dimensions, a page at D = 64 half
 // (256 beams, D = 128: 2 98 us, 3 86, 4 88, 8 98; D = 64: 3 70, 4 66, 5 63; 16 groups of them: 3 73, 4 71, 5 74).
@@ -1378,8 +1379,8 @@ bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int H
 }
 
 // Which kernel takes which units.  Up to 64 rows a group (on average) the row kernel takes both parts:
-// the K/V stream bounds it (four groups of 64 rows over 32K keys: 186 us, on the tcgen05 kernel 265; 32
-// rows fill two warps, 92 us for 256 beams against 125 with one warp twice).  Groups of more rows
+// the K/V stream bounds it (four groups of 64 rows over 32K keys: 176 us, on the tcgen05 kernel 265; 32
+// rows fill two warps, 98 us for 256 beams against 125 with one warp twice).  Groups of more rows
 // have their shared parts on the tcgen05 kernel, two row tiles per CTA (each key tile loaded feeds
 // both) once they fill more than one, and so have own parts of more than 64 rows.
 SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, int D, int sms) {
