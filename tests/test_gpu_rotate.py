@@ -148,6 +148,15 @@ def test_norm_of_zero_and_of_large_heads(jf):
     check(w, "padded", False, 1.0, got, kc, vc, norm_eps=1e-5)
 
 
+@pytest.mark.parametrize("alone", ["wq", "wk"])
+def test_one_norm_alone(jf, alone):
+    for R in (0, 64):
+        w = make(2, 11, 6, 2, 128, [11, 4], [3, 20], seed=12, R=R, norm=True)
+        w[alone] = None
+        got, kc, vc = call(jf, w, "ragged", False, 1.0)
+        check(w, "ragged", False, 1.0, got, kc, vc)
+
+
 def test_packed_equals_padded(jf):
     w = make(5, 40, 8, 2, 128, [40, 1, 17, 39, 2], [0, 15, 16, 100, 31], seed=4, R=64, norm=True)
     a, ka, va = call(jf, w, "ragged", False, 1.0)

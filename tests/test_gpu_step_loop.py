@@ -252,3 +252,48 @@ def test_beams_over_shared_prompts(jf):
                 want_count[t] += 1
             assert torch.equal(count[r].cpu(), want_count), (s, r)
     assert saw_sharing > steps
+
+
+def test_new_tensors_on_a_side_stream(jf):
+    """Calls that make their outputs and workspaces, given a stream: the same bits as on the current one, and
+    padding rows are zero."""
+    g = torch.Generator().manual_seed(8)
+    B, N, Hq, Hkv, D, V = 3, 5, 4, 2, 64, 1000
+    q, k, v = (torch.randn((B, N, H, D), generator=g).to(torch.bfloat16).cuda() for H in (Hq, Hkv, Hkv))
+    table = torch.arange(B * 4, dtype=torch.int32).view(B, 4)
+    table[1:, :2] = table[0, :2]                     # two shared pages
+    lens = torch.tensor([33, 40, 50], dtype=torch.int32).cuda()
+    sizes = torch.tensor([5, 1, 3], dtype=torch.int32).cuda()
+    kc, vc = (torch.randn((B * 4, 16, Hkv, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    _, sees = ref.random_trees(B, N, g)
+    mask, table = ref.pack_bits(sees).cuda(), table.cuda()
+    pos = torch.randint(0, 100, (B, N), generator=g, dtype=torch.int32).cuda()
+    freq, scale = jf.rotary_frequencies(D)
+    start, pages = torch.tensor([0, B], dtype=torch.int32).cuda(), torch.tensor([2], dtype=torch.int32).cuda()
+    x = torch.randn((B, N, V), generator=g).cuda()
+    draft = torch.randint(0, V, (B, N), generator=g, dtype=torch.int32).cuda()
+    rep = torch.full((B,), 1.5).cuda()
+
+    def step(stream):
+        count = jf.count_tokens(None, draft, length=sizes, prompt=True, V=V, stream=stream)
+        k2, v2 = kc.clone(), vc.clone()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        turned = jf.rotate_append_kv(q, k, v, k2, v2, table, lens, pos=pos, freq=freq, rotary_scale=scale,
+                                     tree_len=sizes, stream=stream)
+        out, lse = jf.tree_attention_shared(turned, k2, v2, table, lens, mask, start, pages, with_lse=True,
+                                            tree_len=sizes, stream=stream)
+        y = jf.adjust_logits(x, count=count, draft=draft, mask=mask, repetition=rep, tree_len=sizes, stream=stream)
+        torch.cuda.synchronize()
+        return count, turned, out, lse, y, k2, v2
+
+    want = step(None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        got = step(stream if stream is side else torch.cuda.ExternalStream(stream))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    count, turned, out, lse, y = want[:5]
+    for b, n in enumerate(sizes.tolist()):
+        assert not turned[b, n:].any() and not out[b, n:].any() and not y[b, n:].any() and not lse[b, :, n:].any()
+        assert turned[b, :n].any() and out[b, :n].any() and y[b, :n].any()
