@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     tma_prefetch_desc(&vmap_run);
   }
   grid_dependency_wait();
-  grid_dependents_launch();             // the own parts' kernel may run beside this one; others wait for it
+  grid_dependents_launch();             // whatever follows waits for all of this one before it reads or writes
   make_schedule<TileCut<NT>, 1>(p, v, 1, v == 0 ? p.dev_err : nullptr, reinterpret_cast<int*>(sm), &s_sch);
   fence_proxy_async_smem();             // the scratch becomes the target of TMA copies
   if (warp == 1) {
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
-  if (p.kinds & kShared) grid_dependency_wait();    // else: beside the shared parts' kernel, which waited (see below)
+  grid_dependency_wait();               // (of own parts alone too: behind the shared parts' kernel)
   grid_dependents_launch();
   // (Consecutive ranges lie on different SMs: small calls reach them all.)
   make_schedule<X, kTeams>(p, blockIdx.x, gridDim.x, blockIdx.x == 0 && p.kinds == (kShared | kOwn) ? p.dev_err : nullptr,
@@ -1210,10 +1210,6 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     }
     if (!ok && s_sch[team].tiles > 0 && lane == 0) set_abort(abort, p.dev_err);
   }
-  // A launch of own parts alone runs beside the shared parts' kernel (which lets it start once all its
-  // CTAs have seen their inputs): it must not be complete before that one is, for what follows
-  // waits for this one.
-  if (!(p.kinds & kShared)) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------------ the merge
