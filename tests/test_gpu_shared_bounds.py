@@ -1,0 +1,55 @@
+"""Shared pages right up to the block table's end: ragged and packed trees far smaller than N, tables that end
+with the longest sequence, entries of the other rows that must not be read."""
+import pytest
+import torch
+
+from test_gpu_shared import PAGE, call, check, ints, jf, make, new_err  # noqa: F401  (jf: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def tight(w):
+    """The same sequences under a table that ends with the longest of them."""
+    wide = max(-(-(p + n) // PAGE) for p, n in zip(w["lens"], w["sizes"]))
+    return dict(w, table=w["table"][:, :wide].contiguous(), real=w["real"][:, :wide].contiguous())
+
+
+# name, groups, N, Hq, Hkv, D, shared pages, own tokens, nodes.  "rows" runs in the kernel of few rows alone,
+# "tiles" in that of many alone, "pair" has shared parts in the one and own parts in the other.
+TIGHT = [
+    ("rows", [2, 1], 32, 2, 2, 128, [10, 6], [0, 0, 4], [1, 1, 32]),
+    ("rows", [4], 16, 4, 4, 64, [6], [4, 0, 3, 9], [4, 4, 4, 4]),
+    ("rows", [3, 2], 12, 2, 2, 64, [9, 9], [0, 3, 15, 7, 1], [1, 2, 1, 12, 3]),
+    ("tiles", [2, 1], 64, 8, 2, 128, [10, 6], [0, 0, 4], [1, 1, 64]),
+    ("tiles", [3, 3], 40, 16, 2, 64, [20, 17], [0, 5, 15, 33, 0, 1], [1, 3, 2, 1, 40, 9]),
+    ("pair", [12], 16, 8, 2, 128, [9], [b % 16 for b in range(12)], [1 + b % 4 for b in range(12)]),
+    ("pair", [9, 8], 8, 16, 2, 64, [30, 30], [3 * b % 16 for b in range(17)], [1 + b % 3 for b in range(17)]),
+]
+
+
+@pytest.mark.parametrize("layout", ["ragged", "packed"])
+@pytest.mark.parametrize("case", range(len(TIGHT)), ids=["%s%d" % (c[0], i) for i, c in enumerate(TIGHT)])
+def test_tables_that_end_with_the_longest_sequence(jf, case, layout):  # noqa: F811
+    _, groups, N, Hq, Hkv, D, pages, own, sizes = TIGHT[case]
+    w = tight(make(groups, N, Hq, Hkv, D, pages, own, seed=200 + case, sizes=sizes))
+    err = new_err()
+    out, lse = call(jf, w, layout, err)
+    assert err.item() == 0
+    check(w, layout, out, lse)
+    old = w["table"].clone()                       # pages of other sequences in their place: not read either
+    w["table"] = torch.where(old < 0, torch.full_like(old, int(w["real"][-1, 0])), old)
+    again, lse2 = call(jf, w, layout, err)
+    assert err.item() == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_shared_pages_past_what_a_sequence_has(jf):  # noqa: F811
+    """Shared pages up to the table's end leave no room for the trees: reported, in bounds, the other group right."""
+    for N, Hq in ((2, 4), (40, 16)):
+        w = make([3, 2], N, Hq, 2, 64, [4, 2], [5, 6, 7, 8, 9], seed=210)
+        cap = w["table"].shape[1]
+        for pages in (cap, cap + 1):
+            err = new_err()
+            out, lse = call(jf, dict(w, pages=[pages, 2]), "padded", err)
+            want = jf.DEVERR_BAD_PREFIX | (jf.DEVERR_BAD_GROUP if pages > cap else 0)
+            assert err.item() == want, pages
+            check(w, "padded", out, lse, only={3, 4})

@@ -78,10 +78,11 @@ constexpr int kShared = 1, kOwn = 2;
 // ------------------------------------------------------------------------ the schedule
 
 // Keys that a group's sequences share, of its shared_pages entry: none when it has one sequence
-// (nothing to share).
+// (nothing to share).  The block table alone bounds them: how many nodes follow is each
+// sequence's own matter, and most have fewer than N.
 __device__ __forceinline__ int group_keys(const SharedParams& p, int pages, int b0, int b1) {
   if (b1 - b0 < 2) return 0;
-  return max(0, min(pages, (p.max_pages * kPage - p.N) / kPage)) * kPage;
+  return max(0, min(pages, p.max_pages)) * kPage;
 }
 
 // One unit: rows f0 .. f0 + nr - 1 of q's nodes attend to keys key0 .. L - 1 of block-table row
@@ -117,8 +118,11 @@ template <typename X>
 __device__ __forceinline__ Unit own_unit(const SharedParams& p, int b, int S, int prefix, int row0, int n) {
   Unit t;
   t.bt = b;
-  t.key0 = S;
-  t.P = max(S, min(prefix, p.max_pages * kPage - n));
+  // (A sequence whose nodes have no room behind S is malformed, its P < S or its keys past the table: it
+  // starts where they do have room.)
+  const int last = p.max_pages * kPage - n;
+  t.key0 = min(S, last / kPage * kPage);
+  t.P = max(t.key0, min(prefix, last));
   t.L = t.P + n;
   t.f0 = row0;
   t.nr = n;
