@@ -740,6 +740,7 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
  *                most floor(P_b / page_size) of each of its sequences; 0: nothing is shared.
  *   q, k_cache, v_cache, block_table, prefix_len, mask, scale, out, lse
  *                as in jf_tree_attention, whose results these are (merged in another order).
+ *                A (row, head) that sees a NaN or a +inf score has NaN in out and lse.
  *                out must not overlap q or the caches.
  *   tree_len     int32 [B] or NULL: ragged trees as in jf_tree_attention_ragged, but rows
  *                i >= tree_len[b] of out and lse are left as they were.

@@ -817,8 +817,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
         break;
       }
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m_run + __log2f(l) : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m_run + __log2f(l);
       const bool valid = r < c.nrows, direct = c.direct;
       const int row = (c.node0 + (valid ? r / p.G : 0)) * p.Hq + c.g * p.G + r % p.G;    // (node, head)
       const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
@@ -1199,8 +1199,8 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         const int row = (half == 0 ? na : nb) * p.Hq + c.g * p.G + r % p.G;
         const float l = half == 0 ? la : lb, m = half == 0 ? ma : mb;
         if (!mine) continue;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float lse2 = l == 0.f ? -INFINITY : m + __log2f(l);
         const int prow = c.whole ? (c.b < 0 ? 0 : p.rows) + row : c.slots + r;
 #pragma unroll
         for (int j = 0; j < 8 * kH; ++j) {           // four lanes write a sector of the row
@@ -1221,8 +1221,9 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 // The pieces of a (node, query head) row's shared and own parts, listed by ws_desc, merged by
 // log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap (four rows for two: 144 us for
 // 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps sharing out the pieces.
-// Rows behind the last sequence keep what they hold.  What ws_desc says is checked against
-// the workspace: a malformed group_start or span leaves it unwritten.
+// A piece that saw a NaN or an infinite score has a NaN log-sum-exp and makes its row NaN; one whose keys were
+// all hidden has -inf and is passed over.  Rows behind the last sequence keep what they hold.  What ws_desc
+// says is checked against the workspace: a malformed group_start or span leaves it unwritten.
 template <int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
   constexpr int E = D / 32;
@@ -1289,8 +1290,7 @@ __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_c
     for (int k = 0; k < ROWS; ++k) {
       float top = m[k];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, l[k][j]);
-      if (top == -INFINITY) continue;            // nothing yet that saw a key
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, l[k][j]);      // (passes a NaN by: its weight is one)
       const float f0 = m[k] == -INFINITY ? 0.f : exp2f(m[k] - top);
       m[k] = top;
       sum[k] *= f0;
@@ -1323,7 +1323,7 @@ __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_c
     for (int e = 0; e < E; ++e) acc[0][e] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (s_part[w][D] == -INFINITY) continue;
+      if (s_part[w][D + 1] == 0.f) continue;     // nothing that saw a key
       const float f = exp2f(s_part[w][D] - top);
       sum[0] = fmaf(f, s_part[w][D + 1], sum[0]);
 #pragma unroll
@@ -1333,7 +1333,7 @@ __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_c
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     if (n[k] == 0) continue;
-    const float inv = sum[k] > 0.f ? 1.f / sum[k] : 0.f;
+    const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
     uint32_t y[E / 2];
 #pragma unroll
     for (int e = 0; e < E; e += 2) y[e / 2] = pack_bf16x2(acc[k][e] * inv, acc[k][e + 1] * inv);
@@ -1344,7 +1344,7 @@ __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_c
       const int node = row[k] / p.Hq, h = row[k] - node * p.Hq, b = node / p.N;
       p.lse[p.cu != nullptr ? static_cast<size_t>(h) * p.T + node
                             : (static_cast<size_t>(b) * p.Hq + h) * p.N + (node - b * p.N)] =
-          (sum[k] > 0.f ? m[k] + __log2f(sum[k]) : -INFINITY) * 0.69314718055994531f;
+          (sum[k] == 0.f ? -INFINITY : m[k] + __log2f(sum[k])) * 0.69314718055994531f;
     }
   }
 }
