@@ -753,7 +753,8 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
  * The order of every sum is fixed by the call's sizes and data: the same call gives the same bits.
  * Limits: as jf_tree_attention, and B <= 4096, 1 <= n_groups <= B.
  * jf_tree_attention_shared_packed takes the packed layout (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
- * q and out [T][Hq][D], mask [T][W], lse [Hq][T]); a bad span may spoil the rows of its group.
+ * q and out [T][Hq][D], mask [T][W], lse [Hq][T]); a bad span may spoil the rows of its group, and
+ * with a cu_seqlens that descends no row is computed (_BAD_TREE_LEN; out and lse are unspecified).
  * The workspace size takes T = 0 for the padded call, the number of packed rows otherwise.
  */
 size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, int32_t T, int32_t n_groups,

@@ -53,3 +53,31 @@ def test_shared_pages_past_what_a_sequence_has(jf):  # noqa: F811
             want = jf.DEVERR_BAD_PREFIX | (jf.DEVERR_BAD_GROUP if pages > cap else 0)
             assert err.item() == want, pages
             check(w, "padded", out, lse, only={3, 4})
+
+
+def test_descending_spans(jf):  # noqa: F811
+    """Spans that go back and overlap: nothing is computed, whatever their sum (here several times 2^31 positions)."""
+    w = make([2, 2], 4, 4, 1, 64, [4, 2], [20, 6, 30, 8], seed=211)
+    B, N, Hq, Hkv, D = w["shape"]
+    want, _ = call(jf, w, "packed")
+    q, mask = w["q"].flatten(0, 1).cuda(), w["mask"].flatten(0, 1).cuda()
+    rest = (w["kc"].cuda(), w["vc"].cuda(), w["table"].cuda(), ints(w["lens"]), mask, ints(w["start"]), ints(w["pages"]))
+    for cu in ([0, 4, 8, 4, 8], [4, 0, 4, 8, 12], [0, 4, 8, 12, 11], [0, 16, 0, 16, 0]):
+        err = new_err()
+        jf.tree_attention_shared(q, *rest, cu_seqlens=ints(cu), N_max=N, dev_err=err)
+        assert err.item() == jf.DEVERR_BAD_TREE_LEN, cu
+    err = new_err()
+    jf.tree_attention_shared(q, *rest[:5], ints([0, 3, 2]), rest[6], cu_seqlens=ints([0, 4, 8, 4, 8]), N_max=N, dev_err=err)
+    assert err.item() == jf.DEVERR_BAD_TREE_LEN | jf.DEVERR_BAD_GROUP
+    B, T, H, wide = 128, 4096, 128, 8192
+    big = torch.zeros((T, H, 64), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((8, PAGE, H, 64), dtype=torch.bfloat16, device="cuda")
+    err = new_err()
+    jf.tree_attention_shared(big, pool, pool, torch.zeros((B, wide), dtype=torch.int32, device="cuda"),
+                             ints([wide * PAGE - T] * B), torch.zeros((T, T // 64), dtype=torch.int64, device="cuda"),
+                             ints(list(range(B + 1))), ints([0] * B), cu_seqlens=ints([T * (b % 2) for b in range(B + 1)]),
+                             N_max=T, dev_err=err)
+    assert err.item() & jf.DEVERR_BAD_TREE_LEN
+    err = new_err()
+    out = jf.tree_attention_shared(q, *rest, cu_seqlens=ints(list(range(0, 17, 4))), N_max=N, dev_err=err)
+    assert err.item() == 0 and torch.equal(out, want)

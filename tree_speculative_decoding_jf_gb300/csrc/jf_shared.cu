@@ -162,7 +162,7 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
   __shared__ int s_items[32];
   // (Nothing here is unrolled: it runs once, and what it costs is mostly the instructions' own trip
   // from memory and the barriers.)  One trip for all the data that the schedule depends on.
-  bool bad = false;                  // group_start is not a partition
+  bool bad = false, down = false;    // group_start is not a partition; cu descends
 #pragma unroll 1
   for (int u = tid; u < ng; u += nth) {
     const int g0 = p.group_start[u], g1 = p.group_start[u + 1];
@@ -177,15 +177,15 @@ __device__ __forceinline__ void make_schedule(const SharedParams& p, int v0, int
     const SeqSpan span = seq_span(p.cu, p.tree_len, b, p.N, p.T);
     nn[b] = span.n | (span.ok ? 0 : kClamped);
     if (p.cu != nullptr) {
-      cs[b] = p.cu[b];
-      if (b == B - 1) cs[B] = p.cu[B];
+      const int r0 = p.cu[b], r1 = p.cu[b + 1];
+      cs[b] = r0;
+      if (b == B - 1) cs[B] = r1;
+      down = down || r0 > r1;        // (spans that overlap could add up to more positions than 32 bits hold)
     }
   }
   if (tid < TEAMS) out[tid].tiles = out[tid].lo = out[tid].hi = 0;
-  if (__syncthreads_or(bad)) {       // no work at all
-    if (tid == 0 && err != nullptr) report(err, JF_DEVERR_BAD_GROUP);
-    return;
-  }
+  if (err != nullptr && (bad || down)) report(err, (bad ? JF_DEVERR_BAD_GROUP : 0) | (down ? JF_DEVERR_BAD_TREE_LEN : 0));
+  if (__syncthreads_or(bad || down)) return;       // no work at all
   auto group_of = [&](int e) {       // of unit e: unit u + gs[u] is group u's shared part
     int u = 0, hi = ng;
 #pragma unroll 1
