@@ -751,7 +751,12 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
  *                _BAD_PREFIX (P_b < S or P_b + n_b past the block table), _BAD_PAGE,
  *                _BAD_TREE_LEN, _TIMEOUT.  May be NULL.
  * The order of every sum is fixed by the call's sizes and data: the same call gives the same bits.
- * Limits: as jf_tree_attention, and B <= 4096, 1 <= n_groups <= B.
+ * Limits: as jf_tree_attention, and B <= 4096, 1 <= n_groups <= B; 2 M Hq < 2^31 - 2^20 with M = B * N (packed:
+ * T); and a schedule in 32 bits, with r = M G / n_groups rows a group:
+ *     r <= 64:  Hkv * (2 M G / R + B + n_groups) * (max_pages + 4) < 2^31,
+ *               R = 16 (r <= 16), 32 (r <= 32) or 64
+ *     r > 64:   Hkv * (2 M G / R + B + n_groups) * (max_pages / 8 + 7) < 2^31, R = 128 (r <= 128) or 256,
+ *               and for trees of N G <= 64 rows the first line with n_groups = 0, M G in place of 2 M G and r = N G.
  * jf_tree_attention_shared_packed takes the packed layout (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
  * q and out [T][Hq][D], mask [T][W], lse [Hq][T]); a bad span may spoil the rows of its group, and
  * with a cu_seqlens that descends no row is computed (_BAD_TREE_LEN; out and lse are unspecified).

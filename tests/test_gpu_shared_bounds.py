@@ -81,3 +81,15 @@ def test_descending_spans(jf):  # noqa: F811
     err = new_err()
     out = jf.tree_attention_shared(q, *rest, cu_seqlens=ints(list(range(0, 17, 4))), N_max=N, dev_err=err)
     assert err.item() == 0 and torch.equal(out, want)
+
+
+def test_wide_tables(jf):  # noqa: F811
+    """Tables of 2^20 pages: the positions that they could take fit in the schedule, and the results do not change."""
+    w = make([40, 24], 16, 32, 8, 64, [9, 20], [b % 40 for b in range(64)], seed=212)
+    out, lse = call(jf, w, "padded")
+    table = torch.full((64, 1 << 20), -9, dtype=torch.int32)
+    table[:, :w["table"].shape[1]] = w["table"]
+    err = new_err()
+    far, far_lse = call(jf, dict(w, table=table), "padded", err)
+    assert err.item() == 0 and torch.equal(out, far) and torch.equal(lse, far_lse)
+    check(w, "padded", out, lse, only={0, 39, 40, 63})

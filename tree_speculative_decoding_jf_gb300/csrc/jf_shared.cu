@@ -1364,18 +1364,15 @@ constexpr int kMaxRanges = 1024;   // SMs that the 32-bit limits allow for
 constexpr int kRowKernelRows = 64; // rows of a unit up to which the row kernel takes it
 
 // nodes: B * N padded, T packed.
-bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, int D, int max_pages,
-                      int page_size) {
+bool shared_sizes(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, int D, int max_pages,
+                  int page_size) {
   if (B < 1 || B > kSharedMaxB || N < 1 || N > JF_MAX_NODES || nodes < 1 || Hq < 1 || Hkv < 1 || max_pages < 1) return false;
   if (n_groups < 1 || n_groups > B || (D != 64 && D != 128) || page_size != kPage || Hq % Hkv != 0) return false;
   const int G = Hq / Hkv;
   if (G > kRowTile || (G & (G - 1)) != 0) return false;
   if (static_cast<long long>(max_pages) * kPage < N || static_cast<long long>(max_pages) * kPage > (1ll << 30)) return false;
-  // workspace rows and positions of the schedule are 32-bit
-  const long long tiles = static_cast<long long>(max_pages) + 5;
-  const long long groups = nodes * G / 16 + B + n_groups;
-  return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX && 2 * groups <= INT_MAX / (tiles * Hkv) &&
-         static_cast<long long>(B) * N * Hq < 8ll * INT_MAX;
+  // workspace rows are 32-bit
+  return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX;
 }
 
 // Which kernel takes which units.  Up to 64 rows a group (on average) the row kernel takes both parts:
@@ -1416,6 +1413,26 @@ SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, in
   pl.ws_bytes = static_cast<size_t>(pl.total) * (D + 1) * sizeof(float) +
                 static_cast<size_t>(2 * pl.rows) * sizeof(int4) + 128;
   return pl;
+}
+
+// Whether the schedule's positions fit in 32 bits in each kernel of the plan: every item counts as many key
+// tiles as the block table holds and a change of item, and a unit's last item may be part empty.
+bool positions_fit(const SharedPlan& pl, long long nodes, int B, int n_groups, int Hq, int Hkv, int D, int max_pages) {
+  auto fit = [&](int kinds, long long R, long long KT, int change) {
+    const long long filled = nodes * (Hq / Hkv) / R;
+    const long long items = (kinds & kShared ? filled + n_groups : 0) + (kinds & kOwn ? filled + B : 0);
+    return items <= INT_MAX / (((max_pages * kPage + KT - 1) / KT + change) * Hkv);
+  };
+  return (pl.tile_nt == 0 || fit(pl.tile_kinds, pl.tile_nt * kRowTile, kKeyTile, kTileSwitch)) &&
+         (pl.row_mt == 0 || fit(pl.row_kinds, pl.row_mt * 16, kPage, D == 128 ? kRowSwitch<128> : kRowSwitch<64>));
+}
+
+// The plan of a call on a device of so many SMs, if its sizes are supported.
+bool shared_supported(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, int D, int max_pages,
+                      int page_size, int sms, SharedPlan* pl) {
+  if (!shared_sizes(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return false;
+  *pl = plan_shared(nodes, N, n_groups, Hq, Hkv, D, sms);
+  return positions_fit(*pl, nodes, B, n_groups, Hq, Hkv, D, max_pages);
 }
 
 template <int NT, int D>
@@ -1472,15 +1489,15 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   if (cu != nullptr && static_cast<long long>(T) + N >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * kPage >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   const long long nodes = cu != nullptr ? T : static_cast<long long>(B) * N;
-  if (!shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return JF_ERR_UNSUPPORTED;
+  const int sms = current_sm_count();
+  SharedPlan pl;
+  if (!shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size, sms, &pl)) return JF_ERR_UNSUPPORTED;
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
       !aligned_to(mask, 8))
     return JF_ERR_MISALIGNED;
   const size_t qb = static_cast<size_t>(nodes) * Hq * D * 2, cb = static_cast<size_t>(num_pages) * kPage * Hkv * D * 2;
   if (overlap(out, qb, q, qb) || overlap(out, qb, k_cache, cb) || overlap(out, qb, v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
-  const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  const SharedPlan pl = plan_shared(nodes, N, n_groups, Hq, Hkv, D, sms);
   if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return JF_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned_to(workspace, 16)) return JF_ERR_MISALIGNED;
   const int G = Hq / Hkv;
@@ -1551,9 +1568,10 @@ extern "C" size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, 
                                                           int32_t Hq, int32_t Hkv, int32_t D, int32_t max_pages,
                                                           int32_t page_size) {
   const long long nodes = T > 0 ? T : static_cast<long long>(B) * N;
-  if (!jf::shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size)) return static_cast<size_t>(-1);
   const int sms = jf::current_sm_count();
-  return sms > 0 ? jf::plan_shared(nodes, N, n_groups, Hq, Hkv, D, sms).ws_bytes : static_cast<size_t>(-1);
+  jf::SharedPlan pl;
+  const bool ok = jf::shared_supported(nodes, B, N, n_groups, Hq, Hkv, D, max_pages, page_size, sms, &pl);
+  return ok && sms > 0 ? pl.ws_bytes : static_cast<size_t>(-1);
 }
 
 extern "C" jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache,
