@@ -93,3 +93,22 @@ def test_wide_tables(jf):  # noqa: F811
     far, far_lse = call(jf, dict(w, table=table), "padded", err)
     assert err.item() == 0 and torch.equal(out, far) and torch.equal(lse, far_lse)
     check(w, "padded", out, lse, only={0, 39, 40, 63})
+
+
+@pytest.mark.parametrize("groups,N,Hq,Hkv,D,pages,own,sizes", [
+    ([6, 3], 1, 8, 2, 128, [2, 1], [3, 0, 15, 7, 1, 2, 4, 0, 9], [1] * 9),       # single tokens, three pages at most
+    ([2, 2], 9, 8, 2, 64, [1, 0], [0, 1, 5, 0], [3, 9, 2, 1]),
+    ([3, 1], 30, 4, 1, 64, [12, 3], [2, 9, 0, 1], [30, 4, 17, 22]),
+    ([2, 3], 70, 16, 2, 128, [20, 9], [0, 5, 15, 33, 0], [70, 3, 2, 1, 40]),
+])
+def test_packed_rows_without_n_max(jf, groups, N, Hq, Hkv, D, pages, own, sizes):  # noqa: F811
+    w = tight(make(groups, N, Hq, Hkv, D, pages, own, seed=213, sizes=sizes))
+    q, mask = (torch.cat([x[b, :n] for b, n in enumerate(sizes)]).cuda() for x in (w["q"], w["mask"]))
+    cu = [0]
+    for n in sizes:
+        cu.append(cu[-1] + n)
+    err = new_err()
+    out, lse = jf.tree_attention_shared(q, w["kc"].cuda(), w["vc"].cuda(), w["table"].cuda(), ints(w["lens"]), mask,
+                                        ints(w["start"]), ints(pages), with_lse=True, cu_seqlens=ints(cu), dev_err=err)
+    assert err.item() == 0
+    check(w, "packed", out, lse)

@@ -88,3 +88,16 @@ def test_rows_of_the_workspace(lib):
     T = (2 ** 31 - 2 ** 20) // (2 * 128)
     assert not taken(status(lib, 4096, 4096, 128, 128, 64, 256, 4096, T=T))
     assert taken(status(lib, 4096, 4096, 128, 128, 64, 256, 4096, T=T - 1))
+
+
+def test_largest_tree_of_packed_rows():
+    """What the packed form takes for its largest tree where it is not told."""
+    from tree_speculative_decoding_jf_gb300 import build
+    build.build()
+    from tree_speculative_decoding_jf_gb300 import jf
+    #   T    B  pages words  nodes
+    for T, B, pages, words, want in [(7, 7, 1, 1, 1), (1, 1, 1, 1, 1), (20, 3, 100, 1, 18), (500, 3, 100, 1, 64),
+                                     (500, 3, 2, 1, 32), (500, 3, 100, 2, 128), (70, 3, 100, 2, 68),
+                                     (66, 3, 100, 2, 65), (5, 3, 100, 2, 65), (9000, 2, 1000, 64, 4096)]:
+        got = jf._largest_tree(T, B, pages, words)
+        assert got == want and (got + 63) // 64 == words, (T, B, pages, words)

@@ -1319,12 +1319,19 @@ def rotate_append_kv(q, k, v, k_cache, v_cache, block_table, prefix_len, pos=Non
     return out
 
 
+def _largest_tree(T, B, max_pages, words) -> int:
+    """The most nodes that one of B sequences in T packed rows can have: every other one has a row, the
+    block table holds them, and the mask has `words` words a row (which says at least 64 (words - 1) + 1)."""
+    return max(64 * (words - 1) + 1, min(64 * words, T - B + 1, PAGE_SIZE * max_pages))
+
+
 def tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, group_start, shared_pages, scale=None,
                           with_lse=False, tree_len=None, cu_seqlens=None, N_max=None, out=None, lse=None,
                           workspace=None, dev_err=None, stream=None):
     """Attention of sequences in groups that share a prefix; out, or (out, lse) with with_lse or a
     given lse.  New tensors' padding rows are zero.  With cu_seqlens the rows are packed; N_max is then
-    the largest tree (by default what mask's width allows)."""
+    the largest tree (by default the largest that mask's width, the table's and the number of rows,
+    one at least a sequence, allow)."""
     with_lse = with_lse or lse is not None
     if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
         with _as_current(stream):
@@ -1338,7 +1345,7 @@ def tree_attention_shared(q, k_cache, v_cache, block_table, prefix_len, mask, gr
         scale = D ** -0.5
     packed = cu_seqlens is not None
     if packed and N_max is None:
-        N_max = 64 * mask.shape[-1]
+        N_max = _largest_tree(shape[0], B, max_pages, mask.shape[-1])
     if out is None or (with_lse and lse is None):
         make = torch.zeros if packed or tree_len is not None else torch.empty
         if out is None:
