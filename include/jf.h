@@ -697,8 +697,8 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
  *   block_table, prefix_len, tree_len (may be NULL)  as in jf_tree_attention and its _ragged
  *                form; tokens i >= tree_len[b] are neither written nor do they change anything.
  *                Pages that take new tokens belong to one sequence (shared ones are forked first).
- *   q_out        bf16 [B][N][Hq][D]; may be q itself when q_stride == Hq * D.  Must not overlap
- *                k, v or, in another way, q; the caches must not overlap any input.
+ *   q_out        bf16 [B][N][Hq][D]; may be q itself when q_stride == Hq * D.  Must not otherwise
+ *                overlap an input; nor must the caches, or each other or q_out.
  *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + n_b past the block table: the sequence's
  *                keys and values are not written), _BAD_PAGE (the token's are not written),
  *                _BAD_TREE_LEN.  May be NULL.

@@ -1,0 +1,54 @@
+"""The calls around a step refuse outputs that share a byte with an input, with each other or with the workspace,
+whatever the array.  CPU only, and not even run where there is a device: nothing is dereferenced, and a call that
+were taken has no device to go on with."""
+import ctypes
+
+import pytest
+import torch
+
+P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+INVALID = 1
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would be launched")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from tree_speculative_decoding_jf_gb300 import build
+    return ctypes.CDLL(build.build())
+
+
+def at(n, by=0):
+    return ctypes.c_void_p((n << 32) + by)      # far apart, aligned, never dereferenced
+
+
+def none_overlap(fn, args, outputs, sizes, pairs=()):
+    """sizes: {argument: bytes} of every array.  An output's last 16 bytes over an array's first and its first over the
+    array's last are refused; so is an array that begins where the output does."""
+    for out in outputs:
+        for other, size in sizes.items():
+            if other == out or (out, other) in pairs:
+                continue
+            base = 40 << 32
+            for out_at, other_at in ((base, base), (base, base + sizes[out] - 16), (base + (size - 1) // 16 * 16, base)):
+                bad = list(args)
+                bad[out], bad[other] = ctypes.c_void_p(out_at), ctypes.c_void_p(other_at)
+                assert fn(*bad) == INVALID, (out, other, out_at - base, other_at - base)
+
+
+ROTATE = [P, i64, P, i64, P, i64, P, P, i32, i32, f32, P, P, f32, P, P, P]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_rotate(lib, packed):
+    B, N, T, Hq, Hkv, D, pages, wide = 2, 16, 30, 32, 8, 128, 99, 10
+    rows = T if packed else B * N
+    fn = lib.jf_rotate_append_kv_packed if packed else lib.jf_rotate_append_kv
+    fn.argtypes = ROTATE + [i32] * (9 if packed else 8) + [P] * 5
+    args = [at(1), Hq * D, at(2), Hkv * D, at(3), Hkv * D, at(4), at(5), D, 0, 1.0, at(6), at(7), 1e-6, at(8), at(9), at(10),
+            B, N] + [T] * packed + [Hq, Hkv, D, 16, wide, pages, at(11), at(12), at(13), None, None]
+    q_out = 26 if packed else 25
+    sizes = {0: rows * Hq * D * 2, 2: rows * Hkv * D * 2, 4: rows * Hkv * D * 2, 6: rows * 4, 7: D // 2 * 8, 11: D * 2, 12: D * 2,
+             14: B * wide * 4, 15: B * 4, 16: (B + packed) * 4, q_out: rows * Hq * D * 2, q_out + 1: pages * 16 * Hkv * D * 2,
+             q_out + 2: pages * 16 * Hkv * D * 2}
+    none_overlap(fn, args, [q_out + 1, q_out + 2], sizes)
+    none_overlap(fn, args, [q_out], {k: v for k, v in sizes.items() if k != 0})     # over q: in place

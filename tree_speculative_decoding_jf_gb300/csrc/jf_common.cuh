@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "jf.h"
@@ -18,6 +19,16 @@ inline bool aligned_to(const void* p, uintptr_t a) {
 inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
+struct Extent {
+  const void* at;      // null: not there
+  size_t bytes;
+};
+inline bool overlaps_any(const void* a, size_t a_bytes, std::initializer_list<Extent> others) {
+  for (const Extent& e : others)
+    if (e.at != nullptr && overlap(a, a_bytes, e.at, e.bytes)) return true;
+  return false;
 }
 
 inline jf_status launch_status() {

@@ -313,13 +313,18 @@ jf_status rotate_call(RotateParams p, int D, int page_size, bool inter, bool pac
   const size_t qb = p.q != nullptr ? ((rows - 1) * p.q_stride + qw) * 2 : 0, ob = rows * qw * 2;
   const size_t cb = static_cast<size_t>(p.num_pages) * kPage * kw * 2;
   if (overlap(p.k_cache, cb, p.v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
+  const size_t seqs = static_cast<size_t>(p.B), wb = static_cast<size_t>(D) * 2;
+  auto over_inputs = [&](const void* out, size_t bytes) {
+    return overlaps_any(out, bytes, {{p.k, kb}, {p.v, vb}, {p.freq != nullptr ? p.pos : nullptr, rows * 4},
+                                     {p.freq, static_cast<size_t>(p.R) * 4}, {p.q_norm, wb}, {p.k_norm, wb},
+                                     {p.block_table, seqs * p.max_pages * 4}, {p.prefix_len, seqs * 4},
+                                     {p.tree_len, seqs * 4}, {p.cu, (seqs + 1) * 4}});
+  };
   for (void* out : {static_cast<void*>(p.k_cache), static_cast<void*>(p.v_cache)}) {
-    if (overlap(out, cb, p.k, kb) || overlap(out, cb, p.v, vb)) return JF_ERR_INVALID_ARGUMENT;
-    if (p.q != nullptr && (overlap(out, cb, p.q, qb) || overlap(out, cb, p.q_out, ob)))
-      return JF_ERR_INVALID_ARGUMENT;
+    if (over_inputs(out, cb) || overlaps_any(out, cb, {{p.q, qb}, {p.q_out, ob}})) return JF_ERR_INVALID_ARGUMENT;
   }
   if (p.q != nullptr) {
-    if (overlap(p.q_out, ob, p.k, kb) || overlap(p.q_out, ob, p.v, vb)) return JF_ERR_INVALID_ARGUMENT;
+    if (over_inputs(p.q_out, ob)) return JF_ERR_INVALID_ARGUMENT;
     if (overlap(p.q_out, ob, p.q, qb) && !(p.q_out == p.q && p.q_stride == qw)) return JF_ERR_INVALID_ARGUMENT;
   }
   const int sms = current_sm_count();
