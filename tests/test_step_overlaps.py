@@ -52,3 +52,20 @@ def test_rotate(lib, packed):
              q_out + 2: pages * 16 * Hkv * D * 2}
     none_overlap(fn, args, [q_out + 1, q_out + 2], sizes)
     none_overlap(fn, args, [q_out], {k: v for k, v in sizes.items() if k != 0})     # over q: in place
+
+
+ADJUST = [P, i32, P, P, P, P, P, P, i32, P, P, P, f32, P]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_adjust(lib, packed):
+    B, N, T, V, allowed = 6, 70, 300, 1000, 9
+    rows = T if packed else B * N
+    fn = lib.jf_adjust_logits_packed if packed else lib.jf_adjust_logits
+    fn.argtypes = ADJUST + [i32] * (4 if packed else 3) + [P, i32, P, P]
+    args = [at(1), 0, at(2), at(3), at(4), at(5), at(6), at(7), allowed, at(8), at(9), at(10), -float("inf"), at(11),
+            B, N] + [T] * packed + [V, at(12), 0, None, None]
+    out = 18 if packed else 17
+    sizes = {2: B * V * 4, 3: rows * 4, 4: rows * 2 * 8, 5: B * V * 4, 6: allowed * 32 * 4, 7: rows * 4, 9: B * 4, 10: B * 4,
+             11: B * 4, 13: (B + packed) * 4, out: rows * V * 2}
+    none_overlap(fn, args, [out], sizes)

@@ -421,16 +421,17 @@ jf_status adjust_call(AdjustParams p, int32_t dtype, int32_t out_dtype, bool pac
   // The same array, or no shared byte: blocks read and write their own slices only.
   p.in_place = p.out == p.logits && isz == osz;
   if (!p.in_place && overlap(p.out, rows * p.V * osz, p.logits, rows * p.V * isz)) return JF_ERR_INVALID_ARGUMENT;
-  const size_t seq = static_cast<size_t>(p.B) * p.V * 4;
   p.words = (p.V + 31) / 32;
-  const size_t ob = rows * p.V * osz;
-  if ((p.count != nullptr && overlap(p.out, ob, p.count, seq)) ||
-      (p.bias != nullptr && overlap(p.out, ob, p.bias, seq)) ||
-      (p.allowed != nullptr && overlap(p.out, ob, p.allowed, static_cast<size_t>(p.n_allowed) * p.words * 4)))
+  p.W = (p.N + 63) / 64;
+  const size_t seqs = static_cast<size_t>(p.B), seq = seqs * p.V * 4;
+  if (overlaps_any(p.out, rows * p.V * osz,
+                   {{p.count, seq}, {p.bias, seq}, {p.draft, rows * 4}, {p.mask, rows * p.W * 8},
+                    {p.allowed, static_cast<size_t>(p.n_allowed) * p.words * 4}, {p.allowed_row, rows * 4},
+                    {p.repetition, seqs * 4}, {p.presence, seqs * 4}, {p.frequency, seqs * 4},
+                    {p.tree_len, seqs * 4}, {p.cu, (seqs + 1) * 4}}))
     return JF_ERR_INVALID_ARGUMENT;
   const int sms = current_sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
-  p.W = (p.N + 63) / 64;
   p.slices = (p.V + kSlice - 1) / kSlice;
   if (static_cast<long long>(p.B) * p.N * p.slices > 0x7FFFFFFFll) return JF_ERR_UNSUPPORTED;
   // Rows per block: 16, so that what a block does once weighs little, fewer while the grid would
