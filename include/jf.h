@@ -741,7 +741,7 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
  *   q, k_cache, v_cache, block_table, prefix_len, mask, scale, out, lse
  *                as in jf_tree_attention, whose results these are (merged in another order).
  *                A (row, head) that sees a NaN or a +inf score has NaN in out and lse.
- *                out must not overlap q or the caches.
+ *                out, lse and the workspace must not overlap an input or each other.
  *   tree_len     int32 [B] or NULL: ragged trees as in jf_tree_attention_ragged, but rows
  *                i >= tree_len[b] of out and lse are left as they were.
  *   workspace    at least jf_tree_attention_shared_workspace_size(...) bytes, 16-byte aligned, no

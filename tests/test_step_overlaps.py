@@ -69,3 +69,23 @@ def test_adjust(lib, packed):
     sizes = {2: B * V * 4, 3: rows * 4, 4: rows * 2 * 8, 5: B * V * 4, 6: allowed * 32 * 4, 7: rows * 4, 9: B * 4, 10: B * 4,
              11: B * 4, 13: (B + packed) * 4, out: rows * V * 2}
     none_overlap(fn, args, [out], sizes)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_shared(lib, packed):
+    B, N, T, Hq, Hkv, D, pages, wide, groups = 6, 70, 300, 16, 4, 64, 99, 11, 3
+    rows = T if packed else B * N
+    fn = lib.jf_tree_attention_shared_packed if packed else lib.jf_tree_attention_shared
+    fn.argtypes = [P] * 9 + [i32] * (10 if packed else 9) + [f32, P, P, P, sz, P, P]
+    args = [at(1), at(2), at(3), at(4), at(5), at(6), at(7), at(8), at(9), groups, B, N] + [T] * packed + [
+        Hq, Hkv, D, 16, wide, pages, 0.1, at(10), at(11), at(12), 1 << 40, None, None]
+    out = 20 if packed else 19
+    pool = pages * 16 * Hkv * D * 2
+    sizes = {0: rows * Hq * D * 2, 1: pool, 2: pool, 3: B * wide * 4, 4: B * 4, 5: (B + packed) * 4, 6: rows * 2 * 8,
+             7: (groups + 1) * 4, 8: groups * 4, out: rows * Hq * D * 2, out + 1: rows * Hq * 4,
+             out + 2: 2 * rows * Hq * (D + 1) * 4}       # the workspace holds that much at least
+    if not packed:
+        args[5] = None                                   # then with lengths: another array to stay clear of
+        none_overlap(fn, args, [out, out + 1, out + 2], {k: v for k, v in sizes.items() if k != 5})
+        args[5] = at(6)
+    none_overlap(fn, args, [out, out + 1, out + 2], sizes)

@@ -1495,8 +1495,20 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
   if (!aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(out, 16) ||
       !aligned_to(mask, 8))
     return JF_ERR_MISALIGNED;
+  // What is written shares no byte with what is read or with another output.
   const size_t qb = static_cast<size_t>(nodes) * Hq * D * 2, cb = static_cast<size_t>(num_pages) * kPage * Hkv * D * 2;
-  if (overlap(out, qb, q, qb) || overlap(out, qb, k_cache, cb) || overlap(out, qb, v_cache, cb)) return JF_ERR_INVALID_ARGUMENT;
+  const size_t lb = static_cast<size_t>(nodes) * Hq * 4, seqs = static_cast<size_t>(B), gb = static_cast<size_t>(n_groups) * 4;
+  auto over_inputs = [&](const void* to, size_t bytes) {
+    return overlaps_any(to, bytes, {{q, qb}, {k_cache, cb}, {v_cache, cb}, {block_table, seqs * max_pages * 4},
+                                    {prefix_len, seqs * 4}, {tree_len, seqs * 4}, {cu, (seqs + 1) * 4},
+                                    {mask, static_cast<size_t>(nodes) * ((N + 63) / 64) * 8}, {group_start, gb + 4},
+                                    {shared_pages, gb}});
+  };
+  if (over_inputs(out, qb) || (lse != nullptr && (over_inputs(lse, lb) || overlap(lse, lb, out, qb))))
+    return JF_ERR_INVALID_ARGUMENT;
+  const size_t wb = std::min(workspace_bytes, pl.ws_bytes);       // what of the workspace would be used
+  if (workspace != nullptr && (over_inputs(workspace, wb) || overlaps_any(workspace, wb, {{out, qb}, {lse, lb}})))
+    return JF_ERR_INVALID_ARGUMENT;
   if (sms <= 0) return JF_ERR_CUDA;
   if (workspace == nullptr || workspace_bytes < pl.ws_bytes) return JF_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned_to(workspace, 16)) return JF_ERR_MISALIGNED;
