@@ -809,8 +809,8 @@ jf_status jf_tree_attention_shared_packed(const void* q, const void* k_cache, co
  *                The logits of forbidden tokens need not be finite.
  *   repetition, presence, frequency  float [B], NULL for 1, 0 and 0.  repetition > 0.
  *   masked       what forbidden tokens get, rounded to the output's type: -INFINITY, or a finite
- *                value for calls that want finite logits.  A row whose grammar forbids every
- *                token is masked throughout.
+ *                value for calls that want finite logits (one past the type's range becomes its
+ *                lowest or largest).  A row whose grammar forbids every token is masked throughout.
  *   tree_len     int32 [B] or NULL; rows i >= tree_len[b] are neither read nor written.
  *   dev_err      JF_DEVERR_BAD_TOKEN (a drafted token outside [0, V): not counted), _BAD_PATH
  *                (an allowed_row outside [-1, n_allowed): no grammar), _BAD_TREE_LEN.

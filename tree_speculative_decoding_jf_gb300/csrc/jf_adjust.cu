@@ -33,6 +33,7 @@ constexpr int kSlice = kAdjThreads * kPer;
 constexpr int kMaxRun = 16;                    // rows per block at most (2048 rows: 8 249 us, 16 236, 32 247)
 constexpr int kAdjBlocks = 5;                  // resident blocks per SM (4: 251 us, 5: 236, 6: 233, but 54 odd rows 9.5 -> 11.0)
 constexpr int kPromptFlag = JF_COUNT_PROMPT;
+constexpr float kMaxBf16 = 3.38953138925153547590e38f;      // 2^128 - 2^120
 
 struct AdjustParams {
   const void* logits;
@@ -418,6 +419,8 @@ jf_status adjust_call(AdjustParams p, int32_t dtype, int32_t out_dtype, bool pac
     return JF_ERR_MISALIGNED;
   const size_t rows = packed ? static_cast<size_t>(p.T) : static_cast<size_t>(p.B) * p.N;
   if (rows > (size_t{1} << 40) / p.V) return JF_ERR_UNSUPPORTED;
+  // A finite value stays one: fp32's lowest would round to bf16's -inf.
+  if (osz == 2 && std::isfinite(p.masked)) p.masked = std::min(std::max(p.masked, -kMaxBf16), kMaxBf16);
   // The same array, or no shared byte: blocks read and write their own slices only.
   p.in_place = p.out == p.logits && isz == osz;
   if (!p.in_place && overlap(p.out, rows * p.V * osz, p.logits, rows * p.V * isz)) return JF_ERR_INVALID_ARGUMENT;
