@@ -112,3 +112,22 @@ def test_packed_rows_without_n_max(jf, groups, N, Hq, Hkv, D, pages, own, sizes)
                                         ints(w["start"]), ints(pages), with_lse=True, cu_seqlens=ints(cu), dev_err=err)
     assert err.item() == 0
     check(w, "packed", out, lse)
+
+
+@pytest.mark.parametrize("groups,N", [([3, 2], 2), ([200, 300], 3), ([3, 2], 40)])
+def test_old_descriptors_in_the_workspace(jf, groups, N):  # noqa: F811
+    """A call that computes nothing leaves the merge what the workspace held, here lists of a million pieces and more than
+    the workspace has rows: no row is merged from them."""
+    B = sum(groups)
+    w = make(groups, N, 8, 1, 64, [4, 2], [5 + b % 9 for b in range(B)], seed=214)
+    size = jf.jf_tree_attention_shared_workspace_size(B, N, 2, 8, 1, 64, w["table"].shape[1])
+    rows = size // (65 * 4)
+    for n in (rows // 2, 20000, 10 ** 6):
+        ws = torch.zeros(size // 16 + 1, 4, dtype=torch.int32, device="cuda")
+        ws[:, 0], ws[:, 1] = 3, n
+        out = torch.full(w["q"].shape, -7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, 8, N), -7.0, device="cuda")
+        err = new_err()
+        call(jf, dict(w, start=[0, 3, 2]), "padded", err, workspace=ws.view(torch.uint8).flatten(), out=out, lse=lse)
+        assert err.item() == jf.DEVERR_BAD_GROUP
+        assert (out == -7.0).all() and (lse == -7.0).all()

@@ -1223,9 +1223,10 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 // 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps sharing out the pieces.
 // A piece that saw a NaN or an infinite score has a NaN log-sum-exp and makes its row NaN; one whose keys were
 // all hidden has -inf and is passed over.  Rows behind the last sequence keep what they hold.  What ws_desc
-// says is checked against the workspace: a malformed group_start or span leaves it unwritten.
+// says is checked against the workspace and against the pieces an item can have (`most_pieces`): a malformed
+// group_start or span, or a wait that gave up, leaves it unwritten, with whatever the memory held.
 template <int D, int ROWS, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_constant__ SharedParams p, int total) {
+__global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_constant__ SharedParams p, int total, int most_pieces) {
   constexpr int E = D / 32;
   constexpr int kWarps = WARPS;
   constexpr int kStep = ROWS == 1 ? kWarps : 1;       // pieces a warp skips
@@ -1252,7 +1253,7 @@ __global__ void __launch_bounds__(32 * WARPS) shared_merge_kernel(const __grid_c
     else if (p.tree_len != nullptr) live[k] = live[k] && node % p.N < seq_span(nullptr, p.tree_len, node / p.N, p.N, p.T).n;
   }
   auto bad = [&](const int4& d) {
-    return d.y < 0 || d.y > total || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
+    return d.y < 0 || d.y > most_pieces || (d.y > 0 && (d.x < 0 || d.x >= total)) ||
            (d.y > 1 && (d.z < 0 || d.w < 0 || d.z + static_cast<long long>(d.y - 2) * d.w >= total));
   };
   auto piece = [&](const int4& a, const int4& b, int k) {      // workspace row of piece k
@@ -1461,16 +1462,16 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 }
 
 template <int D>
-jf_status launch_merge(const SharedParams& prm, int total, int sms, cudaStream_t s) {
+jf_status launch_merge(const SharedParams& prm, int total, int most, int sms, cudaStream_t s) {
   // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
   // pieces: 4 beams 13.6 us against 21.2, 64 requests 74 against 79), of eight warps while all blocks
   // are resident (4 beams 12.4, with four 13.7), else of four (64 requests 71.4, with eight 74.6); beyond
   // that two rows a warp (16 trees 131 us against 189, 256 beams 92 against 108).
   const long long rows = prm.rows;
   const dim3 each(static_cast<unsigned>(rows)), half(static_cast<unsigned>((rows + 15) / 16));
-  const cudaError_t e = rows <= 4ll * sms    ? launch_pdl(shared_merge_kernel<D, 1, 8>, each, dim3(256), 0, s, prm, total)
-                        : rows <= 32ll * sms ? launch_pdl(shared_merge_kernel<D, 1, 4>, each, dim3(128), 0, s, prm, total)
-                                             : launch_pdl(shared_merge_kernel<D, 2, 8>, half, dim3(256), 0, s, prm, total);
+  const cudaError_t e = rows <= 4ll * sms    ? launch_pdl(shared_merge_kernel<D, 1, 8>, each, dim3(256), 0, s, prm, total, most)
+                        : rows <= 32ll * sms ? launch_pdl(shared_merge_kernel<D, 1, 4>, each, dim3(128), 0, s, prm, total, most)
+                                             : launch_pdl(shared_merge_kernel<D, 2, 8>, half, dim3(256), 0, s, prm, total, most);
   return e == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
@@ -1569,8 +1570,8 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
       st = pl.row_mt == 1 ? launch_rows<64, 1>(km, vm, prm, s) : (pl.row_mt == 2 ? launch_rows<64, 2>(km, vm, prm, s) : launch_rows<64, 4>(km, vm, prm, s));
     if (st != JF_OK) return st;
   }
-  const int total = static_cast<int>(pl.total);
-  return D == 128 ? launch_merge<128>(prm, total, sms, s) : launch_merge<64>(prm, total, sms, s);
+  const int total = static_cast<int>(pl.total), pieces = std::max(pl.tile_ranges, pl.row_ranges);    // one a range
+  return D == 128 ? launch_merge<128>(prm, total, pieces, sms, s) : launch_merge<64>(prm, total, pieces, sms, s);
 }
 
 }  // namespace
