@@ -1970,7 +1970,8 @@ extern "C" jf_status jf_debug_set_wait_limit_ns(uint64_t limit_ns, int32_t withh
   const uint64_t v = limit_ns == 0 ? jf::kWaitLimitNs : limit_ns;
   const int w = withhold_arrivals != 0 ? 1 : 0;
   if (cudaMemcpyToSymbol(jf::g_wait_limit_ns, &v, sizeof(v)) != cudaSuccess ||
-      cudaMemcpyToSymbol(jf::g_withhold_vouchers, &w, sizeof(w)) != cudaSuccess) {
+      cudaMemcpyToSymbol(jf::g_withhold_vouchers, &w, sizeof(w)) != cudaSuccess ||
+      !jf::set_shared_wait_limit(v, w)) {
     cudaGetLastError();
     return JF_ERR_CUDA;
   }

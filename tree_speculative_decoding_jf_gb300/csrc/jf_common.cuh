@@ -38,6 +38,9 @@ inline jf_status launch_status() {
 // Number of SMs of the current device (cached per device id); 0 if it cannot be queried.
 int current_sm_count();
 
+// The wait limit and the test hook of the kernels in jf_shared.cu (see jf_debug_set_wait_limit_ns).
+bool set_shared_wait_limit(uint64_t limit_ns, int withhold);
+
 __device__ __forceinline__ void report(int32_t* dev_err, int32_t bits) {
   if (dev_err != nullptr) atomicOr(dev_err, bits);
 }

@@ -75,6 +75,11 @@ struct SharedParams {
 };
 constexpr int kShared = 1, kOwn = 2;
 
+// Time limit of the kernels' waits on their own pipeline, and the test hook that makes one run out (see
+// jf_debug_set_wait_limit_ns): non-zero withholds what says that data or a piece is there.
+__constant__ uint64_t c_wait_limit_ns = kWaitLimitNs;
+__constant__ int c_withhold = 0;
+
 // ------------------------------------------------------------------------ the schedule
 
 // Keys that a group's sequences share, of its shared_pages entry: none when it has one sequence
@@ -447,12 +452,12 @@ __device__ __forceinline__ int shared_count(int* c) {
   asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(c)) : "memory");
   return v;
 }
-__device__ __forceinline__ bool wait_shared_count(int* c, int target, volatile int* abort) {
+__device__ __forceinline__ bool wait_shared_count(int* c, int target, volatile int* abort, uint64_t wlim) {
   if (shared_count(c) > target) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
     if (shared_count(c) > target) return true;
-    if ((it & 255u) == 0u && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    if ((it & 255u) == 0u && (*abort || global_timer_ns() - t0 > wlim)) return false;
   }
 }
 
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
   using C = Cfg<NT, D>;
   constexpr int SK = C::kKStages;
   constexpr int SV = C::kVStages;
-  constexpr uint64_t wlim = kWaitLimitNs;
+  const uint64_t wlim = c_wait_limit_ns;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -731,8 +736,8 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     // The last arrival on p_full[t] for tile j: V tile j and K tile j + 1 have landed and, at a
     // piece's last tile, its V tail and the next piece's Q.
     const int t = warp - 2;
-    if (lane == 0) {
-      bool ready = wait_shared_count(&s_posted, 0, abort);
+    if (lane == 0 && c_withhold == 0) {
+      bool ready = wait_shared_count(&s_posted, 0, abort, wlim);
       int s = 0, e = ready ? s_piece[0].T : 0;
       for (int j = 0; j < Wc && ready; ++j) {
         const bool last_of_piece = j + 1 == e;
@@ -740,14 +745,14 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
                 mbar_wait(&v_full[j % SV], static_cast<uint32_t>(j / SV) & 1u, abort, wlim) &&
                 (j + 1 >= Wc ||
                  mbar_wait(&k_full[(j + 1) % SK], static_cast<uint32_t>((j + 1) / SK) & 1u, abort, wlim)) &&
-                (!last_of_piece || wait_shared_count(&s_tails, s, abort)) &&
+                (!last_of_piece || wait_shared_count(&s_tails, s, abort, wlim)) &&
                 (!last_of_piece || j + 1 >= Wc ||
                  mbar_wait(&q_full, static_cast<uint32_t>(s + 1) & 1u, abort, wlim));
         if (!ready) break;
         mbar_arrive(&p_full[t]);
         if (last_of_piece && j + 1 < Wc) {
           ++s;
-          ready = wait_shared_count(&s_posted, s, abort);
+          ready = wait_shared_count(&s_posted, s, abort, wlim);
           if (ready) e += *reinterpret_cast<volatile int*>(&s_piece[s % kPieces].T);
         }
       }
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
     int jg0 = 0;
     for (int s = 0; jg0 < Wc && ok; ++s) {
       int posted = 1;
-      if (lane == 0) posted = wait_shared_count(&s_posted, s, abort) ? 1 : 0;
+      if (lane == 0) posted = wait_shared_count(&s_posted, s, abort, wlim) ? 1 : 0;
       posted = __shfl_sync(0xffffffffu, posted, 0);      // and what the lane acquired is the warp's
       __syncwarp();
       // (The piece is read where it is needed: registers belong to the scores.)
@@ -932,7 +937,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
   constexpr int kTeams = C::kTeams, kS = C::kStages;
   constexpr int kI = D / 32;            // 16-byte chunks of a row per thread (scores)
   constexpr int kH = C::kHalves;
-  constexpr uint64_t wlim = kWaitLimitNs;
+  const uint64_t wlim = c_wait_limit_ns;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -985,7 +990,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         if (lane < steps) ids = __ldg(bt + lane);
         if (lane == 0) {                // its rows' Q can be read while its first page is under way
           s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
-          shared_count_add(&s_posted[team]);
+          if (c_withhold == 0) shared_count_add(&s_posted[team]);
         }
         for (int s = 0; s < steps; ++s) {
           if ((s & 31) == 0 && s + lane < steps) {
@@ -1036,7 +1041,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
     uint32_t phase = 0;
     for (int post = 0; ok; ++post) {
       int there = 1;
-      if (lane == 0) there = wait_shared_count(&s_posted[team], post, abort) ? 1 : 0;
+      if (lane == 0) there = wait_shared_count(&s_posted[team], post, abort, wlim) ? 1 : 0;
       there = __shfl_sync(0xffffffffu, there, 0);
       __syncwarp();                     // what the lane acquired is the warp's
       if (!there) {
@@ -1575,6 +1580,12 @@ jf_status shared_call(const void* q, const void* k_cache, const void* v_cache, c
 }
 
 }  // namespace
+
+bool set_shared_wait_limit(uint64_t limit_ns, int withhold) {
+  return cudaMemcpyToSymbol(c_wait_limit_ns, &limit_ns, sizeof(limit_ns)) == cudaSuccess &&
+         cudaMemcpyToSymbol(c_withhold, &withhold, sizeof(withhold)) == cudaSuccess;
+}
+
 }  // namespace jf
 
 extern "C" size_t jf_tree_attention_shared_workspace_size(int32_t B, int32_t N, int32_t T, int32_t n_groups,
