@@ -126,7 +126,7 @@ __device__ __forceinline__ Unit own_unit(const SharedParams& p, int b, int S, in
   // (A sequence whose nodes have no room behind S is malformed, its P < S or its keys past the table: it
   // starts where they do have room.)
   const int last = p.max_pages * kPage - n;
-  t.key0 = min(S, last / kPage * kPage);
+  t.key0 = min(S, last & -kPage);
   t.P = max(t.key0, min(prefix, last));
   t.L = t.P + n;
   t.f0 = row0;
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         mbar_init(&s_full[t][st], 1);
         mbar_init(&s_empty[t][st], MT);
       }
-      s_posted[t] = 0;
+      s_posted[t] = c_withhold == 0 ? 0 : INT_MIN / 2;      // (withheld: no piece is ever there)
     }
     abort_flag = 0;
     fence_mbar_init();
@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
         if (lane < steps) ids = __ldg(bt + lane);
         if (lane == 0) {                // its rows' Q can be read while its first page is under way
           s_post[team][posted % C::kPosts] = w.piece(sch, blockIdx.x + team * gridDim.x);
-          if (c_withhold == 0) shared_count_add(&s_posted[team]);
+          shared_count_add(&s_posted[team]);
         }
         for (int s = 0; s < steps; ++s) {
           if ((s & 31) == 0 && s + lane < steps) {
