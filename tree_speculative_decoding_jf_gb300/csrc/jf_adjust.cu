@@ -527,7 +527,7 @@ __device__ __forceinline__ void each_token(const CountParams& p, int b, int firs
 // the tokens that fall in it from a table in shared memory, so every byte moves once.
 template <bool VEC>
 __global__ void __launch_bounds__(kCountThreads) count_copy_kernel(const CountParams p) {
-  __shared__ int s_n[kCountSlice];
+  __shared__ __align__(16) int s_n[kCountSlice];      // read four at a time
   grid_dependency_wait();
   const int b = blockIdx.y;
   const int v0 = blockIdx.x * kCountSlice;
