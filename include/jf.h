@@ -688,7 +688,8 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
  *      P_b + i of sequence b's pages.
  * Arithmetic is fp32 (a normalised head's squares must sum within its range) with one rounding to
  * bf16 at the end; the angle is formed modulo one turn in 64 bits (its fraction of a turn is off by
- * about 2^-52 |pos freq / 2 pi| + 2^-25), so far positions cost no precision.
+ * about 2^-52 |pos freq / 2 pi| + 2^-25, with a negative frequency 2^-54 |pos| more), so far positions
+ * cost no precision.
  *   q, k, v      bf16, token rows of [Hq][D], [Hkv][D], [Hkv][D]; consecutive tokens
  *                (row b * N + i) lie *_stride elements apart, so the three may be views of one
  *                projection's output.  q and q_out may both be NULL (keys and values only).
@@ -705,8 +706,10 @@ jf_status jf_beam_fork_kv(void* k_cache, void* v_cache, const int32_t* block_tab
  *   dev_err      JF_DEVERR_BAD_PREFIX (P_b < 0 or P_b + n_b past the block table: the sequence's
  *                keys and values are not written), _BAD_PAGE (the token's are not written),
  *                _BAD_TREE_LEN.  May be NULL.
- * Limits: D in {64, 128}; R a multiple of 16, 16 <= R <= D; page_size 16; B * N + N < 2^31; num_pages *
- * page_size < 2^31; the arrays 16-byte aligned and strides multiples of 8; N may exceed JF_MAX_NODES.
+ * Limits: D in {64, 128}; R a multiple of 16, 16 <= R <= D; page_size 16; B * N + N < 2^31 (packed: T + N_max);
+ * num_pages * page_size < 2^31, max_pages * page_size <= 2^30; Hq, Hkv <= 2^20; the arrays 16-byte aligned
+ * (pos and the int32 arrays 4, freq 8); strides multiples of 8, at least a token's heads, at most 2^31; N may exceed
+ * JF_MAX_NODES.
  * jf_rotate_append_kv_packed takes the packed layout: rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1,
  * pos [T], q_out [T][Hq][D].
  */
@@ -733,8 +736,11 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
 
 /*
  * jf_tree_attention_shared -- jf_tree_attention for sequences that share a long prefix, whose keys
- * and values are then read once for all of them: the beams of a prompt, which share full pages
- * after jf_beam_fork_kv, requests behind one system prompt, samples of one prompt.
+ * and values are then read for many of them at once: the beams of a prompt, which share full pages
+ * after jf_beam_fork_kv, requests behind one system prompt, samples of one prompt.  They are read once per
+ * 16, 32 or 64 of the group's rows (nodes x G) where groups have up to 64 rows on average, else once per
+ * 128 or 256; the average decides since the groups' own sizes are device data, so one large group among
+ * many small ones is better called by itself.
  *   group_start  int32 [n_groups + 1], 0 = group_start[0] <= .. <= group_start[n_groups] = B: group
  *                u holds the sequences group_start[u] .. group_start[u + 1] - 1.
  *   shared_pages int32 [n_groups]: the first S = page_size * shared_pages[u] keys of group u's
@@ -745,8 +751,11 @@ jf_status jf_rotate_append_kv_packed(const void* q, int64_t q_stride, const void
  *                as in jf_tree_attention, whose results these are (merged in another order).
  *                A (row, head) that sees a NaN or a +inf score has NaN in out and lse.
  *                out, lse and the workspace must not overlap an input or each other.
+ *                Probabilities are rounded to bf16 before the product with V as there (two parts for
+ *                sequences with few keys); where a team works on 16 rows, always in two parts.
  *   tree_len     int32 [B] or NULL: ragged trees as in jf_tree_attention_ragged, but rows
- *                i >= tree_len[b] of out and lse are left as they were.
+ *                i >= tree_len[b] of out and lse are left as they were.  A shared part's time goes by
+ *                all its N rows a sequence, padding included: the packed form has none.
  *   workspace    at least jf_tree_attention_shared_workspace_size(...) bytes, 16-byte aligned, no
  *                initialisation.  Calls that overlap need one each.
  *   dev_err      JF_DEVERR_BAD_GROUP (group_start is not such a partition: no row is computed, out and
@@ -818,8 +827,9 @@ jf_status jf_tree_attention_shared_packed(const void* q, const void* k_cache, co
  *   dev_err      JF_DEVERR_BAD_TOKEN (a drafted token outside [0, V): not counted), _BAD_PATH
  *                (an allowed_row outside [-1, n_allowed): no grammar), _BAD_TREE_LEN.
  * Arithmetic is fp32 with one rounding at the end.
- * Limits: 1 <= N <= JF_MAX_NODES, B * N * V <= 2^40.  V a multiple of 8 with 16-byte aligned arrays
- * is read and written 16 bytes at a time, anything else element by element.
+ * Limits: 1 <= N <= JF_MAX_NODES, B * N * V <= 2^40 (packed: T * V), B * N * ceil(V / 2048) < 2^31 (packed:
+ * B * N_max * ceil(V / 2048)).  V a multiple of 8 with 16-byte aligned arrays is read and written 16 bytes
+ * at a time, anything else element by element.
  * jf_adjust_logits_packed takes rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1: logits, out [T][V],
  * draft, allowed_row [T], mask [T][W].
  */

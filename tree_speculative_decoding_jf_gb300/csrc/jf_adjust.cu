@@ -30,8 +30,8 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kPer = 8;                        // tokens per thread
 constexpr int kSlice = kAdjThreads * kPer;
-constexpr int kMaxRun = 16;                    // rows per block at most (2048 rows: 8 249 us, 16 236, 32 247)
-constexpr int kAdjBlocks = 5;                  // resident blocks per SM (4: 251 us, 5: 236, 6: 233, but 54 odd rows 9.5 -> 11.0)
+constexpr int kMaxRun = 16;                    // rows per block at most (2048 rows: 8 248 us, 16 235, 32 245)
+constexpr int kAdjBlocks = 5;                  // resident blocks per SM (4: 249 us, 5: 235, 6: 232, but 54 odd rows 9.4 -> 10.9)
 constexpr int kPromptFlag = JF_COUNT_PROMPT;
 constexpr float kMaxBf16 = 3.38953138925153547590e38f;      // 2^128 - 2^120
 

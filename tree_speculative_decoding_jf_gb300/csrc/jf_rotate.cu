@@ -10,8 +10,9 @@
 // Angles.  Only the fraction of a turn matters, and with integer positions it can be formed
 // exactly modulo one turn: freq / 2 pi as a 64-bit fixed-point fraction of a turn, multiplied
 // by the position in 64-bit integer arithmetic (which wraps at whole turns), is off by at most
-// |pos| 2^-64 turns plus the 2^-52 relative rounding of freq / 2 pi.  The signed fraction is
-// then rounded to fp32 once, so a position of a million costs no more error than position 1;
+// |pos| 2^-64 turns plus the 2^-52 relative rounding of freq / 2 pi (a negative frequency's
+// fraction is taken from one, which rounds too: |pos| 2^-54).  The signed fraction is then
+// rounded to fp32 once, so a position of a million costs no more error than position 1;
 // pos * freq in fp32 would be off by up to 2^-24 * pos radians.
 //
 // Bound: bytes.  Every head row is read and written once, so a thread owns the two 16-byte
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kMaxThreads = 384;
-constexpr int kAhead = 1;                   // tokens whose rows are on their way (trees: 1 13.9 us, 2 15.9, 3 17.1: registers)
+constexpr int kAhead = 1;                   // tokens whose rows are on their way (trees: 1 12.6 us, 2 14.0, 3 15.4: registers)
 constexpr int kMaxChunk = 16;               // tokens whose facts a block settles at once
 constexpr int kBlocks = 4;                  // blocks per SM, resident or next in line (trees: 4 12.6 us, 8 13.8; prompts alike)
 

@@ -19,7 +19,9 @@
 // at its start) and 1; the first piece of an item tells each of its rows where its pieces are.
 // The merge kernel reads that and adds up.
 //
-// Two kernels walk ranges.
+// Two kernels walk ranges; where both run, the one after the other.  (Alternatives' times in this file stand beside
+// the chosen one's of the same run: device times in captured graphs.  Where a step is told as from .. to .., it is
+// the step's own before and after.)
 //   shared_attention_kernel: 256 rows (two tiles of 128) an item, tcgen05 products, one range per SM,
 //     with the pipeline of the stream-K attention kernel (see jf_attention.cu: producer, MMA issuer,
 //     vouchers, softmax warpgroups, all counters running over the range's tiles as one sequence).
@@ -27,9 +29,9 @@
 //     sequences over 8K shared keys, 106 GFLOP, take 120 us in all (0.89 PFLOP/s; rows that fill their
 //     last tile in part, the prologue and the merge are the rest).
 //   shared_rows_kernel (below): 16 to 64 rows an item, bound by the K/V stream: 256 beams in 32
-//     groups over 4K keys take 86 us, 4.7 TB/s.
+//     groups over 4K keys take 87 us, 4.7 TB/s.
 // jf_tree_attention on the same inputs reads a prefix once per sequence and takes 566 us for the
-// beams, 695 us for 64 sequences over 32K shared keys (here 72).
+// beams, 695 us for 64 sequences over 32K shared keys (here 80).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -310,9 +312,10 @@ struct Piece {
 // A piece's slot is written once the S MMAs of the last tile of the piece before it are done: every
 // role has then left the pieces up to the third before it.
 constexpr int kPieces = 4;
-// A change of item costs the tcgen05 kernel four to six tiles' time: the next item's Q and K arrive, the
-// rows leave TMEM (16 trees of up to 64 nodes: 3 130 us, 4 118, 5 119, 6 120; of up to 256: 4 317, 5 303,
-// 6 300; 128 beams in two groups over 16K keys: 4 69.6, 5 66.4, 6 63.9).
+// A change of item costs the tcgen05 kernel some tiles' time: the next item's Q and K arrive, the rows leave TMEM.
+// No one count is best for all: 16 trees of up to 64 nodes 3 129 us, 4 117, 5 118, 6 120, 8 124, 10 129; of up to 256
+// 346, 320, 303, 302, 310, 313; 128 beams in two groups over 16K keys (own parts in the row kernel) 73.3, 75.8,
+// 71.7, 71.5, 69.0, 68.8; 64 requests over 32K keys 82.3, 81.3, 79.6, 80.2, 78.7, 78.1.  6 is within 4% of each one's best.
 constexpr int kTileSwitch = 6;
 template <int NT>
 using TileCut = Cut<NT * kRowTile, kKeyTile, kTileSwitch, 1>;
@@ -890,13 +893,14 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, 1)
 //   chunks lane % 4 + 4 i two rows collide, 186 us for four groups of 64 rows over 32K keys against 181.)
 //   Output: V's fragments come transposed from shared memory (ldmatrix), two n-tiles at a time.
 // Its time is the latency of a page's chain (products, maximum, exponentials, products) at two warps a
-// scheduler: issue slots 43% busy, HBM 69%.  Two pages a step (103 us for 256 beams against 91), four
-// accumulators for the scores (93) and V's fragments kept for the second product (92) gained nothing.
+// scheduler: issue slots 43% busy, HBM 69%.  Two pages a step (103 us for 256 beams), four accumulators for the
+// scores (93) and V's fragments kept for the second product (92) gained nothing on the 91 us of the time.
 // A change of item, in pages: what it costs is the same for both head dimensions, a page at D = 64 half
-// (256 beams, D = 128: 2 98 us, 3 86, 4 88, 8 98; D = 64: 3 70, 4 66, 5 63; 16 groups of them: 3 73, 4 71, 5 74).
+// (256 beams in 32 groups, D = 128: 2 95.3 us, 3 86.8, 4 89.0, 8 98.1, in 16 groups 107, 106, 111, 130; D = 64: 3 72.5,
+// 4 66.9, 5 63.6, in 16 groups 76.5, 72.8, 75.5).
 template <int D>
 constexpr int kRowSwitch = D == 128 ? 3 : 4;
-constexpr int kRowLeast = 4;            // pages (4 beams over 2K keys: 1 17.2 us, 2 14.3, 4 13.6, 8 15.6)
+constexpr int kRowLeast = 4;            // pages (4 beams over 2K keys: 1 15.3 us, 2 13.2, 4 12.8, 8 15.3)
 constexpr int kRowWarps = 8;            // and as many producer warps, of which one per team works
 template <int D, int MT>
 using RowCut = Cut<16 * MT, kPage, kRowSwitch<D>, kRowLeast>;
@@ -1224,8 +1228,8 @@ __global__ void __launch_bounds__(64 * kRowWarps, 1)
 // ------------------------------------------------------------------------ the merge
 
 // The pieces of a (node, query head) row's shared and own parts, listed by ws_desc, merged by
-// log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap (four rows for two: 144 us for
-// 16 trees against 131); ROWS == 1, for few rows: a block merges one, its warps sharing out the pieces.
+// log-sum-exp.  ROWS > 1: a warp merges ROWS rows, whose reads overlap (four rows for two: 131 -> 144 us
+// for 16 trees); ROWS == 1, for few rows: a block merges one, its warps sharing out the pieces.
 // A piece that saw a NaN or an infinite score has a NaN log-sum-exp and makes its row NaN; one whose keys were
 // all hidden has -inf and is passed over.  Rows behind the last sequence keep what they hold.  What ws_desc
 // says is checked against the workspace and against the pieces an item can have (`most_pieces`): a malformed
@@ -1381,11 +1385,16 @@ bool shared_sizes(long long nodes, int B, int N, int n_groups, int Hq, int Hkv, 
   return 2 * nodes * Hq + 8 * kMaxRanges * kRowTile < INT_MAX;
 }
 
-// Which kernel takes which units.  Up to 64 rows a group (on average) the row kernel takes both parts:
-// the K/V stream bounds it (four groups of 64 rows over 32K keys: 176 us, on the tcgen05 kernel 265; 32
-// rows fill two warps, 98 us for 256 beams against 125 with one warp twice).  Groups of more rows
-// have their shared parts on the tcgen05 kernel, two row tiles per CTA (each key tile loaded feeds
-// both) once they fill more than one, and so have own parts of more than 64 rows.
+// Which kernel takes which units, by the average rows of a group: the groups' own sizes are device data.  Up to 64
+// rows the row kernel takes both parts, in teams by the rows (32 rows fill two warps: 256 beams 86.8 us, 126 with one
+// warp twice).  Groups of more rows have their shared parts on the tcgen05 kernel, two row tiles per CTA (each key
+// tile loaded feeds both) once they fill more than one, and so have own parts of more than 64 rows.
+//   33 to 64 rows: the row kernel is ahead while the keys are few (one group of 64 rows over 32K keys 52 us, four over
+// 2K 27; with the shared parts on the tcgen05 kernel 53 and 34), behind where they are many (four over 32K 174 and
+// 121).  How many there are is device data too, of which the host knows the table's width alone.
+//   Uneven groups: one much larger than the average has its shared keys read once per 16 to 64 of its rows (33
+// sequences behind 32K keys beside 31 that share nothing, 8 rows a sequence: 458 us; the group alone 58, the others 316.
+// 900 sequences behind 4K keys beside 63: 566; alone 126 and 108).
 SharedPlan plan_shared(long long nodes, int N, int n_groups, int Hq, int Hkv, int D, int sms) {
   SharedPlan pl = {};
   const long long G = Hq / Hkv, group_rows = (nodes * G + n_groups - 1) / n_groups, own_rows = N * G;
@@ -1469,9 +1478,9 @@ jf_status launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const Shared
 template <int D>
 jf_status launch_merge(const SharedParams& prm, int total, int most, int sms, cudaStream_t s) {
   // A block a row while that keeps the SMs at most 32 blocks deep (its warps share a long list of
-  // pieces: 4 beams 13.6 us against 21.2, 64 requests 74 against 79), of eight warps while all blocks
-  // are resident (4 beams 12.4, with four 13.7), else of four (64 requests 71.4, with eight 74.6); beyond
-  // that two rows a warp (16 trees 131 us against 189, 256 beams 92 against 108).
+  // pieces: 64 requests 80.2 us, with two rows a warp 91.6), of eight warps while all blocks are resident
+  // (4 beams 12.8, with four 14.3), else of four (64 requests 80.2, with eight 82.3); beyond that two rows a
+  // warp (16 trees 120 us, with a block a row 145; 256 beams 86.8 and 94.8).
   const long long rows = prm.rows;
   const dim3 each(static_cast<unsigned>(rows)), half(static_cast<unsigned>((rows + 15) / 16));
   const cudaError_t e = rows <= 4ll * sms    ? launch_pdl(shared_merge_kernel<D, 1, 8>, each, dim3(256), 0, s, prm, total, most)
